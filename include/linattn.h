@@ -91,8 +91,16 @@ typedef enum {
     LA_FM_ELU1 = 0,          /* phi = elu + 1, normalised read               */
     LA_FM_IDENTITY_NORM = 1, /* phi = identity, normalised read (the pages'
                                 hand-worked examples give features directly) */
-    LA_FM_NONE = 2           /* phi = identity, unnormalised (RetNet)        */
+    LA_FM_NONE = 2,          /* phi = identity, unnormalised (RetNet)        */
+    LA_FM_L2 = 3             /* phi(x) = x / sqrt(|x|^2 + 1e-6), unnormalised
+                                read; the delta-rule calls only              */
 } la_feature_map;
+
+typedef enum {
+    LA_ACT_SILU = 0,         /* g sigmoid(g)                                 */
+    LA_ACT_SIGMOID = 1,
+    LA_ACT_NONE = 2          /* the gate as it is                            */
+} la_activation;
 
 typedef enum {
     LA_BF16 = 0,             /* q, k, v are bfloat16                          */
@@ -255,6 +263,100 @@ LA_API la_status la_state_prefix(const float* S_parts, const float* z_parts, int
  */
 LA_API la_status la_favor_features(const void* x, const float* w, void* out, int64_t rows, int d,
                                    int r, int in_dtype, int out_dtype, la_stream_t stream);
+
+/*
+ * Gated delta rule: the state corrects what it holds for a key instead of
+ * adding to it.  With a_t = exp(log_alpha_t) and k_t, q_t the mapped rows,
+ *     e_t = v_t - a_t S_{t-1}^T k_t,
+ *     S_t = a_t S_{t-1} + beta_t k_t e_t^T,   o_t = scale S_t^T q_t
+ * ["Efficient Attention Variants", section 7.3 names the delta rule beside the
+ * additive state].
+ *   q, k      : [B,Hk,N,d], v, out [B,H,N,dv], all in `dtype` (out too, unlike
+ *               la_forward: it feeds la_norm_gate and a projection).  Hk
+ *               divides H; value head h reads key head h / (H / Hk).
+ *   beta      : [B,H,N] fp32, the writing strength.  Any finite value is
+ *               taken; the recurrence is stable for 0 <= beta |k|^2 <= 2.
+ *   log_alpha : [B,H,N] fp32 <= 0, or NULL for no decay.  Values below -128,
+ *               -inf among them, reset the state.  (A token with beta = 0 and
+ *               log_alpha = 0 leaves the state as it was: right padding.)
+ *   feature_map : LA_FM_L2 or LA_FM_NONE, for q and k.
+ *   scale     : finite; 1/sqrt(d) is usual.
+ *   S0, S_out : fp32 [B,H,d,dv] state before the first and after the last
+ *               token, each may be NULL (zero start; not wanted), and they may
+ *               be the same buffer.  out and q may be NULL together for a
+ *               state-only call, which needs S_out.
+ * Inputs are finite: a NaN or infinity may reach the outputs of the 63 tokens
+ * before its own, and every later one.  Workspace:
+ * la_delta_workspace_size() bytes, 256-byte aligned (it may be 0, then the
+ * workspace may be NULL).  N = 0 copies S0 (or zero) to S_out.
+ */
+LA_API size_t la_delta_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv,
+                                      int dtype);
+LA_API la_status la_forward_delta(const void* q, const void* k, const void* v, const float* beta,
+                                  const float* log_alpha, void* out, const float* S0,
+                                  float* S_out, int64_t B, int64_t H, int64_t Hk, int64_t N,
+                                  int d, int dv, int feature_map, float scale, int dtype,
+                                  void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * One token of the gated delta rule for B*H states: S [B,H,d,dv] (fp32) is
+ * updated in place; q, k [B,Hk,d], v, out [B,H,dv] in `dtype`; beta and
+ * log_alpha [B,H] (log_alpha may be NULL).  Arguments as la_forward_delta.
+ */
+LA_API la_status la_decode_step_delta(float* S, const void* q, const void* k, const void* v,
+                                      const float* beta, const float* log_alpha, void* out,
+                                      int64_t B, int64_t H, int64_t Hk, int d, int dv,
+                                      int feature_map, float scale, int dtype,
+                                      la_stream_t stream);
+
+/*
+ * Gradients of la_forward_delta.  dout [B,H,N,dv] (dtype) and dS_out
+ * [B,H,d,dv] (fp32, NULL for zero) are those of out and S_out; the inputs are
+ * the forward's, and nothing else is kept from it.  Written: dq, dk
+ * [B,Hk,N,d] and dv_out [B,H,N,dv] in dtype (the value heads of a key head
+ * summed in fp32, in a fixed order), dbeta [B,H,N] and dlog_alpha [B,H,N]
+ * (NULL exactly when log_alpha is) in fp32, dS0 [B,H,d,dv] fp32 or NULL.
+ * With N = 0, dS0 receives dS_out (or zero).  Workspace:
+ * la_delta_backward_workspace_size() bytes, 256-byte aligned.
+ */
+LA_API size_t la_delta_backward_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int d,
+                                               int dv, int dtype);
+LA_API la_status la_backward_delta(const void* dout, const float* dS_out, const void* q,
+                                   const void* k, const void* v, const float* beta,
+                                   const float* log_alpha, const float* S0, void* dq, void* dk,
+                                   void* dv_out, float* dbeta, float* dlog_alpha, float* dS0,
+                                   int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv,
+                                   int feature_map, float scale, int dtype, void* workspace,
+                                   size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * Norm and gate behind the heads' outputs:
+ *     y[b,n,h,:] = w * x[b,h,n,:] / sqrt(mean(x[b,h,n,:]^2) + eps) * act(gate[b,n,h,:])
+ * x [B,H,N,dv] in x_dtype is head-major, as the forwards write it; gate (NULL:
+ * no gate) and y [B,N,H,dv] in dtype are token-major, as projections read and
+ * write them.  weight: fp32 [dv] (weight_heads = 0), [H,dv] (weight_heads = 1)
+ * or NULL for 1.  activation: la_activation.  eps > 0.  dv in {32, 64, 128}.
+ */
+LA_API la_status la_norm_gate(const void* x, const void* gate, const float* weight, void* y,
+                              int64_t B, int64_t H, int64_t N, int dv, int activation,
+                              int weight_heads, float eps, int x_dtype, int dtype,
+                              la_stream_t stream);
+
+/*
+ * Gradients of la_norm_gate from dy [B,N,H,dv] (dtype): dx [B,H,N,dv] in
+ * x_dtype, dgate [B,N,H,dv] in dtype (NULL exactly when gate is) and dweight,
+ * fp32 in weight's layout (NULL exactly when weight is; zero for N = 0),
+ * summed in fp32 in a fixed order.  Workspace:
+ * la_norm_gate_backward_workspace_size() bytes, 256-byte aligned, needed only
+ * with a weight.
+ */
+LA_API size_t la_norm_gate_backward_workspace_size(int64_t B, int64_t H, int64_t N, int dv);
+LA_API la_status la_norm_gate_backward(const void* dy, const void* x, const void* gate,
+                                       const float* weight, void* dx, void* dgate, float* dweight,
+                                       int64_t B, int64_t H, int64_t N, int dv, int activation,
+                                       int weight_heads, float eps, int x_dtype, int dtype,
+                                       void* workspace, size_t workspace_bytes,
+                                       la_stream_t stream);
 
 /*
  * la_forward without a workspace argument, for callers that cannot allocate

@@ -15,6 +15,9 @@ from __future__ import annotations
 _EXPORTS = {
     "la_forward", "la_forward_noalloc", "la_forward_with_state", "la_favor_features", "la_state_prefix", "la_forward_gla", "la_gla_workspace_size", "la_decode_step_gla", "la_state", "la_decode_step", "la_get_device_status", "la_status_string",
     "la_version", "la_launch_count", "la_debug_set_tc_faults", "la_forward_path", "la_forward_workspace_size", "la_state_workspace_size", "LinAttnError",
+    "la_forward_delta", "la_decode_step_delta", "la_backward_delta", "la_delta_workspace_size",
+    "la_delta_backward_workspace_size", "la_norm_gate", "la_norm_gate_backward",
+    "la_norm_gate_backward_workspace_size",
 }
 
 

@@ -28,10 +28,12 @@ LA_OK = 0
 STATUS_NAMES = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_CUDA",
                 4: "LA_ERR_TIMEOUT", 5: "LA_ERR_DEVICE_CHECK", 6: "LA_ERR_WORKSPACE",
                 7: "LA_ERR_TOO_LARGE"}
-FEATURE_MAPS = {"elu1": 0, "identity_norm": 1, "none": 2}
+FEATURE_MAPS = {"elu1": 0, "identity_norm": 1, "none": 2, "l2": 3}
+ACTIVATIONS = {"silu": 0, "sigmoid": 1, "none": 2}
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 _vp, _i64, _i, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_f = ctypes.c_float
 _fp = ctypes.POINTER(ctypes.c_float)
 
 _lib.la_version.restype = _i
@@ -67,6 +69,23 @@ _lib.la_state_prefix.argtypes = [_vp, _vp, _i, ctypes.POINTER(ctypes.c_int64), _
                                  _i64, _i, _i, _fp, _vp]
 _lib.la_favor_features.restype = _i
 _lib.la_favor_features.argtypes = [_vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp]
+_lib.la_delta_workspace_size.restype = _sz
+_lib.la_delta_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i, _i, _i]
+_lib.la_forward_delta.restype = _i
+_lib.la_forward_delta.argtypes = [_vp] * 8 + [_i64] * 4 + [_i, _i, _i, _f, _i, _vp, _sz, _vp]
+_lib.la_decode_step_delta.restype = _i
+_lib.la_decode_step_delta.argtypes = [_vp] * 7 + [_i64] * 3 + [_i, _i, _i, _f, _i, _vp]
+_lib.la_delta_backward_workspace_size.restype = _sz
+_lib.la_delta_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i, _i, _i]
+_lib.la_backward_delta.restype = _i
+_lib.la_backward_delta.argtypes = [_vp] * 14 + [_i64] * 4 + [_i, _i, _i, _f, _i, _vp, _sz, _vp]
+_lib.la_norm_gate.restype = _i
+_lib.la_norm_gate.argtypes = [_vp] * 4 + [_i64] * 3 + [_i, _i, _i, _f, _i, _i, _vp]
+_lib.la_norm_gate_backward_workspace_size.restype = _sz
+_lib.la_norm_gate_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i]
+_lib.la_norm_gate_backward.restype = _i
+_lib.la_norm_gate_backward.argtypes = [_vp] * 7 + [_i64] * 3 + [_i, _i, _i, _f, _i, _i, _vp, _sz,
+                                                               _vp]
 _lib.la_forward_noalloc.restype = _i
 _lib.la_forward_noalloc.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _fp,
                                     _i, _vp]
@@ -330,6 +349,240 @@ def la_favor_features(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None
                                   _stream_handle(stream))
     _check(code, "la_favor_features")
     return out
+
+
+def _arg(t: torch.Tensor | None, name: str, shape, dtype, device) -> int | None:
+    """Device pointer of a tensor that has to have this shape, type and place."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    ptr = _dev_ptr(t, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    return ptr
+
+
+def _current(t: torch.Tensor, name: str) -> torch.device:
+    """The device of a call: its tensors' device, which has to be the current one."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    _dtype(t)
+    return t.device
+
+
+class _Call:
+    """The stream of a call and what is allocated for it: outputs and scratch
+    belong to that stream, so none is handed out again before it has run."""
+
+    def __init__(self, stream, device):
+        self.device = device
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            self.stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+                torch.cuda.default_stream(device)
+        else:
+            self.stream = stream
+        self.other = self.stream != torch.cuda.current_stream(device)
+        self.handle = self.stream.cuda_stream or None
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other:
+            # allocated for the current stream: the call's own may write only
+            # once what had the memory before is done, and the memory stays
+            # until the call is
+            self.stream.wait_stream(torch.cuda.current_stream(self.device))
+            t.record_stream(self.stream)
+        return t
+
+    def scratch(self, workspace, need):
+        """Pointer and size of the given workspace, or of a new one."""
+        if workspace is None:
+            if need == 0:
+                return None, 0
+            workspace = self.empty(need, torch.uint8)
+        ptr = _dev_ptr(workspace, "workspace")
+        if workspace.device != self.device:
+            raise ValueError(f"workspace is on {workspace.device}, not {self.device}")
+        return ptr, workspace.numel() * workspace.element_size()
+
+
+def _delta_sizes(k, v):
+    if k.dim() != v.dim() or k.shape[0] != v.shape[0] or k.shape[2:-1] != v.shape[2:-1]:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not belong together")
+    return v.shape[0], v.shape[1], k.shape[1], k.shape[-1], v.shape[-1]
+
+
+def la_delta_workspace_size(B, H, Hk, N, d, dv, dtype=torch.bfloat16) -> int:
+    return int(_lib.la_delta_workspace_size(B, H, Hk, N, d, dv, DTYPES[dtype]))
+
+
+def la_delta_backward_workspace_size(B, H, Hk, N, d, dv, dtype=torch.bfloat16) -> int:
+    return int(_lib.la_delta_backward_workspace_size(B, H, Hk, N, d, dv, DTYPES[dtype]))
+
+
+def la_forward_delta(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                     beta: torch.Tensor, log_alpha: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, *, feature_map="l2",
+                     scale: float | None = None, S0: torch.Tensor | None = None,
+                     S_out: torch.Tensor | None = None, return_state: bool = False,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """Gated delta rule over whole sequences -> (out, S_out).
+
+    q, k [B,Hk,N,d], v [B,H,N,dv] (bf16 or fp32), beta and log_alpha [B,H,N]
+    fp32 (None: no decay); out [B,H,N,dv] in v's type.  S0 is the state before
+    the first token (None: zero); the final state is written when S_out is
+    given or return_state is set, else None is returned for it.  q = None
+    computes the final state alone.  scale defaults to 1/sqrt(d)."""
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hk,N,d]")
+    dev = _current(k, "k")
+    B, H, Hk, d, dv = _delta_sizes(k, v)
+    N = k.shape[2]
+    call = _Call(stream, dev)
+    if q is not None and out is None:
+        out = call.empty((B, H, N, dv), k.dtype)
+    if S_out is None and (return_state or q is None):
+        S_out = call.empty((B, H, d, dv), torch.float32)
+    f32, gates, state = torch.float32, (B, H, N), (B, H, d, dv)
+    ptrs = (_arg(q, "q", k.shape, k.dtype, dev), _arg(k, "k", k.shape, k.dtype, dev),
+            _arg(v, "v", (B, H, N, dv), k.dtype, dev), _arg(beta, "beta", gates, f32, dev),
+            _arg(log_alpha, "log_alpha", gates, f32, dev),
+            _arg(out, "out", (B, H, N, dv), k.dtype, dev), _arg(S0, "S0", state, f32, dev),
+            _arg(S_out, "S_out", state, f32, dev))
+    ws = call.scratch(workspace, la_delta_workspace_size(B, H, Hk, N, d, dv, k.dtype))
+    code = _lib.la_forward_delta(*ptrs, B, H, Hk, N, d, dv, _fm(feature_map),
+                                 d ** -0.5 if scale is None else float(scale), _dtype(k), *ws,
+                                 call.handle)
+    _check(code, "la_forward_delta")
+    return out, S_out
+
+
+def la_decode_step_delta(S: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         beta: torch.Tensor, log_alpha: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, *, feature_map="l2",
+                         scale: float | None = None, stream=None) -> torch.Tensor:
+    """One token per sequence: q, k [B,Hk,d], v [B,H,dv], beta and log_alpha
+    [B,H]; S [B,H,d,dv] updated in place -> out [B,H,dv] in v's type."""
+    if k.dim() != 3:
+        raise ValueError("k must be [B,Hk,d]")
+    dev = _current(k, "k")
+    B, H, Hk, d, dv = _delta_sizes(k, v)
+    call = _Call(stream, dev)
+    if out is None:
+        out = call.empty((B, H, dv), k.dtype)
+    f32 = torch.float32
+    code = _lib.la_decode_step_delta(
+        _arg(S, "S", (B, H, d, dv), f32, dev), _arg(q, "q", k.shape, k.dtype, dev),
+        _arg(k, "k", k.shape, k.dtype, dev), _arg(v, "v", (B, H, dv), k.dtype, dev),
+        _arg(beta, "beta", (B, H), f32, dev), _arg(log_alpha, "log_alpha", (B, H), f32, dev),
+        _arg(out, "out", (B, H, dv), k.dtype, dev), B, H, Hk, d, dv, _fm(feature_map),
+        d ** -0.5 if scale is None else float(scale), _dtype(k), call.handle)
+    _check(code, "la_decode_step_delta")
+    return out
+
+
+def la_backward_delta(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      beta: torch.Tensor, log_alpha: torch.Tensor | None = None, *,
+                      feature_map="l2", scale: float | None = None,
+                      S0: torch.Tensor | None = None, dS_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of la_forward_delta -> (dq, dk, dv, dbeta, dlog_alpha, dS0),
+    with None for dlog_alpha without log_alpha and for dS0 without S0.  dout
+    and dS_out (None: zero) are the gradients of out and of the final state."""
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hk,N,d]")
+    dev = _current(k, "k")
+    B, H, Hk, d, dv = _delta_sizes(k, v)
+    N = k.shape[2]
+    call = _Call(stream, dev)
+    f32, gates, state, vs = torch.float32, (B, H, N), (B, H, d, dv), (B, H, N, dv)
+    ins = (_arg(dout, "dout", vs, k.dtype, dev), _arg(dS_out, "dS_out", state, f32, dev),
+           _arg(q, "q", k.shape, k.dtype, dev), _arg(k, "k", k.shape, k.dtype, dev),
+           _arg(v, "v", vs, k.dtype, dev), _arg(beta, "beta", gates, f32, dev),
+           _arg(log_alpha, "log_alpha", gates, f32, dev), _arg(S0, "S0", state, f32, dev))
+    grads = (call.empty(k.shape, k.dtype), call.empty(k.shape, k.dtype), call.empty(vs, k.dtype),
+             call.empty(gates, f32), call.empty(gates, f32) if log_alpha is not None else None,
+             call.empty(state, f32) if S0 is not None else None)
+    ws = call.scratch(workspace, la_delta_backward_workspace_size(B, H, Hk, N, d, dv, k.dtype))
+    code = _lib.la_backward_delta(*ins, *(None if g is None else g.data_ptr() for g in grads), B, H,
+                                  Hk, N, d, dv, _fm(feature_map),
+                                  d ** -0.5 if scale is None else float(scale), _dtype(k), *ws,
+                                  call.handle)
+    _check(code, "la_backward_delta")
+    return grads
+
+
+def _act(activation) -> int:
+    return ACTIVATIONS[activation] if isinstance(activation, str) else int(activation)
+
+
+def _norm_weight(weight, H, dv, dev):
+    """(pointer, 1 if there is a row for each head)."""
+    heads = weight is not None and weight.dim() == 2
+    return _arg(weight, "weight", (H, dv) if heads else (dv,), torch.float32, dev), int(heads)
+
+
+def la_norm_gate_backward_workspace_size(B, H, N, dv) -> int:
+    return int(_lib.la_norm_gate_backward_workspace_size(B, H, N, dv))
+
+
+def la_norm_gate(x: torch.Tensor, gate: torch.Tensor | None = None,
+                 weight: torch.Tensor | None = None, y: torch.Tensor | None = None, *,
+                 activation="silu", eps: float = 1e-6, stream=None) -> torch.Tensor:
+    """Head-major x [B,H,N,dv] -> token-major y [B,N,H,dv]: RMS norm of each
+    row, times weight (fp32 [dv] or [H,dv]), times activation(gate) with gate
+    [B,N,H,dv].  y has gate's type (x's without a gate, or that of a given y)."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B,H,N,dv]")
+    dev = _current(x, "x")
+    B, H, N, dv = x.shape
+    call = _Call(stream, dev)
+    dtype = gate.dtype if gate is not None else y.dtype if y is not None else x.dtype
+    if y is None:
+        y = call.empty((B, N, H, dv), dtype)
+    _dtype(y)
+    w, heads = _norm_weight(weight, H, dv, dev)
+    code = _lib.la_norm_gate(_arg(x, "x", x.shape, x.dtype, dev),
+                             _arg(gate, "gate", (B, N, H, dv), dtype, dev), w,
+                             _arg(y, "y", (B, N, H, dv), dtype, dev), B, H, N, dv,
+                             _act(activation), heads, float(eps), _dtype(x), DTYPES[dtype],
+                             call.handle)
+    _check(code, "la_norm_gate")
+    return y
+
+
+def la_norm_gate_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor | None = None,
+                          weight: torch.Tensor | None = None, *, activation="silu",
+                          eps: float = 1e-6, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of la_norm_gate from dy [B,N,H,dv] -> (dx [B,H,N,dv], dgate,
+    dweight), None for a gate or weight that was not given."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B,H,N,dv]")
+    dev = _current(x, "x")
+    B, H, N, dv = x.shape
+    call = _Call(stream, dev)
+    _dtype(dy)
+    w, heads = _norm_weight(weight, H, dv, dev)
+    ins = (_arg(dy, "dy", (B, N, H, dv), dy.dtype, dev), _arg(x, "x", x.shape, x.dtype, dev),
+           _arg(gate, "gate", (B, N, H, dv), dy.dtype, dev), w)
+    grads = (call.empty(x.shape, x.dtype),
+             call.empty(dy.shape, dy.dtype) if gate is not None else None,
+             call.empty(weight.shape, torch.float32) if weight is not None else None)
+    need = la_norm_gate_backward_workspace_size(B, H, N, dv) if weight is not None else 0
+    ws = call.scratch(workspace, need)
+    code = _lib.la_norm_gate_backward(*ins, *(None if g is None else g.data_ptr() for g in grads),
+                                      B, H, N, dv, _act(activation), heads, float(eps), _dtype(x),
+                                      _dtype(dy), *ws, call.handle)
+    _check(code, "la_norm_gate_backward")
+    return grads
 
 
 def la_forward_path(B, H, N, d, dv, causal=True, feature_map="elu1", has_decay=False,

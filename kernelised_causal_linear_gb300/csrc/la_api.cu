@@ -403,6 +403,207 @@ la_status la_decode_step_gla(float* S, float* z, const void* q, const void* k, c
     return from_cuda(decode_step(a));
 }
 
+// Sizes, enums and scale of the delta-rule calls.
+static la_status check_delta(const DeltaArgs& a)
+{
+    if (a.B < 1 || a.H < 1 || a.Hk < 1 || a.N < 0 || a.d < 1 || a.dv < 1 || a.H % a.Hk)
+        return LA_ERR_INVALID_ARG;
+    if (a.fm != LA_FM_ELU1 && a.fm != LA_FM_IDENTITY_NORM && a.fm != LA_FM_NONE && a.fm != LA_FM_L2)
+        return LA_ERR_INVALID_ARG;
+    if ((a.dtype != LA_BF16 && a.dtype != LA_FP32) || !isfinite(a.scale))
+        return LA_ERR_INVALID_ARG;
+    if (!dim_ok(a.d) || !dim_ok(a.dv) || (a.fm != LA_FM_NONE && a.fm != LA_FM_L2))
+        return LA_ERR_UNSUPPORTED;
+    if (a.B > INT32_MAX / a.H || !delta_grid_ok(a))
+        return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// NULL where `need` is not set, else a 16-byte aligned pointer.
+static bool ptr_ok(const void* p, bool need = true) { return p ? aligned16(p) : !need; }
+
+static bool workspace_ok(const void* ws, size_t bytes, size_t need)
+{
+    return need == 0 || (ws && bytes >= need && aligned256(ws));
+}
+
+static DeltaArgs delta_sizes(int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv, int fm,
+                             float scale, int dtype)
+{
+    DeltaArgs a{};
+    a.B = B, a.H = H, a.Hk = Hk, a.N = N, a.d = d, a.dv = dv;
+    a.fm = fm, a.scale = scale, a.dtype = dtype;
+    return a;
+}
+
+// dst <- src, or zero for a NULL src (the state of an empty sequence)
+static la_status copy_state(float* dst, const float* src, const DeltaArgs& a)
+{
+    const size_t n = sizeof(float) * (size_t)(a.B * a.H) * a.d * a.dv;
+    if (!dst || dst == src)
+        return LA_OK;
+    return from_cuda(src ? cudaMemcpyAsync(dst, src, n, cudaMemcpyDeviceToDevice, a.stream)
+                         : cudaMemsetAsync(dst, 0, n, a.stream));
+}
+
+size_t la_delta_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv,
+                               int dtype)
+{
+    const DeltaArgs a = delta_sizes(B, H, Hk, N, d, dv, LA_FM_L2, 1.0f, dtype);
+    return check_delta(a) != LA_OK || N == 0 ? 0 : delta_forward_workspace(a);
+}
+
+la_status la_forward_delta(const void* q, const void* k, const void* v, const float* beta,
+                           const float* log_alpha, void* out, const float* S0, float* S_out,
+                           int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv,
+                           int feature_map, float scale, int dtype, void* workspace,
+                           size_t workspace_bytes, la_stream_t stream)
+{
+    DeltaArgs a = delta_sizes(B, H, Hk, N, d, dv, feature_map, scale, dtype);
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    const la_status st = check_delta(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S0, false) || !ptr_ok(S_out, false))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0)
+        return copy_state(S_out, S0, a);
+    if (!q != !out || (!out && !S_out) || !ptr_ok(q, false) || !ptr_ok(out, false) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(beta) ||
+        !ptr_ok(log_alpha, false))
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, delta_forward_workspace(a)))
+        return LA_ERR_WORKSPACE;
+    a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha, a.out = out;
+    a.S0 = S0, a.S_out = S_out, a.ws = workspace, a.ws_bytes = workspace_bytes;
+    return from_cuda(delta_forward(a));
+}
+
+la_status la_decode_step_delta(float* S, const void* q, const void* k, const void* v,
+                               const float* beta, const float* log_alpha, void* out, int64_t B,
+                               int64_t H, int64_t Hk, int d, int dv, int feature_map, float scale,
+                               int dtype, la_stream_t stream)
+{
+    DeltaArgs a = delta_sizes(B, H, Hk, 1, d, dv, feature_map, scale, dtype);
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    const la_status st = check_delta(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S) || !ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(beta) ||
+        !ptr_ok(log_alpha, false) || !ptr_ok(out))
+        return LA_ERR_INVALID_ARG;
+    a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha, a.out = out, a.S_out = S;
+    return from_cuda(delta_decode(a));
+}
+
+size_t la_delta_backward_workspace_size(int64_t B, int64_t H, int64_t Hk, int64_t N, int d, int dv,
+                                        int dtype)
+{
+    const DeltaArgs a = delta_sizes(B, H, Hk, N, d, dv, LA_FM_L2, 1.0f, dtype);
+    return check_delta(a) != LA_OK || N == 0 ? 0 : delta_backward_workspace(a);
+}
+
+la_status la_backward_delta(const void* dout, const float* dS_out, const void* q, const void* k,
+                            const void* v, const float* beta, const float* log_alpha,
+                            const float* S0, void* dq, void* dk, void* dv_out, float* dbeta,
+                            float* dlog_alpha, float* dS0, int64_t B, int64_t H, int64_t Hk,
+                            int64_t N, int d, int dv, int feature_map, float scale, int dtype,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream)
+{
+    DeltaArgs a = delta_sizes(B, H, Hk, N, d, dv, feature_map, scale, dtype);
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    const la_status st = check_delta(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S0, false) || !ptr_ok(dS_out, false) || !ptr_ok(dS0, false))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0)
+        return copy_state(dS0, dS_out, a);
+    if (!log_alpha != !dlog_alpha || !ptr_ok(dout) || !ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(beta) ||
+        !ptr_ok(log_alpha, false) || !ptr_ok(dq) || !ptr_ok(dk) || !ptr_ok(dv_out) ||
+        !ptr_ok(dbeta) || !ptr_ok(dlog_alpha, false))
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, delta_backward_workspace(a)))
+        return LA_ERR_WORKSPACE;
+    a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha;
+    a.S0 = S0, a.dout = dout, a.dS_out = dS_out, a.dq = dq, a.dk = dk, a.dv_ = dv_out;
+    a.dbeta = dbeta, a.dlog_alpha = dlog_alpha, a.dS0 = dS0;
+    a.ws = workspace, a.ws_bytes = workspace_bytes;
+    return from_cuda(delta_backward(a));
+}
+
+static la_status check_norm(const NormGateArgs& a)
+{
+    if (a.B < 1 || a.H < 1 || a.N < 0 || a.dv < 1 || !(a.eps > 0.0f) || !isfinite(a.eps))
+        return LA_ERR_INVALID_ARG;
+    if ((a.act != LA_ACT_SILU && a.act != LA_ACT_SIGMOID && a.act != LA_ACT_NONE) ||
+        (a.weight_heads != 0 && a.weight_heads != 1) ||
+        (a.x_dtype != LA_BF16 && a.x_dtype != LA_FP32) ||
+        (a.dtype != LA_BF16 && a.dtype != LA_FP32))
+        return LA_ERR_INVALID_ARG;
+    // rows and the blocks of a gradient are counted in a 32-bit grid
+    if (!dim_ok(a.dv) || a.H > (1 << 20) || a.B > INT32_MAX / a.H ||
+        (a.N > 0 && a.B * a.H > INT32_MAX / a.N))
+        return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+static NormGateArgs norm_sizes(int64_t B, int64_t H, int64_t N, int dv, int act, int weight_heads,
+                               float eps, int x_dtype, int dtype, la_stream_t stream)
+{
+    NormGateArgs a{};
+    a.B = B, a.H = H, a.N = N, a.dv = dv, a.act = act, a.weight_heads = weight_heads;
+    a.eps = eps, a.x_dtype = x_dtype, a.dtype = dtype;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return a;
+}
+
+la_status la_norm_gate(const void* x, const void* gate, const float* weight, void* y, int64_t B,
+                       int64_t H, int64_t N, int dv, int activation, int weight_heads, float eps,
+                       int x_dtype, int dtype, la_stream_t stream)
+{
+    NormGateArgs a = norm_sizes(B, H, N, dv, activation, weight_heads, eps, x_dtype, dtype, stream);
+    const la_status st = check_norm(a);
+    if (st != LA_OK || N == 0)
+        return st;
+    if (!ptr_ok(x) || !ptr_ok(y) || !ptr_ok(gate, false) || !ptr_ok(weight, false))
+        return LA_ERR_INVALID_ARG;
+    a.x = x, a.gate = gate, a.weight = weight, a.y = y;
+    return from_cuda(norm_gate(a));
+}
+
+size_t la_norm_gate_backward_workspace_size(int64_t B, int64_t H, int64_t N, int dv)
+{
+    const NormGateArgs a =
+        norm_sizes(B, H, N, dv, LA_ACT_SILU, 0, 1.0f, LA_FP32, LA_FP32, nullptr);
+    return check_norm(a) != LA_OK || N == 0 ? 0 : norm_gate_backward_workspace(a);
+}
+
+la_status la_norm_gate_backward(const void* dy, const void* x, const void* gate,
+                                const float* weight, void* dx, void* dgate, float* dweight,
+                                int64_t B, int64_t H, int64_t N, int dv, int activation,
+                                int weight_heads, float eps, int x_dtype, int dtype,
+                                void* workspace, size_t workspace_bytes, la_stream_t stream)
+{
+    NormGateArgs a = norm_sizes(B, H, N, dv, activation, weight_heads, eps, x_dtype, dtype, stream);
+    const la_status st = check_norm(a);
+    if (st != LA_OK)
+        return st;
+    if (!weight != !dweight || !ptr_ok(dweight, false))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0)
+        return !dweight ? LA_OK
+                        : from_cuda(cudaMemsetAsync(
+                              dweight, 0, sizeof(float) * (weight_heads ? H : 1) * dv, a.stream));
+    if (!gate != !dgate || !ptr_ok(dy) || !ptr_ok(x) || !ptr_ok(dx) || !ptr_ok(gate, false) || !ptr_ok(dgate, false) ||
+        !ptr_ok(weight, false))
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, weight ? norm_gate_backward_workspace(a) : 0))
+        return LA_ERR_WORKSPACE;
+    a.dy = dy, a.x = x, a.gate = gate, a.weight = weight, a.dx = dx, a.dgate = dgate;
+    a.dweight = dweight, a.ws = workspace;
+    return from_cuda(norm_gate_backward(a));
+}
+
 la_status la_state_prefix(const float* S_parts, const float* z_parts, int nparts,
                           const int64_t* part_len, int upto, float* S_out, float* z_out,
                           int64_t B, int64_t H, int d, int dv, const float* gamma,

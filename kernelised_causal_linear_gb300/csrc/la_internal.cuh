@@ -40,6 +40,13 @@ template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16
     return __bfloat162float(x);
 }
 
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x)
+{
+    return __float2bfloat16_rn(x);
+}
+
 // The feature map in fp32: elu(x)+1 = max(x,0) + exp(min(x,0)), or identity.
 __device__ __forceinline__ float phi_f32(float x, int fm)
 {
@@ -139,6 +146,60 @@ cudaError_t state_prefix(const float* S, const float* z, int nparts, const int64
 bool favor_shape_ok(int d, int r);
 cudaError_t favor_features(const void* x, const float* w, void* out, int64_t rows, int d, int r,
                            int in_dtype, int out_dtype, int* status, cudaStream_t st);
+
+// gated delta rule (la_forward_delta, la_decode_step_delta, la_backward_delta).
+// q and k have Hk heads; value head h reads key head h / (H / Hk).
+struct DeltaArgs {
+    const void* q;           // [B,Hk,N,d], NULL for a state-only forward
+    const void* k;           // [B,Hk,N,d]
+    const void* v;           // [B,H,N,dv]
+    const float* beta;       // [B,H,N]
+    const float* log_alpha;  // [B,H,N], or NULL for no decay
+    void* out;               // [B,H,N,dv] in dtype
+    const float* S0;         // [B,H,d,dv], or NULL for a zero start
+    float* S_out;            // [B,H,d,dv], or NULL; decode: the state, updated in place
+    int64_t B, H, Hk, N;
+    int d, dv, fm, dtype;
+    float scale;
+    void* ws;
+    size_t ws_bytes;
+    cudaStream_t stream;
+    // gradients (la_backward_delta)
+    const void* dout;        // [B,H,N,dv]
+    const float* dS_out;     // [B,H,d,dv], or NULL for zero
+    void* dq;                // [B,Hk,N,d]
+    void* dk;
+    void* dv_;               // [B,H,N,dv]
+    float* dbeta;            // [B,H,N]
+    float* dlog_alpha;       // [B,H,N], NULL when log_alpha is
+    float* dS0;              // [B,H,d,dv], or NULL
+};
+size_t delta_forward_workspace(const DeltaArgs& a);
+size_t delta_backward_workspace(const DeltaArgs& a);
+bool delta_grid_ok(const DeltaArgs& a);
+cudaError_t delta_forward(const DeltaArgs& a);
+cudaError_t delta_decode(const DeltaArgs& a);
+cudaError_t delta_backward(const DeltaArgs& a);
+
+// per-head RMS norm with weight and gate (la_norm_gate, la_norm_gate_backward)
+struct NormGateArgs {
+    const void* x;           // [B,H,N,dv]
+    const void* gate;        // [B,N,H,dv], or NULL
+    const float* weight;     // [dv] or [H,dv], or NULL
+    void* y;                 // [B,N,H,dv]
+    const void* dy;          // [B,N,H,dv]
+    void* dx;                // [B,H,N,dv]
+    void* dgate;             // [B,N,H,dv], NULL when gate is
+    float* dweight;          // as weight, NULL when weight is
+    int64_t B, H, N;
+    int dv, act, weight_heads, x_dtype, dtype;
+    float eps;
+    void* ws;
+    cudaStream_t stream;
+};
+size_t norm_gate_backward_workspace(const NormGateArgs& a);
+cudaError_t norm_gate(const NormGateArgs& a);
+cudaError_t norm_gate_backward(const NormGateArgs& a);
 
 struct DecodeArgs {
     float* S;

@@ -1,0 +1,293 @@
+// la_norm.cu -- per-head RMS norm with weight and gate behind the heads'
+// outputs, and its gradient.
+//
+//   xh = x rsqrt(mean(x^2) + eps),   y = w xh act(gate)
+//   c  = dy w act(gate),  dx = r (c - xh mean(c xh)),  r = rsqrt(mean(x^2) + eps)
+//   dgate = dy w xh act'(gate),  dw = sum over rows of dy xh act(gate)
+//
+// x is head-major [B,H,N,dv] as the attention kernels write it; gate and y are
+// token-major [B,N,H,dv] as the projections around them read it, so the
+// transposition costs no pass of its own.  A row is dv / 8 lanes of eight
+// elements (16 bytes of bf16): its sums are shuffles, and each tensor is read
+// or written once.  Bound by HBM.
+#include "la_internal.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Row8 {
+    float f[8];
+};
+
+__device__ __forceinline__ Row8 load8(const float* p)
+{
+    Row8 r;
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
+    r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
+    return r;
+}
+
+__device__ __forceinline__ Row8 load8(const __nv_bfloat16* p)
+{
+    Row8 r;
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.f[2 * i] = __uint_as_float(u[i] << 16);
+        r.f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    return r;
+}
+
+__device__ __forceinline__ void store8(float* p, const Row8& r)
+{
+    __stcs(reinterpret_cast<float4*>(p), make_float4(r.f[0], r.f[1], r.f[2], r.f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.f[4], r.f[5], r.f[6], r.f[7]));
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Row8& r)
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(r.f[2 * i], r.f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
+}
+
+// sum over the LPR lanes of a row (LPR a power of two, rows aligned in the warp)
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// act(g) and act'(g)
+__device__ __forceinline__ float2 activate(float g, int act)
+{
+    if (act == LA_ACT_NONE)
+        return make_float2(g, 1.0f);
+    const float s = 1.0f / (1.0f + expf(-g));
+    if (act == LA_ACT_SIGMOID)
+        return make_float2(s, s * (1.0f - s));
+    return make_float2(g * s, s * (1.0f + g * (1.0f - s)));
+}
+
+// Rows in token-major order, kRows per lane group with every load issued first.
+constexpr int kRows = 2;
+
+template <int DV, typename TX, typename T>
+__global__ void __launch_bounds__(kThreads)
+    k_norm_gate(const TX* __restrict__ x, const T* __restrict__ gate, const float* __restrict__ w,
+                T* __restrict__ y, int64_t rows, int64_t N, int H, int act, int weight_heads,
+                float eps)
+{
+    constexpr int LPR = DV / 8, RPC = kThreads / LPR;
+    const int sub = threadIdx.x % LPR;
+    Row8 xr[kRows], gr[kRows];
+    int64_t row[kRows];
+    int head[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        row[i] = ((int64_t)blockIdx.x * kRows + i) * RPC + threadIdx.x / LPR;
+        const int64_t at = min(row[i], rows - 1);  // lanes past the end read the last row, write nothing
+        const int64_t bn = at / H;
+        head[i] = (int)(at % H);
+        xr[i] = load8(x + ((bn / N * H + head[i]) * N + bn % N) * DV + sub * 8);
+        if (gate)
+            gr[i] = load8(gate + at * DV + sub * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            ss = fmaf(xr[i].f[j], xr[i].f[j], ss);
+        const float r = rsqrtf(row_sum<LPR>(ss) * (1.0f / DV) + eps);
+        Row8 o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            o.f[j] = xr[i].f[j] * r;
+            if (w)
+                o.f[j] *= w[(weight_heads ? head[i] * DV : 0) + sub * 8 + j];
+            if (gate)
+                o.f[j] *= activate(gr[i].f[j], act).x;
+        }
+        if (row[i] < rows)
+            store8(y + row[i] * DV + sub * 8, o);
+    }
+}
+
+// Gradient.  Block h * X + i takes every X-th group of head h's rows, so a
+// block's part of dw belongs to one head; part [H X][DV] is summed by k_norm_dw
+// in a fixed order (no atomics: repeat runs are bitwise equal).
+template <int DV, typename TX, typename T>
+__global__ void __launch_bounds__(kThreads)
+    k_norm_gate_grad(const T* __restrict__ dy, const TX* __restrict__ x, const T* __restrict__ gate,
+                     const float* __restrict__ w, TX* __restrict__ dx, T* __restrict__ dgate,
+                     float* __restrict__ part, int64_t BN, int64_t N, int H, int X, int act,
+                     int weight_heads, float eps)
+{
+    constexpr int LPR = DV / 8, RPC = kThreads / LPR;
+    __shared__ float sw[RPC][DV];
+    const int sub = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const int h = blockIdx.x / X;
+    Row8 wr, acc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        wr.f[j] = w ? w[(weight_heads ? h * DV : 0) + sub * 8 + j] : 1.0f;
+        acc.f[j] = 0.f;
+    }
+    for (int64_t base = (int64_t)(blockIdx.x % X) * RPC; base < BN; base += (int64_t)X * RPC) {
+        const bool live = base + grp < BN;
+        const int64_t bn = live ? base + grp : BN - 1;
+        const int64_t xa = ((bn / N * H + h) * N + bn % N) * DV + sub * 8;
+        const int64_t ya = (bn * H + h) * DV + sub * 8;
+        const Row8 xr = load8(x + xa), dr = load8(dy + ya);
+        Row8 gr;
+        if (gate)
+            gr = load8(gate + ya);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            ss = fmaf(xr.f[j], xr.f[j], ss);
+        const float r = rsqrtf(row_sum<LPR>(ss) * (1.0f / DV) + eps);
+        Row8 c, dg;
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float xh = xr.f[j] * r;
+            const float2 a = gate ? activate(gr.f[j], act) : make_float2(1.0f, 0.0f);
+            const float t = dr.f[j] * xh;
+            if (live)
+                acc.f[j] = fmaf(t, a.x, acc.f[j]);
+            dg.f[j] = t * wr.f[j] * a.y;
+            c.f[j] = dr.f[j] * wr.f[j] * a.x;
+            dot = fmaf(c.f[j], xh, dot);
+        }
+        dot = row_sum<LPR>(dot) * (1.0f / DV);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c.f[j] = r * (c.f[j] - xr.f[j] * r * dot);
+        if (live) {
+            store8(dx + xa, c);
+            if (gate)
+                store8(dgate + ya, dg);
+        }
+    }
+    if (part) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sw[grp][sub * 8 + j] = acc.f[j];
+        __syncthreads();
+        if (threadIdx.x < DV) {
+            float s = 0.f;
+            for (int i = 0; i < RPC; ++i)
+                s += sw[i][threadIdx.x];
+            part[(int64_t)blockIdx.x * DV + threadIdx.x] = s;
+        }
+    }
+}
+
+// dw[head or 0][c] = sum of the blocks' parts; 32 columns x 32 partial sums per block
+__global__ void __launch_bounds__(1024)
+    k_norm_dw(const float* __restrict__ part, float* __restrict__ dw, int64_t count, int DV)
+{
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int per = DV / 32;
+    const int64_t set = blockIdx.x / per;
+    const int c = blockIdx.x % per * 32 + lane;
+    float x = 0.f;
+    for (int64_t i = grp; i < count; i += 32)
+        x += part[(set * count + i) * DV + c];
+    s[grp][lane] = x;
+    __syncthreads();
+    if (grp == 0) {
+        x = 0.f;
+        for (int i = 0; i < 32; ++i)
+            x += s[i][lane];
+        dw[set * DV + c] = x;
+    }
+}
+
+// Blocks per head of the gradient: about four waves of eight resident blocks
+// per SM in all, no more than there are row groups.
+int64_t grad_blocks(const NormGateArgs& a)
+{
+    const int64_t rpc = kThreads / (a.dv / 8);
+    const int64_t groups = (a.B * a.N + rpc - 1) / rpc;
+    const int64_t want = (4 * 8 * 152 + a.H - 1) / a.H;
+    return want < groups ? want : groups;
+}
+
+template <int DV, typename TX, typename T>
+cudaError_t run_norm(const NormGateArgs& a, bool grad)
+{
+    const TX* x = static_cast<const TX*>(a.x);
+    const T* gate = static_cast<const T*>(a.gate);
+    if (!grad) {
+        const int64_t rows = a.B * a.N * a.H;
+        const int64_t per = (int64_t)kRows * (kThreads / (DV / 8));
+        k_norm_gate<DV, TX, T><<<(unsigned)((rows + per - 1) / per), kThreads, 0, a.stream>>>(
+            x, gate, a.weight, static_cast<T*>(a.y), rows, a.N, (int)a.H, a.act, a.weight_heads,
+            a.eps);
+        count_launches(1);
+        return cudaGetLastError();
+    }
+    const int64_t X = grad_blocks(a);
+    float* part = a.dweight ? static_cast<float*>(a.ws) : nullptr;
+    k_norm_gate_grad<DV, TX, T><<<(unsigned)(a.H * X), kThreads, 0, a.stream>>>(
+        static_cast<const T*>(a.dy), x, gate, a.weight, static_cast<TX*>(a.dx),
+        static_cast<T*>(a.dgate), part, a.B * a.N, a.N, (int)a.H, (int)X, a.act, a.weight_heads,
+        a.eps);
+    count_launches(1);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !part)
+        return e;
+    const int64_t sets = a.weight_heads ? a.H : 1;
+    k_norm_dw<<<(unsigned)(sets * (DV / 32)), 1024, 0, a.stream>>>(part, a.dweight, a.H * X / sets,
+                                                                   DV);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int DV>
+cudaError_t norm_types(const NormGateArgs& a, bool grad)
+{
+    if (a.x_dtype == LA_BF16)
+        return a.dtype == LA_BF16 ? run_norm<DV, __nv_bfloat16, __nv_bfloat16>(a, grad)
+                                  : run_norm<DV, __nv_bfloat16, float>(a, grad);
+    return a.dtype == LA_BF16 ? run_norm<DV, float, __nv_bfloat16>(a, grad)
+                              : run_norm<DV, float, float>(a, grad);
+}
+
+cudaError_t norm_dims(const NormGateArgs& a, bool grad)
+{
+    switch (a.dv) {
+    case 32: return norm_types<32>(a, grad);
+    case 64: return norm_types<64>(a, grad);
+    default: return norm_types<128>(a, grad);
+    }
+}
+
+}  // namespace
+
+size_t norm_gate_backward_workspace(const NormGateArgs& a)
+{
+    return sizeof(float) * (size_t)(a.H * grad_blocks(a)) * a.dv;
+}
+
+cudaError_t norm_gate(const NormGateArgs& a) { return norm_dims(a, false); }
+cudaError_t norm_gate_backward(const NormGateArgs& a) { return norm_dims(a, true); }
+
+}  // namespace la
