@@ -475,6 +475,7 @@ la_status la_forward_delta(const void* q, const void* k, const void* v, const fl
         return LA_ERR_WORKSPACE;
     a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha, a.out = out;
     a.S0 = S0, a.S_out = S_out, a.ws = workspace, a.ws_bytes = workspace_bytes;
+    a.status = status_ptr();
     return from_cuda(delta_forward(a));
 }
 
@@ -528,6 +529,7 @@ la_status la_backward_delta(const void* dout, const float* dS_out, const void* q
     a.S0 = S0, a.dout = dout, a.dS_out = dS_out, a.dq = dq, a.dk = dk, a.dv_ = dv_out;
     a.dbeta = dbeta, a.dlog_alpha = dlog_alpha, a.dS0 = dS0;
     a.ws = workspace, a.ws_bytes = workspace_bytes;
+    a.status = status_ptr();
     return from_cuda(delta_backward(a));
 }
 

@@ -680,12 +680,17 @@ bool delta_grid_ok(const DeltaArgs& a)
     return a.N <= most && rec_blocks(a.N) + 1 <= most / (a.B * a.H) && a.B * a.Hk <= most / (a.N > 0 ? a.N : 1);
 }
 
-size_t delta_forward_workspace(const DeltaArgs&) { return 0; }
+size_t delta_forward_workspace(const DeltaArgs& a)
+{
+    return delta_tc_eligible(a) ? delta_tc_forward_workspace(a) : 0;
+}
 
 size_t delta_backward_workspace(const DeltaArgs& a) { return grad_layout(a).total; }
 
 cudaError_t delta_forward(const DeltaArgs& a)
 {
+    if (delta_tc_eligible(a))
+        return delta_tc_forward(a);
     const bool bf = a.dtype == LA_BF16;
     switch (a.d) {
     case 32: return bf ? run_rec<32, __nv_bfloat16>(a, nullptr, nullptr) : run_rec<32, float>(a, nullptr, nullptr);

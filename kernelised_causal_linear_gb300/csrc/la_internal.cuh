@@ -163,6 +163,7 @@ struct DeltaArgs {
     float scale;
     void* ws;
     size_t ws_bytes;
+    int* status;             // device status word
     cudaStream_t stream;
     // gradients (la_backward_delta)
     const void* dout;        // [B,H,N,dv]
@@ -180,6 +181,10 @@ bool delta_grid_ok(const DeltaArgs& a);
 cudaError_t delta_forward(const DeltaArgs& a);
 cudaError_t delta_decode(const DeltaArgs& a);
 cudaError_t delta_backward(const DeltaArgs& a);
+// tensor-core path (bf16), chosen by the three calls above
+bool delta_tc_eligible(const DeltaArgs& a);
+size_t delta_tc_forward_workspace(const DeltaArgs& a);
+cudaError_t delta_tc_forward(const DeltaArgs& a);
 
 // per-head RMS norm with weight and gate (la_norm_gate, la_norm_gate_backward)
 struct NormGateArgs {
