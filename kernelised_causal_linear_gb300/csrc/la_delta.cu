@@ -685,7 +685,10 @@ size_t delta_forward_workspace(const DeltaArgs& a)
     return delta_tc_eligible(a) ? delta_tc_forward_workspace(a) : 0;
 }
 
-size_t delta_backward_workspace(const DeltaArgs& a) { return grad_layout(a).total; }
+size_t delta_backward_workspace(const DeltaArgs& a)
+{
+    return delta_tc_eligible(a) ? delta_tc_backward_workspace(a) : grad_layout(a).total;
+}
 
 cudaError_t delta_forward(const DeltaArgs& a)
 {
@@ -711,6 +714,8 @@ cudaError_t delta_decode(const DeltaArgs& a)
 
 cudaError_t delta_backward(const DeltaArgs& a)
 {
+    if (delta_tc_eligible(a))
+        return delta_tc_backward(a);
     switch (a.d) {
     case 32: return grad_dims<32>(a);
     case 64: return grad_dims<64>(a);

@@ -43,7 +43,8 @@ __device__ __forceinline__ void h2_split(float a, float b, uint32_t& hi, uint32_
 }
 
 // The power of two that brings m (>= 0) to [2^8, 2^9), and its inverse.  Zero
-// and numbers too small to be scaled in one step get the largest scale.
+// and numbers under 2^-118 get the largest scale, 2^126: an operand's own factors
+// are multiplied in before it, so that no product of scales overflows.
 struct Pow2 {
     float to, from;
 };

@@ -184,7 +184,9 @@ cudaError_t delta_backward(const DeltaArgs& a);
 // tensor-core path (bf16), chosen by the three calls above
 bool delta_tc_eligible(const DeltaArgs& a);
 size_t delta_tc_forward_workspace(const DeltaArgs& a);
+size_t delta_tc_backward_workspace(const DeltaArgs& a);
 cudaError_t delta_tc_forward(const DeltaArgs& a);
+cudaError_t delta_tc_backward(const DeltaArgs& a);
 
 // per-head RMS norm with weight and gate (la_norm_gate, la_norm_gate_backward)
 struct NormGateArgs {

@@ -451,3 +451,15 @@ def test_refusals_of_the_binding():
         la.la_decode_step_delta(p["S0"], *a)
     with pytest.raises(ValueError):
         la.la_norm_gate(p["dout"], p["dout"])
+
+
+def test_backward_with_a_loss_scale():
+    """Output gradients of 2^16 and more beside rows that get none (beta = 0, no
+    state yet): scales of operands that are zero multiply scales of large ones."""
+    p = problem(1, 2, 2, 130, 64, 64, BF, 26, state=False)
+    p["dout"] = (p["dout"].float() * 2.0 ** 18).to(BF)
+    p["beta"][:, :, :3] = 0
+    p["beta"][:, :, 64:70] = 0
+    check_backward(p)
+    p["dout"] = (p["dout"].float() * 2.0 ** -70).to(BF)
+    check_backward(p)
