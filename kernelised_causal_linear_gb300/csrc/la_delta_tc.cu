@@ -78,7 +78,7 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // ------------------------------------------------------------- k_delta_prep --
 // 4 warps.  The Gram products are exact fp16 MMAs on the lower blocks; F is
 // fp32 on the CUDA cores in 16 x 16 blocks: the diagonal ones by substitution
-// (a column per lane), then by distance from the diagonal
+// (a column per lane), then by distance from the diagonal, all threads on each,
 //   X = A_IJ + sum_{J <= L < I} A_IL beta_L F_LJ,   F_IJ = -X - F_II beta_I X.
 constexpr int kPrepThreads = 128;
 constexpr int kLd = 68;  // row stride of the fp32 tiles (16-byte rows, spread over banks)
@@ -89,7 +89,7 @@ struct PrepSmem {
     static constexpr int A = img;
     static constexpr int F = A + kC * kLd * 4;
     static constexpr int X = F + kC * kLd * 4;
-    static constexpr int vec = X + 4 * 16 * 20 * 4;
+    static constexpr int vec = X + 3 * 16 * 20 * 4;
     static constexpr int bytes = vec + (8 + n_factors<GRAD>()) * kC * 4;
 };
 
@@ -291,43 +291,38 @@ __global__ void __launch_bounds__(kPrepThreads)
         }
     }
     __syncthreads();
-    float* sX = reinterpret_cast<float*>(smem + SM::X) + warp * 16 * 20;
+    // off-diagonal blocks, all threads on the 4 - dist blocks of a distance: thread
+    // -> row of a block and 2 (dist 1: 6, dist 2: 4) of its columns
+    float* sX = reinterpret_cast<float*>(smem + SM::X);  // [block][16][20]
+#pragma unroll
     for (int dist = 1; dist < 4; ++dist) {
-        const int J = warp, I = J + dist;
-        if (I < 4) {
-            const int r = lane >> 1, c0 = (lane & 1) * 8;
-            const float* arow = sA + (16 * I + r) * kLd;
-            float x[8];
+        const int r = (tid >> 3) & 15, c0 = (tid & 7) * 2;
+        float x[3][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = arow[16 * J + c0 + i];
-            for (int l = 16 * J; l < 16 * I; ++l) {
+        for (int J = 0; J < 4 - dist; ++J) {
+            const float* arow = sA + (16 * (J + dist) + r) * kLd;
+            x[J][0] = arow[16 * J + c0], x[J][1] = arow[16 * J + c0 + 1];
+#pragma unroll 8
+            for (int l = 16 * J; l < 16 * (J + dist); ++l) {
                 const float a = arow[l] * sb[l];
-                const float4 u = *reinterpret_cast<const float4*>(sF + l * kLd + 16 * J + c0);
-                const float4 v = *reinterpret_cast<const float4*>(sF + l * kLd + 16 * J + c0 + 4);
-                x[0] = fmaf(a, u.x, x[0]), x[1] = fmaf(a, u.y, x[1]);
-                x[2] = fmaf(a, u.z, x[2]), x[3] = fmaf(a, u.w, x[3]);
-                x[4] = fmaf(a, v.x, x[4]), x[5] = fmaf(a, v.y, x[5]);
-                x[6] = fmaf(a, v.z, x[6]), x[7] = fmaf(a, v.w, x[7]);
+                const float2 f = *reinterpret_cast<const float2*>(sF + l * kLd + 16 * J + c0);
+                x[J][0] = fmaf(a, f.x, x[J][0]), x[J][1] = fmaf(a, f.y, x[J][1]);
             }
+            *reinterpret_cast<float2*>(sX + (J * 16 + r) * 20 + c0) = make_float2(x[J][0], x[J][1]);
+        }
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sX[r * 20 + c0 + i] = x[i];
-            __syncwarp();
+        for (int J = 0; J < 4 - dist; ++J) {
+            const int I = J + dist;
             const float* frow = sF + (16 * I + r) * kLd + 16 * I;
+            float y0 = -x[J][0], y1 = -x[J][1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = -x[i];
-            for (int l = 0; l < r; ++l) {
+            for (int l = 0; l < 16; ++l) {  // F_II is zero from its diagonal on
                 const float a = -frow[l] * sb[16 * I + l];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = fmaf(a, sX[l * 20 + c0 + i], x[i]);
+                const float2 f = *reinterpret_cast<const float2*>(sX + (J * 16 + l) * 20 + c0);
+                y0 = fmaf(a, f.x, y0), y1 = fmaf(a, f.y, y1);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sF[(16 * I + r) * kLd + 16 * J + c0 + i] = x[i];
-            __syncwarp();
+            *reinterpret_cast<float2*>(sF + (16 * I + r) * kLd + 16 * J + c0) = make_float2(y0, y1);
         }
         __syncthreads();
     }
@@ -1264,34 +1259,50 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
 //          - sum_{i<j} D_ji (dV_j.U_i) k_i - e^{G_j} S0 dV_j + e^{G_C-G_j} dS1 U_j
 //
 // then through scale and norm to the inputs.  Warps 0-3 own 16 tokens of dQ
-// each, warps 4-7 of dK.  A row's products all run under one power of two into
-// one set of accumulators.  Kept planes carry a scale per value column, which is
-// the contracted index here: it goes to the A operand, whose registers are
-// rescaled before use.  One fp16 part each (2^-12 of a term, under the results'
-// own rounding to bf16).  The warps of threads 0-63 also finish dbeta and
-// dlog_alpha from the columns' dots.
+// each, warps 4-7 of dK.  The kept planes arrive with a scale per value column,
+// the contracted index here; they are brought under one scale each in shared
+// memory (a power of two: exact but for columns under 2^-24 of the largest), so
+// that fragments go from ldmatrix into the MMA as they are and every factor is
+// one of a row, applied to fp32 accumulators.  The 64 x 64 matrices pass through a
+// tile of the warp's own as fp16 rows under a power of two each.  One fp16 part
+// throughout (2^-12 of a term, under the results' own rounding to bf16).
+// Loops over fragments stay rolled: unrolled, the two roles' code overran the
+// instruction cache and its misses were half of all stalls.
 constexpr int kDqkThreads = 256;
+constexpr int kLdD = 66;  // row stride of the decay matrix
 
 template <int D, int DV>
 struct DqkSmem {
     static constexpr int K = 0, Q = row_image<D>(), E = 2 * row_image<D>(), dV = E + kC * DV * 2,
                          dO = dV + kC * DV * 2, S = dO + kC * DV * 2, dS = S + D * DV * 2,
-                         vec = dS + D * DV * 2, cols = vec + 16 * kC * 4, bytes = cols + 4 * DV * 4 + 64;
+                         tile = dS + D * DV * 2, dm = tile + 8 * 16 * 128, vec = dm + kC * kLdD * 4,
+                         cols = vec + 16 * kC * 4, bytes = cols + 4 * DV * 4 + 64;
 };
 
-// A fragments rescaled: x (fp16 pairs, columns 2 tq ..) times the column factors
-// f, the row factors r0 (rows g), r1 (rows g + 8) and the rows' powers of two
-__device__ __forceinline__ void rescale(const uint32_t (&x)[4], float2 f0, float2 f1, float r0, float r1,
-                                        float t0, float t1, float (&y)[8])
+// Kept blocks (16 value columns x 16) times their columns' factors c[col] / m
+__device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int per_slice, const float* c, float inv_m)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-        const float2 f = i >> 1 ? f1 : f0;
-        const float r = i & 1 ? r1 : r0, t = i & 1 ? t1 : t0;
-        y[2 * i] = h.x * f.x * r * t;
-        y[2 * i + 1] = h.y * f.y * r * t;
+    for (int u = threadIdx.x; u < blocks * 32; u += kDqkThreads) {
+        const int block = u >> 5, col = block / per_slice * 16 + ((u >> 3) & 1) * 8 + (u & 7);
+        const __half2 f = __float2half2_rn(c[col] * inv_m);
+        uint4* at = reinterpret_cast<uint4*>(plane) + u;
+        uint4 x = *at;
+        __half2* h = reinterpret_cast<__half2*>(&x);
+        h[0] = __hmul2(h[0], f), h[1] = __hmul2(h[1], f), h[2] = __hmul2(h[2], f), h[3] = __hmul2(h[3], f);
+        *at = x;
     }
+}
+
+// largest of c[0 .. n), by every lane of a warp
+__device__ __forceinline__ float warp_max(const float* c, int n)
+{
+    float m = 0.f;
+    for (int i = threadIdx.x & 31; i < n; i += 32)
+        m = fmaxf(m, c[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
 }
 
 template <int D, int DV>
@@ -1306,10 +1317,11 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     constexpr int RB = 2 * D, VB = 2 * DV, NT = D / 8, KS = DV / 16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const uint32_t base = smem_addr(smem);
-    float* vec = reinterpret_cast<float*>(smem + SM::vec);  // [kGradFactors][kC], then dO's row scales
-    float* sdo = vec + kGradFactors * kC;
-    float* eg = sdo + kC;        // e^G
-    float* ege = eg + kC;        // e^{G_C - G}
+    float* dm = reinterpret_cast<float*>(smem + SM::dm);    // [i][j], j <= i
+    float* vec = reinterpret_cast<float*>(smem + SM::vec);  // [kGradFactors][kC], then
+    float* sdo = vec + kGradFactors * kC;                   // dO's row scales
+    float* eg = sdo + kC;                                   // e^G
+    float* ege = eg + kC;                                   // e^{G_C - G}
     float* cE = reinterpret_cast<float*>(smem + SM::cols);
     float *cS = cE + DV, *cV = cS + DV, *cD = cV + DV;
     uint64_t* full = reinterpret_cast<uint64_t*>(cD + DV);
@@ -1319,7 +1331,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     const int64_t t0 = (int64_t)c * kC;
     const int n = (int)min((int64_t)kC, N - t0);
     const bool role_k = warp >= 4;
-    const int r0 = 16 * (warp & 3), rt = warp & 3;
+    const int rt = warp & 3, r0 = 16 * rt;
+    const uint32_t mytile = base + SM::tile + warp * 16 * 128;
 
     if (tid == 0) {
         sm100::mbar_init(full, 1);
@@ -1338,7 +1351,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         const int64_t at = bh * nchunk + c;
         __syncthreads();  // the head before is done with the tiles
         if (tid == 0) {
-            uint32_t bytes = 2 * kC * DV * 2 + 2 * D * DV * 2 + (p == 0 ? 2 * row_image<D>() : 0);
+            sm100::fence_proxy_async_smem();  // their rescaling was written by threads
+            const uint32_t bytes = 2 * kC * DV * 2 + 2 * D * DV * 2 + (p == 0 ? 2 * row_image<D>() : 0);
             sm100::mbar_arrive_expect_tx(full, bytes);
             if (p == 0)
                 delta::bulk_load(base + SM::K, rows + (kh * nchunk + c) * (int64_t)(2 * row_image<D>()),
@@ -1354,47 +1368,206 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
 #pragma unroll
         for (int b = 0; b < kC; b += RPP) {
             const int r = b + tid / LPR, part = tid % LPR;
-            if (RPP <= kC || r < kC) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (r < n)
-                    w = *reinterpret_cast<const uint4*>(dout + (bh * N + t0 + r) * DV + part * 8);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                float f[8], mx = 0.f;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < n)
+                w = *reinterpret_cast<const uint4*>(dout + (bh * N + t0 + r) * DV + part * 8);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            float f[8], mx = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[2 * i] = __uint_as_float(u[i] << 16);
-                    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-                    mx = max_abs(max_abs(mx, f[2 * i]), f[2 * i + 1]);
-                }
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const Pow2 s = pow2_for(mx);
-                uint4 h;
-                h.x = h2(f[0] * s.to, f[1] * s.to), h.y = h2(f[2] * s.to, f[3] * s.to);
-                h.z = h2(f[4] * s.to, f[5] * s.to), h.w = h2(f[6] * s.to, f[7] * s.to);
-                *reinterpret_cast<uint4*>(smem + SM::dO + tile_off<VB>(r, part)) = h;
-                if (part == 0)
-                    sdo[r] = s.from;
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+                mx = max_abs(max_abs(mx, f[2 * i]), f[2 * i + 1]);
             }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const Pow2 s = pow2_for(mx);
+            uint4 h;
+            h.x = h2(f[0] * s.to, f[1] * s.to), h.y = h2(f[2] * s.to, f[3] * s.to);
+            h.z = h2(f[4] * s.to, f[5] * s.to), h.w = h2(f[6] * s.to, f[7] * s.to);
+            *reinterpret_cast<uint4*>(smem + SM::dO + tile_off<VB>(r, part)) = h;
+            if (part == 0)
+                sdo[r] = s.from;
         }
         const float* fac = reinterpret_cast<const float*>(blobs + at * (int64_t)blob_bytes<true>() + fac_at<true>());
         for (int i = tid; i < kGradFactors * kC; i += kDqkThreads)
             vec[i] = fac[i];
-        if (tid < kC) {
-            const float gh = fac[kFacGh * kC + tid], gl = fac[kFacGl * kC + tid];
-            eg[tid] = exp2f(gh + gl);
-            ege[tid] = exp2f((fac[kFacGh * kC + kC - 1] - gh) + (fac[kFacGl * kC + kC - 1] - gl));
-        }
         for (int i = tid; i < DV; i += kDqkThreads) {
             cE[i] = kept.sE[at * DV + i];
             cV[i] = kept.sV[at * DV + i];
             cD[i] = kept.sD[at * DV + i];
             cS[i] = kept.sS[(bh * (nchunk + 1) + c) * DV + i];
         }
+        __syncthreads();
+        const float *fB = vec + kFacB * kC, *fK = vec + kFacK * kC, *fQ = vec + kFacQ * kC,
+                    *gh = vec + kFacGh * kC, *gl = vec + kFacGl * kC;
+        for (int i = tid; i < kC * kC; i += kDqkThreads) {
+            const int y = i / kC, x = i % kC;
+            if (x <= y)
+                dm[y * kLdD + x] = exp2f((gh[y] - gh[x]) + (gl[y] - gl[x]));
+        }
+        if (tid < kC) {
+            eg[tid] = exp2f(gh[tid] + gl[tid]);
+            ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
+        }
+        const float mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, DV), mD = warp_max(cD, DV);
+        ok = ok && sm100::mbar_wait(full, p & 1, kWaitPolls);
+        if (ok) {  // 1 / m of a power of two is exact
+            one_scale(smem + SM::E, KS * 4, 4, cE, 1.0f / mE);
+            one_scale(smem + SM::dV, KS * 4, 4, cV, 1.0f / mV);
+            one_scale(smem + SM::S, KS * (D / 16), D / 16, cS, 1.0f / mS);
+            one_scale(smem + SM::dS, KS * (D / 16), D / 16, cD, 1.0f / mD);
+        }
+        ok = __syncthreads_and(ok);
+        if (!ok)
+            break;
+
+        const int ia = r0 + g, ib = ia + 8;
+        // A fragments of this warp's rows, 16 value columns ks: dO is row-major, kept
+        // planes lie turned
+        auto a_rows = [&](uint32_t (&x)[4], int plane, int ks) {
+            if (plane == SM::dO) {
+                ldsm4(x, addr_a<VB>(base + SM::dO, lane, r0, 16 * ks));
+            } else {
+                uint32_t y[4];
+                ldsm4t(y, base + plane + (ks * 4 + rt) * 512 + lane * 16);
+                x[0] = y[0], x[1] = y[2], x[2] = y[1], x[3] = y[3];
+            }
+        };
+        // x[row][token] = this warp's rows of plane `a` dot the tokens of plane `b`,
+        // token tiles lo .. hi
+        auto dots = [&](float (&x)[8][4], int a_plane, int b_plane, int lo, int hi) {
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[nt][e] = 0.f;
+#pragma unroll 2
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a[4], b[4];
+                a_rows(a, a_plane, ks);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= lo && j <= hi) {
+                        if (b_plane == SM::dO)
+                            ldsm4(b, addr_b<VB>(base + SM::dO, lane, 16 * j, 16 * ks));
+                        else
+                            ldsm4t(b, base + b_plane + (ks * 4 + j) * 512 + lane * 16);
+                        mma(x[2 * j], a, b[0], b[1]);
+                        mma(x[2 * j + 1], a, b[2], b[3]);
+                    }
+                }
+            }
+        };
+        auto add = [&](const float (&acc)[NT][4], float fa, float fb) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                tot[nt][0] = fmaf(fa, acc[nt][0], tot[nt][0]), tot[nt][1] = fmaf(fa, acc[nt][1], tot[nt][1]);
+                tot[nt][2] = fmaf(fb, acc[nt][2], tot[nt][2]), tot[nt][3] = fmaf(fb, acc[nt][3], tot[nt][3]);
+            }
+        };
+        // tot += (fa, fb) o this warp's rows of plane `a` times a kept state plane
+        auto state = [&](int a_plane, int b_plane, float fa, float fb) {
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[nt][e] = 0.f;
+#pragma unroll 1
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a[4], b[4];
+                a_rows(a, a_plane, ks);
+#pragma unroll
+                for (int j = 0; j < NT / 2; ++j) {
+                    ldsm4t(b, base + b_plane + (ks * (D / 16) + j) * 512 + lane * 16);
+                    mma(acc[2 * j], a, b[0], b[1]);
+                    mma(acc[2 * j + 1], a, b[2], b[3]);
+                }
+            }
+            add(acc, fa, fb);
+        };
+        // tot += x (64 tokens, zero outside tiles lo .. hi) times a row image
+        auto rows_product = [&](const float (&x)[8][4], int image, int lo, int hi) {
+            float ma = 0.f, mb = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                ma = max_abs(max_abs(ma, x[nt][0]), x[nt][1]);
+                mb = max_abs(max_abs(mb, x[nt][2]), x[nt][3]);
+            }
+            const Pow2 pa = pow2_for(quad_max(ma)), pb = pow2_for(quad_max(mb));
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g, nt) + 4 * tq) =
+                    h2(x[nt][0] * pa.to, x[nt][1] * pa.to);
+                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g + 8, nt) + 4 * tq) =
+                    h2(x[nt][2] * pb.to, x[nt][3] * pb.to);
+            }
+            __syncwarp();
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[nt][e] = 0.f;
+#pragma unroll 1
+            for (int kk = lo; kk <= hi; ++kk) {
+                uint32_t a[4], b[4];
+                ldsm4(a, addr_a<128>(mytile, lane, 0, 16 * kk));
+#pragma unroll
+                for (int j = 0; j < NT / 2; ++j) {
+                    ldsm4t(b, addr_bt<RB>(base + image, lane, 16 * kk, 16 * j));
+                    mma(acc[2 * j], a, b[0], b[1]);
+                    mma(acc[2 * j + 1], a, b[2], b[3]);
+                }
+            }
+            add(acc, pa.from, pb.from);
+        };
+        float x[8][4];
+        if (!role_k) {
+            dots(x, SM::dO, SM::E, 0, rt);
+            const float fa = mE * sdo[ia], fb = mE * sdo[ib];
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = e >> 1 ? ib : ia, j = 8 * nt + 2 * tq + (e & 1);
+                    x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * dm[i * kLdD + j] * (fB[j] * fK[j]) : 0.f;
+                }
+            rows_product(x, SM::K, 0, rt);
+            state(SM::dO, SM::S, eg[ia] * (sdo[ia] * mS), eg[ib] * (sdo[ib] * mS));
+        } else {
+            float y[8][4];
+            const float fm = mE * mV;
+            dots(x, SM::E, SM::dV, rt, 3);
+            dots(y, SM::dV, SM::E, 0, rt);
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
+                    y[nt][e] = i > j   ? -x[nt][e] * fm * dm[i * kLdD + j] * (fB[j] * fK[i])
+                               : i < j ? -y[nt][e] * fm * dm[j * kLdD + i] * (fB[i] * fK[i])
+                                       : 0.f;
+                }
+            rows_product(y, SM::K, 0, 3);
+            dots(x, SM::E, SM::dO, rt, 3);
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
+                    x[nt][e] = i >= j ? x[nt][e] * (mE * sdo[i]) * dm[i * kLdD + j] * (fB[j] * (fQ[i] * scale)) : 0.f;
+                }
+            rows_product(x, SM::Q, rt, 3);
+            state(SM::dV, SM::S, -eg[ia] * (mV * mS), -eg[ib] * (mV * mS));
+            state(SM::E, SM::dS, ege[ia] * fB[ia] * (mE * mD), ege[ib] * fB[ib] * (mE * mD));
+        }
         // the gates' gradients from the dots over 16 columns each
         if (warp == 0) {
-            float x[2], after = 0.f;
+            float z[2], after = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = lane + 32 * h;
@@ -1408,7 +1581,7 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                     }
                     dbeta[bh * N + t0 + t] = b;
                 }
-                x[h] = y;
+                z[h] = y;
             }
             if (dlog_alpha) {
                 for (int s = 0; s < KS; ++s)
@@ -1417,245 +1590,15 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 for (int h = 1; h >= 0; --h) {
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
-                        const float y = __shfl_down_sync(0xffffffffu, x[h], o);
+                        const float y = __shfl_down_sync(0xffffffffu, z[h], o);
                         if (lane + o < 32)
-                            x[h] += y;
+                            z[h] += y;
                     }
                     const int t = lane + 32 * h;
                     if (t < n)
-                        dlog_alpha[bh * N + t0 + t] = x[h] + after;
-                    after += __shfl_sync(0xffffffffu, x[h], 0);
+                        dlog_alpha[bh * N + t0 + t] = z[h] + after;
+                    after += __shfl_sync(0xffffffffu, z[h], 0);
                 }
-            }
-        }
-        ok = ok && sm100::mbar_wait(full, p & 1, kWaitPolls);
-        ok = __syncthreads_and(ok);
-        if (!ok)
-            break;
-
-        const int ia = r0 + g, ib = ia + 8;
-        const float *fB = vec + kFacB * kC, *fK = vec + kFacK * kC, *fQ = vec + kFacQ * kC,
-                    *gh = vec + kFacGh * kC, *gl = vec + kFacGl * kC;
-        auto decay = [&](int i, int j) { return exp2f((gh[i] - gh[j]) + (gl[i] - gl[j])); };
-        // A fragments of this warp's rows from dO (row-major) and from a kept plane
-        // [16 columns][tokens] (turned), for 16 value columns ks
-        auto a_dO = [&](uint32_t (&x)[4], int ks) { ldsm4(x, addr_a<VB>(base + SM::dO, lane, r0, 16 * ks)); };
-        auto a_plane = [&](uint32_t (&x)[4], int at_, int ks) {
-            uint32_t y[4];
-            ldsm4t(y, base + at_ + (ks * 4 + rt) * 512 + lane * 16);
-            x[0] = y[0], x[1] = y[2], x[2] = y[1], x[3] = y[3];
-        };
-        auto colf = [&](const float* f, int ks, float2& f0, float2& f1) {
-            f0 = *reinterpret_cast<const float2*>(f + 16 * ks + 2 * tq);
-            f1 = *reinterpret_cast<const float2*>(f + 16 * ks + 8 + 2 * tq);
-        };
-        // largest of a row's A values under two column factors (either may be one)
-        auto row_max = [&](bool from_dO, int plane, const float* c1, const float* c2, float& ma, float& mb) {
-            ma = mb = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t x[4];
-                float y[8];
-                float2 f0, f1, h0, h1;
-                if (from_dO)
-                    a_dO(x, ks);
-                else
-                    a_plane(x, plane, ks);
-                colf(c1, ks, f0, f1);
-                if (c2) {
-                    colf(c2, ks, h0, h1);
-                    f0.x *= h0.x, f0.y *= h0.y, f1.x *= h1.x, f1.y *= h1.y;
-                }
-                rescale(x, f0, f1, 1.f, 1.f, 1.f, 1.f, y);
-                ma = max_abs(max_abs(max_abs(max_abs(ma, y[0]), y[1]), y[4]), y[5]);
-                mb = max_abs(max_abs(max_abs(max_abs(mb, y[2]), y[3]), y[6]), y[7]);
-            }
-            ma = quad_max(ma), mb = quad_max(mb);
-        };
-        auto a_scaled = [&](uint32_t (&a)[4], bool from_dO, int plane, const float* c1, const float* c2, int ks,
-                            float fa, float fb, float ta, float tb) {
-            uint32_t x[4];
-            float y[8];
-            float2 f0, f1, h0, h1;
-            if (from_dO)
-                a_dO(x, ks);
-            else
-                a_plane(x, plane, ks);
-            colf(c1, ks, f0, f1);
-            if (c2) {
-                colf(c2, ks, h0, h1);
-                f0.x *= h0.x, f0.y *= h0.y, f1.x *= h1.x, f1.y *= h1.y;
-            }
-            rescale(x, f0, f1, fa, fb, ta, tb, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = h2(y[2 * i], y[2 * i + 1]);
-        };
-        auto zero8 = [&](float (&x)[8][4]) {
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[nt][e] = 0.f;
-        };
-        // acc += A (scaled columns) x kept token plane, token tiles [lo, hi]
-        auto dots_plane = [&](float (&x)[8][4], bool from_dO, int plane, const float* c1, const float* c2, float ta,
-                              float tb, int b_plane, int lo, int hi) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t a[4], b[4];
-                a_scaled(a, from_dO, plane, c1, c2, ks, 1.f, 1.f, ta, tb);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j >= lo && j <= hi) {
-                        ldsm4t(b, base + b_plane + (ks * 4 + j) * 512 + lane * 16);
-                        mma(x[2 * j], a, b[0], b[1]);
-                        mma(x[2 * j + 1], a, b[2], b[3]);
-                    }
-                }
-            }
-        };
-        // acc[D] += A (scaled columns) x kept state plane
-        auto state_plane = [&](float (&x)[NT][4], bool from_dO, int plane, const float* c1, const float* c2, float fa,
-                               float fb, float ta, float tb, int b_plane) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t a[4], b[4];
-                a_scaled(a, from_dO, plane, c1, c2, ks, fa, fb, ta, tb);
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, base + b_plane + (ks * (D / 16) + j) * 512 + lane * 16);
-                    mma(x[2 * j], a, b[0], b[1]);
-                    mma(x[2 * j + 1], a, b[2], b[3]);
-                }
-            }
-        };
-        // acc[D] += A (64 tokens, fp32 in C tiles, under fa, fb) x row image, tiles [lo, hi]
-        auto rows_product = [&](float (&x)[NT][4], const float (&y)[8][4], float fa, float fb, int image, int lo,
-                                int hi) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                if (kk >= lo && kk <= hi) {
-                    const uint32_t a[4] = {h2(y[2 * kk][0] * fa, y[2 * kk][1] * fa),
-                                           h2(y[2 * kk][2] * fb, y[2 * kk][3] * fb),
-                                           h2(y[2 * kk + 1][0] * fa, y[2 * kk + 1][1] * fa),
-                                           h2(y[2 * kk + 1][2] * fb, y[2 * kk + 1][3] * fb)};
-                    uint32_t b[4];
-#pragma unroll
-                    for (int j = 0; j < NT / 2; ++j) {
-                        ldsm4t(b, addr_bt<RB>(base + image, lane, 16 * kk, 16 * j));
-                        mma(x[2 * j], a, b[0], b[1]);
-                        mma(x[2 * j + 1], a, b[2], b[3]);
-                    }
-                }
-            }
-        };
-        auto max8 = [&](const float (&x)[8][4], float& ma, float& mb) {
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                ma = max_abs(max_abs(ma, x[nt][0]), x[nt][1]);
-                mb = max_abs(max_abs(mb, x[nt][2]), x[nt][3]);
-            }
-        };
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[nt][e] = 0.f;
-        if (!role_k) {
-            float x[8][4], ma, mb, sa, sb;
-            zero8(x);
-            row_max(true, 0, cE, nullptr, ma, mb);
-            const Pow2 pa = pow2_for(ma), pb = pow2_for(mb);
-            dots_plane(x, true, 0, cE, nullptr, pa.to, pb.to, SM::E, 0, rt);
-            const float fa = pa.from * sdo[ia], fb = pb.from * sdo[ib];
-            sa = sb = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = e >> 1 ? ib : ia, j = 8 * nt + 2 * tq + (e & 1);
-                    x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * decay(i, j) * fB[j] * fK[j] : 0.f;
-                }
-            max8(x, sa, sb);
-            float na, nb;
-            row_max(true, 0, cS, nullptr, na, nb);
-            const float ga = eg[ia] * sdo[ia], gb = eg[ib] * sdo[ib];
-            const Pow2 ra = pow2_for(fmaxf(quad_max(sa), na * ga)), rb = pow2_for(fmaxf(quad_max(sb), nb * gb));
-            rows_product(acc, x, ra.to, rb.to, SM::K, 0, rt);
-            state_plane(acc, true, 0, cS, nullptr, ga, gb, ra.to, rb.to, SM::S);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                tot[nt][0] = fmaf(ra.from, acc[nt][0], tot[nt][0]), tot[nt][1] = fmaf(ra.from, acc[nt][1], tot[nt][1]);
-                tot[nt][2] = fmaf(rb.from, acc[nt][2], tot[nt][2]), tot[nt][3] = fmaf(rb.from, acc[nt][3], tot[nt][3]);
-            }
-        } else {
-            float x[8][4], y[8][4], ma, mb, sa = 0.f, sb = 0.f;
-            // y[j][i] = -D (dV_i.U_j) fk_i (i > j) and -D (dV_j.U_i) fk_i (i < j)
-            zero8(x);
-            row_max(false, SM::E, cE, cV, ma, mb);
-            Pow2 pa = pow2_for(ma), pb = pow2_for(mb);
-            dots_plane(x, false, SM::E, cE, cV, pa.to, pb.to, SM::dV, rt, 3);
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
-                    y[nt][e] = i > j ? -x[nt][e] * (e >> 1 ? pb : pa).from * fB[j] * decay(i, j) * fK[i] : 0.f;
-                }
-            zero8(x);
-            row_max(false, SM::dV, cE, cV, ma, mb);
-            pa = pow2_for(ma), pb = pow2_for(mb);
-            dots_plane(x, false, SM::dV, cE, cV, pa.to, pb.to, SM::E, 0, rt);
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
-                    if (i < j)
-                        y[nt][e] = -x[nt][e] * (e >> 1 ? pb : pa).from * fB[i] * decay(j, i) * fK[i];
-                }
-            // x[j][i] = D (dO_i.U_j) fq_i (i >= j)
-            zero8(x);
-            row_max(false, SM::E, cE, nullptr, ma, mb);
-            pa = pow2_for(ma), pb = pow2_for(mb);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t a[4], b[4];
-                a_scaled(a, false, SM::E, cE, nullptr, ks, 1.f, 1.f, pa.to, pb.to);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j >= rt) {
-                        ldsm4(b, addr_b<VB>(base + SM::dO, lane, 16 * j, 16 * ks));
-                        mma(x[2 * j], a, b[0], b[1]);
-                        mma(x[2 * j + 1], a, b[2], b[3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
-                    x[nt][e] = i >= j ? x[nt][e] * (e >> 1 ? pb : pa).from * sdo[i] * fB[j] * decay(i, j) * (fQ[i] * scale) : 0.f;
-                }
-            max8(x, sa, sb);
-            max8(y, sa, sb);
-            float va, vb, ua, ub;
-            row_max(false, SM::dV, cV, cS, va, vb);
-            row_max(false, SM::E, cE, cD, ua, ub);
-            const float da = eg[ia], db = eg[ib], wa = ege[ia] * fB[ia], wb = ege[ib] * fB[ib];
-            const Pow2 ra = pow2_for(fmaxf(quad_max(sa), fmaxf(va * da, ua * fabsf(wa))));
-            const Pow2 rb = pow2_for(fmaxf(quad_max(sb), fmaxf(vb * db, ub * fabsf(wb))));
-            rows_product(acc, x, ra.to, rb.to, SM::Q, rt, 3);
-            rows_product(acc, y, ra.to, rb.to, SM::K, 0, 3);
-            state_plane(acc, false, SM::dV, cV, cS, -da, -db, ra.to, rb.to, SM::S);
-            state_plane(acc, false, SM::E, cE, cD, wa, wb, ra.to, rb.to, SM::dS);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                tot[nt][0] = fmaf(ra.from, acc[nt][0], tot[nt][0]), tot[nt][1] = fmaf(ra.from, acc[nt][1], tot[nt][1]);
-                tot[nt][2] = fmaf(rb.from, acc[nt][2], tot[nt][2]), tot[nt][3] = fmaf(rb.from, acc[nt][3], tot[nt][3]);
             }
         }
     }
