@@ -360,39 +360,49 @@ __global__ void __launch_bounds__(kPrepThreads)
 }
 
 // ------------------------------------------------------------ k_delta_chain --
-// W warps of 16 value columns.  The tiles of a chunk are shared by the warps and
-// arrive by bulk copies kStages chunks ahead; a warp's own columns of V come by
-// cp.async one chunk ahead, and its outputs leave through its own tile, turned
-// back to token-major by stmatrix.
+// Slices of 16 value columns; the tiles of a chunk are shared by a CTA's slices and
+// arrive by bulk copies kStages chunks ahead; V comes by cp.async one chunk ahead,
+// and outputs leave through the slice's own tile, turned back to token-major by
+// stmatrix.
+//
+// SP = 1: a warp does all of a slice's chunk.  SP = 2: two warps share it, each with
+// half of the state's rows (the contracted index of S^T K^T and of S^T Q^T, the
+// columns of the update) and half of the chunk's token tiles (0 and 3, or 1 and 2:
+// equal shares of the triangular products).  They exchange fp32 sums through shared
+// memory three times a chunk.  A warp's products follow one another, each waiting
+// for the last: with a slice per warp a chunk is 7100 cycles at d = 128 of which
+// the tensor core works 3100, so two warps shorten it where there are SMs to spare.
 constexpr int kStages = 2;
 constexpr uint32_t kWaitPolls = 1u << 22;
+constexpr int kXch = 2048;  // bytes of one warp's exchange buffer: 16 floats per lane
 
-template <int D, bool GRAD>
+template <int D, bool GRAD, int SP>
 struct ChainSmem {
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<GRAD>();
-    static constexpr int v = kStages * stage;  // per warp: V twice, O (GRAD: dO)
-    static constexpr int per_warp = 3 * kC * 32;
-    static int bytes(int W) { return v + W * per_warp + 64; }
+    static constexpr int v = kStages * stage;
+    // per slice: V twice, O (GRAD: dO), and for each of two warps four exchange buffers
+    static constexpr int x = 3 * kC * 32, per_slice = x + (SP > 1 ? SP * 4 * kXch : 0);
+    static int bytes(int W) { return v + W * per_slice + 64; }
 };
 
 // What the forward pass of a gradient keeps per chunk, in the fragments' own
 // order ([16 columns][16-step][register][lane], every store 128 bytes): the state
-// before the chunk and E, as two fp16 parts with a scale per value column.  An
-// 8 x 8 block is 128 bytes with its rows in order, so k_delta_dqk reads it with
-// ldmatrix whichever way round it needs it.  Per value head and chunk, bytes:
+// before the chunk and E, as two fp16 parts with a scale per value column (states:
+// per column and half of their rows).  An 8 x 8 block is 128 bytes with its rows in
+// order, so k_delta_dqk reads it with ldmatrix whichever way round it needs it.
 struct Kept {
-    unsigned char* S;  // [BH][nchunk + 1][2 parts][D DV] fp16
-    float* sS;         // [BH][nchunk + 1][DV]
-    unsigned char* E;  // [BH][nchunk][2 parts][64 DV] fp16
-    float* sE;         // [BH][nchunk][DV]
-    unsigned char* dS; // [BH][nchunk][D DV] fp16: gradient of the state after the chunk
-    float* sD;         // [BH][nchunk][DV]
-    unsigned char* dV; // [BH][nchunk][64 DV] fp16
-    float* sV;         // [BH][nchunk][DV]
-    float* oo;         // [BH][DV / 16][N] dO.O over 16 columns
-    float* vv;         // [BH][DV / 16][N] v.dV
-    float* bb;         // [BH][DV / 16][N] Y.E
-    float* cd;         // [BH][DV / 16][nchunk] <S1, dS1>
+    unsigned char* S;   // [BH][nchunk + 1][2 parts][D DV] fp16
+    float* sS;          // [BH][nchunk + 1][2][DV]
+    unsigned char* E;   // [BH][nchunk][2 parts][64 DV] fp16
+    float* sE;          // [BH][nchunk][DV]
+    unsigned char* dS;  // [BH][nchunk][D DV] fp16: gradient of the state after the chunk
+    float* sD;          // [BH][nchunk][2][DV]
+    unsigned char* dV;  // [BH][nchunk][64 DV] fp16
+    float* sV;          // [BH][nchunk][DV]
+    float* oo;          // [BH][DV / 16][N] dO.O over 16 columns
+    float* vv;          // [BH][DV / 16][N] v.dV
+    float* bb;          // [BH][DV / 16][N] Y.E
+    float* cd;          // [BH][DV / 16][2][nchunk] <S1, dS1> over half of the rows
 };
 
 // One fragment's registers of plane `plane` (part_bytes each part, block = 16 x 16)
@@ -427,7 +437,70 @@ __device__ __forceinline__ void store_dot(float* row, int64_t t, int64_t N, int 
     }
 }
 
-template <int D, bool GRAD>
+// One warp's place in a slice shared by SP warps.  Token tiles (16 tokens) are
+// held in local order: this warp's own first, then the other's.
+template <int SP>
+struct Share {
+    static constexpr int own = 4 / SP;  // token tiles of a warp
+    int slice, half;
+    unsigned char *mine, *other;  // exchange buffers
+    int lane;
+    __device__ __forceinline__ int tile(int i) const
+    {
+        return SP == 1 ? i : (i >> 1 ? !half : half) ? 1 + (i & 1) : 3 * (i & 1);
+    }
+    __device__ __forceinline__ void sync() const
+    {
+        if (SP > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * SP) : "memory");
+        else
+            __syncwarp();
+    }
+    // two token tiles (C layout) to buffer b, and the partner's from it
+    __device__ __forceinline__ void put(int b, const float (&x)[2][4], const float (&y)[2][4]) const
+    {
+        float4* at = reinterpret_cast<float4*>(mine + b * kXch) + lane;
+        at[0] = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+        at[32] = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+        at[64] = make_float4(y[0][0], y[0][1], y[0][2], y[0][3]);
+        at[96] = make_float4(y[1][0], y[1][1], y[1][2], y[1][3]);
+    }
+    template <bool ADD>
+    __device__ __forceinline__ void get(int b, float (&x)[2][4], float (&y)[2][4]) const
+    {
+        const float4* at = reinterpret_cast<const float4*>(other + b * kXch) + lane;
+        float(*to[2])[4] = {x, y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = at[32 * i];
+            float* d = to[i >> 1][i & 1];
+            d[0] = ADD ? d[0] + v.x : v.x, d[1] = ADD ? d[1] + v.y : v.y;
+            d[2] = ADD ? d[2] + v.z : v.z, d[3] = ADD ? d[3] + v.w : v.w;
+        }
+    }
+};
+
+// factor pair of the tokens of C tile `nt` of token tile `t`
+__device__ __forceinline__ float2 fac2(const float* fac, int which, int t, int nt, int tq)
+{
+    return *reinterpret_cast<const float2*>(fac + which * kC + 16 * t + 8 * nt + 2 * tq);
+}
+
+template <int N_>
+__device__ __forceinline__ void clear(float (&x)[N_][4])
+{
+#pragma unroll
+    for (int i = 0; i < N_; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[i][e] = 0.f;
+}
+
+// bf16 pair -> two fp32
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <int D, bool GRAD, int SP>
 __global__ void __launch_bounds__(256, 1)
     k_delta_chain(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                   const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ out,
@@ -435,21 +508,29 @@ __global__ void __launch_bounds__(256, 1)
                   const __nv_bfloat16* __restrict__ dout, Kept kept, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
-    using SM = ChainSmem<D, GRAD>;
+    using SM = ChainSmem<D, GRAD, SP>;
     constexpr int kBlob = blob_bytes<GRAD>();
+    constexpr int RB = 2 * D;                    // bytes per row
+    constexpr int NT = D / 8 / SP, KK = NT / 2;  // n tiles of this warp's part of S^T; its 16-steps
+    constexpr int OWN = Share<SP>::own;
     const bool reads = GRAD || out;  // o is wanted
-    constexpr int RB = 2 * D, NT = D / 8;  // bytes per row; n tiles of S^T
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, W = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, W = blockDim.x / (32 * SP);
     const int g = lane >> 2, tq = lane & 3;
+    Share<SP> sh;
+    sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
     const int slices = DV / (16 * W);
     const int64_t bh = blockIdx.x / slices;
-    const int col0 = (blockIdx.x % slices) * 16 * W + 16 * warp;
+    const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const uint32_t base = smem_addr(smem);
-    const uint32_t sv = base + SM::v + warp * SM::per_warp, so = sv + 2 * kC * 32;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::v + W * SM::per_warp);
+    const int my = SM::v + sh.slice * SM::per_slice;
+    sh.mine = smem + my + SM::x + sh.half * 4 * kXch;
+    sh.other = smem + my + SM::x + (SP - 1 - sh.half) * 4 * kXch;
+    const uint32_t sv = base + my, so = sv + 2 * kC * 32;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::v + W * SM::per_slice);
     const unsigned char* row_src = rows + kh * nchunk * (int64_t)(2 * row_image<D>());
     const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)kBlob;
+    const int d0 = sh.half * (D / SP);  // first state row of this warp
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i)
@@ -464,320 +545,347 @@ __global__ void __launch_bounds__(256, 1)
         delta::bulk_load(dst, row_src + c * (int64_t)(2 * row_image<D>()), 2 * row_image<D>(), bar);
         delta::bulk_load(dst + 2 * row_image<D>(), blob_src + c * (int64_t)kBlob, kBlob, bar);
     };
-    auto load_v = [&](int c) {
+    // this warp's token tiles of the slice's columns
+    auto load_cols = [&](uint32_t dst, const __nv_bfloat16* src, int c) {
         const int64_t t0 = (int64_t)c * kC;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = (lane >> 1) + 16 * i, p = lane & 1;
+        for (int i = 0; i < OWN; ++i) {
+            const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
             const bool live = t0 + t < N;
-            const int64_t at = (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8;
-            cp16(sv + (c & 1) * kC * 32 + tile_off<32>(t, p), v + at, live);
+            cp16(dst + tile_off<32>(t, p), src + (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8, live);
         }
     };
     if (tid == 0)
         for (int c = 0; c < kStages && c < nchunk; ++c)
             load_stage(c);
-    load_v(0);
+    load_cols(sv, v, 0);
     cp_commit();
 
-    float s[NT][4];  // S^T[col0 + g, + 8][8 nt + 2 tq, + 1]
+    float s[NT][4];  // S^T[col0 + g, + 8][d0 + 8 nt + 2 tq, + 1]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            s[nt][e] = S0 ? S0[(bh * D + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
+            s[nt][e] = S0 ? S0[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
 
-    bool ok = true;
+    auto row_max = [&](float& m0, float& m1) {
+        m0 = m1 = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m0 = max_abs(max_abs(m0, s[nt][0]), s[nt][1]);
+            m1 = max_abs(max_abs(m1, s[nt][2]), s[nt][3]);
+        }
+        m0 = quad_max(m0), m1 = quad_max(m1);
+    };
+    auto split_state = [&](int kk, Pow2 p0, Pow2 p1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+        h2_split(s[2 * kk][0] * p0.to, s[2 * kk][1] * p0.to, hi[0], lo[0]);
+        h2_split(s[2 * kk][2] * p1.to, s[2 * kk][3] * p1.to, hi[1], lo[1]);
+        h2_split(s[2 * kk + 1][0] * p0.to, s[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
+        h2_split(s[2 * kk + 1][2] * p1.to, s[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
+    };
+    auto keep_state_scale = [&](int64_t c, Pow2 p0, Pow2 p1) {
+        if (tq == 0) {
+            float* ss = kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0;
+            ss[g] = p0.from, ss[g + 8] = p1.from;
+            if (SP == 1)
+                ss[DV + g] = p0.from, ss[DV + g + 8] = p1.from;
+        }
+    };
+
+    bool ok = sm100::mbar_wait(full, 0, kWaitPolls);
+    ok = __syncthreads_and(ok);
     int c = 0;
-    for (; c < nchunk; ++c) {
+    for (; ok && c < nchunk; ++c) {
         const uint32_t st = base + (c % kStages) * SM::stage;
-        const uint32_t sK = st, sQ = st + row_image<D>(), sFh = st + 2 * row_image<D>();
+        const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
         const float* fac = reinterpret_cast<const float*>(smem + (c % kStages) * SM::stage +
                                                           2 * row_image<D>() + fac_at<GRAD>());
         if (GRAD) {  // dO, wanted at the end of the chunk
-            const int64_t t0 = (int64_t)c * kC;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = (lane >> 1) + 16 * i, p = lane & 1;
-                const bool live = t0 + t < N;
-                cp16(so + tile_off<32>(t, p),
-                     dout + (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8, live);
-            }
+            load_cols(so, dout, c);
             cp_commit();
         }
         if (c + 1 < nchunk)
-            load_v(c + 1);
+            load_cols(sv + ((c + 1) & 1) * kC * 32, v, c + 1);
         cp_commit();
-        ok = ok && sm100::mbar_wait(full + c % kStages, (c / kStages) & 1, kWaitPolls);
-        cp_wait<GRAD ? 2 : 1>();
-        __syncwarp();
-        if (ok) {
-            // S^T K^T and S^T Q^T, S split on the way
-            float m0 = 0.f, m1 = 0.f;
+
+        // S^T K^T and S^T Q^T over this warp's rows of S, split on the way
+        float m0, m1;
+        row_max(m0, m1);
+        const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
+        float r[8][4], o[8][4];  // local token order
+        clear(r);
+        clear(o);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                m0 = max_abs(max_abs(m0, s[nt][0]), s[nt][1]);
-                m1 = max_abs(max_abs(m1, s[nt][2]), s[nt][3]);
-            }
-            m0 = quad_max(m0), m1 = quad_max(m1);
-            const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
-            float r[8][4], o[8][4];
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r[nt][e] = o[nt][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
-                h2_split(s[2 * kk][0] * p0.to, s[2 * kk][1] * p0.to, hi[0], lo[0]);
-                h2_split(s[2 * kk][2] * p1.to, s[2 * kk][3] * p1.to, hi[1], lo[1]);
-                h2_split(s[2 * kk + 1][0] * p0.to, s[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
-                h2_split(s[2 * kk + 1][2] * p1.to, s[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
-                if (GRAD)
-                    keep_parts(kept.S, bh * (nchunk + 1) + c, D * DV * 2, (col0 / 16) * (D / 16) + kk, lane,
-                               hi, lo);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ldsm4(b, addr_b<RB>(sK, lane, 16 * j, 16 * kk));
-                    mma(r[2 * j], hi, b[0], b[1]);
-                    mma(r[2 * j + 1], hi, b[2], b[3]);
-                    mma(r[2 * j], lo, b[0], b[1]);
-                    mma(r[2 * j + 1], lo, b[2], b[3]);
-                    if (reads) {
-                        ldsm4(b, addr_b<RB>(sQ, lane, 16 * j, 16 * kk));
-                        mma(o[2 * j], hi, b[0], b[1]);
-                        mma(o[2 * j + 1], hi, b[2], b[3]);
-                        if (GRAD) {  // o enters an fp32 gradient
-                            mma(o[2 * j], lo, b[0], b[1]);
-                            mma(o[2 * j + 1], lo, b[2], b[3]);
-                        }
-                    }
-                }
-            }
-            // R, and the largest |beta R| of a column
-            float br0 = 0.f, br1 = 0.f;
+        for (int kk = 0; kk < KK; ++kk) {
+            uint32_t hi[4], lo[4], b[4];
+            split_state(kk, p0, p1, hi, lo);
+            if (GRAD)
+                keep_parts(kept.S, bh * (nchunk + 1) + c, D * DV * 2,
+                           (col0 / 16) * (D / 16) + d0 / 16 + kk, lane, hi, lo);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-                ldsm4t(w, addr_ct<32>(sv + (c & 1) * kC * 32, lane, 16 * j, 0));
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int nt = 2 * j + u;
-                    const float2 a = *reinterpret_cast<const float2*>(fac + kFacA * kC + 8 * nt + 2 * tq);
-                    const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                    r[nt][0] = __uint_as_float(w[2 * u] << 16) - a.x * (r[nt][0] * p0.from);
-                    r[nt][1] = __uint_as_float(w[2 * u] & 0xffff0000u) - a.y * (r[nt][1] * p0.from);
-                    r[nt][2] = __uint_as_float(w[2 * u + 1] << 16) - a.x * (r[nt][2] * p1.from);
-                    r[nt][3] = __uint_as_float(w[2 * u + 1] & 0xffff0000u) - a.y * (r[nt][3] * p1.from);
-                    br0 = max_abs(max_abs(br0, be.x * r[nt][0]), be.y * r[nt][1]);
-                    br1 = max_abs(max_abs(br1, be.x * r[nt][2]), be.y * r[nt][3]);
-                    if (reads) {
-                        const float2 fo = *reinterpret_cast<const float2*>(fac + kFacO * kC + 8 * nt + 2 * tq);
-                        o[nt][0] *= fo.x * p0.from, o[nt][1] *= fo.y * p0.from;
-                        o[nt][2] *= fo.x * p1.from, o[nt][3] *= fo.y * p1.from;
+                ldsm4(b, addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
+                mma(r[2 * j], hi, b[0], b[1]);
+                mma(r[2 * j + 1], hi, b[2], b[3]);
+                mma(r[2 * j], lo, b[0], b[1]);
+                mma(r[2 * j + 1], lo, b[2], b[3]);
+                if (reads) {
+                    ldsm4(b, addr_b<RB>(sQ, lane, 16 * sh.tile(j), d0 + 16 * kk));
+                    mma(o[2 * j], hi, b[0], b[1]);
+                    mma(o[2 * j + 1], hi, b[2], b[3]);
+                    if (GRAD) {  // o enters an fp32 gradient
+                        mma(o[2 * j], lo, b[0], b[1]);
+                        mma(o[2 * j + 1], lo, b[2], b[3]);
                     }
-                }
-            }
-            // E = R + F (beta R)
-            float x[8][4];
-            const Pow2 b0 = pow2_for(quad_max(br0)), b1 = pow2_for(quad_max(br1));
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[nt][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int nt = 2 * kk + u;
-                    const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                    h2_split(be.x * r[nt][0] * b0.to, be.y * r[nt][1] * b0.to, hi[2 * u], lo[2 * u]);
-                    h2_split(be.x * r[nt][2] * b1.to, be.y * r[nt][3] * b1.to, hi[2 * u + 1], lo[2 * u + 1]);
-                }
-#pragma unroll
-                for (int j = kk; j < 4; ++j) {  // F is strictly lower
-                    ldsm4(b, addr_b<128>(sFh, lane, 16 * j, 16 * kk));
-                    mma(x[2 * j], hi, b[0], b[1]);
-                    mma(x[2 * j + 1], hi, b[2], b[3]);
-                    mma(x[2 * j], lo, b[0], b[1]);
-                    mma(x[2 * j + 1], lo, b[2], b[3]);
-                    ldsm4(b, addr_b<128>(sFh + kTile, lane, 16 * j, 16 * kk));
-                    mma(x[2 * j], hi, b[0], b[1]);
-                    mma(x[2 * j + 1], hi, b[2], b[3]);
-                }
-            }
-            float e0 = 0.f, e1 = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 f = *reinterpret_cast<const float2*>(fac + kFacF * kC + 8 * nt + 2 * tq);
-                r[nt][0] = fmaf(f.x * b0.from, x[nt][0], r[nt][0]);
-                r[nt][1] = fmaf(f.y * b0.from, x[nt][1], r[nt][1]);
-                r[nt][2] = fmaf(f.x * b1.from, x[nt][2], r[nt][2]);
-                r[nt][3] = fmaf(f.y * b1.from, x[nt][3], r[nt][3]);
-                e0 = max_abs(max_abs(e0, r[nt][0]), r[nt][1]);
-                e1 = max_abs(max_abs(e1, r[nt][2]), r[nt][3]);
-            }
-            if (GRAD) {
-                const Pow2 q0 = pow2_for(quad_max(e0)), q1 = pow2_for(quad_max(e1));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int nt = 2 * kk + u;
-                        h2_split(r[nt][0] * q0.to, r[nt][1] * q0.to, hi[2 * u], lo[2 * u]);
-                        h2_split(r[nt][2] * q1.to, r[nt][3] * q1.to, hi[2 * u + 1], lo[2 * u + 1]);
-                    }
-                    keep_parts(kept.E, bh * nchunk + c, kC * DV * 2, (col0 / 16) * 4 + kk, lane, hi, lo);
-                }
-                if (tq == 0) {
-                    float* se = kept.sE + (bh * nchunk + c) * DV + col0;
-                    float* ss = kept.sS + (bh * (nchunk + 1) + c) * DV + col0;
-                    se[g] = q0.from, se[g + 8] = q1.from;
-                    ss[g] = p0.from, ss[g + 8] = p1.from;
-                }
-            }
-            // U = beta E, and the largest of the state update's factor times it
-            float w0 = 0.f, w1 = 0.f;
-            auto to_u = [&]() {
-                e0 = e1 = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                    const float2 w = *reinterpret_cast<const float2*>(fac + kFacW * kC + 8 * nt + 2 * tq);
-                    r[nt][0] *= be.x, r[nt][1] *= be.y, r[nt][2] *= be.x, r[nt][3] *= be.y;
-                    e0 = max_abs(max_abs(e0, r[nt][0]), r[nt][1]);
-                    e1 = max_abs(max_abs(e1, r[nt][2]), r[nt][3]);
-                    w0 = max_abs(max_abs(w0, w.x * r[nt][0]), w.y * r[nt][1]);
-                    w1 = max_abs(max_abs(w1, w.x * r[nt][2]), w.y * r[nt][3]);
-                }
-            };
-            if (GRAD)
-                to_u();
-            // O = inter + (P beta) E: with beta in P, a token that writes nothing does not
-            // set the scale of its row.  For the output alone one fp16 part of each is
-            // enough (2^-12 of a term, under the output's own rounding); a gradient
-            // takes both, and P without beta and U for E, since it needs P itself
-            if (reads) {
-                const Pow2 q0 = pow2_for(quad_max(e0)), q1 = pow2_for(quad_max(e1));
-#pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[nt][e] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    uint32_t hi[4], lo[4], b[4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int nt = 2 * kk + u;
-                        h2_split(r[nt][0] * q0.to, r[nt][1] * q0.to, hi[2 * u], lo[2 * u]);
-                        h2_split(r[nt][2] * q1.to, r[nt][3] * q1.to, hi[2 * u + 1], lo[2 * u + 1]);
-                    }
-#pragma unroll
-                    for (int j = kk; j < 4; ++j) {
-                        ldsm4(b, addr_b<128>(sFh + 2 * kTile, lane, 16 * j, 16 * kk));
-                        mma(x[2 * j], hi, b[0], b[1]);
-                        mma(x[2 * j + 1], hi, b[2], b[3]);
-                        if (GRAD) {
-                            mma(x[2 * j], lo, b[0], b[1]);
-                            mma(x[2 * j + 1], lo, b[2], b[3]);
-                            ldsm4(b, addr_b<128>(sFh + 3 * kTile, lane, 16 * j, 16 * kk));
-                            mma(x[2 * j], hi, b[0], b[1]);
-                            mma(x[2 * j + 1], hi, b[2], b[3]);
-                        }
-                    }
-                }
-                if (GRAD) {
-                    cp_wait<1>();  // dO is in
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-                    if (GRAD)
-                        ldsm4t(w, addr_ct<32>(so, lane, 16 * j, 0));
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int nt = 2 * j + u;
-                        const float2 fp = *reinterpret_cast<const float2*>(fac + kFacP * kC + 8 * nt + 2 * tq);
-                        o[nt][0] = fmaf(fp.x * q0.from, x[nt][0], o[nt][0]);
-                        o[nt][1] = fmaf(fp.y * q0.from, x[nt][1], o[nt][1]);
-                        o[nt][2] = fmaf(fp.x * q1.from, x[nt][2], o[nt][2]);
-                        o[nt][3] = fmaf(fp.y * q1.from, x[nt][3], o[nt][3]);
-                        if (GRAD) {
-                            const float y0 = o[nt][0] * __uint_as_float(w[2 * u] << 16) +
-                                             o[nt][2] * __uint_as_float(w[2 * u + 1] << 16);
-                            const float y1 = o[nt][1] * __uint_as_float(w[2 * u] & 0xffff0000u) +
-                                             o[nt][3] * __uint_as_float(w[2 * u + 1] & 0xffff0000u);
-                            store_dot(kept.oo + (bh * (DV / 16) + col0 / 16) * N, (int64_t)c * kC + 8 * nt + 2 * tq,
-                                      N, g, y0, y1);
-                        } else {
-                            w[2 * u] = sm100::pack_bf16x2(o[nt][0], o[nt][1]);
-                            w[2 * u + 1] = sm100::pack_bf16x2(o[nt][2], o[nt][3]);
-                        }
-                    }
-                    if (!GRAD)
-                        stsm4t(addr_ct<32>(so, lane, 16 * j, 0), w);
-                }
-            }
-            if (!GRAD)
-                to_u();
-            // S1 = e^{G_C} S0 + (W U)^T K16 on accumulators scaled with the operand:
-            // both under one power of two, so neither overflows nor loses bits the
-            // other does not drown
-            const float gend = fac[kFacEnd * kC];
-            const Pow2 u0 = pow2_for(fmaxf(quad_max(w0), m0 * gend * 0.00390625f));
-            const Pow2 u1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
-            const float g0 = gend * u0.to, g1 = gend * u1.to;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] *= g0, s[nt][1] *= g0;
-                s[nt][2] *= g1, s[nt][3] *= g1;
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int nt = 2 * kk + u;
-                    const float2 w = *reinterpret_cast<const float2*>(fac + kFacW * kC + 8 * nt + 2 * tq);
-                    h2_split(w.x * r[nt][0] * u0.to, w.y * r[nt][1] * u0.to, hi[2 * u], lo[2 * u]);
-                    h2_split(w.x * r[nt][2] * u1.to, w.y * r[nt][3] * u1.to, hi[2 * u + 1], lo[2 * u + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, addr_bt<RB>(sK, lane, 16 * kk, 16 * j));
-                    mma(s[2 * j], hi, b[0], b[1]);
-                    mma(s[2 * j + 1], hi, b[2], b[3]);
-                    mma(s[2 * j], lo, b[0], b[1]);
-                    mma(s[2 * j + 1], lo, b[2], b[3]);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] *= u0.from, s[nt][1] *= u0.from;
-                s[nt][2] *= u1.from, s[nt][3] *= u1.from;
-            }
-            if (!GRAD && out) {
-                __syncwarp();
-                const int64_t t0 = (int64_t)c * kC;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = (lane >> 1) + 16 * i, p = lane & 1;
-                    if (t0 + t < N)
-                        *reinterpret_cast<uint4*>(out + (bh * N + t0 + t) * DV + col0 + p * 8) =
-                            *reinterpret_cast<const uint4*>(smem + (so - base) + tile_off<32>(t, p));
                 }
             }
         }
-        ok = __syncthreads_and(ok);  // every warp is done with the stage
-        if (!ok)
-            break;
-        if (tid == 0 && c + kStages < nchunk)
+        if (GRAD)
+            keep_state_scale(c, p0, p1);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            r[nt][0] *= p0.from, r[nt][1] *= p0.from, r[nt][2] *= p1.from, r[nt][3] *= p1.from;
+            if (reads)
+                o[nt][0] *= p0.from, o[nt][1] *= p0.from, o[nt][2] *= p1.from, o[nt][3] *= p1.from;
+        }
+        auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
+            return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
+        };
+        if (SP > 1) {
+            sh.put(0, pair(r, 2), pair(r, 3));
+            if (reads)
+                sh.put(1, pair(o, 2), pair(o, 3));
+            sh.sync();
+            sh.template get<true>(0, pair(r, 0), pair(r, 1));
+            if (reads)
+                sh.template get<true>(1, pair(o, 0), pair(o, 1));
+        }
+        cp_wait<GRAD ? 2 : 1>();  // V
+        __syncwarp();
+        // R of the own tiles, z = beta R
+        float z[8][4];
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            uint32_t w[4];
+            ldsm4t(w, addr_ct<32>(sv + (c & 1) * kC * 32, lane, 16 * sh.tile(i), 0));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int nt = 2 * i + u;
+                const float2 a = fac2(fac, kFacA, sh.tile(i), u, tq), be = fac2(fac, kFacB, sh.tile(i), u, tq);
+                r[nt][0] = fmaf(-a.x, r[nt][0], lo_f(w[2 * u]));
+                r[nt][1] = fmaf(-a.y, r[nt][1], hi_f(w[2 * u]));
+                r[nt][2] = fmaf(-a.x, r[nt][2], lo_f(w[2 * u + 1]));
+                r[nt][3] = fmaf(-a.y, r[nt][3], hi_f(w[2 * u + 1]));
+                z[nt][0] = be.x * r[nt][0], z[nt][1] = be.y * r[nt][1];
+                z[nt][2] = be.x * r[nt][2], z[nt][3] = be.y * r[nt][3];
+                if (reads) {
+                    const float2 fo = fac2(fac, kFacO, sh.tile(i), u, tq);
+                    o[nt][0] *= fo.x, o[nt][1] *= fo.y, o[nt][2] *= fo.x, o[nt][3] *= fo.y;
+                }
+            }
+        }
+        if (SP > 1) {
+            sh.put(2, pair(z, 0), pair(z, 1));
+            sh.sync();
+            sh.template get<false>(2, pair(z, 2), pair(z, 3));
+        }
+        float e0 = 0.f, e1 = 0.f;
+        auto max8 = [&](const float (&x)[8][4]) {
+            e0 = e1 = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                e0 = max_abs(max_abs(e0, x[nt][0]), x[nt][1]);
+                e1 = max_abs(max_abs(e1, x[nt][2]), x[nt][3]);
+            }
+            e0 = quad_max(e0), e1 = quad_max(e1);
+        };
+        auto split8 = [&](const float (&x)[8][4], int kk, Pow2 q0, Pow2 q1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                h2_split(x[2 * kk + u][0] * q0.to, x[2 * kk + u][1] * q0.to, hi[2 * u], lo[2 * u]);
+                h2_split(x[2 * kk + u][2] * q1.to, x[2 * kk + u][3] * q1.to, hi[2 * u + 1], lo[2 * u + 1]);
+            }
+        };
+        // E = R + F z on the own tiles
+        float x[2 * OWN][4];
+        clear(x);
+        max8(z);
+        {
+            const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t hi[4], lo[4], b[4];
+                split8(z, kk, q0, q1, hi, lo);
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    if (sh.tile(kk) <= sh.tile(i)) {  // F is strictly lower
+                        ldsm4(b, addr_b<128>(sF, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                        mma(x[2 * i], hi, b[0], b[1]);
+                        mma(x[2 * i + 1], hi, b[2], b[3]);
+                        mma(x[2 * i], lo, b[0], b[1]);
+                        mma(x[2 * i + 1], lo, b[2], b[3]);
+                        ldsm4(b, addr_b<128>(sF + kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                        mma(x[2 * i], hi, b[0], b[1]);
+                        mma(x[2 * i + 1], hi, b[2], b[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * OWN; ++i) {
+                const float2 f = fac2(fac, kFacF, sh.tile(i >> 1), i & 1, tq);
+                r[i][0] = fmaf(f.x * q0.from, x[i][0], r[i][0]);
+                r[i][1] = fmaf(f.y * q0.from, x[i][1], r[i][1]);
+                r[i][2] = fmaf(f.x * q1.from, x[i][2], r[i][2]);
+                r[i][3] = fmaf(f.y * q1.from, x[i][3], r[i][3]);
+            }
+        }
+        if (SP > 1) {
+            sh.put(3, pair(r, 0), pair(r, 1));
+            sh.sync();
+            sh.template get<false>(3, pair(r, 2), pair(r, 3));
+        }
+        // r is E; its largest is wanted for O, and for what a gradient keeps
+        max8(r);
+        if (GRAD) {
+            const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t hi[4], lo[4];
+                split8(r, i, q0, q1, hi, lo);
+                keep_parts(kept.E, bh * nchunk + c, kC * DV * 2, (col0 / 16) * 4 + sh.tile(i), lane, hi, lo);
+            }
+            if (tq == 0 && sh.half == 0) {
+                float* se = kept.sE + (bh * nchunk + c) * DV + col0;
+                se[g] = q0.from, se[g + 8] = q1.from;
+            }
+        }
+        // U = beta E, and the largest of the state update's factor times it
+        float w0 = 0.f, w1 = 0.f;
+        auto to_u = [&]() {
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
+                const float2 w = fac2(fac, kFacW, sh.tile(nt >> 1), nt & 1, tq);
+                r[nt][0] *= be.x, r[nt][1] *= be.y, r[nt][2] *= be.x, r[nt][3] *= be.y;
+                w0 = max_abs(max_abs(w0, w.x * r[nt][0]), w.y * r[nt][1]);
+                w1 = max_abs(max_abs(w1, w.x * r[nt][2]), w.y * r[nt][3]);
+            }
+        };
+        if (GRAD) {
+            to_u();
+            max8(r);
+        }
+        // O = inter + (P beta) E: with beta in P, a token that writes nothing does not
+        // set the scale of its row.  For the output alone one fp16 part of each is
+        // enough (2^-12 of a term, under the output's own rounding); a gradient
+        // takes both, and P without beta and U for E, since it needs P itself
+        if (reads) {
+            const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
+            clear(x);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t hi[4], lo[4], b[4];
+                split8(r, kk, q0, q1, hi, lo);
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    if (sh.tile(kk) <= sh.tile(i)) {
+                        ldsm4(b, addr_b<128>(sP, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                        mma(x[2 * i], hi, b[0], b[1]);
+                        mma(x[2 * i + 1], hi, b[2], b[3]);
+                        if (GRAD) {
+                            mma(x[2 * i], lo, b[0], b[1]);
+                            mma(x[2 * i + 1], lo, b[2], b[3]);
+                            ldsm4(b, addr_b<128>(sP + kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                            mma(x[2 * i], hi, b[0], b[1]);
+                            mma(x[2 * i + 1], hi, b[2], b[3]);
+                        }
+                    }
+                }
+            }
+            if (GRAD) {
+                cp_wait<1>();  // dO
+                __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t w[4];
+                if (GRAD)
+                    ldsm4t(w, addr_ct<32>(so, lane, 16 * sh.tile(i), 0));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int nt = 2 * i + u;
+                    const float2 fp = fac2(fac, kFacP, sh.tile(i), u, tq);
+                    o[nt][0] = fmaf(fp.x * q0.from, x[nt][0], o[nt][0]);
+                    o[nt][1] = fmaf(fp.y * q0.from, x[nt][1], o[nt][1]);
+                    o[nt][2] = fmaf(fp.x * q1.from, x[nt][2], o[nt][2]);
+                    o[nt][3] = fmaf(fp.y * q1.from, x[nt][3], o[nt][3]);
+                    if (GRAD) {
+                        store_dot(kept.oo + (bh * (DV / 16) + col0 / 16) * N,
+                                  (int64_t)c * kC + 16 * sh.tile(i) + 8 * u + 2 * tq, N, g,
+                                  o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]),
+                                  o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]));
+                    } else {
+                        w[2 * u] = sm100::pack_bf16x2(o[nt][0], o[nt][1]);
+                        w[2 * u + 1] = sm100::pack_bf16x2(o[nt][2], o[nt][3]);
+                    }
+                }
+                if (!GRAD)
+                    stsm4t(addr_ct<32>(so, lane, 16 * sh.tile(i), 0), w);
+            }
+        }
+        if (!GRAD)
+            to_u();
+        // S1 = e^{G_C} S0 + (W U)^T K16 on accumulators scaled with the operand: both
+        // under one power of two, so neither overflows nor loses bits the other does
+        // not drown
+        const float gend = fac[kFacEnd * kC];
+        const Pow2 u0 = pow2_for(fmaxf(quad_max(w0), m0 * gend * 0.00390625f));
+        const Pow2 u1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
+        const float g0 = gend * u0.to, g1 = gend * u1.to;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] *= g0, s[nt][1] *= g0;
+            s[nt][2] *= g1, s[nt][3] *= g1;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t hi[4], lo[4], b[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int nt = 2 * kk + u;
+                const float2 w = fac2(fac, kFacW, sh.tile(kk), u, tq);
+                h2_split(w.x * r[nt][0] * u0.to, w.y * r[nt][1] * u0.to, hi[2 * u], lo[2 * u]);
+                h2_split(w.x * r[nt][2] * u1.to, w.y * r[nt][3] * u1.to, hi[2 * u + 1], lo[2 * u + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < KK; ++j) {
+                ldsm4t(b, addr_bt<RB>(sK, lane, 16 * sh.tile(kk), d0 + 16 * j));
+                mma(s[2 * j], hi, b[0], b[1]);
+                mma(s[2 * j + 1], hi, b[2], b[3]);
+                mma(s[2 * j], lo, b[0], b[1]);
+                mma(s[2 * j + 1], lo, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] *= u0.from, s[nt][1] *= u0.from;
+            s[nt][2] *= u1.from, s[nt][3] *= u1.from;
+        }
+        if (!GRAD && out) {
+            __syncwarp();
+            const int64_t t0 = (int64_t)c * kC;
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
+                if (t0 + t < N)
+                    *reinterpret_cast<uint4*>(out + (bh * N + t0 + t) * DV + col0 + p * 8) =
+                        *reinterpret_cast<const uint4*>(smem + (so - base) + tile_off<32>(t, p));
+            }
+        }
+        if (c + 1 < nchunk)
+            ok = sm100::mbar_wait(full + (c + 1) % kStages, ((c + 1) / kStages) & 1, kWaitPolls);
+        ok = __syncthreads_and(ok);  // every warp is done with the stage, and has the next
+        if (ok && tid == 0 && c + kStages < nchunk)
             load_stage(c + kStages);
     }
     cp_wait<0>();
@@ -790,39 +898,31 @@ __global__ void __launch_bounds__(256, 1)
         return;
     }
     if (GRAD) {  // the final state, for <S1, dS1> of the last chunk
-        float m0 = 0.f, m1 = 0.f;
+        float m0, m1;
+        row_max(m0, m1);
+        const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m0 = max_abs(max_abs(m0, s[nt][0]), s[nt][1]);
-            m1 = max_abs(max_abs(m1, s[nt][2]), s[nt][3]);
-        }
-        const Pow2 p0 = pow2_for(quad_max(m0)), p1 = pow2_for(quad_max(m1));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int kk = 0; kk < KK; ++kk) {
             uint32_t hi[4], lo[4];
-            h2_split(s[2 * kk][0] * p0.to, s[2 * kk][1] * p0.to, hi[0], lo[0]);
-            h2_split(s[2 * kk][2] * p1.to, s[2 * kk][3] * p1.to, hi[1], lo[1]);
-            h2_split(s[2 * kk + 1][0] * p0.to, s[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
-            h2_split(s[2 * kk + 1][2] * p1.to, s[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
-            keep_parts(kept.S, bh * (nchunk + 1) + nchunk, D * DV * 2, (col0 / 16) * (D / 16) + kk, lane, hi, lo);
+            split_state(kk, p0, p1, hi, lo);
+            keep_parts(kept.S, bh * (nchunk + 1) + nchunk, D * DV * 2, (col0 / 16) * (D / 16) + d0 / 16 + kk, lane,
+                       hi, lo);
         }
-        if (tq == 0) {
-            float* ss = kept.sS + (bh * (nchunk + 1) + nchunk) * DV + col0;
-            ss[g] = p0.from, ss[g + 8] = p1.from;
-        }
+        keep_state_scale(nchunk, p0, p1);
     }
     if (S_out) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                S_out[(bh * D + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = s[nt][e];
+                S_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = s[nt][e];
     }
 }
 
 // -------------------------------------------------------------- k_delta_rev --
-// The chunks from the last to the first, dS^T [16 x d] of a warp's columns in
-// registers (dS1 entering a chunk, dS0 leaving it):
+// The chunks from the last to the first, dS^T [16 x d] of a slice's columns in
+// registers (dS1 entering a chunk, dS0 leaving it), shared between warps as in
+// k_delta_chain:
 //
 //   dU = P^T dO + diag(e^{G_C - G}) K dS1,  z = beta dU
 //   Y  = dU + F^T z,  dV = beta Y          ((I + diag(beta) A)^{-T} = I + F^T beta)
@@ -830,20 +930,19 @@ __global__ void __launch_bounds__(256, 1)
 //
 // and the dot products that need both directions' fp32 values: v.dV, Y.E, and
 // <S0, dS0> (which is <S1, dS1> of the chunk before).
-constexpr int kRevWarps = 4;
-
-template <int D>
+template <int D, int SP>
 struct RevSmem {
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<true>();
-    static constexpr int warp0 = kStages * stage;
-    // per warp: dO twice, V (then dV), E hi and lo, S hi and lo
-    static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, s = e + 2 * kC * 32,
-                         per_warp = s + 2 * D * 32;
-    static int bytes(int W) { return warp0 + W * per_warp + 64; }
+    static constexpr int slice0 = kStages * stage;
+    // per slice: dO twice, V (then dV), E hi and lo, S hi and lo, three exchange
+    // buffers for each of two warps
+    static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, s = e + 2 * kC * 32, x = s + 2 * D * 32,
+                         per_slice = x + (SP > 1 ? SP * 3 * kXch : 0);
+    static int bytes(int W) { return slice0 + W * per_slice + 64; }
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kRevWarps, 1)
+template <int D, int SP>
+__global__ void __launch_bounds__(128, 1)
     k_delta_rev(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
                 const float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dv,
@@ -851,20 +950,26 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
                 Kept kept, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
-    using SM = RevSmem<D>;
-    constexpr int RB = 2 * D, NT = D / 8, kBlob = blob_bytes<true>();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, W = blockDim.x >> 5;
+    using SM = RevSmem<D, SP>;
+    constexpr int RB = 2 * D, kBlob = blob_bytes<true>();
+    constexpr int NT = D / 8 / SP, KK = NT / 2, OWN = Share<SP>::own;
+    const int tid = threadIdx.x, lane = tid & 31, W = blockDim.x / (32 * SP);
     const int g = lane >> 2, tq = lane & 3;
+    Share<SP> sh;
+    sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
     const int slices = DV / (16 * W);
     const int64_t bh = blockIdx.x / slices;
-    const int col0 = (blockIdx.x % slices) * 16 * W + 16 * warp, slice = col0 / 16;
+    const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice, slice = col0 / 16;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const uint32_t base = smem_addr(smem);
-    const uint32_t mine = SM::warp0 + warp * SM::per_warp;
+    const int mine = SM::slice0 + sh.slice * SM::per_slice;
+    sh.mine = smem + mine + SM::x + sh.half * 3 * kXch;
+    sh.other = smem + mine + SM::x + (SP - 1 - sh.half) * 3 * kXch;
     const uint32_t sdo = base + mine + SM::dO, sv = base + mine + SM::v;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::warp0 + W * SM::per_warp);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::slice0 + W * SM::per_slice);
     const unsigned char* row_src = rows + kh * nchunk * (int64_t)(2 * row_image<D>());
     const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)kBlob;
+    const int d0 = sh.half * (D / SP);
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i)
@@ -883,31 +988,41 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
     auto load_cols = [&](uint32_t dst, const __nv_bfloat16* src, int c) {
         const int64_t t0 = (int64_t)c * kC;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = (lane >> 1) + 16 * i, p = lane & 1;
+        for (int i = 0; i < OWN; ++i) {
+            const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
             const bool live = t0 + t < N;
             cp16(dst + tile_off<32>(t, p), src + (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8, live);
         }
     };
-    // a warp's part of a kept plane, `n` blocks of 512 bytes
-    auto load_blocks = [&](uint32_t dst, const unsigned char* plane, int64_t part, int64_t part_bytes, int n) {
-        const unsigned char* src = plane + part * part_bytes + (int64_t)slice * n * 512;
-        for (int i = 0; i < n; ++i)
-            cp16(dst + i * 512 + lane * 16, src + i * 512 + lane * 16, true);
+    auto load_E = [&](int c) {  // the own token tiles' blocks
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                cp16(base + mine + SM::e + part * kC * 32 + sh.tile(i) * 512 + lane * 16,
+                     kept.E + (2 * (bh * nchunk + c) + part) * (int64_t)(kC * DV * 2) +
+                         (slice * 4 + sh.tile(i)) * 512 + lane * 16,
+                     true);
     };
-    auto load_S = [&](int64_t c) {
-        load_blocks(base + mine + SM::s, kept.S, 2 * (bh * (nchunk + 1) + c), D * DV * 2, D / 16);
-        load_blocks(base + mine + SM::s + D * 32, kept.S, 2 * (bh * (nchunk + 1) + c) + 1, D * DV * 2, D / 16);
+    auto load_S = [&](int64_t c) {  // the own rows' blocks
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                cp16(base + mine + SM::s + part * D * 32 + (d0 / 16 + kk) * 512 + lane * 16,
+                     kept.S + (2 * (bh * (nchunk + 1) + c) + part) * (int64_t)(D * DV * 2) +
+                         (slice * (D / 16) + d0 / 16 + kk) * 512 + lane * 16,
+                     true);
     };
-    float ds[NT][4];  // dS^T[col0 + g, + 8][8 nt + 2 tq, + 1]
-    // <S of chunk c, dS> over the warp's columns -> kept.cd of the chunk before
+    float ds[NT][4];  // dS^T[col0 + g, + 8][d0 + 8 nt + 2 tq, + 1]
+    // <S of chunk c, dS> over the warp's part -> kept.cd of the chunk before
     auto dot_state = [&](int64_t c) {
-        const uint32_t* hi = reinterpret_cast<const uint32_t*>(smem + mine + SM::s) + lane;
+        const uint32_t* hi = reinterpret_cast<const uint32_t*>(smem + mine + SM::s) + (d0 / 16) * 128 + lane;
         const uint32_t* lo = hi + D * 8;
-        const float* sc = kept.sS + (bh * (nchunk + 1) + c) * DV + col0;
+        const float* sc = kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0;
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // register i: row g + 8 (i & 1), tile 2 kk + (i >> 1)
                 const uint32_t x = hi[(kk * 4 + i) * 32], y = lo[(kk * 4 + i) * 32];
@@ -922,8 +1037,12 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0)
-            kept.cd[(bh * (DV / 16) + slice) * nchunk + c - 1] = x;
+        if (lane == 0) {
+            float* cd = kept.cd + (bh * (DV / 16) + slice) * 2 * nchunk + c - 1;
+            cd[sh.half * nchunk] = x;
+            if (SP == 1)
+                cd[nchunk] = 0.f;
+        }
     };
 
     if (tid == 0)
@@ -938,16 +1057,16 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             ds[nt][e] =
-                dS_out ? dS_out[(bh * D + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
+                dS_out ? dS_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
     cp_wait<0>();
     __syncwarp();
     if (gated)
         dot_state(nchunk);
-    __syncwarp();
 
-    bool ok = true;
+    bool ok = sm100::mbar_wait(full, 0, kWaitPolls);
+    ok = __syncthreads_and(ok);
     int it = 0;
-    for (; it < nchunk; ++it) {
+    for (; ok && it < nchunk; ++it) {
         const int c = nchunk - 1 - it;
         const uint32_t st = base + (it % kStages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
@@ -956,8 +1075,7 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
         const uint32_t tdo = sdo + (c & 1) * kC * 32;
         // this chunk's V, E and S, wanted from the middle on, and the next dO
         load_cols(sv, v, c);
-        load_blocks(base + mine + SM::e, kept.E, 2 * (bh * nchunk + c), kC * DV * 2, 4);
-        load_blocks(base + mine + SM::e + kC * 32, kept.E, 2 * (bh * nchunk + c) + 1, kC * DV * 2, 4);
+        load_E(c);
         if (gated && c > 0)
             load_S(c);
         if (c > 0)
@@ -965,271 +1083,292 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
         cp_commit();
         const float* se = kept.sE + (bh * nchunk + c) * DV + col0;
         const float se0 = se[g], se1 = se[g + 8];
-        ok = ok && sm100::mbar_wait(full + it % kStages, (it / kStages) & 1, kWaitPolls);
-        if (ok) {
-            // dS1^T K^T; dS1 is kept for k_delta_dqk
-            float m0 = 0.f, m1 = 0.f;
+        auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
+            return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
+        };
+
+        // dS1^T K^T over this warp's rows; dS1 is kept for k_delta_dqk
+        float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                m0 = max_abs(max_abs(m0, ds[nt][0]), ds[nt][1]);
-                m1 = max_abs(max_abs(m1, ds[nt][2]), ds[nt][3]);
-            }
-            m0 = quad_max(m0), m1 = quad_max(m1);
-            const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
-            float u[8][4], x[8][4];
+        for (int nt = 0; nt < NT; ++nt) {
+            m0 = max_abs(max_abs(m0, ds[nt][0]), ds[nt][1]);
+            m1 = max_abs(max_abs(m1, ds[nt][2]), ds[nt][3]);
+        }
+        m0 = quad_max(m0), m1 = quad_max(m1);
+        const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
+        float u[8][4], x[2 * OWN][4];  // u in local token order
+        clear(u);
+        clear(x);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[nt][e] = x[nt][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
-                h2_split(ds[2 * kk][0] * p0.to, ds[2 * kk][1] * p0.to, hi[0], lo[0]);
-                h2_split(ds[2 * kk][2] * p1.to, ds[2 * kk][3] * p1.to, hi[1], lo[1]);
-                h2_split(ds[2 * kk + 1][0] * p0.to, ds[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
-                h2_split(ds[2 * kk + 1][2] * p1.to, ds[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
-                keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + kk, lane, hi);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ldsm4(b, addr_b<RB>(sK, lane, 16 * j, 16 * kk));
-                    mma(u[2 * j], hi, b[0], b[1]);
-                    mma(u[2 * j + 1], hi, b[2], b[3]);
-                    mma(u[2 * j], lo, b[0], b[1]);
-                    mma(u[2 * j + 1], lo, b[2], b[3]);
-                }
-            }
-            // dO^T P: the rows of P carry powers of two, which go to dO (exact)
-            float d0 = 0.f, d1 = 0.f;
+        for (int kk = 0; kk < KK; ++kk) {
+            uint32_t hi[4], lo[4], b[4];
+            h2_split(ds[2 * kk][0] * p0.to, ds[2 * kk][1] * p0.to, hi[0], lo[0]);
+            h2_split(ds[2 * kk][2] * p1.to, ds[2 * kk][3] * p1.to, hi[1], lo[1]);
+            h2_split(ds[2 * kk + 1][0] * p0.to, ds[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
+            h2_split(ds[2 * kk + 1][2] * p1.to, ds[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
+            keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + d0 / 16 + kk, lane, hi);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-                ldsm4t(w, addr_ct<32>(tdo, lane, 16 * j, 0));
+                ldsm4(b, addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
+                mma(u[2 * j], hi, b[0], b[1]);
+                mma(u[2 * j + 1], hi, b[2], b[3]);
+                mma(u[2 * j], lo, b[0], b[1]);
+                mma(u[2 * j + 1], lo, b[2], b[3]);
+            }
+        }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 fp = *reinterpret_cast<const float2*>(fac + kFacP * kC + 16 * j + 8 * h + 2 * tq);
-                    d0 = max_abs(max_abs(d0, fp.x * __uint_as_float(w[2 * h] << 16)),
-                                 fp.y * __uint_as_float(w[2 * h] & 0xffff0000u));
-                    d1 = max_abs(max_abs(d1, fp.x * __uint_as_float(w[2 * h + 1] << 16)),
-                                 fp.y * __uint_as_float(w[2 * h + 1] & 0xffff0000u));
+        for (int nt = 0; nt < 8; ++nt)
+            u[nt][0] *= p0.from, u[nt][1] *= p0.from, u[nt][2] *= p1.from, u[nt][3] *= p1.from;
+        if (SP > 1)
+            sh.put(0, pair(u, 2), pair(u, 3));
+        // dO^T P on the own tiles: the rows of P carry powers of two, which go to dO
+        // (exact)
+        float q_0 = 0.f, q_1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+            ldsm4t(w, addr_ct<32>(tdo, lane, 16 * j, 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 fp = fac2(fac, kFacP, j, h, tq);
+                q_0 = max_abs(max_abs(q_0, fp.x * lo_f(w[2 * h])), fp.y * hi_f(w[2 * h]));
+                q_1 = max_abs(max_abs(q_1, fp.x * lo_f(w[2 * h + 1])), fp.y * hi_f(w[2 * h + 1]));
+            }
+        }
+        const Pow2 q0 = pow2_for(quad_max(q_0)), q1 = pow2_for(quad_max(q_1));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t w[4], a[4], b[4];
+            ldsm4t(w, addr_ct<32>(tdo, lane, 16 * kk, 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 fp = fac2(fac, kFacP, kk, h, tq);
+                a[2 * h] = h2(fp.x * lo_f(w[2 * h]) * q0.to, fp.y * hi_f(w[2 * h]) * q0.to);
+                a[2 * h + 1] = h2(fp.x * lo_f(w[2 * h + 1]) * q1.to, fp.y * hi_f(w[2 * h + 1]) * q1.to);
+            }
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                if (sh.tile(i) <= kk) {  // P_ij, j <= i
+                    ldsm4t(b, addr_bt<128>(sP, lane, 16 * kk, 16 * sh.tile(i)));
+                    mma(x[2 * i], a, b[0], b[1]);
+                    mma(x[2 * i + 1], a, b[2], b[3]);
+                    ldsm4t(b, addr_bt<128>(sP + kTile, lane, 16 * kk, 16 * sh.tile(i)));
+                    mma(x[2 * i], a, b[0], b[1]);
+                    mma(x[2 * i + 1], a, b[2], b[3]);
                 }
             }
-            const Pow2 q0 = pow2_for(quad_max(d0)), q1 = pow2_for(quad_max(d1));
+        }
+        if (SP > 1) {
+            sh.sync();
+            sh.template get<true>(0, pair(u, 0), pair(u, 1));
+        }
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                uint32_t w[4], a[4], b[4];
-                ldsm4t(w, addr_ct<32>(tdo, lane, 16 * kk, 0));
+        for (int i = 0; i < 2 * OWN; ++i) {  // dU
+            const float2 w = fac2(fac, kFacW, sh.tile(i >> 1), i & 1, tq);
+            u[i][0] = fmaf(w.x, u[i][0], q0.from * x[i][0]);
+            u[i][1] = fmaf(w.y, u[i][1], q0.from * x[i][1]);
+            u[i][2] = fmaf(w.x, u[i][2], q1.from * x[i][2]);
+            u[i][3] = fmaf(w.y, u[i][3], q1.from * x[i][3]);
+        }
+        if (SP > 1) {
+            sh.put(1, pair(u, 0), pair(u, 1));
+            sh.sync();
+            sh.template get<false>(1, pair(u, 2), pair(u, 3));
+        }
+        // F^T z on the own tiles; F's row scales go to z
+        float z0 = 0.f, z1 = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 fp = *reinterpret_cast<const float2*>(fac + kFacP * kC + 16 * kk + 8 * h + 2 * tq);
-                    a[2 * h] = h2(fp.x * __uint_as_float(w[2 * h] << 16) * q0.to,
-                                  fp.y * __uint_as_float(w[2 * h] & 0xffff0000u) * q0.to);
-                    a[2 * h + 1] = h2(fp.x * __uint_as_float(w[2 * h + 1] << 16) * q1.to,
-                                      fp.y * __uint_as_float(w[2 * h + 1] & 0xffff0000u) * q1.to);
-                }
+        for (int nt = 0; nt < 8; ++nt) {
+            const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
+            const float2 ff = fac2(fac, kFacF, sh.tile(nt >> 1), nt & 1, tq);
+            z0 = max_abs(max_abs(z0, be.x * ff.x * u[nt][0]), be.y * ff.y * u[nt][1]);
+            z1 = max_abs(max_abs(z1, be.x * ff.x * u[nt][2]), be.y * ff.y * u[nt][3]);
+        }
+        const Pow2 y0 = pow2_for(quad_max(z0)), y1 = pow2_for(quad_max(z1));
+        clear(x);
 #pragma unroll
-                for (int j = 0; j <= kk; ++j) {  // P_ij, j <= i
-                    ldsm4t(b, addr_bt<128>(sP, lane, 16 * kk, 16 * j));
-                    mma(x[2 * j], a, b[0], b[1]);
-                    mma(x[2 * j + 1], a, b[2], b[3]);
-                    ldsm4t(b, addr_bt<128>(sP + kTile, lane, 16 * kk, 16 * j));
-                    mma(x[2 * j], a, b[0], b[1]);
-                    mma(x[2 * j + 1], a, b[2], b[3]);
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t hi[4], lo[4], b[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int nt = 2 * kk + h;
+                const float2 be = fac2(fac, kFacB, sh.tile(kk), h, tq);
+                const float2 ff = fac2(fac, kFacF, sh.tile(kk), h, tq);
+                const float fx = be.x * ff.x, fy = be.y * ff.y;
+                h2_split(fx * u[nt][0] * y0.to, fy * u[nt][1] * y0.to, hi[2 * h], lo[2 * h]);
+                h2_split(fx * u[nt][2] * y1.to, fy * u[nt][3] * y1.to, hi[2 * h + 1], lo[2 * h + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                if (sh.tile(i) <= sh.tile(kk)) {
+                    ldsm4t(b, addr_bt<128>(sF, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
+                    mma(x[2 * i], hi, b[0], b[1]);
+                    mma(x[2 * i + 1], hi, b[2], b[3]);
+                    mma(x[2 * i], lo, b[0], b[1]);
+                    mma(x[2 * i + 1], lo, b[2], b[3]);
+                    ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
+                    mma(x[2 * i], hi, b[0], b[1]);
+                    mma(x[2 * i + 1], hi, b[2], b[3]);
                 }
             }
-            // dU, and the largest |z| with F's row scales
-            float z0 = 0.f, z1 = 0.f;
+        }
+        cp_wait<0>();
+        __syncwarp();
+        // Y, the dots, dV on the own tiles
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 w = *reinterpret_cast<const float2*>(fac + kFacW * kC + 8 * nt + 2 * tq);
-                const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                const float2 ff = *reinterpret_cast<const float2*>(fac + kFacF * kC + 8 * nt + 2 * tq);
-                u[nt][0] = fmaf(w.x * p0.from, u[nt][0], q0.from * x[nt][0]);
-                u[nt][1] = fmaf(w.y * p0.from, u[nt][1], q0.from * x[nt][1]);
-                u[nt][2] = fmaf(w.x * p1.from, u[nt][2], q1.from * x[nt][2]);
-                u[nt][3] = fmaf(w.y * p1.from, u[nt][3], q1.from * x[nt][3]);
-                z0 = max_abs(max_abs(z0, be.x * ff.x * u[nt][0]), be.y * ff.y * u[nt][1]);
-                z1 = max_abs(max_abs(z1, be.x * ff.x * u[nt][2]), be.y * ff.y * u[nt][3]);
+        for (int i = 0; i < OWN; ++i) {
+            uint32_t w[4];
+            ldsm4t(w, addr_ct<32>(sv, lane, 16 * sh.tile(i), 0));
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[nt][e] = 0.f;
+            for (int h = 0; h < 2; ++h) {
+                const int nt = 2 * i + h;
+                const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
+                u[nt][0] = fmaf(y0.from, x[nt][0], u[nt][0]);
+                u[nt][1] = fmaf(y0.from, x[nt][1], u[nt][1]);
+                u[nt][2] = fmaf(y1.from, x[nt][2], u[nt][2]);
+                u[nt][3] = fmaf(y1.from, x[nt][3], u[nt][3]);
+                const uint32_t* eh =
+                    reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
+                const uint32_t* el = eh + kC * 8;
+                const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(eh));
+                const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
+                const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
+                const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
+                const int64_t t = (int64_t)c * kC + 16 * sh.tile(i) + 8 * h + 2 * tq;
+                store_dot(kept.bb + (bh * (DV / 16) + slice) * N, t, N, g,
+                          u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x)),
+                          u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y)));
+                u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
+                if (gated)
+                    store_dot(kept.vv + (bh * (DV / 16) + slice) * N, t, N, g,
+                              u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]),
+                              u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]));
             }
-            const Pow2 y0 = pow2_for(quad_max(z0)), y1 = pow2_for(quad_max(z1));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * kk + h;
-                    const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                    const float2 ff = *reinterpret_cast<const float2*>(fac + kFacF * kC + 8 * nt + 2 * tq);
-                    const float fx = be.x * ff.x, fy = be.y * ff.y;
-                    h2_split(fx * u[nt][0] * y0.to, fy * u[nt][1] * y0.to, hi[2 * h], lo[2 * h]);
-                    h2_split(fx * u[nt][2] * y1.to, fy * u[nt][3] * y1.to, hi[2 * h + 1], lo[2 * h + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j <= kk; ++j) {
-                    ldsm4t(b, addr_bt<128>(sF, lane, 16 * kk, 16 * j));
-                    mma(x[2 * j], hi, b[0], b[1]);
-                    mma(x[2 * j + 1], hi, b[2], b[3]);
-                    mma(x[2 * j], lo, b[0], b[1]);
-                    mma(x[2 * j + 1], lo, b[2], b[3]);
-                    ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * kk, 16 * j));
-                    mma(x[2 * j], hi, b[0], b[1]);
-                    mma(x[2 * j + 1], hi, b[2], b[3]);
-                }
-            }
-            cp_wait<0>();
+        }
+        if (SP > 1) {
+            sh.put(2, pair(u, 0), pair(u, 1));
+            sh.sync();
+            sh.template get<false>(2, pair(u, 2), pair(u, 3));
+        } else {
             __syncwarp();
-            // Y, the dots, dV
-            float v0 = 0.f, v1 = 0.f;
+        }
+        // dV leaves as bf16 (V's tile is read) and is kept as scaled fp16
+        float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-                ldsm4t(w, addr_ct<32>(sv, lane, 16 * j, 0));
+        for (int nt = 0; nt < 8; ++nt) {
+            v0 = max_abs(max_abs(v0, u[nt][0]), u[nt][1]);
+            v1 = max_abs(max_abs(v1, u[nt][2]), u[nt][3]);
+        }
+        {
+            const Pow2 s0 = pow2_for(quad_max(v0)), s1 = pow2_for(quad_max(v1));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t w[4], a[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * j + h;
-                    const float2 be = *reinterpret_cast<const float2*>(fac + kFacB * kC + 8 * nt + 2 * tq);
-                    u[nt][0] = fmaf(y0.from, x[nt][0], u[nt][0]);
-                    u[nt][1] = fmaf(y0.from, x[nt][1], u[nt][1]);
-                    u[nt][2] = fmaf(y1.from, x[nt][2], u[nt][2]);
-                    u[nt][3] = fmaf(y1.from, x[nt][3], u[nt][3]);
-                    const uint32_t* eh = reinterpret_cast<const uint32_t*>(smem + mine + SM::e) +
-                                         (j * 4 + 2 * h) * 32 + lane;
-                    const uint32_t* el = eh + kC * 8;
-                    const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(eh));
-                    const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
-                    const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
-                    const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
-                    const int64_t t = (int64_t)c * kC + 8 * nt + 2 * tq;
-                    store_dot(kept.bb + (bh * (DV / 16) + slice) * N, t, N, g,
-                              u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x)),
-                              u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y)));
-                    u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
-                    if (gated)
-                        store_dot(kept.vv + (bh * (DV / 16) + slice) * N, t, N, g,
-                                  u[nt][0] * __uint_as_float(w[2 * h] << 16) +
-                                      u[nt][2] * __uint_as_float(w[2 * h + 1] << 16),
-                                  u[nt][1] * __uint_as_float(w[2 * h] & 0xffff0000u) +
-                                      u[nt][3] * __uint_as_float(w[2 * h + 1] & 0xffff0000u));
-                    v0 = max_abs(max_abs(v0, u[nt][0]), u[nt][1]);
-                    v1 = max_abs(max_abs(v1, u[nt][2]), u[nt][3]);
+                    const int nt = 2 * i + h;
+                    w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
+                    w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
+                    a[2 * h] = h2(u[nt][0] * s0.to, u[nt][1] * s0.to);
+                    a[2 * h + 1] = h2(u[nt][2] * s1.to, u[nt][3] * s1.to);
                 }
+                stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
+                keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
             }
-            __syncwarp();  // V is read; dV takes its place
-            v0 = quad_max(v0), v1 = quad_max(v1);
-            {
-                const Pow2 s0 = pow2_for(v0), s1 = pow2_for(v1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4], a[4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int nt = 2 * j + h;
-                        w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
-                        w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
-                        a[2 * h] = h2(u[nt][0] * s0.to, u[nt][1] * s0.to);
-                        a[2 * h + 1] = h2(u[nt][2] * s1.to, u[nt][3] * s1.to);
-                    }
-                    stsm4t(addr_ct<32>(sv, lane, 16 * j, 0), w);
-                    keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + j, lane, a);
-                }
-                if (tq == 0) {
-                    float* sd = kept.sD + (bh * nchunk + c) * DV + col0;
+            if (tq == 0) {
+                float* sd = kept.sD + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
+                sd[g] = p0.from, sd[g + 8] = p1.from;
+                if (SP == 1)
+                    sd[DV + g] = p0.from, sd[DV + g + 8] = p1.from;
+                if (sh.half == 0) {
                     float* sw = kept.sV + (bh * nchunk + c) * DV + col0;
-                    sd[g] = p0.from, sd[g + 8] = p1.from;
                     sw[g] = s0.from, sw[g + 8] = s1.from;
                 }
             }
-            __syncwarp();
-            {
-                const int64_t t0 = (int64_t)c * kC;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = (lane >> 1) + 16 * i, p = lane & 1;
-                    if (t0 + t < N)
-                        *reinterpret_cast<uint4*>(dv + (bh * N + t0 + t) * DV + col0 + p * 8) =
-                            *reinterpret_cast<const uint4*>(smem + mine + SM::v + tile_off<32>(t, p));
-                }
-            }
-            // dS0: both products on accumulators under one power of two
-            float w0 = 0.f, w1 = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-                ldsm4t(w, addr_ct<32>(tdo, lane, 16 * j, 0));
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * j + h;
-                    const float2 fo = *reinterpret_cast<const float2*>(fac + kFacO * kC + 8 * nt + 2 * tq);
-                    const float2 fa = *reinterpret_cast<const float2*>(fac + kFacA * kC + 8 * nt + 2 * tq);
-                    w0 = max_abs(max_abs(w0, fo.x * __uint_as_float(w[2 * h] << 16)),
-                                 fo.y * __uint_as_float(w[2 * h] & 0xffff0000u));
-                    w1 = max_abs(max_abs(w1, fo.x * __uint_as_float(w[2 * h + 1] << 16)),
-                                 fo.y * __uint_as_float(w[2 * h + 1] & 0xffff0000u));
-                    u[nt][0] *= -fa.x, u[nt][1] *= -fa.y, u[nt][2] *= -fa.x, u[nt][3] *= -fa.y;
-                    w0 = max_abs(max_abs(w0, u[nt][0]), u[nt][1]);
-                    w1 = max_abs(max_abs(w1, u[nt][2]), u[nt][3]);
-                }
-            }
-            const float gend = fac[kFacEnd * kC];
-            const Pow2 r0 = pow2_for(fmaxf(quad_max(w0), m0 * gend * 0.00390625f));
-            const Pow2 r1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
-            const float g0 = gend * r0.to, g1 = gend * r1.to;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                ds[nt][0] *= g0, ds[nt][1] *= g0;
-                ds[nt][2] *= g1, ds[nt][3] *= g1;
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                uint32_t w[4], hi[4], lo[4], b[4];
-                ldsm4t(w, addr_ct<32>(tdo, lane, 16 * kk, 0));
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 fo = *reinterpret_cast<const float2*>(fac + kFacO * kC + 16 * kk + 8 * h + 2 * tq);
-                    h2_split(fo.x * __uint_as_float(w[2 * h] << 16) * r0.to,
-                             fo.y * __uint_as_float(w[2 * h] & 0xffff0000u) * r0.to, hi[2 * h], lo[2 * h]);
-                    h2_split(fo.x * __uint_as_float(w[2 * h + 1] << 16) * r1.to,
-                             fo.y * __uint_as_float(w[2 * h + 1] & 0xffff0000u) * r1.to, hi[2 * h + 1],
-                             lo[2 * h + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, addr_bt<RB>(sQ, lane, 16 * kk, 16 * j));
-                    mma(ds[2 * j], hi, b[0], b[1]);
-                    mma(ds[2 * j + 1], hi, b[2], b[3]);
-                    mma(ds[2 * j], lo, b[0], b[1]);
-                    mma(ds[2 * j + 1], lo, b[2], b[3]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * kk + h;
-                    h2_split(u[nt][0] * r0.to, u[nt][1] * r0.to, hi[2 * h], lo[2 * h]);
-                    h2_split(u[nt][2] * r1.to, u[nt][3] * r1.to, hi[2 * h + 1], lo[2 * h + 1]);
-                }
-#pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, addr_bt<RB>(sK, lane, 16 * kk, 16 * j));
-                    mma(ds[2 * j], hi, b[0], b[1]);
-                    mma(ds[2 * j + 1], hi, b[2], b[3]);
-                    mma(ds[2 * j], lo, b[0], b[1]);
-                    mma(ds[2 * j + 1], lo, b[2], b[3]);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                ds[nt][0] *= r0.from, ds[nt][1] *= r0.from;
-                ds[nt][2] *= r1.from, ds[nt][3] *= r1.from;
-            }
-            if (gated && c > 0)
-                dot_state(c);
         }
+        __syncwarp();
+        {
+            const int64_t t0 = (int64_t)c * kC;
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
+                if (t0 + t < N)
+                    *reinterpret_cast<uint4*>(dv + (bh * N + t0 + t) * DV + col0 + p * 8) =
+                        *reinterpret_cast<const uint4*>(smem + mine + SM::v + tile_off<32>(t, p));
+            }
+        }
+        // dS0 on this warp's rows: both products on accumulators under one power of two
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+            ldsm4t(w, addr_ct<32>(tdo, lane, 16 * sh.tile(j), 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int nt = 2 * j + h;
+                const float2 fo = fac2(fac, kFacO, sh.tile(j), h, tq), fa = fac2(fac, kFacA, sh.tile(j), h, tq);
+                w0 = max_abs(max_abs(w0, fo.x * lo_f(w[2 * h])), fo.y * hi_f(w[2 * h]));
+                w1 = max_abs(max_abs(w1, fo.x * lo_f(w[2 * h + 1])), fo.y * hi_f(w[2 * h + 1]));
+                u[nt][0] *= -fa.x, u[nt][1] *= -fa.y, u[nt][2] *= -fa.x, u[nt][3] *= -fa.y;
+                w0 = max_abs(max_abs(w0, u[nt][0]), u[nt][1]);
+                w1 = max_abs(max_abs(w1, u[nt][2]), u[nt][3]);
+            }
+        }
+        const float gend = fac[kFacEnd * kC];
+        const Pow2 r0 = pow2_for(fmaxf(quad_max(w0), m0 * gend * 0.00390625f));
+        const Pow2 r1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
+        const float g0 = gend * r0.to, g1 = gend * r1.to;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ds[nt][0] *= g0, ds[nt][1] *= g0;
+            ds[nt][2] *= g1, ds[nt][3] *= g1;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t w[4], hi[4], lo[4], b[4];
+            ldsm4t(w, addr_ct<32>(tdo, lane, 16 * sh.tile(kk), 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 fo = fac2(fac, kFacO, sh.tile(kk), h, tq);
+                h2_split(fo.x * lo_f(w[2 * h]) * r0.to, fo.y * hi_f(w[2 * h]) * r0.to, hi[2 * h], lo[2 * h]);
+                h2_split(fo.x * lo_f(w[2 * h + 1]) * r1.to, fo.y * hi_f(w[2 * h + 1]) * r1.to, hi[2 * h + 1],
+                         lo[2 * h + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < KK; ++j) {
+                ldsm4t(b, addr_bt<RB>(sQ, lane, 16 * sh.tile(kk), d0 + 16 * j));
+                mma(ds[2 * j], hi, b[0], b[1]);
+                mma(ds[2 * j + 1], hi, b[2], b[3]);
+                mma(ds[2 * j], lo, b[0], b[1]);
+                mma(ds[2 * j + 1], lo, b[2], b[3]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int nt = 2 * kk + h;
+                h2_split(u[nt][0] * r0.to, u[nt][1] * r0.to, hi[2 * h], lo[2 * h]);
+                h2_split(u[nt][2] * r1.to, u[nt][3] * r1.to, hi[2 * h + 1], lo[2 * h + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < KK; ++j) {
+                ldsm4t(b, addr_bt<RB>(sK, lane, 16 * sh.tile(kk), d0 + 16 * j));
+                mma(ds[2 * j], hi, b[0], b[1]);
+                mma(ds[2 * j + 1], hi, b[2], b[3]);
+                mma(ds[2 * j], lo, b[0], b[1]);
+                mma(ds[2 * j + 1], lo, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ds[nt][0] *= r0.from, ds[nt][1] *= r0.from;
+            ds[nt][2] *= r1.from, ds[nt][3] *= r1.from;
+        }
+        if (gated && c > 0)
+            dot_state(c);
+        if (it + 1 < nchunk)
+            ok = sm100::mbar_wait(full + (it + 1) % kStages, ((it + 1) / kStages) & 1, kWaitPolls);
         ok = __syncthreads_and(ok);
-        if (!ok)
-            break;
-        if (tid == 0 && it + kStages < nchunk)
+        if (ok && tid == 0 && it + kStages < nchunk)
             load_stage(it + kStages);
     }
     cp_wait<0>();
@@ -1246,7 +1385,7 @@ __global__ void __launch_bounds__(32 * kRevWarps, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                dS0[(bh * D + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = ds[nt][e];
+                dS0[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = ds[nt][e];
     }
 }
 
@@ -1276,15 +1415,17 @@ struct DqkSmem {
     static constexpr int K = 0, Q = row_image<D>(), E = 2 * row_image<D>(), dV = E + kC * DV * 2,
                          dO = dV + kC * DV * 2, S = dO + kC * DV * 2, dS = S + D * DV * 2,
                          tile = dS + D * DV * 2, dm = tile + 8 * 16 * 128, vec = dm + kC * kLdD * 4,
-                         cols = vec + 16 * kC * 4, bytes = cols + 4 * DV * 4 + 64;
+                         cols = vec + 16 * kC * 4, bytes = cols + 6 * DV * 4 + 64;
 };
 
-// Kept blocks (16 value columns x 16) times their columns' factors c[col] / m
-__device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int per_slice, const float* c, float inv_m)
+// Kept blocks (16 value columns x 16; `per` of them per slice, the last half of
+// those with factors of their own behind the first) times c[col] / m
+__device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int per, int half, int DV, const float* c,
+                                          float inv_m)
 {
     for (int u = threadIdx.x; u < blocks * 32; u += kDqkThreads) {
-        const int block = u >> 5, col = block / per_slice * 16 + ((u >> 3) & 1) * 8 + (u & 7);
-        const __half2 f = __float2half2_rn(c[col] * inv_m);
+        const int block = u >> 5, col = block / per * 16 + ((u >> 3) & 1) * 8 + (u & 7);
+        const __half2 f = __float2half2_rn(c[col + (block % per >= half ? DV : 0)] * inv_m);
         uint4* at = reinterpret_cast<uint4*>(plane) + u;
         uint4 x = *at;
         __half2* h = reinterpret_cast<__half2*>(&x);
@@ -1323,8 +1464,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     float* eg = sdo + kC;                                   // e^G
     float* ege = eg + kC;                                   // e^{G_C - G}
     float* cE = reinterpret_cast<float*>(smem + SM::cols);
-    float *cS = cE + DV, *cV = cS + DV, *cD = cV + DV;
-    uint64_t* full = reinterpret_cast<uint64_t*>(cD + DV);
+    float *cV = cE + DV, *cS = cV + DV, *cD = cS + 2 * DV;  // cS, cD: per half of the rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(cD + 2 * DV);
     const int64_t kh = blockIdx.x / nchunk;
     const int c = blockIdx.x % nchunk;
     const int per = H / Hk;
@@ -1396,8 +1537,10 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         for (int i = tid; i < DV; i += kDqkThreads) {
             cE[i] = kept.sE[at * DV + i];
             cV[i] = kept.sV[at * DV + i];
-            cD[i] = kept.sD[at * DV + i];
-            cS[i] = kept.sS[(bh * (nchunk + 1) + c) * DV + i];
+        }
+        for (int i = tid; i < 2 * DV; i += kDqkThreads) {
+            cD[i] = kept.sD[at * 2 * DV + i];
+            cS[i] = kept.sS[(bh * (nchunk + 1) + c) * 2 * DV + i];
         }
         __syncthreads();
         const float *fB = vec + kFacB * kC, *fK = vec + kFacK * kC, *fQ = vec + kFacQ * kC,
@@ -1411,13 +1554,13 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             eg[tid] = exp2f(gh[tid] + gl[tid]);
             ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
         }
-        const float mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, DV), mD = warp_max(cD, DV);
+        const float mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
         ok = ok && sm100::mbar_wait(full, p & 1, kWaitPolls);
         if (ok) {  // 1 / m of a power of two is exact
-            one_scale(smem + SM::E, KS * 4, 4, cE, 1.0f / mE);
-            one_scale(smem + SM::dV, KS * 4, 4, cV, 1.0f / mV);
-            one_scale(smem + SM::S, KS * (D / 16), D / 16, cS, 1.0f / mS);
-            one_scale(smem + SM::dS, KS * (D / 16), D / 16, cD, 1.0f / mD);
+            one_scale(smem + SM::E, KS * 4, 4, 4, DV, cE, 1.0f / mE);
+            one_scale(smem + SM::dV, KS * 4, 4, 4, DV, cV, 1.0f / mV);
+            one_scale(smem + SM::S, KS * (D / 16), D / 16, D / 32, DV, cS, 1.0f / mS);
+            one_scale(smem + SM::dS, KS * (D / 16), D / 16, D / 32, DV, cD, 1.0f / mD);
         }
         ok = __syncthreads_and(ok);
         if (!ok)
@@ -1584,8 +1727,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 z[h] = y;
             }
             if (dlog_alpha) {
-                for (int s = 0; s < KS; ++s)
-                    after += kept.cd[(bh * KS + s) * nchunk + c];
+                for (int s = 0; s < 2 * KS; ++s)
+                    after += kept.cd[(bh * 2 * KS + s) * nchunk + c];
 #pragma unroll
                 for (int h = 1; h >= 0; --h) {
 #pragma unroll
@@ -1678,41 +1821,86 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
     l.rows = take((size_t)(a.B * a.Hk) * n * 2 * kC * a.d * 2);
     l.blobs = take(BH * n * blob_bytes<true>());
     l.S = take(BH * (n + 1) * 2 * state);
-    l.sS = take(BH * (n + 1) * a.dv * 4);
+    l.sS = take(BH * (n + 1) * 2 * a.dv * 4);
     l.E = take(BH * n * 2 * toks);
     l.sE = take(BH * n * a.dv * 4);
     l.dS = take(BH * n * state);
-    l.sD = take(BH * n * a.dv * 4);
+    l.sD = take(BH * n * 2 * a.dv * 4);
     l.dV = take(BH * n * toks);
     l.sV = take(BH * n * a.dv * 4);
     l.oo = take(BH * sl * (size_t)a.N * 4);
     l.vv = take(BH * sl * (size_t)a.N * 4);
     l.bb = take(BH * sl * (size_t)a.N * 4);
-    l.cd = take(BH * sl * n * 4);
+    l.cd = take(BH * sl * 2 * n * 4);
     l.total = at;
     return l;
 }
 
-// Warps per CTA of the chain: as few as give no more CTAs than SMs (a warp alone
-// on its sub-partition has that tensor core to itself), at most all columns.
-int chain_warps(const DeltaArgs& a, int cap)
+// How a chain kernel is cut.  SP = 2 (two warps per slice) while that gives no
+// more warps than the GPU has sub-partitions to give each a tensor core of its own;
+// slices per CTA: as few as give no more CTAs than SMs, at most `cap`.
+struct Cut {
+    int SP, W;
+};
+Cut cut_of(const DeltaArgs& a, int cap1, int cap2)
 {
-    const int most = a.dv / 16 < cap ? a.dv / 16 : cap, sms = device_sm_count();
-    int W = 1;
-    while (W < most && a.B * a.H * (a.dv / (16 * W)) > sms)
-        W *= 2;
-    return W;
+    const int sms = device_sm_count();
+    const int64_t slices = a.B * a.H * (a.dv / 16);
+    Cut c;
+    c.SP = 2 * slices <= 4 * (int64_t)sms ? 2 : 1;
+    const int cap = c.SP == 2 ? cap2 : cap1;
+    c.W = 1;
+    while (2 * c.W <= cap && 2 * c.W <= a.dv / 16 && slices / c.W > sms)
+        c.W *= 2;
+    return c;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int D, bool GRAD, int SP>
+cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
+                         const Kept& kept)
+{
+    const int smem = ChainSmem<D, GRAD, SP>::bytes(W);
+    const cudaError_t e = allow_smem(k_delta_chain<D, GRAD, SP>, smem);
+    if (e != cudaSuccess)
+        return e;
+    k_delta_chain<D, GRAD, SP><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+        rows, blobs, static_cast<const __nv_bfloat16*>(a.v), GRAD ? nullptr : static_cast<__nv_bfloat16*>(a.out), a.S0,
+        GRAD ? nullptr : a.S_out, a.N, n, (int)a.H, (int)a.Hk, a.dv, static_cast<const __nv_bfloat16*>(a.dout), kept,
+        a.status);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int D, int SP>
+cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
+                       const Kept& kept)
+{
+    const int smem = RevSmem<D, SP>::bytes(W);
+    const cudaError_t e = allow_smem(k_delta_rev<D, SP>, smem);
+    if (e != cudaSuccess)
+        return e;
+    k_delta_rev<D, SP><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+        rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
+        static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, n, (int)a.H, (int)a.Hk, a.dv, a.log_alpha != nullptr, kept,
+        a.status);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t run_forward(const DeltaArgs& a, int* status)
+cudaError_t run_forward(const DeltaArgs& a)
 {
     const TcLayout l = tc_layout(a);
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     const int n = chunks_of(a.N);
     const int64_t BH = a.B * a.H;
-    cudaError_t e = cudaFuncSetAttribute(
-        k_delta_prep<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrepSmem<D, false>::bytes);
+    cudaError_t e = allow_smem(k_delta_prep<D, false>, PrepSmem<D, false>::bytes);
     if (e != cudaSuccess)
         return e;
     k_delta_prep<D, false><<<(unsigned)(BH * n), kPrepThreads, PrepSmem<D, false>::bytes, a.stream>>>(
@@ -1723,22 +1911,9 @@ cudaError_t run_forward(const DeltaArgs& a, int* status)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    const int W = chain_warps(a, 8);
-    const int smem = ChainSmem<D, false>::bytes(W);
-    e = cudaFuncSetAttribute(k_delta_chain<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    k_delta_chain<D, false><<<(unsigned)(BH * (a.dv / (16 * W))), 32 * W, smem, a.stream>>>(
-        ws + l.rows, ws + l.blobs, static_cast<const __nv_bfloat16*>(a.v),
-        static_cast<__nv_bfloat16*>(a.out), a.S0, a.S_out, a.N, n, (int)a.H, (int)a.Hk, a.dv, nullptr, Kept{}, status);
-    count_launches(1);
-    return cudaGetLastError();
-}
-
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes)
-{
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const Cut cut = cut_of(a, 8, 4);
+    return cut.SP == 2 ? launch_chain<D, false, 2>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{})
+                       : launch_chain<D, false, 1>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{});
 }
 
 template <int D, int DV>
@@ -1751,15 +1926,8 @@ cudaError_t run_backward(const DeltaArgs& a)
                        ws + l.dV, f32(l.sV), f32(l.oo), f32(l.vv), f32(l.bb), f32(l.cd)};
     const int n = chunks_of(a.N), H = (int)a.H, Hk = (int)a.Hk, l2 = a.fm == LA_FM_L2;
     const int64_t BH = a.B * a.H;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v);
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(a.dout);
-    const int Wc = chain_warps(a, 8), Wr = chain_warps(a, kRevWarps);
-    const int smem_c = ChainSmem<D, true>::bytes(Wc), smem_r = RevSmem<D>::bytes(Wr);
     cudaError_t e = allow_smem(k_delta_prep<D, true>, PrepSmem<D, true>::bytes);
-    if (e == cudaSuccess)
-        e = allow_smem(k_delta_chain<D, true>, smem_c);
-    if (e == cudaSuccess)
-        e = allow_smem(k_delta_rev<D>, smem_r);
     if (e == cudaSuccess)
         e = allow_smem(k_delta_dqk<D, DV>, DqkSmem<D, DV>::bytes);
     if (e != cudaSuccess)
@@ -1770,16 +1938,14 @@ cudaError_t run_backward(const DeltaArgs& a)
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    k_delta_chain<D, true><<<(unsigned)(BH * (DV / (16 * Wc))), 32 * Wc, smem_c, a.stream>>>(
-        ws + l.rows, ws + l.blobs, v, nullptr, a.S0, nullptr, a.N, n, H, Hk, DV, dout, kept, a.status);
-    count_launches(1);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
-    k_delta_rev<D><<<(unsigned)(BH * (DV / (16 * Wr))), 32 * Wr, smem_r, a.stream>>>(
-        ws + l.rows, ws + l.blobs, v, dout, a.dS_out, static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, n,
-        H, Hk, DV, a.log_alpha != nullptr, kept, a.status);
-    count_launches(1);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    const Cut cut = cut_of(a, 8, 4), rev = cut_of(a, 4, 2);
+    const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
+    e = cut.SP == 2 ? launch_chain<D, true, 2>(a, cut.W, rows, blobs, n, kept)
+                    : launch_chain<D, true, 1>(a, cut.W, rows, blobs, n, kept);
+    if (e == cudaSuccess)
+        e = rev.SP == 2 ? launch_rev<D, 2>(a, rev.W, rows, blobs, n, kept)
+                        : launch_rev<D, 1>(a, rev.W, rows, blobs, n, kept);
+    if (e != cudaSuccess)
         return e;
     k_delta_dqk<D, DV><<<(unsigned)(a.B * a.Hk * n), kDqkThreads, DqkSmem<D, DV>::bytes, a.stream>>>(
         ws + l.rows, ws + l.blobs, dout, kept, static_cast<__nv_bfloat16*>(a.dq),
@@ -1807,9 +1973,9 @@ size_t delta_tc_forward_workspace(const DeltaArgs& a) { return tc_layout(a).tota
 cudaError_t delta_tc_forward(const DeltaArgs& a)
 {
     switch (a.d) {
-    case 32: return run_forward<32>(a, a.status);
-    case 64: return run_forward<64>(a, a.status);
-    default: return run_forward<128>(a, a.status);
+    case 32: return run_forward<32>(a);
+    case 64: return run_forward<64>(a);
+    default: return run_forward<128>(a);
     }
 }
 

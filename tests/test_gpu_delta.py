@@ -463,3 +463,13 @@ def test_backward_with_a_loss_scale():
     check_backward(p)
     p["dout"] = (p["dout"].float() * 2.0 ** -70).to(BF)
     check_backward(p)
+
+
+@pytest.mark.parametrize("B,H,Hk,N,d,dv", [(10, 8, 4, 150, 64, 64), (40, 2, 1, 97, 128, 128),
+                                           (160, 2, 2, 70, 32, 32), (13, 12, 12, 66, 64, 128)])
+def test_many_heads(B, H, Hk, N, d, dv):
+    """More 16-column slices than the GPU gives two warps each: one warp per
+    slice, several slices per CTA."""
+    p = problem(B, H, Hk, N, d, dv, BF, B + d)
+    check_forward(p)
+    check_backward(p)
