@@ -335,7 +335,8 @@ LA_API la_status la_backward_delta(const void* dout, const float* dS_out, const 
  * x [B,H,N,dv] in x_dtype is head-major, as the forwards write it; gate (NULL:
  * no gate) and y [B,N,H,dv] in dtype are token-major, as projections read and
  * write them.  weight: fp32 [dv] (weight_heads = 0), [H,dv] (weight_heads = 1)
- * or NULL for 1.  activation: la_activation.  eps > 0.  dv in {32, 64, 128}.
+ * or NULL for 1.  activation: la_activation.  eps > 0.  dv in {32, 64, 128},
+ * H <= 16384, fewer than 2^31 rows.
  */
 LA_API la_status la_norm_gate(const void* x, const void* gate, const float* weight, void* y,
                               int64_t B, int64_t H, int64_t N, int dv, int activation,

@@ -25,5 +25,6 @@ def __getattr__(name):
     if name in _EXPORTS:
         from . import _binding
 
-        return getattr(_binding, name)
+        globals()[name] = value = getattr(_binding, name)  # looked up once
+        return value
     raise AttributeError(name)

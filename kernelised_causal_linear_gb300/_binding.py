@@ -351,55 +351,56 @@ def la_favor_features(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None
     return out
 
 
-def _arg(t: torch.Tensor | None, name: str, shape, dtype, device) -> int | None:
+def _arg(t: torch.Tensor | None, name: str, shape, dtype, index: int) -> int | None:
     """Device pointer of a tensor that has to have this shape, type and place."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    ptr = _dev_ptr(t, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
-    return ptr
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _current(t: torch.Tensor, name: str) -> torch.device:
+def _current(t: torch.Tensor, name: str) -> int:
     """The device of a call: its tensors' device, which has to be the current one."""
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     _dtype(t)
-    return t.device
+    return index
 
 
 class _Call:
     """The stream of a call and what is allocated for it: outputs and scratch
     belong to that stream, so none is handed out again before it has run."""
 
-    def __init__(self, stream, device):
-        self.device = device
-        if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-        elif isinstance(stream, int):
-            self.stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
-                torch.cuda.default_stream(device)
-        else:
-            self.stream = stream
-        self.other = self.stream != torch.cuda.current_stream(device)
-        self.handle = self.stream.cuda_stream or None
+    def __init__(self, stream, index: int):
+        self.index = index
+        self.handle = torch._C._cuda_getCurrentRawStream(index)
+        self.side = None  # the call's stream where it is not the current one
+        if stream is not None:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            if handle != self.handle:
+                self.handle = handle
+                self.side = torch.cuda.ExternalStream(handle, device=index) if handle else \
+                    torch.cuda.default_stream(index)
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other:
+        t = torch.empty(shape, dtype=dtype, device=self.index)
+        if self.side is not None:
             # allocated for the current stream: the call's own may write only
             # once what had the memory before is done, and the memory stays
             # until the call is
-            self.stream.wait_stream(torch.cuda.current_stream(self.device))
-            t.record_stream(self.stream)
+            self.side.wait_stream(torch.cuda.current_stream(self.index))
+            t.record_stream(self.side)
         return t
 
     def scratch(self, workspace, need):
@@ -408,10 +409,9 @@ class _Call:
             if need == 0:
                 return None, 0
             workspace = self.empty(need, torch.uint8)
-        ptr = _dev_ptr(workspace, "workspace")
-        if workspace.device != self.device:
-            raise ValueError(f"workspace is on {workspace.device}, not {self.device}")
-        return ptr, workspace.numel() * workspace.element_size()
+        elif workspace.get_device() != self.index:
+            raise ValueError(f"workspace is on {workspace.device}, not cuda:{self.index}")
+        return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
 def _delta_sizes(k, v):

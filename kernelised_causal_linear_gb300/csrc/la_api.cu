@@ -542,8 +542,9 @@ static la_status check_norm(const NormGateArgs& a)
         (a.x_dtype != LA_BF16 && a.x_dtype != LA_FP32) ||
         (a.dtype != LA_BF16 && a.dtype != LA_FP32))
         return LA_ERR_INVALID_ARG;
-    // rows and the blocks of a gradient are counted in a 32-bit grid
-    if (!dim_ok(a.dv) || a.H > (1 << 20) || a.B > INT32_MAX / a.H ||
+    // rows are counted in 32 bits; a gradient with a weight for each head keeps up to
+    // H rows of partial sums per lane group
+    if (!dim_ok(a.dv) || a.H > 16384 || a.B > INT32_MAX / a.H ||
         (a.N > 0 && a.B * a.H > INT32_MAX / a.N))
         return LA_ERR_UNSUPPORTED;
     return LA_OK;

@@ -112,6 +112,15 @@ def test_many_rows_repeat_bitwise():
     check(x, gate, w, dy, "silu")
 
 
+@pytest.mark.parametrize("B,H,N,dv", [(1, 7, 3, 32), (2, 33, 29, 64), (1, 130, 11, 128),
+                                      (3, 64, 40, 32), (1, 1, 5000, 128), (2, 48, 333, 64)])
+def test_head_counts(B, H, N, dv):
+    """Weights for each head with head counts that do and do not divide a block's
+    rows, more heads than rows per block among them."""
+    check(*problem(B, H, N, dv, F32, F32, True, H), "silu")
+    check(*problem(B, H, N, dv, BF, BF, False, H), "sigmoid")
+
+
 def test_no_tokens():
     x, gate, w, dy = problem(2, 3, 0, 64, F32, F32, True, 5)
     assert la.la_norm_gate(x, gate, w).shape == (2, 0, 3, 64)
