@@ -1407,15 +1407,22 @@ __global__ void __launch_bounds__(128, 1)
 // throughout (2^-12 of a term, under the results' own rounding to bf16).
 // Loops over fragments stay rolled: unrolled, the two roles' code overran the
 // instruction cache and its misses were half of all stalls.
+//
+// A CTA per SM takes every gridDim-th chunk.  Its loads run a step (one value head
+// of one chunk) ahead: the token planes have two buffers; the state planes are used
+// first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
+// waiting for its own 150 KB: 508 against 330 us at B4 H8 N8192 d=128.)
 constexpr int kDqkThreads = 256;
-constexpr int kLdD = 66;  // row stride of the decay matrix
 
 template <int D, int DV>
 struct DqkSmem {
-    static constexpr int K = 0, Q = row_image<D>(), E = 2 * row_image<D>(), dV = E + kC * DV * 2,
-                         dO = dV + kC * DV * 2, S = dO + kC * DV * 2, dS = S + D * DV * 2,
-                         tile = dS + D * DV * 2, dm = tile + 8 * 16 * 128, vec = dm + kC * kLdD * 4,
-                         cols = vec + 16 * kC * 4, bytes = cols + 6 * DV * 4 + 64;
+    // a step's token planes, factors and column scales, twice
+    static constexpr int E = 0, dV = kC * DV * 2, dO = 2 * kC * DV * 2, fac = 3 * kC * DV * 2,
+                         cols = fac + kGradFactors * kC * 4, step = cols + 6 * DV * 4;
+    static constexpr int S = 2 * step, dS = S + D * DV * 2, K = dS + D * DV * 2, Q = K + row_image<D>(),
+                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + 3 * kC * 4,
+                         bytes = bar + 64;
+    static_assert(bytes <= 232448, "shared memory");
 };
 
 // Kept blocks (16 value columns x 16; `per` of them per slice, the last half of
@@ -1432,6 +1439,12 @@ __device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int 
         h[0] = __hmul2(h[0], f), h[1] = __hmul2(h[1], f), h[2] = __hmul2(h[2], f), h[3] = __hmul2(h[3], f);
         *at = x;
     }
+}
+
+// a warp's wait: one verdict for all lanes
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, kWaitPolls));
 }
 
 // largest of c[0 .. n), by every lane of a warp
@@ -1451,114 +1464,134 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     k_delta_dqk(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ dout, Kept kept, __nv_bfloat16* __restrict__ dq,
                 __nv_bfloat16* __restrict__ dk, float* __restrict__ dbeta, float* __restrict__ dlog_alpha,
-                int64_t N, int nchunk, int H, int Hk, int l2, float scale, int* status)
+                int64_t N, int nchunk, int items, int H, int Hk, int l2, float scale, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = DqkSmem<D, DV>;
     constexpr int RB = 2 * D, VB = 2 * DV, NT = D / 8, KS = DV / 16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const uint32_t base = smem_addr(smem);
-    float* dm = reinterpret_cast<float*>(smem + SM::dm);    // [i][j], j <= i
-    float* vec = reinterpret_cast<float*>(smem + SM::vec);  // [kGradFactors][kC], then
-    float* sdo = vec + kGradFactors * kC;                   // dO's row scales
+    float* sdo = reinterpret_cast<float*>(smem + SM::vec);  // dO's row scales
     float* eg = sdo + kC;                                   // e^G
     float* ege = eg + kC;                                   // e^{G_C - G}
-    float* cE = reinterpret_cast<float*>(smem + SM::cols);
-    float *cV = cE + DV, *cS = cV + DV, *cD = cS + 2 * DV;  // cS, cD: per half of the rows
-    uint64_t* full = reinterpret_cast<uint64_t*>(cD + 2 * DV);
-    const int64_t kh = blockIdx.x / nchunk;
-    const int c = blockIdx.x % nchunk;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bar);  // token planes (2), states, row images
     const int per = H / Hk;
-    const int64_t t0 = (int64_t)c * kC;
-    const int n = (int)min((int64_t)kC, N - t0);
     const bool role_k = warp >= 4;
     const int rt = warp & 3, r0 = 16 * rt;
     const uint32_t mytile = base + SM::tile + warp * 16 * 128;
+    const int steps = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * per;
 
     if (tid == 0) {
-        sm100::mbar_init(full, 1);
+        for (int i = 0; i < 4; ++i)
+            sm100::mbar_init(full + i, 1);
         sm100::fence_mbar_init();
     }
+    __syncthreads();
+    struct Step {
+        int64_t kh, bh, at, t0;
+        int c, n;
+    };
+    auto step_of = [&](int s) {
+        Step x;
+        const int item = blockIdx.x + s / per * gridDim.x;
+        x.kh = item / nchunk, x.c = item % nchunk;
+        x.bh = x.kh / Hk * H + (x.kh % Hk) * per + s % per;
+        x.at = x.bh * nchunk + x.c;
+        x.t0 = (int64_t)x.c * kC;
+        x.n = (int)min((int64_t)kC, N - x.t0);
+        return x;
+    };
+    // loads, by one thread, after every thread's accesses to the buffer are fenced
+    auto load_tokens = [&](int s) {
+        const Step x = step_of(s);
+        const uint32_t to = base + (s & 1) * SM::step;
+        uint64_t* bar = full + (s & 1);
+        sm100::mbar_arrive_expect_tx(bar, 2 * kC * DV * 2 + x.n * DV * 2 + kGradFactors * kC * 4 + 6 * DV * 4);
+        delta::bulk_load(to + SM::E, kept.E + 2 * x.at * (kC * DV * 2), kC * DV * 2, bar);
+        delta::bulk_load(to + SM::dV, kept.dV + x.at * (kC * DV * 2), kC * DV * 2, bar);
+        delta::bulk_load(to + SM::dO, dout + (x.bh * N + x.t0) * DV, x.n * DV * 2, bar);
+        delta::bulk_load(to + SM::fac, blobs + x.at * (int64_t)blob_bytes<true>() + fac_at<true>(),
+                         kGradFactors * kC * 4, bar);
+        delta::bulk_load(to + SM::cols, kept.sE + x.at * DV, DV * 4, bar);
+        delta::bulk_load(to + SM::cols + DV * 4, kept.sV + x.at * DV, DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 2 * DV * 4, kept.sS + (x.bh * (nchunk + 1) + x.c) * 2 * DV, 2 * DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 4 * DV * 4, kept.sD + x.at * 2 * DV, 2 * DV * 4, bar);
+    };
+    auto load_states = [&](int s) {
+        const Step x = step_of(s);
+        sm100::mbar_arrive_expect_tx(full + 2, 2 * D * DV * 2);
+        delta::bulk_load(base + SM::S, kept.S + 2 * (x.bh * (nchunk + 1) + x.c) * (int64_t)(D * DV * 2), D * DV * 2,
+                         full + 2);
+        delta::bulk_load(base + SM::dS, kept.dS + x.at * (D * DV * 2), D * DV * 2, full + 2);
+    };
+    auto load_rows = [&](int s) {
+        const Step x = step_of(s);
+        sm100::mbar_arrive_expect_tx(full + 3, 2 * row_image<D>());
+        delta::bulk_load(base + SM::K, rows + (x.kh * nchunk + x.c) * (int64_t)(2 * row_image<D>()),
+                         2 * row_image<D>(), full + 3);
+    };
+    if (tid == 0 && steps > 0) {
+        load_tokens(0);
+        load_states(0);
+        load_rows(0);
+    }
     float tot[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            tot[nt][e] = 0.f;
-
     bool ok = true;
-    for (int p = 0; p < per; ++p) {
-        const int64_t bh = kh / Hk * H + (kh % Hk) * per + p;
-        const int64_t at = bh * nchunk + c;
-        __syncthreads();  // the head before is done with the tiles
-        if (tid == 0) {
-            sm100::fence_proxy_async_smem();  // their rescaling was written by threads
-            const uint32_t bytes = 2 * kC * DV * 2 + 2 * D * DV * 2 + (p == 0 ? 2 * row_image<D>() : 0);
-            sm100::mbar_arrive_expect_tx(full, bytes);
-            if (p == 0)
-                delta::bulk_load(base + SM::K, rows + (kh * nchunk + c) * (int64_t)(2 * row_image<D>()),
-                                 2 * row_image<D>(), full);
-            delta::bulk_load(base + SM::E, kept.E + 2 * at * (kC * DV * 2), kC * DV * 2, full);
-            delta::bulk_load(base + SM::dV, kept.dV + at * (kC * DV * 2), kC * DV * 2, full);
-            delta::bulk_load(base + SM::S, kept.S + 2 * (bh * (nchunk + 1) + c) * (int64_t)(D * DV * 2),
-                             D * DV * 2, full);
-            delta::bulk_load(base + SM::dS, kept.dS + at * (D * DV * 2), D * DV * 2, full);
-        }
-        // dO as scaled fp16 rows, factors, column scales
-        constexpr int LPR = DV / 8, RPP = kDqkThreads / LPR;
+    for (int s = 0; s < steps; ++s) {
+        const Step me = step_of(s);
+        const int buf = (s & 1) * SM::step, p = s % per, n = me.n;
+        const int64_t t0 = me.t0, bh = me.bh;
+        if (p == 0)
+            clear(tot);
+        if (tid == 0 && s + 1 < steps)
+            load_tokens(s + 1);
+        const int oE = buf + SM::E, odV = buf + SM::dV, odO = buf + SM::dO;
+        const float* fac = reinterpret_cast<const float*>(smem + buf + SM::fac);
+        const float *cE = reinterpret_cast<const float*>(smem + buf + SM::cols), *cV = cE + DV, *cS = cV + DV,
+                    *cD = cS + 2 * DV;
+        const float *fB = fac + kFacB * kC, *fK = fac + kFacK * kC, *fQ = fac + kFacQ * kC, *gh = fac + kFacGh * kC,
+                    *gl = fac + kFacGl * kC;
+        ok = ok && wait_warp(full + (s & 1), (s >> 1) & 1);
+        float mE = 0.f, mV = 0.f, mS = 0.f, mD = 0.f;
+        if (ok) {
+            // dO to scaled fp16 rows in place, a row by the lanes of one warp
+            constexpr int LPR = DV / 8, RPP = kDqkThreads / LPR;
 #pragma unroll
-        for (int b = 0; b < kC; b += RPP) {
-            const int r = b + tid / LPR, part = tid % LPR;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < n)
-                w = *reinterpret_cast<const uint4*>(dout + (bh * N + t0 + r) * DV + part * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float f[8], mx = 0.f;
+            for (int b = 0; b < kC; b += RPP) {
+                const int r = b + tid / LPR, part = tid % LPR;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (r < n)
+                    w = *reinterpret_cast<const uint4*>(smem + odO + r * VB + part * 16);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                float f[8], mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(u[i] << 16);
-                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-                mx = max_abs(max_abs(mx, f[2 * i]), f[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    f[2 * i] = lo_f(u[i]), f[2 * i + 1] = hi_f(u[i]);
+                    mx = max_abs(max_abs(mx, f[2 * i]), f[2 * i + 1]);
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const Pow2 q = pow2_for(mx);
+                uint4 h;
+                h.x = h2(f[0] * q.to, f[1] * q.to), h.y = h2(f[2] * q.to, f[3] * q.to);
+                h.z = h2(f[4] * q.to, f[5] * q.to), h.w = h2(f[6] * q.to, f[7] * q.to);
+                __syncwarp();
+                *reinterpret_cast<uint4*>(smem + odO + tile_off<VB>(r, part)) = h;
+                if (part == 0)
+                    sdo[r] = q.from;
             }
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const Pow2 s = pow2_for(mx);
-            uint4 h;
-            h.x = h2(f[0] * s.to, f[1] * s.to), h.y = h2(f[2] * s.to, f[3] * s.to);
-            h.z = h2(f[4] * s.to, f[5] * s.to), h.w = h2(f[6] * s.to, f[7] * s.to);
-            *reinterpret_cast<uint4*>(smem + SM::dO + tile_off<VB>(r, part)) = h;
-            if (part == 0)
-                sdo[r] = s.from;
+            if (tid < kC) {
+                eg[tid] = exp2f(gh[tid] + gl[tid]);
+                ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
+            }
+            mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
+            // 1 / m of a power of two is exact
+            one_scale(smem + oE, KS * 4, 4, 4, DV, cE, 1.0f / mE);
+            one_scale(smem + odV, KS * 4, 4, 4, DV, cV, 1.0f / mV);
         }
-        const float* fac = reinterpret_cast<const float*>(blobs + at * (int64_t)blob_bytes<true>() + fac_at<true>());
-        for (int i = tid; i < kGradFactors * kC; i += kDqkThreads)
-            vec[i] = fac[i];
-        for (int i = tid; i < DV; i += kDqkThreads) {
-            cE[i] = kept.sE[at * DV + i];
-            cV[i] = kept.sV[at * DV + i];
-        }
-        for (int i = tid; i < 2 * DV; i += kDqkThreads) {
-            cD[i] = kept.sD[at * 2 * DV + i];
-            cS[i] = kept.sS[(bh * (nchunk + 1) + c) * 2 * DV + i];
-        }
-        __syncthreads();
-        const float *fB = vec + kFacB * kC, *fK = vec + kFacK * kC, *fQ = vec + kFacQ * kC,
-                    *gh = vec + kFacGh * kC, *gl = vec + kFacGl * kC;
-        for (int i = tid; i < kC * kC; i += kDqkThreads) {
-            const int y = i / kC, x = i % kC;
-            if (x <= y)
-                dm[y * kLdD + x] = exp2f((gh[y] - gh[x]) + (gl[y] - gl[x]));
-        }
-        if (tid < kC) {
-            eg[tid] = exp2f(gh[tid] + gl[tid]);
-            ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
-        }
-        const float mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
-        ok = ok && sm100::mbar_wait(full, p & 1, kWaitPolls);
-        if (ok) {  // 1 / m of a power of two is exact
-            one_scale(smem + SM::E, KS * 4, 4, 4, DV, cE, 1.0f / mE);
-            one_scale(smem + SM::dV, KS * 4, 4, 4, DV, cV, 1.0f / mV);
+        ok = ok && wait_warp(full + 2, s & 1);
+        if (ok) {
             one_scale(smem + SM::S, KS * (D / 16), D / 16, D / 32, DV, cS, 1.0f / mS);
             one_scale(smem + SM::dS, KS * (D / 16), D / 16, D / 32, DV, cD, 1.0f / mD);
         }
@@ -1570,8 +1603,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         // A fragments of this warp's rows, 16 value columns ks: dO is row-major, kept
         // planes lie turned
         auto a_rows = [&](uint32_t (&x)[4], int plane, int ks) {
-            if (plane == SM::dO) {
-                ldsm4(x, addr_a<VB>(base + SM::dO, lane, r0, 16 * ks));
+            if (plane == odO) {
+                ldsm4(x, addr_a<VB>(base + odO, lane, r0, 16 * ks));
             } else {
                 uint32_t y[4];
                 ldsm4t(y, base + plane + (ks * 4 + rt) * 512 + lane * 16);
@@ -1593,8 +1626,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j >= lo && j <= hi) {
-                        if (b_plane == SM::dO)
-                            ldsm4(b, addr_b<VB>(base + SM::dO, lane, 16 * j, 16 * ks));
+                        if (b_plane == odO)
+                            ldsm4(b, addr_b<VB>(base + odO, lane, 16 * j, 16 * ks));
                         else
                             ldsm4t(b, base + b_plane + (ks * 4 + j) * 512 + lane * 16);
                         mma(x[2 * j], a, b[0], b[1]);
@@ -1668,48 +1701,59 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             }
             add(acc, pa.from, pb.from);
         };
-        float x[8][4];
+        // the products with the states first: their planes are refilled meanwhile
         if (!role_k) {
-            dots(x, SM::dO, SM::E, 0, rt);
+            state(odO, SM::S, eg[ia] * (sdo[ia] * mS), eg[ib] * (sdo[ib] * mS));
+        } else {
+            state(odV, SM::S, -eg[ia] * (mV * mS), -eg[ib] * (mV * mS));
+            state(oE, SM::dS, ege[ia] * fB[ia] * (mE * mD), ege[ib] * fB[ib] * (mE * mD));
+        }
+        sm100::fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0 && s + 1 < steps)
+            load_states(s + 1);
+        if (p == 0)
+            ok = wait_warp(full + 3, (s / per) & 1);
+        if (ok && !role_k) {
+            float x[8][4];
+            dots(x, odO, oE, 0, rt);
             const float fa = mE * sdo[ia], fb = mE * sdo[ib];
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int nt = 0; nt < 8; ++nt) {
+                const int j0 = 8 * nt + 2 * tq;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = e >> 1 ? ib : ia, j = 8 * nt + 2 * tq + (e & 1);
-                    x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * dm[i * kLdD + j] * (fB[j] * fK[j]) : 0.f;
+                    const int i = e >> 1 ? ib : ia, j = j0 + (e & 1);
+                    const float dec = ex2((gh[i] - gh[j]) + (gl[i] - gl[j]));
+                    x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * dec * (fB[j] * fK[j]) : 0.f;
                 }
+            }
             rows_product(x, SM::K, 0, rt);
-            state(SM::dO, SM::S, eg[ia] * (sdo[ia] * mS), eg[ib] * (sdo[ib] * mS));
-        } else {
-            float y[8][4];
-            const float fm = mE * mV;
-            dots(x, SM::E, SM::dV, rt, 3);
-            dots(y, SM::dV, SM::E, 0, rt);
+        } else if (ok) {
+            float x[8][4], y[8][4];
+            {
+                float z[8][4];
+                const float fm = mE * mV;
+                dots(z, oE, odV, rt, 3);
+                dots(y, odV, oE, 0, rt);
+                dots(x, oE, odO, rt, 3);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+                for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
-                    y[nt][e] = i > j   ? -x[nt][e] * fm * dm[i * kLdD + j] * (fB[j] * fK[i])
-                               : i < j ? -y[nt][e] * fm * dm[j * kLdD + i] * (fB[i] * fK[i])
-                                       : 0.f;
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
+                        const float d = (gh[i] - gh[j]) + (gl[i] - gl[j]), dec = ex2(i >= j ? d : -d);
+                        y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * fK[i])
+                                   : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i])
+                                           : 0.f;
+                        x[nt][e] = i >= j ? x[nt][e] * (mE * sdo[i]) * dec * (fB[j] * (fQ[i] * scale)) : 0.f;
+                    }
+            }
             rows_product(y, SM::K, 0, 3);
-            dots(x, SM::E, SM::dO, rt, 3);
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
-                    x[nt][e] = i >= j ? x[nt][e] * (mE * sdo[i]) * dm[i * kLdD + j] * (fB[j] * (fQ[i] * scale)) : 0.f;
-                }
             rows_product(x, SM::Q, rt, 3);
-            state(SM::dV, SM::S, -eg[ia] * (mV * mS), -eg[ib] * (mV * mS));
-            state(SM::E, SM::dS, ege[ia] * fB[ia] * (mE * mD), ege[ib] * fB[ib] * (mE * mD));
         }
         // the gates' gradients from the dots over 16 columns each
-        if (warp == 0) {
+        if (ok && warp == 0) {
             float z[2], after = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1728,7 +1772,7 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             }
             if (dlog_alpha) {
                 for (int s = 0; s < 2 * KS; ++s)
-                    after += kept.cd[(bh * 2 * KS + s) * nchunk + c];
+                    after += kept.cd[(bh * 2 * KS + s) * nchunk + me.c];
 #pragma unroll
                 for (int h = 1; h >= 0; --h) {
 #pragma unroll
@@ -1744,46 +1788,55 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 }
             }
         }
-    }
-    if (!ok) {
-        if (tid == 0)
-            set_status(status, LA_ERR_TIMEOUT);
-        return;
-    }
-    // through scale and norm: unit = f image, dx = r (x - unit (unit.x))
-    const int image = role_k ? SM::K : SM::Q;
-    const float* f = vec + (role_k ? kFacK : kFacQ) * kC;
-    const float* rr = vec + (role_k ? kFacRk : kFacRq) * kC;
-    __nv_bfloat16* dst = role_k ? dk : dq;
-    const float mul = role_k ? 1.0f : scale;
+        if (ok && p == per - 1) {
+            // through scale and norm: unit = f image, dx = r (x - unit (unit.x))
+            const int image = role_k ? SM::K : SM::Q;
+            const float* f = fac + (role_k ? kFacK : kFacQ) * kC;
+            const float* rr = fac + (role_k ? kFacRk : kFacRq) * kC;
+            __nv_bfloat16* dst = role_k ? dk : dq;
+            const float mul = role_k ? 1.0f : scale;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int i = r0 + g + 8 * h;
-        const float r = rr[i];
-        float dot = 0.f;
-        if (l2) {
+            for (int h = 0; h < 2; ++h) {
+                const int i = r0 + g + 8 * h;
+                const float r = rr[i];
+                float dot = 0.f;
+                if (l2) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float2 u = __half22float2(
-                    *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
-                dot = fmaf(u.x, tot[nt][2 * h], fmaf(u.y, tot[nt][2 * h + 1], dot));
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 u = __half22float2(
+                            *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
+                        dot = fmaf(u.x, tot[nt][2 * h], fmaf(u.y, tot[nt][2 * h + 1], dot));
+                    }
+                    dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+                }
+                dot *= f[i] * f[i];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x0 = tot[nt][2 * h], x1 = tot[nt][2 * h + 1];
+                    if (l2) {
+                        const float2 u = __half22float2(
+                            *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
+                        x0 -= u.x * dot, x1 -= u.y * dot;
+                    }
+                    if (i < n)
+                        *reinterpret_cast<uint32_t*>(dst + (me.kh * N + t0 + i) * D + 8 * nt + 2 * tq) =
+                            sm100::pack_bf16x2(r * mul * x0, r * mul * x1);
+                }
             }
-            dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-            dot += __shfl_xor_sync(0xffffffffu, dot, 2);
         }
-        dot *= f[i] * f[i];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x0 = tot[nt][2 * h], x1 = tot[nt][2 * h + 1];
-            if (l2) {
-                const float2 u = __half22float2(
-                    *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
-                x0 -= u.x * dot, x1 -= u.y * dot;
-            }
-            if (i < n)
-                *reinterpret_cast<uint32_t*>(dst + (kh * N + t0 + i) * D + 8 * nt + 2 * tq) =
-                    sm100::pack_bf16x2(r * mul * x0, r * mul * x1);
-        }
+        sm100::fence_proxy_async_smem();
+        ok = __syncthreads_and(ok);
+        if (!ok)
+            break;
+        if (tid == 0 && p == per - 1 && s + 1 < steps)
+            load_rows(s + 1);
+    }
+    if (!ok && tid == 0) {  // a copy never arrived: give the others their time, report, leave
+        for (int i = 0; i < 4; ++i)
+            for (int parity = 0; parity < 2; ++parity)
+                sm100::mbar_wait(full + i, parity, kWaitPolls >> 3);
+        set_status(status, LA_ERR_TIMEOUT);
     }
 }
 
@@ -1947,9 +2000,12 @@ cudaError_t run_backward(const DeltaArgs& a)
                         : launch_rev<D, 1>(a, rev.W, rows, blobs, n, kept);
     if (e != cudaSuccess)
         return e;
-    k_delta_dqk<D, DV><<<(unsigned)(a.B * a.Hk * n), kDqkThreads, DqkSmem<D, DV>::bytes, a.stream>>>(
+    const int64_t items = a.B * a.Hk * n;
+    const int sms = device_sm_count() > 0 ? device_sm_count() : 1;
+    k_delta_dqk<D, DV><<<(unsigned)(items < sms ? items : sms), kDqkThreads, DqkSmem<D, DV>::bytes, a.stream>>>(
         ws + l.rows, ws + l.blobs, dout, kept, static_cast<__nv_bfloat16*>(a.dq),
-        static_cast<__nv_bfloat16*>(a.dk), a.dbeta, a.dlog_alpha, a.N, n, H, Hk, l2, a.scale, a.status);
+        static_cast<__nv_bfloat16*>(a.dk), a.dbeta, a.dlog_alpha, a.N, n, (int)items, H, Hk, l2, a.scale,
+        a.status);
     count_launches(1);
     return cudaGetLastError();
 }

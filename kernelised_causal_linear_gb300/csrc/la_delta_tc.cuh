@@ -151,6 +151,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// 2^x on the hardware (2 ulp, denormals to zero)
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ float max_abs(float m, float x) { return fmaxf(m, fabsf(x)); }
 
 // largest over the four lanes of a fragment row

@@ -473,3 +473,11 @@ def test_many_heads(B, H, Hk, N, d, dv):
     p = problem(B, H, Hk, N, d, dv, BF, B + d)
     check_forward(p)
     check_backward(p)
+
+
+@pytest.mark.parametrize("B,H,Hk,N,d,dv", [(3, 8, 2, 900, 64, 64), (2, 6, 6, 1100, 128, 32),
+                                           (4, 12, 2, 333, 32, 128)])
+def test_backward_more_chunks_than_sms(B, H, Hk, N, d, dv):
+    """Each CTA of the dQ, dK kernel takes several chunks, and several value heads
+    of each."""
+    check_backward(problem(B, H, Hk, N, d, dv, BF, N + dv))
