@@ -1397,13 +1397,13 @@ __global__ void __launch_bounds__(128, 1)
 //   dK_j = sum_{i>=j} D_ij (dO_i.U_j) q_i - sum_{i>j} D_ij (dV_i.U_j) k_i
 //          - sum_{i<j} D_ji (dV_j.U_i) k_i - e^{G_j} S0 dV_j + e^{G_C-G_j} dS1 U_j
 //
-// then through scale and norm to the inputs.  Warps 0-3 own 16 tokens of dQ
-// each, warps 4-7 of dK.  The kept planes arrive with a scale per value column,
+// then through scale and norm to the inputs.  Two warps own 16 tokens of dQ or
+// of dK, each half of the d columns and of the token tiles.  The kept planes arrive with a scale per value column,
 // the contracted index here; they are brought under one scale each in shared
 // memory (a power of two: exact but for columns under 2^-24 of the largest), so
 // that fragments go from ldmatrix into the MMA as they are and every factor is
 // one of a row, applied to fp32 accumulators.  The 64 x 64 matrices pass through a
-// tile of the warp's own as fp16 rows under a power of two each.  One fp16 part
+// tile of the two warps' own as fp16 rows, each half under a power of two.  One fp16 part
 // throughout (2^-12 of a term, under the results' own rounding to bf16).
 // Loops over fragments stay rolled: unrolled, the two roles' code overran the
 // instruction cache and its misses were half of all stalls.
@@ -1412,7 +1412,7 @@ __global__ void __launch_bounds__(128, 1)
 // of one chunk) ahead: the token planes have two buffers; the state planes are used
 // first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
 // waiting for its own 150 KB: 508 against 330 us at B4 H8 N8192 d=128.)
-constexpr int kDqkThreads = 256;
+constexpr int kDqkThreads = 512;
 
 template <int D, int DV>
 struct DqkSmem {
@@ -1420,7 +1420,7 @@ struct DqkSmem {
     static constexpr int E = 0, dV = kC * DV * 2, dO = 2 * kC * DV * 2, fac = 3 * kC * DV * 2,
                          cols = fac + kGradFactors * kC * 4, step = cols + 6 * DV * 4;
     static constexpr int S = 2 * step, dS = S + D * DV * 2, K = dS + D * DV * 2, Q = K + row_image<D>(),
-                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + 3 * kC * 4,
+                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + (3 * kC + 8 * 32) * 4,
                          bytes = bar + 64;
     static_assert(bytes <= 232448, "shared memory");
 };
@@ -1468,17 +1468,20 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = DqkSmem<D, DV>;
-    constexpr int RB = 2 * D, VB = 2 * DV, NT = D / 8, KS = DV / 16;
+    constexpr int RB = 2 * D, VB = 2 * DV, NT = D / 16, KS = DV / 16;  // NT: n tiles of half a row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     const uint32_t base = smem_addr(smem);
     float* sdo = reinterpret_cast<float*>(smem + SM::vec);  // dO's row scales
     float* eg = sdo + kC;                                   // e^G
     float* ege = eg + kC;                                   // e^{G_C - G}
+    float* prow = ege + kC + (warp >> 1) * 32;              // [half][16 rows], the two warps' own
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bar);  // token planes (2), states, row images
     const int per = H / Hk;
-    const bool role_k = warp >= 4;
-    const int rt = warp & 3, r0 = 16 * rt;
-    const uint32_t mytile = base + SM::tile + warp * 16 * 128;
+    const bool role_k = warp >= 8;
+    const int pr = warp >> 1, h = warp & 1, rt = pr & 3, r0 = 16 * rt;
+    const int dg = h * (D / 32);  // first 16-column group
+    const uint32_t mytile = base + SM::tile + pr * 16 * 128;
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + pr) : "memory"); };
     const int steps = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * per;
 
     if (tid == 0) {
@@ -1577,9 +1580,11 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 h.x = h2(f[0] * q.to, f[1] * q.to), h.y = h2(f[2] * q.to, f[3] * q.to);
                 h.z = h2(f[4] * q.to, f[5] * q.to), h.w = h2(f[6] * q.to, f[7] * q.to);
                 __syncwarp();
-                *reinterpret_cast<uint4*>(smem + odO + tile_off<VB>(r, part)) = h;
-                if (part == 0)
-                    sdo[r] = q.from;
+                if (r < kC) {  // at DV = 32 half of the warps have no row
+                    *reinterpret_cast<uint4*>(smem + odO + tile_off<VB>(r, part)) = h;
+                    if (part == 0)
+                        sdo[r] = q.from;
+                }
             }
             if (tid < kC) {
                 eg[tid] = exp2f(gh[tid] + gl[tid]);
@@ -1612,26 +1617,23 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             }
         };
         // x[row][token] = this warp's rows of plane `a` dot the tokens of plane `b`,
-        // token tiles lo .. hi
-        auto dots = [&](float (&x)[8][4], int a_plane, int b_plane, int lo, int hi) {
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[nt][e] = 0.f;
+        // its token tiles h and h + 2 of lo .. hi
+        auto dots = [&](float (&x)[4][4], int a_plane, int b_plane, int lo, int hi) {
+            clear(x);
 #pragma unroll 2
             for (int ks = 0; ks < KS; ++ks) {
                 uint32_t a[4], b[4];
                 a_rows(a, a_plane, ks);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int u = 0; u < 2; ++u) {
+                    const int j = h + 2 * u;
                     if (j >= lo && j <= hi) {
                         if (b_plane == odO)
                             ldsm4(b, addr_b<VB>(base + odO, lane, 16 * j, 16 * ks));
                         else
                             ldsm4t(b, base + b_plane + (ks * 4 + j) * 512 + lane * 16);
-                        mma(x[2 * j], a, b[0], b[1]);
-                        mma(x[2 * j + 1], a, b[2], b[3]);
+                        mma(x[2 * u], a, b[0], b[1]);
+                        mma(x[2 * u + 1], a, b[2], b[3]);
                     }
                 }
             }
@@ -1646,60 +1648,62 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         // tot += (fa, fb) o this warp's rows of plane `a` times a kept state plane
         auto state = [&](int a_plane, int b_plane, float fa, float fb) {
             float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[nt][e] = 0.f;
-#pragma unroll 1
+            clear(acc);
+#pragma unroll 2
             for (int ks = 0; ks < KS; ++ks) {
                 uint32_t a[4], b[4];
                 a_rows(a, a_plane, ks);
 #pragma unroll
                 for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, base + b_plane + (ks * (D / 16) + j) * 512 + lane * 16);
+                    ldsm4t(b, base + b_plane + (ks * (D / 16) + dg + j) * 512 + lane * 16);
                     mma(acc[2 * j], a, b[0], b[1]);
                     mma(acc[2 * j + 1], a, b[2], b[3]);
                 }
             }
             add(acc, fa, fb);
         };
-        // tot += x (64 tokens, zero outside tiles lo .. hi) times a row image
-        auto rows_product = [&](const float (&x)[8][4], int image, int lo, int hi) {
+        // tot += x (64 tokens over the two warps, zero outside tiles lo .. hi) times a
+        // row image
+        auto rows_product = [&](const float (&x)[4][4], int image, int lo, int hi) {
             float ma = 0.f, mb = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
+            for (int nt = 0; nt < 4; ++nt) {
                 ma = max_abs(max_abs(ma, x[nt][0]), x[nt][1]);
                 mb = max_abs(max_abs(mb, x[nt][2]), x[nt][3]);
             }
             const Pow2 pa = pow2_for(quad_max(ma)), pb = pow2_for(quad_max(mb));
-            __syncwarp();
+            pair_sync();  // the tile is read
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g, nt) + 4 * tq) =
+            for (int nt = 0; nt < 4; ++nt) {
+                const int part = 2 * (h + (nt & 2)) + (nt & 1);  // 16-byte part of a row
+                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g, part) + 4 * tq) =
                     h2(x[nt][0] * pa.to, x[nt][1] * pa.to);
-                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g + 8, nt) + 4 * tq) =
+                *reinterpret_cast<uint32_t*>(smem + (mytile - base) + tile_off<128>(g + 8, part) + 4 * tq) =
                     h2(x[nt][2] * pb.to, x[nt][3] * pb.to);
             }
-            __syncwarp();
-            float acc[NT][4];
+            if (tq == 0)
+                prow[16 * h + g] = pa.from, prow[16 * h + g + 8] = pb.from;
+            pair_sync();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int half = 0; half < 2; ++half) {
+                float acc[NT][4];
+                clear(acc);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[nt][e] = 0.f;
-#pragma unroll 1
-            for (int kk = lo; kk <= hi; ++kk) {
-                uint32_t a[4], b[4];
-                ldsm4(a, addr_a<128>(mytile, lane, 0, 16 * kk));
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = half + 2 * u;
+                    if (kk >= lo && kk <= hi) {
+                        uint32_t a[4], b[4];
+                        ldsm4(a, addr_a<128>(mytile, lane, 0, 16 * kk));
 #pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    ldsm4t(b, addr_bt<RB>(base + image, lane, 16 * kk, 16 * j));
-                    mma(acc[2 * j], a, b[0], b[1]);
-                    mma(acc[2 * j + 1], a, b[2], b[3]);
+                        for (int j = 0; j < NT / 2; ++j) {
+                            ldsm4t(b, addr_bt<RB>(base + image, lane, 16 * kk, 16 * (dg + j)));
+                            mma(acc[2 * j], a, b[0], b[1]);
+                            mma(acc[2 * j + 1], a, b[2], b[3]);
+                        }
+                    }
                 }
+                add(acc, prow[16 * half + g], prow[16 * half + g + 8]);
             }
-            add(acc, pa.from, pb.from);
         };
         // the products with the states first: their planes are refilled meanwhile
         if (!role_k) {
@@ -1712,15 +1716,18 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         __syncthreads();
         if (tid == 0 && s + 1 < steps)
             load_states(s + 1);
-        if (p == 0)
-            ok = wait_warp(full + 3, (s / per) & 1);
-        if (ok && !role_k) {
-            float x[8][4];
+        if (p == 0) {
+            ok = __syncthreads_and(wait_warp(full + 3, (s / per) & 1));
+            if (!ok)
+                break;
+        }
+        if (!role_k) {
+            float x[4][4];
             dots(x, odO, oE, 0, rt);
             const float fa = mE * sdo[ia], fb = mE * sdo[ib];
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const int j0 = 8 * nt + 2 * tq;
+            for (int nt = 0; nt < 4; ++nt) {
+                const int j0 = 16 * (h + (nt & 2)) + 8 * (nt & 1) + 2 * tq;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = e >> 1 ? ib : ia, j = j0 + (e & 1);
@@ -1729,19 +1736,19 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 }
             }
             rows_product(x, SM::K, 0, rt);
-        } else if (ok) {
-            float x[8][4], y[8][4];
+        } else {
+            float x[4][4], y[4][4];
             {
-                float z[8][4];
+                float z[4][4];
                 const float fm = mE * mV;
                 dots(z, oE, odV, rt, 3);
                 dots(y, odV, oE, 0, rt);
                 dots(x, oE, odO, rt, 3);
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt)
+                for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = e >> 1 ? ib : ia, i = 8 * nt + 2 * tq + (e & 1);
+                        const int j = e >> 1 ? ib : ia, i = 16 * (h + (nt & 2)) + 8 * (nt & 1) + 2 * tq + (e & 1);
                         const float d = (gh[i] - gh[j]) + (gl[i] - gl[j]), dec = ex2(i >= j ? d : -d);
                         y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * fK[i])
                                    : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i])
@@ -1753,7 +1760,7 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             rows_product(x, SM::Q, rt, 3);
         }
         // the gates' gradients from the dots over 16 columns each
-        if (ok && warp == 0) {
+        if (warp == 0) {
             float z[2], after = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1788,47 +1795,55 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 }
             }
         }
-        if (ok && p == per - 1) {
+        if (p == per - 1) {
             // through scale and norm: unit = f image, dx = r (x - unit (unit.x))
             const int image = role_k ? SM::K : SM::Q;
             const float* f = fac + (role_k ? kFacK : kFacQ) * kC;
             const float* rr = fac + (role_k ? kFacRk : kFacRq) * kC;
             __nv_bfloat16* dst = role_k ? dk : dq;
             const float mul = role_k ? 1.0f : scale;
+            auto unit = [&](int i, int nt) {
+                return __half22float2(*reinterpret_cast<const __half2*>(
+                    smem + image + tile_off<RB>(i, 2 * dg + nt) + 4 * tq));
+            };
+            float dot[2] = {0.f, 0.f};
+            if (l2) {  // a row's dot over both warps' columns
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = r0 + g + 8 * h;
-                const float r = rr[i];
-                float dot = 0.f;
-                if (l2) {
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float2 u = __half22float2(
-                            *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
-                        dot = fmaf(u.x, tot[nt][2 * h], fmaf(u.y, tot[nt][2 * h + 1], dot));
+                        const float2 u = unit(r0 + g + 8 * e, nt);
+                        dot[e] = fmaf(u.x, tot[nt][2 * e], fmaf(u.y, tot[nt][2 * e + 1], dot[e]));
                     }
-                    dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+                    dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 1);
+                    dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], 2);
                 }
-                dot *= f[i] * f[i];
+                pair_sync();  // the products' factors are read
+                if (tq == 0)
+                    prow[16 * h + g] = dot[0], prow[16 * h + g + 8] = dot[1];
+                pair_sync();
+                dot[0] = prow[g] + prow[16 + g];
+                dot[1] = prow[8 + g] + prow[24 + g];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = r0 + g + 8 * e;
+                const float r = rr[i] * mul, d = dot[e] * f[i] * f[i];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float x0 = tot[nt][2 * h], x1 = tot[nt][2 * h + 1];
+                    float x0 = tot[nt][2 * e], x1 = tot[nt][2 * e + 1];
                     if (l2) {
-                        const float2 u = __half22float2(
-                            *reinterpret_cast<const __half2*>(smem + image + tile_off<RB>(i, nt) + 4 * tq));
-                        x0 -= u.x * dot, x1 -= u.y * dot;
+                        const float2 u = unit(i, nt);
+                        x0 -= u.x * d, x1 -= u.y * d;
                     }
                     if (i < n)
-                        *reinterpret_cast<uint32_t*>(dst + (me.kh * N + t0 + i) * D + 8 * nt + 2 * tq) =
-                            sm100::pack_bf16x2(r * mul * x0, r * mul * x1);
+                        *reinterpret_cast<uint32_t*>(dst + (me.kh * N + t0 + i) * D + 16 * dg + 8 * nt + 2 * tq) =
+                            sm100::pack_bf16x2(r * x0, r * x1);
                 }
             }
         }
         sm100::fence_proxy_async_smem();
-        ok = __syncthreads_and(ok);
-        if (!ok)
-            break;
+        __syncthreads();
         if (tid == 0 && p == per - 1 && s + 1 < steps)
             load_rows(s + 1);
     }
