@@ -421,20 +421,18 @@ __device__ __forceinline__ void keep_parts(unsigned char* p, int64_t plane, int6
     keep_part(p, 2 * plane + 1, part_bytes, block, lane, lo);
 }
 
-// Two tokens' sums over the warp's 16 columns (the lanes' g) -> row[t], row[t + 1]
-__device__ __forceinline__ void store_dot(float* row, int64_t t, int64_t N, int g, float y0, float y1)
+// Eight sums over the warp's 16 columns (the lanes' g): halves are traded so that
+// lane 4 g + t ends with the sum of y[g] over its t, seven shuffles instead of 24.
+__device__ __forceinline__ float sum8(const float (&y)[8], int lane)
 {
+    float a[4], b[2];
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        y0 += __shfl_xor_sync(0xffffffffu, y0, o);
-        y1 += __shfl_xor_sync(0xffffffffu, y1, o);
-    }
-    if (g == 0) {
-        if (t < N)
-            row[t] = y0;
-        if (t + 1 < N)
-            row[t + 1] = y1;
-    }
+    for (int i = 0; i < 4; ++i)
+        a[i] = (lane & 16 ? y[i + 4] : y[i]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? y[i] : y[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = (lane & 8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? a[i] : a[i + 2], 8);
+    return (lane & 4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? b[0] : b[1], 4);
 }
 
 // One warp's place in a slice shared by SP warps.  Token tiles (16 tokens) are
@@ -455,6 +453,16 @@ struct Share {
             asm volatile("bar.sync %0, %1;" ::"r"(1 + slice), "r"(32 * SP) : "memory");
         else
             __syncwarp();
+    }
+    // y[tile][C tile][token of a pair], local tiles 2 part and 2 part + 1, summed over
+    // the columns -> row[first token of the chunk + ..]
+    __device__ __forceinline__ void store_sums(float* row, const float (&y)[8], int part, int64_t t0, int64_t N) const
+    {
+        const float x = sum8(y, lane);
+        const int g = lane >> 2;
+        const int64_t t = t0 + 16 * tile(2 * part + (g >> 2)) + 8 * ((g >> 1) & 1) + 2 * (lane & 3) + (g & 1);
+        if (t < N)
+            row[t] = x;
     }
     // two token tiles (C layout) to buffer b, and the partner's from it
     __device__ __forceinline__ void put(int b, const float (&x)[2][4], const float (&y)[2][4]) const
@@ -806,6 +814,7 @@ __global__ void __launch_bounds__(256, 1)
                 cp_wait<1>();  // dO
                 __syncwarp();
             }
+            float dots[OWN / 2][8];
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 uint32_t w[4];
@@ -820,10 +829,8 @@ __global__ void __launch_bounds__(256, 1)
                     o[nt][2] = fmaf(fp.x * q1.from, x[nt][2], o[nt][2]);
                     o[nt][3] = fmaf(fp.y * q1.from, x[nt][3], o[nt][3]);
                     if (GRAD) {
-                        store_dot(kept.oo + (bh * (DV / 16) + col0 / 16) * N,
-                                  (int64_t)c * kC + 16 * sh.tile(i) + 8 * u + 2 * tq, N, g,
-                                  o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]),
-                                  o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]));
+                        dots[nt >> 2][2 * (nt & 3)] = o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]);
+                        dots[nt >> 2][2 * (nt & 3) + 1] = o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]);
                     } else {
                         w[2 * u] = sm100::pack_bf16x2(o[nt][0], o[nt][1]);
                         w[2 * u + 1] = sm100::pack_bf16x2(o[nt][2], o[nt][3]);
@@ -831,6 +838,11 @@ __global__ void __launch_bounds__(256, 1)
                 }
                 if (!GRAD)
                     stsm4t(addr_ct<32>(so, lane, 16 * sh.tile(i), 0), w);
+            }
+            if (GRAD) {
+#pragma unroll
+                for (int part = 0; part < OWN / 2; ++part)
+                    sh.store_sums(kept.oo + (bh * (DV / 16) + col0 / 16) * N, dots[part], part, (int64_t)c * kC, N);
             }
         }
         if (!GRAD)
@@ -934,15 +946,15 @@ template <int D, int SP>
 struct RevSmem {
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<true>();
     static constexpr int slice0 = kStages * stage;
-    // per slice: dO twice, V (then dV), E hi and lo, S hi and lo, three exchange
-    // buffers for each of two warps
-    static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, s = e + 2 * kC * 32, x = s + 2 * D * 32,
+    // per slice: dO twice, V (then dV), E hi and lo, three exchange buffers for each
+    // of two warps
+    static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, x = e + 2 * kC * 32,
                          per_slice = x + (SP > 1 ? SP * 3 * kXch : 0);
     static int bytes(int W) { return slice0 + W * per_slice + 64; }
 };
 
 template <int D, int SP>
-__global__ void __launch_bounds__(128, 1)
+__global__ void __launch_bounds__(256, 1)
     k_delta_rev(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
                 const float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dv,
@@ -1004,28 +1016,28 @@ __global__ void __launch_bounds__(128, 1)
                          (slice * 4 + sh.tile(i)) * 512 + lane * 16,
                      true);
     };
-    auto load_S = [&](int64_t c) {  // the own rows' blocks
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                cp16(base + mine + SM::s + part * D * 32 + (d0 / 16 + kk) * 512 + lane * 16,
-                     kept.S + (2 * (bh * (nchunk + 1) + c) + part) * (int64_t)(D * DV * 2) +
-                         (slice * (D / 16) + d0 / 16 + kk) * 512 + lane * 16,
-                     true);
-    };
     float ds[NT][4];  // dS^T[col0 + g, + 8][d0 + 8 nt + 2 tq, + 1]
-    // <S of chunk c, dS> over the warp's part -> kept.cd of the chunk before
-    auto dot_state = [&](int64_t c) {
-        const uint32_t* hi = reinterpret_cast<const uint32_t*>(smem + mine + SM::s) + (d0 / 16) * 128 + lane;
-        const uint32_t* lo = hi + D * 8;
-        const float* sc = kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0;
+    // <S of chunk c, dS> over the warp's part -> kept.cd of the chunk before.  S is
+    // read where it lies (128 bytes per load; asked into L2 at the chunk's start):
+    // staging it took the shared memory of half of the slices
+    auto state_at = [&](int64_t c, int part) {
+        return kept.S + (2 * (bh * (nchunk + 1) + c) + part) * (int64_t)(D * DV * 2) +
+               (slice * (D / 16) + d0 / 16) * 512;
+    };
+    auto ask_state = [&](int64_t c) {
+#pragma unroll
+        for (int i = lane; i < 2 * KK * 4; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(state_at(c, i / (KK * 4)) + i % (KK * 4) * 128));
+    };
+    auto dot_state = [&](int64_t c, float sc0, float sc1) {
+        const uint32_t* hi = reinterpret_cast<const uint32_t*>(state_at(c, 0)) + lane;
+        const uint32_t* lo = reinterpret_cast<const uint32_t*>(state_at(c, 1)) + lane;
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // register i: row g + 8 (i & 1), tile 2 kk + (i >> 1)
-                const uint32_t x = hi[(kk * 4 + i) * 32], y = lo[(kk * 4 + i) * 32];
+                const uint32_t x = __ldg(hi + (kk * 4 + i) * 32), y = __ldg(lo + (kk * 4 + i) * 32);
                 const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x));
                 const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&y));
                 const float* d = ds[2 * kk + (i >> 1)] + 2 * (i & 1);
@@ -1033,7 +1045,7 @@ __global__ void __launch_bounds__(128, 1)
                 a = fmaf(h.x + l.x, d[0], fmaf(h.y + l.y, d[1], a));
             }
         }
-        float x = a0 * sc[g] + a1 * sc[g + 8];
+        float x = a0 * sc0 + a1 * sc1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -1044,13 +1056,14 @@ __global__ void __launch_bounds__(128, 1)
                 cd[nchunk] = 0.f;
         }
     };
+    auto state_scale = [&](int64_t c, int row) {
+        return __ldg(kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0 + row);
+    };
 
     if (tid == 0)
         for (int i = 0; i < kStages && i < nchunk; ++i)
             load_stage(i);
     load_cols(sdo + ((nchunk - 1) & 1) * kC * 32, dout, nchunk - 1);
-    if (gated)
-        load_S(nchunk);
     cp_commit();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1061,7 +1074,7 @@ __global__ void __launch_bounds__(128, 1)
     cp_wait<0>();
     __syncwarp();
     if (gated)
-        dot_state(nchunk);
+        dot_state(nchunk, state_scale(nchunk, g), state_scale(nchunk, g + 8));
 
     bool ok = sm100::mbar_wait(full, 0, kWaitPolls);
     ok = __syncthreads_and(ok);
@@ -1076,8 +1089,11 @@ __global__ void __launch_bounds__(128, 1)
         // this chunk's V, E and S, wanted from the middle on, and the next dO
         load_cols(sv, v, c);
         load_E(c);
-        if (gated && c > 0)
-            load_S(c);
+        float sc0 = 0.f, sc1 = 0.f;
+        if (gated && c > 0) {
+            ask_state(c);
+            sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
+        }
         if (c > 0)
             load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
         cp_commit();
@@ -1215,6 +1231,7 @@ __global__ void __launch_bounds__(128, 1)
         cp_wait<0>();
         __syncwarp();
         // Y, the dots, dV on the own tiles
+        float bsum[OWN / 2][8], vsum[OWN / 2][8];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             uint32_t w[4];
@@ -1234,16 +1251,19 @@ __global__ void __launch_bounds__(128, 1)
                 const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
                 const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
                 const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
-                const int64_t t = (int64_t)c * kC + 16 * sh.tile(i) + 8 * h + 2 * tq;
-                store_dot(kept.bb + (bh * (DV / 16) + slice) * N, t, N, g,
-                          u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x)),
-                          u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y)));
+                const int part = nt >> 2, k = 2 * (nt & 3);
+                bsum[part][k] = u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x));
+                bsum[part][k + 1] = u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y));
                 u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
-                if (gated)
-                    store_dot(kept.vv + (bh * (DV / 16) + slice) * N, t, N, g,
-                              u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]),
-                              u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]));
+                vsum[part][k] = u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]);
+                vsum[part][k + 1] = u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]);
             }
+        }
+#pragma unroll
+        for (int part = 0; part < OWN / 2; ++part) {
+            sh.store_sums(kept.bb + (bh * (DV / 16) + slice) * N, bsum[part], part, (int64_t)c * kC, N);
+            if (gated)
+                sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
         }
         if (SP > 1) {
             sh.put(2, pair(u, 0), pair(u, 1));
@@ -1364,7 +1384,7 @@ __global__ void __launch_bounds__(128, 1)
             ds[nt][2] *= r1.from, ds[nt][3] *= r1.from;
         }
         if (gated && c > 0)
-            dot_state(c);
+            dot_state(c, sc0, sc1);
         if (it + 1 < nchunk)
             ok = sm100::mbar_wait(full + (it + 1) % kStages, ((it + 1) / kStages) & 1, kWaitPolls);
         ok = __syncthreads_and(ok);
@@ -1906,17 +1926,19 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
 
 // How a chain kernel is cut.  SP = 2 (two warps per slice) while that gives no
 // more warps than the GPU has sub-partitions to give each a tensor core of its own;
-// slices per CTA: as few as give no more CTAs than SMs, at most `cap`.
+// slices per CTA: as few as give no more CTAs than SMs, at most 8 warps.  Measured at
+// d = 128: 32 heads of 8192 tokens 468 us with one warp per slice, 304 us with two;
+// 512 heads of 2011 tokens 736 us with one, 886 us with two.
 struct Cut {
     int SP, W;
 };
-Cut cut_of(const DeltaArgs& a, int cap1, int cap2)
+Cut cut_of(const DeltaArgs& a)
 {
     const int sms = device_sm_count();
     const int64_t slices = a.B * a.H * (a.dv / 16);
     Cut c;
     c.SP = 2 * slices <= 4 * (int64_t)sms ? 2 : 1;
-    const int cap = c.SP == 2 ? cap2 : cap1;
+    const int cap = 8 / c.SP;
     c.W = 1;
     while (2 * c.W <= cap && 2 * c.W <= a.dv / 16 && slices / c.W > sms)
         c.W *= 2;
@@ -1979,7 +2001,7 @@ cudaError_t run_forward(const DeltaArgs& a)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    const Cut cut = cut_of(a, 8, 4);
+    const Cut cut = cut_of(a);
     return cut.SP == 2 ? launch_chain<D, false, 2>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{})
                        : launch_chain<D, false, 1>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{});
 }
@@ -2006,13 +2028,13 @@ cudaError_t run_backward(const DeltaArgs& a)
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const Cut cut = cut_of(a, 8, 4), rev = cut_of(a, 4, 2);
+    const Cut cut = cut_of(a);
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
     e = cut.SP == 2 ? launch_chain<D, true, 2>(a, cut.W, rows, blobs, n, kept)
                     : launch_chain<D, true, 1>(a, cut.W, rows, blobs, n, kept);
     if (e == cudaSuccess)
-        e = rev.SP == 2 ? launch_rev<D, 2>(a, rev.W, rows, blobs, n, kept)
-                        : launch_rev<D, 1>(a, rev.W, rows, blobs, n, kept);
+        e = cut.SP == 2 ? launch_rev<D, 2>(a, cut.W, rows, blobs, n, kept)
+                        : launch_rev<D, 1>(a, cut.W, rows, blobs, n, kept);
     if (e != cudaSuccess)
         return e;
     const int64_t items = a.B * a.Hk * n;
