@@ -76,21 +76,25 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 }
 
 // ------------------------------------------------------------- k_delta_prep --
-// 4 warps.  The Gram products are exact fp16 MMAs on the lower blocks; F is
-// fp32 on the CUDA cores in 16 x 16 blocks: the diagonal ones by substitution
-// (a column per lane), then by distance from the diagonal, all threads on each,
-//   X = A_IJ + sum_{J <= L < I} A_IL beta_L F_LJ,   F_IJ = -X - F_II beta_I X.
+// 4 warps, a row block of 16 tokens each.  The Gram products are exact fp16 MMAs on
+// the lower blocks and stay in the warp's registers as A and P.  F in 16 x 16 blocks:
+// the diagonal ones by fp32 substitution (a column per lane), then by distance from
+// the diagonal
+//   X = A_IJ + sum_{J <= L < I} (A beta)_IL F_LJ,   F_IJ = -X - F_II beta X
+// as MMAs on two-part operands: (A beta)_IL are warp I's own accumulators, F_LJ the
+// image it is writing.  All of F is under one power of two per chunk (with 2^11 to
+// spare over the largest |A|; a stable recurrence does not grow that far).  Decays of
+// off-diagonal blocks are a row's factor to the column block's end times a column's
+// from there, both at most 1, so only diagonal blocks take an exponential per element.
+// Issue-bound; on the CUDA cores the off-diagonal blocks alone were a quarter of it.
 constexpr int kPrepThreads = 128;
-constexpr int kLd = 68;  // row stride of the fp32 tiles (16-byte rows, spread over banks)
 
 template <int D, bool GRAD>
 struct PrepSmem {
     static constexpr int img = 2 * row_image<D>() > fac_at<GRAD>() ? 2 * row_image<D>() : fac_at<GRAD>();
-    static constexpr int A = img;
-    static constexpr int F = A + kC * kLd * 4;
-    static constexpr int X = F + kC * kLd * 4;
-    static constexpr int vec = X + 3 * 16 * 20 * 4;
-    static constexpr int bytes = vec + (8 + n_factors<GRAD>()) * kC * 4;
+    static constexpr int diag = img;                     // [4][16][20] fp32
+    static constexpr int vec = diag + 4 * 16 * 20 * 4;
+    static constexpr int bytes = vec + (10 + n_factors<GRAD>()) * kC * 4 + 64;
 };
 
 template <int D, bool GRAD>
@@ -103,12 +107,12 @@ __global__ void __launch_bounds__(kPrepThreads)
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = PrepSmem<D, GRAD>;
     constexpr int RB = 2 * D;  // bytes per row
-    float* sA = reinterpret_cast<float*>(smem + SM::A);
-    float* sF = reinterpret_cast<float*>(smem + SM::F);
     float* vec = reinterpret_cast<float*>(smem + SM::vec);
     float *fk = vec, *fq = vec + kC, *gh = vec + 2 * kC, *gl = vec + 3 * kC, *sb = vec + 4 * kC;
     float *rk = vec + 5 * kC, *rq = vec + 6 * kC, *uq = vec + 7 * kC;
-    float* fac = vec + 8 * kC;  // [factors][kC]
+    float* ck = vec + 8 * kC;   // fk_j times the decay from j to its block's end
+    float* top = vec + 9 * kC;  // [4] largest |A|, [4] largest |A beta| of the warps
+    float* fac = vec + 10 * kC;  // [factors][kC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / nchunk;
@@ -119,28 +123,32 @@ __global__ void __launch_bounds__(kPrepThreads)
     const int n = (int)min((int64_t)kC, N - t0);
     const uint32_t sK = smem_addr(smem), sQ = sK + row_image<D>();
 
-    // rows: scaled fp16 images and factors
-    constexpr int LPR = D / 8, RPP = kPrepThreads / LPR;
-#pragma unroll 4
+    // rows: scaled fp16 images and factors; 16 elements per thread
+    constexpr int LPR = D / 16, RPP = kPrepThreads / LPR;
+#pragma unroll
     for (int r0 = 0; r0 < kC; r0 += RPP) {
         const int r = r0 + tid / LPR, p = tid % LPR;
+        if (RPP > kC && r >= kC)
+            break;  // whole warps
+        uint4 w[2][2];
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const __nv_bfloat16* src = which ? q : k;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < n && src)
-                w = *reinterpret_cast<const uint4*>(src + (kh * N + t0 + r) * D + p * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float f[8], ss = 0.f, mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(u[i] << 16);
-                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
+            for (int h = 0; h < 2; ++h)
+                w[which][h] = r < n && src ? *reinterpret_cast<const uint4*>(src + (kh * N + t0 + r) * D + (2 * p + h) * 8)
+                                           : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint32_t u[8] = {w[which][0].x, w[which][0].y, w[which][0].z, w[which][0].w,
+                                   w[which][1].x, w[which][1].y, w[which][1].z, w[which][1].w};
+            float ss = 0.f, mx = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                ss = fmaf(f[i], f[i], ss);
-                mx = max_abs(mx, f[i]);
+                const float a = __uint_as_float(u[i] << 16), b = __uint_as_float(u[i] & 0xffff0000u);
+                ss = fmaf(a, a, fmaf(b, b, ss));
+                mx = max_abs(max_abs(mx, a), b);
             }
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) {
@@ -148,12 +156,16 @@ __global__ void __launch_bounds__(kPrepThreads)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             }
             const Pow2 s = pow2_for(mx);
-            uint4 h;
-            h.x = h2(f[0] * s.to, f[1] * s.to);
-            h.y = h2(f[2] * s.to, f[3] * s.to);
-            h.z = h2(f[4] * s.to, f[5] * s.to);
-            h.w = h2(f[6] * s.to, f[7] * s.to);
-            *reinterpret_cast<uint4*>(smem + (which ? row_image<D>() : 0) + tile_off<RB>(r, p)) = h;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = h2(__uint_as_float(u[4 * h + i] << 16) * s.to,
+                              __uint_as_float(u[4 * h + i] & 0xffff0000u) * s.to);
+                *reinterpret_cast<uint4*>(smem + (which ? row_image<D>() : 0) + tile_off<RB>(r, 2 * p + h)) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
+            }
             if (p == 0) {
                 const float norm = l2 ? rsqrtf(ss + kL2Eps) : 1.0f;
                 (which ? rq : rk)[r] = norm;
@@ -219,22 +231,62 @@ __global__ void __launch_bounds__(kPrepThreads)
     // the images go out; one value head of a key head writes them
     if ((bh % H) % per == 0) {
         uint4* dst = reinterpret_cast<uint4*>(rows + (kh * nchunk + c) * (int64_t)(2 * row_image<D>()));
+#pragma unroll 4
         for (int i = tid; i < 2 * row_image<D>() / 16; i += kPrepThreads)
             dst[i] = reinterpret_cast<const uint4*>(smem)[i];
     }
+    if (tid < kC) {
+        const float h = gh[tid], l = gl[tid], hc = gh[kC - 1], lc = gl[kC - 1];
+        const float e = exp2f(h + l);
+        ck[tid] = fk[tid] * exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l));
+        fac[kFacA * kC + tid] = e * fk[tid];
+        fac[kFacB * kC + tid] = sb[tid];
+        fac[kFacO * kC + tid] = e * fq[tid];
+        fac[kFacW * kC + tid] = exp2f((hc - h) + (lc - l)) * fk[tid];
+        fac[kFacEnd * kC + tid] = exp2f(hc + lc);
+        if (GRAD) {
+            fac[kFacK * kC + tid] = fk[tid];
+            fac[kFacQ * kC + tid] = uq[tid];
+            fac[kFacRk * kC + tid] = rk[tid];
+            fac[kFacRq * kC + tid] = rq[tid];
+            fac[kFacGh * kC + tid] = h;
+            fac[kFacGl * kC + tid] = l;
+        }
+    }
     __syncthreads();  // the images are read: F and P take their place
 
+    // A and P, their largest entries; blocks right of the diagonal are never read
     const int i0 = 16 * warp + g;
-    float pm[2] = {0.f, 0.f};
+    float pm[2] = {0.f, 0.f}, am = 0.f, abm = 0.f;
+    const float fki[2] = {fk[i0], fk[i0 + 8]}, fqi[2] = {fq[i0], fq[i0 + 8]};
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
+    for (int b = 0; b < 4; ++b) {
+        if (b <= warp) {
+            float row[2];  // decay from block b's end to the row
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + (e >> 1) * 8, j = 8 * nt + 2 * tq + (e & 1);
-            const float dec = j <= i ? exp2f((gh[i] - gh[j]) + (gl[i] - gl[j])) : 0.f;
-            sA[i * kLd + j] = j < i ? ak[nt][e] * fk[i] * fk[j] * dec : 0.f;
-            aq[nt][e] = j <= i ? aq[nt][e] * fq[i] * fk[j] * dec * (GRAD ? 1.0f : sb[j]) : 0.f;
-            pm[e >> 1] = max_abs(pm[e >> 1], aq[nt][e]);
+            for (int r = 0; r < 2; ++r)
+                row[r] = exp2f((gh[i0 + 8 * r] - gh[16 * b + 15]) + (gl[i0 + 8 * r] - gl[16 * b + 15]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int nt = 2 * b + h, j = 8 * nt + 2 * tq;
+                const float2 col = *reinterpret_cast<const float2*>((b < warp ? ck : fk) + j);
+                const float2 be = *reinterpret_cast<const float2*>(sb + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + (e >> 1) * 8, jj = j + (e & 1);
+                    float dec = row[e >> 1];
+                    if (b == warp)
+                        dec = jj <= i ? exp2f((gh[i] - gh[jj]) + (gl[i] - gl[jj])) : 0.f;
+                    dec *= e & 1 ? col.y : col.x;
+                    const float bj = e & 1 ? be.y : be.x;
+                    // a select, not a product with 0: nothing to the right of the diagonal counts
+                    ak[nt][e] = b < warp || jj < i ? ak[nt][e] * fki[e >> 1] * dec : 0.f;
+                    aq[nt][e] = b < warp || jj <= i ? aq[nt][e] * fqi[e >> 1] * dec * (GRAD ? 1.0f : bj) : 0.f;
+                    pm[e >> 1] = max_abs(pm[e >> 1], aq[nt][e]);
+                    am = max_abs(am, ak[nt][e]);
+                    abm = max_abs(abm, ak[nt][e] * bj);
+                }
+            }
         }
     }
 #pragma unroll
@@ -245,114 +297,141 @@ __global__ void __launch_bounds__(kPrepThreads)
             fac[kFacP * kC + i] = s.from;
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            uint32_t hi, lo;
-            h2_split(aq[nt][2 * r] * s.to, aq[nt][2 * r + 1] * s.to, hi, lo);
-            unsigned char* at = smem + 2 * kTile + tile_off<128>(i, nt) + 4 * tq;
-            *reinterpret_cast<uint32_t*>(at) = hi;
-            if (GRAD)
-                *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+            if (nt <= 2 * warp + 1) {
+                uint32_t hi, lo;
+                h2_split(aq[nt][2 * r] * s.to, aq[nt][2 * r + 1] * s.to, hi, lo);
+                unsigned char* at = smem + 2 * kTile + tile_off<128>(i, nt) + 4 * tq;
+                *reinterpret_cast<uint32_t*>(at) = hi;
+                if (GRAD)
+                    *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+            }
         }
     }
-    if (tid < kC) {
-        const float e = exp2f(gh[tid] + gl[tid]);
-        const float w = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
-        fac[kFacA * kC + tid] = e * fk[tid];
-        fac[kFacB * kC + tid] = sb[tid];
-        fac[kFacO * kC + tid] = e * fq[tid];
-        fac[kFacW * kC + tid] = w * fk[tid];
-        fac[kFacEnd * kC + tid] = exp2f(gh[kC - 1] + gl[kC - 1]);
-        if (GRAD) {
-            fac[kFacK * kC + tid] = fk[tid];
-            fac[kFacQ * kC + tid] = uq[tid];
-            fac[kFacRk * kC + tid] = rk[tid];
-            fac[kFacRq * kC + tid] = rq[tid];
-            fac[kFacGh * kC + tid] = gh[tid];
-            fac[kFacGl * kC + tid] = gl[tid];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        abm = fmaxf(abm, __shfl_xor_sync(0xffffffffu, abm, o));
+    }
+    if (lane == 0)
+        top[warp] = am, top[4 + warp] = abm;
+    // the diagonal block, for the substitution
+    float* sd = reinterpret_cast<float*>(smem + SM::diag) + warp * 16 * 20;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        if (b == warp) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<float2*>(sd + g * 20 + 8 * h + 2 * tq) = make_float2(ak[2 * b + h][0], ak[2 * b + h][1]);
+                *reinterpret_cast<float2*>(sd + (g + 8) * 20 + 8 * h + 2 * tq) =
+                    make_float2(ak[2 * b + h][2], ak[2 * b + h][3]);
+            }
         }
     }
     __syncthreads();
-
-    // F, diagonal blocks: column `lane & 15` of block `warp`
-    {
+    // F s for s = 2^4 / max |A| and (A beta) t, both powers of two
+    Pow2 s = pow2_for(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * 16.0f);
+    const Pow2 t = pow2_for(fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
+    if (tid < kC)
+        fac[kFacF * kC + tid] = s.from;
+    // one element of F's images, two of a row
+    auto put2 = [&](int i, int j, float x, float y) {
+        uint32_t hi, lo;
+        h2_split(x, y, hi, lo);
+        unsigned char* at = smem + tile_off<128>(i, j >> 3) + (j & 7) * 2;
+        *reinterpret_cast<uint32_t*>(at) = hi;
+        *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+    };
+    {  // diagonal: column `lane & 15` of block `warp`
         const int b = 16 * warp, j = lane & 15;
         float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float x = -sA[(b + i) * kLd + b + j];
+            float x = -sd[i * 20 + j];
 #pragma unroll
             for (int l = 0; l < i; ++l)
-                x = fmaf(-sA[(b + i) * kLd + b + l] * sb[b + l], f[l], x);
+                x = fmaf(-sd[i * 20 + l] * sb[b + l], f[l], x);
             f[i] = x;
         }
-        if (lane < 16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sF[(b + i) * kLd + b + j] = f[i];
+        for (int i = 0; i < 16; ++i) {  // even columns write their right neighbour's too
+            const float y = __shfl_down_sync(0xffffffffu, f[i], 1);
+            if (lane < 16 && (lane & 1) == 0)
+                put2(b + i, b + j, f[i] * s.to, y * s.to);
         }
     }
     __syncthreads();
-    // off-diagonal blocks, all threads on the 4 - dist blocks of a distance: thread
-    // -> row of a block and 2 (dist 1: 6, dist 2: 4) of its columns
-    float* sX = reinterpret_cast<float*>(smem + SM::X);  // [block][16][20]
+    // off-diagonal: at distance `dist` warp I computes block (I, I - dist)
+    const uint32_t sF = smem_addr(smem);
 #pragma unroll
     for (int dist = 1; dist < 4; ++dist) {
-        const int r = (tid >> 3) & 15, c0 = (tid & 7) * 2;
-        float x[3][2];
+        if (warp >= dist) {
+            const int J = warp - dist;
+            float x[2][4];
+            clear(x);
+            uint32_t hi[4], lo[4], b[4];
 #pragma unroll
-        for (int J = 0; J < 4 - dist; ++J) {
-            const float* arow = sA + (16 * (J + dist) + r) * kLd;
-            x[J][0] = arow[16 * J + c0], x[J][1] = arow[16 * J + c0 + 1];
-#pragma unroll 8
-            for (int l = 16 * J; l < 16 * (J + dist); ++l) {
-                const float a = arow[l] * sb[l];
-                const float2 f = *reinterpret_cast<const float2*>(sF + l * kLd + 16 * J + c0);
-                x[J][0] = fmaf(a, f.x, x[J][0]), x[J][1] = fmaf(a, f.y, x[J][1]);
+            for (int L = 0; L < 3; ++L) {
+                if (L >= J && L < warp) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 be = *reinterpret_cast<const float2*>(sb + 16 * L + 8 * h + 2 * tq);
+                        h2_split(ak[2 * L + h][0] * be.x * t.to, ak[2 * L + h][1] * be.y * t.to, hi[2 * h], lo[2 * h]);
+                        h2_split(ak[2 * L + h][2] * be.x * t.to, ak[2 * L + h][3] * be.y * t.to, hi[2 * h + 1],
+                                 lo[2 * h + 1]);
+                    }
+                    ldsm4t(b, addr_bt<128>(sF, lane, 16 * L, 16 * J));
+                    mma(x[0], hi, b[0], b[1]);
+                    mma(x[1], hi, b[2], b[3]);
+                    mma(x[0], lo, b[0], b[1]);
+                    mma(x[1], lo, b[2], b[3]);
+                    ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * L, 16 * J));
+                    mma(x[0], hi, b[0], b[1]);
+                    mma(x[1], hi, b[2], b[3]);
+                }
             }
-            *reinterpret_cast<float2*>(sX + (J * 16 + r) * 20 + c0) = make_float2(x[J][0], x[J][1]);
-        }
-        __syncthreads();
+            // X s, then beta X in F's place as the second product's operand
+            const float be0 = sb[i0], be1 = sb[i0 + 8];
 #pragma unroll
-        for (int J = 0; J < 4 - dist; ++J) {
-            const int I = J + dist;
-            const float* frow = sF + (16 * I + r) * kLd + 16 * I;
-            float y0 = -x[J][0], y1 = -x[J][1];
+            for (int L = 0; L < 3; ++L) {
+                if (L == J) {
 #pragma unroll
-            for (int l = 0; l < 16; ++l) {  // F_II is zero from its diagonal on
-                const float a = -frow[l] * sb[16 * I + l];
-                const float2 f = *reinterpret_cast<const float2*>(sX + (J * 16 + l) * 20 + c0);
-                y0 = fmaf(a, f.x, y0), y1 = fmaf(a, f.y, y1);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[h][e] = fmaf(ak[2 * L + h][e], s.to, x[h][e] * t.from);
+                }
             }
-            *reinterpret_cast<float2*>(sF + (16 * I + r) * kLd + 16 * J + c0) = make_float2(y0, y1);
+            const int j0 = 16 * J + 2 * tq;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                put2(i0, j0 + 8 * h, be0 * x[h][0], be0 * x[h][1]);
+                put2(i0 + 8, j0 + 8 * h, be1 * x[h][2], be1 * x[h][3]);
+            }
+            __syncwarp();
+            float y[2][4];
+            clear(y);
+            uint32_t bl[4];
+            ldsm4(hi, addr_a<128>(sF, lane, 16 * warp, 16 * warp));
+            ldsm4(lo, addr_a<128>(sF + kTile, lane, 16 * warp, 16 * warp));
+            ldsm4t(b, addr_bt<128>(sF, lane, 16 * warp, 16 * J));
+            ldsm4t(bl, addr_bt<128>(sF + kTile, lane, 16 * warp, 16 * J));
+            mma(y[0], hi, b[0], b[1]);
+            mma(y[1], hi, b[2], b[3]);
+            mma(y[0], lo, b[0], b[1]);
+            mma(y[1], lo, b[2], b[3]);
+            mma(y[0], hi, bl[0], bl[1]);
+            mma(y[1], hi, bl[2], bl[3]);
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                put2(i0, j0 + 8 * h, fmaf(-s.from, y[h][0], -x[h][0]), fmaf(-s.from, y[h][1], -x[h][1]));
+                put2(i0 + 8, j0 + 8 * h, fmaf(-s.from, y[h][2], -x[h][2]), fmaf(-s.from, y[h][3], -x[h][3]));
+            }
         }
         __syncthreads();
     }
-    // F to two fp16 parts, rows scaled; two threads per row
-    {
-        const int r = tid >> 1, half = (tid & 1) * 32;
-        float f[32], m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            f[i] = half + i < r ? sF[r * kLd + half + i] : 0.f;
-            m = max_abs(m, f[i]);
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const Pow2 s = pow2_for(m);
-        if (half == 0)
-            fac[kFacF * kC + r] = s.from;
-#pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            uint4 hi, lo;
-            h2_split(f[i] * s.to, f[i + 1] * s.to, hi.x, lo.x);
-            h2_split(f[i + 2] * s.to, f[i + 3] * s.to, hi.y, lo.y);
-            h2_split(f[i + 4] * s.to, f[i + 5] * s.to, hi.z, lo.z);
-            h2_split(f[i + 6] * s.to, f[i + 7] * s.to, hi.w, lo.w);
-            const uint32_t at = tile_off<128>(r, (half + i) >> 3);
-            *reinterpret_cast<uint4*>(smem + at) = hi;
-            *reinterpret_cast<uint4*>(smem + kTile + at) = lo;
-        }
-    }
-    __syncthreads();
     uint4* blob = reinterpret_cast<uint4*>(blobs + (bh * nchunk + c) * (int64_t)blob_bytes<GRAD>());
+#pragma unroll 4
     for (int i = tid; i < fac_at<GRAD>() / 16; i += kPrepThreads)
         blob[i] = reinterpret_cast<const uint4*>(smem)[i];
     for (int i = tid; i < n_factors<GRAD>() * kC / 4; i += kPrepThreads)
@@ -492,16 +571,6 @@ struct Share {
 __device__ __forceinline__ float2 fac2(const float* fac, int which, int t, int nt, int tq)
 {
     return *reinterpret_cast<const float2*>(fac + which * kC + 16 * t + 8 * nt + 2 * tq);
-}
-
-template <int N_>
-__device__ __forceinline__ void clear(float (&x)[N_][4])
-{
-#pragma unroll
-    for (int i = 0; i < N_; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            x[i][e] = 0.f;
 }
 
 // bf16 pair -> two fp32

@@ -161,6 +161,16 @@ __device__ __forceinline__ float ex2(float x)
 
 __device__ __forceinline__ float max_abs(float m, float x) { return fmaxf(m, fabsf(x)); }
 
+template <int N_>
+__device__ __forceinline__ void clear(float (&x)[N_][4])
+{
+#pragma unroll
+    for (int i = 0; i < N_; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[i][e] = 0.f;
+}
+
 // largest over the four lanes of a fragment row
 __device__ __forceinline__ float quad_max(float x)
 {
