@@ -573,6 +573,59 @@ __device__ __forceinline__ float2 fac2(const float* fac, int which, int t, int n
     return *reinterpret_cast<const float2*>(fac + which * kC + 16 * t + 8 * nt + 2 * tq);
 }
 
+// acc[2 i], acc[2 i + 1] += a b[i].  A product on two parts goes over all tiles with
+// the one, then with the other: MMAs on the same accumulator stay apart
+template <int N_>
+__device__ __forceinline__ void mma_tiles(float (*acc)[4], const uint32_t (&a)[4], const uint32_t (&b)[N_][4])
+{
+#pragma unroll
+    for (int i = 0; i < N_; ++i) {
+        mma(acc[2 * i], a, b[i][0], b[i][1]);
+        mma(acc[2 * i + 1], a, b[i][2], b[i][3]);
+    }
+}
+
+// x[tile i] += (hi + lo) (B hi + B lo) without lo lo, over the tiles that `want` names;
+// load(b, i, part) fetches B
+template <int N_, typename Want, typename Load>
+__device__ __forceinline__ void three_products(float (&x)[2 * N_][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                               Want want, Load load)
+{
+    uint32_t b[N_][4], c[N_][4];
+#pragma unroll
+    for (int i = 0; i < N_; ++i)
+        if (want(i))
+            load(b[i], i, 0), load(c[i], i, 1);
+    auto all = [&](const uint32_t(&a)[4], const uint32_t(&t)[N_][4]) {
+#pragma unroll
+        for (int i = 0; i < N_; ++i)
+            if (want(i)) {
+                mma(x[2 * i], a, t[i][0], t[i][1]);
+                mma(x[2 * i + 1], a, t[i][2], t[i][3]);
+            }
+    };
+    all(hi, b);
+    all(lo, b);
+    all(hi, c);
+}
+
+// s += (hi + lo) times rows row0 .. + 15 of an image, columns d0 .. + 16 KK
+template <int RB, int KK>
+__device__ __forceinline__ void rows_update(float (&s)[2 * KK][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                            uint32_t image, int lane, int row0, int d0)
+{
+    constexpr int G = KK < 4 ? KK : 4;
+#pragma unroll
+    for (int j = 0; j < KK; j += G) {
+        uint32_t b[G][4];
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            ldsm4t(b[i], addr_bt<RB>(image, lane, row0, d0 + 16 * (j + i)));
+        mma_tiles<G>(s + 2 * j, hi, b);
+        mma_tiles<G>(s + 2 * j, lo, b);
+    }
+}
+
 // bf16 pair -> two fp32
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -694,27 +747,28 @@ __global__ void __launch_bounds__(256, 1)
         clear(o);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            uint32_t hi[4], lo[4], b[4];
+            uint32_t hi[4], lo[4];
             split_state(kk, p0, p1, hi, lo);
             if (GRAD)
                 keep_parts(kept.S, bh * (nchunk + 1) + c, D * DV * 2,
                            (col0 / 16) * (D / 16) + d0 / 16 + kk, lane, hi, lo);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ldsm4(b, addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
-                mma(r[2 * j], hi, b[0], b[1]);
-                mma(r[2 * j + 1], hi, b[2], b[3]);
-                mma(r[2 * j], lo, b[0], b[1]);
-                mma(r[2 * j + 1], lo, b[2], b[3]);
+            for (int j = 0; j < 4; j += 2) {
+                uint32_t bk[2][4], bq[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    ldsm4(bk[i], addr_b<RB>(sK, lane, 16 * sh.tile(j + i), d0 + 16 * kk));
                 if (reads) {
-                    ldsm4(b, addr_b<RB>(sQ, lane, 16 * sh.tile(j), d0 + 16 * kk));
-                    mma(o[2 * j], hi, b[0], b[1]);
-                    mma(o[2 * j + 1], hi, b[2], b[3]);
-                    if (GRAD) {  // o enters an fp32 gradient
-                        mma(o[2 * j], lo, b[0], b[1]);
-                        mma(o[2 * j + 1], lo, b[2], b[3]);
-                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        ldsm4(bq[i], addr_b<RB>(sQ, lane, 16 * sh.tile(j + i), d0 + 16 * kk));
                 }
+                mma_tiles<2>(r + 2 * j, hi, bk);
+                if (reads)
+                    mma_tiles<2>(o + 2 * j, hi, bq);
+                mma_tiles<2>(r + 2 * j, lo, bk);
+                if (GRAD)  // o enters an fp32 gradient
+                    mma_tiles<2>(o + 2 * j, lo, bq);
             }
         }
         if (GRAD)
@@ -791,21 +845,14 @@ __global__ void __launch_bounds__(256, 1)
             const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                uint32_t hi[4], lo[4], b[4];
+                uint32_t hi[4], lo[4];
                 split8(z, kk, q0, q1, hi, lo);
-#pragma unroll
-                for (int i = 0; i < OWN; ++i) {
-                    if (sh.tile(kk) <= sh.tile(i)) {  // F is strictly lower
-                        ldsm4(b, addr_b<128>(sF, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
-                        mma(x[2 * i], hi, b[0], b[1]);
-                        mma(x[2 * i + 1], hi, b[2], b[3]);
-                        mma(x[2 * i], lo, b[0], b[1]);
-                        mma(x[2 * i + 1], lo, b[2], b[3]);
-                        ldsm4(b, addr_b<128>(sF + kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
-                        mma(x[2 * i], hi, b[0], b[1]);
-                        mma(x[2 * i + 1], hi, b[2], b[3]);
-                    }
-                }
+                // F is strictly lower
+                three_products<OWN>(
+                    x, hi, lo, [&](int i) { return sh.tile(kk) <= sh.tile(i); },
+                    [&](uint32_t(&b)[4], int i, int part) {
+                        ldsm4(b, addr_b<128>(sF + part * kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                    });
             }
 #pragma unroll
             for (int i = 0; i < 2 * OWN; ++i) {
@@ -863,16 +910,17 @@ __global__ void __launch_bounds__(256, 1)
             for (int kk = 0; kk < 4; ++kk) {
                 uint32_t hi[4], lo[4], b[4];
                 split8(r, kk, q0, q1, hi, lo);
+                if (GRAD) {
+                    three_products<OWN>(
+                        x, hi, lo, [&](int i) { return sh.tile(kk) <= sh.tile(i); },
+                        [&](uint32_t(&b)[4], int i, int part) {
+                            ldsm4(b, addr_b<128>(sP + part * kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                        });
+                } else {
 #pragma unroll
-                for (int i = 0; i < OWN; ++i) {
-                    if (sh.tile(kk) <= sh.tile(i)) {
-                        ldsm4(b, addr_b<128>(sP, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
-                        mma(x[2 * i], hi, b[0], b[1]);
-                        mma(x[2 * i + 1], hi, b[2], b[3]);
-                        if (GRAD) {
-                            mma(x[2 * i], lo, b[0], b[1]);
-                            mma(x[2 * i + 1], lo, b[2], b[3]);
-                            ldsm4(b, addr_b<128>(sP + kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                    for (int i = 0; i < OWN; ++i) {
+                        if (sh.tile(kk) <= sh.tile(i)) {
+                            ldsm4(b, addr_b<128>(sP, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
                             mma(x[2 * i], hi, b[0], b[1]);
                             mma(x[2 * i + 1], hi, b[2], b[3]);
                         }
@@ -930,7 +978,7 @@ __global__ void __launch_bounds__(256, 1)
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            uint32_t hi[4], lo[4], b[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * kk + u;
@@ -938,14 +986,7 @@ __global__ void __launch_bounds__(256, 1)
                 h2_split(w.x * r[nt][0] * u0.to, w.y * r[nt][1] * u0.to, hi[2 * u], lo[2 * u]);
                 h2_split(w.x * r[nt][2] * u1.to, w.y * r[nt][3] * u1.to, hi[2 * u + 1], lo[2 * u + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < KK; ++j) {
-                ldsm4t(b, addr_bt<RB>(sK, lane, 16 * sh.tile(kk), d0 + 16 * j));
-                mma(s[2 * j], hi, b[0], b[1]);
-                mma(s[2 * j + 1], hi, b[2], b[3]);
-                mma(s[2 * j], lo, b[0], b[1]);
-                mma(s[2 * j + 1], lo, b[2], b[3]);
-            }
+            rows_update<RB, KK>(s, hi, lo, sK, lane, 16 * sh.tile(kk), d0);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1186,20 +1227,17 @@ __global__ void __launch_bounds__(256, 1)
         clear(x);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            uint32_t hi[4], lo[4], b[4];
+            uint32_t hi[4], lo[4], b[4][4];
             h2_split(ds[2 * kk][0] * p0.to, ds[2 * kk][1] * p0.to, hi[0], lo[0]);
             h2_split(ds[2 * kk][2] * p1.to, ds[2 * kk][3] * p1.to, hi[1], lo[1]);
             h2_split(ds[2 * kk + 1][0] * p0.to, ds[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
             h2_split(ds[2 * kk + 1][2] * p1.to, ds[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
             keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + d0 / 16 + kk, lane, hi);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                ldsm4(b, addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
-                mma(u[2 * j], hi, b[0], b[1]);
-                mma(u[2 * j + 1], hi, b[2], b[3]);
-                mma(u[2 * j], lo, b[0], b[1]);
-                mma(u[2 * j + 1], lo, b[2], b[3]);
-            }
+            for (int j = 0; j < 4; ++j)
+                ldsm4(b[j], addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
+            mma_tiles<4>(u, hi, b);
+            mma_tiles<4>(u, lo, b);
         }
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
@@ -1273,7 +1311,7 @@ __global__ void __launch_bounds__(256, 1)
         clear(x);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            uint32_t hi[4], lo[4], b[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * kk + h;
@@ -1283,19 +1321,11 @@ __global__ void __launch_bounds__(256, 1)
                 h2_split(fx * u[nt][0] * y0.to, fy * u[nt][1] * y0.to, hi[2 * h], lo[2 * h]);
                 h2_split(fx * u[nt][2] * y1.to, fy * u[nt][3] * y1.to, hi[2 * h + 1], lo[2 * h + 1]);
             }
-#pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                if (sh.tile(i) <= sh.tile(kk)) {
-                    ldsm4t(b, addr_bt<128>(sF, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
-                    mma(x[2 * i], hi, b[0], b[1]);
-                    mma(x[2 * i + 1], hi, b[2], b[3]);
-                    mma(x[2 * i], lo, b[0], b[1]);
-                    mma(x[2 * i + 1], lo, b[2], b[3]);
-                    ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
-                    mma(x[2 * i], hi, b[0], b[1]);
-                    mma(x[2 * i + 1], hi, b[2], b[3]);
-                }
-            }
+            three_products<OWN>(
+                x, hi, lo, [&](int i) { return sh.tile(i) <= sh.tile(kk); },
+                [&](uint32_t(&b)[4], int i, int part) {
+                    ldsm4t(b, addr_bt<128>(sF + part * kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
+                });
         }
         cp_wait<0>();
         __syncwarp();
@@ -1415,7 +1445,7 @@ __global__ void __launch_bounds__(256, 1)
         }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            uint32_t w[4], hi[4], lo[4], b[4];
+            uint32_t w[4], hi[4], lo[4];
             ldsm4t(w, addr_ct<32>(tdo, lane, 16 * sh.tile(kk), 0));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1424,28 +1454,14 @@ __global__ void __launch_bounds__(256, 1)
                 h2_split(fo.x * lo_f(w[2 * h + 1]) * r1.to, fo.y * hi_f(w[2 * h + 1]) * r1.to, hi[2 * h + 1],
                          lo[2 * h + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < KK; ++j) {
-                ldsm4t(b, addr_bt<RB>(sQ, lane, 16 * sh.tile(kk), d0 + 16 * j));
-                mma(ds[2 * j], hi, b[0], b[1]);
-                mma(ds[2 * j + 1], hi, b[2], b[3]);
-                mma(ds[2 * j], lo, b[0], b[1]);
-                mma(ds[2 * j + 1], lo, b[2], b[3]);
-            }
+            rows_update<RB, KK>(ds, hi, lo, sQ, lane, 16 * sh.tile(kk), d0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * kk + h;
                 h2_split(u[nt][0] * r0.to, u[nt][1] * r0.to, hi[2 * h], lo[2 * h]);
                 h2_split(u[nt][2] * r1.to, u[nt][3] * r1.to, hi[2 * h + 1], lo[2 * h + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < KK; ++j) {
-                ldsm4t(b, addr_bt<RB>(sK, lane, 16 * sh.tile(kk), d0 + 16 * j));
-                mma(ds[2 * j], hi, b[0], b[1]);
-                mma(ds[2 * j + 1], hi, b[2], b[3]);
-                mma(ds[2 * j], lo, b[0], b[1]);
-                mma(ds[2 * j + 1], lo, b[2], b[3]);
-            }
+            rows_update<RB, KK>(ds, hi, lo, sK, lane, 16 * sh.tile(kk), d0);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
