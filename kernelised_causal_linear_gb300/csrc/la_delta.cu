@@ -25,7 +25,8 @@ using delta::kL2Eps;
 // 8 warps of 4 columns each; lane = 4 r + c holds rows 4 r .. 4 r + 3 of every
 // 32 for column c.  Tokens are staged in blocks of kRecTok, q and k already
 // normalised, so the step itself is D / 8 FMAs four times and three shuffles
-// of two values.  Bound by the latency of that chain, once per token.
+// of two values.  Bound by the latency of that chain, once per token; the next
+// block's rows are in flight (in registers) while a block's tokens run.
 constexpr int kRecThreads = 256;
 constexpr int kRecCols = 32;  // columns per CTA
 constexpr int kRecTok = 32;   // tokens per staged block
@@ -58,19 +59,40 @@ __global__ void __launch_bounds__(kRecThreads)
     for (int i = 0; i < D / 8; ++i)
         s[i] = S0 ? S0[(bh * D + (i / 4) * 32 + 4 * r + i % 4) * DV + c0 + col] : 0.0f;
 
+    // a warp stages rows warp, warp + 8, ..
+    constexpr int kRows = kRecTok / (kRecThreads / 32);
+    T nk[kRows][D / 32], nq[kRows][D / 32], nv[kRows];
+    float nb[kRows], na[kRows];
+    auto fetch = [&](int64_t b) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t t = b * kRecTok + warp + i * (kRecThreads / 32);
+            const bool live = t < N;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                nk[i][x] = live ? kp[t * D + lane + 32 * x] : from_f32<T>(0.f);
+                nq[i][x] = live && qp ? qp[t * D + lane + 32 * x] : from_f32<T>(0.f);
+            }
+            nv[i] = live ? vp[t * DV + lane] : from_f32<T>(0.f);
+            nb[i] = live ? beta[bh * N + t] : 0.f;
+            na[i] = live && log_alpha ? log_alpha[bh * N + t] : 0.f;
+        }
+    };
+    fetch(0);
     for (int64_t b = 0; b < nblk; ++b) {
         const int64_t t0 = b * kRecTok;
         const int n = (int)min((int64_t)kRecTok, N - t0);
         __syncthreads();  // the previous block's tiles are read
-        for (int t = warp; t < n; t += kRecThreads / 32) {
-            float kk[D / 32], qq[D / 32], k2 = 0.f, q2 = 0.f, kq = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                kk[i] = to_f32<T>(kp[(t0 + t) * D + lane + 32 * i]);
-                qq[i] = qp ? to_f32<T>(qp[(t0 + t) * D + lane + 32 * i]) : 0.f;
-                k2 = fmaf(kk[i], kk[i], k2);
-                q2 = fmaf(qq[i], qq[i], q2);
-                kq = fmaf(kk[i], qq[i], kq);
+        for (int i = 0; i < kRows; ++i) {
+            const int t = warp + i * (kRecThreads / 32);
+            float k2 = 0.f, q2 = 0.f, kq = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                const float kk = to_f32<T>(nk[i][x]), qq = to_f32<T>(nq[i][x]);
+                k2 = fmaf(kk, kk, k2);
+                q2 = fmaf(qq, qq, q2);
+                kq = fmaf(kk, qq, kq);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
@@ -81,26 +103,29 @@ __global__ void __launch_bounds__(kRecThreads)
             const float rk = l2 ? rsqrtf(k2 + kL2Eps) : 1.0f;
             const float rq = (l2 ? rsqrtf(q2 + kL2Eps) : 1.0f) * scale;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                sk[t][lane + 32 * i] = kk[i] * rk;
-                sq[t][lane + 32 * i] = qq[i] * rq;
+            for (int x = 0; x < D / 32; ++x) {
+                sk[t][lane + 32 * x] = to_f32<T>(nk[i][x]) * rk;
+                sq[t][lane + 32 * x] = to_f32<T>(nq[i][x]) * rq;
             }
-            sv[t][lane] = to_f32<T>(vp[(t0 + t) * DV + lane]);
+            sv[t][lane] = to_f32<T>(nv[i]);
             if (lane == 0) {
                 skq[t] = kq * rk * rq;
-                sbeta[t] = beta[bh * N + t0 + t];
-                salpha[t] = log_alpha ? expf(log_alpha[bh * N + t0 + t]) : 1.0f;
+                sbeta[t] = nb[i];
+                salpha[t] = expf(na[i]);
             }
         }
+        if (b + 1 < nblk)
+            fetch(b + 1);
         if (chk) {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
                 chk[((bh * (nblk + 1) + b) * D + (i / 4) * 32 + 4 * r + i % 4) * DV + c0 + col] = s[i];
         }
         __syncthreads();
+#pragma unroll 2
         for (int t = 0; t < n; ++t) {
             const float a = salpha[t];
-            float pk = 0.f, pq = 0.f, kf[D / 8];
+            float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f}, kf[D / 8];
 #pragma unroll
             for (int m = 0; m < D / 32; ++m) {
                 const float4 x = *reinterpret_cast<const float4*>(&sk[t][32 * m + 4 * r]);
@@ -109,23 +134,23 @@ __global__ void __launch_bounds__(kRecThreads)
                 const float yf[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[4 * m + j] *= a;
-                    pk = fmaf(kf[4 * m + j], s[4 * m + j], pk);
-                    pq = fmaf(yf[j], s[4 * m + j], pq);
+                    pk[j] = fmaf(kf[4 * m + j], s[4 * m + j], pk[j]);
+                    pq[j] = fmaf(yf[j], s[4 * m + j], pq[j]);
                 }
             }
+            float dk = (pk[0] + pk[1]) + (pk[2] + pk[3]), dq = (pq[0] + pq[1]) + (pq[2] + pq[3]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
-                pk += __shfl_xor_sync(0xffffffffu, pk, o);
-                pq += __shfl_xor_sync(0xffffffffu, pq, o);
+                dk += __shfl_xor_sync(0xffffffffu, dk, o);
+                dq += __shfl_xor_sync(0xffffffffu, dq, o);
             }
-            const float e = sv[t][col] - pk;
+            const float e = fmaf(-a, dk, sv[t][col]);  // the decay off the chain: S' = a S
             const float u = sbeta[t] * e;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-                s[i] = fmaf(kf[i], u, s[i]);
+                s[i] = fmaf(kf[i], u, a * s[i]);
             if (r == 0) {
-                so[t][col] = fmaf(skq[t], u, pq);
+                so[t][col] = fmaf(skq[t], u, a * dq);
                 if (err)
                     err[(bh * N + t0 + t) * DV + c0 + col] = e;
             }
@@ -247,87 +272,129 @@ __global__ void __launch_bounds__(kDecThreads)
 }
 
 // -------------------------------------------------------------- gradient ----
-// Chunks of C = kRecTok tokens in reverse, one CTA per value head.  With G the
-// running sum of log_alpha inside the chunk, D_ij = exp(G_i - G_j), U = beta E,
-// S0 and S1 the states before and after the chunk, dS1 the gradient of S1:
+// Chunks of C = kRecTok tokens.  With G the running sum of log_alpha inside the
+// chunk, D_ij = exp(G_i - G_j), U = beta E, S0 and S1 the states before and after
+// the chunk, dS1 the gradient of S1:
 //
 //   P_ij = D_ij q_i.k_j (j <= i),  A_ij = D_ij k_i.k_j (j < i)
 //   dU = P^T dO + diag(e^{G_C - G}) K dS1
-//   Y  = (I + diag(beta) A)^{-T} dU      from the last token back, a column per thread
+//   Y  = (I + diag(beta) A)^{-T} dU      from the last token back
 //   dV = beta Y,  dbeta_i = Y_i.E_i
+//   dS0 = e^{G_C} dS1 + (diag(e^G) Q)^T dO - (diag(e^G) K)^T dV
 //   dQ = (dO U^T o D) K + diag(e^G) dO S0^T
-//   dK = (dO U^T o D)^T Q + M K + M^T K - diag(beta e^G) Y S0^T + diag(e^{G_C - G}) U dS1^T
-//        with M_ij = -beta_i D_ij Y_i.U_j (j < i)
-//   dS0 = e^{G_C} dS1 + (diag(e^G) Q)^T dO - (diag(beta e^G) K)^T Y
+//   dK = (dO U^T o D)^T Q + M K + M^T K - diag(e^G) dV S0^T + diag(e^{G_C - G}) U dS1^T
+//        with M_ij = -D_ij dV_i.U_j (j < i)
 //   dlog_alpha_t = <S1, dS1> + sum_{i >= t in the chunk} (q_i.dQ_i - v_i.dV_i)
 //
 // (the last line: every place where G_i enters is a factor of o_i's or of
 // e_i's right-hand side, and those products are q_i.dQ_i and v_i.dV_i).
-// S0 and E come from the recurrence above, which stored them.  Everything is
-// fp32 in shared memory; the products are bound by shared-memory reads.
-constexpr int kGradThreads = 512;
-
-template <int D, int DV>
-struct GradSmem {
-    static constexpr int C = kRecTok;
-    static constexpr int LS = DV + 1, LK = D + 1, LV = DV + 1, LC = C + 1;
-    static constexpr int floats = 2 * D * LS + 2 * C * LK + 3 * C * LV + 3 * C * LC + 8 * C + 32;
-    static constexpr size_t bytes = sizeof(float) * floats;
-    static_assert(bytes <= 232448, "shared memory");
+// S0 and E come from the recurrence above, which stored them.  Two kernels: the
+// columns of dS, Y and dV never mix, so k_delta_grad_rev runs the chunks in reverse
+// for 32 columns per CTA and keeps dS1, dV and the dots over its columns;
+// k_delta_grad_dqk then takes every chunk on its own.  fp32 in shared memory, bound
+// by its reads.
+struct GradKept {
+    float* dS;  // [BH][nblk][D][DV] gradient of the state after the chunk
+    float* dV;  // [BH][N][DV]
+    float* bb;  // [BH][DV / 32][N] Y.E over 32 columns
+    float* vv;  // [BH][DV / 32][N] v.dV
+    float* cd;  // [BH][DV / 32][nblk] <S1, dS1>
 };
 
-template <int D, int DV, typename T>
-__global__ void __launch_bounds__(kGradThreads)
-    k_delta_grad(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                 const float* __restrict__ beta, const float* __restrict__ log_alpha,
-                 const T* __restrict__ dout, const float* __restrict__ dS_out,
-                 const float* __restrict__ chk, const float* __restrict__ err,
-                 float* __restrict__ dq, float* __restrict__ dk, T* __restrict__ dv,
-                 float* __restrict__ dbeta, float* __restrict__ dlog_alpha, float* dS0, int64_t N,
-                 int H, int Hk, int l2, float scale)
+constexpr int kRevThreads = 256;
+
+// K and Q rows of a chunk (normalised, Q scaled; zero past n) by warps of a block
+template <int D, typename T>
+__device__ __forceinline__ void load_rows(float* sk, float* sq, int LK, const T* k, const T* q, int64_t row0, int n, int l2,
+                                          float scale)
 {
-    using SM = GradSmem<D, DV>;
-    constexpr int C = SM::C, LS = SM::LS, LK = SM::LK, LV = SM::LV, LC = SM::LC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int t = warp; t < kRecTok; t += blockDim.x >> 5) {
+        float kk[D / 32], qq[D / 32], k2 = 0.f, q2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int64_t at = (row0 + t) * D + lane + 32 * i;
+            kk[i] = t < n ? to_f32<T>(k[at]) : 0.f;
+            qq[i] = t < n ? to_f32<T>(q[at]) : 0.f;
+            k2 = fmaf(kk[i], kk[i], k2);
+            q2 = fmaf(qq[i], qq[i], q2);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            k2 += __shfl_xor_sync(0xffffffffu, k2, o);
+            q2 += __shfl_xor_sync(0xffffffffu, q2, o);
+        }
+        const float rk = l2 ? rsqrtf(k2 + kL2Eps) : 1.0f;
+        const float rq = (l2 ? rsqrtf(q2 + kL2Eps) : 1.0f) * scale;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            sk[t * LK + lane + 32 * i] = kk[i] * rk;
+            sq[t * LK + lane + 32 * i] = qq[i] * rq;
+        }
+    }
+}
+
+// Running sums of a chunk's gates by one warp: G (64 bits), e^G, e^{G_C - G}
+__device__ __forceinline__ void load_gates(double* G, float* eg, float* ege, const float* log_alpha, int n)
+{
+    const int lane = threadIdx.x & 31;
+    double g = log_alpha && lane < n ? (double)delta::clamp_gate(log_alpha[lane]) : 0.0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, g, o);
+        if (lane >= o)
+            g += x;
+    }
+    G[lane] = g;
+    eg[lane] = expf((float)g);
+    ege[lane] = expf((float)(__shfl_sync(0xffffffffu, g, 31) - g));
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kRevThreads)
+    k_delta_grad_rev(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                     const float* __restrict__ beta, const float* __restrict__ log_alpha,
+                     const T* __restrict__ dout, const float* __restrict__ dS_out,
+                     const float* __restrict__ chk, const float* __restrict__ err, T* __restrict__ dv,
+                     float* __restrict__ dS0, GradKept kept, int64_t N, int H, int Hk, int DV, int l2,
+                     float scale)
+{
+    constexpr int C = kRecTok, LK = D + 4, LC = C + 4, R = D / 8;  // R: state rows per thread
     extern __shared__ __align__(16) float smem[];
-    float* S = smem;             // [D][LS] state before the chunk
-    float* dS = S + D * LS;      // [D][LS] gradient of the state after the chunk
-    float* sk = dS + D * LS;     // [C][LK]
-    float* sq = sk + C * LK;     // [C][LK], scaled
-    float* sdo = sq + C * LK;    // [C][LV]
-    float* se = sdo + C * LV;    // [C][LV]
-    float* sy = se + C * LV;     // [C][LV]
-    float* P = sy + C * LV;      // [C][LC] P, then dO U^T o D
-    float* A = P + C * LC;       // [C][LC] A, then M
-    float* Dm = A + C * LC;      // [C][LC] decay
-    float* sb = Dm + C * LC;     // beta
-    float* eg = sb + C;          // e^G
-    float* ege = eg + C;         // e^{G_C - G}
-    float* dG = ege + C;
-    float* vdv = dG + C;
-    float* red = vdv + C;        // [32]
+    float* dS = smem;           // [D][32]
+    float* sk = dS + D * 32;    // [C][LK]
+    float* sq = sk + C * LK;    // [C][LK], scaled
+    float* sdo = sq + C * LK;   // [C][32]
+    float* sy = sdo + C * 32;   // [C][32] dU, then Y, then dV
+    float* P = sy + C * 32;     // [C][LC]
+    float* A = P + C * LC;      // [C][LC] beta_i A_ij
     __shared__ double G[C];
+    __shared__ float eg[C], ege[C], sb[C], red[8];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int W = kGradThreads / 32;
     const int64_t bh = blockIdx.x;
+    const int c0 = blockIdx.y * 32, nsl = gridDim.y;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const int64_t nblk = (N + C - 1) / C;
-    const float* ck = chk + bh * (nblk + 1) * (int64_t)(D * DV);
 
-    for (int i = tid; i < D * DV; i += kGradThreads) {
-        S[i / DV * LS + i % DV] = ck[nblk * D * DV + i];
-        dS[i / DV * LS + i % DV] = dS_out ? dS_out[bh * D * DV + i] : 0.f;
+    // a thread keeps rows warp R .. of column lane in registers too
+    float ds[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        ds[i] = dS_out ? dS_out[(bh * D + warp * R + i) * DV + c0 + lane] : 0.f;
+        dS[(warp * R + i) * 32 + lane] = ds[i];
     }
     for (int64_t b = nblk - 1; b >= 0; --b) {
         const int64_t t0 = b * C;
         const int n = (int)min((int64_t)C, N - t0);
-        __syncthreads();
-        // <S1, dS1>, then S <- S0
+        // dS1 out, <S1, dS1>
         float dot = 0.f;
-        for (int i = tid; i < D * DV; i += kGradThreads) {
-            const int at = i / DV * LS + i % DV;
-            dot = fmaf(S[at], dS[at], dot);
-            S[at] = ck[b * D * DV + i];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int64_t row = warp * R + i;
+            kept.dS[((bh * nblk + b) * D + row) * DV + c0 + lane] = ds[i];
+            if (log_alpha)
+                dot = fmaf(chk[((bh * (nblk + 1) + b + 1) * D + row) * DV + c0 + lane], ds[i], dot);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -335,182 +402,327 @@ __global__ void __launch_bounds__(kGradThreads)
         if (lane == 0)
             red[warp] = dot;
         // rows past the end stay zero and leave nothing behind (beta = 0, G constant)
-        for (int t = warp; t < C; t += W) {
-            float kk[D / 32], qq[D / 32], k2 = 0.f, q2 = 0.f;
+        load_rows<D, T>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int64_t at = (kh * N + t0 + t) * D + lane + 32 * i;
-                kk[i] = t < n ? to_f32<T>(k[at]) : 0.f;
-                qq[i] = t < n ? to_f32<T>(q[at]) : 0.f;
-                k2 = fmaf(kk[i], kk[i], k2);
-                q2 = fmaf(qq[i], qq[i], q2);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                k2 += __shfl_xor_sync(0xffffffffu, k2, o);
-                q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-            }
-            const float rk = l2 ? rsqrtf(k2 + kL2Eps) : 1.0f;
-            const float rq = (l2 ? rsqrtf(q2 + kL2Eps) : 1.0f) * scale;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                sk[t * LK + lane + 32 * i] = kk[i] * rk;
-                sq[t * LK + lane + 32 * i] = qq[i] * rq;
-            }
-            for (int c = lane; c < DV; c += 32) {
-                const int64_t at = (bh * N + t0 + t) * DV + c;
-                sdo[t * LV + c] = t < n ? to_f32<T>(dout[at]) : 0.f;
-                se[t * LV + c] = t < n ? err[at] : 0.f;
-            }
-            if (lane == 0)
-                sb[t] = t < n ? beta[bh * N + t0 + t] : 0.f;
-        }
+        for (int t = warp; t < C; t += 8)
+            sdo[t * 32 + lane] = t < n ? to_f32<T>(dout[(bh * N + t0 + t) * DV + c0 + lane]) : 0.f;
         if (warp == 0) {
-            double g = log_alpha && lane < n ? (double)delta::clamp_gate(log_alpha[bh * N + t0 + lane]) : 0.0;
+            load_gates(G, eg, ege, log_alpha ? log_alpha + bh * N + t0 : nullptr, n);
+            sb[lane] = lane < n ? beta[bh * N + t0 + lane] : 0.f;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            float x = 0.f;
+            for (int w = 0; w < 8; ++w)
+                x += red[w];
+            kept.cd[(bh * nsl + blockIdx.y) * nblk + b] = x;
+        }
+        // P and beta A: 4 rows (warp) x a column (lane) per thread
+        {
+            float p[4] = {}, a[4] = {};
+            for (int x = 0; x < D; x += 4) {
+                const float4 kj = *reinterpret_cast<const float4*>(sk + lane * LK + x);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, g, o);
-                if (lane >= o)
-                    g += x;
-            }
-            G[lane] = g;
-            eg[lane] = expf((float)g);
-            ege[lane] = expf((float)(__shfl_sync(0xffffffffu, g, 31) - g));
-        }
-        __syncthreads();
-        // P, A, D: a row per warp pass, a column j per lane
-        for (int i = warp; i < C; i += W) {
-            float p = 0.f, a = 0.f;
-            for (int x = 0; x < D; ++x) {
-                const float kj = sk[lane * LK + x];
-                p = fmaf(sq[i * LK + x], kj, p);
-                a = fmaf(sk[i * LK + x], kj, a);
-            }
-            const float dec = lane <= i ? expf((float)(G[i] - G[lane])) : 0.f;
-            Dm[i * LC + lane] = dec;
-            P[i * LC + lane] = lane <= i ? p * dec : 0.f;
-            A[i * LC + lane] = lane < i ? a * dec : 0.f;
-        }
-        __syncthreads();
-        // dU
-        for (int at = tid; at < C * DV; at += kGradThreads) {
-            const int j = at / DV, c = at % DV;
-            float x = 0.f, y = 0.f;
-            for (int i = j; i < C; ++i)
-                x = fmaf(P[i * LC + j], sdo[i * LV + c], x);
-            for (int i = 0; i < D; ++i)
-                y = fmaf(sk[j * LK + i], dS[i * LS + c], y);
-            sy[j * LV + c] = fmaf(ege[j], y, x);
-        }
-        __syncthreads();
-        // Y, a column per thread
-        if (tid < DV) {
-            for (int j = C - 2; j >= 0; --j) {
-                float y = sy[j * LV + tid];
-                for (int i = j + 1; i < C; ++i)
-                    y = fmaf(-sb[i] * A[i * LC + j], sy[i * LV + tid], y);
-                sy[j * LV + tid] = y;
-            }
-        }
-        __syncthreads();
-        // dV, dbeta, v.dV; E becomes U
-        for (int t = warp; t < C; t += W) {
-            float db = 0.f, x = 0.f;
-            for (int c = lane; c < DV; c += 32) {
-                const float y = sy[t * LV + c], e = se[t * LV + c];
-                db = fmaf(y, e, db);
-                se[t * LV + c] = sb[t] * e;
-                if (t < n) {
-                    const int64_t at = (bh * N + t0 + t) * DV + c;
-                    const float g = sb[t] * y;
-                    dv[at] = from_f32<T>(g);
-                    x = fmaf(g, to_f32<T>(v[at]), x);
+                for (int i = 0; i < 4; ++i) {
+                    const float4 qi = *reinterpret_cast<const float4*>(sq + (4 * warp + i) * LK + x);
+                    const float4 ki = *reinterpret_cast<const float4*>(sk + (4 * warp + i) * LK + x);
+                    p[i] = fmaf(qi.x, kj.x, fmaf(qi.y, kj.y, fmaf(qi.z, kj.z, fmaf(qi.w, kj.w, p[i]))));
+                    a[i] = fmaf(ki.x, kj.x, fmaf(ki.y, kj.y, fmaf(ki.z, kj.z, fmaf(ki.w, kj.w, a[i]))));
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * warp + r;
+                const float dec = lane <= i ? expf((float)(G[i] - G[lane])) : 0.f;
+                P[i * LC + lane] = lane <= i ? p[r] * dec : 0.f;
+                A[i * LC + lane] = lane < i ? a[r] * dec * sb[i] : 0.f;
+            }
+        }
+        __syncthreads();
+        // dU: rows 4 warp .. + 3 of column lane
+        {
+            float u[4] = {}, w[4] = {};
+            for (int x = 0; x < D; x += 4) {
+                const float d0 = dS[x * 32 + lane], d1 = dS[(x + 1) * 32 + lane], d2 = dS[(x + 2) * 32 + lane],
+                            d3 = dS[(x + 3) * 32 + lane];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 kj = *reinterpret_cast<const float4*>(sk + (4 * warp + r) * LK + x);
+                    w[r] = fmaf(kj.x, d0, fmaf(kj.y, d1, fmaf(kj.z, d2, fmaf(kj.w, d3, w[r]))));
+                }
+            }
+            for (int i = 4 * warp; i < C; ++i) {
+                const float4 p = *reinterpret_cast<const float4*>(P + i * LC + 4 * warp);
+                const float d = sdo[i * 32 + lane];
+                u[0] = fmaf(p.x, d, u[0]), u[1] = fmaf(p.y, d, u[1]);
+                u[2] = fmaf(p.z, d, u[2]), u[3] = fmaf(p.w, d, u[3]);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                sy[(4 * warp + r) * 32 + lane] = fmaf(ege[4 * warp + r], w[r], u[r]);
+        }
+        __syncthreads();
+        // Y: one warp, a column per lane; each solved token leaves the earlier ones
+        if (warp == 0) {
+            float y[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                y[j] = sy[j * 32 + lane];
+#pragma unroll
+            for (int i = C - 1; i > 0; --i) {
+#pragma unroll
+                for (int j = 0; j < i; j += 4) {  // A is zero from the diagonal on
+                    const float4 a = *reinterpret_cast<const float4*>(A + i * LC + j);
+                    y[j] = fmaf(-a.x, y[i], y[j]);
+                    if (j + 1 < i)
+                        y[j + 1] = fmaf(-a.y, y[i], y[j + 1]);
+                    if (j + 2 < i)
+                        y[j + 2] = fmaf(-a.z, y[i], y[j + 2]);
+                    if (j + 3 < i)
+                        y[j + 3] = fmaf(-a.w, y[i], y[j + 3]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                sy[j * 32 + lane] = y[j];
+        }
+        __syncthreads();
+        // dV, the dots over the columns
+#pragma unroll
+        for (int t = warp; t < C; t += 8) {
+            float y = sy[t * 32 + lane], db = 0.f, x = 0.f;
+            const float g = sb[t] * y;
+            sy[t * 32 + lane] = g;
+            if (t < n) {
+                const int64_t at = (bh * N + t0 + t) * DV + c0 + lane;
+                dv[at] = from_f32<T>(g);
+                kept.dV[at] = g;
+                db = y * err[at];
+                x = g * to_f32<T>(v[at]);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 db += __shfl_xor_sync(0xffffffffu, db, o);
                 x += __shfl_xor_sync(0xffffffffu, x, o);
             }
-            if (lane == 0) {
-                vdv[t] = x;
-                if (t < n)
-                    dbeta[bh * N + t0 + t] = db;
+            if (lane == 0 && t < n) {
+                kept.bb[(bh * nsl + blockIdx.y) * N + t0 + t] = db;
+                kept.vv[(bh * nsl + blockIdx.y) * N + t0 + t] = x;
             }
         }
         __syncthreads();
-        // P <- dO U^T o D, A <- M
-        for (int i = warp; i < C; i += W) {
-            float p = 0.f, m = 0.f;
-            for (int c = 0; c < DV; ++c) {
-                const float uj = se[lane * LV + c];
-                p = fmaf(sdo[i * LV + c], uj, p);
-                m = fmaf(sy[i * LV + c], uj, m);
-            }
-            const float dec = Dm[i * LC + lane];
-            P[i * LC + lane] = p * dec;
-            A[i * LC + lane] = lane < i ? -sb[i] * m * dec : 0.f;
-        }
-        __syncthreads();
-        // dQ, q.dQ
-        for (int i = warp; i < n; i += W) {
-            float dot_q = 0.f;
-            for (int x = lane; x < D; x += 32) {
-                float z = 0.f, w = 0.f;
-                for (int j = 0; j <= i; ++j)
-                    z = fmaf(P[i * LC + j], sk[j * LK + x], z);
-                for (int c = 0; c < DV; ++c)
-                    w = fmaf(sdo[i * LV + c], S[x * LS + c], w);
-                z = fmaf(eg[i], w, z);
-                dot_q = fmaf(z, sq[i * LK + x], dot_q);
-                dq[(bh * N + t0 + i) * D + x] = z;
-            }
+        // dS <- dS0
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                dot_q += __shfl_xor_sync(0xffffffffu, dot_q, o);
-            if (lane == 0)
-                dG[i] = dot_q - vdv[i];
-        }
-        // dK
-        for (int j = warp; j < n; j += W) {
-            for (int x = lane; x < D; x += 32) {
-                float z = 0.f, w = 0.f, u = 0.f;
-                for (int i = j; i < C; ++i)
-                    z = fmaf(P[i * LC + j], sq[i * LK + x], z);
-                for (int i = 0; i < C; ++i)
-                    z = fmaf(i < j ? A[j * LC + i] : A[i * LC + j], sk[i * LK + x], z);
-                for (int c = 0; c < DV; ++c) {
-                    w = fmaf(sy[j * LV + c], S[x * LS + c], w);
-                    u = fmaf(se[j * LV + c], dS[x * LS + c], u);
-                }
-                dk[(bh * N + t0 + j) * D + x] = z - sb[j] * eg[j] * w + ege[j] * u;
+        for (int i = 0; i < R; ++i)
+            ds[i] *= eg[C - 1];
+        for (int i = 0; i < C; ++i) {
+            const float o = eg[i] * sdo[i * 32 + lane], g = -eg[i] * sy[i * 32 + lane];
+#pragma unroll
+            for (int x = 0; x < R; x += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(sq + i * LK + warp * R + x);
+                const float4 c = *reinterpret_cast<const float4*>(sk + i * LK + warp * R + x);
+                ds[x] = fmaf(a.x, o, fmaf(c.x, g, ds[x]));
+                ds[x + 1] = fmaf(a.y, o, fmaf(c.y, g, ds[x + 1]));
+                ds[x + 2] = fmaf(a.z, o, fmaf(c.z, g, ds[x + 2]));
+                ds[x + 3] = fmaf(a.w, o, fmaf(c.w, g, ds[x + 3]));
             }
         }
         __syncthreads();
-        if (dlog_alpha && tid < n) {
-            float x = 0.f;
-            for (int w = 0; w < W; ++w)
-                x += red[w];
-            for (int i = n - 1; i >= tid; --i)
-                x += dG[i];
-            dlog_alpha[bh * N + t0 + tid] = x;
-        }
-        // dS <- dS0; S keeps S0, the next chunk's S1
-        for (int at = tid; at < D * DV; at += kGradThreads) {
-            const int x = at / DV, c = at % DV;
-            float z = eg[C - 1] * dS[x * LS + c];
-            for (int i = 0; i < C; ++i) {
-                z = fmaf(eg[i] * sq[i * LK + x], sdo[i * LV + c], z);
-                z = fmaf(-sb[i] * eg[i] * sk[i * LK + x], sy[i * LV + c], z);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            dS[(warp * R + i) * 32 + lane] = ds[i];
+    }
+    if (dS0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            dS0[(bh * D + warp * R + i) * DV + c0 + lane] = ds[i];
+    }
+}
+
+template <int D>
+constexpr size_t rev_smem()
+{
+    return sizeof(float) * (D * 32 + 2 * kRecTok * (D + 4) + 2 * kRecTok * 32 + 2 * kRecTok * (kRecTok + 4));
+}
+
+constexpr int kGradThreads = 256;
+
+template <int D, int DV>
+struct GradSmem {
+    static constexpr int C = kRecTok;
+    static constexpr int LS = DV + 4, LK = D + 4, LV = DV + 4, LC = C + 4;
+    static constexpr int floats = D * LS + 2 * C * LK + 3 * C * LV + 3 * C * LC;
+    static constexpr size_t bytes = sizeof(float) * floats;
+    static_assert(bytes <= 232448, "shared memory");
+};
+
+// 16 x 16 threads per 32 x D result: thread (ty, tx) owns rows 2 ty, 2 ty + 1 and
+// columns tx, tx + 16, .. (stride: rows of S at 4 banks' distance from each other)
+template <int D, int DV, typename T>
+__global__ void __launch_bounds__(kGradThreads)
+    k_delta_grad_dqk(const T* __restrict__ q, const T* __restrict__ k, const float* __restrict__ beta,
+                     const float* __restrict__ log_alpha, const T* __restrict__ dout,
+                     const float* __restrict__ chk, const float* __restrict__ err, GradKept kept,
+                     float* __restrict__ dq, float* __restrict__ dk, float* __restrict__ dbeta,
+                     float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale)
+{
+    using SM = GradSmem<D, DV>;
+    constexpr int C = SM::C, LS = SM::LS, LK = SM::LK, LV = SM::LV, LC = SM::LC, CX = D / 16;
+    extern __shared__ __align__(16) float smem[];
+    float* S = smem;           // [D][LS] S0, then dS1
+    float* sk = S + D * LS;    // [C][LK]
+    float* sq = sk + C * LK;   // [C][LK], scaled
+    float* sdo = sq + C * LK;  // [C][LV]
+    float* su = sdo + C * LV;  // [C][LV] U
+    float* sg = su + C * LV;   // [C][LV] dV
+    float* P = sg + C * LV;    // [i][j] dO_i.U_j D_ij
+    float* Pt = P + C * LC;    // its transpose
+    float* M = Pt + C * LC;    // [j][i] M_ij (i > j), M_ji (i < j): the matrix on K for dK
+    __shared__ double G[C];
+    __shared__ float eg[C], ege[C], sb[C], dG[C];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ty = tid >> 4, tx = tid & 15;
+    const int64_t nblk = (N + C - 1) / C;
+    const int64_t bh = blockIdx.x / nblk, b = blockIdx.x % nblk;
+    const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
+    const int64_t t0 = b * C;
+    const int n = (int)min((int64_t)C, N - t0);
+
+    load_rows<D, T>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
+    if (warp == 0)
+        load_gates(G, eg, ege, log_alpha ? log_alpha + bh * N + t0 : nullptr, n);
+    if (tid < C)
+        sb[tid] = tid < n ? beta[bh * N + t0 + tid] : 0.f;
+    for (int i = tid; i < D * DV; i += kGradThreads)
+        S[i / DV * LS + i % DV] = chk[(bh * (nblk + 1) + b) * (int64_t)(D * DV) + i];
+    for (int i = tid; i < C * DV; i += kGradThreads) {
+        const int t = i / DV, c = i % DV;
+        const int64_t at = (bh * N + t0 + t) * DV + c;
+        sdo[t * LV + c] = t < n ? to_f32<T>(dout[at]) : 0.f;
+        su[t * LV + c] = t < n ? beta[bh * N + t0 + t] * err[at] : 0.f;
+        sg[t * LV + c] = t < n ? kept.dV[at] : 0.f;
+    }
+    __syncthreads();
+    // dO_i.U_j and dV_i.U_j: 4 rows (warp) x a column (lane) per thread
+    {
+        float p[4] = {}, m[4] = {};
+        for (int x = 0; x < DV; x += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(su + lane * LV + x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 o = *reinterpret_cast<const float4*>(sdo + (4 * warp + r) * LV + x);
+                const float4 g = *reinterpret_cast<const float4*>(sg + (4 * warp + r) * LV + x);
+                p[r] = fmaf(o.x, u.x, fmaf(o.y, u.y, fmaf(o.z, u.z, fmaf(o.w, u.w, p[r]))));
+                m[r] = fmaf(g.x, u.x, fmaf(g.y, u.y, fmaf(g.z, u.z, fmaf(g.w, u.w, m[r]))));
             }
-            dS[x * LS + c] = z;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * warp + r, j = lane;
+            const float dec = j <= i ? expf((float)(G[i] - G[j])) : 0.f;
+            const float x = j <= i ? p[r] * dec : 0.f;
+            P[i * LC + j] = x;
+            Pt[j * LC + i] = x;
+            if (j < i)
+                M[i * LC + j] = M[j * LC + i] = -m[r] * dec;
+            else if (j == i)
+                M[i * LC + i] = 0.f;
         }
     }
     __syncthreads();
-    if (dS0) {
-        for (int i = tid; i < D * DV; i += kGradThreads)
-            dS0[bh * D * DV + i] = dS[i / DV * LS + i % DV];
+    // x[row][column] += a[row][0 .. C) b[0 .. C)[column], rows 2 ty, 2 ty + 1
+    auto tokens = [&](float (&x)[2][CX], const float* a, const float* bm) {
+#pragma unroll 2
+        for (int j = 0; j < C; j += 4) {
+            const float4 a0 = *reinterpret_cast<const float4*>(a + 2 * ty * LC + j);
+            const float4 a1 = *reinterpret_cast<const float4*>(a + (2 * ty + 1) * LC + j);
+#pragma unroll
+            for (int i = 0; i < CX; ++i) {
+                const float* at = bm + j * LK + tx + 16 * i;
+                const float b0 = at[0], b1 = at[LK], b2 = at[2 * LK], b3 = at[3 * LK];
+                x[0][i] = fmaf(a0.x, b0, fmaf(a0.y, b1, fmaf(a0.z, b2, fmaf(a0.w, b3, x[0][i]))));
+                x[1][i] = fmaf(a1.x, b0, fmaf(a1.y, b1, fmaf(a1.z, b2, fmaf(a1.w, b3, x[1][i]))));
+            }
+        }
+    };
+    // x[row][column] += f[row] a[row] . S[column]
+    auto states = [&](float (&x)[2][CX], const float* a, float f0, float f1) {
+        float y[2][CX] = {};
+#pragma unroll 2
+        for (int c = 0; c < DV; c += 4) {
+            const float4 a0 = *reinterpret_cast<const float4*>(a + 2 * ty * LV + c);
+            const float4 a1 = *reinterpret_cast<const float4*>(a + (2 * ty + 1) * LV + c);
+#pragma unroll
+            for (int i = 0; i < CX; ++i) {
+                const float4 s = *reinterpret_cast<const float4*>(S + (tx + 16 * i) * LS + c);
+                y[0][i] = fmaf(a0.x, s.x, fmaf(a0.y, s.y, fmaf(a0.z, s.z, fmaf(a0.w, s.w, y[0][i]))));
+                y[1][i] = fmaf(a1.x, s.x, fmaf(a1.y, s.y, fmaf(a1.z, s.z, fmaf(a1.w, s.w, y[1][i]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CX; ++i)
+            x[0][i] = fmaf(f0, y[0][i], x[0][i]), x[1][i] = fmaf(f1, y[1][i], x[1][i]);
+    };
+    const int i0 = 2 * ty, i1 = i0 + 1;
+    auto put = [&](float* dst, const float (&x)[2][CX]) {
+#pragma unroll
+        for (int i = 0; i < CX; ++i) {
+            if (i0 < n)
+                dst[(bh * N + t0 + i0) * D + tx + 16 * i] = x[0][i];
+            if (i1 < n)
+                dst[(bh * N + t0 + i1) * D + tx + 16 * i] = x[1][i];
+        }
+    };
+    {  // dQ, q.dQ
+        float x[2][CX] = {}, d0 = 0.f, d1 = 0.f;
+        tokens(x, P, sk);
+        states(x, sdo, eg[i0], eg[i1]);
+#pragma unroll
+        for (int i = 0; i < CX; ++i) {
+            d0 = fmaf(x[0][i], sq[i0 * LK + tx + 16 * i], d0);
+            d1 = fmaf(x[1][i], sq[i1 * LK + tx + 16 * i], d1);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+            d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+        }
+        if (tx == 0)
+            dG[i0] = d0, dG[i1] = d1;
+        put(dq, x);
     }
+    float x[2][CX] = {};
+    tokens(x, Pt, sq);
+    tokens(x, M, sk);
+    states(x, sg, -eg[i0], -eg[i1]);
+    __syncthreads();  // S0 is read
+    for (int i = tid; i < D * DV; i += kGradThreads)
+        S[i / DV * LS + i % DV] = kept.dS[(bh * nblk + b) * (int64_t)(D * DV) + i];
+    if (warp == 0) {  // the gates' gradients
+        const int nsl = DV / 32;
+        float y = lane < n ? dG[lane] : 0.f, db = 0.f, after = 0.f;
+        for (int s = 0; s < nsl; ++s) {
+            if (lane < n) {
+                db += kept.bb[(bh * nsl + s) * N + t0 + lane];
+                y -= kept.vv[(bh * nsl + s) * N + t0 + lane];
+            }
+            after += kept.cd[(bh * nsl + s) * nblk + b];
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float z = __shfl_down_sync(0xffffffffu, y, o);
+            if (lane + o < 32)
+                y += z;
+        }
+        if (lane < n) {
+            dbeta[bh * N + t0 + lane] = db;
+            if (dlog_alpha)
+                dlog_alpha[bh * N + t0 + lane] = y + after;
+        }
+    }
+    __syncthreads();
+    states(x, su, ege[i0], ege[i1]);
+    put(dk, x);
 }
 
 // Gradients of the key heads' rows from those of the value heads that read
@@ -602,17 +814,28 @@ cudaError_t run_decode(const DeltaArgs& a)
 }
 
 struct GradLayout {
-    size_t chk, err, dq, dk, total;
+    size_t chk, err, dq, dk, dS, dV, bb, vv, cd, total;
 };
 GradLayout grad_layout(const DeltaArgs& a)
 {
-    const size_t BH = (size_t)(a.B * a.H), N = (size_t)a.N;
+    const size_t BH = (size_t)(a.B * a.H), N = (size_t)a.N, sl = (size_t)a.dv / 32, nb = (size_t)rec_blocks(a.N);
     GradLayout l;
-    l.chk = 0;
-    l.err = up256(4 * BH * ((size_t)rec_blocks(a.N) + 1) * a.d * a.dv);
-    l.dq = l.err + up256(4 * BH * N * a.dv);
-    l.dk = l.dq + up256(4 * BH * N * a.d);
-    l.total = l.dk + up256(4 * BH * N * a.d);
+    size_t at = 0;
+    auto take = [&](size_t floats) {
+        const size_t p = at;
+        at += up256(4 * floats);
+        return p;
+    };
+    l.chk = take(BH * (nb + 1) * a.d * a.dv);
+    l.err = take(BH * N * a.dv);
+    l.dq = take(BH * N * a.d);
+    l.dk = take(BH * N * a.d);
+    l.dS = take(BH * nb * a.d * a.dv);
+    l.dV = take(BH * N * a.dv);
+    l.bb = take(BH * sl * N);
+    l.vv = take(BH * sl * N);
+    l.cd = take(BH * sl * nb);
+    l.total = at;
     return l;
 }
 
@@ -621,53 +844,55 @@ cudaError_t run_grad(const DeltaArgs& a)
 {
     const GradLayout l = grad_layout(a);
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
-    float* chk = reinterpret_cast<float*>(ws + l.chk);
-    float* err = reinterpret_cast<float*>(ws + l.err);
-    float* dq = reinterpret_cast<float*>(ws + l.dq);
-    float* dk = reinterpret_cast<float*>(ws + l.dk);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const GradKept kept = {f32(l.dS), f32(l.dV), f32(l.bb), f32(l.vv), f32(l.cd)};
     DeltaArgs f = a;
     f.out = nullptr, f.S_out = nullptr;
-    cudaError_t e = run_rec<D, T>(f, chk, err);
+    cudaError_t e = run_rec<D, T>(f, f32(l.chk), f32(l.err));
     if (e != cudaSuccess)
         return e;
-    auto kern = k_delta_grad<D, DV, T>;
-    const size_t smem = GradSmem<D, DV>::bytes;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t rev = rev_smem<D>(), dqk = GradSmem<D, DV>::bytes;
+    e = cudaFuncSetAttribute(k_delta_grad_rev<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_delta_grad_dqk<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dqk);
     if (e != cudaSuccess)
         return e;
     const T* q = static_cast<const T*>(a.q);
     const T* k = static_cast<const T*>(a.k);
-    const int l2 = a.fm == LA_FM_L2;
-    kern<<<(unsigned)(a.B * a.H), kGradThreads, smem, a.stream>>>(
-        q, k, static_cast<const T*>(a.v), a.beta, a.log_alpha, static_cast<const T*>(a.dout),
-        a.dS_out, chk, err, dq, dk, static_cast<T*>(a.dv_), a.dbeta, a.dlog_alpha, a.dS0, a.N,
-        (int)a.H, (int)a.Hk, l2, a.scale);
+    const T* dout = static_cast<const T*>(a.dout);
+    const int l2 = a.fm == LA_FM_L2, H = (int)a.H, Hk = (int)a.Hk;
+    const int64_t BH = a.B * a.H;
+    k_delta_grad_rev<D, T><<<dim3((unsigned)BH, DV / 32), kRevThreads, rev, a.stream>>>(
+        q, k, static_cast<const T*>(a.v), a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
+        static_cast<T*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    k_delta_grad_dqk<D, DV, T><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
+        q, k, a.beta, a.log_alpha, dout, f32(l.chk), f32(l.err), kept, f32(l.dq), f32(l.dk), a.dbeta,
+        a.dlog_alpha, a.N, H, Hk, l2, a.scale);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     const int64_t rows = a.B * a.Hk * a.N;
     const unsigned grid = (unsigned)((rows + 7) / 8);
-    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(dq, q, static_cast<T*>(a.dq), rows, a.N,
-                                                     (int)a.H, (int)a.Hk, l2, a.scale);
-    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(dk, k, static_cast<T*>(a.dk), rows, a.N,
-                                                     (int)a.H, (int)a.Hk, l2, 1.0f);
+    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(f32(l.dq), q, static_cast<T*>(a.dq), rows, a.N, H, Hk, l2,
+                                                     a.scale);
+    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(f32(l.dk), k, static_cast<T*>(a.dk), rows, a.N, H, Hk, l2,
+                                                     1.0f);
     count_launches(2);
     return cudaGetLastError();
 }
 
-template <int D, int DV>
-cudaError_t grad_type(const DeltaArgs& a)
-{
-    return a.dtype == LA_BF16 ? run_grad<D, DV, __nv_bfloat16>(a) : run_grad<D, DV, float>(a);
-}
 template <int D>
 cudaError_t grad_dims(const DeltaArgs& a)
 {
     switch (a.dv) {
-    case 32: return grad_type<D, 32>(a);
-    case 64: return grad_type<D, 64>(a);
-    default: return grad_type<D, 128>(a);
+    case 32: return run_grad<D, 32, float>(a);
+    case 64: return run_grad<D, 64, float>(a);
+    default: return run_grad<D, 128, float>(a);
     }
 }
 
@@ -680,19 +905,42 @@ bool delta_grid_ok(const DeltaArgs& a)
     return a.N <= most && rec_blocks(a.N) + 1 <= most / (a.B * a.H) && a.B * a.Hk <= most / (a.N > 0 ? a.N : 1);
 }
 
+namespace {
+
+// Sequences shorter than this take the recurrence whatever their number.
+constexpr int64_t kShort = 12;
+
+// The tensor-core forward pays for whole chunks of 64 tokens and two launches (14 to
+// 15 us up to 64 tokens at 32 heads, d = 128, against 5.4 us for the recurrence at 8
+// tokens, 10.7 at 32, 15.2 at 48); with more 32-column slices than the GPU holds at
+// once the recurrence queues (512 heads: 63 us at 17 tokens against 48).
+bool forward_on_tensor_cores(const DeltaArgs& a)
+{
+    if (a.dtype != LA_BF16 || a.N <= kShort)
+        return false;
+    return a.N > 44 || a.B * a.H * (a.dv / kRecCols) > 2 * (int64_t)device_sm_count();
+}
+
+// Its gradient is ahead at every length (8 tokens: 37 against 63 us at 32 heads,
+// 172 against 370 us at 512).
+bool backward_on_tensor_cores(const DeltaArgs& a) { return a.dtype == LA_BF16; }
+
+}  // namespace
+
+// By type and length alone: a size asked for without the GPU at hand serves there.
 size_t delta_forward_workspace(const DeltaArgs& a)
 {
-    return delta_tc_eligible(a) ? delta_tc_forward_workspace(a) : 0;
+    return a.dtype == LA_BF16 && a.N > kShort ? delta_tc_forward_workspace(a) : 0;
 }
 
 size_t delta_backward_workspace(const DeltaArgs& a)
 {
-    return delta_tc_eligible(a) ? delta_tc_backward_workspace(a) : grad_layout(a).total;
+    return backward_on_tensor_cores(a) ? delta_tc_backward_workspace(a) : grad_layout(a).total;
 }
 
 cudaError_t delta_forward(const DeltaArgs& a)
 {
-    if (delta_tc_eligible(a))
+    if (forward_on_tensor_cores(a))
         return delta_tc_forward(a);
     const bool bf = a.dtype == LA_BF16;
     switch (a.d) {
@@ -714,7 +962,7 @@ cudaError_t delta_decode(const DeltaArgs& a)
 
 cudaError_t delta_backward(const DeltaArgs& a)
 {
-    if (delta_tc_eligible(a))
+    if (backward_on_tensor_cores(a))
         return delta_tc_backward(a);
     switch (a.d) {
     case 32: return grad_dims<32>(a);

@@ -2144,7 +2144,6 @@ cudaError_t backward_dims(const DeltaArgs& a)
 
 }  // namespace
 
-bool delta_tc_eligible(const DeltaArgs& a) { return a.dtype == LA_BF16 && a.N > 16; }
 
 size_t delta_tc_forward_workspace(const DeltaArgs& a) { return tc_layout(a).total; }
 

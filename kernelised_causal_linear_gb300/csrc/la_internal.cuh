@@ -181,8 +181,7 @@ bool delta_grid_ok(const DeltaArgs& a);
 cudaError_t delta_forward(const DeltaArgs& a);
 cudaError_t delta_decode(const DeltaArgs& a);
 cudaError_t delta_backward(const DeltaArgs& a);
-// tensor-core path (bf16), chosen by the three calls above
-bool delta_tc_eligible(const DeltaArgs& a);
+// tensor-core path (bf16), chosen by the calls above
 size_t delta_tc_forward_workspace(const DeltaArgs& a);
 size_t delta_tc_backward_workspace(const DeltaArgs& a);
 cudaError_t delta_tc_forward(const DeltaArgs& a);
