@@ -36,7 +36,7 @@ using namespace delta;
 // rows, fk and fq holding the image's power of two, the L2 norm and the scale.
 enum Factor {
     kFacA,    // e^{G_i} fk_i
-    kFacF,    // scale of F's row (a power of two)
+    kFacF,    // [any] = scale of F (a power of two)
     kFacB,    // beta
     kFacO,    // e^{G_i} fq_i
     kFacP,    // scale of P's row (a power of two)
@@ -629,6 +629,7 @@ __device__ __forceinline__ void rows_update(float (&s)[2 * KK][4], const uint32_
 // bf16 pair -> two fp32
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(lo_f(w), hi_f(w)); }
 
 template <int D, bool GRAD, int SP>
 __global__ void __launch_bounds__(256, 1)
@@ -708,10 +709,10 @@ __global__ void __launch_bounds__(256, 1)
         m0 = quad_max(m0), m1 = quad_max(m1);
     };
     auto split_state = [&](int kk, Pow2 p0, Pow2 p1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-        h2_split(s[2 * kk][0] * p0.to, s[2 * kk][1] * p0.to, hi[0], lo[0]);
-        h2_split(s[2 * kk][2] * p1.to, s[2 * kk][3] * p1.to, hi[1], lo[1]);
-        h2_split(s[2 * kk + 1][0] * p0.to, s[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
-        h2_split(s[2 * kk + 1][2] * p1.to, s[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
+        h2_split(row_a(s[2 * kk]), p0.to, hi[0], lo[0]);
+        h2_split(row_b(s[2 * kk]), p1.to, hi[1], lo[1]);
+        h2_split(row_a(s[2 * kk + 1]), p0.to, hi[2], lo[2]);
+        h2_split(row_b(s[2 * kk + 1]), p1.to, hi[3], lo[3]);
     };
     auto keep_state_scale = [&](int64_t c, Pow2 p0, Pow2 p1) {
         if (tq == 0) {
@@ -775,9 +776,9 @@ __global__ void __launch_bounds__(256, 1)
             keep_state_scale(c, p0, p1);
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            r[nt][0] *= p0.from, r[nt][1] *= p0.from, r[nt][2] *= p1.from, r[nt][3] *= p1.from;
+            scale_rows(r[nt], p0.from, p1.from);
             if (reads)
-                o[nt][0] *= p0.from, o[nt][1] *= p0.from, o[nt][2] *= p1.from, o[nt][3] *= p1.from;
+                scale_rows(o[nt], p0.from, p1.from);
         }
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
             return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
@@ -803,16 +804,11 @@ __global__ void __launch_bounds__(256, 1)
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * i + u;
                 const float2 a = fac2(fac, kFacA, sh.tile(i), u, tq), be = fac2(fac, kFacB, sh.tile(i), u, tq);
-                r[nt][0] = fmaf(-a.x, r[nt][0], lo_f(w[2 * u]));
-                r[nt][1] = fmaf(-a.y, r[nt][1], hi_f(w[2 * u]));
-                r[nt][2] = fmaf(-a.x, r[nt][2], lo_f(w[2 * u + 1]));
-                r[nt][3] = fmaf(-a.y, r[nt][3], hi_f(w[2 * u + 1]));
-                z[nt][0] = be.x * r[nt][0], z[nt][1] = be.y * r[nt][1];
-                z[nt][2] = be.x * r[nt][2], z[nt][3] = be.y * r[nt][3];
-                if (reads) {
-                    const float2 fo = fac2(fac, kFacO, sh.tile(i), u, tq);
-                    o[nt][0] *= fo.x, o[nt][1] *= fo.y, o[nt][2] *= fo.x, o[nt][3] *= fo.y;
-                }
+                const float2 minus = make_float2(-a.x, -a.y);
+                set_rows(r[nt], fma2(minus, row_a(r[nt]), bf2(w[2 * u])), fma2(minus, row_b(r[nt]), bf2(w[2 * u + 1])));
+                set_rows(z[nt], mul2(be, row_a(r[nt])), mul2(be, row_b(r[nt])));
+                if (reads)
+                    scale_cols(o[nt], fac2(fac, kFacO, sh.tile(i), u, tq));
             }
         }
         if (SP > 1) {
@@ -833,8 +829,8 @@ __global__ void __launch_bounds__(256, 1)
         auto split8 = [&](const float (&x)[8][4], int kk, Pow2 q0, Pow2 q1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                h2_split(x[2 * kk + u][0] * q0.to, x[2 * kk + u][1] * q0.to, hi[2 * u], lo[2 * u]);
-                h2_split(x[2 * kk + u][2] * q1.to, x[2 * kk + u][3] * q1.to, hi[2 * u + 1], lo[2 * u + 1]);
+                h2_split(row_a(x[2 * kk + u]), q0.to, hi[2 * u], lo[2 * u]);
+                h2_split(row_b(x[2 * kk + u]), q1.to, hi[2 * u + 1], lo[2 * u + 1]);
             }
         };
         // E = R + F z on the own tiles
@@ -857,10 +853,8 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int i = 0; i < 2 * OWN; ++i) {
                 const float2 f = fac2(fac, kFacF, sh.tile(i >> 1), i & 1, tq);
-                r[i][0] = fmaf(f.x * q0.from, x[i][0], r[i][0]);
-                r[i][1] = fmaf(f.y * q0.from, x[i][1], r[i][1]);
-                r[i][2] = fmaf(f.x * q1.from, x[i][2], r[i][2]);
-                r[i][3] = fmaf(f.y * q1.from, x[i][3], r[i][3]);
+                set_rows(r[i], fma2(mul2(f, both(q0.from)), row_a(x[i]), row_a(r[i])),
+                         fma2(mul2(f, both(q1.from)), row_b(x[i]), row_b(r[i])));
             }
         }
         if (SP > 1) {
@@ -890,9 +884,12 @@ __global__ void __launch_bounds__(256, 1)
             for (int nt = 0; nt < 8; ++nt) {
                 const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
                 const float2 w = fac2(fac, kFacW, sh.tile(nt >> 1), nt & 1, tq);
-                r[nt][0] *= be.x, r[nt][1] *= be.y, r[nt][2] *= be.x, r[nt][3] *= be.y;
-                w0 = max_abs(max_abs(w0, w.x * r[nt][0]), w.y * r[nt][1]);
-                w1 = max_abs(max_abs(w1, w.x * r[nt][2]), w.y * r[nt][3]);
+                scale_cols(r[nt], be);
+                const float2 a = mul2(w, row_a(r[nt])), b = mul2(w, row_b(r[nt]));
+                w0 = max_abs(max_abs(w0, a.x), a.y);
+                w1 = max_abs(max_abs(w1, b.x), b.y);
+                if (!GRAD)
+                    set_rows(r[nt], a, b);  // W U, all that is wanted from here on
             }
         };
         if (GRAD) {
@@ -941,10 +938,8 @@ __global__ void __launch_bounds__(256, 1)
                 for (int u = 0; u < 2; ++u) {
                     const int nt = 2 * i + u;
                     const float2 fp = fac2(fac, kFacP, sh.tile(i), u, tq);
-                    o[nt][0] = fmaf(fp.x * q0.from, x[nt][0], o[nt][0]);
-                    o[nt][1] = fmaf(fp.y * q0.from, x[nt][1], o[nt][1]);
-                    o[nt][2] = fmaf(fp.x * q1.from, x[nt][2], o[nt][2]);
-                    o[nt][3] = fmaf(fp.y * q1.from, x[nt][3], o[nt][3]);
+                    set_rows(o[nt], fma2(mul2(fp, both(q0.from)), row_a(x[nt]), row_a(o[nt])),
+                             fma2(mul2(fp, both(q1.from)), row_b(x[nt]), row_b(o[nt])));
                     if (GRAD) {
                         dots[nt >> 2][2 * (nt & 3)] = o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]);
                         dots[nt >> 2][2 * (nt & 3) + 1] = o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]);
@@ -972,27 +967,24 @@ __global__ void __launch_bounds__(256, 1)
         const Pow2 u1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
         const float g0 = gend * u0.to, g1 = gend * u1.to;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] *= g0, s[nt][1] *= g0;
-            s[nt][2] *= g1, s[nt][3] *= g1;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            scale_rows(s[nt], g0, g1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * kk + u;
-                const float2 w = fac2(fac, kFacW, sh.tile(kk), u, tq);
-                h2_split(w.x * r[nt][0] * u0.to, w.y * r[nt][1] * u0.to, hi[2 * u], lo[2 * u]);
-                h2_split(w.x * r[nt][2] * u1.to, w.y * r[nt][3] * u1.to, hi[2 * u + 1], lo[2 * u + 1]);
+                if (GRAD)
+                    scale_cols(r[nt], fac2(fac, kFacW, sh.tile(kk), u, tq));
+                h2_split(row_a(r[nt]), u0.to, hi[2 * u], lo[2 * u]);
+                h2_split(row_b(r[nt]), u1.to, hi[2 * u + 1], lo[2 * u + 1]);
             }
             rows_update<RB, KK>(s, hi, lo, sK, lane, 16 * sh.tile(kk), d0);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] *= u0.from, s[nt][1] *= u0.from;
-            s[nt][2] *= u1.from, s[nt][3] *= u1.from;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            scale_rows(s[nt], u0.from, u1.from);
         if (!GRAD && out) {
             __syncwarp();
             const int64_t t0 = (int64_t)c * kC;
@@ -1228,10 +1220,10 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             uint32_t hi[4], lo[4], b[4][4];
-            h2_split(ds[2 * kk][0] * p0.to, ds[2 * kk][1] * p0.to, hi[0], lo[0]);
-            h2_split(ds[2 * kk][2] * p1.to, ds[2 * kk][3] * p1.to, hi[1], lo[1]);
-            h2_split(ds[2 * kk + 1][0] * p0.to, ds[2 * kk + 1][1] * p0.to, hi[2], lo[2]);
-            h2_split(ds[2 * kk + 1][2] * p1.to, ds[2 * kk + 1][3] * p1.to, hi[3], lo[3]);
+            h2_split(row_a(ds[2 * kk]), p0.to, hi[0], lo[0]);
+            h2_split(row_b(ds[2 * kk]), p1.to, hi[1], lo[1]);
+            h2_split(row_a(ds[2 * kk + 1]), p0.to, hi[2], lo[2]);
+            h2_split(row_b(ds[2 * kk + 1]), p1.to, hi[3], lo[3]);
             keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + d0 / 16 + kk, lane, hi);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -1241,7 +1233,7 @@ __global__ void __launch_bounds__(256, 1)
         }
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt)
-            u[nt][0] *= p0.from, u[nt][1] *= p0.from, u[nt][2] *= p1.from, u[nt][3] *= p1.from;
+            scale_rows(u[nt], p0.from, p1.from);
         if (SP > 1)
             sh.put(0, pair(u, 2), pair(u, 3));
         // dO^T P on the own tiles: the rows of P carry powers of two, which go to dO
@@ -1254,8 +1246,9 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 fp = fac2(fac, kFacP, j, h, tq);
-                q_0 = max_abs(max_abs(q_0, fp.x * lo_f(w[2 * h])), fp.y * hi_f(w[2 * h]));
-                q_1 = max_abs(max_abs(q_1, fp.x * lo_f(w[2 * h + 1])), fp.y * hi_f(w[2 * h + 1]));
+                const float2 a = mul2(fp, bf2(w[2 * h])), b = mul2(fp, bf2(w[2 * h + 1]));
+                q_0 = max_abs(max_abs(q_0, a.x), a.y);
+                q_1 = max_abs(max_abs(q_1, b.x), b.y);
             }
         }
         const Pow2 q0 = pow2_for(quad_max(q_0)), q1 = pow2_for(quad_max(q_1));
@@ -1266,8 +1259,9 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 fp = fac2(fac, kFacP, kk, h, tq);
-                a[2 * h] = h2(fp.x * lo_f(w[2 * h]) * q0.to, fp.y * hi_f(w[2 * h]) * q0.to);
-                a[2 * h + 1] = h2(fp.x * lo_f(w[2 * h + 1]) * q1.to, fp.y * hi_f(w[2 * h + 1]) * q1.to);
+                const float2 x0 = mul2(mul2(fp, bf2(w[2 * h])), both(q0.to));
+                const float2 x1 = mul2(mul2(fp, bf2(w[2 * h + 1])), both(q1.to));
+                a[2 * h] = h2(x0.x, x0.y), a[2 * h + 1] = h2(x1.x, x1.y);
             }
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
@@ -1288,24 +1282,22 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int i = 0; i < 2 * OWN; ++i) {  // dU
             const float2 w = fac2(fac, kFacW, sh.tile(i >> 1), i & 1, tq);
-            u[i][0] = fmaf(w.x, u[i][0], q0.from * x[i][0]);
-            u[i][1] = fmaf(w.y, u[i][1], q0.from * x[i][1]);
-            u[i][2] = fmaf(w.x, u[i][2], q1.from * x[i][2]);
-            u[i][3] = fmaf(w.y, u[i][3], q1.from * x[i][3]);
+            set_rows(u[i], fma2(w, row_a(u[i]), mul2(row_a(x[i]), both(q0.from))),
+                     fma2(w, row_b(u[i]), mul2(row_b(x[i]), both(q1.from))));
         }
         if (SP > 1) {
             sh.put(1, pair(u, 0), pair(u, 1));
             sh.sync();
             sh.template get<false>(1, pair(u, 2), pair(u, 3));
         }
-        // F^T z on the own tiles; F's row scales go to z
-        float z0 = 0.f, z1 = 0.f;
+        // F^T z on the own tiles (all of F is under one power of two)
+        float z0 = 0.f, z1 = 0.f, z[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
             const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
-            const float2 ff = fac2(fac, kFacF, sh.tile(nt >> 1), nt & 1, tq);
-            z0 = max_abs(max_abs(z0, be.x * ff.x * u[nt][0]), be.y * ff.y * u[nt][1]);
-            z1 = max_abs(max_abs(z1, be.x * ff.x * u[nt][2]), be.y * ff.y * u[nt][3]);
+            set_rows(z[nt], mul2(be, row_a(u[nt])), mul2(be, row_b(u[nt])));
+            z0 = max_abs(max_abs(z0, z[nt][0]), z[nt][1]);
+            z1 = max_abs(max_abs(z1, z[nt][2]), z[nt][3]);
         }
         const Pow2 y0 = pow2_for(quad_max(z0)), y1 = pow2_for(quad_max(z1));
         clear(x);
@@ -1314,12 +1306,8 @@ __global__ void __launch_bounds__(256, 1)
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int nt = 2 * kk + h;
-                const float2 be = fac2(fac, kFacB, sh.tile(kk), h, tq);
-                const float2 ff = fac2(fac, kFacF, sh.tile(kk), h, tq);
-                const float fx = be.x * ff.x, fy = be.y * ff.y;
-                h2_split(fx * u[nt][0] * y0.to, fy * u[nt][1] * y0.to, hi[2 * h], lo[2 * h]);
-                h2_split(fx * u[nt][2] * y1.to, fy * u[nt][3] * y1.to, hi[2 * h + 1], lo[2 * h + 1]);
+                h2_split(row_a(z[2 * kk + h]), y0.to, hi[2 * h], lo[2 * h]);
+                h2_split(row_b(z[2 * kk + h]), y1.to, hi[2 * h + 1], lo[2 * h + 1]);
             }
             three_products<OWN>(
                 x, hi, lo, [&](int i) { return sh.tile(i) <= sh.tile(kk); },
@@ -1330,6 +1318,7 @@ __global__ void __launch_bounds__(256, 1)
         cp_wait<0>();
         __syncwarp();
         // Y, the dots, dV on the own tiles
+        const float f0 = y0.from * fac[kFacF * kC], f1 = y1.from * fac[kFacF * kC];
         float bsum[OWN / 2][8], vsum[OWN / 2][8];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
@@ -1339,10 +1328,8 @@ __global__ void __launch_bounds__(256, 1)
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * i + h;
                 const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
-                u[nt][0] = fmaf(y0.from, x[nt][0], u[nt][0]);
-                u[nt][1] = fmaf(y0.from, x[nt][1], u[nt][1]);
-                u[nt][2] = fmaf(y1.from, x[nt][2], u[nt][2]);
-                u[nt][3] = fmaf(y1.from, x[nt][3], u[nt][3]);
+                set_rows(u[nt], fma2(both(f0), row_a(x[nt]), row_a(u[nt])),
+                         fma2(both(f1), row_b(x[nt]), row_b(u[nt])));
                 const uint32_t* eh =
                     reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
                 const uint32_t* el = eh + kC * 8;
@@ -1427,9 +1414,10 @@ __global__ void __launch_bounds__(256, 1)
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * j + h;
                 const float2 fo = fac2(fac, kFacO, sh.tile(j), h, tq), fa = fac2(fac, kFacA, sh.tile(j), h, tq);
-                w0 = max_abs(max_abs(w0, fo.x * lo_f(w[2 * h])), fo.y * hi_f(w[2 * h]));
-                w1 = max_abs(max_abs(w1, fo.x * lo_f(w[2 * h + 1])), fo.y * hi_f(w[2 * h + 1]));
-                u[nt][0] *= -fa.x, u[nt][1] *= -fa.y, u[nt][2] *= -fa.x, u[nt][3] *= -fa.y;
+                const float2 a = mul2(fo, bf2(w[2 * h])), b = mul2(fo, bf2(w[2 * h + 1]));
+                w0 = max_abs(max_abs(w0, a.x), a.y);
+                w1 = max_abs(max_abs(w1, b.x), b.y);
+                scale_cols(u[nt], make_float2(-fa.x, -fa.y));
                 w0 = max_abs(max_abs(w0, u[nt][0]), u[nt][1]);
                 w1 = max_abs(max_abs(w1, u[nt][2]), u[nt][3]);
             }
@@ -1439,10 +1427,8 @@ __global__ void __launch_bounds__(256, 1)
         const Pow2 r1 = pow2_for(fmaxf(quad_max(w1), m1 * gend * 0.00390625f));
         const float g0 = gend * r0.to, g1 = gend * r1.to;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            ds[nt][0] *= g0, ds[nt][1] *= g0;
-            ds[nt][2] *= g1, ds[nt][3] *= g1;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            scale_rows(ds[nt], g0, g1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             uint32_t w[4], hi[4], lo[4];
@@ -1450,24 +1436,21 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 fo = fac2(fac, kFacO, sh.tile(kk), h, tq);
-                h2_split(fo.x * lo_f(w[2 * h]) * r0.to, fo.y * hi_f(w[2 * h]) * r0.to, hi[2 * h], lo[2 * h]);
-                h2_split(fo.x * lo_f(w[2 * h + 1]) * r1.to, fo.y * hi_f(w[2 * h + 1]) * r1.to, hi[2 * h + 1],
-                         lo[2 * h + 1]);
+                h2_split(mul2(fo, bf2(w[2 * h])), r0.to, hi[2 * h], lo[2 * h]);
+                h2_split(mul2(fo, bf2(w[2 * h + 1])), r1.to, hi[2 * h + 1], lo[2 * h + 1]);
             }
             rows_update<RB, KK>(ds, hi, lo, sQ, lane, 16 * sh.tile(kk), d0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * kk + h;
-                h2_split(u[nt][0] * r0.to, u[nt][1] * r0.to, hi[2 * h], lo[2 * h]);
-                h2_split(u[nt][2] * r1.to, u[nt][3] * r1.to, hi[2 * h + 1], lo[2 * h + 1]);
+                h2_split(row_a(u[nt]), r0.to, hi[2 * h], lo[2 * h]);
+                h2_split(row_b(u[nt]), r1.to, hi[2 * h + 1], lo[2 * h + 1]);
             }
             rows_update<RB, KK>(ds, hi, lo, sK, lane, 16 * sh.tile(kk), d0);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            ds[nt][0] *= r0.from, ds[nt][1] *= r0.from;
-            ds[nt][2] *= r1.from, ds[nt][3] *= r1.from;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            scale_rows(ds[nt], r0.from, r1.from);
         if (gated && c > 0)
             dot_state(c, sc0, sc1);
         if (it + 1 < nchunk)

@@ -42,6 +42,55 @@ __device__ __forceinline__ void h2_split(float a, float b, uint32_t& hi, uint32_
     lo = h2(a - f.x, b - f.y);
 }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The two rows of a C tile: row g (registers 0, 1), row g + 8 (2, 3)
+__device__ __forceinline__ float2 row_a(const float (&x)[4]) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ float2 row_b(const float (&x)[4]) { return make_float2(x[2], x[3]); }
+__device__ __forceinline__ void set_rows(float (&x)[4], float2 a, float2 b)
+{
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+// x times a factor for each row, or for each column
+__device__ __forceinline__ void scale_rows(float (&x)[4], float a, float b)
+{
+    set_rows(x, mul2(row_a(x), both(a)), mul2(row_b(x), both(b)));
+}
+__device__ __forceinline__ void scale_cols(float (&x)[4], float2 f)
+{
+    set_rows(x, mul2(row_a(x), f), mul2(row_b(x), f));
+}
+
+// x times a power of two -> packed fp16 parts
+__device__ __forceinline__ void h2_split(float2 x, float to, uint32_t& hi, uint32_t& lo)
+{
+    const float2 y = mul2(x, both(to));
+    const __half2 h = __floats2half2_rn(y.x, y.y);
+    const float2 f = __half22float2(h);
+    const float2 r = fma2(f, both(-1.0f), y);  // exact
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = h2(r.x, r.y);
+}
+
 // The power of two that brings m (>= 0) to [2^8, 2^9), and its inverse.  Zero
 // and numbers under 2^-118 get the largest scale, 2^126: an operand's own factors
 // are multiplied in before it, so that no product of scales overflows.
