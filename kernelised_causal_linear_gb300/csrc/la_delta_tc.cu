@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 
 // ------------------------------------------------------------ k_delta_chain --
 // Slices of 16 value columns; the tiles of a chunk are shared by a CTA's slices and
-// arrive by bulk copies kStages chunks ahead; V comes by cp.async one chunk ahead,
+// arrive by bulk copies a ring of stages ahead; V comes by cp.async one chunk ahead,
 // and outputs leave through the slice's own tile, turned back to token-major by
 // stmatrix.
 //
@@ -451,17 +451,25 @@ __global__ void __launch_bounds__(kPrepThreads)
 // memory three times a chunk.  A warp's products follow one another, each waiting
 // for the last: with a slice per warp a chunk is 7100 cycles at d = 128 of which
 // the tensor core works 3100, so two warps shorten it where there are SMs to spare.
-constexpr int kStages = 2;
+//
+// With two warps on a sub-partition (SP = 1, eight warps) no barrier spans the CTA
+// inside the loop: the warp that is last to finish with a stage asks for the chunk
+// that takes its place, so warps drift apart and one's products run under another's
+// arithmetic (512 heads of 2011 tokens: 734 us in step, 690 us adrift).  Alone on
+// their sub-partitions (SP = 2) warps only lose by it: in step they share what the
+// instruction cache fetches (reverse chain, 32 heads of 8192 tokens: 529 us in step,
+// 595 us adrift).
 constexpr uint32_t kWaitPolls = 1u << 22;
 constexpr int kXch = 2048;  // bytes of one warp's exchange buffer: 16 floats per lane
 
 template <int D, bool GRAD, int SP>
 struct ChainSmem {
+    static constexpr int stages = SP == 1 && !GRAD ? 3 : 2;  // what fits at d = 128
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<GRAD>();
-    static constexpr int v = kStages * stage;
+    static constexpr int v = stages * stage;
     // per slice: V twice, O (GRAD: dO), and for each of two warps four exchange buffers
     static constexpr int x = 3 * kC * 32, per_slice = x + (SP > 1 ? SP * 4 * kXch : 0);
-    static int bytes(int W) { return v + W * per_slice + 64; }
+    static int bytes(int W) { return v + W * per_slice + 128; }
 };
 
 // What the forward pass of a gradient keeps per chunk, in the fragments' own
@@ -513,6 +521,53 @@ __device__ __forceinline__ float sum8(const float (&y)[8], int lane)
         b[i] = (lane & 8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? a[i] : a[i + 2], 8);
     return (lane & 4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? b[0] : b[1], 4);
 }
+
+// The ring of stages: barriers for filled and for read, and how many warps have read
+// (STEP: a barrier of the CTA in their place).  A warp's reads are ordered before the refill by its arrival and the refiller's
+// (satisfied) wait on the same barrier; the count only tells who is last.  A fence
+// instead would also wait for the chunk's stores to global memory.
+template <int STAGES, bool STEP>
+struct Ring {
+    uint64_t *full, *read;
+    unsigned* done;
+    unsigned warps;
+    bool ok;  // false once a wait has run out: nothing is waited for any more
+    __device__ __forceinline__ Ring(void* at, unsigned w)
+        : full(static_cast<uint64_t*>(at)), read(full + STAGES), done(reinterpret_cast<unsigned*>(read + STAGES)),
+          warps(w), ok(true)
+    {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < STAGES; ++i) {
+                sm100::mbar_init(full + i, 1);
+                sm100::mbar_init(read + i, w);
+                done[i] = 0;
+            }
+            sm100::fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void wait(int i)
+    {
+        if (ok)
+            ok = __all_sync(0xffffffffu, sm100::mbar_wait(full + i % STAGES, (i / STAGES) & 1, kWaitPolls));
+    }
+    // this warp is done with chunk i; true in one thread once all are
+    __device__ __forceinline__ bool last(int i)
+    {
+        if (STEP) {
+            __syncthreads();
+            return threadIdx.x == 0;
+        }
+        __syncwarp();
+        if ((threadIdx.x & 31) != 0)
+            return false;
+        sm100::mbar_arrive(read + i % STAGES);
+        if (atomicAdd_block(done + i % STAGES, 1u) != warps - 1)
+            return false;
+        done[i % STAGES] = 0;
+        return sm100::mbar_wait(read + i % STAGES, (i / STAGES) & 1, kWaitPolls);
+    }
+};
 
 // One warp's place in a slice shared by SP warps.  Token tiles (16 tokens) are
 // held in local order: this warp's own first, then the other's.
@@ -658,20 +713,14 @@ __global__ void __launch_bounds__(256, 1)
     sh.mine = smem + my + SM::x + sh.half * 4 * kXch;
     sh.other = smem + my + SM::x + (SP - 1 - sh.half) * 4 * kXch;
     const uint32_t sv = base + my, so = sv + 2 * kC * 32;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::v + W * SM::per_slice);
+    Ring<SM::stages, (SP > 1)> ring(smem + SM::v + W * SM::per_slice, blockDim.x >> 5);
     const unsigned char* row_src = rows + kh * nchunk * (int64_t)(2 * row_image<D>());
     const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)kBlob;
     const int d0 = sh.half * (D / SP);  // first state row of this warp
 
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i)
-            sm100::mbar_init(full + i, 1);
-        sm100::fence_mbar_init();
-    }
-    __syncthreads();
     auto load_stage = [&](int c) {
-        const uint32_t dst = base + (c % kStages) * SM::stage;
-        uint64_t* bar = full + c % kStages;
+        const uint32_t dst = base + (c % SM::stages) * SM::stage;
+        uint64_t* bar = ring.full + c % SM::stages;
         sm100::mbar_arrive_expect_tx(bar, SM::stage);
         delta::bulk_load(dst, row_src + c * (int64_t)(2 * row_image<D>()), 2 * row_image<D>(), bar);
         delta::bulk_load(dst + 2 * row_image<D>(), blob_src + c * (int64_t)kBlob, kBlob, bar);
@@ -687,7 +736,7 @@ __global__ void __launch_bounds__(256, 1)
         }
     };
     if (tid == 0)
-        for (int c = 0; c < kStages && c < nchunk; ++c)
+        for (int c = 0; c < SM::stages && c < nchunk; ++c)
             load_stage(c);
     load_cols(sv, v, 0);
     cp_commit();
@@ -723,13 +772,11 @@ __global__ void __launch_bounds__(256, 1)
         }
     };
 
-    bool ok = sm100::mbar_wait(full, 0, kWaitPolls);
-    ok = __syncthreads_and(ok);
-    int c = 0;
-    for (; ok && c < nchunk; ++c) {
-        const uint32_t st = base + (c % kStages) * SM::stage;
+    ring.wait(0);
+    for (int c = 0; c < nchunk; ++c) {
+        const uint32_t st = base + (c % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
-        const float* fac = reinterpret_cast<const float*>(smem + (c % kStages) * SM::stage +
+        const float* fac = reinterpret_cast<const float*>(smem + (c % SM::stages) * SM::stage +
                                                           2 * row_image<D>() + fac_at<GRAD>());
         if (GRAD) {  // dO, wanted at the end of the chunk
             load_cols(so, dout, c);
@@ -996,21 +1043,16 @@ __global__ void __launch_bounds__(256, 1)
                         *reinterpret_cast<const uint4*>(smem + (so - base) + tile_off<32>(t, p));
             }
         }
+        if (ring.last(c) && c + SM::stages < nchunk)
+            load_stage(c + SM::stages);
+        // here and not at the chunk's start: what is issued there (copies, addresses)
+        // then shares a stretch without branches with the first products
         if (c + 1 < nchunk)
-            ok = sm100::mbar_wait(full + (c + 1) % kStages, ((c + 1) / kStages) & 1, kWaitPolls);
-        ok = __syncthreads_and(ok);  // every warp is done with the stage, and has the next
-        if (ok && tid == 0 && c + kStages < nchunk)
-            load_stage(c + kStages);
+            ring.wait(c + 1);
     }
     cp_wait<0>();
-    if (!ok) {  // a copy never arrived: see the others home, report, leave
-        if (tid == 0) {
-            for (int i = c; i < c + kStages && i < nchunk; ++i)
-                sm100::mbar_wait(full + i % kStages, (i / kStages) & 1, kWaitPolls);
-            set_status(status, LA_ERR_TIMEOUT);
-        }
-        return;
-    }
+    if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
+        set_status(status, LA_ERR_TIMEOUT);
     if (GRAD) {  // the final state, for <S1, dS1> of the last chunk
         float m0, m1;
         row_max(m0, m1);
@@ -1046,13 +1088,14 @@ __global__ void __launch_bounds__(256, 1)
 // <S0, dS0> (which is <S1, dS1> of the chunk before).
 template <int D, int SP>
 struct RevSmem {
+    static constexpr int stages = 2;
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<true>();
-    static constexpr int slice0 = kStages * stage;
+    static constexpr int slice0 = stages * stage;
     // per slice: dO twice, V (then dV), E hi and lo, three exchange buffers for each
     // of two warps
     static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, x = e + 2 * kC * 32,
                          per_slice = x + (SP > 1 ? SP * 3 * kXch : 0);
-    static int bytes(int W) { return slice0 + W * per_slice + 64; }
+    static int bytes(int W) { return slice0 + W * per_slice + 128; }
 };
 
 template <int D, int SP>
@@ -1080,21 +1123,15 @@ __global__ void __launch_bounds__(256, 1)
     sh.mine = smem + mine + SM::x + sh.half * 3 * kXch;
     sh.other = smem + mine + SM::x + (SP - 1 - sh.half) * 3 * kXch;
     const uint32_t sdo = base + mine + SM::dO, sv = base + mine + SM::v;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::slice0 + W * SM::per_slice);
+    Ring<SM::stages, (SP > 1)> ring(smem + SM::slice0 + W * SM::per_slice, blockDim.x >> 5);
     const unsigned char* row_src = rows + kh * nchunk * (int64_t)(2 * row_image<D>());
     const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)kBlob;
     const int d0 = sh.half * (D / SP);
 
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i)
-            sm100::mbar_init(full + i, 1);
-        sm100::fence_mbar_init();
-    }
-    __syncthreads();
     auto load_stage = [&](int it) {
         const int64_t c = nchunk - 1 - it;
-        const uint32_t dst = base + (it % kStages) * SM::stage;
-        uint64_t* bar = full + it % kStages;
+        const uint32_t dst = base + (it % SM::stages) * SM::stage;
+        uint64_t* bar = ring.full + it % SM::stages;
         sm100::mbar_arrive_expect_tx(bar, SM::stage);
         delta::bulk_load(dst, row_src + c * (2 * row_image<D>()), 2 * row_image<D>(), bar);
         delta::bulk_load(dst + 2 * row_image<D>(), blob_src + c * kBlob, kBlob, bar);
@@ -1163,7 +1200,7 @@ __global__ void __launch_bounds__(256, 1)
     };
 
     if (tid == 0)
-        for (int i = 0; i < kStages && i < nchunk; ++i)
+        for (int i = 0; i < SM::stages && i < nchunk; ++i)
             load_stage(i);
     load_cols(sdo + ((nchunk - 1) & 1) * kC * 32, dout, nchunk - 1);
     cp_commit();
@@ -1173,32 +1210,31 @@ __global__ void __launch_bounds__(256, 1)
         for (int e = 0; e < 4; ++e)
             ds[nt][e] =
                 dS_out ? dS_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
-    cp_wait<0>();
-    __syncwarp();
     if (gated)
         dot_state(nchunk, state_scale(nchunk, g), state_scale(nchunk, g + 8));
-
-    bool ok = sm100::mbar_wait(full, 0, kWaitPolls);
-    ok = __syncthreads_and(ok);
-    int it = 0;
-    for (; ok && it < nchunk; ++it) {
+    cp_wait<0>();
+    sh.sync();
+    ring.wait(0);
+    for (int it = 0; it < nchunk; ++it) {
         const int c = nchunk - 1 - it;
-        const uint32_t st = base + (it % kStages) * SM::stage;
+        const uint32_t st = base + (it % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
-        const float* fac = reinterpret_cast<const float*>(smem + (it % kStages) * SM::stage +
+        const float* fac = reinterpret_cast<const float*>(smem + (it % SM::stages) * SM::stage +
                                                           2 * row_image<D>() + fac_at<true>());
         const uint32_t tdo = sdo + (c & 1) * kC * 32;
-        // this chunk's V, E and S, wanted from the middle on, and the next dO
+        // this chunk's V, E and S, wanted from the middle on; the next dO, each warp its
+        // token tiles, which both await before they meet at the chunk's end
         load_cols(sv, v, c);
         load_E(c);
+        cp_commit();
+        if (c > 0)
+            load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
+        cp_commit();
         float sc0 = 0.f, sc1 = 0.f;
         if (gated && c > 0) {
             ask_state(c);
             sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
         }
-        if (c > 0)
-            load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
-        cp_commit();
         const float* se = kept.sE + (bh * nchunk + c) * DV + col0;
         const float se0 = se[g], se1 = se[g + 8];
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
@@ -1315,7 +1351,7 @@ __global__ void __launch_bounds__(256, 1)
                     ldsm4t(b, addr_bt<128>(sF + part * kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
                 });
         }
-        cp_wait<0>();
+        cp_wait<1>();  // V, E
         __syncwarp();
         // Y, the dots, dV on the own tiles
         const float f0 = y0.from * fac[kFacF * kC], f1 = y1.from * fac[kFacF * kC];
@@ -1351,13 +1387,11 @@ __global__ void __launch_bounds__(256, 1)
             if (gated)
                 sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
         }
-        if (SP > 1) {
+        if (SP > 1)
             sh.put(2, pair(u, 0), pair(u, 1));
-            sh.sync();
+        sh.sync();
+        if (SP > 1)
             sh.template get<false>(2, pair(u, 2), pair(u, 3));
-        } else {
-            __syncwarp();
-        }
         // dV leaves as bf16 (V's tile is read) and is kept as scaled fp16
         float v0 = 0.f, v1 = 0.f;
 #pragma unroll
@@ -1453,21 +1487,16 @@ __global__ void __launch_bounds__(256, 1)
             scale_rows(ds[nt], r0.from, r1.from);
         if (gated && c > 0)
             dot_state(c, sc0, sc1);
+        cp_wait<0>();
+        sh.sync();
+        if (ring.last(it) && it + SM::stages < nchunk)
+            load_stage(it + SM::stages);
         if (it + 1 < nchunk)
-            ok = sm100::mbar_wait(full + (it + 1) % kStages, ((it + 1) / kStages) & 1, kWaitPolls);
-        ok = __syncthreads_and(ok);
-        if (ok && tid == 0 && it + kStages < nchunk)
-            load_stage(it + kStages);
+            ring.wait(it + 1);
     }
     cp_wait<0>();
-    if (!ok) {  // a copy never arrived: see the others home, report, leave
-        if (tid == 0) {
-            for (int i = it; i < it + kStages && i < nchunk; ++i)
-                sm100::mbar_wait(full + i % kStages, (i / kStages) & 1, kWaitPolls);
-            set_status(status, LA_ERR_TIMEOUT);
-        }
-        return;
-    }
+    if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
+        set_status(status, LA_ERR_TIMEOUT);
     if (dS0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
