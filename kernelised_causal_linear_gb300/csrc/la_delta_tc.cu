@@ -686,7 +686,9 @@ __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(lo_f(w), hi_f(w)); }
 
-template <int D, bool GRAD, int SP>
+// READS: outputs are wanted (a branch on the pointer instead cuts every stretch of
+// products in two)
+template <int D, bool GRAD, int SP, bool READS>
 __global__ void __launch_bounds__(256, 1)
     k_delta_chain(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                   const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ out,
@@ -699,7 +701,6 @@ __global__ void __launch_bounds__(256, 1)
     constexpr int RB = 2 * D;                    // bytes per row
     constexpr int NT = D / 8 / SP, KK = NT / 2;  // n tiles of this warp's part of S^T; its 16-steps
     constexpr int OWN = Share<SP>::own;
-    const bool reads = GRAD || out;  // o is wanted
     const int tid = threadIdx.x, lane = tid & 31, W = blockDim.x / (32 * SP);
     const int g = lane >> 2, tq = lane & 3;
     Share<SP> sh;
@@ -806,13 +807,13 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     ldsm4(bk[i], addr_b<RB>(sK, lane, 16 * sh.tile(j + i), d0 + 16 * kk));
-                if (reads) {
+                if (READS) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         ldsm4(bq[i], addr_b<RB>(sQ, lane, 16 * sh.tile(j + i), d0 + 16 * kk));
                 }
                 mma_tiles<2>(r + 2 * j, hi, bk);
-                if (reads)
+                if (READS)
                     mma_tiles<2>(o + 2 * j, hi, bq);
                 mma_tiles<2>(r + 2 * j, lo, bk);
                 if (GRAD)  // o enters an fp32 gradient
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
             scale_rows(r[nt], p0.from, p1.from);
-            if (reads)
+            if (READS)
                 scale_rows(o[nt], p0.from, p1.from);
         }
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
@@ -832,11 +833,11 @@ __global__ void __launch_bounds__(256, 1)
         };
         if (SP > 1) {
             sh.put(0, pair(r, 2), pair(r, 3));
-            if (reads)
+            if (READS)
                 sh.put(1, pair(o, 2), pair(o, 3));
             sh.sync();
             sh.template get<true>(0, pair(r, 0), pair(r, 1));
-            if (reads)
+            if (READS)
                 sh.template get<true>(1, pair(o, 0), pair(o, 1));
         }
         cp_wait<GRAD ? 2 : 1>();  // V
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(256, 1)
                 const float2 minus = make_float2(-a.x, -a.y);
                 set_rows(r[nt], fma2(minus, row_a(r[nt]), bf2(w[2 * u])), fma2(minus, row_b(r[nt]), bf2(w[2 * u + 1])));
                 set_rows(z[nt], mul2(be, row_a(r[nt])), mul2(be, row_b(r[nt])));
-                if (reads)
+                if (READS)
                     scale_cols(o[nt], fac2(fac, kFacO, sh.tile(i), u, tq));
             }
         }
@@ -947,7 +948,7 @@ __global__ void __launch_bounds__(256, 1)
         // set the scale of its row.  For the output alone one fp16 part of each is
         // enough (2^-12 of a term, under the output's own rounding); a gradient
         // takes both, and P without beta and U for E, since it needs P itself
-        if (reads) {
+        if (READS) {
             const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
             clear(x);
 #pragma unroll
@@ -1032,7 +1033,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             scale_rows(s[nt], u0.from, u1.from);
-        if (!GRAD && out) {
+        if (!GRAD && READS) {
             __syncwarp();
             const int64_t t0 = (int64_t)c * kC;
 #pragma unroll
@@ -2048,15 +2049,15 @@ cudaError_t allow_smem(K kern, int bytes)
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int D, bool GRAD, int SP>
+template <int D, bool GRAD, int SP, bool READS>
 cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
                          const Kept& kept)
 {
     const int smem = ChainSmem<D, GRAD, SP>::bytes(W);
-    const cudaError_t e = allow_smem(k_delta_chain<D, GRAD, SP>, smem);
+    const cudaError_t e = allow_smem(k_delta_chain<D, GRAD, SP, READS>, smem);
     if (e != cudaSuccess)
         return e;
-    k_delta_chain<D, GRAD, SP><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+    k_delta_chain<D, GRAD, SP, READS><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
         rows, blobs, static_cast<const __nv_bfloat16*>(a.v), GRAD ? nullptr : static_cast<__nv_bfloat16*>(a.out), a.S0,
         GRAD ? nullptr : a.S_out, a.N, n, (int)a.H, (int)a.Hk, a.dv, static_cast<const __nv_bfloat16*>(a.dout), kept,
         a.status);
@@ -2099,8 +2100,12 @@ cudaError_t run_forward(const DeltaArgs& a)
     if (e != cudaSuccess)
         return e;
     const Cut cut = cut_of(a);
-    return cut.SP == 2 ? launch_chain<D, false, 2>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{})
-                       : launch_chain<D, false, 1>(a, cut.W, ws + l.rows, ws + l.blobs, n, Kept{});
+    const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
+    if (a.out)
+        return cut.SP == 2 ? launch_chain<D, false, 2, true>(a, cut.W, rows, blobs, n, Kept{})
+                           : launch_chain<D, false, 1, true>(a, cut.W, rows, blobs, n, Kept{});
+    return cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, n, Kept{})
+                       : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, n, Kept{});
 }
 
 template <int D, int DV>
@@ -2127,8 +2132,8 @@ cudaError_t run_backward(const DeltaArgs& a)
         return e;
     const Cut cut = cut_of(a);
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
-    e = cut.SP == 2 ? launch_chain<D, true, 2>(a, cut.W, rows, blobs, n, kept)
-                    : launch_chain<D, true, 1>(a, cut.W, rows, blobs, n, kept);
+    e = cut.SP == 2 ? launch_chain<D, true, 2, true>(a, cut.W, rows, blobs, n, kept)
+                    : launch_chain<D, true, 1, true>(a, cut.W, rows, blobs, n, kept);
     if (e == cudaSuccess)
         e = cut.SP == 2 ? launch_rev<D, 2>(a, cut.W, rows, blobs, n, kept)
                         : launch_rev<D, 1>(a, cut.W, rows, blobs, n, kept);
