@@ -783,8 +783,7 @@ __global__ void __launch_bounds__(256, 1)
             load_cols(so, dout, c);
             cp_commit();
         }
-        if (c + 1 < nchunk)
-            load_cols(sv + ((c + 1) & 1) * kC * 32, v, c + 1);
+        load_cols(sv + ((c + 1) & 1) * kC * 32, v, c + 1);  // nothing past the last chunk
         cp_commit();
 
         // S^T K^T and S^T Q^T over this warp's rows of S, split on the way
@@ -1099,13 +1098,13 @@ struct RevSmem {
     static int bytes(int W) { return slice0 + W * per_slice + 128; }
 };
 
-template <int D, int SP>
+template <int D, int SP, bool GATED>
 __global__ void __launch_bounds__(256, 1)
     k_delta_rev(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
                 const float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dv,
-                float* __restrict__ dS0, int64_t N, int nchunk, int H, int Hk, int DV, int gated,
-                Kept kept, int* status)
+                float* __restrict__ dS0, int64_t N, int nchunk, int H, int Hk, int DV, Kept kept,
+                int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = RevSmem<D, SP>;
@@ -1138,11 +1137,11 @@ __global__ void __launch_bounds__(256, 1)
         delta::bulk_load(dst + 2 * row_image<D>(), blob_src + c * kBlob, kBlob, bar);
     };
     auto load_cols = [&](uint32_t dst, const __nv_bfloat16* src, int c) {
-        const int64_t t0 = (int64_t)c * kC;
+        const int64_t t0 = (int64_t)c * kC;  // c = -1: nothing
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
-            const bool live = t0 + t < N;
+            const bool live = t0 >= 0 && t0 + t < N;
             cp16(dst + tile_off<32>(t, p), src + (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8, live);
         }
     };
@@ -1189,7 +1188,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) {
+        if (lane == 0 && c > 0) {
             float* cd = kept.cd + (bh * (DV / 16) + slice) * 2 * nchunk + c - 1;
             cd[sh.half * nchunk] = x;
             if (SP == 1)
@@ -1211,7 +1210,7 @@ __global__ void __launch_bounds__(256, 1)
         for (int e = 0; e < 4; ++e)
             ds[nt][e] =
                 dS_out ? dS_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
-    if (gated)
+    if (GATED)
         dot_state(nchunk, state_scale(nchunk, g), state_scale(nchunk, g + 8));
     cp_wait<0>();
     sh.sync();
@@ -1228,11 +1227,10 @@ __global__ void __launch_bounds__(256, 1)
         load_cols(sv, v, c);
         load_E(c);
         cp_commit();
-        if (c > 0)
-            load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
+        load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
         cp_commit();
         float sc0 = 0.f, sc1 = 0.f;
-        if (gated && c > 0) {
+        if (GATED) {
             ask_state(c);
             sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
         }
@@ -1385,7 +1383,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int part = 0; part < OWN / 2; ++part) {
             sh.store_sums(kept.bb + (bh * (DV / 16) + slice) * N, bsum[part], part, (int64_t)c * kC, N);
-            if (gated)
+            if (GATED)
                 sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
         }
         if (SP > 1)
@@ -1486,7 +1484,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             scale_rows(ds[nt], r0.from, r1.from);
-        if (gated && c > 0)
+        if (GATED)
             dot_state(c, sc0, sc1);
         cp_wait<0>();
         sh.sync();
@@ -2065,18 +2063,17 @@ cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, c
     return cudaGetLastError();
 }
 
-template <int D, int SP>
+template <int D, int SP, bool GATED>
 cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
                        const Kept& kept)
 {
     const int smem = RevSmem<D, SP>::bytes(W);
-    const cudaError_t e = allow_smem(k_delta_rev<D, SP>, smem);
+    const cudaError_t e = allow_smem(k_delta_rev<D, SP, GATED>, smem);
     if (e != cudaSuccess)
         return e;
-    k_delta_rev<D, SP><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+    k_delta_rev<D, SP, GATED><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
         rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
-        static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, n, (int)a.H, (int)a.Hk, a.dv, a.log_alpha != nullptr, kept,
-        a.status);
+        static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, n, (int)a.H, (int)a.Hk, a.dv, kept, a.status);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -2135,8 +2132,10 @@ cudaError_t run_backward(const DeltaArgs& a)
     e = cut.SP == 2 ? launch_chain<D, true, 2, true>(a, cut.W, rows, blobs, n, kept)
                     : launch_chain<D, true, 1, true>(a, cut.W, rows, blobs, n, kept);
     if (e == cudaSuccess)
-        e = cut.SP == 2 ? launch_rev<D, 2>(a, cut.W, rows, blobs, n, kept)
-                        : launch_rev<D, 1>(a, cut.W, rows, blobs, n, kept);
+        e = cut.SP == 2 ? a.log_alpha ? launch_rev<D, 2, true>(a, cut.W, rows, blobs, n, kept)
+                                      : launch_rev<D, 2, false>(a, cut.W, rows, blobs, n, kept)
+            : a.log_alpha ? launch_rev<D, 1, true>(a, cut.W, rows, blobs, n, kept)
+                          : launch_rev<D, 1, false>(a, cut.W, rows, blobs, n, kept);
     if (e != cudaSuccess)
         return e;
     const int64_t items = a.B * a.Hk * n;
