@@ -1536,7 +1536,7 @@ struct DqkSmem {
     static constexpr int E = 0, dV = kC * DV * 2, dO = 2 * kC * DV * 2, fac = 3 * kC * DV * 2,
                          cols = fac + kGradFactors * kC * 4, step = cols + 6 * DV * 4;
     static constexpr int S = 2 * step, dS = S + D * DV * 2, K = dS + D * DV * 2, Q = K + row_image<D>(),
-                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + (3 * kC + 8 * 32) * 4,
+                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + (4 * kC + 8 * 32) * 4,
                          bytes = bar + 64;
     static_assert(bytes <= 232448, "shared memory");
 };
@@ -1590,7 +1590,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     float* sdo = reinterpret_cast<float*>(smem + SM::vec);  // dO's row scales
     float* eg = sdo + kC;                                   // e^G
     float* ege = eg + kC;                                   // e^{G_C - G}
-    float* prow = ege + kC + (warp >> 1) * 32;              // [half][16 rows], the two warps' own
+    float* cd = ege + kC;                                   // decay from a token to its tile's end
+    float* prow = cd + kC + (warp >> 1) * 32;               // [half][16 rows], the two warps' own
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bar);  // token planes (2), states, row images
     const int per = H / Hk;
     const bool role_k = warp >= 8;
@@ -1705,6 +1706,7 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             if (tid < kC) {
                 eg[tid] = exp2f(gh[tid] + gl[tid]);
                 ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
+                cd[tid] = exp2f((gh[tid | 15] - gh[tid]) + (gl[tid | 15] - gl[tid]));
             }
             mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
             // 1 / m of a power of two is exact
@@ -1821,6 +1823,10 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 add(acc, prow[16 * half + g], prow[16 * half + g + 8]);
             }
         };
+        // decays in base 2: between two tokens, and from a tile's end to a later token
+        auto gap = [&](int i, int j) { return (gh[i] - gh[j]) + (gl[i] - gl[j]); };
+        auto since = [&](int i, int tile) { return ex2(gap(i, 16 * tile + 15)); };
+        auto pair2 = [&](const float* f, int i) { return *reinterpret_cast<const float2*>(f + i); };
         // the products with the states first: their planes are refilled meanwhile
         if (!role_k) {
             state(odO, SM::S, eg[ia] * (sdo[ia] * mS), eg[ib] * (sdo[ib] * mS));
@@ -1842,13 +1848,24 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             dots(x, odO, oE, 0, rt);
             const float fa = mE * sdo[ia], fb = mE * sdo[ib];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int j0 = 16 * (h + (nt & 2)) + 8 * (nt & 1) + 2 * tq;
+            for (int u = 0; u < 2; ++u) {
+                const int tile = h + 2 * u;
+                if (tile < rt) {  // a row's decay from the tile's end, a column's to it
+                    const float da = fa * since(ia, tile), db = fb * since(ib, tile);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = e >> 1 ? ib : ia, j = j0 + (e & 1);
-                    const float dec = ex2((gh[i] - gh[j]) + (gl[i] - gl[j]));
-                    x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * dec * (fB[j] * fK[j]) : 0.f;
+                    for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
+                        const int j = 16 * tile + 8 * (nt & 1) + 2 * tq;
+                        const float2 f = mul2(mul2(pair2(fB, j), pair2(fK, j)), pair2(cd, j));
+                        set_rows(x[nt], mul2(mul2(row_a(x[nt]), both(da)), f), mul2(mul2(row_b(x[nt]), both(db)), f));
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 2 * u; nt < 2 * u + 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = e >> 1 ? ib : ia, j = 16 * tile + 8 * (nt & 1) + 2 * tq + (e & 1);
+                            x[nt][e] = j <= i ? x[nt][e] * (e >> 1 ? fb : fa) * ex2(gap(i, j)) * (fB[j] * fK[j]) : 0.f;
+                        }
                 }
             }
             rows_product(x, SM::K, 0, rt);
@@ -1861,16 +1878,43 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 dots(y, odV, oE, 0, rt);
                 dots(x, oE, odO, rt, 3);
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+                for (int u = 0; u < 2; ++u) {
+                    const int tile = h + 2 * u;
+                    if (tile > rt) {  // i > j: the columns' decay from the rows' tile's end
+                        const float da = fB[ia] * cd[ia], db = fB[ib] * cd[ib];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = e >> 1 ? ib : ia, i = 16 * (h + (nt & 2)) + 8 * (nt & 1) + 2 * tq + (e & 1);
-                        const float d = (gh[i] - gh[j]) + (gl[i] - gl[j]), dec = ex2(i >= j ? d : -d);
-                        y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * fK[i])
-                                   : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i])
-                                           : 0.f;
-                        x[nt][e] = i >= j ? x[nt][e] * (mE * sdo[i]) * dec * (fB[j] * (fQ[i] * scale)) : 0.f;
+                        for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
+                            const int i = 16 * tile + 8 * (nt & 1) + 2 * tq;
+                            const float2 dec = make_float2(since(i, rt), since(i + 1, rt));
+                            const float2 fy = mul2(mul2(dec, pair2(fK, i)), both(-fm));
+                            const float2 fx = mul2(mul2(mul2(dec, pair2(fQ, i)), pair2(sdo, i)), both(mE * scale));
+                            set_rows(y[nt], mul2(mul2(row_a(z[nt]), both(da)), fy), mul2(mul2(row_b(z[nt]), both(db)), fy));
+                            set_rows(x[nt], mul2(mul2(row_a(x[nt]), both(da)), fx), mul2(mul2(row_b(x[nt]), both(db)), fx));
+                        }
+                    } else if (tile < rt) {  // i < j: M alone
+                        const float da = -fm * since(ia, tile), db = -fm * since(ib, tile);
+#pragma unroll
+                        for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
+                            const int i = 16 * tile + 8 * (nt & 1) + 2 * tq;
+                            const float2 f = mul2(mul2(pair2(fB, i), pair2(fK, i)), pair2(cd, i));
+                            set_rows(y[nt], mul2(mul2(row_a(y[nt]), both(da)), f), mul2(mul2(row_b(y[nt]), both(db)), f));
+                            set_rows(x[nt], both(0.f), both(0.f));
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 2 * u; nt < 2 * u + 2; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = e >> 1 ? ib : ia, i = 16 * tile + 8 * (nt & 1) + 2 * tq + (e & 1);
+                                const float d = gap(i, j), dec = ex2(i >= j ? d : -d);
+                                y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * fK[i])
+                                           : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i])
+                                                   : 0.f;
+                                x[nt][e] =
+                                    i >= j ? x[nt][e] * (mE * sdo[i]) * dec * (fB[j] * (fQ[i] * scale)) : 0.f;
+                            }
                     }
+                }
             }
             rows_product(y, SM::K, 0, 3);
             rows_product(x, SM::Q, rt, 3);
@@ -1945,16 +1989,39 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             for (int e = 0; e < 2; ++e) {
                 const int i = r0 + g + 8 * e;
                 const float r = rr[i] * mul, d = dot[e] * f[i] * f[i];
+                uint32_t w[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float x0 = tot[nt][2 * e], x1 = tot[nt][2 * e + 1];
-                    if (l2) {
-                        const float2 u = unit(i, nt);
-                        x0 -= u.x * d, x1 -= u.y * d;
+                    float2 x = make_float2(tot[nt][2 * e], tot[nt][2 * e + 1]);
+                    if (l2)
+                        x = fma2(unit(i, nt), both(-d), x);
+                    w[nt] = sm100::pack_bf16x2(r * x.x, r * x.y);
+                }
+                __nv_bfloat16* row = dst + (me.kh * N + t0 + i) * D + 16 * dg;
+                if (NT % 4 == 0) {
+                    // lane tq of a quad gathers tile 4 m + tq of its row: 16 bytes
+#pragma unroll
+                    for (int m = 0; m < NT / 4; ++m) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            // round k: give the part of tile tq ^ k, get that of the own
+                            const int want = tq ^ k;
+                            const uint32_t give = want & 2 ? (want & 1 ? w[4 * m + 3] : w[4 * m + 2])
+                                                           : (want & 1 ? w[4 * m + 1] : w[4 * m]);
+                            v[k] = __shfl_xor_sync(0xffffffffu, give, k);
+                        }
+                        // v[k] came from lane tq ^ k: its columns are 2 (tq ^ k)
+                        const uint32_t q0 = tq & 1 ? v[1] : v[0], q1 = tq & 1 ? v[0] : v[1],
+                                       q2 = tq & 1 ? v[3] : v[2], q3 = tq & 1 ? v[2] : v[3];
+                        const uint4 o = tq & 2 ? make_uint4(q2, q3, q0, q1) : make_uint4(q0, q1, q2, q3);
+                        if (i < n)
+                            *reinterpret_cast<uint4*>(row + 8 * (4 * m + tq)) = o;
                     }
-                    if (i < n)
-                        *reinterpret_cast<uint32_t*>(dst + (me.kh * N + t0 + i) * D + 16 * dg + 8 * nt + 2 * tq) =
-                            sm100::pack_bf16x2(r * x0, r * x1);
+                } else if (i < n) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        *reinterpret_cast<uint32_t*>(row + 8 * nt + 2 * tq) = w[nt];
                 }
             }
         }
