@@ -92,8 +92,8 @@ constexpr int kPrepThreads = 128;
 template <int D, bool GRAD>
 struct PrepSmem {
     static constexpr int img = 2 * row_image<D>() > fac_at<GRAD>() ? 2 * row_image<D>() : fac_at<GRAD>();
-    static constexpr int diag = img;                     // [4][16][20] fp32
-    static constexpr int vec = diag + 4 * 16 * 20 * 4;
+    static constexpr int diag = img;  // [4][2][16][20] fp32
+    static constexpr int vec = diag + 4 * 2 * 16 * 20 * 4;
     static constexpr int bytes = vec + (10 + n_factors<GRAD>()) * kC * 4 + 64;
 };
 
@@ -143,13 +143,15 @@ __global__ void __launch_bounds__(kPrepThreads)
         for (int which = 0; which < 2; ++which) {
             const uint32_t u[8] = {w[which][0].x, w[which][0].y, w[which][0].z, w[which][0].w,
                                    w[which][1].x, w[which][1].y, w[which][1].z, w[which][1].w};
-            float ss = 0.f, mx = 0.f;
+            float2 s2 = both(0.f), f[8];
+            float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float a = __uint_as_float(u[i] << 16), b = __uint_as_float(u[i] & 0xffff0000u);
-                ss = fmaf(a, a, fmaf(b, b, ss));
-                mx = max_abs(max_abs(mx, a), b);
+                f[i] = bf2(u[i]);
+                s2 = fma2(f[i], f[i], s2);
+                mx = max_abs(max_abs(mx, f[i].x), f[i].y);
             }
+            float ss = s2.x + s2.y;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) {
                 ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -160,9 +162,10 @@ __global__ void __launch_bounds__(kPrepThreads)
             for (int h = 0; h < 2; ++h) {
                 uint32_t x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = h2(__uint_as_float(u[4 * h + i] << 16) * s.to,
-                              __uint_as_float(u[4 * h + i] & 0xffff0000u) * s.to);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = mul2(f[4 * h + i], both(s.to));
+                    x[i] = h2(y.x, y.y);
+                }
                 *reinterpret_cast<uint4*>(smem + (which ? row_image<D>() : 0) + tile_off<RB>(r, 2 * p + h)) =
                     make_uint4(x[0], x[1], x[2], x[3]);
             }
@@ -315,15 +318,20 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (lane == 0)
         top[warp] = am, top[4 + warp] = abm;
     // the diagonal block, for the substitution
-    float* sd = reinterpret_cast<float*>(smem + SM::diag) + warp * 16 * 20;
+    float* sd = reinterpret_cast<float*>(smem + SM::diag) + warp * 2 * 16 * 20;
+    float* sdb = sd + 16 * 20;  // -A beta
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         if (b == warp) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                *reinterpret_cast<float2*>(sd + g * 20 + 8 * h + 2 * tq) = make_float2(ak[2 * b + h][0], ak[2 * b + h][1]);
-                *reinterpret_cast<float2*>(sd + (g + 8) * 20 + 8 * h + 2 * tq) =
-                    make_float2(ak[2 * b + h][2], ak[2 * b + h][3]);
+                const int at = g * 20 + 8 * h + 2 * tq;
+                const float2 be = *reinterpret_cast<const float2*>(sb + 16 * b + 8 * h + 2 * tq);
+                const float2 minus = make_float2(-be.x, -be.y);
+                *reinterpret_cast<float2*>(sd + at) = row_a(ak[2 * b + h]);
+                *reinterpret_cast<float2*>(sd + at + 160) = row_b(ak[2 * b + h]);
+                *reinterpret_cast<float2*>(sdb + at) = mul2(minus, row_a(ak[2 * b + h]));
+                *reinterpret_cast<float2*>(sdb + at + 160) = mul2(minus, row_b(ak[2 * b + h]));
             }
         }
     }
@@ -341,22 +349,37 @@ __global__ void __launch_bounds__(kPrepThreads)
         *reinterpret_cast<uint32_t*>(at) = hi;
         *reinterpret_cast<uint32_t*>(at + kTile) = lo;
     };
-    {  // diagonal: column `lane & 15` of block `warp`
+    {  // diagonal: column `lane & 15` of block `warp`, then its images by row pairs
         const int b = 16 * warp, j = lane & 15;
         float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float x = -sd[i * 20 + j];
 #pragma unroll
-            for (int l = 0; l < i; ++l)
-                x = fmaf(-sd[i * 20 + l] * sb[b + l], f[l], x);
+            for (int l = 0; l < i; l += 4) {  // zero from the diagonal on
+                const float4 a = *reinterpret_cast<const float4*>(sdb + i * 20 + l);
+                x = fmaf(a.x, f[l], x);
+                if (l + 1 < i)
+                    x = fmaf(a.y, f[l + 1], x);
+                if (l + 2 < i)
+                    x = fmaf(a.z, f[l + 2], x);
+                if (l + 3 < i)
+                    x = fmaf(a.w, f[l + 3], x);
+            }
             f[i] = x;
         }
+        __syncwarp();
+        if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {  // even columns write their right neighbour's too
-            const float y = __shfl_down_sync(0xffffffffu, f[i], 1);
-            if (lane < 16 && (lane & 1) == 0)
-                put2(b + i, b + j, f[i] * s.to, y * s.to);
+            for (int i = 0; i < 16; ++i)
+                sd[i * 20 + j] = f[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int i = (lane >> 3) + 4 * m, jj = (lane & 7) * 2;
+            const float2 x = mul2(*reinterpret_cast<const float2*>(sd + i * 20 + jj), both(s.to));
+            put2(b + i, b + jj, x.x, x.y);
         }
     }
     __syncthreads();
@@ -681,10 +704,6 @@ __device__ __forceinline__ void rows_update(float (&s)[2 * KK][4], const uint32_
     }
 }
 
-// bf16 pair -> two fp32
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(lo_f(w), hi_f(w)); }
 
 // READS: outputs are wanted (a branch on the pointer instead cuts every stretch of
 // products in two)

@@ -42,6 +42,11 @@ __device__ __forceinline__ void h2_split(float a, float b, uint32_t& hi, uint32_
     lo = h2(a - f.x, b - f.y);
 }
 
+// bf16 pair -> two fp32
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 bf2(uint32_t w) { return make_float2(lo_f(w), hi_f(w)); }
+
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
