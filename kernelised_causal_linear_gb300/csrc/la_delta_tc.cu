@@ -705,6 +705,20 @@ __device__ __forceinline__ void rows_update(float (&s)[2 * KK][4], const uint32_
 }
 
 
+// A sequence may be cut into segments of `len` chunks that run at once.  A chunk's
+// map of the state is affine in it, S1 = M S0 + B with B from V, column by column.
+// So with S0 = 0 a segment's columns give its B, and d more columns with V = 0 that
+// start as the unit matrix give its M (carry: only these ends are wanted);
+// k_delta_join then walks the segments, and the run that counts starts each from its
+// own state.
+struct Segments {
+    int count, len;      // segments that run, chunks of one
+    const float* start;  // [BH][count][d][dv] state before each, or NULL: one segment from S0
+    int carry;
+    float *B, *M;        // carry: [BH][count][d][dv], [BH][count][d][d]
+    int blob, fac;       // bytes of a blob, where its factors lie
+};
+
 // READS: outputs are wanted (a branch on the pointer instead cuts every stretch of
 // products in two)
 template <int D, bool GRAD, int SP, bool READS>
@@ -712,11 +726,10 @@ __global__ void __launch_bounds__(256, 1)
     k_delta_chain(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                   const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ out,
                   const float* S0, float* S_out, int64_t N, int nchunk, int H, int Hk, int DV,
-                  const __nv_bfloat16* __restrict__ dout, Kept kept, int* status)
+                  const __nv_bfloat16* __restrict__ dout, Kept kept, Segments seg, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = ChainSmem<D, GRAD, SP>;
-    constexpr int kBlob = blob_bytes<GRAD>();
     constexpr int RB = 2 * D;                    // bytes per row
     constexpr int NT = D / 8 / SP, KK = NT / 2;  // n tiles of this warp's part of S^T; its 16-steps
     constexpr int OWN = Share<SP>::own;
@@ -724,8 +737,10 @@ __global__ void __launch_bounds__(256, 1)
     const int g = lane >> 2, tq = lane & 3;
     Share<SP> sh;
     sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
-    const int slices = DV / (16 * W);
-    const int64_t bh = blockIdx.x / slices;
+    const int slices = (DV + (seg.carry ? D : 0)) / (16 * W);
+    const int64_t run = blockIdx.x / slices;  // head and segment
+    const int64_t bh = run / seg.count;
+    const int lo = (int)(run % seg.count) * seg.len, len = min(seg.len, nchunk - lo);
     const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const uint32_t base = smem_addr(smem);
@@ -735,15 +750,24 @@ __global__ void __launch_bounds__(256, 1)
     const uint32_t sv = base + my, so = sv + 2 * kC * 32;
     Ring<SM::stages, (SP > 1)> ring(smem + SM::v + W * SM::per_slice, blockDim.x >> 5);
     const unsigned char* row_src = rows + kh * nchunk * (int64_t)(2 * row_image<D>());
-    const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)kBlob;
+    const unsigned char* blob_src = blobs + bh * nchunk * (int64_t)seg.blob;
     const int d0 = sh.half * (D / SP);  // first state row of this warp
 
-    auto load_stage = [&](int c) {
-        const uint32_t dst = base + (c % SM::stages) * SM::stage;
-        uint64_t* bar = ring.full + c % SM::stages;
-        sm100::mbar_arrive_expect_tx(bar, SM::stage);
-        delta::bulk_load(dst, row_src + c * (int64_t)(2 * row_image<D>()), 2 * row_image<D>(), bar);
-        delta::bulk_load(dst + 2 * row_image<D>(), blob_src + c * (int64_t)kBlob, kBlob, bar);
+    auto load_stage = [&](int i) {
+        const int64_t c = lo + i;
+        const uint32_t dst = base + (i % SM::stages) * SM::stage;
+        uint64_t* bar = ring.full + i % SM::stages;
+        const unsigned char *r = row_src + c * (2 * row_image<D>()), *f = blob_src + c * seg.blob;
+        if (READS) {
+            sm100::mbar_arrive_expect_tx(bar, SM::stage);
+            delta::bulk_load(dst, r, 2 * row_image<D>(), bar);
+            delta::bulk_load(dst + 2 * row_image<D>(), f, blob_bytes<GRAD>(), bar);
+        } else {  // neither Q nor P
+            sm100::mbar_arrive_expect_tx(bar, row_image<D>() + 2 * kTile + kFactors * kC * 4);
+            delta::bulk_load(dst, r, row_image<D>(), bar);
+            delta::bulk_load(dst + 2 * row_image<D>(), f, 2 * kTile, bar);
+            delta::bulk_load(dst + 2 * row_image<D>() + fac_at<GRAD>(), f + seg.fac, kFactors * kC * 4, bar);
+        }
     };
     // this warp's token tiles of the slice's columns
     auto load_cols = [&](uint32_t dst, const __nv_bfloat16* src, int c) {
@@ -751,22 +775,25 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
-            const bool live = t0 + t < N;
-            cp16(dst + tile_off<32>(t, p), src + (bh * N + (live ? t0 + t : 0)) * DV + col0 + p * 8, live);
+            const bool live = t0 + t < N && col0 < DV;  // the unit columns have no V
+            cp16(dst + tile_off<32>(t, p), src + (live ? (bh * N + t0 + t) * DV + col0 + p * 8 : 0), live);
         }
     };
     if (tid == 0)
-        for (int c = 0; c < SM::stages && c < nchunk; ++c)
-            load_stage(c);
-    load_cols(sv, v, 0);
+        for (int i = 0; i < SM::stages && i < len; ++i)
+            load_stage(i);
+    load_cols(sv, v, lo);
     cp_commit();
 
     float s[NT][4];  // S^T[col0 + g, + 8][d0 + 8 nt + 2 tq, + 1]
+    const float* start = seg.start ? seg.start + run * D * DV : S0 ? S0 + bh * D * DV : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            s[nt][e] = S0 ? S0[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
+        for (int e = 0; e < 4; ++e) {
+            const int row = d0 + 8 * nt + 2 * tq + (e & 1), col = col0 + g + (e >> 1) * 8;
+            s[nt][e] = seg.carry ? (row == col - DV ? 1.f : 0.f) : start ? start[row * DV + col] : 0.f;
+        }
 
     auto row_max = [&](float& m0, float& m1) {
         m0 = m1 = 0.f;
@@ -793,16 +820,17 @@ __global__ void __launch_bounds__(256, 1)
     };
 
     ring.wait(0);
-    for (int c = 0; c < nchunk; ++c) {
-        const uint32_t st = base + (c % SM::stages) * SM::stage;
+    for (int step = 0; step < len; ++step) {
+        const int c = lo + step;
+        const uint32_t st = base + (step % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
-        const float* fac = reinterpret_cast<const float*>(smem + (c % SM::stages) * SM::stage +
+        const float* fac = reinterpret_cast<const float*>(smem + (step % SM::stages) * SM::stage +
                                                           2 * row_image<D>() + fac_at<GRAD>());
         if (GRAD) {  // dO, wanted at the end of the chunk
             load_cols(so, dout, c);
             cp_commit();
         }
-        load_cols(sv + ((c + 1) & 1) * kC * 32, v, c + 1);  // nothing past the last chunk
+        load_cols(sv + ((step + 1) & 1) * kC * 32, v, c + 1);  // nothing past the last chunk
         cp_commit();
 
         // S^T K^T and S^T Q^T over this warp's rows of S, split on the way
@@ -865,7 +893,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
             uint32_t w[4];
-            ldsm4t(w, addr_ct<32>(sv + (c & 1) * kC * 32, lane, 16 * sh.tile(i), 0));
+            ldsm4t(w, addr_ct<32>(sv + (step & 1) * kC * 32, lane, 16 * sh.tile(i), 0));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * i + u;
@@ -1062,17 +1090,17 @@ __global__ void __launch_bounds__(256, 1)
                         *reinterpret_cast<const uint4*>(smem + (so - base) + tile_off<32>(t, p));
             }
         }
-        if (ring.last(c) && c + SM::stages < nchunk)
-            load_stage(c + SM::stages);
+        if (ring.last(step) && step + SM::stages < len)
+            load_stage(step + SM::stages);
         // here and not at the chunk's start: what is issued there (copies, addresses)
         // then shares a stretch without branches with the first products
-        if (c + 1 < nchunk)
-            ring.wait(c + 1);
+        if (step + 1 < len)
+            ring.wait(step + 1);
     }
     cp_wait<0>();
     if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
         set_status(status, LA_ERR_TIMEOUT);
-    if (GRAD) {  // the final state, for <S1, dS1> of the last chunk
+    if (GRAD && lo + len == nchunk) {  // the final state, for <S1, dS1> of the last chunk
         float m0, m1;
         row_max(m0, m1);
         const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
@@ -1085,12 +1113,88 @@ __global__ void __launch_bounds__(256, 1)
         }
         keep_state_scale(nchunk, p0, p1);
     }
-    if (S_out) {
+    float* end = nullptr;
+    int ld = DV;
+    if (seg.carry) {
+        end = col0 < DV ? seg.B + run * D * DV : seg.M + run * D * D - DV;  // unit column c is M's c - DV
+        ld = col0 < DV ? DV : D;
+    } else if (S_out && lo + len == nchunk) {
+        end = S_out + bh * D * DV;
+    }
+    if (end) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                S_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = s[nt][e];
+                end[(int64_t)(d0 + 8 * nt + 2 * tq + (e & 1)) * ld + col0 + g + (e >> 1) * 8] = s[nt][e];
+    }
+}
+
+// The states before the segments of a sequence from their ends: S_0, then
+// S_{i+1} = M_i S_i + B_i.  A CTA owns 32 columns; a thread D / 8 rows of one.  The next
+// M comes into shared memory and the next B into registers while a step runs (read
+// from L2 as it was wanted, M made a step 13 us at d = 128).
+template <int D>
+constexpr int join_smem()
+{
+    return (2 * D * D + D * 32) * 4;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+    k_delta_join(const float* __restrict__ S0, const float* __restrict__ B, const float* __restrict__ M,
+                 float* __restrict__ start, int count, int DV)
+{
+    constexpr int R = D / 8;
+    extern __shared__ __align__(16) float sm[];
+    float* sM = sm;               // [2][D][D]
+    float* sS = sm + 2 * D * D;   // [D][32]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t bh = blockIdx.x;
+    const int c = blockIdx.y * 32 + lane;
+    float x[R], next[R];
+    auto fetch = [&](int i) {  // the last segment's end is not wanted
+        if (i + 1 < count) {
+            const int64_t at = bh * (count - 1) + i;
+            const uint32_t dst = smem_addr(sM + (i & 1) * D * D);
+            for (int k = tid; k < D * D / 4; k += 256)
+                cp16(dst + k * 16, M + at * D * D + k * 4, true);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                next[r] = B[(at * D + warp * R + r) * DV + c];
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        x[r] = S0 ? S0[(bh * D + warp * R + r) * DV + c] : 0.f;
+    fetch(0);
+    for (int i = 0;; ++i) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            start[((bh * count + i) * D + warp * R + r) * DV + c] = x[r];
+        if (i + 1 == count)
+            return;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            sS[(warp * R + r) * 32 + lane] = x[r];
+            x[r] = next[r];
+        }
+        cp_wait<0>();
+        __syncthreads();
+        fetch(i + 1);
+        const float* m = sM + (i & 1) * D * D + warp * R * D;
+#pragma unroll 2
+        for (int k = 0; k < D; k += 4) {
+            const float s0 = sS[k * 32 + lane], s1 = sS[(k + 1) * 32 + lane], s2 = sS[(k + 2) * 32 + lane],
+                        s3 = sS[(k + 3) * 32 + lane];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 a = *reinterpret_cast<const float4*>(m + r * D + k);
+                x[r] = fmaf(a.x, s0, fmaf(a.y, s1, fmaf(a.z, s2, fmaf(a.w, s3, x[r]))));
+            }
+        }
+        __syncthreads();  // S and this M are read
     }
 }
 
@@ -2061,8 +2165,40 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int chunks_of(int64_t N) { return (int)((N + kC - 1) / kC); }
 
+// Segments of a sequence.  Two runs over a segment and a walk over their ends take
+// the place of one run over the whole, worth it from four segments on (B1 H4 N32768
+// d = 64: 938 us whole, 194 us cut); no more than give each warp of the second run
+// a sub-partition of its own at 152 SMs, and no more than 32: the walk is serial.  By
+// sizes alone, so that workspaces can be sized without the GPU.
+int segments_of(const DeltaArgs& a)
+{
+    const int64_t slices = a.B * a.H * (a.dv / 16);
+    int64_t n = 2 * 152 / slices;
+    n = n < chunks_of(a.N) / 8 ? n : chunks_of(a.N) / 8;
+    n = n < 32 ? n : 32;
+    if (n < 4)
+        return 1;
+    const int64_t len = (chunks_of(a.N) + n - 1) / n;  // chunks of a segment; the last may be short
+    return (int)((chunks_of(a.N) + len - 1) / len);
+}
+
+struct SegLayout {
+    size_t start, B, M, total;  // relative to its own beginning
+};
+SegLayout seg_layout(const DeltaArgs& a)
+{
+    const size_t n = (size_t)segments_of(a), BH = (size_t)(a.B * a.H);
+    SegLayout l = {};
+    if (n > 1) {
+        l.B = up256(BH * n * a.d * a.dv * 4);
+        l.M = l.B + up256(BH * (n - 1) * a.d * a.dv * 4);
+        l.total = l.M + up256(BH * (n - 1) * a.d * a.d * 4);
+    }
+    return l;
+}
+
 struct TcLayout {
-    size_t rows, blobs, total;
+    size_t rows, blobs, seg, total;
 };
 TcLayout tc_layout(const DeltaArgs& a)
 {
@@ -2070,12 +2206,13 @@ TcLayout tc_layout(const DeltaArgs& a)
     const size_t n = (size_t)chunks_of(a.N);
     l.rows = 0;
     l.blobs = up256((size_t)(a.B * a.Hk) * n * 2 * kC * a.d * 2);
-    l.total = l.blobs + up256((size_t)(a.B * a.H) * n * blob_bytes<false>());
+    l.seg = l.blobs + up256((size_t)(a.B * a.H) * n * blob_bytes<false>());
+    l.total = l.seg + seg_layout(a).total;
     return l;
 }
 
 struct GradTcLayout {
-    size_t rows, blobs, S, sS, E, sE, dS, sD, dV, sV, oo, vv, bb, cd, total;
+    size_t rows, blobs, S, sS, E, sE, dS, sD, dV, sV, oo, vv, bb, cd, seg, total;
 };
 GradTcLayout grad_tc_layout(const DeltaArgs& a)
 {
@@ -2102,6 +2239,7 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
     l.vv = take(BH * sl * (size_t)a.N * 4);
     l.bb = take(BH * sl * (size_t)a.N * 4);
     l.cd = take(BH * sl * 2 * n * 4);
+    l.seg = take(seg_layout(a).total);
     l.total = at;
     return l;
 }
@@ -2114,15 +2252,15 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
 struct Cut {
     int SP, W;
 };
-Cut cut_of(const DeltaArgs& a)
+Cut cut_of(int64_t runs, int columns)  // sequences or segments, value columns of each
 {
     const int sms = device_sm_count();
-    const int64_t slices = a.B * a.H * (a.dv / 16);
+    const int64_t slices = runs * (columns / 16);
     Cut c;
     c.SP = 2 * slices <= 4 * (int64_t)sms ? 2 : 1;
     const int cap = 8 / c.SP;
     c.W = 1;
-    while (2 * c.W <= cap && 2 * c.W <= a.dv / 16 && slices / c.W > sms)
+    while (2 * c.W <= cap && columns / 16 % (2 * c.W) == 0 && slices / c.W > sms)
         c.W *= 2;
     return c;
 }
@@ -2134,19 +2272,55 @@ cudaError_t allow_smem(K kern, int bytes)
 }
 
 template <int D, bool GRAD, int SP, bool READS>
-cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
-                         const Kept& kept)
+cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs,
+                         const Kept& kept, const Segments& seg)
 {
     const int smem = ChainSmem<D, GRAD, SP>::bytes(W);
     const cudaError_t e = allow_smem(k_delta_chain<D, GRAD, SP, READS>, smem);
     if (e != cudaSuccess)
         return e;
-    k_delta_chain<D, GRAD, SP, READS><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
-        rows, blobs, static_cast<const __nv_bfloat16*>(a.v), GRAD ? nullptr : static_cast<__nv_bfloat16*>(a.out), a.S0,
-        GRAD ? nullptr : a.S_out, a.N, n, (int)a.H, (int)a.Hk, a.dv, static_cast<const __nv_bfloat16*>(a.dout), kept,
-        a.status);
+    const int columns = a.dv + (seg.carry ? a.d : 0);
+    k_delta_chain<D, GRAD, SP, READS>
+        <<<(unsigned)(a.B * a.H * seg.count * (columns / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+            rows, blobs, static_cast<const __nv_bfloat16*>(a.v),
+            READS && !GRAD ? static_cast<__nv_bfloat16*>(a.out) : nullptr, a.S0,
+            GRAD || seg.carry ? nullptr : a.S_out, a.N, chunks_of(a.N), (int)a.H, (int)a.Hk, a.dv,
+            static_cast<const __nv_bfloat16*>(a.dout), kept, seg, a.status);
     count_launches(1);
     return cudaGetLastError();
+}
+
+// A chain over whole sequences, or over segments once their states are known.
+template <int D, bool GRAD, bool READS>
+cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
+                      unsigned char* ws)
+{
+    const int n = segments_of(a);
+    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, blob_bytes<GRAD>(), fac_at<GRAD>()};
+    if (n > 1) {
+        const SegLayout l = seg_layout(a);
+        float* start = reinterpret_cast<float*>(ws + l.start);
+        float* B = reinterpret_cast<float*>(ws + l.B);
+        float* M = reinterpret_cast<float*>(ws + l.M);
+        seg.len = (chunks_of(a.N) + n - 1) / n;
+        const Segments ends = {n - 1, seg.len, nullptr, 1, B, M, seg.blob, seg.fac};
+        const Cut cut = cut_of(a.B * a.H * (n - 1), a.dv + a.d);
+        cudaError_t e = cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, Kept{}, ends)
+                                    : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, Kept{}, ends);
+        if (e != cudaSuccess)
+            return e;
+        if ((e = allow_smem(k_delta_join<D>, join_smem<D>())) != cudaSuccess)
+            return e;
+        k_delta_join<D><<<dim3((unsigned)(a.B * a.H), a.dv / 32), 256, join_smem<D>(), a.stream>>>(a.S0, B, M, start, n,
+                                                                                                   a.dv);
+        count_launches(1);
+        if ((e = cudaGetLastError()) != cudaSuccess)
+            return e;
+        seg.count = n, seg.start = start;
+    }
+    const Cut cut = cut_of(a.B * a.H * n, a.dv);
+    return cut.SP == 2 ? launch_chain<D, GRAD, 2, READS>(a, cut.W, rows, blobs, kept, seg)
+                       : launch_chain<D, GRAD, 1, READS>(a, cut.W, rows, blobs, kept, seg);
 }
 
 template <int D, int SP, bool GATED>
@@ -2182,13 +2356,9 @@ cudaError_t run_forward(const DeltaArgs& a)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    const Cut cut = cut_of(a);
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
-    if (a.out)
-        return cut.SP == 2 ? launch_chain<D, false, 2, true>(a, cut.W, rows, blobs, n, Kept{})
-                           : launch_chain<D, false, 1, true>(a, cut.W, rows, blobs, n, Kept{});
-    return cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, n, Kept{})
-                       : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, n, Kept{});
+    return a.out ? run_chain<D, false, true>(a, rows, blobs, Kept{}, ws + l.seg)
+                 : run_chain<D, false, false>(a, rows, blobs, Kept{}, ws + l.seg);
 }
 
 template <int D, int DV>
@@ -2213,10 +2383,9 @@ cudaError_t run_backward(const DeltaArgs& a)
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const Cut cut = cut_of(a);
+    const Cut cut = cut_of(BH, a.dv);
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
-    e = cut.SP == 2 ? launch_chain<D, true, 2, true>(a, cut.W, rows, blobs, n, kept)
-                    : launch_chain<D, true, 1, true>(a, cut.W, rows, blobs, n, kept);
+    e = run_chain<D, true, true>(a, rows, blobs, kept, ws + l.seg);
     if (e == cudaSuccess)
         e = cut.SP == 2 ? a.log_alpha ? launch_rev<D, 2, true>(a, cut.W, rows, blobs, n, kept)
                                       : launch_rev<D, 2, false>(a, cut.W, rows, blobs, n, kept)
