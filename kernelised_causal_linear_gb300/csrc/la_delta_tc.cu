@@ -716,6 +716,7 @@ struct Segments {
     const float* start;  // [BH][count][d][dv] state before each, or NULL: one segment from S0
     int carry;
     float *B, *M;        // carry: [BH][count][d][dv], [BH][count][d][d]
+    int first;           // the first segment that runs
     int blob, fac;       // bytes of a blob, where its factors lie
 };
 
@@ -1130,20 +1131,21 @@ __global__ void __launch_bounds__(256, 1)
     }
 }
 
-// The states before the segments of a sequence from their ends: S_0, then
-// S_{i+1} = M_i S_i + B_i.  A CTA owns 32 columns; a thread D / 8 rows of one.  The next
-// M comes into shared memory and the next B into registers while a step runs (read
-// from L2 as it was wanted, M made a step 13 us at d = 128).
+// The states before the segments of a sequence from their ends, S_{i+1} = M_i S_i + B_i
+// from S_0, or (REV) the gradients of the states after them, dS_{i-1} = M_i^T dS_i + C_i
+// from that of the last.  A CTA owns 32 columns; a thread D / 8 rows of one.  The next M
+// comes into shared memory and the next B into registers while a step runs (read from
+// L2 as it was wanted, M made a step 13 us at d = 128).
 template <int D>
 constexpr int join_smem()
 {
     return (2 * D * D + D * 32) * 4;
 }
 
-template <int D>
+template <int D, bool REV>
 __global__ void __launch_bounds__(256)
     k_delta_join(const float* __restrict__ S0, const float* __restrict__ B, const float* __restrict__ M,
-                 float* __restrict__ start, int count, int DV)
+                 float* __restrict__ start, int count, int mcount, int DV)
 {
     constexpr int R = D / 8;
     extern __shared__ __align__(16) float sm[];
@@ -1153,15 +1155,19 @@ __global__ void __launch_bounds__(256)
     const int64_t bh = blockIdx.x;
     const int c = blockIdx.y * 32 + lane;
     float x[R], next[R];
-    auto fetch = [&](int i) {  // the last segment's end is not wanted
+    // step i leads out of segment `of`; M and B have mcount segments, C count - 1 (not
+    // the first)
+    auto fetch = [&](int i) {
         if (i + 1 < count) {
-            const int64_t at = bh * (count - 1) + i;
+            const int of = REV ? count - 1 - i : i;
+            const float* m = M + (bh * mcount + of) * D * D;
+            const float* b = B + (REV ? bh * (count - 1) + of - 1 : bh * mcount + of) * D * DV;
             const uint32_t dst = smem_addr(sM + (i & 1) * D * D);
             for (int k = tid; k < D * D / 4; k += 256)
-                cp16(dst + k * 16, M + at * D * D + k * 4, true);
+                cp16(dst + k * 16, m + k * 4, true);
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                next[r] = B[(at * D + warp * R + r) * DV + c];
+                next[r] = b[(warp * R + r) * DV + c];
         }
         cp_commit();
     };
@@ -1170,9 +1176,10 @@ __global__ void __launch_bounds__(256)
         x[r] = S0 ? S0[(bh * D + warp * R + r) * DV + c] : 0.f;
     fetch(0);
     for (int i = 0;; ++i) {
+        const int of = REV ? count - 1 - i : i;
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            start[((bh * count + i) * D + warp * R + r) * DV + c] = x[r];
+            start[((bh * count + of) * D + warp * R + r) * DV + c] = x[r];
         if (i + 1 == count)
             return;
 #pragma unroll
@@ -1183,15 +1190,28 @@ __global__ void __launch_bounds__(256)
         cp_wait<0>();
         __syncthreads();
         fetch(i + 1);
-        const float* m = sM + (i & 1) * D * D + warp * R * D;
-#pragma unroll 2
-        for (int k = 0; k < D; k += 4) {
-            const float s0 = sS[k * 32 + lane], s1 = sS[(k + 1) * 32 + lane], s2 = sS[(k + 2) * 32 + lane],
-                        s3 = sS[(k + 3) * 32 + lane];
+        const float* m = sM + (i & 1) * D * D;
+        if (REV) {
+#pragma unroll 4
+            for (int k = 0; k < D; ++k) {
+                const float s0 = sS[k * 32 + lane];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float4 a = *reinterpret_cast<const float4*>(m + r * D + k);
-                x[r] = fmaf(a.x, s0, fmaf(a.y, s1, fmaf(a.z, s2, fmaf(a.w, s3, x[r]))));
+                for (int r = 0; r < R; r += 4) {
+                    const float4 a = *reinterpret_cast<const float4*>(m + k * D + warp * R + r);
+                    x[r] = fmaf(a.x, s0, x[r]), x[r + 1] = fmaf(a.y, s0, x[r + 1]);
+                    x[r + 2] = fmaf(a.z, s0, x[r + 2]), x[r + 3] = fmaf(a.w, s0, x[r + 3]);
+                }
+            }
+        } else {
+#pragma unroll 2
+            for (int k = 0; k < D; k += 4) {
+                const float s0 = sS[k * 32 + lane], s1 = sS[(k + 1) * 32 + lane], s2 = sS[(k + 2) * 32 + lane],
+                            s3 = sS[(k + 3) * 32 + lane];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float4 a = *reinterpret_cast<const float4*>(m + (warp * R + r) * D + k);
+                    x[r] = fmaf(a.x, s0, fmaf(a.y, s1, fmaf(a.z, s2, fmaf(a.w, s3, x[r]))));
+                }
             }
         }
         __syncthreads();  // S and this M are read
@@ -1209,6 +1229,10 @@ __global__ void __launch_bounds__(256)
 //
 // and the dot products that need both directions' fp32 values: v.dV, Y.E, and
 // <S0, dS0> (which is <S1, dS1> of the chunk before).
+//
+// Over segments as in k_delta_chain: dS0 is affine in dS1, and its matrix over a
+// segment is the transpose of the M that the states' run gave.  ENDS: a run from
+// dS = 0 that leaves each segment's constant part in seg.B and nothing else.
 template <int D, int SP>
 struct RevSmem {
     static constexpr int stages = 2;
@@ -1221,13 +1245,13 @@ struct RevSmem {
     static int bytes(int W) { return slice0 + W * per_slice + 128; }
 };
 
-template <int D, int SP, bool GATED>
+template <int D, int SP, bool GATED, bool ENDS>
 __global__ void __launch_bounds__(256, 1)
     k_delta_rev(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
                 const float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dv,
                 float* __restrict__ dS0, int64_t N, int nchunk, int H, int Hk, int DV, Kept kept,
-                int* status)
+                Segments seg, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = RevSmem<D, SP>;
@@ -1238,7 +1262,9 @@ __global__ void __launch_bounds__(256, 1)
     Share<SP> sh;
     sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
     const int slices = DV / (16 * W);
-    const int64_t bh = blockIdx.x / slices;
+    const int64_t run = blockIdx.x / slices;  // head and segment
+    const int64_t bh = run / seg.count;
+    const int lo = ((int)(run % seg.count) + seg.first) * seg.len, len = min(seg.len, nchunk - lo);
     const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice, slice = col0 / 16;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const uint32_t base = smem_addr(smem);
@@ -1252,7 +1278,7 @@ __global__ void __launch_bounds__(256, 1)
     const int d0 = sh.half * (D / SP);
 
     auto load_stage = [&](int it) {
-        const int64_t c = nchunk - 1 - it;
+        const int64_t c = lo + len - 1 - it;
         const uint32_t dst = base + (it % SM::stages) * SM::stage;
         uint64_t* bar = ring.full + it % SM::stages;
         sm100::mbar_arrive_expect_tx(bar, SM::stage);
@@ -1292,14 +1318,14 @@ __global__ void __launch_bounds__(256, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(state_at(c, i / (KK * 4)) + i % (KK * 4) * 128));
     };
     auto dot_state = [&](int64_t c, float sc0, float sc1) {
-        const uint32_t* hi = reinterpret_cast<const uint32_t*>(state_at(c, 0)) + lane;
-        const uint32_t* lo = reinterpret_cast<const uint32_t*>(state_at(c, 1)) + lane;
+        const uint32_t* part0 = reinterpret_cast<const uint32_t*>(state_at(c, 0)) + lane;
+        const uint32_t* part1 = reinterpret_cast<const uint32_t*>(state_at(c, 1)) + lane;
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // register i: row g + 8 (i & 1), tile 2 kk + (i >> 1)
-                const uint32_t x = __ldg(hi + (kk * 4 + i) * 32), y = __ldg(lo + (kk * 4 + i) * 32);
+                const uint32_t x = __ldg(part0 + (kk * 4 + i) * 32), y = __ldg(part1 + (kk * 4 + i) * 32);
                 const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x));
                 const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&y));
                 const float* d = ds[2 * kk + (i >> 1)] + 2 * (i & 1);
@@ -1311,7 +1337,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0 && c > 0) {
+        if (lane == 0 && c > lo) {  // the segment before sees to its own end
             float* cd = kept.cd + (bh * (DV / 16) + slice) * 2 * nchunk + c - 1;
             cd[sh.half * nchunk] = x;
             if (SP == 1)
@@ -1323,23 +1349,23 @@ __global__ void __launch_bounds__(256, 1)
     };
 
     if (tid == 0)
-        for (int i = 0; i < SM::stages && i < nchunk; ++i)
+        for (int i = 0; i < SM::stages && i < len; ++i)
             load_stage(i);
-    load_cols(sdo + ((nchunk - 1) & 1) * kC * 32, dout, nchunk - 1);
+    load_cols(sdo + ((lo + len - 1) & 1) * kC * 32, dout, lo + len - 1);
     cp_commit();
+    const float* end = ENDS ? nullptr : seg.start ? seg.start + run * D * DV : dS_out ? dS_out + bh * D * DV : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            ds[nt][e] =
-                dS_out ? dS_out[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
+            ds[nt][e] = end ? end[(d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
     if (GATED)
-        dot_state(nchunk, state_scale(nchunk, g), state_scale(nchunk, g + 8));
+        dot_state(lo + len, state_scale(lo + len, g), state_scale(lo + len, g + 8));
     cp_wait<0>();
     sh.sync();
     ring.wait(0);
-    for (int it = 0; it < nchunk; ++it) {
-        const int c = nchunk - 1 - it;
+    for (int it = 0; it < len; ++it) {
+        const int c = lo + len - 1 - it;
         const uint32_t st = base + (it % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
         const float* fac = reinterpret_cast<const float*>(smem + (it % SM::stages) * SM::stage +
@@ -1347,8 +1373,10 @@ __global__ void __launch_bounds__(256, 1)
         const uint32_t tdo = sdo + (c & 1) * kC * 32;
         // this chunk's V, E and S, wanted from the middle on; the next dO, each warp its
         // token tiles, which both await before they meet at the chunk's end
-        load_cols(sv, v, c);
-        load_E(c);
+        if (!ENDS) {
+            load_cols(sv, v, c);
+            load_E(c);
+        }
         cp_commit();
         load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
         cp_commit();
@@ -1357,8 +1385,11 @@ __global__ void __launch_bounds__(256, 1)
             ask_state(c);
             sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
         }
-        const float* se = kept.sE + (bh * nchunk + c) * DV + col0;
-        const float se0 = se[g], se1 = se[g + 8];
+        float se0 = 0.f, se1 = 0.f;
+        if (!ENDS) {
+            const float* se = kept.sE + (bh * nchunk + c) * DV + col0;
+            se0 = se[g], se1 = se[g + 8];
+        }
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
             return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
         };
@@ -1382,7 +1413,8 @@ __global__ void __launch_bounds__(256, 1)
             h2_split(row_b(ds[2 * kk]), p1.to, hi[1], lo[1]);
             h2_split(row_a(ds[2 * kk + 1]), p0.to, hi[2], lo[2]);
             h2_split(row_b(ds[2 * kk + 1]), p1.to, hi[3], lo[3]);
-            keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + d0 / 16 + kk, lane, hi);
+            if (!ENDS)
+                keep_part(kept.dS, bh * nchunk + c, D * DV * 2, slice * (D / 16) + d0 / 16 + kk, lane, hi);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 ldsm4(b[j], addr_b<RB>(sK, lane, 16 * sh.tile(j), d0 + 16 * kk));
@@ -1473,91 +1505,102 @@ __global__ void __launch_bounds__(256, 1)
                     ldsm4t(b, addr_bt<128>(sF + part * kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
                 });
         }
-        cp_wait<1>();  // V, E
-        __syncwarp();
-        // Y, the dots, dV on the own tiles
         const float f0 = y0.from * fac[kFacF * kC], f1 = y1.from * fac[kFacF * kC];
-        float bsum[OWN / 2][8], vsum[OWN / 2][8];
+        if (ENDS) {  // dV alone
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            uint32_t w[4];
-            ldsm4t(w, addr_ct<32>(sv, lane, 16 * sh.tile(i), 0));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int nt = 2 * i + h;
-                const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
+            for (int nt = 0; nt < 2 * OWN; ++nt) {
                 set_rows(u[nt], fma2(both(f0), row_a(x[nt]), row_a(u[nt])),
                          fma2(both(f1), row_b(x[nt]), row_b(u[nt])));
-                const uint32_t* eh =
-                    reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
-                const uint32_t* el = eh + kC * 8;
-                const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(eh));
-                const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
-                const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
-                const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
-                const int part = nt >> 2, k = 2 * (nt & 3);
-                bsum[part][k] = u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x));
-                bsum[part][k + 1] = u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y));
-                u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
-                vsum[part][k] = u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]);
-                vsum[part][k + 1] = u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]);
+                scale_cols(u[nt], fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq));
             }
-        }
+        } else {
+            cp_wait<1>();  // V, E
+            __syncwarp();
+            // Y, the dots, dV on the own tiles
+            float bsum[OWN / 2][8], vsum[OWN / 2][8];
 #pragma unroll
-        for (int part = 0; part < OWN / 2; ++part) {
-            sh.store_sums(kept.bb + (bh * (DV / 16) + slice) * N, bsum[part], part, (int64_t)c * kC, N);
-            if (GATED)
-                sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t w[4];
+                ldsm4t(w, addr_ct<32>(sv, lane, 16 * sh.tile(i), 0));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int nt = 2 * i + h;
+                    const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
+                    set_rows(u[nt], fma2(both(f0), row_a(x[nt]), row_a(u[nt])),
+                             fma2(both(f1), row_b(x[nt]), row_b(u[nt])));
+                    const uint32_t* eh =
+                        reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
+                    const uint32_t* el = eh + kC * 8;
+                    const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(eh));
+                    const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
+                    const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
+                    const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
+                    const int part = nt >> 2, k = 2 * (nt & 3);
+                    bsum[part][k] = u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x));
+                    bsum[part][k + 1] = u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y));
+                    u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
+                    vsum[part][k] = u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]);
+                    vsum[part][k + 1] = u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]);
+                }
+            }
+#pragma unroll
+            for (int part = 0; part < OWN / 2; ++part) {
+                sh.store_sums(kept.bb + (bh * (DV / 16) + slice) * N, bsum[part], part, (int64_t)c * kC, N);
+                if (GATED)
+                    sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
+            }
         }
         if (SP > 1)
             sh.put(2, pair(u, 0), pair(u, 1));
         sh.sync();
         if (SP > 1)
             sh.template get<false>(2, pair(u, 2), pair(u, 3));
-        // dV leaves as bf16 (V's tile is read) and is kept as scaled fp16
-        float v0 = 0.f, v1 = 0.f;
+        if (!ENDS) {
+            // dV leaves as bf16 (V's tile is read) and is kept as scaled fp16
+            float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            v0 = max_abs(max_abs(v0, u[nt][0]), u[nt][1]);
-            v1 = max_abs(max_abs(v1, u[nt][2]), u[nt][3]);
-        }
-        {
-            const Pow2 s0 = pow2_for(quad_max(v0)), s1 = pow2_for(quad_max(v1));
+            for (int nt = 0; nt < 8; ++nt) {
+                v0 = max_abs(max_abs(v0, u[nt][0]), u[nt][1]);
+                v1 = max_abs(max_abs(v1, u[nt][2]), u[nt][3]);
+            }
+            {
+                const Pow2 s0 = pow2_for(quad_max(v0)), s1 = pow2_for(quad_max(v1));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    uint32_t w[4], a[4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int nt = 2 * i + h;
+                        w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
+                        w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
+                        a[2 * h] = h2(u[nt][0] * s0.to, u[nt][1] * s0.to);
+                        a[2 * h + 1] = h2(u[nt][2] * s1.to, u[nt][3] * s1.to);
+                    }
+                    stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
+                    keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
+                }
+                if (tq == 0) {
+                    float* sd = kept.sD + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
+                    sd[g] = p0.from, sd[g + 8] = p1.from;
+                    if (SP == 1)
+                        sd[DV + g] = p0.from, sd[DV + g + 8] = p1.from;
+                    if (sh.half == 0) {
+                        float* sw = kept.sV + (bh * nchunk + c) * DV + col0;
+                        sw[g] = s0.from, sw[g + 8] = s1.from;
+                    }
+                }
+            }
             __syncwarp();
+            {
+                const int64_t t0 = (int64_t)c * kC;
 #pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                uint32_t w[4], a[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * i + h;
-                    w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
-                    w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
-                    a[2 * h] = h2(u[nt][0] * s0.to, u[nt][1] * s0.to);
-                    a[2 * h + 1] = h2(u[nt][2] * s1.to, u[nt][3] * s1.to);
+                for (int i = 0; i < OWN; ++i) {
+                    const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
+                    if (t0 + t < N)
+                        *reinterpret_cast<uint4*>(dv + (bh * N + t0 + t) * DV + col0 + p * 8) =
+                            *reinterpret_cast<const uint4*>(smem + mine + SM::v + tile_off<32>(t, p));
                 }
-                stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
-                keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
-            }
-            if (tq == 0) {
-                float* sd = kept.sD + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
-                sd[g] = p0.from, sd[g + 8] = p1.from;
-                if (SP == 1)
-                    sd[DV + g] = p0.from, sd[DV + g + 8] = p1.from;
-                if (sh.half == 0) {
-                    float* sw = kept.sV + (bh * nchunk + c) * DV + col0;
-                    sw[g] = s0.from, sw[g + 8] = s1.from;
-                }
-            }
-        }
-        __syncwarp();
-        {
-            const int64_t t0 = (int64_t)c * kC;
-#pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                const int t = 16 * sh.tile(i) + (lane >> 1), p = lane & 1;
-                if (t0 + t < N)
-                    *reinterpret_cast<uint4*>(dv + (bh * N + t0 + t) * DV + col0 + p * 8) =
-                        *reinterpret_cast<const uint4*>(smem + mine + SM::v + tile_off<32>(t, p));
             }
         }
         // dS0 on this warp's rows: both products on accumulators under one power of two
@@ -1611,20 +1654,21 @@ __global__ void __launch_bounds__(256, 1)
             dot_state(c, sc0, sc1);
         cp_wait<0>();
         sh.sync();
-        if (ring.last(it) && it + SM::stages < nchunk)
+        if (ring.last(it) && it + SM::stages < len)
             load_stage(it + SM::stages);
-        if (it + 1 < nchunk)
+        if (it + 1 < len)
             ring.wait(it + 1);
     }
     cp_wait<0>();
     if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
         set_status(status, LA_ERR_TIMEOUT);
-    if (dS0) {
+    float* to = ENDS ? seg.B + run * D * DV : dS0 && lo == 0 ? dS0 + bh * D * DV : nullptr;
+    if (to) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                dS0[(bh * D + d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = ds[nt][e];
+                to[(d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] = ds[nt][e];
     }
 }
 
@@ -2182,6 +2226,7 @@ int segments_of(const DeltaArgs& a)
     return (int)((chunks_of(a.N) + len - 1) / len);
 }
 
+// Beginnings (or gradients of the ends), constant parts and matrices of the segments.
 struct SegLayout {
     size_t start, B, M, total;  // relative to its own beginning
 };
@@ -2191,8 +2236,8 @@ SegLayout seg_layout(const DeltaArgs& a)
     SegLayout l = {};
     if (n > 1) {
         l.B = up256(BH * n * a.d * a.dv * 4);
-        l.M = l.B + up256(BH * (n - 1) * a.d * a.dv * 4);
-        l.total = l.M + up256(BH * (n - 1) * a.d * a.d * 4);
+        l.M = l.B + up256(BH * n * a.d * a.dv * 4);
+        l.total = l.M + up256(BH * n * a.d * a.d * 4);
     }
     return l;
 }
@@ -2290,31 +2335,65 @@ cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, c
     return cudaGetLastError();
 }
 
-// A chain over whole sequences, or over segments once their states are known.
+template <int D, int SP, bool GATED, bool ENDS>
+cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs,
+                       const Kept& kept, const Segments& seg)
+{
+    const int smem = RevSmem<D, SP>::bytes(W);
+    const cudaError_t e = allow_smem(k_delta_rev<D, SP, GATED, ENDS>, smem);
+    if (e != cudaSuccess)
+        return e;
+    k_delta_rev<D, SP, GATED, ENDS>
+        <<<(unsigned)(a.B * a.H * seg.count * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+            rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
+            static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, chunks_of(a.N), (int)a.H, (int)a.Hk, a.dv, kept, seg,
+            a.status);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int D, bool GATED, bool ENDS>
+cudaError_t run_rev_cut(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
+                        const Segments& seg)
+{
+    const Cut cut = cut_of(a.B * a.H * seg.count, a.dv);
+    return cut.SP == 2 ? launch_rev<D, 2, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg)
+                       : launch_rev<D, 1, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg);
+}
+
+template <int D, bool REV>
+cudaError_t launch_join(const DeltaArgs& a, const float* from, const float* B, const float* M, float* start, int n,
+                        int mcount)
+{
+    const cudaError_t e = allow_smem(k_delta_join<D, REV>, join_smem<D>());
+    if (e != cudaSuccess)
+        return e;
+    k_delta_join<D, REV><<<dim3((unsigned)(a.B * a.H), a.dv / 32), 256, join_smem<D>(), a.stream>>>(from, B, M, start,
+                                                                                                 n, mcount, a.dv);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+// A chain over whole sequences, or over segments once their states are known.  A
+// gradient's reverse chain wants the last segment's M too.
 template <int D, bool GRAD, bool READS>
 cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
                       unsigned char* ws)
 {
     const int n = segments_of(a);
-    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, blob_bytes<GRAD>(), fac_at<GRAD>()};
+    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<GRAD>(), fac_at<GRAD>()};
     if (n > 1) {
         const SegLayout l = seg_layout(a);
         float* start = reinterpret_cast<float*>(ws + l.start);
         float* B = reinterpret_cast<float*>(ws + l.B);
         float* M = reinterpret_cast<float*>(ws + l.M);
         seg.len = (chunks_of(a.N) + n - 1) / n;
-        const Segments ends = {n - 1, seg.len, nullptr, 1, B, M, seg.blob, seg.fac};
-        const Cut cut = cut_of(a.B * a.H * (n - 1), a.dv + a.d);
+        const int m = GRAD ? n : n - 1;
+        const Segments ends = {m, seg.len, nullptr, 1, B, M, 0, seg.blob, seg.fac};
+        const Cut cut = cut_of(a.B * a.H * m, a.dv + a.d);
         cudaError_t e = cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, Kept{}, ends)
                                     : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, Kept{}, ends);
-        if (e != cudaSuccess)
-            return e;
-        if ((e = allow_smem(k_delta_join<D>, join_smem<D>())) != cudaSuccess)
-            return e;
-        k_delta_join<D><<<dim3((unsigned)(a.B * a.H), a.dv / 32), 256, join_smem<D>(), a.stream>>>(a.S0, B, M, start, n,
-                                                                                                   a.dv);
-        count_launches(1);
-        if ((e = cudaGetLastError()) != cudaSuccess)
+        if (e != cudaSuccess || (e = launch_join<D, false>(a, a.S0, B, M, start, n, m)) != cudaSuccess)
             return e;
         seg.count = n, seg.start = start;
     }
@@ -2323,19 +2402,29 @@ cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsig
                        : launch_chain<D, GRAD, 1, READS>(a, cut.W, rows, blobs, kept, seg);
 }
 
-template <int D, int SP, bool GATED>
-cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs, int n,
-                       const Kept& kept)
+// The reverse chain, after run_chain<GRAD>: it finds the segments' M where that left
+// them.
+template <int D>
+cudaError_t run_rev(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
+                    unsigned char* ws)
 {
-    const int smem = RevSmem<D, SP>::bytes(W);
-    const cudaError_t e = allow_smem(k_delta_rev<D, SP, GATED>, smem);
-    if (e != cudaSuccess)
-        return e;
-    k_delta_rev<D, SP, GATED><<<(unsigned)(a.B * a.H * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
-        rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
-        static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, n, (int)a.H, (int)a.Hk, a.dv, kept, a.status);
-    count_launches(1);
-    return cudaGetLastError();
+    const int n = segments_of(a);
+    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<true>(), fac_at<true>()};
+    if (n > 1) {
+        const SegLayout l = seg_layout(a);
+        float* start = reinterpret_cast<float*>(ws + l.start);
+        float* C = reinterpret_cast<float*>(ws + l.B);
+        const float* M = reinterpret_cast<const float*>(ws + l.M);
+        seg.len = (chunks_of(a.N) + n - 1) / n;
+        Segments ends = seg;
+        ends.count = n - 1, ends.first = 1, ends.B = C;
+        cudaError_t e = run_rev_cut<D, false, true>(a, rows, blobs, kept, ends);
+        if (e != cudaSuccess || (e = launch_join<D, true>(a, a.dS_out, C, M, start, n, n)) != cudaSuccess)
+            return e;
+        seg.count = n, seg.start = start;
+    }
+    return a.log_alpha ? run_rev_cut<D, true, false>(a, rows, blobs, kept, seg)
+                       : run_rev_cut<D, false, false>(a, rows, blobs, kept, seg);
 }
 
 template <int D>
@@ -2383,14 +2472,10 @@ cudaError_t run_backward(const DeltaArgs& a)
     count_launches(1);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const Cut cut = cut_of(BH, a.dv);
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
     e = run_chain<D, true, true>(a, rows, blobs, kept, ws + l.seg);
     if (e == cudaSuccess)
-        e = cut.SP == 2 ? a.log_alpha ? launch_rev<D, 2, true>(a, cut.W, rows, blobs, n, kept)
-                                      : launch_rev<D, 2, false>(a, cut.W, rows, blobs, n, kept)
-            : a.log_alpha ? launch_rev<D, 1, true>(a, cut.W, rows, blobs, n, kept)
-                          : launch_rev<D, 1, false>(a, cut.W, rows, blobs, n, kept);
+        e = run_rev<D>(a, rows, blobs, kept, ws + l.seg);
     if (e != cudaSuccess)
         return e;
     const int64_t items = a.B * a.Hk * n;
