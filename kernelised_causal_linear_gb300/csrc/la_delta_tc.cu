@@ -11,7 +11,6 @@
 // With F = -(I + A diag(beta))^{-1} A the solution is E = R + F (beta R): the
 // large part R enters as it is, and only the correction is a product.
 //
-// Two launches.
 //   k_delta_prep   every chunk and value head on its own: scaled fp16 images of
 //                  K and Q, F, P and the factors of each token.  Nothing here
 //                  depends on the state.
@@ -21,8 +20,22 @@
 //                  Everything is computed transposed: S^T K^T, E^T = R^T + ..,
 //                  S^T += U^T K.  The accumulators of one product are the A
 //                  fragments of the next (see la_delta_tc.cuh), so between a
-//                  chunk's products nothing passes through shared memory and no
-//                  other warp is waited for.
+//                  chunk's products nothing passes through shared memory.  Few
+//                  slices are shared by two warps each.
+//   k_delta_join   few long sequences are cut into segments: a first run of the
+//                  chain gives each segment's map of the state, this walks them,
+//                  a second run starts every segment from its own state.
+//
+// The gradient: k_delta_prep, the chain again keeping the states before the chunks
+// and E (k_delta_chain<GRAD>), k_delta_rev for the chunks in reverse, k_delta_dqk for
+// dQ and dK of every chunk on its own.
+//
+// Why warp-level MMAs and not tcgen05: the chain is a string of small dependent
+// products (64 tokens x 16 columns x d), whose operands are the fp32 results of the
+// one before, split in two.  In registers a result is the next operand after a few
+// conversions; in tensor memory each would be read out, split and written back
+// between any two products, for M = 128 columns of one head on one SM, where a head
+// here spreads over as many SMs as there are.
 #include "la_delta_tc.cuh"
 
 namespace la {
@@ -482,7 +495,6 @@ __global__ void __launch_bounds__(kPrepThreads)
 // their sub-partitions (SP = 2) warps only lose by it: in step they share what the
 // instruction cache fetches (reverse chain, 32 heads of 8192 tokens: 529 us in step,
 // 595 us adrift).
-constexpr uint32_t kWaitPolls = 1u << 22;
 constexpr int kXch = 2048;  // bytes of one warp's exchange buffer: 16 floats per lane
 
 template <int D, bool GRAD, int SP>
@@ -572,7 +584,14 @@ struct Ring {
     __device__ __forceinline__ void wait(int i)
     {
         if (ok)
-            ok = __all_sync(0xffffffffu, sm100::mbar_wait(full + i % STAGES, (i / STAGES) & 1, kWaitPolls));
+            ok = __all_sync(0xffffffffu, wait_for(full + i % STAGES, (i / STAGES) & 1));
+    }
+    // after a wait has run out: what is in flight gets as long again
+    __device__ __forceinline__ void drain()
+    {
+        for (int i = 0; i < STAGES; ++i)
+            for (int parity = 0; parity < 2; ++parity)
+                wait_for(full + i, parity);
     }
     // this warp is done with chunk i; true in one thread once all are
     __device__ __forceinline__ bool last(int i)
@@ -588,7 +607,7 @@ struct Ring {
         if (atomicAdd_block(done + i % STAGES, 1u) != warps - 1)
             return false;
         done[i % STAGES] = 0;
-        return sm100::mbar_wait(read + i % STAGES, (i / STAGES) & 1, kWaitPolls);
+        return wait_for(read + i % STAGES, (i / STAGES) & 1);
     }
 };
 
@@ -1099,8 +1118,10 @@ __global__ void __launch_bounds__(256, 1)
             ring.wait(step + 1);
     }
     cp_wait<0>();
-    if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
+    if (!ring.ok && lane == 0) {  // a copy did not arrive in time: the results are void
+        ring.drain();
         set_status(status, LA_ERR_TIMEOUT);
+    }
     if (GRAD && lo + len == nchunk) {  // the final state, for <S1, dS1> of the last chunk
         float m0, m1;
         row_max(m0, m1);
@@ -1660,8 +1681,10 @@ __global__ void __launch_bounds__(256, 1)
             ring.wait(it + 1);
     }
     cp_wait<0>();
-    if (!ring.ok && lane == 0)  // a copy did not arrive in time: the results are void
+    if (!ring.ok && lane == 0) {  // a copy did not arrive in time: the results are void
+        ring.drain();
         set_status(status, LA_ERR_TIMEOUT);
+    }
     float* to = ENDS ? seg.B + run * D * DV : dS0 && lo == 0 ? dS0 + bh * D * DV : nullptr;
     if (to) {
 #pragma unroll
@@ -1727,7 +1750,7 @@ __device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int 
 // a warp's wait: one verdict for all lanes
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity)
 {
-    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, kWaitPolls));
+    return __all_sync(0xffffffffu, wait_for(bar, parity));
 }
 
 // largest of c[0 .. n), by every lane of a warp
@@ -2197,10 +2220,13 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         if (tid == 0 && p == per - 1 && s + 1 < steps)
             load_rows(s + 1);
     }
-    if (!ok && tid == 0) {  // a copy never arrived: give the others their time, report, leave
+    if (!ok && tid == 0) {
+        // a copy did not arrive in time: the results are void.  Whatever else is in
+        // flight gets as long again before its shared memory goes
         for (int i = 0; i < 4; ++i)
             for (int parity = 0; parity < 2; ++parity)
-                sm100::mbar_wait(full + i, parity, kWaitPolls >> 3);
+                if (!wait_for(full + i, parity))
+                    break;
         set_status(status, LA_ERR_TIMEOUT);
     }
 }

@@ -205,6 +205,25 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// Wait for phase `parity` of a barrier, two seconds at most (the copies waited for are
+// a few microseconds old): false then, and the caller records LA_ERR_TIMEOUT.
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity)
+{
+    if (sm100::mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t until = now_ns() + 2000000000ull;
+    while (!sm100::mbar_try_wait(bar, parity))
+        if (now_ns() > until)
+            return false;
+    return true;
+}
+
 // 2^x on the hardware (2 ulp, denormals to zero)
 __device__ __forceinline__ float ex2(float x)
 {
