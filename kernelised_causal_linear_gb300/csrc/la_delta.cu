@@ -31,12 +31,24 @@ constexpr int kRecThreads = 256;
 constexpr int kRecCols = 32;  // columns per CTA
 constexpr int kRecTok = 32;   // tokens per staged block
 
+// Few long sequences are cut into segments of `len` tokens that run at once, each from
+// its own state.  The state is affine in the one before, column by column: a run from
+// zero gives a segment's constant part B, and d more columns without V that start as
+// the unit matrix its matrix M (carry: only these ends are wanted).
+struct Segments {
+    int count, first;    // segments that run, the first of them
+    int64_t len;         // a multiple of kRecTok
+    const float* start;  // [BH][count][d][dv], or NULL: one segment from S0
+    int carry;
+    float *B, *M;        // carry: [BH][count][d][dv], [BH][count][d][d]
+};
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kRecThreads)
     k_delta_rec(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                 const float* __restrict__ beta, const float* __restrict__ log_alpha,
                 T* __restrict__ out, const float* S0, float* S_out, float* __restrict__ chk,
-                float* __restrict__ err, int64_t N, int H, int Hk, int DV, int l2, float scale)
+                float* __restrict__ err, int64_t N, int H, int Hk, int DV, int l2, float scale, Segments seg)
 {
     __shared__ __align__(16) float sk[kRecTok][D];
     __shared__ __align__(16) float sq[kRecTok][D];
@@ -46,18 +58,23 @@ __global__ void __launch_bounds__(kRecThreads)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, col = warp * 4 + (lane & 3);
-    const int64_t bh = blockIdx.x;
+    const int64_t run = blockIdx.x, bh = run / seg.count;  // head and segment; head
+    const int64_t lo = (run % seg.count + seg.first) * seg.len, hi = min(N, lo + seg.len);
     const int c0 = blockIdx.y * kRecCols;
+    const bool unit = c0 >= DV;  // carry: columns of the unit matrix
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const T* qp = q ? q + kh * N * D : nullptr;
     const T* kp = k + kh * N * D;
-    const T* vp = v + bh * N * DV + c0;
+    const T* vp = unit ? nullptr : v + bh * N * DV + c0;
     const int64_t nblk = (N + kRecTok - 1) / kRecTok;
 
     float s[D / 8];
+    const float* start = seg.start ? seg.start + run * D * DV : S0 ? S0 + bh * D * DV : nullptr;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-        s[i] = S0 ? S0[(bh * D + (i / 4) * 32 + 4 * r + i % 4) * DV + c0 + col] : 0.0f;
+    for (int i = 0; i < D / 8; ++i) {
+        const int row = (i / 4) * 32 + 4 * r + i % 4;
+        s[i] = seg.carry ? (row == c0 - DV + col ? 1.0f : 0.0f) : start ? start[row * DV + c0 + col] : 0.0f;
+    }
 
     // a warp stages rows warp, warp + 8, ..
     constexpr int kRows = kRecTok / (kRecThreads / 32);
@@ -67,21 +84,22 @@ __global__ void __launch_bounds__(kRecThreads)
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int64_t t = b * kRecTok + warp + i * (kRecThreads / 32);
-            const bool live = t < N;
+            const bool live = t < hi;
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
                 nk[i][x] = live ? kp[t * D + lane + 32 * x] : from_f32<T>(0.f);
                 nq[i][x] = live && qp ? qp[t * D + lane + 32 * x] : from_f32<T>(0.f);
             }
-            nv[i] = live ? vp[t * DV + lane] : from_f32<T>(0.f);
+            nv[i] = live && !unit ? vp[t * DV + lane] : from_f32<T>(0.f);
             nb[i] = live ? beta[bh * N + t] : 0.f;
             na[i] = live && log_alpha ? log_alpha[bh * N + t] : 0.f;
         }
     };
-    fetch(0);
-    for (int64_t b = 0; b < nblk; ++b) {
+    const int64_t b0 = lo / kRecTok, b1 = (hi + kRecTok - 1) / kRecTok;
+    fetch(b0);
+    for (int64_t b = b0; b < b1; ++b) {
         const int64_t t0 = b * kRecTok;
-        const int n = (int)min((int64_t)kRecTok, N - t0);
+        const int n = (int)min((int64_t)kRecTok, hi - t0);
         __syncthreads();  // the previous block's tiles are read
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -114,7 +132,7 @@ __global__ void __launch_bounds__(kRecThreads)
                 salpha[t] = expf(na[i]);
             }
         }
-        if (b + 1 < nblk)
+        if (b + 1 < b1)
             fetch(b + 1);
         if (chk) {
 #pragma unroll
@@ -164,12 +182,20 @@ __global__ void __launch_bounds__(kRecThreads)
         }
         __syncwarp();
     }
+    float* end = nullptr;
+    int ld = DV;
+    if (seg.carry) {
+        end = unit ? seg.M + run * D * D - DV : seg.B + run * D * DV;  // unit column c is M's c - DV
+        ld = unit ? D : DV;
+    } else if (S_out && hi == N) {
+        end = S_out + bh * D * DV;
+    }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
         const int row = (i / 4) * 32 + 4 * r + i % 4;
-        if (S_out)
-            S_out[(bh * D + row) * DV + c0 + col] = s[i];
-        if (chk)
+        if (end)
+            end[(int64_t)row * ld + c0 + col] = s[i];
+        if (chk && hi == N)
             chk[((bh * (nblk + 1) + nblk) * D + row) * DV + c0 + col] = s[i];
     }
 }
@@ -290,7 +316,8 @@ __global__ void __launch_bounds__(kDecThreads)
 // e_i's right-hand side, and those products are q_i.dQ_i and v_i.dV_i).
 // S0 and E come from the recurrence above, which stored them.  Two kernels: the
 // columns of dS, Y and dV never mix, so k_delta_grad_rev runs the chunks in reverse
-// for 32 columns per CTA and keeps dS1, dV and the dots over its columns;
+// for 32 columns per CTA and keeps dS1, dV and the dots over its columns (over
+// segments like the recurrence: dS0 is affine in dS1, its matrix the transposed M);
 // k_delta_grad_dqk then takes every chunk on its own.  fp32 in shared memory, bound
 // by its reads.
 struct GradKept {
@@ -357,7 +384,7 @@ __global__ void __launch_bounds__(kRevThreads)
                      const T* __restrict__ dout, const float* __restrict__ dS_out,
                      const float* __restrict__ chk, const float* __restrict__ err, T* __restrict__ dv,
                      float* __restrict__ dS0, GradKept kept, int64_t N, int H, int Hk, int DV, int l2,
-                     float scale)
+                     float scale, Segments seg)
 {
     constexpr int C = kRecTok, LK = D + 4, LC = C + 4, R = D / 8;  // R: state rows per thread
     extern __shared__ __align__(16) float smem[];
@@ -372,25 +399,28 @@ __global__ void __launch_bounds__(kRevThreads)
     __shared__ float eg[C], ege[C], sb[C], red[8];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t bh = blockIdx.x;
+    const int64_t run = blockIdx.x, bh = run / seg.count;
+    const int64_t lo = (run % seg.count + seg.first) * seg.len, hi = min(N, lo + seg.len);
+    const bool ends = seg.carry;  // a run from dS = 0 that leaves the constant part in seg.B
     const int c0 = blockIdx.y * 32, nsl = gridDim.y;
     const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk);
     const int64_t nblk = (N + C - 1) / C;
 
     // a thread keeps rows warp R .. of column lane in registers too
     float ds[R];
+    const float* end = ends ? nullptr : seg.start ? seg.start + run * D * DV : dS_out ? dS_out + bh * D * DV : nullptr;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        ds[i] = dS_out ? dS_out[(bh * D + warp * R + i) * DV + c0 + lane] : 0.f;
+        ds[i] = end ? end[(warp * R + i) * DV + c0 + lane] : 0.f;
         dS[(warp * R + i) * 32 + lane] = ds[i];
     }
-    for (int64_t b = nblk - 1; b >= 0; --b) {
+    for (int64_t b = (hi - 1) / C; b >= lo / C; --b) {
         const int64_t t0 = b * C;
         const int n = (int)min((int64_t)C, N - t0);
         // dS1 out, <S1, dS1>
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < R && !ends; ++i) {
             const int64_t row = warp * R + i;
             kept.dS[((bh * nblk + b) * D + row) * DV + c0 + lane] = ds[i];
             if (log_alpha)
@@ -411,7 +441,7 @@ __global__ void __launch_bounds__(kRevThreads)
             sb[lane] = lane < n ? beta[bh * N + t0 + lane] : 0.f;
         }
         __syncthreads();
-        if (tid == 0) {
+        if (tid == 0 && !ends) {
             float x = 0.f;
             for (int w = 0; w < 8; ++w)
                 x += red[w];
@@ -493,7 +523,7 @@ __global__ void __launch_bounds__(kRevThreads)
             float y = sy[t * 32 + lane], db = 0.f, x = 0.f;
             const float g = sb[t] * y;
             sy[t * 32 + lane] = g;
-            if (t < n) {
+            if (t < n && !ends) {
                 const int64_t at = (bh * N + t0 + t) * DV + c0 + lane;
                 dv[at] = from_f32<T>(g);
                 kept.dV[at] = g;
@@ -505,7 +535,7 @@ __global__ void __launch_bounds__(kRevThreads)
                 db += __shfl_xor_sync(0xffffffffu, db, o);
                 x += __shfl_xor_sync(0xffffffffu, x, o);
             }
-            if (lane == 0 && t < n) {
+            if (lane == 0 && t < n && !ends) {
                 kept.bb[(bh * nsl + blockIdx.y) * N + t0 + t] = db;
                 kept.vv[(bh * nsl + blockIdx.y) * N + t0 + t] = x;
             }
@@ -532,10 +562,11 @@ __global__ void __launch_bounds__(kRevThreads)
         for (int i = 0; i < R; ++i)
             dS[(warp * R + i) * 32 + lane] = ds[i];
     }
-    if (dS0) {
+    float* to = ends ? seg.B + run * D * DV : dS0 && lo == 0 ? dS0 + bh * D * DV : nullptr;
+    if (to) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            dS0[(bh * D + warp * R + i) * DV + c0 + lane] = ds[i];
+            to[(warp * R + i) * DV + c0 + lane] = ds[i];
     }
 }
 
@@ -779,16 +810,73 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int64_t rec_blocks(int64_t N) { return (N + kRecTok - 1) / kRecTok; }
 
-template <int D, typename T>
-cudaError_t run_rec(const DeltaArgs& a, float* chk, float* err)
+// Segments of a sequence on this path (1: whole), and their tokens: as many as give
+// two CTAs per SM at 152 SMs, none under 256 tokens, at most 32 (they are joined one
+// after the other), at least 4 to pay for the second run (fp32 B1 H4 N16384 d = 64:
+// 3097 us whole, 473 us cut).  By sizes alone, as workspaces are sized without the GPU.
+int rec_segments(const DeltaArgs& a, int64_t* len)
 {
-    const dim3 grid((unsigned)(a.B * a.H), (unsigned)(a.dv / kRecCols));
+    const int64_t slices = a.B * a.H * (a.dv / kRecCols);
+    int64_t n = 2 * 152 / slices;
+    n = n < a.N / 256 ? n : a.N / 256;
+    n = n < 32 ? n : 32;
+    *len = (a.N + kRecTok - 1) / kRecTok * kRecTok;
+    if (n < 4)
+        return 1;
+    *len = ((a.N + n - 1) / n + kRecTok - 1) / kRecTok * kRecTok;
+    return (int)((a.N + *len - 1) / *len);
+}
+
+struct RecLayout {
+    size_t start, B, M, total;
+};
+RecLayout rec_layout(const DeltaArgs& a)
+{
+    int64_t len;
+    const size_t n = (size_t)rec_segments(a, &len), BH = (size_t)(a.B * a.H);
+    RecLayout l = {};
+    if (n > 1) {
+        l.B = up256(BH * n * a.d * a.dv * 4);
+        l.M = l.B + up256(BH * n * a.d * a.dv * 4);
+        l.total = l.M + up256(BH * n * a.d * a.d * 4);
+    }
+    return l;
+}
+
+template <int D, typename T>
+cudaError_t launch_rec(const DeltaArgs& a, float* chk, float* err, const Segments& seg)
+{
+    const dim3 grid((unsigned)(a.B * a.H * seg.count), (unsigned)((a.dv + (seg.carry ? a.d : 0)) / kRecCols));
     k_delta_rec<D, T><<<grid, kRecThreads, 0, a.stream>>>(
         static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.beta,
         a.log_alpha, static_cast<T*>(a.out), a.S0, a.S_out, chk, err, a.N, (int)a.H, (int)a.Hk,
-        a.dv, a.fm == LA_FM_L2, a.scale);
+        a.dv, a.fm == LA_FM_L2, a.scale, seg);
     count_launches(1);
     return cudaGetLastError();
+}
+
+// The recurrence, over segments (ws: rec_layout) where there are any; a gradient
+// (chk) wants the last segment's M too.
+template <int D, typename T>
+cudaError_t run_rec(const DeltaArgs& a, float* chk, float* err, unsigned char* ws)
+{
+    Segments seg = {1, 0, 0, nullptr, 0, nullptr, nullptr};
+    const int n = rec_segments(a, &seg.len);
+    if (n > 1) {
+        const RecLayout l = rec_layout(a);
+        float* start = reinterpret_cast<float*>(ws + l.start);
+        float* B = reinterpret_cast<float*>(ws + l.B);
+        float* M = reinterpret_cast<float*>(ws + l.M);
+        const int m = chk ? n : n - 1;
+        const Segments ends = {m, 0, seg.len, nullptr, 1, B, M};
+        DeltaArgs f = a;
+        f.q = nullptr, f.out = nullptr, f.S_out = nullptr;
+        cudaError_t e = launch_rec<D, T>(f, nullptr, nullptr, ends);
+        if (e != cudaSuccess || (e = delta::join_segments(a, false, a.S0, B, M, start, n, m)) != cudaSuccess)
+            return e;
+        seg.count = n, seg.start = start;
+    }
+    return launch_rec<D, T>(a, chk, err, seg);
 }
 
 template <int D, int CS, typename T>
@@ -814,7 +902,7 @@ cudaError_t run_decode(const DeltaArgs& a)
 }
 
 struct GradLayout {
-    size_t chk, err, dq, dk, dS, dV, bb, vv, cd, total;
+    size_t chk, err, dq, dk, dS, dV, bb, vv, cd, seg, total;
 };
 GradLayout grad_layout(const DeltaArgs& a)
 {
@@ -835,7 +923,8 @@ GradLayout grad_layout(const DeltaArgs& a)
     l.bb = take(BH * sl * N);
     l.vv = take(BH * sl * N);
     l.cd = take(BH * sl * nb);
-    l.total = at;
+    l.seg = at;
+    l.total = at + rec_layout(a).total;
     return l;
 }
 
@@ -848,7 +937,7 @@ cudaError_t run_grad(const DeltaArgs& a)
     const GradKept kept = {f32(l.dS), f32(l.dV), f32(l.bb), f32(l.vv), f32(l.cd)};
     DeltaArgs f = a;
     f.out = nullptr, f.S_out = nullptr;
-    cudaError_t e = run_rec<D, T>(f, f32(l.chk), f32(l.err));
+    cudaError_t e = run_rec<D, T>(f, f32(l.chk), f32(l.err), ws + l.seg);
     if (e != cudaSuccess)
         return e;
     const size_t rev = rev_smem<D>(), dqk = GradSmem<D, DV>::bytes;
@@ -862,12 +951,26 @@ cudaError_t run_grad(const DeltaArgs& a)
     const T* dout = static_cast<const T*>(a.dout);
     const int l2 = a.fm == LA_FM_L2, H = (int)a.H, Hk = (int)a.Hk;
     const int64_t BH = a.B * a.H;
-    k_delta_grad_rev<D, T><<<dim3((unsigned)BH, DV / 32), kRevThreads, rev, a.stream>>>(
-        q, k, static_cast<const T*>(a.v), a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
-        static_cast<T*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale);
-    count_launches(1);
-    e = cudaGetLastError();
-    if (e != cudaSuccess)
+    Segments seg = {1, 0, 0, nullptr, 0, nullptr, nullptr};
+    const int n = rec_segments(a, &seg.len);
+    auto reverse = [&](const Segments& x) {
+        k_delta_grad_rev<D, T><<<dim3((unsigned)(BH * x.count), DV / 32), kRevThreads, rev, a.stream>>>(
+            q, k, static_cast<const T*>(a.v), a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
+            static_cast<T*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale, x);
+        count_launches(1);
+        return cudaGetLastError();
+    };
+    if (n > 1) {  // M is where the recurrence's run left it
+        const RecLayout r = rec_layout(a);
+        float* start = f32(l.seg + r.start);
+        float* C = f32(l.seg + r.B);
+        const Segments ends = {n - 1, 1, seg.len, nullptr, 1, C, nullptr};
+        if ((e = reverse(ends)) != cudaSuccess ||
+            (e = delta::join_segments(a, true, a.dS_out, C, f32(l.seg + r.M), start, n, n)) != cudaSuccess)
+            return e;
+        seg.count = n, seg.start = start;
+    }
+    if ((e = reverse(seg)) != cudaSuccess)
         return e;
     k_delta_grad_dqk<D, DV, T><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
         q, k, a.beta, a.log_alpha, dout, f32(l.chk), f32(l.err), kept, f32(l.dq), f32(l.dk), a.dbeta,
@@ -930,7 +1033,9 @@ bool backward_on_tensor_cores(const DeltaArgs& a) { return a.dtype == LA_BF16; }
 // By type and length alone: a size asked for without the GPU at hand serves there.
 size_t delta_forward_workspace(const DeltaArgs& a)
 {
-    return a.dtype == LA_BF16 && a.N > kShort ? delta_tc_forward_workspace(a) : 0;
+    if (a.dtype != LA_BF16)
+        return rec_layout(a).total;
+    return a.N > kShort ? delta_tc_forward_workspace(a) : 0;
 }
 
 size_t delta_backward_workspace(const DeltaArgs& a)
@@ -942,11 +1047,12 @@ cudaError_t delta_forward(const DeltaArgs& a)
 {
     if (forward_on_tensor_cores(a))
         return delta_tc_forward(a);
-    const bool bf = a.dtype == LA_BF16;
+    const bool bf = a.dtype == LA_BF16;  // short: one segment
+    unsigned char* ws = static_cast<unsigned char*>(a.ws);
     switch (a.d) {
-    case 32: return bf ? run_rec<32, __nv_bfloat16>(a, nullptr, nullptr) : run_rec<32, float>(a, nullptr, nullptr);
-    case 64: return bf ? run_rec<64, __nv_bfloat16>(a, nullptr, nullptr) : run_rec<64, float>(a, nullptr, nullptr);
-    default: return bf ? run_rec<128, __nv_bfloat16>(a, nullptr, nullptr) : run_rec<128, float>(a, nullptr, nullptr);
+    case 32: return bf ? run_rec<32, __nv_bfloat16>(a, nullptr, nullptr, ws) : run_rec<32, float>(a, nullptr, nullptr, ws);
+    case 64: return bf ? run_rec<64, __nv_bfloat16>(a, nullptr, nullptr, ws) : run_rec<64, float>(a, nullptr, nullptr, ws);
+    default: return bf ? run_rec<128, __nv_bfloat16>(a, nullptr, nullptr, ws) : run_rec<128, float>(a, nullptr, nullptr, ws);
     }
 }
 

@@ -13,5 +13,10 @@ constexpr float kL2Eps = 1e-6f;
 // them, is a full reset, and running sums stay finite.  NaN passes through.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -128.0f ? -128.0f : g; }
 
+// From segments' ends to their starts: S_{i+1} = M_i S_i + B_i from S_0 (mcount M and B
+// per head), or with rev dS_{i-1} = M_i^T dS_i + C_i from the last (B: n - 1 C per head).
+cudaError_t join_segments(const DeltaArgs& a, bool rev, const float* from, const float* B, const float* M, float* start,
+                          int n, int mcount);
+
 }  // namespace delta
 }  // namespace la

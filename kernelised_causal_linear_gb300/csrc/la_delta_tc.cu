@@ -2527,6 +2527,23 @@ cudaError_t backward_dims(const DeltaArgs& a)
 }  // namespace
 
 
+namespace delta {
+
+cudaError_t join_segments(const DeltaArgs& a, bool rev, const float* from, const float* B, const float* M, float* start,
+                          int n, int mcount)
+{
+    switch (a.d) {
+    case 32: return rev ? launch_join<32, true>(a, from, B, M, start, n, mcount)
+                        : launch_join<32, false>(a, from, B, M, start, n, mcount);
+    case 64: return rev ? launch_join<64, true>(a, from, B, M, start, n, mcount)
+                        : launch_join<64, false>(a, from, B, M, start, n, mcount);
+    default: return rev ? launch_join<128, true>(a, from, B, M, start, n, mcount)
+                        : launch_join<128, false>(a, from, B, M, start, n, mcount);
+    }
+}
+
+}  // namespace delta
+
 size_t delta_tc_forward_workspace(const DeltaArgs& a) { return tc_layout(a).total; }
 
 cudaError_t delta_tc_forward(const DeltaArgs& a)

@@ -483,14 +483,15 @@ def test_backward_more_chunks_than_sms(B, H, Hk, N, d, dv):
     check_backward(problem(B, H, Hk, N, d, dv, BF, N + dv))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("B,H,Hk,N,d,dv,gated,state", [
     (1, 1, 1, 2048, 64, 64, True, True), (1, 2, 1, 2100, 128, 32, True, False),
     (1, 3, 3, 2623, 32, 128, False, True), (2, 1, 1, 3000, 64, 128, True, True),
     (1, 4, 2, 2561, 128, 128, True, True), (1, 1, 1, 2111, 32, 32, True, False)])
-def test_few_sequences_in_segments(B, H, Hk, N, d, dv, gated, state):
+def test_few_sequences_in_segments(B, H, Hk, N, d, dv, gated, state, dtype):
     """Few heads over many chunks: segments that run at once from the states their
     ends' maps give; the last segment is short."""
-    p = problem(B, H, Hk, N, d, dv, BF, N, gated, state)
+    p = problem(B, H, Hk, N, d, dv, dtype, N, gated, state)
     check_forward(p)
     check_backward(p)
     _, S = la.la_forward_delta(None, *(p[n] for n in INPUTS[1:]), S0=p["S0"])
