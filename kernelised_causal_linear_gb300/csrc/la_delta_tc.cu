@@ -99,7 +99,10 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // spare over the largest |A|; a stable recurrence does not grow that far).  Decays of
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
-// Issue-bound; on the CUDA cores the off-diagonal blocks alone were a quarter of it.
+// Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
+// value heads per key head), 3.8 TB/s of its own bytes; short stretches between six
+// barriers with four blocks per SM, 36% of issue slots used.  (On the CUDA cores the
+// off-diagonal blocks alone were a quarter of it.)
 constexpr int kPrepThreads = 128;
 
 template <int D, bool GRAD>
@@ -485,8 +488,12 @@ __global__ void __launch_bounds__(kPrepThreads)
 // columns of the update) and half of the chunk's token tiles (0 and 3, or 1 and 2:
 // equal shares of the triangular products).  They exchange fp32 sums through shared
 // memory three times a chunk.  A warp's products follow one another, each waiting
-// for the last: with a slice per warp a chunk is 7100 cycles at d = 128 of which
+// for the last: with a slice per warp a chunk was 7100 cycles at d = 128 of which
 // the tensor core works 3100, so two warps shorten it where there are SMs to spare.
+// Measured: 277 us for the 128 chunks of B4 H8 N8192 d=128 (SP = 2: 4300 cycles per
+// chunk, tensor cores of the warps' sub-partitions 36% busy, bound by the latency of
+// its dependent products and conversions), 683 us for B16 H32 N2011 (SP = 1: four
+// rounds of 152 CTAs, tensor cores 60% busy).
 //
 // With two warps on a sub-partition (SP = 1, eight warps) no barrier spans the CTA
 // inside the loop: the warp that is last to finish with a stage asks for the chunk
@@ -1254,6 +1261,9 @@ __global__ void __launch_bounds__(256)
 // Over segments as in k_delta_chain: dS0 is affine in dS1, and its matrix over a
 // segment is the transpose of the M that the states' run gave.  ENDS: a run from
 // dS = 0 that leaves each segment's constant part in seg.B and nothing else.
+//
+// Measured: 485 us at B4 H8 N8192 d=128 (7600 cycles per chunk, twice the chain's
+// products), 306 to 330 us at B8 H32 N1037; bound like the chain.
 template <int D, int SP>
 struct RevSmem {
     static constexpr int stages = 2;
@@ -1717,7 +1727,10 @@ __global__ void __launch_bounds__(256, 1)
 // A CTA per SM takes every gridDim-th chunk.  Its loads run a step (one value head
 // of one chunk) ahead: the token planes have two buffers; the state planes are used
 // first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
-// waiting for its own 150 KB: 508 against 330 us at B4 H8 N8192 d=128.)
+// waiting for its own 150 KB: 508 against 399 us at B4 H8 N8192 d=128.)  Measured there:
+// 378 us for 4096 chunks, 1.6 TB/s of 5.9e8 bytes; the loads alone take 165 us, the
+// rest is a step's dependent stretches between its barriers (issue slots 40% used,
+// a quarter of the stalls at barriers: the dK warps have the longer share).
 constexpr int kDqkThreads = 512;
 
 template <int D, int DV>
