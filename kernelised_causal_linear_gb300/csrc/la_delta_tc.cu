@@ -100,8 +100,9 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
 // Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
-// value heads per key head), 3.8 TB/s of its own bytes; short stretches between six
-// barriers with four blocks per SM, 36% of issue slots used.  (On the CUDA cores the
+// value heads per key head).  By counters on 16 x 32 heads of 512 tokens 40% of the
+// issue slots are used, DRAM moves 3.2 TB/s and the tensor cores are 18% busy: short
+// stretches between barriers, with four blocks per SM.  (On the CUDA cores the
 // off-diagonal blocks alone were a quarter of it.)
 constexpr int kPrepThreads = 128;
 
@@ -491,9 +492,10 @@ __global__ void __launch_bounds__(kPrepThreads)
 // for the last: with a slice per warp a chunk was 7100 cycles at d = 128 of which
 // the tensor core works 3100, so two warps shorten it where there are SMs to spare.
 // Measured: 277 us for the 128 chunks of B4 H8 N8192 d=128 (SP = 2: 4300 cycles per
-// chunk, tensor cores of the warps' sub-partitions 36% busy, bound by the latency of
-// its dependent products and conversions), 683 us for B16 H32 N2011 (SP = 1: four
-// rounds of 152 CTAs, tensor cores 60% busy).
+// chunk, tensor cores 36% busy on an SM, bound by the latency of its dependent
+// products and conversions), 680 to 700 us for B16 H32 N2011 (SP = 1: 512 CTAs at one
+// per SM are 3.4 rounds of 152; at N = 512 the busiest SM's tensor cores work 57% of
+// the time, 48% on average).
 //
 // With two warps on a sub-partition (SP = 1, eight warps) no barrier spans the CTA
 // inside the loop: the warp that is last to finish with a stage asks for the chunk
@@ -1262,8 +1264,8 @@ __global__ void __launch_bounds__(256)
 // segment is the transpose of the M that the states' run gave.  ENDS: a run from
 // dS = 0 that leaves each segment's constant part in seg.B and nothing else.
 //
-// Measured: 485 us at B4 H8 N8192 d=128 (7600 cycles per chunk, twice the chain's
-// products), 306 to 330 us at B8 H32 N1037; bound like the chain.
+// Measured: 485 us at B4 H8 N8192 d=128 (7600 cycles per chunk; 1.7 times the
+// forward chain's instructions), 306 to 332 us at B8 H32 N1037; bound like the chain.
 template <int D, int SP>
 struct RevSmem {
     static constexpr int stages = 2;
@@ -1729,8 +1731,8 @@ __global__ void __launch_bounds__(256, 1)
 // first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
 // waiting for its own 150 KB: 508 against 399 us at B4 H8 N8192 d=128.)  Measured there:
 // 378 us for 4096 chunks, 1.6 TB/s of 5.9e8 bytes; the loads alone take 165 us, the
-// rest is a step's dependent stretches between its barriers (issue slots 40% used,
-// a quarter of the stalls at barriers: the dK warps have the longer share).
+// rest is a step's dependent stretches between its barriers (40% of the issue slots
+// used, a quarter of a warp's cycles per instruction at barriers).
 constexpr int kDqkThreads = 512;
 
 template <int D, int DV>
