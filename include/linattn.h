@@ -265,6 +265,9 @@ LA_API la_status la_favor_features(const void* x, const float* w, void* out, int
                                    int r, int in_dtype, int out_dtype, la_stream_t stream);
 
 /*
+ * The calls from here to la_norm_gate_backward: but for S_out in the place of
+ * S0, no output may overlap an input or another output.
+ *
  * Gated delta rule: the state corrects what it holds for a key instead of
  * adding to it.  With a_t = exp(log_alpha_t) and k_t, q_t the mapped rows,
  *     e_t = v_t - a_t S_{t-1}^T k_t,

@@ -366,6 +366,12 @@ def _arg(t: torch.Tensor | None, name: str, shape, dtype, index: int) -> int | N
     return t.data_ptr()
 
 
+def _apart(name: str, out: int | None, *inputs) -> None:
+    """An output may not be one of the inputs: other blocks still read those."""
+    if out and out in inputs:
+        raise ValueError(f"{name} shares its memory with an input")
+
+
 def _current(t: torch.Tensor, name: str) -> int:
     """The device of a call: its tensors' device, which has to be the current one."""
     index = t.get_device()
@@ -457,6 +463,7 @@ def la_forward_delta(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
             _arg(log_alpha, "log_alpha", gates, f32, dev),
             _arg(out, "out", (B, H, N, dv), k.dtype, dev), _arg(S0, "S0", state, f32, dev),
             _arg(S_out, "S_out", state, f32, dev))
+    _apart("out", ptrs[5], *ptrs[:3])
     ws = call.scratch(workspace, la_delta_workspace_size(B, H, Hk, N, d, dv, k.dtype))
     code = _lib.la_forward_delta(*ptrs, B, H, Hk, N, d, dv, _fm(feature_map),
                                  d ** -0.5 if scale is None else float(scale), _dtype(k), *ws,
@@ -479,12 +486,13 @@ def la_decode_step_delta(S: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     if out is None:
         out = call.empty((B, H, dv), k.dtype)
     f32 = torch.float32
+    ptrs = (_arg(S, "S", (B, H, d, dv), f32, dev), _arg(q, "q", k.shape, k.dtype, dev),
+            _arg(k, "k", k.shape, k.dtype, dev), _arg(v, "v", (B, H, dv), k.dtype, dev),
+            _arg(beta, "beta", (B, H), f32, dev), _arg(log_alpha, "log_alpha", (B, H), f32, dev),
+            _arg(out, "out", (B, H, dv), k.dtype, dev))
+    _apart("out", ptrs[6], *ptrs[1:4])
     code = _lib.la_decode_step_delta(
-        _arg(S, "S", (B, H, d, dv), f32, dev), _arg(q, "q", k.shape, k.dtype, dev),
-        _arg(k, "k", k.shape, k.dtype, dev), _arg(v, "v", (B, H, dv), k.dtype, dev),
-        _arg(beta, "beta", (B, H), f32, dev), _arg(log_alpha, "log_alpha", (B, H), f32, dev),
-        _arg(out, "out", (B, H, dv), k.dtype, dev), B, H, Hk, d, dv, _fm(feature_map),
-        d ** -0.5 if scale is None else float(scale), _dtype(k), call.handle)
+        *ptrs, B, H, Hk, d, dv, _fm(feature_map), d ** -0.5 if scale is None else float(scale), _dtype(k), call.handle)
     _check(code, "la_decode_step_delta")
     return out
 
@@ -550,11 +558,11 @@ def la_norm_gate(x: torch.Tensor, gate: torch.Tensor | None = None,
         y = call.empty((B, N, H, dv), dtype)
     _dtype(y)
     w, heads = _norm_weight(weight, H, dv, dev)
-    code = _lib.la_norm_gate(_arg(x, "x", x.shape, x.dtype, dev),
-                             _arg(gate, "gate", (B, N, H, dv), dtype, dev), w,
-                             _arg(y, "y", (B, N, H, dv), dtype, dev), B, H, N, dv,
-                             _act(activation), heads, float(eps), _dtype(x), DTYPES[dtype],
-                             call.handle)
+    ptrs = (_arg(x, "x", x.shape, x.dtype, dev), _arg(gate, "gate", (B, N, H, dv), dtype, dev), w,
+            _arg(y, "y", (B, N, H, dv), dtype, dev))
+    _apart("y", ptrs[3], *ptrs[:2])
+    code = _lib.la_norm_gate(*ptrs, B, H, N, dv, _act(activation), heads, float(eps), _dtype(x),
+                             DTYPES[dtype], call.handle)
     _check(code, "la_norm_gate")
     return y
 

@@ -499,3 +499,72 @@ def test_few_sequences_in_segments(B, H, Hk, N, d, dv, gated, state, dtype):
     _, S2 = la.la_forward_delta(*(p[n] for n in INPUTS), S0=St, S_out=St)
     # the state-only run and the run with outputs differ in nothing that enters S
     assert torch.equal(S, S2)
+
+
+def test_an_output_in_an_inputs_place_is_refused():
+    x = torch.zeros(1, 2, 40, 64, device="cuda", dtype=BF)
+    b = torch.zeros(1, 2, 40, device="cuda")
+    for kw in (dict(q=x.clone(), k=x.clone(), v=x), dict(q=x, k=x.clone(), v=x.clone()),
+               dict(q=x.clone(), k=x, v=x.clone())):
+        with pytest.raises(ValueError, match="shares"):
+            la.la_forward_delta(*kw.values(), b, out=x)
+        with pytest.raises(ValueError, match="shares"):
+            y = x[:, :, 0].contiguous()
+            one = {n: y if t is x else t[:, :, 0].contiguous() for n, t in kw.items()}
+            la.la_decode_step_delta(torch.zeros(1, 2, 64, 64, device="cuda"), *one.values(),
+                                    b[:, :, 0].contiguous(), out=y)
+
+
+@pytest.mark.parametrize("dtype,H,N", [(BF, 2100, 8100), (F32, 16600, 1025)])
+def test_offsets_past_32_bits(dtype, H, N):
+    """v, out and their gradients hold more than 2^31 elements.  Every head has
+    the same inputs and the same arithmetic, so every head's result is the
+    first's bit for bit, and the first is right by a call of a few heads."""
+    if torch.cuda.mem_get_info()[0] < (140 << 30):
+        pytest.skip("needs 140 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(11)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")
+    q, k, v1, do1 = (n(1, 1, N, w).to(dtype) for w in (32, 32, 128, 128))
+    beta1, la1 = torch.sigmoid(n(1, 1, N)), -torch.nn.functional.softplus(n(1, 1, N) - 2)
+    few = 512  # enough heads for the same path: no segments, one warp per slice
+
+    def run(heads):
+        v, do, beta, gate = (t.expand(-1, heads, *t.shape[2:]).contiguous()
+                             for t in (v1, do1, beta1, la1))
+        out, S = la.la_forward_delta(q, k, v, beta, gate, return_state=True)
+        return out, S, *la.la_backward_delta(do, q, k, v, beta, gate)[:5]
+
+    want = run(few)
+    got = run(H)
+    assert got[0].numel() > 2 ** 31
+    for i, (w, x) in enumerate(zip(want, got)):
+        if i in (2, 3):  # dq, dk: sums over the heads that share the key head
+            # fp32 sums of H equal numbers, one rounding to dtype on each side
+            tol = torch.finfo(dtype).eps + 2 * H * 2.0 ** -24
+            a, b = w.double() / few, x.double() / H
+            assert (a - b).norm() <= tol * a.norm(), i
+            continue
+        assert torch.equal(x[:, :1], w[:, :1]), i
+        for h in range(1, H, 64):
+            part = x[:, h:h + 64]
+            assert torch.equal(part, x[:, :1].expand_as(part)), (i, h)
+
+
+def test_decode_offsets_past_32_bits():
+    """The states hold more than 2^31 elements."""
+    B, H = 131073 // 3, 3
+    if torch.cuda.mem_get_info()[0] < (30 << 30):
+        pytest.skip("needs 30 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")
+    S1, q1, k1, v1 = n(1, H, 128, 128), n(1, H, 128).to(BF), n(1, H, 128).to(BF), n(1, H, 128).to(BF)
+    b1, a1 = torch.sigmoid(n(1, H)), -torch.sigmoid(n(1, H))
+    many = lambda t: t.expand(B, *t.shape[1:]).contiguous()
+    S = many(S1)
+    assert S.numel() > 2 ** 31
+    out = la.la_decode_step_delta(S, *(many(t) for t in (q1, k1, v1, b1, a1)))
+    want = la.la_decode_step_delta(S1, q1, k1, v1, b1, a1)
+    assert torch.equal(out, want.expand_as(out))
+    for i in range(0, B, 4096):
+        part = S[i:i + 4096]
+        assert torch.equal(part, S1.expand_as(part)), i

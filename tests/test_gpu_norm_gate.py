@@ -145,3 +145,32 @@ def test_graph_and_stream():
         y3.zero_()
         graph.replay()
         assert torch.equal(y, y3) and all(torch.equal(a, b) for a, b in zip(grads, g3))
+
+
+def test_an_output_in_an_inputs_place_is_refused():
+    x = torch.zeros(1, 2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="shares"):
+        la.la_norm_gate(x, x.clone(), y=x)
+    with pytest.raises(ValueError, match="shares"):
+        la.la_norm_gate(x.clone(), x, y=x)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: every batch row has the same inputs, so the same
+    results bit for bit, and the first row's are those of a call of its own."""
+    if torch.cuda.mem_get_info()[0] < (60 << 30):
+        pytest.skip("needs 60 GB of device memory")
+    B, H, N, dv = 257, 8, 8192, 128
+    g = torch.Generator(device="cuda").manual_seed(13)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    x1, g1, dy1 = n(1, H, N, dv), n(1, N, H, dv), n(1, N, H, dv)
+    w = torch.randn(H, dv, generator=g, device="cuda")
+    many = lambda t: t.expand(B, *t.shape[1:]).contiguous()
+    x, gate, dy = many(x1), many(g1), many(dy1)
+    assert x.numel() > 2 ** 31
+    got = (la.la_norm_gate(x, gate, w), *la.la_norm_gate_backward(dy, x, gate, w)[:2])
+    want = (la.la_norm_gate(x1, g1, w), *la.la_norm_gate_backward(dy1, x1, g1, w)[:2])
+    for a, b in zip(got, want):
+        for i in range(0, B, 32):
+            part = a[i:i + 32]
+            assert torch.equal(part, b.expand_as(part)), i
