@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kGradThreads)
                      const float* __restrict__ log_alpha, const T* __restrict__ dout,
                      const float* __restrict__ chk, const float* __restrict__ err, GradKept kept,
                      float* __restrict__ dq, float* __restrict__ dk, float* __restrict__ dbeta,
-                     float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale)
+                     float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale, int zero_start)
 {
     using SM = GradSmem<D, DV>;
     constexpr int C = SM::C, LS = SM::LS, LK = SM::LK, LV = SM::LV, LC = SM::LC, CX = D / 16;
@@ -749,8 +749,8 @@ __global__ void __launch_bounds__(kGradThreads)
         }
         if (lane < n) {
             dbeta[bh * N + t0 + lane] = db;
-            if (dlog_alpha)
-                dlog_alpha[bh * N + t0 + lane] = y + after;
+            if (dlog_alpha)  // a first gate on a zero state has no gradient, the sums leave their rounding
+                dlog_alpha[bh * N + t0 + lane] = zero_start && t0 + lane == 0 ? 0.f : y + after;
         }
     }
     __syncthreads();
@@ -976,7 +976,7 @@ cudaError_t run_grad(const DeltaArgs& a)
         return e;
     k_delta_grad_dqk<D, DV, T><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
         q, k, a.beta, a.log_alpha, dout, f32(l.chk), f32(l.err), kept, f32(l.dq), f32(l.dk), a.dbeta,
-        a.dlog_alpha, a.N, H, Hk, l2, a.scale);
+        a.dlog_alpha, a.N, H, Hk, l2, a.scale, !a.S0);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess)

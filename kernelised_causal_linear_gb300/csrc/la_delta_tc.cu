@@ -1785,7 +1785,7 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     k_delta_dqk(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ dout, Kept kept, __nv_bfloat16* __restrict__ dq,
                 __nv_bfloat16* __restrict__ dk, float* __restrict__ dbeta, float* __restrict__ dlog_alpha,
-                int64_t N, int nchunk, int items, int H, int Hk, int l2, float scale, int* status)
+                int64_t N, int nchunk, int items, int H, int Hk, int l2, float scale, int zero_start, int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = DqkSmem<D, DV>;
@@ -2154,8 +2154,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                             z[h] += y;
                     }
                     const int t = lane + 32 * h;
-                    if (t < n)
-                        dlog_alpha[bh * N + t0 + t] = z[h] + after;
+                    if (t < n)  // a first gate on a zero state has no gradient, the sums leave their rounding
+                        dlog_alpha[bh * N + t0 + t] = zero_start && t0 + t == 0 ? 0.f : z[h] + after;
                     after += __shfl_sync(0xffffffffu, z[h], 0);
                 }
             }
@@ -2524,7 +2524,7 @@ cudaError_t run_backward(const DeltaArgs& a)
     k_delta_dqk<D, DV><<<(unsigned)(items < sms ? items : sms), kDqkThreads, DqkSmem<D, DV>::bytes, a.stream>>>(
         ws + l.rows, ws + l.blobs, dout, kept, static_cast<__nv_bfloat16*>(a.dq),
         static_cast<__nv_bfloat16*>(a.dk), a.dbeta, a.dlog_alpha, a.N, n, (int)items, H, Hk, l2, a.scale,
-        a.status);
+        !a.S0, a.status);
     count_launches(1);
     return cudaGetLastError();
 }

@@ -568,3 +568,14 @@ def test_decode_offsets_past_32_bits():
     for i in range(0, B, 4096):
         part = S[i:i + 4096]
         assert torch.equal(part, S1.expand_as(part)), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [1, 2, 130])
+def test_the_first_gate_of_a_zero_start_has_no_gradient(N, dtype):
+    """It multiplies a zero state: exactly 0, which is all there is at N = 1."""
+    p = problem(2, 4, 2, N, 64, 64, dtype, 14, state=False)
+    got = check_backward(p)
+    assert (got[4][:, :, 0] == 0).all()
+    if N > 1:
+        assert (got[4][:, :, 1:] != 0).any()
