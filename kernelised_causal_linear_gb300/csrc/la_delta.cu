@@ -813,19 +813,26 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t rec_blocks(int64_t N) { return (N + kRecTok - 1) / kRecTok; }
 
 // Segments of a sequence on this path (1: whole), and their tokens: as many as give
-// two CTAs per SM at 152 SMs, none under 256 tokens, at most 32 (they are joined one
-// after the other), at least 4 to pay for the second run (fp32 B1 H4 N16384 d = 64:
-// 3097 us whole, 473 us cut).  By sizes alone, as workspaces are sized without the GPU.
+// two CTAs per SM at 152 SMs, at least 4 to pay for the second run, at most 32 (they
+// are joined one after the other, about 1 us each), of at least 64 tokens, or 32 in a
+// short sequence.  Forward and gradient, whole and cut: B1 H4 d = 64, N = 160 33 and
+// 120 against 22 and 80 us, N = 1000 192 and 590 against 54 and 142 us; B1 H4 N512
+// d = 128 131 and 433 against 65 and 187 us (83 and 201 us in segments of 32); with
+// as few as four the forward may lose (B2 H8 N1000 d = 128: 254 against 276 us) what
+// the gradient gains (1045 against 891 us).  By sizes alone, as workspaces are sized without the GPU.
 int rec_segments(const DeltaArgs& a, int64_t* len)
 {
     const int64_t slices = a.B * a.H * (a.dv / kRecCols);
+    const int64_t least = a.N > 256 ? 2 * kRecTok : kRecTok;
     int64_t n = 2 * 152 / slices;
-    n = n < a.N / 256 ? n : a.N / 256;
+    n = n < a.N / kRecTok ? n : a.N / kRecTok;
     n = n < 32 ? n : 32;
     *len = (a.N + kRecTok - 1) / kRecTok * kRecTok;
     if (n < 4)
         return 1;
     *len = ((a.N + n - 1) / n + kRecTok - 1) / kRecTok * kRecTok;
+    if (*len < least)
+        *len = least;
     return (int)((a.N + *len - 1) / *len);
 }
 

@@ -1163,88 +1163,132 @@ __global__ void __launch_bounds__(256, 1)
 
 // The states before the segments of a sequence from their ends, S_{i+1} = M_i S_i + B_i
 // from S_0, or (REV) the gradients of the states after them, dS_{i-1} = M_i^T dS_i + C_i
-// from that of the last.  A CTA owns 32 columns; a thread D / 8 rows of one.  The next M
-// comes into shared memory and the next B into registers while a step runs (read from
-// L2 as it was wanted, M made a step 13 us at d = 128).
-template <int D>
-constexpr int join_smem()
-{
-    return (2 * D * D + D * 32) * 4;
-}
+// from that of the last.  The steps follow one another, so a step is cut as fine as it
+// goes: a CTA owns 8 columns, a warp D / 8 rows of M, a lane D / 32 columns of M; lane
+// 4 g + t of a warp holds the state's column g in rows t, t + 4, .. of the warp's.  The
+// next M and B come into registers while a step runs, each row as the one before it is
+// used up.
+constexpr int kJoinCols = 8;
 
 template <int D, bool REV>
 __global__ void __launch_bounds__(256)
     k_delta_join(const float* __restrict__ S0, const float* __restrict__ B, const float* __restrict__ M,
                  float* __restrict__ start, int count, int mcount, int DV)
 {
-    constexpr int R = D / 8;
-    extern __shared__ __align__(16) float sm[];
-    float* sM = sm;               // [2][D][D]
-    float* sS = sm + 2 * D * D;   // [D][32]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int V = D / 32, RW = D / 8, LS = D + 4;  // M's columns per lane, rows per warp
+    // the state by columns, twice; REV: the warps' parts of the next, and the state's rows
+    __shared__ __align__(16) float sm[REV ? 8 * 8 * LS + 8 * D : 2 * 8 * LS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int64_t bh = blockIdx.x;
-    const int c = blockIdx.y * 32 + lane;
-    float x[R], next[R];
+    const int c = blockIdx.y * kJoinCols + g, row0 = warp * RW + t;
+    float x[RW / 4], next[RW / 4], m[RW][V];
     // step i leads out of segment `of`; M and B have mcount segments, C count - 1 (not
     // the first)
-    auto fetch = [&](int i) {
-        if (i + 1 < count) {
-            const int of = REV ? count - 1 - i : i;
-            const float* m = M + (bh * mcount + of) * D * D;
-            const float* b = B + (REV ? bh * (count - 1) + of - 1 : bh * mcount + of) * D * DV;
-            const uint32_t dst = smem_addr(sM + (i & 1) * D * D);
-            for (int k = tid; k < D * D / 4; k += 256)
-                cp16(dst + k * 16, m + k * 4, true);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                next[r] = b[(warp * R + r) * DV + c];
+    auto matrix = [&](int i, int r) {
+        const int of = REV ? count - 1 - i : i;
+        const float* p = M + ((bh * mcount + of) * D + warp * RW + r) * D + V * lane;
+        if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            m[r][0] = y.x, m[r][1] = y.y, m[r][2] = y.z, m[r][3] = y.w;
+        } else if constexpr (V == 2) {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            m[r][0] = y.x, m[r][1] = y.y;
+        } else {
+            m[r][0] = *p;
         }
-        cp_commit();
+    };
+    auto constant = [&](int i) {
+        const int of = REV ? count - 1 - i : i;
+        const float* b = B + (REV ? bh * (count - 1) + of - 1 : bh * mcount + of) * D * DV;
+#pragma unroll
+        for (int r = 0; r < RW / 4; ++r)
+            next[r] = b[(row0 + 4 * r) * DV + c];
     };
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        x[r] = S0 ? S0[(bh * D + warp * R + r) * DV + c] : 0.f;
-    fetch(0);
+    for (int r = 0; r < RW / 4; ++r)
+        x[r] = S0 ? S0[(bh * D + row0 + 4 * r) * DV + c] : 0.f;
+    if (count > 1) {
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+            matrix(0, r);
+        constant(0);
+    }
     for (int i = 0;; ++i) {
         const int of = REV ? count - 1 - i : i;
+        const bool more = i + 2 < count;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            start[((bh * count + of) * D + warp * R + r) * DV + c] = x[r];
+        for (int r = 0; r < RW / 4; ++r)
+            start[((bh * count + of) * D + row0 + 4 * r) * DV + c] = x[r];
         if (i + 1 == count)
             return;
+        if constexpr (REV) {
+            float* mine = sm + 64 * LS + warp * RW * 8;  // [row][column]
+            __syncwarp();
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            sS[(warp * R + r) * 32 + lane] = x[r];
-            x[r] = next[r];
-        }
-        cp_wait<0>();
-        __syncthreads();
-        fetch(i + 1);
-        const float* m = sM + (i & 1) * D * D;
-        if (REV) {
-#pragma unroll 4
-            for (int k = 0; k < D; ++k) {
-                const float s0 = sS[k * 32 + lane];
+            for (int r = 0; r < RW / 4; ++r)
+                mine[(t + 4 * r) * 8 + g] = x[r];
+            __syncwarp();
+            float y[8][V] = {};
 #pragma unroll
-                for (int r = 0; r < R; r += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(m + k * D + warp * R + r);
-                    x[r] = fmaf(a.x, s0, x[r]), x[r + 1] = fmaf(a.y, s0, x[r + 1]);
-                    x[r + 2] = fmaf(a.z, s0, x[r + 2]), x[r + 3] = fmaf(a.w, s0, x[r + 3]);
-                }
+            for (int r = 0; r < RW; ++r) {
+                const float4 a = *reinterpret_cast<const float4*>(mine + r * 8);
+                const float4 b = *reinterpret_cast<const float4*>(mine + r * 8 + 4);
+                const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        y[j][v] = fmaf(m[r][v], s[j], y[j][v]);
+                if (more)
+                    matrix(i + 1, r);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    sm[(warp * 8 + j) * LS + V * lane + v] = y[j][v];
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < RW / 4; ++r) {
+                x[r] = next[r];
+#pragma unroll
+                for (int w = 0; w < 8; ++w)
+                    x[r] += sm[(w * 8 + g) * LS + row0 + 4 * r];
+            }
+            __syncthreads();  // the parts are read
         } else {
-#pragma unroll 2
-            for (int k = 0; k < D; k += 4) {
-                const float s0 = sS[k * 32 + lane], s1 = sS[(k + 1) * 32 + lane], s2 = sS[(k + 2) * 32 + lane],
-                            s3 = sS[(k + 3) * 32 + lane];
+            float* s = sm + (i & 1) * 8 * LS;  // [column][row]
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float4 a = *reinterpret_cast<const float4*>(m + (warp * R + r) * D + k);
-                    x[r] = fmaf(a.x, s0, fmaf(a.y, s1, fmaf(a.z, s2, fmaf(a.w, s3, x[r]))));
+            for (int r = 0; r < RW / 4; ++r)
+                s[g * LS + row0 + 4 * r] = x[r];
+            __syncthreads();
+            float k[8][V];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    k[j][v] = s[j * LS + V * lane + v];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = m[r][0] * k[j][0];
+#pragma unroll
+                    for (int v = 1; v < V; ++v)
+                        y[j] = fmaf(m[r][v], k[j][v], y[j]);
                 }
+                if (more)
+                    matrix(i + 1, r);
+                float z = sum8(y, lane);
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                if ((r & 3) == t)
+                    x[r / 4] = z + next[r / 4];
             }
         }
-        __syncthreads();  // S and this M are read
+        if (more)
+            constant(i + 1);
     }
 }
 
@@ -2251,17 +2295,22 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int chunks_of(int64_t N) { return (int)((N + kC - 1) / kC); }
 
 // Segments of a sequence.  Two runs over a segment and a walk over their ends take
-// the place of one run over the whole, worth it from four segments on (B1 H4 N32768
-// d = 64: 938 us whole, 194 us cut); no more than give each warp of the second run
-// a sub-partition of its own at 152 SMs, and no more than 32: the walk is serial.  By
-// sizes alone, so that workspaces can be sized without the GPU.
+// the place of one run over the whole, worth it from three segments on (forward and
+// gradient, B1 H12 N4096 d = 128: 156 and 500 us whole, 142 and 389 us in three; B1 H16
+// in two: 160 and 523 against 165 and 510 us); no more than give each warp of the
+// second run a sub-partition of its own at 152 SMs, and no more than 32: the walk is
+// serial, 0.7 us a step at d = 64, 1.9 us at 128.  So a segment is at least four chunks
+// at d = 128 and two below (B1 H4: N1000 d = 128 44 and 123 us in segments of eight
+// chunks, 39 and 90 us of four, 44 and 89 us of two; N700 d = 64 29 and 76 us whole, 27
+// and 60 us of two or three; under eight chunks whole: N400 22 and 57 us, 26 and 58 us
+// in three).  By sizes alone, so that workspaces can be sized without the GPU.
 int segments_of(const DeltaArgs& a)
 {
-    const int64_t slices = a.B * a.H * (a.dv / 16);
+    const int64_t slices = a.B * a.H * (a.dv / 16), most = chunks_of(a.N) / (a.d > 64 ? 4 : 2);
     int64_t n = 2 * 152 / slices;
-    n = n < chunks_of(a.N) / 8 ? n : chunks_of(a.N) / 8;
+    n = n < most ? n : most;
     n = n < 32 ? n : 32;
-    if (n < 4)
+    if (n < 3 || chunks_of(a.N) < 8)
         return 1;
     const int64_t len = (chunks_of(a.N) + n - 1) / n;  // chunks of a segment; the last may be short
     return (int)((chunks_of(a.N) + len - 1) / len);
@@ -2406,11 +2455,8 @@ template <int D, bool REV>
 cudaError_t launch_join(const DeltaArgs& a, const float* from, const float* B, const float* M, float* start, int n,
                         int mcount)
 {
-    const cudaError_t e = allow_smem(k_delta_join<D, REV>, join_smem<D>());
-    if (e != cudaSuccess)
-        return e;
-    k_delta_join<D, REV><<<dim3((unsigned)(a.B * a.H), a.dv / 32), 256, join_smem<D>(), a.stream>>>(from, B, M, start,
-                                                                                                 n, mcount, a.dv);
+    k_delta_join<D, REV><<<dim3((unsigned)(a.B * a.H), a.dv / kJoinCols), 256, 0, a.stream>>>(from, B, M, start, n,
+                                                                                             mcount, a.dv);
     count_launches(1);
     return cudaGetLastError();
 }
