@@ -9,9 +9,14 @@
 //
 // The columns of S (value channels) never mix: column c needs only v[:, c].
 // So a column belongs to one warp for the whole sequence and no token step
-// needs a barrier.  With S' = a_t S_{t-1} the two products S'^T k_t and
-// S'^T q_t are taken in one pass over the registers, and
-// o_t = scale (S'^T q_t + (k_t . q_t) beta_t e_t).
+// needs a barrier.  The recurrence takes four tokens at a time, with S the state
+// before them, A_j = a_1 .. a_j and p_ji = a_{i+1} .. a_j:
+//
+//   e_j = v_j - A_j S^T k_j - sum_{i < j} p_ji (k_j . k_i) u_i,   u_i = beta_i e_i
+//   o_j = scale (A_j S^T q_j + sum_{i <= j} p_ji (q_j . k_i) u_i)
+//   S <- A_4 S + sum_j p_4j k_j u_j^T
+//
+// so that the products with the state do not wait for one another.
 #include <math.h>
 
 #include "la_delta.cuh"
@@ -24,10 +29,10 @@ using delta::kL2Eps;
 // ------------------------------------------------------ token recurrence ----
 // 8 warps of 4 columns each; lane = 4 r + c holds rows 4 r .. 4 r + 3 of every
 // 32 for column c.  Tokens are staged in blocks of kRecTok, q and k already
-// normalised, so the step itself is D / 8 FMAs four times and three shuffles
-// of two values.  Bound by the latency of that chain, once per token (0.21 us at
-// d = 64); the next block's rows are in flight (in registers) while a block's tokens
-// run (300 ns per token without).
+// normalised and a group's four tokens by one warp, which leaves their products with
+// each other.  A group's eight dots with the state come down in one exchange (sum8),
+// and what is left in order is a triangular solve of four scalars.
+constexpr int kGroup = 4;     // tokens taken together
 constexpr int kRecThreads = 256;
 constexpr int kRecCols = 32;  // columns per CTA
 constexpr int kRecTok = 32;   // tokens per staged block
@@ -55,7 +60,10 @@ __global__ void __launch_bounds__(kRecThreads)
     __shared__ __align__(16) float sq[kRecTok][D];
     __shared__ float sv[kRecTok][kRecCols];
     __shared__ float so[kRecTok][kRecCols];
-    __shared__ float sbeta[kRecTok], salpha[kRecTok], skq[kRecTok];
+    // a token's row: p_ji k_j.k_i (i < j) and A_j; p_ji q_j.k_i (i <= j)
+    __shared__ __align__(16) float4 skk[kRecTok], sqk[kRecTok];
+    __shared__ __align__(16) float sbeta[kRecTok], slast[kRecTok];  // slast: p_4j
+    __shared__ float raw[kRecThreads / 32][2][kGroup * kGroup];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, col = warp * 4 + (lane & 3);
@@ -77,14 +85,15 @@ __global__ void __launch_bounds__(kRecThreads)
         s[i] = seg.carry ? (row == c0 - DV + col ? 1.0f : 0.0f) : start ? start[row * DV + c0 + col] : 0.0f;
     }
 
-    // a warp stages rows warp, warp + 8, ..
-    constexpr int kRows = kRecTok / (kRecThreads / 32);
+    // a warp stages a group of tokens
+    constexpr int kRows = kGroup;
+    static_assert(kRecTok == kGroup * (kRecThreads / 32), "a group per warp");
     T nk[kRows][D / 32], nq[kRows][D / 32], nv[kRows];
     float nb[kRows], na[kRows];
     auto fetch = [&](int64_t b) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int64_t t = b * kRecTok + warp + i * (kRecThreads / 32);
+            const int64_t t = b * kRecTok + warp * kGroup + i;
             const bool live = t < hi;
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
@@ -102,35 +111,73 @@ __global__ void __launch_bounds__(kRecThreads)
         const int64_t t0 = b * kRecTok;
         const int n = (int)min((int64_t)kRecTok, hi - t0);
         __syncthreads();  // the previous block's tiles are read
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int t = warp + i * (kRecThreads / 32);
-            float k2 = 0.f, q2 = 0.f, kq = 0.f;
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                const float kk = to_f32<T>(nk[i][x]), qq = to_f32<T>(nq[i][x]);
-                k2 = fmaf(kk, kk, k2);
-                q2 = fmaf(qq, qq, q2);
-                kq = fmaf(kk, qq, kq);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                k2 += __shfl_xor_sync(0xffffffffu, k2, o);
-                q2 += __shfl_xor_sync(0xffffffffu, q2, o);
-                kq += __shfl_xor_sync(0xffffffffu, kq, o);
-            }
-            const float rk = l2 ? rsqrtf(k2 + kL2Eps) : 1.0f;
-            const float rq = (l2 ? rsqrtf(q2 + kL2Eps) : 1.0f) * scale;
+        {
+            const int g = lane >> 2, j = g & 3, i = lane & 3;
+            float y[3][8] = {};
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
-                sk[t][lane + 32 * x] = to_f32<T>(nk[i][x]) * rk;
-                sq[t][lane + 32 * x] = to_f32<T>(nq[i][x]) * rq;
+                float kk[kRows], qq[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    kk[r] = to_f32<T>(nk[r][x]), qq[r] = to_f32<T>(nq[r][x]);
+                    y[0][r] = fmaf(kk[r], kk[r], y[0][r]);
+                    y[0][4 + r] = fmaf(qq[r], qq[r], y[0][4 + r]);
+                    y[1][r] = fmaf(qq[r], kk[r], y[1][r]);
+                }
+                y[1][4] = fmaf(kk[1], kk[0], y[1][4]), y[1][5] = fmaf(kk[2], kk[0], y[1][5]);
+                y[1][6] = fmaf(kk[3], kk[0], y[1][6]), y[1][7] = fmaf(kk[2], kk[1], y[1][7]);
+                y[2][0] = fmaf(kk[3], kk[1], y[2][0]), y[2][1] = fmaf(kk[3], kk[2], y[2][1]);
+                y[2][2] = fmaf(qq[1], kk[0], y[2][2]), y[2][3] = fmaf(qq[2], kk[0], y[2][3]);
+                y[2][4] = fmaf(qq[3], kk[0], y[2][4]), y[2][5] = fmaf(qq[2], kk[1], y[2][5]);
+                y[2][6] = fmaf(qq[3], kk[1], y[2][6]), y[2][7] = fmaf(qq[3], kk[2], y[2][7]);
             }
-            sv[t][lane] = to_f32<T>(nv[i]);
-            if (lane == 0) {
-                skq[t] = kq * rk * rq;
-                sbeta[t] = nb[i];
-                salpha[t] = expf(na[i]);
+            float z[3];  // lanes 4 g ..: sum g
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                z[m] = delta::sum8(y[m], lane);
+                z[m] += __shfl_xor_sync(0xffffffffu, z[m], 2);
+                z[m] += __shfl_xor_sync(0xffffffffu, z[m], 1);
+            }
+            // 1 / norms, the queries' with the scale: lanes 4 r .. of k_r, 16 + 4 r .. of q_r
+            const float inv = (l2 ? rsqrtf(z[0] + kL2Eps) : 1.0f) * (g < 4 ? 1.0f : scale);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float rk = __shfl_sync(0xffffffffu, inv, 4 * r), rq = __shfl_sync(0xffffffffu, inv, 16 + 4 * r);
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    sk[warp * kGroup + r][lane + 32 * x] = to_f32<T>(nk[r][x]) * rk;
+                    sq[warp * kGroup + r][lane + 32 * x] = to_f32<T>(nq[r][x]) * rq;
+                }
+                sv[warp * kGroup + r][lane] = to_f32<T>(nv[r]);  // kRecCols lanes
+            }
+            if (i == 0) {  // the sums to their places, 4 j + i, a digit for each
+                raw[warp][g < 4][0x9c84fa50u >> (4 * g) & 15] = z[1];
+                raw[warp][g >= 2][0xed9c84edu >> (4 * g) & 15] = z[2];
+            }
+            __syncwarp();
+            // entry (j, i): lanes < 16 of k.k, the others of q.k
+            float a[kRows], p = 1.0f, A = 1.0f, last = 1.0f;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                a[r] = expf(na[r]);
+                p *= r > i && r <= j ? a[r] : 1.0f;
+                A *= r <= j ? a[r] : 1.0f;
+                last *= r > j ? a[r] : 1.0f;
+            }
+            const float rj = __shfl_sync(0xffffffffu, inv, g < 4 ? 4 * j : 16 + 4 * j);
+            const float ri = __shfl_sync(0xffffffffu, inv, 4 * i);
+            float* row = reinterpret_cast<float*>((g < 4 ? skk : sqk) + warp * kGroup + j);
+            if (g < 4)
+                row[i] = i == 3 ? A : i < j ? raw[warp][0][4 * j + i] * (rj * ri * p) : 0.0f;
+            else
+                row[i] = i <= j ? raw[warp][1][4 * j + i] * (rj * ri * p) : 0.0f;
+            if (lane < 16 && i == 0) {
+                float b = nb[0];
+#pragma unroll
+                for (int r = 1; r < kRows; ++r)
+                    b = j == r ? nb[r] : b;
+                sbeta[warp * kGroup + j] = b;
+                slast[warp * kGroup + j] = last;
             }
         }
         if (b + 1 < b1)
@@ -141,37 +188,47 @@ __global__ void __launch_bounds__(kRecThreads)
                 chk[((bh * (nblk + 1) + b) * D + (i / 4) * 32 + 4 * r + i % 4) * DV + c0 + col] = s[i];
         }
         __syncthreads();
-#pragma unroll 2
-        for (int t = 0; t < n; ++t) {
-            const float a = salpha[t];
-            float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f}, kf[D / 8];
+        for (int t = 0; t < n; t += kGroup) {  // past the end: zero rows, no decay
+            float y[8] = {}, kf[kGroup][D / 8];
 #pragma unroll
             for (int m = 0; m < D / 32; ++m) {
-                const float4 x = *reinterpret_cast<const float4*>(&sk[t][32 * m + 4 * r]);
-                const float4 y = *reinterpret_cast<const float4*>(&sq[t][32 * m + 4 * r]);
-                kf[4 * m] = x.x, kf[4 * m + 1] = x.y, kf[4 * m + 2] = x.z, kf[4 * m + 3] = x.w;
-                const float yf[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pk[j] = fmaf(kf[4 * m + j], s[4 * m + j], pk[j]);
-                    pq[j] = fmaf(yf[j], s[4 * m + j], pq[j]);
+                for (int j = 0; j < kGroup; ++j) {
+                    const float4 x = *reinterpret_cast<const float4*>(&sk[t + j][32 * m + 4 * r]);
+                    const float4 w = *reinterpret_cast<const float4*>(&sq[t + j][32 * m + 4 * r]);
+                    kf[j][4 * m] = x.x, kf[j][4 * m + 1] = x.y, kf[j][4 * m + 2] = x.z, kf[j][4 * m + 3] = x.w;
+                    y[j] = fmaf(x.x, s[4 * m], fmaf(x.y, s[4 * m + 1], fmaf(x.z, s[4 * m + 2], fmaf(x.w, s[4 * m + 3], y[j]))));
+                    y[4 + j] = fmaf(w.x, s[4 * m], fmaf(w.y, s[4 * m + 1], fmaf(w.z, s[4 * m + 2], fmaf(w.w, s[4 * m + 3], y[4 + j]))));
                 }
             }
-            float dk = (pk[0] + pk[1]) + (pk[2] + pk[3]), dq = (pq[0] + pq[1]) + (pq[2] + pq[3]);
+            const float z = delta::sum8(y, lane);  // row r < 4: k_r, else q_{r - 4}
+            const float4 be = *reinterpret_cast<const float4*>(sbeta + t), pl = *reinterpret_cast<const float4*>(slast + t);
+            const float b[4] = {be.x, be.y, be.z, be.w}, p[4] = {pl.x, pl.y, pl.z, pl.w};
+            float e[kGroup], u[kGroup], A = 1.0f;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                dk += __shfl_xor_sync(0xffffffffu, dk, o);
-                dq += __shfl_xor_sync(0xffffffffu, dq, o);
+            for (int j = 0; j < kGroup; ++j) {
+                const float4 g = skk[t + j];
+                const float c[3] = {g.x, g.y, g.z};
+                A = g.w;
+                e[j] = fmaf(-A, __shfl_sync(0xffffffffu, z, 4 * j + (lane & 3)), sv[t + j][col]);
+#pragma unroll
+                for (int i = 0; i < j; ++i)
+                    e[j] = fmaf(-c[i], u[i], e[j]);
+                u[j] = b[j] * e[j];
             }
-            const float e = fmaf(-a, dk, sv[t][col]);  // the decay off the chain: S' = a S
-            const float u = sbeta[t] * e;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                s[i] = fmaf(kf[i], u, a * s[i]);
-            if (r == 0) {
-                so[t][col] = fmaf(skq[t], u, a * dq);
-                if (err)
-                    err[(bh * N + t0 + t) * DV + c0 + col] = e;
+            for (int i = 0; i < D / 8; ++i) {
+                float x = A * s[i];
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    x = fmaf(kf[j][i], p[j] * u[j], x);
+                s[i] = x;
+            }
+            if (r >= 4) {
+                const float4 h = sqk[t + r - 4];
+                so[t + r - 4][col] = fmaf(skk[t + r - 4].w, z, fmaf(h.x, u[0], fmaf(h.y, u[1], fmaf(h.z, u[2], h.w * u[3]))));
+            } else if (err && t + r < n) {
+                err[(bh * N + t0 + t + r) * DV + c0 + col] = r == 0 ? e[0] : r == 1 ? e[1] : r == 2 ? e[2] : e[3];
             }
         }
         __syncwarp();

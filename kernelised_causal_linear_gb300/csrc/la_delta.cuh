@@ -13,6 +13,20 @@ constexpr float kL2Eps = 1e-6f;
 // them, is a full reset, and running sums stay finite.  NaN passes through.
 __device__ __forceinline__ float clamp_gate(float g) { return g < -128.0f ? -128.0f : g; }
 
+// Eight sums over lanes of the same t = lane & 3: halves are traded so that lane
+// 4 g + t ends with the sum of y[g], seven shuffles instead of 24.
+__device__ __forceinline__ float sum8(const float (&y)[8], int lane)
+{
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a[i] = (lane & 16 ? y[i + 4] : y[i]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? y[i] : y[i + 4], 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = (lane & 8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? a[i] : a[i + 2], 8);
+    return (lane & 4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? b[0] : b[1], 4);
+}
+
 // From segments' ends to their starts: S_{i+1} = M_i S_i + B_i from S_0 (mcount M and B
 // per head), or with rev dS_{i-1} = M_i^T dS_i + C_i from the last (B: n - 1 C per head).
 cudaError_t join_segments(const DeltaArgs& a, bool rev, const float* from, const float* B, const float* M, float* start,

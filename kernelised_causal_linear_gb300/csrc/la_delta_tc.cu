@@ -552,20 +552,6 @@ __device__ __forceinline__ void keep_parts(unsigned char* p, int64_t plane, int6
     keep_part(p, 2 * plane + 1, part_bytes, block, lane, lo);
 }
 
-// Eight sums over the warp's 16 columns (the lanes' g): halves are traded so that
-// lane 4 g + t ends with the sum of y[g] over its t, seven shuffles instead of 24.
-__device__ __forceinline__ float sum8(const float (&y)[8], int lane)
-{
-    float a[4], b[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        a[i] = (lane & 16 ? y[i + 4] : y[i]) + __shfl_xor_sync(0xffffffffu, lane & 16 ? y[i] : y[i + 4], 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        b[i] = (lane & 8 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, lane & 8 ? a[i] : a[i + 2], 8);
-    return (lane & 4 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? b[0] : b[1], 4);
-}
-
 // The ring of stages: barriers for filled and for read, and how many warps have read
 // (STEP: a barrier of the CTA in their place).  A warp's reads are ordered before the refill by its arrival and the refiller's
 // (satisfied) wait on the same barrier; the count only tells who is last.  A fence
@@ -643,7 +629,7 @@ struct Share {
     // the columns -> row[first token of the chunk + ..]
     __device__ __forceinline__ void store_sums(float* row, const float (&y)[8], int part, int64_t t0, int64_t N) const
     {
-        const float x = sum8(y, lane);
+        const float x = delta::sum8(y, lane);
         const int g = lane >> 2;
         const int64_t t = t0 + 16 * tile(2 * part + (g >> 2)) + 8 * ((g >> 1) & 1) + 2 * (lane & 3) + (g & 1);
         if (t < N)
@@ -1280,7 +1266,7 @@ __global__ void __launch_bounds__(256)
                 }
                 if (more)
                     matrix(i + 1, r);
-                float z = sum8(y, lane);
+                float z = delta::sum8(y, lane);
                 z += __shfl_xor_sync(0xffffffffu, z, 2);
                 z += __shfl_xor_sync(0xffffffffu, z, 1);
                 if ((r & 3) == t)
