@@ -24,7 +24,10 @@
 namespace la {
 namespace {
 
+using delta::both;
+using delta::fma2;
 using delta::kL2Eps;
+using delta::mul2;
 
 // ------------------------------------------------------ token recurrence ----
 // 8 warps of 4 columns each; lane = 4 r + c holds rows 4 r .. 4 r + 3 of every
@@ -77,12 +80,14 @@ __global__ void __launch_bounds__(kRecThreads)
     const T* vp = unit ? nullptr : v + bh * N * DV + c0;
     const int64_t nblk = (N + kRecTok - 1) / kRecTok;
 
-    float s[D / 8];
+    float2 s[D / 16];  // rows 4 r + 2 (i % 2) and the next of the 32 from 32 (i / 2)
     const float* start = seg.start ? seg.start + run * D * DV : S0 ? S0 + bh * D * DV : nullptr;
+    auto row_of = [&](int i) { return i / 2 * 32 + 4 * r + i % 2 * 2; };
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const int row = (i / 4) * 32 + 4 * r + i % 4;
-        s[i] = seg.carry ? (row == c0 - DV + col ? 1.0f : 0.0f) : start ? start[row * DV + c0 + col] : 0.0f;
+    for (int i = 0; i < D / 16; ++i) {
+        const int row = row_of(i), at = row * DV + c0 + col, u = c0 + col - DV;
+        s[i].x = seg.carry ? (row == u ? 1.0f : 0.0f) : start ? start[at] : 0.0f;
+        s[i].y = seg.carry ? (row + 1 == u ? 1.0f : 0.0f) : start ? start[at + DV] : 0.0f;
     }
 
     // a warp stages a group of tokens
@@ -184,23 +189,29 @@ __global__ void __launch_bounds__(kRecThreads)
             fetch(b + 1);
         if (chk) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                chk[((bh * (nblk + 1) + b) * D + (i / 4) * 32 + 4 * r + i % 4) * DV + c0 + col] = s[i];
+            for (int i = 0; i < D / 16; ++i) {
+                float* at = chk + ((bh * (nblk + 1) + b) * D + row_of(i)) * DV + c0 + col;
+                at[0] = s[i].x, at[DV] = s[i].y;
+            }
         }
         __syncthreads();
         for (int t = 0; t < n; t += kGroup) {  // past the end: zero rows, no decay
-            float y[8] = {}, kf[kGroup][D / 8];
+            float2 d[8] = {}, kf[kGroup][D / 16];
 #pragma unroll
             for (int m = 0; m < D / 32; ++m) {
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j) {
                     const float4 x = *reinterpret_cast<const float4*>(&sk[t + j][32 * m + 4 * r]);
                     const float4 w = *reinterpret_cast<const float4*>(&sq[t + j][32 * m + 4 * r]);
-                    kf[j][4 * m] = x.x, kf[j][4 * m + 1] = x.y, kf[j][4 * m + 2] = x.z, kf[j][4 * m + 3] = x.w;
-                    y[j] = fmaf(x.x, s[4 * m], fmaf(x.y, s[4 * m + 1], fmaf(x.z, s[4 * m + 2], fmaf(x.w, s[4 * m + 3], y[j]))));
-                    y[4 + j] = fmaf(w.x, s[4 * m], fmaf(w.y, s[4 * m + 1], fmaf(w.z, s[4 * m + 2], fmaf(w.w, s[4 * m + 3], y[4 + j]))));
+                    kf[j][2 * m] = make_float2(x.x, x.y), kf[j][2 * m + 1] = make_float2(x.z, x.w);
+                    d[j] = fma2(kf[j][2 * m], s[2 * m], fma2(kf[j][2 * m + 1], s[2 * m + 1], d[j]));
+                    d[4 + j] = fma2(make_float2(w.x, w.y), s[2 * m], fma2(make_float2(w.z, w.w), s[2 * m + 1], d[4 + j]));
                 }
             }
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = d[j].x + d[j].y;
             const float z = delta::sum8(y, lane);  // row r < 4: k_r, else q_{r - 4}
             const float4 be = *reinterpret_cast<const float4*>(sbeta + t), pl = *reinterpret_cast<const float4*>(slast + t);
             const float b[4] = {be.x, be.y, be.z, be.w}, p[4] = {pl.x, pl.y, pl.z, pl.w};
@@ -216,13 +227,13 @@ __global__ void __launch_bounds__(kRecThreads)
                     e[j] = fmaf(-c[i], u[i], e[j]);
                 u[j] = b[j] * e[j];
             }
+            const float2 w[kGroup] = {both(p[0] * u[0]), both(p[1] * u[1]), both(p[2] * u[2]), both(p[3] * u[3])};
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                float x = A * s[i];
+            for (int i = 0; i < D / 16; ++i) {
+                s[i] = mul2(both(A), s[i]);
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j)
-                    x = fmaf(kf[j][i], p[j] * u[j], x);
-                s[i] = x;
+                    s[i] = fma2(kf[j][i], w[j], s[i]);
             }
             if (r >= 4) {
                 const float4 h = sqk[t + r - 4];
@@ -249,12 +260,15 @@ __global__ void __launch_bounds__(kRecThreads)
         end = S_out + bh * D * DV;
     }
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const int row = (i / 4) * 32 + 4 * r + i % 4;
-        if (end)
-            end[(int64_t)row * ld + c0 + col] = s[i];
-        if (chk && hi == N)
-            chk[((bh * (nblk + 1) + nblk) * D + row) * DV + c0 + col] = s[i];
+    for (int i = 0; i < D / 16; ++i) {
+        if (end) {
+            float* at = end + (int64_t)row_of(i) * ld + c0 + col;
+            at[0] = s[i].x, at[ld] = s[i].y;
+        }
+        if (chk && hi == N) {
+            float* at = chk + ((bh * (nblk + 1) + nblk) * D + row_of(i)) * DV + c0 + col;
+            at[0] = s[i].x, at[DV] = s[i].y;
+        }
     }
 }
 
