@@ -1090,18 +1090,19 @@ bool delta_grid_ok(const DeltaArgs& a)
 
 namespace {
 
-// Sequences shorter than this take the recurrence whatever their number.
-constexpr int64_t kShort = 12;
-
-// The tensor-core forward pays for whole chunks of 64 tokens and two launches (14 to
-// 15 us up to 64 tokens at 32 heads, d = 128, against 5.4 us for the recurrence at 8
-// tokens, 10.7 at 32, 15.2 at 48); with more 32-column slices than the GPU holds at
-// once the recurrence queues (512 heads: 63 us at 17 tokens against 48).
+// The tensor-core forward pays for whole chunks of 64 tokens and two launches; the
+// recurrence for every token, in rounds where its CTAs are more than the GPU holds
+// (one per SM at d = 128, two below).  They meet near 64 tokens times rounds (us,
+// recurrence and tensor cores): B4 H8 d = 128 8.7 and 14.4 at 32 tokens, 14.6 and 14.9
+// at 64, 17.7 and 16.9 at 80; B8 H16 d = 128 (four rounds) 18.5 and 19.1 at 12, 26 and
+// 19 at 24; B8 H32 d = 64 (two) 17.7 and 18.9 at 32, 25 and 19 at 44.  For 152 SMs by
+// sizes alone: a workspace sized without the GPU at hand serves there.
 bool forward_on_tensor_cores(const DeltaArgs& a)
 {
-    if (a.dtype != LA_BF16 || a.N <= kShort)
+    if (a.dtype != LA_BF16)
         return false;
-    return a.N > 44 || a.B * a.H * (a.dv / kRecCols) > 2 * (int64_t)device_sm_count();
+    const int64_t held = a.d > 64 ? 152 : 2 * 152, ctas = a.B * a.H * (a.dv / kRecCols);
+    return a.N > 64 || a.N * ((ctas + held - 1) / held) > 64;
 }
 
 // Its gradient is ahead at every length (8 tokens: 37 against 63 us at 32 heads,
@@ -1110,12 +1111,9 @@ bool backward_on_tensor_cores(const DeltaArgs& a) { return a.dtype == LA_BF16; }
 
 }  // namespace
 
-// By type and length alone: a size asked for without the GPU at hand serves there.
 size_t delta_forward_workspace(const DeltaArgs& a)
 {
-    if (a.dtype != LA_BF16)
-        return rec_layout(a).total;
-    return a.N > kShort ? delta_tc_forward_workspace(a) : 0;
+    return forward_on_tensor_cores(a) ? delta_tc_forward_workspace(a) : rec_layout(a).total;
 }
 
 size_t delta_backward_workspace(const DeltaArgs& a)

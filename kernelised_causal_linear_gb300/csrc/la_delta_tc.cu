@@ -1752,7 +1752,9 @@ __global__ void __launch_bounds__(256, 1)
 // that fragments go from ldmatrix into the MMA as they are and every factor is
 // one of a row, applied to fp32 accumulators.  The 64 x 64 matrices pass through a
 // tile of the two warps' own as fp16 rows, each half under a power of two.  One fp16 part
-// throughout (2^-12 of a term, under the results' own rounding to bf16).
+// throughout: 2^-12 of a term, a sixteenth of the bf16 rounding of the results.  (A result
+// that cancels to less than a sixteenth of its terms shows it: one token, one key head
+// and value heads whose gradients happen to oppose.)
 // Loops over fragments stay rolled: unrolled, the two roles' code overran the
 // instruction cache and its misses were half of all stalls.
 //

@@ -579,3 +579,12 @@ def test_the_first_gate_of_a_zero_start_has_no_gradient(N, dtype):
     assert (got[4][:, :, 0] == 0).all()
     if N > 1:
         assert (got[4][:, :, 1:] != 0).any()
+
+
+@pytest.mark.parametrize("N", [3, 7, 13, 40, 63])
+@pytest.mark.parametrize("d,dv", [(128, 64), (32, 128)])
+def test_short_sequences_of_many_heads(N, d, dv):
+    """Both sides of the lengths where the forward changes its kernels."""
+    p = problem(24, 16, 4, N, d, dv, BF, N + d)
+    check_forward(p)
+    check_backward(p)
