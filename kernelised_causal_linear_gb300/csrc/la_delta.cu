@@ -34,7 +34,10 @@ using delta::mul2;
 // 32 for column c.  Tokens are staged in blocks of kRecTok, q and k already
 // normalised and a group's four tokens by one warp, which leaves their products with
 // each other.  A group's eight dots with the state come down in one exchange (sum8),
-// and what is left in order is a triangular solve of four scalars.
+// and what is left in order is a triangular solve of four scalars.  Bound by the latency
+// of that chain: 0.14 us per token at d = 64, 0.18 at 128, two warps per sub-partition
+// and 45% of their issue slots used.  (Token by token 0.19 and 0.25; two columns per
+// lane, half the reads for twice the exchange, 207 against 182 us at B3 H8 N1000 d = 128.)
 constexpr int kGroup = 4;     // tokens taken together
 constexpr int kRecThreads = 256;
 constexpr int kRecCols = 32;  // columns per CTA
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kDecThreads)
 // for 32 columns per CTA and keeps dS1, dV and the dots over its columns (over
 // segments like the recurrence: dS0 is affine in dS1, its matrix the transposed M);
 // k_delta_grad_dqk then takes every chunk on its own.  fp32 in shared memory, bound
-// by its reads.
+// by its reads: B2 H4 N201 d = 64 2 x 22 us and 24 us.
 struct GradKept {
     float* dS;  // [BH][nblk][D][DV] gradient of the state after the chunk
     float* dV;  // [BH][N][DV]
@@ -884,23 +887,25 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int64_t rec_blocks(int64_t N) { return (N + kRecTok - 1) / kRecTok; }
 
 // Segments of a sequence on this path (1: whole), and their tokens: as many as give
-// two CTAs per SM at 152 SMs, at least 4 to pay for the second run, at most 32 (they
-// are joined one after the other, about 1 us each), of at least 64 tokens, or 32 in a
-// short sequence.  Forward and gradient, whole and cut: B1 H4 d = 64, N = 160 33 and
-// 120 against 22 and 80 us, N = 1000 192 and 590 against 54 and 142 us; B1 H4 N512
-// d = 128 131 and 433 against 65 and 187 us (83 and 201 us in segments of 32); with
-// as few as four the forward may lose (B2 H8 N1000 d = 128: 254 against 276 us) what
-// the gradient gains (1045 against 891 us).  By sizes alone, as workspaces are sized without the GPU.
+// two CTAs per SM at 152 SMs, at most 32 (they are joined one after the other, about
+// 1 us each), of at least 64 tokens, or 32 in a short sequence.  At least 4 pay for the
+// second run; where heads are what limits them 6 at d = 128, whose CTAs have an SM each.
+// Forward and gradient, whole against cut (us): B1 H4 d = 64 N128 20 and 92 against 17
+// and 72, N1000 139 and 514 against 46 and 133, N16384 2228 and 9524 against 353 and
+// 1135; B1 H4 N512 d = 128 93 and 380 against 58 and 179 (81 and 199 in segments of
+// 32); in four, B1 H16 N4096 64 x 128 559 and 2917 against 429 and 2120, but B2 H8
+// N1000 d = 128 179 and 943 against 243 and 857.  By sizes alone, as workspaces are
+// sized without the GPU.
 int rec_segments(const DeltaArgs& a, int64_t* len)
 {
     const int64_t slices = a.B * a.H * (a.dv / kRecCols);
     const int64_t least = a.N > 256 ? 2 * kRecTok : kRecTok;
     int64_t n = 2 * 152 / slices;
+    *len = (a.N + kRecTok - 1) / kRecTok * kRecTok;
+    if (n < (a.d > 64 ? 6 : 4) || a.N < 4 * kRecTok)
+        return 1;
     n = n < a.N / kRecTok ? n : a.N / kRecTok;
     n = n < 32 ? n : 32;
-    *len = (a.N + kRecTok - 1) / kRecTok * kRecTok;
-    if (n < 4)
-        return 1;
     *len = ((a.N + n - 1) / n + kRecTok - 1) / kRecTok * kRecTok;
     if (*len < least)
         *len = least;

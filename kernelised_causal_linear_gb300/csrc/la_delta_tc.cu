@@ -1762,7 +1762,7 @@ __global__ void __launch_bounds__(256, 1)
 // of one chunk) ahead: the token planes have two buffers; the state planes are used
 // first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
 // waiting for its own 150 KB: 508 against 399 us at B4 H8 N8192 d=128.)  Measured there:
-// 378 us for 4096 chunks, 1.6 TB/s of 5.9e8 bytes; the loads alone take 165 us, the
+// 357 us for 4096 chunks, 1.7 TB/s of 5.9e8 bytes; the loads alone take 165 us, the
 // rest is a step's dependent stretches between its barriers (40% of the issue slots
 // used, a quarter of a warp's cycles per instruction at barriers).
 constexpr int kDqkThreads = 512;
