@@ -9,8 +9,8 @@
 // token-major [B,N,H,dv] as the projections around them read it, so the
 // transposition costs no pass of its own.  A row is dv / 8 lanes of eight
 // elements (16 bytes of bf16): its sums are shuffles, and each tensor is read
-// or written once.  Bound by HBM: 67 M fp32 elements with a bf16 gate 90 us (6.0
-// TB/s), 33.5 M bf16 elements 43 us (4.7 TB/s) and their gradient 66 us (5.1 TB/s).
+// or written once.  Bound by HBM: 67 M fp32 elements with a bf16 gate 84 us (6.4
+// TB/s), 33.5 M bf16 elements 36 us (5.5 TB/s) and their gradient 62 us (5.4 TB/s).
 #include "la_internal.cuh"
 
 namespace la {
@@ -22,21 +22,35 @@ struct Row8 {
     float f[8];
 };
 
-__device__ __forceinline__ Row8 load8(const float* p)
+// Eight elements as they come, and as fp32: what is in flight stays as narrow as it is
+// in memory, for more of it in a thread's registers.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+};
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 w;
+};
+
+__device__ __forceinline__ Raw8<float> fetch8(const float* p)
 {
-    Row8 r;
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    r.f[0] = a.x, r.f[1] = a.y, r.f[2] = a.z, r.f[3] = a.w;
-    r.f[4] = b.x, r.f[5] = b.y, r.f[6] = b.z, r.f[7] = b.w;
-    return r;
+    return {__ldcs(reinterpret_cast<const float4*>(p)), __ldcs(reinterpret_cast<const float4*>(p) + 1)};
 }
 
-__device__ __forceinline__ Row8 load8(const __nv_bfloat16* p)
+__device__ __forceinline__ Raw8<__nv_bfloat16> fetch8(const __nv_bfloat16* p)
+{
+    return {__ldcs(reinterpret_cast<const uint4*>(p))};
+}
+
+__device__ __forceinline__ Row8 wide(const Raw8<float>& x)
+{
+    return {{x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w}};
+}
+
+__device__ __forceinline__ Row8 wide(const Raw8<__nv_bfloat16>& x)
 {
     Row8 r;
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[4] = {x.w.x, x.w.y, x.w.z, x.w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         r.f[2 * i] = __uint_as_float(u[i] << 16);
@@ -74,7 +88,7 @@ __device__ __forceinline__ float row_sum(float x)
 
 // act(g) and act'(g).  The hardware exponential and quotient: their errors (a few
 // 2^-23, |g| 2^-24 for far gates) stay under fp32 sums' own, and with the library
-// forms this arithmetic, not memory, set the pace (69 -> 43 us for 33.5 M bf16
+// forms this arithmetic, not memory, set the pace (69 against 43 us for 33.5 M bf16
 // elements together with 32-bit row indexes).
 __device__ __forceinline__ float2 activate(float g, int act)
 {
@@ -103,8 +117,14 @@ __device__ __forceinline__ Row8 weights(const float* w, int at)
     return r;
 }
 
-// Rows in token-major order, kRows per lane group with every load issued first.
-constexpr int kRows = 2;
+// Rows in token-major order, some per lane group with every load issued first (33.5 M
+// bf16 elements: one row 38.9 us, two 36.8, three 36.5, four 37.5; 67 M from fp32 to
+// bf16 84.8, 88.0, 83.3 and 85.2 us; with an fp32 gate two, 51 against 53 us).
+template <typename T>
+constexpr int rows_at_once()
+{
+    return sizeof(T) == 2 ? 3 : 2;
+}
 
 template <int DV, typename TX, typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -113,8 +133,10 @@ __global__ void __launch_bounds__(kThreads)
                 float eps)
 {
     constexpr uint32_t LPR = DV / 8, RPC = kThreads / LPR;
+    constexpr int kRows = rows_at_once<T>();
     const uint32_t sub = threadIdx.x % LPR;
-    Row8 xr[kRows], gr[kRows];
+    Raw8<TX> xr[kRows];
+    Raw8<T> gr[kRows];
     uint32_t row[kRows], head[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -122,24 +144,28 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t at = min(row[i], rows - 1);  // lanes past the end read the last row, write nothing
         const uint32_t bn = at / H, b = bn / N;
         head[i] = at - bn * H;
-        xr[i] = load8(x + ((int64_t)(b * H + head[i]) * N + (bn - b * N)) * DV + sub * 8);
+        xr[i] = fetch8(x + ((int64_t)(b * H + head[i]) * N + (bn - b * N)) * DV + sub * 8);
         if (gate)
-            gr[i] = load8(gate + (int64_t)at * DV + sub * 8);
+            gr[i] = fetch8(gate + (int64_t)at * DV + sub * 8);
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+        const Row8 xs = wide(xr[i]);
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            ss = fmaf(xr[i].f[j], xr[i].f[j], ss);
+            ss = fmaf(xs.f[j], xs.f[j], ss);
         const float r = rsqrtf(row_sum<LPR>(ss) * (1.0f / DV) + eps);
         const Row8 wr = weights(w, (weight_heads ? head[i] * DV : 0) + sub * 8);
         Row8 o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            o.f[j] = xr[i].f[j] * r * wr.f[j];
-            if (gate)
-                o.f[j] *= activate(gr[i].f[j], act).x;
+        for (int j = 0; j < 8; ++j)
+            o.f[j] = xs.f[j] * r * wr.f[j];
+        if (gate) {
+            const Row8 gs = wide(gr[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o.f[j] *= activate(gs.f[j], act).x;
         }
         if (row[i] < rows)
             store8(y + (int64_t)row[i] * DV + sub * 8, o);
@@ -152,8 +178,12 @@ __global__ void __launch_bounds__(kThreads)
 // is a multiple of H, so a group's part of dw belongs to one head.  A block leaves
 // one part [DV], or one for each of its min(RPC, H) heads; k_norm_dw sums them in a
 // fixed order (no atomics: repeat runs are bitwise equal).
+// Blocks on an SM, as many as their registers leave room for: the grid is what the GPU
+// holds at once.
+constexpr int grad_per_sm(bool fp32_gate) { return fp32_gate ? 2 : 3; }
+
 template <int DV, typename TX, typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, grad_per_sm(sizeof(T) == 4))
     k_norm_gate_grad(const T* __restrict__ dy, const TX* __restrict__ x, const T* __restrict__ gate,
                      const float* __restrict__ w, TX* __restrict__ dx, T* __restrict__ dgate,
                      float* __restrict__ part, uint32_t rows, uint32_t N, uint32_t H, int act,
@@ -168,16 +198,29 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         acc.f[j] = 0.f;
-    // whole warps stay in the loop together: the shuffles need every lane
+    // where a row lies; groups past the end read the last row and write nothing
+    auto x_row = [&](uint32_t at) {
+        const uint32_t bn = at / H, b = bn / N, h = at - bn * H;
+        return (b * H + h) * N + (bn - b * N);
+    };
+    auto place = [&](uint32_t row) { return (int64_t)row * DV + sub * 8; };
+    uint32_t at = min(first, rows - 1), xa = x_row(at);
+    Raw8<TX> xn = fetch8(x + place(xa));
+    Raw8<T> dn = fetch8(dy + place(at)), gn;
+    if (gate)
+        gn = fetch8(gate + place(at));
+    // whole warps stay in the loop together: the shuffles need every lane.  The next
+    // row is in flight under this one's arithmetic
     for (uint32_t base = first; __any_sync(0xffffffffu, base < rows); base += GT) {
         const bool live = base < rows;
-        const uint32_t at = live ? base : rows - 1, bn = at / H, b = bn / N, h = at - bn * H;
-        const int64_t xa = ((int64_t)(b * H + h) * N + (bn - b * N)) * DV + sub * 8;
-        const int64_t ya = (int64_t)at * DV + sub * 8;
-        const Row8 xr = load8(x + xa), dr = load8(dy + ya);
+        const Row8 xr = wide(xn), dr = wide(dn);
         Row8 gr;
         if (gate)
-            gr = load8(gate + ya);
+            gr = wide(gn);
+        const uint32_t next = min(base + GT, rows - 1), xb = x_row(next);
+        xn = fetch8(x + place(xb)), dn = fetch8(dy + place(next));
+        if (gate)
+            gn = fetch8(gate + place(next));
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -201,10 +244,11 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 8; ++j)
             c.f[j] = r * (c.f[j] - xr.f[j] * r * dot);
         if (live) {
-            store8(dx + xa, c);
+            store8(dx + place(xa), c);
             if (gate)
-                store8(dgate + ya, dg);
+                store8(dgate + place(at), dg);
         }
+        at = next, xa = xb;
     }
     if (part) {
 #pragma unroll
@@ -251,21 +295,16 @@ __global__ void __launch_bounds__(1024)
 
 uint32_t gcd(uint32_t a, uint32_t b) { return b ? gcd(b, a % b) : a; }
 
-// Blocks of the gradient: about four per SM (each leaves rows of dw to be summed: 4.7 us for them, 7.6 at eight),
-// no more than there are row groups, a multiple of what keeps a group on one head.
-int64_t grad_blocks(const NormGateArgs& a, bool heads)
+// Blocks of the gradient: what 152 SMs hold at once (one more per SM is a
+// second round: bf16 77 us for four, 62 us for three), no more
+// than there are row groups, a multiple of what keeps a group on one head.
+int64_t grad_blocks(const NormGateArgs& a, bool heads, bool fp32_gate)
 {
-    const int64_t rpc = kThreads / (a.dv / 8);
+    const int64_t rpc = kThreads / (a.dv / 8), most = grad_per_sm(fp32_gate) * 152;
     const int64_t groups = (a.B * a.N * a.H + rpc - 1) / rpc;
-    const int64_t want = 4 * 152 < groups ? 4 * 152 : groups;
+    const int64_t want = most < groups ? most : groups;
     const int64_t unit = heads ? a.H / gcd((uint32_t)a.H, (uint32_t)rpc) : 1;
     return (want + unit - 1) / unit * unit;
-}
-
-int64_t grad_parts(const NormGateArgs& a, bool heads)
-{
-    const int64_t rpc = kThreads / (a.dv / 8);
-    return grad_blocks(a, heads) * (!heads ? 1 : a.H < rpc ? a.H : rpc);
 }
 
 template <int DV, typename TX, typename T>
@@ -275,7 +314,7 @@ cudaError_t run_norm(const NormGateArgs& a, bool grad)
     const T* gate = static_cast<const T*>(a.gate);
     if (!grad) {
         const int64_t rows = a.B * a.N * a.H;
-        const int64_t per = (int64_t)kRows * (kThreads / (DV / 8));
+        const int64_t per = (int64_t)rows_at_once<T>() * (kThreads / (DV / 8));
         k_norm_gate<DV, TX, T><<<(unsigned)((rows + per - 1) / per), kThreads, 0, a.stream>>>(
             x, gate, a.weight, static_cast<T*>(a.y), (uint32_t)rows, (uint32_t)a.N, (uint32_t)a.H, a.act,
             a.weight_heads, a.eps);
@@ -283,7 +322,7 @@ cudaError_t run_norm(const NormGateArgs& a, bool grad)
         return cudaGetLastError();
     }
     const bool heads = a.weight && a.weight_heads;
-    const uint32_t blocks = (uint32_t)grad_blocks(a, heads);
+    const uint32_t blocks = (uint32_t)grad_blocks(a, heads, sizeof(T) == 4);
     float* part = a.dweight ? static_cast<float*>(a.ws) : nullptr;
     k_norm_gate_grad<DV, TX, T><<<blocks, kThreads, 0, a.stream>>>(
         static_cast<const T*>(a.dy), x, gate, a.weight, static_cast<TX*>(a.dx),
@@ -320,10 +359,11 @@ cudaError_t norm_dims(const NormGateArgs& a, bool grad)
 
 }  // namespace
 
-// for either layout of the weight
+// for either layout of the weight and any types
 size_t norm_gate_backward_workspace(const NormGateArgs& a)
 {
-    const int64_t p = grad_parts(a, true), q = grad_parts(a, false);
+    const int64_t rpc = kThreads / (a.dv / 8);
+    const int64_t p = grad_blocks(a, true, false) * (a.H < rpc ? a.H : rpc), q = grad_blocks(a, false, false);
     return sizeof(float) * (size_t)(p > q ? p : q) * a.dv;
 }
 
