@@ -377,11 +377,16 @@ def _current(t: torch.Tensor, name: str) -> int:
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    _dtype(t)
+    current = torch._C._cuda_getDevice()  # a CUDA tensor exists: there is a context
+    if index != current:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
+    if t.dtype not in DTYPES:
+        _dtype(t)
     return index
+
+
+# a number in place of the device costs torch.empty 2 us more
+_DEVICES = [torch.device("cuda", i) for i in range(64)]
 
 
 class _Call:
@@ -400,7 +405,7 @@ class _Call:
                     torch.cuda.default_stream(index)
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.index)
+        t = torch.empty(shape, dtype=dtype, device=_DEVICES[self.index])
         if self.side is not None:
             # allocated for the current stream: the call's own may write only
             # once what had the memory before is done, and the memory stays
@@ -421,9 +426,10 @@ class _Call:
 
 
 def _delta_sizes(k, v):
-    if k.dim() != v.dim() or k.shape[0] != v.shape[0] or k.shape[2:-1] != v.shape[2:-1]:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not belong together")
-    return v.shape[0], v.shape[1], k.shape[1], k.shape[-1], v.shape[-1]
+    x, y = k.shape, v.shape
+    if len(x) != len(y) or x[0] != y[0] or (len(x) == 4 and x[2] != y[2]):
+        raise ValueError(f"k {tuple(x)} and v {tuple(y)} do not belong together")
+    return y[0], y[1], x[1], x[-1], y[-1]
 
 
 def la_delta_workspace_size(B, H, Hk, N, d, dv, dtype=torch.bfloat16) -> int:
