@@ -1763,7 +1763,7 @@ __global__ void __launch_bounds__(256, 1)
 // first in a step and refilled while the rest of it runs.  (One chunk per CTA, each
 // waiting for its own 150 KB: 508 against 399 us at B4 H8 N8192 d=128.)  Measured there:
 // 357 us for 4096 chunks, 1.7 TB/s of 5.9e8 bytes; the loads alone take 165 us, the
-// rest is a step's dependent stretches between its barriers (40% of the issue slots
+// rest is a step's dependent stretches between its barriers (42% of the issue slots
 // used, a quarter of a warp's cycles per instruction at barriers).
 constexpr int kDqkThreads = 512;
 
@@ -2371,16 +2371,19 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
 // more warps than the GPU has sub-partitions to give each a tensor core of its own;
 // slices per CTA: as few as give no more CTAs than SMs, at most 8 warps.  Measured at
 // d = 128: 32 heads of 8192 tokens 468 us with one warp per slice, 304 us with two;
-// 512 heads of 2011 tokens 736 us with one, 886 us with two.
+// 512 heads of 2011 tokens 736 us with one, 886 us with two.  Two also where a head has
+// two slices, which would be two warps on an SM (dv = 32, forward and gradient, one and
+// two: 256 heads of 1024 tokens d = 128 204 and 702, 175 and 588 us; 512 of d = 64 303
+// and 1016, 283 and 942 us; not at d = 32, 240 and 742, 199 and 854 us).
 struct Cut {
     int SP, W;
 };
-Cut cut_of(int64_t runs, int columns)  // sequences or segments, value columns of each
+Cut cut_of(int64_t runs, int columns, int d)  // sequences or segments, value columns of each
 {
     const int sms = device_sm_count();
     const int64_t slices = runs * (columns / 16);
     Cut c;
-    c.SP = 2 * slices <= 4 * (int64_t)sms ? 2 : 1;
+    c.SP = 2 * slices <= 4 * (int64_t)sms || (columns <= 32 && d > 32) ? 2 : 1;
     const int cap = 8 / c.SP;
     c.W = 1;
     while (2 * c.W <= cap && columns / 16 % (2 * c.W) == 0 && slices / c.W > sms)
@@ -2434,7 +2437,7 @@ template <int D, bool GATED, bool ENDS>
 cudaError_t run_rev_cut(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
                         const Segments& seg)
 {
-    const Cut cut = cut_of(a.B * a.H * seg.count, a.dv);
+    const Cut cut = cut_of(a.B * a.H * seg.count, a.dv, D);
     return cut.SP == 2 ? launch_rev<D, 2, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg)
                        : launch_rev<D, 1, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg);
 }
@@ -2465,14 +2468,14 @@ cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsig
         seg.len = (chunks_of(a.N) + n - 1) / n;
         const int m = GRAD ? n : n - 1;
         const Segments ends = {m, seg.len, nullptr, 1, B, M, 0, seg.blob, seg.fac};
-        const Cut cut = cut_of(a.B * a.H * m, a.dv + a.d);
+        const Cut cut = cut_of(a.B * a.H * m, a.dv + a.d, D);
         cudaError_t e = cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, Kept{}, ends)
                                     : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, Kept{}, ends);
         if (e != cudaSuccess || (e = launch_join<D, false>(a, a.S0, B, M, start, n, m)) != cudaSuccess)
             return e;
         seg.count = n, seg.start = start;
     }
-    const Cut cut = cut_of(a.B * a.H * n, a.dv);
+    const Cut cut = cut_of(a.B * a.H * n, a.dv, D);
     return cut.SP == 2 ? launch_chain<D, GRAD, 2, READS>(a, cut.W, rows, blobs, kept, seg)
                        : launch_chain<D, GRAD, 1, READS>(a, cut.W, rows, blobs, kept, seg);
 }

@@ -588,3 +588,11 @@ def test_short_sequences_of_many_heads(N, d, dv):
     p = problem(24, 16, 4, N, d, dv, BF, N + d)
     check_forward(p)
     check_backward(p)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_heads_of_32_columns(d):
+    """Two warps per slice although there are more slices than SMs."""
+    p = problem(20, 16, 8, 140, d, 32, BF, d)
+    check_forward(p)
+    check_backward(p)
