@@ -493,9 +493,9 @@ __global__ void __launch_bounds__(kPrepThreads)
 // the tensor core works 3100, so two warps shorten it where there are SMs to spare.
 // Measured: 277 us for the 128 chunks of B4 H8 N8192 d=128 (SP = 2: 4300 cycles per
 // chunk, tensor cores 36% busy on an SM, bound by the latency of its dependent
-// products and conversions), 680 to 700 us for B16 H32 N2011 (SP = 1: 512 CTAs at one
-// per SM are 3.4 rounds of 152; at N = 512 the busiest SM's tensor cores work 57% of
-// the time, 48% on average).
+// products and conversions), 629 us for B16 H32 N2011 (SP = 1: three rounds of 152
+// CTAs, 509 us, the rest with SP = 2, 120 us; by counters at N = 512, all in one launch,
+// the busiest SM's tensor cores work 57% of the time).
 //
 // With two warps on a sub-partition (SP = 1, eight warps) no barrier spans the CTA
 // inside the loop: the warp that is last to finish with a stage asks for the chunk
@@ -732,6 +732,7 @@ struct Segments {
     float *B, *M;        // carry: [BH][count][d][dv], [BH][count][d][d]
     int first;           // the first segment that runs
     int blob, fac;       // bytes of a blob, where its factors lie
+    int64_t skip;        // runs that another launch takes
 };
 
 // READS: outputs are wanted (a branch on the pointer instead cuts every stretch of
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(256, 1)
     Share<SP> sh;
     sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
     const int slices = (DV + (seg.carry ? D : 0)) / (16 * W);
-    const int64_t run = blockIdx.x / slices;  // head and segment
+    const int64_t run = blockIdx.x / slices + seg.skip;  // head and segment
     const int64_t bh = run / seg.count;
     const int lo = (int)(run % seg.count) * seg.len, len = min(seg.len, nchunk - lo);
     const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice;
@@ -1325,7 +1326,7 @@ __global__ void __launch_bounds__(256, 1)
     Share<SP> sh;
     sh.slice = (tid >> 5) / SP, sh.half = (tid >> 5) % SP, sh.lane = lane;
     const int slices = DV / (16 * W);
-    const int64_t run = blockIdx.x / slices;  // head and segment
+    const int64_t run = blockIdx.x / slices + seg.skip;  // head and segment
     const int64_t bh = run / seg.count;
     const int lo = ((int)(run % seg.count) + seg.first) * seg.len, len = min(seg.len, nchunk - lo);
     const int col0 = (blockIdx.x % slices) * 16 * W + 16 * sh.slice, slice = col0 / 16;
@@ -2391,6 +2392,31 @@ Cut cut_of(int64_t runs, int columns, int d)  // sequences or segments, value co
     return c;
 }
 
+// The runs of the last round of CTAs, where they are few enough for two CTAs each:
+// two warps per slice then end sooner than one would.  Forward and gradient, in one
+// launch and in two (us): B5 H32 N1024 d = 128 241 and 812, 219 and 752; B16 H32 N2011
+// 1052 and 3834, 1004 and 3713; B14 H16 N1024 64 x 128 190 and 705, 185 and 676.  Not
+// for smaller states: B20 H16 N1024 64 x 64 214 and 754, 215 and 766; B10 H16 32 x 32
+// 103 and 271, 101 and 348.
+int64_t tail_of(const Cut& cut, int64_t runs, int columns, int d)
+{
+    const int sms = device_sm_count();
+    if (cut.SP == 2 || columns != 16 * cut.W || d < 64 || d + columns <= 128 || runs <= sms)
+        return 0;
+    const int64_t tail = runs % sms;
+    return 2 * tail <= sms ? tail : 0;
+}
+
+// launch(cut, first run, runs) for all runs
+template <typename Launch>
+cudaError_t in_rounds(int64_t runs, int columns, int d, Launch launch)
+{
+    const Cut cut = cut_of(runs, columns, d);
+    const int64_t tail = tail_of(cut, runs, columns, d);
+    const cudaError_t e = launch(cut, (int64_t)0, runs - tail);
+    return e != cudaSuccess || !tail ? e : launch(Cut{2, cut.W / 2}, runs - tail, tail);
+}
+
 template <typename K>
 cudaError_t allow_smem(K kern, int bytes)
 {
@@ -2399,7 +2425,7 @@ cudaError_t allow_smem(K kern, int bytes)
 
 template <int D, bool GRAD, int SP, bool READS>
 cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs,
-                         const Kept& kept, const Segments& seg)
+                         const Kept& kept, const Segments& seg, int64_t runs)
 {
     const int smem = ChainSmem<D, GRAD, SP>::bytes(W);
     const cudaError_t e = allow_smem(k_delta_chain<D, GRAD, SP, READS>, smem);
@@ -2407,7 +2433,7 @@ cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, c
         return e;
     const int columns = a.dv + (seg.carry ? a.d : 0);
     k_delta_chain<D, GRAD, SP, READS>
-        <<<(unsigned)(a.B * a.H * seg.count * (columns / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+        <<<(unsigned)(runs * (columns / (16 * W))), 32 * SP * W, smem, a.stream>>>(
             rows, blobs, static_cast<const __nv_bfloat16*>(a.v),
             READS && !GRAD ? static_cast<__nv_bfloat16*>(a.out) : nullptr, a.S0,
             GRAD || seg.carry ? nullptr : a.S_out, a.N, chunks_of(a.N), (int)a.H, (int)a.Hk, a.dv,
@@ -2418,14 +2444,14 @@ cudaError_t launch_chain(const DeltaArgs& a, int W, const unsigned char* rows, c
 
 template <int D, int SP, bool GATED, bool ENDS>
 cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, const unsigned char* blobs,
-                       const Kept& kept, const Segments& seg)
+                       const Kept& kept, const Segments& seg, int64_t runs)
 {
     const int smem = RevSmem<D, SP>::bytes(W);
     const cudaError_t e = allow_smem(k_delta_rev<D, SP, GATED, ENDS>, smem);
     if (e != cudaSuccess)
         return e;
     k_delta_rev<D, SP, GATED, ENDS>
-        <<<(unsigned)(a.B * a.H * seg.count * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
+        <<<(unsigned)(runs * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
             rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
             static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, chunks_of(a.N), (int)a.H, (int)a.Hk, a.dv, kept, seg,
             a.status);
@@ -2437,9 +2463,12 @@ template <int D, bool GATED, bool ENDS>
 cudaError_t run_rev_cut(const DeltaArgs& a, const unsigned char* rows, const unsigned char* blobs, const Kept& kept,
                         const Segments& seg)
 {
-    const Cut cut = cut_of(a.B * a.H * seg.count, a.dv, D);
-    return cut.SP == 2 ? launch_rev<D, 2, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg)
-                       : launch_rev<D, 1, GATED, ENDS>(a, cut.W, rows, blobs, kept, seg);
+    return in_rounds(a.B * a.H * seg.count, a.dv, D, [&](Cut cut, int64_t first, int64_t runs) {
+        Segments x = seg;
+        x.skip = first;
+        return cut.SP == 2 ? launch_rev<D, 2, GATED, ENDS>(a, cut.W, rows, blobs, kept, x, runs)
+                           : launch_rev<D, 1, GATED, ENDS>(a, cut.W, rows, blobs, kept, x, runs);
+    });
 }
 
 template <int D, bool REV>
@@ -2459,7 +2488,7 @@ cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsig
                       unsigned char* ws)
 {
     const int n = segments_of(a);
-    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<GRAD>(), fac_at<GRAD>()};
+    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<GRAD>(), fac_at<GRAD>(), 0};
     if (n > 1) {
         const SegLayout l = seg_layout(a);
         float* start = reinterpret_cast<float*>(ws + l.start);
@@ -2467,17 +2496,21 @@ cudaError_t run_chain(const DeltaArgs& a, const unsigned char* rows, const unsig
         float* M = reinterpret_cast<float*>(ws + l.M);
         seg.len = (chunks_of(a.N) + n - 1) / n;
         const int m = GRAD ? n : n - 1;
-        const Segments ends = {m, seg.len, nullptr, 1, B, M, 0, seg.blob, seg.fac};
-        const Cut cut = cut_of(a.B * a.H * m, a.dv + a.d, D);
-        cudaError_t e = cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, Kept{}, ends)
-                                    : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, Kept{}, ends);
+        const Segments ends = {m, seg.len, nullptr, 1, B, M, 0, seg.blob, seg.fac, 0};
+        const int64_t runs = a.B * a.H * m;
+        const Cut cut = cut_of(runs, a.dv + a.d, D);
+        cudaError_t e = cut.SP == 2 ? launch_chain<D, false, 2, false>(a, cut.W, rows, blobs, Kept{}, ends, runs)
+                                    : launch_chain<D, false, 1, false>(a, cut.W, rows, blobs, Kept{}, ends, runs);
         if (e != cudaSuccess || (e = launch_join<D, false>(a, a.S0, B, M, start, n, m)) != cudaSuccess)
             return e;
         seg.count = n, seg.start = start;
     }
-    const Cut cut = cut_of(a.B * a.H * n, a.dv, D);
-    return cut.SP == 2 ? launch_chain<D, GRAD, 2, READS>(a, cut.W, rows, blobs, kept, seg)
-                       : launch_chain<D, GRAD, 1, READS>(a, cut.W, rows, blobs, kept, seg);
+    return in_rounds(a.B * a.H * n, a.dv, D, [&](Cut cut, int64_t first, int64_t runs) {
+        Segments x = seg;
+        x.skip = first;
+        return cut.SP == 2 ? launch_chain<D, GRAD, 2, READS>(a, cut.W, rows, blobs, kept, x, runs)
+                           : launch_chain<D, GRAD, 1, READS>(a, cut.W, rows, blobs, kept, x, runs);
+    });
 }
 
 // The reverse chain, after run_chain<GRAD>: it finds the segments' M where that left
@@ -2487,7 +2520,7 @@ cudaError_t run_rev(const DeltaArgs& a, const unsigned char* rows, const unsigne
                     unsigned char* ws)
 {
     const int n = segments_of(a);
-    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<true>(), fac_at<true>()};
+    Segments seg = {1, chunks_of(a.N), nullptr, 0, nullptr, nullptr, 0, blob_bytes<true>(), fac_at<true>(), 0};
     if (n > 1) {
         const SegLayout l = seg_layout(a);
         float* start = reinterpret_cast<float*>(ws + l.start);

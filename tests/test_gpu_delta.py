@@ -520,6 +520,7 @@ def test_offsets_past_32_bits(dtype, H, N):
     """v, out and their gradients hold more than 2^31 elements.  Every head has
     the same inputs and the same arithmetic, so every head's result is the
     first's bit for bit, and the first is right by a call of a few heads."""
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < (140 << 30):
         pytest.skip("needs 140 GB of device memory")
     g = torch.Generator(device="cuda").manual_seed(11)
@@ -553,6 +554,7 @@ def test_offsets_past_32_bits(dtype, H, N):
 def test_decode_offsets_past_32_bits():
     """The states hold more than 2^31 elements."""
     B, H = 131073 // 3, 3
+    torch.cuda.empty_cache()
     if torch.cuda.mem_get_info()[0] < (30 << 30):
         pytest.skip("needs 30 GB of device memory")
     g = torch.Generator(device="cuda").manual_seed(12)
@@ -594,5 +596,15 @@ def test_short_sequences_of_many_heads(N, d, dv):
 def test_many_heads_of_32_columns(d):
     """Two warps per slice although there are more slices than SMs."""
     p = problem(20, 16, 8, 140, d, 32, BF, d)
+    check_forward(p)
+    check_backward(p)
+
+
+@pytest.mark.parametrize("B,H,Hk,N,d,dv", [(10, 16, 4, 100, 128, 128), (13, 12, 6, 190, 64, 128),
+                                           (80, 4, 1, 77, 128, 64)])
+def test_a_few_heads_more_than_a_round(B, H, Hk, N, d, dv):
+    """The heads of the last round of CTAs run two warps per slice, in a launch
+    of their own."""
+    p = problem(B, H, Hk, N, d, dv, BF, B)
     check_forward(p)
     check_backward(p)
