@@ -46,11 +46,14 @@ using namespace delta;
 // What k_delta_prep writes per chunk and value head: [F hi][F lo][P hi][P lo, for
 // gradients][factors], tiles of 64 x 64 fp16 in the layout the chains read them
 // from shared memory.  k^_i = fk_i K16_i and scale q^_i = fq_i Q16_i are the mapped
-// rows, fk and fq holding the image's power of two, the L2 norm and the scale.
+// rows, fk and fq holding the image's power of two, the L2 norm and the scale.  p_i is
+// the power of two under |k^_i| (1 with LA_FM_L2): F's image is F_ij / (p_i p_j) under
+// one more power of two.
 enum Factor {
     kFacA,    // e^{G_i} fk_i
-    kFacF,    // [any] = scale of F (a power of two)
+    kFacF,    // p_i times the scale of F (a power of two)
     kFacB,    // beta
+    kFacZ,    // beta_i p_i
     kFacO,    // e^{G_i} fq_i
     kFacP,    // scale of P's row (a power of two)
     kFacW,    // e^{G_C - G_i} fk_i
@@ -61,6 +64,7 @@ enum Factor {
     kFacQ,             // fq without the scale
     kFacRk,            // 1 / |k|, or 1 without the norm
     kFacRq,
+    kFacPk,  // p
     kFacGh,  // G in base 2: a multiple of 2^-6 and the rest
     kFacGl,
     kGradFactors
@@ -95,8 +99,13 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // the diagonal
 //   X = A_IJ + sum_{J <= L < I} (A beta)_IL F_LJ,   F_IJ = -X - F_II beta X
 // as MMAs on two-part operands: (A beta)_IL are warp I's own accumulators, F_LJ the
-// image it is writing.  All of F is under one power of two per chunk (with 2^11 to
-// spare over the largest |A|; a stable recurrence does not grow that far).  Decays of
+// image it is writing.  A stable recurrence has beta_i |k_i|^2 <= 2, so with keys as
+// given beta may be as large as the key is short; everything here is therefore in units
+// of p_i, keys of length 1 to 2 with beta_i p_i^2 for beta_i: |F_ij| and |X_ij| are at
+// most |k_i| |k_j| < 4 there and beta X at most twice that, and keys of all lengths keep
+// the same bits (with beta itself in F's place beta X left fp16 at beta = 4096, and keys
+// of 1e-3 beside keys of 1 lost half of their digits).  All of F is under one power of
+// two per chunk (with 2^11 to spare over the largest |A|).  Decays of
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
 // Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
@@ -111,7 +120,7 @@ struct PrepSmem {
     static constexpr int img = 2 * row_image<D>() > fac_at<GRAD>() ? 2 * row_image<D>() : fac_at<GRAD>();
     static constexpr int diag = img;  // [4][2][16][20] fp32
     static constexpr int vec = diag + 4 * 2 * 16 * 20 * 4;
-    static constexpr int bytes = vec + (10 + n_factors<GRAD>()) * kC * 4 + 64;
+    static constexpr int bytes = vec + (13 + n_factors<GRAD>()) * kC * 4 + 64;
 };
 
 template <int D, bool GRAD>
@@ -129,7 +138,9 @@ __global__ void __launch_bounds__(kPrepThreads)
     float *rk = vec + 5 * kC, *rq = vec + 6 * kC, *uq = vec + 7 * kC;
     float* ck = vec + 8 * kC;   // fk_j times the decay from j to its block's end
     float* top = vec + 9 * kC;  // [4] largest |A|, [4] largest |A beta| of the warps
-    float* fac = vec + 10 * kC;  // [factors][kC]
+    float *pw = vec + 10 * kC, *bp = vec + 11 * kC;  // p, beta p^2
+    float* pb = vec + 12 * kC;   // what P's column takes beside fk: p beta, or p for gradients
+    float* fac = vec + 13 * kC;  // [factors][kC]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / nchunk;
@@ -189,9 +200,14 @@ __global__ void __launch_bounds__(kPrepThreads)
             if (p == 0) {
                 const float norm = l2 ? rsqrtf(ss + kL2Eps) : 1.0f;
                 (which ? rq : rk)[r] = norm;
-                (which ? fq : fk)[r] = s.from * norm * (which ? scale : 1.0f);
-                if (which)
+                if (which) {
+                    fq[r] = s.from * norm * scale;
                     uq[r] = s.from * norm;
+                } else {  // fk in units of p = 2^e, |k|^2 in [2^{2 e}, 2^{2 e + 2})
+                    const int e = l2 ? 0 : ((int)(__float_as_uint(ss) >> 23) - 127) >> 1;
+                    pw[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+                    fk[r] = s.from * norm * __uint_as_float((uint32_t)(127 - e) << 23);
+                }
             }
         }
     }
@@ -257,15 +273,19 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     if (tid < kC) {
         const float h = gh[tid], l = gl[tid], hc = gh[kC - 1], lc = gl[kC - 1];
-        const float e = exp2f(h + l);
+        const float e = exp2f(h + l), p = pw[tid], f = fk[tid] * p;
+        bp[tid] = sb[tid] * p * p;
+        pb[tid] = GRAD ? p : sb[tid] * p;
         ck[tid] = fk[tid] * exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l));
-        fac[kFacA * kC + tid] = e * fk[tid];
+        fac[kFacA * kC + tid] = e * f;
         fac[kFacB * kC + tid] = sb[tid];
+        fac[kFacZ * kC + tid] = sb[tid] * p;
         fac[kFacO * kC + tid] = e * fq[tid];
-        fac[kFacW * kC + tid] = exp2f((hc - h) + (lc - l)) * fk[tid];
+        fac[kFacW * kC + tid] = exp2f((hc - h) + (lc - l)) * f;
         fac[kFacEnd * kC + tid] = exp2f(hc + lc);
         if (GRAD) {
-            fac[kFacK * kC + tid] = fk[tid];
+            fac[kFacK * kC + tid] = f;
+            fac[kFacPk * kC + tid] = p;
             fac[kFacQ * kC + tid] = uq[tid];
             fac[kFacRk * kC + tid] = rk[tid];
             fac[kFacRq * kC + tid] = rq[tid];
@@ -290,7 +310,8 @@ __global__ void __launch_bounds__(kPrepThreads)
             for (int h = 0; h < 2; ++h) {
                 const int nt = 2 * b + h, j = 8 * nt + 2 * tq;
                 const float2 col = *reinterpret_cast<const float2*>((b < warp ? ck : fk) + j);
-                const float2 be = *reinterpret_cast<const float2*>(sb + j);
+                const float2 be = *reinterpret_cast<const float2*>(bp + j);
+                const float2 to = *reinterpret_cast<const float2*>(pb + j);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + (e >> 1) * 8, jj = j + (e & 1);
@@ -301,7 +322,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                     const float bj = e & 1 ? be.y : be.x;
                     // a select, not a product with 0: nothing to the right of the diagonal counts
                     ak[nt][e] = b < warp || jj < i ? ak[nt][e] * fki[e >> 1] * dec : 0.f;
-                    aq[nt][e] = b < warp || jj <= i ? aq[nt][e] * fqi[e >> 1] * dec * (GRAD ? 1.0f : bj) : 0.f;
+                    aq[nt][e] = b < warp || jj <= i ? aq[nt][e] * fqi[e >> 1] * dec * (e & 1 ? to.y : to.x) : 0.f;
                     pm[e >> 1] = max_abs(pm[e >> 1], aq[nt][e]);
                     am = max_abs(am, ak[nt][e]);
                     abm = max_abs(abm, ak[nt][e] * bj);
@@ -343,7 +364,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int at = g * 20 + 8 * h + 2 * tq;
-                const float2 be = *reinterpret_cast<const float2*>(sb + 16 * b + 8 * h + 2 * tq);
+                const float2 be = *reinterpret_cast<const float2*>(bp + 16 * b + 8 * h + 2 * tq);
                 const float2 minus = make_float2(-be.x, -be.y);
                 *reinterpret_cast<float2*>(sd + at) = row_a(ak[2 * b + h]);
                 *reinterpret_cast<float2*>(sd + at + 160) = row_b(ak[2 * b + h]);
@@ -357,7 +378,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     Pow2 s = pow2_for(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * 16.0f);
     const Pow2 t = pow2_for(fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
     if (tid < kC)
-        fac[kFacF * kC + tid] = s.from;
+        fac[kFacF * kC + tid] = s.from * pw[tid];
     // one element of F's images, two of a row
     auto put2 = [&](int i, int j, float x, float y) {
         uint32_t hi, lo;
@@ -414,7 +435,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                 if (L >= J && L < warp) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float2 be = *reinterpret_cast<const float2*>(sb + 16 * L + 8 * h + 2 * tq);
+                        const float2 be = *reinterpret_cast<const float2*>(bp + 16 * L + 8 * h + 2 * tq);
                         h2_split(ak[2 * L + h][0] * be.x * t.to, ak[2 * L + h][1] * be.y * t.to, hi[2 * h], lo[2 * h]);
                         h2_split(ak[2 * L + h][2] * be.x * t.to, ak[2 * L + h][3] * be.y * t.to, hi[2 * h + 1],
                                  lo[2 * h + 1]);
@@ -430,7 +451,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                 }
             }
             // X s, then beta X in F's place as the second product's operand
-            const float be0 = sb[i0], be1 = sb[i0 + 8];
+            const float be0 = bp[i0], be1 = bp[i0 + 8];
 #pragma unroll
             for (int L = 0; L < 3; ++L) {
                 if (L == J) {
@@ -904,7 +925,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         cp_wait<GRAD ? 2 : 1>();  // V
         __syncwarp();
-        // R of the own tiles, z = beta R
+        // R of the own tiles, z = beta p R
         float z[8][4];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
@@ -913,7 +934,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * i + u;
-                const float2 a = fac2(fac, kFacA, sh.tile(i), u, tq), be = fac2(fac, kFacB, sh.tile(i), u, tq);
+                const float2 a = fac2(fac, kFacA, sh.tile(i), u, tq), be = fac2(fac, kFacZ, sh.tile(i), u, tq);
                 const float2 minus = make_float2(-a.x, -a.y);
                 set_rows(r[nt], fma2(minus, row_a(r[nt]), bf2(w[2 * u])), fma2(minus, row_b(r[nt]), bf2(w[2 * u + 1])));
                 set_rows(z[nt], mul2(be, row_a(r[nt])), mul2(be, row_b(r[nt])));
@@ -1544,11 +1565,12 @@ __global__ void __launch_bounds__(256, 1)
             sh.sync();
             sh.template get<false>(1, pair(u, 2), pair(u, 3));
         }
-        // F^T z on the own tiles (all of F is under one power of two)
+        // F^T z on the own tiles: F's rows carry their factors, which go to z = beta dU
         float z0 = 0.f, z1 = 0.f, z[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
+            const float2 be = mul2(fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq),
+                                   fac2(fac, kFacF, sh.tile(nt >> 1), nt & 1, tq));
             set_rows(z[nt], mul2(be, row_a(u[nt])), mul2(be, row_b(u[nt])));
             z0 = max_abs(max_abs(z0, z[nt][0]), z[nt][1]);
             z1 = max_abs(max_abs(z1, z[nt][2]), z[nt][3]);
@@ -1569,12 +1591,12 @@ __global__ void __launch_bounds__(256, 1)
                     ldsm4t(b, addr_bt<128>(sF + part * kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
                 });
         }
-        const float f0 = y0.from * fac[kFacF * kC], f1 = y1.from * fac[kFacF * kC];
+        auto back = [&](int nt, Pow2 y) { return mul2(fac2(fac, kFacPk, sh.tile(nt >> 1), nt & 1, tq), both(y.from)); };
         if (ENDS) {  // dV alone
 #pragma unroll
             for (int nt = 0; nt < 2 * OWN; ++nt) {
-                set_rows(u[nt], fma2(both(f0), row_a(x[nt]), row_a(u[nt])),
-                         fma2(both(f1), row_b(x[nt]), row_b(u[nt])));
+                set_rows(u[nt], fma2(back(nt, y0), row_a(x[nt]), row_a(u[nt])),
+                         fma2(back(nt, y1), row_b(x[nt]), row_b(u[nt])));
                 scale_cols(u[nt], fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq));
             }
         } else {
@@ -1590,8 +1612,8 @@ __global__ void __launch_bounds__(256, 1)
                 for (int h = 0; h < 2; ++h) {
                     const int nt = 2 * i + h;
                     const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
-                    set_rows(u[nt], fma2(both(f0), row_a(x[nt]), row_a(u[nt])),
-                             fma2(both(f1), row_b(x[nt]), row_b(u[nt])));
+                    set_rows(u[nt], fma2(back(nt, y0), row_a(x[nt]), row_a(u[nt])),
+                             fma2(back(nt, y1), row_b(x[nt]), row_b(u[nt])));
                     const uint32_t* eh =
                         reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
                     const uint32_t* el = eh + kC * 8;
