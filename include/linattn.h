@@ -279,6 +279,8 @@ LA_API la_status la_favor_features(const void* x, const float* w, void* out, int
  *               divides H; value head h reads key head h / (H / Hk).
  *   beta      : [B,H,N] fp32, the writing strength.  Any finite value is
  *               taken; the recurrence is stable for 0 <= beta |k|^2 <= 2.
+ *               Beyond that the state grows, and errors are relative to the
+ *               largest values among 64 tokens.
  *   log_alpha : [B,H,N] fp32 <= 0, or NULL for no decay.  Values below -128,
  *               -inf among them, reset the state.  (A token with beta = 0 and
  *               log_alpha = 0 leaves the state as it was: right padding.)

@@ -51,7 +51,7 @@ using namespace delta;
 // one more power of two.
 enum Factor {
     kFacA,    // e^{G_i} fk_i
-    kFacF,    // p_i times the scale of F (a power of two)
+    kFacF,    // p_i times the scale of F's 16 rows (a power of two)
     kFacB,    // beta
     kFacZ,    // beta_i p_i
     kFacO,    // e^{G_i} fq_i
@@ -104,8 +104,10 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // of p_i, keys of length 1 to 2 with beta_i p_i^2 for beta_i: |F_ij| and |X_ij| are at
 // most |k_i| |k_j| < 4 there and beta X at most twice that, and keys of all lengths keep
 // the same bits (with beta itself in F's place beta X left fp16 at beta = 4096, and keys
-// of 1e-3 beside keys of 1 lost half of their digits).  All of F is under one power of
-// two per chunk (with 2^11 to spare over the largest |A|).  Decays of
+// of 1e-3 beside keys of 1 lost half of their digits).  F is under one power of two per
+// chunk, with 2^10 to spare over the largest |A|; what grows past that, in a recurrence
+// that is not stable, takes a power of two of its own per block, and at the end one per
+// 16 rows.  Decays of
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
 // Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
@@ -138,6 +140,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     float *rk = vec + 5 * kC, *rq = vec + 6 * kC, *uq = vec + 7 * kC;
     float* ck = vec + 8 * kC;   // fk_j times the decay from j to its block's end
     float* top = vec + 9 * kC;  // [4] largest |A|, [4] largest |A beta| of the warps
+    float* blk = top + 8;       // [4][4] inverse scales of F's blocks
     float *pw = vec + 10 * kC, *bp = vec + 11 * kC;  // p, beta p^2
     float* pb = vec + 12 * kC;   // what P's column takes beside fk: p beta, or p for gradients
     float* fac = vec + 13 * kC;  // [factors][kC]
@@ -375,10 +378,23 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     __syncthreads();
     // F s for s = 2^4 / max |A| and (A beta) t, both powers of two
-    Pow2 s = pow2_for(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * 16.0f);
+    const Pow2 s = pow2_for(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * 16.0f);
     const Pow2 t = pow2_for(fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
-    if (tid < kC)
-        fac[kFacF * kC + tid] = s.from * pw[tid];
+    // the scale of a block with m its largest entry of this lane: s while fp16 holds it
+    auto scale_of = [&](float m) {
+        if (!__any_sync(0xffffffffu, m * s.to > 32768.0f))
+            return s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return pow2_for(m);
+    };
+    Pow2 own = s;  // the smallest scale of the warp's blocks
+    auto keep_scale = [&](int J, Pow2 b) {
+        if (lane == 0)
+            blk[4 * warp + J] = b.from;
+        own = b.to < own.to ? b : own;
+    };
     // one element of F's images, two of a row
     auto put2 = [&](int i, int j, float x, float y) {
         uint32_t hi, lo;
@@ -389,7 +405,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     };
     {  // diagonal: column `lane & 15` of block `warp`, then its images by row pairs
         const int b = 16 * warp, j = lane & 15;
-        float f[16];
+        float f[16], m = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float x = -sd[i * 20 + j];
@@ -405,7 +421,10 @@ __global__ void __launch_bounds__(kPrepThreads)
                     x = fmaf(a.w, f[l + 3], x);
             }
             f[i] = x;
+            m = max_abs(m, x);
         }
+        const Pow2 to = scale_of(m);
+        keep_scale(warp, to);
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int i = (lane >> 3) + 4 * m, jj = (lane & 7) * 2;
-            const float2 x = mul2(*reinterpret_cast<const float2*>(sd + i * 20 + jj), both(s.to));
+            const float2 x = mul2(*reinterpret_cast<const float2*>(sd + i * 20 + jj), both(to.to));
             put2(b + i, b + jj, x.x, x.y);
         }
     }
@@ -428,11 +447,22 @@ __global__ void __launch_bounds__(kPrepThreads)
         if (warp >= dist) {
             const int J = warp - dist;
             float x[2][4];
-            clear(x);
             uint32_t hi[4], lo[4], b[4];
 #pragma unroll
             for (int L = 0; L < 3; ++L) {
+                if (L == J) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[h][e] = ak[2 * L + h][e];
+                }
+            }
+#pragma unroll
+            for (int L = 0; L < 3; ++L) {
                 if (L >= J && L < warp) {
+                    float z[2][4];
+                    clear(z);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float2 be = *reinterpret_cast<const float2*>(bp + 16 * L + 8 * h + 2 * tq);
@@ -441,32 +471,34 @@ __global__ void __launch_bounds__(kPrepThreads)
                                  lo[2 * h + 1]);
                     }
                     ldsm4t(b, addr_bt<128>(sF, lane, 16 * L, 16 * J));
-                    mma(x[0], hi, b[0], b[1]);
-                    mma(x[1], hi, b[2], b[3]);
-                    mma(x[0], lo, b[0], b[1]);
-                    mma(x[1], lo, b[2], b[3]);
+                    mma(z[0], hi, b[0], b[1]);
+                    mma(z[1], hi, b[2], b[3]);
+                    mma(z[0], lo, b[0], b[1]);
+                    mma(z[1], lo, b[2], b[3]);
                     ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * L, 16 * J));
-                    mma(x[0], hi, b[0], b[1]);
-                    mma(x[1], hi, b[2], b[3]);
-                }
-            }
-            // X s, then beta X in F's place as the second product's operand
-            const float be0 = bp[i0], be1 = bp[i0 + 8];
-#pragma unroll
-            for (int L = 0; L < 3; ++L) {
-                if (L == J) {
+                    mma(z[0], hi, b[0], b[1]);
+                    mma(z[1], hi, b[2], b[3]);
+                    const float from = t.from * blk[4 * L + J];
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            x[h][e] = fmaf(ak[2 * L + h][e], s.to, x[h][e] * t.from);
+                            x[h][e] = fmaf(z[h][e], from, x[h][e]);
                 }
             }
+            // X, then beta X in F's place as the second product's operand
             const int j0 = 16 * J + 2 * tq;
+            float m = 0.f, bx[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    bx[h][e] = bp[i0 + 8 * (e >> 1)] * x[h][e], m = max_abs(m, bx[h][e]);
+            const Pow2 q = scale_of(m);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                put2(i0, j0 + 8 * h, be0 * x[h][0], be0 * x[h][1]);
-                put2(i0 + 8, j0 + 8 * h, be1 * x[h][2], be1 * x[h][3]);
+                put2(i0, j0 + 8 * h, bx[h][0] * q.to, bx[h][1] * q.to);
+                put2(i0 + 8, j0 + 8 * h, bx[h][2] * q.to, bx[h][3] * q.to);
             }
             __syncwarp();
             float y[2][4];
@@ -483,10 +515,36 @@ __global__ void __launch_bounds__(kPrepThreads)
             mma(y[0], hi, bl[0], bl[1]);
             mma(y[1], hi, bl[2], bl[3]);
             __syncwarp();
+            const float from = -q.from * blk[5 * warp];
+            m = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[h][e] = fmaf(from, y[h][e], -x[h][e]), m = max_abs(m, y[h][e]);
+            const Pow2 f = scale_of(m);
+            keep_scale(J, f);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                put2(i0, j0 + 8 * h, fmaf(-s.from, y[h][0], -x[h][0]), fmaf(-s.from, y[h][1], -x[h][1]));
-                put2(i0 + 8, j0 + 8 * h, fmaf(-s.from, y[h][2], -x[h][2]), fmaf(-s.from, y[h][3], -x[h][3]));
+                put2(i0, j0 + 8 * h, y[h][0] * f.to, y[h][1] * f.to);
+                put2(i0 + 8, j0 + 8 * h, y[h][2] * f.to, y[h][3] * f.to);
+            }
+        }
+        if (dist < 3)
+            __syncthreads();
+    }
+    if (lane < 16)
+        fac[kFacF * kC + 16 * warp + lane] = own.from * pw[16 * warp + lane];
+    if (__syncthreads_or(own.to != s.to)) {  // the blocks of 16 rows under one scale
+        for (int J = 0; J <= warp; ++J) {
+            const __half2 f = __float2half2_rn(own.to * blk[4 * warp + J]);  // at most 1
+            unsigned char* at = smem + tile_off<128>(16 * warp + (lane >> 1), 2 * J + (lane & 1));
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint4 x = *reinterpret_cast<const uint4*>(at + part * kTile);
+                __half2* h = reinterpret_cast<__half2*>(&x);
+                h[0] = __hmul2(h[0], f), h[1] = __hmul2(h[1], f), h[2] = __hmul2(h[2], f), h[3] = __hmul2(h[3], f);
+                *reinterpret_cast<uint4*>(at + part * kTile) = x;
             }
         }
         __syncthreads();

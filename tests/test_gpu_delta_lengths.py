@@ -91,3 +91,40 @@ def test_keys_of_mixed_lengths(N, d, dv, least, dtype):
     lengths = torch.exp(torch.rand(1, 2, N, generator=g) * float(np.log(least)))
     p = problem(N, lengths, 1.0, N + 1, dtype, d, dv)
     check(p, rows=("dv",))
+
+
+def beyond(p):
+    """Outside the stable range results grow by orders of magnitude within a chunk: they are finite while
+    fp32 holds them, and of a chunk's largest values as right as bf16 numbers are (2 x 2^-8)."""
+    h = lambda n: None if p[n] is None else to_np(p[n])  # noqa: E731
+    scale = p["q"].shape[-1] ** -0.5
+    args = [p[n] for n in INPUTS]
+    got = list(la.la_forward_delta(*args, feature_map="none", return_state=True))
+    ref = list(delta.forward(*map(h, INPUTS), scale=scale, l2=False))
+    got += la.la_backward_delta(p["dout"], *args, feature_map="none")
+    ref += delta.backward(h("dout"), *map(h, INPUTS), scale=scale, l2=False)
+    for name, g, r in zip(("out", "S") + NAMES, got, ref):
+        if g is not None:
+            two, most, _ = errors(g, r)
+            print(f"{name}: 2-norm {two:.2e}, largest {most:.2e}")
+            assert two <= 2 * 2.0 ** -8 and most <= 2 * 2.0 ** -8, (name, two, most)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [17, 64, 100, 130])
+@pytest.mark.parametrize("writing", [2.2])
+def test_a_repeated_key_that_grows(N, writing, dtype):
+    """One key everywhere: the state's row is multiplied by 1 - beta |k|^2 = -1.2 or -1.5 at each token,
+    1e5 or 1e11 over a chunk."""
+    p = problem(N, torch.ones(1, 2, N), writing, 5, dtype, gated=False)
+    p["k"][:] = p["k"][:, :, :1]
+    beyond(p)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("at", [3, 30, 63])
+def test_one_token_writes_far_too_strongly(at, dtype):
+    """beta |k|^2 = 1e4 at one token among ones."""
+    p = problem(100, torch.ones(1, 2, 100), 1.0, 6 + at, dtype)
+    p["beta"][:, :, at] *= 1e4
+    beyond(p)
