@@ -47,19 +47,20 @@ using namespace delta;
 // gradients][factors], tiles of 64 x 64 fp16 in the layout the chains read them
 // from shared memory.  k^_i = fk_i K16_i and scale q^_i = fq_i Q16_i are the mapped
 // rows, fk and fq holding the image's power of two, the L2 norm and the scale.  p_i is
-// the power of two under |k^_i| (1 with LA_FM_L2): F's image is F_ij / (p_i p_j) under
-// one more power of two.
+// the power of two under |k^_i| (1 with LA_FM_L2): F's image is F_ij / (p_i p_j r_i c_j)
+// with powers of two r and c of 16 tokens each (r one for the chunk and c = 1 in a stable
+// recurrence).
 enum Factor {
     kFacA,    // e^{G_i} fk_i
-    kFacF,    // p_i times the scale of F's 16 rows (a power of two)
-    kFacB,    // beta
-    kFacZ,    // beta_i p_i
+    kFacF,    // p_i r_i
+    kFacZ,    // beta_i p_i c_i
     kFacO,    // e^{G_i} fq_i
     kFacP,    // scale of P's row (a power of two)
     kFacW,    // e^{G_C - G_i} fk_i
     kFacEnd,  // [0] = e^{G_C}
+    kFacB,    // beta
     kFactors,
-    // gradients only
+    // gradients only; k_delta_dqk reads kFacB to kFacGl
     kFacK = kFactors,  // fk
     kFacQ,             // fq without the scale
     kFacRk,            // 1 / |k|, or 1 without the norm
@@ -67,6 +68,8 @@ enum Factor {
     kFacPk,  // p
     kFacGh,  // G in base 2: a multiple of 2^-6 and the rest
     kFacGl,
+    kFacC,   // p c
+    kFacBF,  // beta p r
     kGradFactors
 };
 constexpr int kTile = kC * kC * 2;  // bytes of a 64 x 64 fp16 tile
@@ -107,7 +110,8 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // of 1e-3 beside keys of 1 lost half of their digits).  F is under one power of two per
 // chunk, with 2^10 to spare over the largest |A|; what grows past that, in a recurrence
 // that is not stable, takes a power of two of its own per block, and at the end one per
-// 16 rows.  Decays of
+// 16 rows and one per 16 columns (growth over i - j tokens is a product of the two).
+// Decays of
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
 // Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
@@ -122,7 +126,10 @@ struct PrepSmem {
     static constexpr int img = 2 * row_image<D>() > fac_at<GRAD>() ? 2 * row_image<D>() : fac_at<GRAD>();
     static constexpr int diag = img;  // [4][2][16][20] fp32
     static constexpr int vec = diag + 4 * 2 * 16 * 20 * 4;
-    static constexpr int bytes = vec + (13 + n_factors<GRAD>()) * kC * 4 + 64;
+    // arrays beside the factors.  With four blocks on an SM a gradient stays under 196 KB
+    // of shared memory, which leaves L1 twice of what more would (108 against 116 us)
+    static constexpr int own = GRAD ? 6 : 9;
+    static constexpr int bytes = vec + (own + n_factors<GRAD>()) * kC * 4 + 64;
 };
 
 template <int D, bool GRAD>
@@ -136,14 +143,15 @@ __global__ void __launch_bounds__(kPrepThreads)
     using SM = PrepSmem<D, GRAD>;
     constexpr int RB = 2 * D;  // bytes per row
     float* vec = reinterpret_cast<float*>(smem + SM::vec);
-    float *fk = vec, *fq = vec + kC, *gh = vec + 2 * kC, *gl = vec + 3 * kC, *sb = vec + 4 * kC;
-    float *rk = vec + 5 * kC, *rq = vec + 6 * kC, *uq = vec + 7 * kC;
-    float* ck = vec + 8 * kC;   // fk_j times the decay from j to its block's end
-    float* top = vec + 9 * kC;  // [4] largest |A|, [4] largest |A beta| of the warps
-    float* blk = top + 8;       // [4][4] inverse scales of F's blocks
-    float *pw = vec + 10 * kC, *bp = vec + 11 * kC;  // p, beta p^2
-    float* pb = vec + 12 * kC;   // what P's column takes beside fk: p beta, or p for gradients
-    float* fac = vec + 13 * kC;  // [factors][kC]
+    float *fk = vec, *fq = vec + kC;  // fk: in units of p
+    float* ck = vec + 2 * kC;         // fk_j times the decay from j to its block's end
+    float* bp = vec + 3 * kC;         // beta p^2
+    float *pk = vec + 4 * kC, *pck = vec + 5 * kC;  // fk and ck of P's columns: times p beta (gradients: p)
+    float* fac = vec + SM::own * kC;  // [factors][kC]
+    float *gh = GRAD ? fac + kFacGh * kC : vec + 6 * kC, *gl = GRAD ? fac + kFacGl * kC : vec + 7 * kC;
+    float *pw = GRAD ? fac + kFacPk * kC : vec + 8 * kC, *sb = fac + kFacB * kC;
+    float* top = fac + kFacEnd * kC + 8;  // [4] largest |A|, [4] largest |A beta| of the warps
+    float* blk = top + 8;                 // [4][4] inverse scales of F's blocks beside the chunk's
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t bh = blockIdx.x / nchunk;
@@ -202,15 +210,13 @@ __global__ void __launch_bounds__(kPrepThreads)
             }
             if (p == 0) {
                 const float norm = l2 ? rsqrtf(ss + kL2Eps) : 1.0f;
-                (which ? rq : rk)[r] = norm;
-                if (which) {
-                    fq[r] = s.from * norm * scale;
-                    uq[r] = s.from * norm;
-                } else {  // fk in units of p = 2^e, |k|^2 in [2^{2 e}, 2^{2 e + 2})
-                    const int e = l2 ? 0 : ((int)(__float_as_uint(ss) >> 23) - 127) >> 1;
-                    pw[r] = __uint_as_float((uint32_t)(127 + e) << 23);
-                    fk[r] = s.from * norm * __uint_as_float((uint32_t)(127 - e) << 23);
-                }
+                (which ? fq : fk)[r] = s.from * norm * (which ? scale : 1.0f);
+                if (!which)
+                    pw[r] = ss;  // for now
+                if (GRAD)
+                    fac[(which ? kFacRq : kFacRk) * kC + r] = norm;
+                if (GRAD && which)
+                    fac[kFacQ * kC + r] = s.from * norm;
             }
         }
     }
@@ -276,24 +282,24 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     if (tid < kC) {
         const float h = gh[tid], l = gl[tid], hc = gh[kC - 1], lc = gl[kC - 1];
-        const float e = exp2f(h + l), p = pw[tid], f = fk[tid] * p;
+        // p = 2^x where |k|^2 is in [2^{2 x}, 2^{2 x + 2}), and fk in units of it
+        const int x = l2 ? 0 : ((int)(__float_as_uint(pw[tid]) >> 23) - 127) >> 1;
+        const float e = exp2f(h + l), f = fk[tid], p = __uint_as_float((uint32_t)(127 + x) << 23);
+        pw[tid] = p;
+        fk[tid] = f * __uint_as_float((uint32_t)(127 - x) << 23);
         bp[tid] = sb[tid] * p * p;
-        pb[tid] = GRAD ? p : sb[tid] * p;
-        ck[tid] = fk[tid] * exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l));
+        const float to = exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l)), fp = GRAD ? f : f * sb[tid];
+        ck[tid] = fk[tid] * to;
+        pk[tid] = fp, pck[tid] = fp * to;
         fac[kFacA * kC + tid] = e * f;
-        fac[kFacB * kC + tid] = sb[tid];
         fac[kFacZ * kC + tid] = sb[tid] * p;
         fac[kFacO * kC + tid] = e * fq[tid];
         fac[kFacW * kC + tid] = exp2f((hc - h) + (lc - l)) * f;
-        fac[kFacEnd * kC + tid] = exp2f(hc + lc);
+        if (tid == 0)
+            fac[kFacEnd * kC] = exp2f(hc + lc);
         if (GRAD) {
             fac[kFacK * kC + tid] = f;
-            fac[kFacPk * kC + tid] = p;
-            fac[kFacQ * kC + tid] = uq[tid];
-            fac[kFacRk * kC + tid] = rk[tid];
-            fac[kFacRq * kC + tid] = rq[tid];
-            fac[kFacGh * kC + tid] = h;
-            fac[kFacGl * kC + tid] = l;
+            fac[kFacC * kC + tid] = p;
         }
     }
     __syncthreads();  // the images are read: F and P take their place
@@ -314,18 +320,17 @@ __global__ void __launch_bounds__(kPrepThreads)
                 const int nt = 2 * b + h, j = 8 * nt + 2 * tq;
                 const float2 col = *reinterpret_cast<const float2*>((b < warp ? ck : fk) + j);
                 const float2 be = *reinterpret_cast<const float2*>(bp + j);
-                const float2 to = *reinterpret_cast<const float2*>(pb + j);
+                const float2 pcol = *reinterpret_cast<const float2*>((b < warp ? pck : pk) + j);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = i0 + (e >> 1) * 8, jj = j + (e & 1);
                     float dec = row[e >> 1];
                     if (b == warp)
                         dec = jj <= i ? exp2f((gh[i] - gh[jj]) + (gl[i] - gl[jj])) : 0.f;
-                    dec *= e & 1 ? col.y : col.x;
                     const float bj = e & 1 ? be.y : be.x;
                     // a select, not a product with 0: nothing to the right of the diagonal counts
-                    ak[nt][e] = b < warp || jj < i ? ak[nt][e] * fki[e >> 1] * dec : 0.f;
-                    aq[nt][e] = b < warp || jj <= i ? aq[nt][e] * fqi[e >> 1] * dec * (e & 1 ? to.y : to.x) : 0.f;
+                    ak[nt][e] = b < warp || jj < i ? ak[nt][e] * fki[e >> 1] * (dec * (e & 1 ? col.y : col.x)) : 0.f;
+                    aq[nt][e] = b < warp || jj <= i ? aq[nt][e] * fqi[e >> 1] * (dec * (e & 1 ? pcol.y : pcol.x)) : 0.f;
                     pm[e >> 1] = max_abs(pm[e >> 1], aq[nt][e]);
                     am = max_abs(am, ak[nt][e]);
                     abm = max_abs(abm, ak[nt][e] * bj);
@@ -380,32 +385,37 @@ __global__ void __launch_bounds__(kPrepThreads)
     // F s for s = 2^4 / max |A| and (A beta) t, both powers of two
     const Pow2 s = pow2_for(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * 16.0f);
     const Pow2 t = pow2_for(fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
-    // the scale of a block with m its largest entry of this lane: s while fp16 holds it
-    auto scale_of = [&](float m) {
-        if (!__any_sync(0xffffffffu, m * s.to > 32768.0f))
-            return s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        return pow2_for(m);
-    };
-    Pow2 own = s;  // the smallest scale of the warp's blocks
-    auto keep_scale = [&](int J, Pow2 b) {
-        if (lane == 0)
-            blk[4 * warp + J] = b.from;
-        own = b.to < own.to ? b : own;
-    };
-    // one element of F's images, two of a row
+    // The first time round every block is under s, and what fp16 does not hold is only
+    // noticed; then a block that leaves fp16 under s takes a scale of its own beside it
+    bool careful = false;
+    uint32_t bad = 0;  // not 0 once infinities have come
+    // two elements of F's images, x and y of a row
     auto put2 = [&](int i, int j, float x, float y) {
         uint32_t hi, lo;
         h2_split(x, y, hi, lo);
+        asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(bad) : "r"(hi), "r"(0));
         unsigned char* at = smem + tile_off<128>(i, j >> 3) + (j & 7) * 2;
         *reinterpret_cast<uint32_t*>(at) = hi;
         *reinterpret_cast<uint32_t*>(at + kTile) = lo;
     };
-    {  // diagonal: column `lane & 15` of block `warp`, then its images by row pairs
-        const int b = 16 * warp, j = lane & 15;
-        float f[16], m = 0.f;
+    // that scale for a block's 16 x 16 entries x, which are multiplied by it
+    auto own_scale = [&](float* x, int n) {
+        float m = 0.f;
+        for (int i = 0; i < n; ++i)
+            m = max_abs(m, x[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        Pow2 q = {1.0f, 1.0f};
+        if (m > 32768.0f)
+            q = pow2_for(m);
+        for (int i = 0; i < n; ++i)
+            x[i] *= q.to;
+        return q.from;
+    };
+    {  // the diagonal block: column `lane & 15` of block `warp`
+        const int j = lane & 15;
+        float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float x = -sd[i * 20 + j];
@@ -421,10 +431,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                     x = fmaf(a.w, f[l + 3], x);
             }
             f[i] = x;
-            m = max_abs(m, x);
         }
-        const Pow2 to = scale_of(m);
-        keep_scale(warp, to);
         __syncwarp();
         if (lane < 16) {
 #pragma unroll
@@ -432,112 +439,136 @@ __global__ void __launch_bounds__(kPrepThreads)
                 sd[i * 20 + j] = f[i];
         }
         __syncwarp();
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int i = (lane >> 3) + 4 * m, jj = (lane & 7) * 2;
-            const float2 x = mul2(*reinterpret_cast<const float2*>(sd + i * 20 + jj), both(to.to));
-            put2(b + i, b + jj, x.x, x.y);
-        }
     }
-    __syncthreads();
-    // off-diagonal: at distance `dist` warp I computes block (I, I - dist)
+    auto keep_rows = [&](float r) {
+        if (lane < 16) {
+            const int i = 16 * warp + lane;
+            fac[kFacF * kC + i] = r * pw[i];
+            if (GRAD)
+                fac[kFacBF * kC + i] = r * pw[i] * sb[i];
+        }
+    };
+    keep_rows(s.from);
     const uint32_t sF = smem_addr(smem);
+    for (;; careful = true) {
+        {  // its images by row pairs
+            const int i = 16 * warp + (lane >> 3), jj = (lane & 7) * 2;
+            float f[8];
 #pragma unroll
-    for (int dist = 1; dist < 4; ++dist) {
-        if (warp >= dist) {
-            const int J = warp - dist;
-            float x[2][4];
-            uint32_t hi[4], lo[4], b[4];
-#pragma unroll
-            for (int L = 0; L < 3; ++L) {
-                if (L == J) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[h][e] = ak[2 * L + h][e];
-                }
+            for (int m = 0; m < 4; ++m) {
+                const float2 x = mul2(*reinterpret_cast<const float2*>(sd + (i + 4 * m - 16 * warp) * 20 + jj), both(s.to));
+                f[2 * m] = x.x, f[2 * m + 1] = x.y;
             }
+            if (careful)
+                blk[5 * warp] = own_scale(f, 8);
 #pragma unroll
-            for (int L = 0; L < 3; ++L) {
-                if (L >= J && L < warp) {
-                    float z[2][4];
-                    clear(z);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 be = *reinterpret_cast<const float2*>(bp + 16 * L + 8 * h + 2 * tq);
-                        h2_split(ak[2 * L + h][0] * be.x * t.to, ak[2 * L + h][1] * be.y * t.to, hi[2 * h], lo[2 * h]);
-                        h2_split(ak[2 * L + h][2] * be.x * t.to, ak[2 * L + h][3] * be.y * t.to, hi[2 * h + 1],
-                                 lo[2 * h + 1]);
-                    }
-                    ldsm4t(b, addr_bt<128>(sF, lane, 16 * L, 16 * J));
-                    mma(z[0], hi, b[0], b[1]);
-                    mma(z[1], hi, b[2], b[3]);
-                    mma(z[0], lo, b[0], b[1]);
-                    mma(z[1], lo, b[2], b[3]);
-                    ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * L, 16 * J));
-                    mma(z[0], hi, b[0], b[1]);
-                    mma(z[1], hi, b[2], b[3]);
-                    const float from = t.from * blk[4 * L + J];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[h][e] = fmaf(z[h][e], from, x[h][e]);
-                }
-            }
-            // X, then beta X in F's place as the second product's operand
-            const int j0 = 16 * J + 2 * tq;
-            float m = 0.f, bx[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    bx[h][e] = bp[i0 + 8 * (e >> 1)] * x[h][e], m = max_abs(m, bx[h][e]);
-            const Pow2 q = scale_of(m);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                put2(i0, j0 + 8 * h, bx[h][0] * q.to, bx[h][1] * q.to);
-                put2(i0 + 8, j0 + 8 * h, bx[h][2] * q.to, bx[h][3] * q.to);
-            }
-            __syncwarp();
-            float y[2][4];
-            clear(y);
-            uint32_t bl[4];
-            ldsm4(hi, addr_a<128>(sF, lane, 16 * warp, 16 * warp));
-            ldsm4(lo, addr_a<128>(sF + kTile, lane, 16 * warp, 16 * warp));
-            ldsm4t(b, addr_bt<128>(sF, lane, 16 * warp, 16 * J));
-            ldsm4t(bl, addr_bt<128>(sF + kTile, lane, 16 * warp, 16 * J));
-            mma(y[0], hi, b[0], b[1]);
-            mma(y[1], hi, b[2], b[3]);
-            mma(y[0], lo, b[0], b[1]);
-            mma(y[1], lo, b[2], b[3]);
-            mma(y[0], hi, bl[0], bl[1]);
-            mma(y[1], hi, bl[2], bl[3]);
-            __syncwarp();
-            const float from = -q.from * blk[5 * warp];
-            m = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[h][e] = fmaf(from, y[h][e], -x[h][e]), m = max_abs(m, y[h][e]);
-            const Pow2 f = scale_of(m);
-            keep_scale(J, f);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                put2(i0, j0 + 8 * h, y[h][0] * f.to, y[h][1] * f.to);
-                put2(i0 + 8, j0 + 8 * h, y[h][2] * f.to, y[h][3] * f.to);
-            }
+            for (int m = 0; m < 4; ++m)
+                put2(i + 4 * m, 16 * warp + jj, f[2 * m], f[2 * m + 1]);
         }
-        if (dist < 3)
-            __syncthreads();
+        __syncthreads();
+        // off-diagonal: at distance `dist` warp I computes block (I, I - dist)
+#pragma unroll 1
+        for (int dist = 1; dist < 4; ++dist) {
+            if (warp >= dist) {
+                const int J = warp - dist;
+                float x[2][4];
+                uint32_t hi[4], lo[4], b[4];
+#pragma unroll
+                for (int L = 0; L < 3; ++L) {
+                    if (L == J) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[h][e] = ak[2 * L + h][e] * s.to;
+                    }
+                }
+#pragma unroll
+                for (int L = 0; L < 3; ++L) {
+                    if (L >= J && L < warp) {
+                        float z[2][4];
+                        clear(z);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 be = *reinterpret_cast<const float2*>(bp + 16 * L + 8 * h + 2 * tq);
+                            h2_split(ak[2 * L + h][0] * be.x * t.to, ak[2 * L + h][1] * be.y * t.to, hi[2 * h], lo[2 * h]);
+                            h2_split(ak[2 * L + h][2] * be.x * t.to, ak[2 * L + h][3] * be.y * t.to, hi[2 * h + 1],
+                                     lo[2 * h + 1]);
+                        }
+                        ldsm4t(b, addr_bt<128>(sF, lane, 16 * L, 16 * J));
+                        mma(z[0], hi, b[0], b[1]);
+                        mma(z[1], hi, b[2], b[3]);
+                        mma(z[0], lo, b[0], b[1]);
+                        mma(z[1], lo, b[2], b[3]);
+                        ldsm4t(b, addr_bt<128>(sF + kTile, lane, 16 * L, 16 * J));
+                        mma(z[0], hi, b[0], b[1]);
+                        mma(z[1], hi, b[2], b[3]);
+                        const float from = careful ? t.from * blk[4 * L + J] : t.from;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[h][e] = fmaf(z[h][e], from, x[h][e]);
+                    }
+                }
+                // X s, then beta X in F's place as the second product's operand
+                const int j0 = 16 * J + 2 * tq;
+                const float be0 = bp[i0], be1 = bp[i0 + 8];
+                float from = -s.from, y[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[h][e] = (e >> 1 ? be1 : be0) * x[h][e];
+                if (careful)
+                    from *= own_scale(y[0], 8) * blk[5 * warp];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    put2(i0, j0 + 8 * h, y[h][0], y[h][1]);
+                    put2(i0 + 8, j0 + 8 * h, y[h][2], y[h][3]);
+                }
+                __syncwarp();
+                clear(y);
+                uint32_t bl[4];
+                ldsm4(hi, addr_a<128>(sF, lane, 16 * warp, 16 * warp));
+                ldsm4(lo, addr_a<128>(sF + kTile, lane, 16 * warp, 16 * warp));
+                ldsm4t(b, addr_bt<128>(sF, lane, 16 * warp, 16 * J));
+                ldsm4t(bl, addr_bt<128>(sF + kTile, lane, 16 * warp, 16 * J));
+                mma(y[0], hi, b[0], b[1]);
+                mma(y[1], hi, b[2], b[3]);
+                mma(y[0], lo, b[0], b[1]);
+                mma(y[1], lo, b[2], b[3]);
+                mma(y[0], hi, bl[0], bl[1]);
+                mma(y[1], hi, bl[2], bl[3]);
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[h][e] = fmaf(from, y[h][e], -x[h][e]);
+                if (careful)
+                    blk[4 * warp + J] = own_scale(y[0], 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    put2(i0, j0 + 8 * h, y[h][0], y[h][1]);
+                    put2(i0 + 8, j0 + 8 * h, y[h][2], y[h][3]);
+                }
+            }
+            if (dist < 3)
+                __syncthreads();
+        }
+        if (careful || !__syncthreads_or(bad))
+            break;
     }
-    if (lane < 16)
-        fac[kFacF * kC + 16 * warp + lane] = own.from * pw[16 * warp + lane];
-    if (__syncthreads_or(own.to != s.to)) {  // the blocks of 16 rows under one scale
+    if (careful) {  // blocks to rows and columns: c by the last rows, r what is left
+        __syncthreads();
+        const int last = (n - 1) >> 4;
+        auto c = [&](int J) { return J <= last ? blk[4 * last + J] / blk[4 * last] : 1.0f; };
+        float r = 0.f;
+        for (int J = 0; J <= warp; ++J)
+            r = fmaxf(r, blk[4 * warp + J] / c(J));
         for (int J = 0; J <= warp; ++J) {
-            const __half2 f = __float2half2_rn(own.to * blk[4 * warp + J]);  // at most 1
+            const __half2 f = __float2half2_rn(blk[4 * warp + J] / (r * c(J)));  // at most 1
             unsigned char* at = smem + tile_off<128>(16 * warp + (lane >> 1), 2 * J + (lane & 1));
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -546,6 +577,13 @@ __global__ void __launch_bounds__(kPrepThreads)
                 h[0] = __hmul2(h[0], f), h[1] = __hmul2(h[1], f), h[2] = __hmul2(h[2], f), h[3] = __hmul2(h[3], f);
                 *reinterpret_cast<uint4*>(at + part * kTile) = x;
             }
+        }
+        keep_rows(s.from * r);
+        if (lane < 16) {
+            const int i = 16 * warp + lane;
+            fac[kFacZ * kC + i] *= c(warp);
+            if (GRAD)
+                fac[kFacC * kC + i] *= c(warp);
         }
         __syncthreads();
     }
@@ -598,17 +636,18 @@ struct ChainSmem {
 // What the forward pass of a gradient keeps per chunk, in the fragments' own
 // order ([16 columns][16-step][register][lane], every store 128 bytes): the state
 // before the chunk and E, as two fp16 parts with a scale per value column (states:
-// per column and half of their rows).  An 8 x 8 block is 128 bytes with its rows in
+// per column and half of their rows; E and dV: per column and 16 tokens, dV in units of
+// 1 / p as beta goes with the square of that).  An 8 x 8 block is 128 bytes with its rows in
 // order, so k_delta_dqk reads it with ldmatrix whichever way round it needs it.
 struct Kept {
     unsigned char* S;   // [BH][nchunk + 1][2 parts][D DV] fp16
     float* sS;          // [BH][nchunk + 1][2][DV]
     unsigned char* E;   // [BH][nchunk][2 parts][64 DV] fp16
-    float* sE;          // [BH][nchunk][DV]
+    float* sE;          // [BH][nchunk][4][DV]
     unsigned char* dS;  // [BH][nchunk][D DV] fp16: gradient of the state after the chunk
     float* sD;          // [BH][nchunk][2][DV]
     unsigned char* dV;  // [BH][nchunk][64 DV] fp16
-    float* sV;          // [BH][nchunk][DV]
+    float* sV;          // [BH][nchunk][4][DV]
     float* oo;          // [BH][DV / 16][N] dO.O over 16 columns
     float* vv;          // [BH][DV / 16][N] v.dV
     float* bb;          // [BH][DV / 16][N] Y.E
@@ -742,6 +781,13 @@ struct Share {
 __device__ __forceinline__ float2 fac2(const float* fac, int which, int t, int nt, int tq)
 {
     return *reinterpret_cast<const float2*>(fac + which * kC + 16 * t + 8 * nt + 2 * tq);
+}
+
+// the scale of one column (e = 0: g, 2: g + 8) over the 16 tokens of tile i of x
+__device__ __forceinline__ Pow2 tile_scale(const float (&x)[8][4], int i, int e)
+{
+    const float *a = x[2 * i] + e, *b = x[2 * i + 1] + e;
+    return pow2_for(quad_max(fmaxf(fmaxf(fabsf(a[0]), fabsf(a[1])), fmaxf(fabsf(b[0]), fabsf(b[1])))));
 }
 
 // acc[2 i], acc[2 i + 1] += a b[i].  A product on two parts goes over all tiles with
@@ -983,7 +1029,7 @@ __global__ void __launch_bounds__(256, 1)
         }
         cp_wait<GRAD ? 2 : 1>();  // V
         __syncwarp();
-        // R of the own tiles, z = beta p R
+        // R of the own tiles, z = beta p c R
         float z[8][4];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
@@ -1051,19 +1097,19 @@ __global__ void __launch_bounds__(256, 1)
             sh.sync();
             sh.template get<false>(3, pair(r, 2), pair(r, 3));
         }
-        // r is E; its largest is wanted for O, and for what a gradient keeps
+        // r is E; its largest is wanted for O
         max8(r);
         if (GRAD) {
-            const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
+                const Pow2 q0 = tile_scale(r, i, 0), q1 = tile_scale(r, i, 2);
                 uint32_t hi[4], lo[4];
                 split8(r, i, q0, q1, hi, lo);
                 keep_parts(kept.E, bh * nchunk + c, kC * DV * 2, (col0 / 16) * 4 + sh.tile(i), lane, hi, lo);
-            }
-            if (tq == 0 && sh.half == 0) {
-                float* se = kept.sE + (bh * nchunk + c) * DV + col0;
-                se[g] = q0.from, se[g + 8] = q1.from;
+                if (tq == 0) {
+                    float* se = kept.sE + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
+                    se[g] = q0.from, se[g + 8] = q1.from;
+                }
             }
         }
         // U = beta E, and the largest of the state update's factor times it
@@ -1528,10 +1574,13 @@ __global__ void __launch_bounds__(256, 1)
             ask_state(c);
             sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
         }
-        float se0 = 0.f, se1 = 0.f;
+        float se[OWN][2];
         if (!ENDS) {
-            const float* se = kept.sE + (bh * nchunk + c) * DV + col0;
-            se0 = se[g], se1 = se[g + 8];
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const float* at = kept.sE + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
+                se[i][0] = at[g], se[i][1] = at[g + 8];
+            }
         }
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
             return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
@@ -1627,8 +1676,7 @@ __global__ void __launch_bounds__(256, 1)
         float z0 = 0.f, z1 = 0.f, z[8][4];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
-            const float2 be = mul2(fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq),
-                                   fac2(fac, kFacF, sh.tile(nt >> 1), nt & 1, tq));
+            const float2 be = fac2(fac, kFacBF, sh.tile(nt >> 1), nt & 1, tq);
             set_rows(z[nt], mul2(be, row_a(u[nt])), mul2(be, row_b(u[nt])));
             z0 = max_abs(max_abs(z0, z[nt][0]), z[nt][1]);
             z1 = max_abs(max_abs(z1, z[nt][2]), z[nt][3]);
@@ -1649,7 +1697,7 @@ __global__ void __launch_bounds__(256, 1)
                     ldsm4t(b, addr_bt<128>(sF + part * kTile, lane, 16 * sh.tile(kk), 16 * sh.tile(i)));
                 });
         }
-        auto back = [&](int nt, Pow2 y) { return mul2(fac2(fac, kFacPk, sh.tile(nt >> 1), nt & 1, tq), both(y.from)); };
+        auto back = [&](int nt, Pow2 y) { return mul2(fac2(fac, kFacC, sh.tile(nt >> 1), nt & 1, tq), both(y.from)); };
         if (ENDS) {  // dV alone
 #pragma unroll
             for (int nt = 0; nt < 2 * OWN; ++nt) {
@@ -1680,8 +1728,8 @@ __global__ void __launch_bounds__(256, 1)
                     const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
                     const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
                     const int part = nt >> 2, k = 2 * (nt & 3);
-                    bsum[part][k] = u[nt][0] * (se0 * (a0.x + l0.x)) + u[nt][2] * (se1 * (a1.x + l1.x));
-                    bsum[part][k + 1] = u[nt][1] * (se0 * (a0.y + l0.y)) + u[nt][3] * (se1 * (a1.y + l1.y));
+                    bsum[part][k] = u[nt][0] * (se[i][0] * (a0.x + l0.x)) + u[nt][2] * (se[i][1] * (a1.x + l1.x));
+                    bsum[part][k + 1] = u[nt][1] * (se[i][0] * (a0.y + l0.y)) + u[nt][3] * (se[i][1] * (a1.y + l1.y));
                     u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
                     vsum[part][k] = u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]);
                     vsum[part][k + 1] = u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]);
@@ -1700,40 +1748,38 @@ __global__ void __launch_bounds__(256, 1)
         if (SP > 1)
             sh.template get<false>(2, pair(u, 2), pair(u, 3));
         if (!ENDS) {
-            // dV leaves as bf16 (V's tile is read) and is kept as scaled fp16
-            float v0 = 0.f, v1 = 0.f;
+            // dV leaves as bf16 (V's tile is read) and is kept, times p, as scaled fp16
+            __syncwarp();
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                v0 = max_abs(max_abs(v0, u[nt][0]), u[nt][1]);
-                v1 = max_abs(max_abs(v1, u[nt][2]), u[nt][3]);
-            }
-            {
-                const Pow2 s0 = pow2_for(quad_max(v0)), s1 = pow2_for(quad_max(v1));
-                __syncwarp();
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t w[4], a[4];
+                float y[8][4];  // the first two C tiles: p dV
 #pragma unroll
-                for (int i = 0; i < OWN; ++i) {
-                    uint32_t w[4], a[4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int nt = 2 * i + h;
-                        w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
-                        w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
-                        a[2 * h] = h2(u[nt][0] * s0.to, u[nt][1] * s0.to);
-                        a[2 * h + 1] = h2(u[nt][2] * s1.to, u[nt][3] * s1.to);
-                    }
-                    stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
-                    keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 p = fac2(fac, kFacPk, sh.tile(i), h, tq);
+                    set_rows(y[h], mul2(p, row_a(u[2 * i + h])), mul2(p, row_b(u[2 * i + h])));
                 }
+                const Pow2 s0 = tile_scale(y, 0, 0), s1 = tile_scale(y, 0, 2);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int nt = 2 * i + h;
+                    w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
+                    w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
+                    a[2 * h] = h2(y[h][0] * s0.to, y[h][1] * s0.to);
+                    a[2 * h + 1] = h2(y[h][2] * s1.to, y[h][3] * s1.to);
+                }
+                stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
+                keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
                 if (tq == 0) {
-                    float* sd = kept.sD + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
-                    sd[g] = p0.from, sd[g + 8] = p1.from;
-                    if (SP == 1)
-                        sd[DV + g] = p0.from, sd[DV + g + 8] = p1.from;
-                    if (sh.half == 0) {
-                        float* sw = kept.sV + (bh * nchunk + c) * DV + col0;
-                        sw[g] = s0.from, sw[g + 8] = s1.from;
-                    }
+                    float* sw = kept.sV + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
+                    sw[g] = s0.from, sw[g + 8] = s1.from;
                 }
+            }
+            if (tq == 0) {
+                float* sd = kept.sD + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
+                sd[g] = p0.from, sd[g + 8] = p1.from;
+                if (SP == 1)
+                    sd[DV + g] = p0.from, sd[DV + g + 8] = p1.from;
             }
             __syncwarp();
             {
@@ -1828,9 +1874,9 @@ __global__ void __launch_bounds__(256, 1)
 //
 // then through scale and norm to the inputs.  Two warps own 16 tokens of dQ or
 // of dK, each half of the d columns and of the token tiles.  The kept planes arrive with a scale per value column,
-// the contracted index here; they are brought under one scale each in shared
-// memory (a power of two: exact but for columns under 2^-24 of the largest), so
-// that fragments go from ldmatrix into the MMA as they are and every factor is
+// the contracted index here; they are brought under one scale each (E and dV: one for
+// 16 tokens) in shared memory (a power of two: exact but for columns under 2^-24 of the
+// largest), so that fragments go from ldmatrix into the MMA as they are and every factor is
 // one of a row, applied to fp32 accumulators.  The 64 x 64 matrices pass through a
 // tile of the two warps' own as fp16 rows, each half under a power of two.  One fp16 part
 // throughout: 2^-12 of a term, a sixteenth of the bf16 rounding of the results.  (A result
@@ -1852,21 +1898,21 @@ template <int D, int DV>
 struct DqkSmem {
     // a step's token planes, factors and column scales, twice
     static constexpr int E = 0, dV = kC * DV * 2, dO = 2 * kC * DV * 2, fac = 3 * kC * DV * 2,
-                         cols = fac + kGradFactors * kC * 4, step = cols + 6 * DV * 4;
+                         facs = (kFacC - kFacB) * kC * 4, cols = fac + facs, step = cols + 12 * DV * 4;
     static constexpr int S = 2 * step, dS = S + D * DV * 2, K = dS + D * DV * 2, Q = K + row_image<D>(),
-                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + (4 * kC + 8 * 32) * 4,
+                         tile = Q + row_image<D>(), vec = tile + 8 * 16 * 128, bar = vec + (6 * kC + 8 * 32) * 4,
                          bytes = bar + 64;
     static_assert(bytes <= 232448, "shared memory");
 };
 
-// Kept blocks (16 value columns x 16; `per` of them per slice, the last half of
-// those with factors of their own behind the first) times c[col] / m
-__device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int per, int half, int DV, const float* c,
+// Kept blocks (16 value columns x 16; `per` of them per slice, the factors of every
+// `group` of those behind one another) times c[col] / m
+__device__ __forceinline__ void one_scale(unsigned char* plane, int blocks, int per, int group, int DV, const float* c,
                                           float inv_m)
 {
     for (int u = threadIdx.x; u < blocks * 32; u += kDqkThreads) {
         const int block = u >> 5, col = block / per * 16 + ((u >> 3) & 1) * 8 + (u & 7);
-        const __half2 f = __float2half2_rn(c[col + (block % per >= half ? DV : 0)] * inv_m);
+        const __half2 f = __float2half2_rn(c[col + block % per / group * DV] * inv_m);
         uint4* at = reinterpret_cast<uint4*>(plane) + u;
         uint4 x = *at;
         __half2* h = reinterpret_cast<__half2*>(&x);
@@ -1909,8 +1955,11 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     float* eg = sdo + kC;                                   // e^G
     float* ege = eg + kC;                                   // e^{G_C - G}
     float* cd = ege + kC;                                   // decay from a token to its tile's end
-    float* prow = cd + kC + (warp >> 1) * 32;               // [half][16 rows], the two warps' own
+    float* ip = cd + kC;                                    // 1 / p
+    float* kp = ip + kC;                                    // fk / p
+    float* prow = kp + kC + (warp >> 1) * 32;               // [half][16 rows], the two warps' own
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bar);  // token planes (2), states, row images
+    float *mE = reinterpret_cast<float*>(full + 4), *mV = mE + 4;  // E's and dV's scales, of 16 tokens each
     const int per = H / Hk;
     const bool role_k = warp >= 8;
     const int pr = warp >> 1, h = warp & 1, rt = pr & 3, r0 = 16 * rt;
@@ -1944,16 +1993,16 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         const Step x = step_of(s);
         const uint32_t to = base + (s & 1) * SM::step;
         uint64_t* bar = full + (s & 1);
-        sm100::mbar_arrive_expect_tx(bar, 2 * kC * DV * 2 + x.n * DV * 2 + kGradFactors * kC * 4 + 6 * DV * 4);
+        sm100::mbar_arrive_expect_tx(bar, 2 * kC * DV * 2 + x.n * DV * 2 + SM::facs + 12 * DV * 4);
         delta::bulk_load(to + SM::E, kept.E + 2 * x.at * (kC * DV * 2), kC * DV * 2, bar);
         delta::bulk_load(to + SM::dV, kept.dV + x.at * (kC * DV * 2), kC * DV * 2, bar);
         delta::bulk_load(to + SM::dO, dout + (x.bh * N + x.t0) * DV, x.n * DV * 2, bar);
-        delta::bulk_load(to + SM::fac, blobs + x.at * (int64_t)blob_bytes<true>() + fac_at<true>(),
-                         kGradFactors * kC * 4, bar);
-        delta::bulk_load(to + SM::cols, kept.sE + x.at * DV, DV * 4, bar);
-        delta::bulk_load(to + SM::cols + DV * 4, kept.sV + x.at * DV, DV * 4, bar);
-        delta::bulk_load(to + SM::cols + 2 * DV * 4, kept.sS + (x.bh * (nchunk + 1) + x.c) * 2 * DV, 2 * DV * 4, bar);
-        delta::bulk_load(to + SM::cols + 4 * DV * 4, kept.sD + x.at * 2 * DV, 2 * DV * 4, bar);
+        delta::bulk_load(to + SM::fac, blobs + x.at * (int64_t)blob_bytes<true>() + fac_at<true>() + kFacB * kC * 4,
+                         SM::facs, bar);
+        delta::bulk_load(to + SM::cols, kept.sE + x.at * 4 * DV, 4 * DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 4 * DV * 4, kept.sV + x.at * 4 * DV, 4 * DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 8 * DV * 4, kept.sS + (x.bh * (nchunk + 1) + x.c) * 2 * DV, 2 * DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 10 * DV * 4, kept.sD + x.at * 2 * DV, 2 * DV * 4, bar);
     };
     auto load_states = [&](int s) {
         const Step x = step_of(s);
@@ -1976,24 +2025,23 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     float tot[NT][4];
     bool ok = true;
     for (int s = 0; s < steps; ++s) {
-        const Step me = step_of(s);
-        const int buf = (s & 1) * SM::step, p = s % per, n = me.n;
-        const int64_t t0 = me.t0, bh = me.bh;
+        const int buf = (s & 1) * SM::step, p = s % per;
         if (p == 0)
             clear(tot);
         if (tid == 0 && s + 1 < steps)
             load_tokens(s + 1);
         const int oE = buf + SM::E, odV = buf + SM::dV, odO = buf + SM::dO;
-        const float* fac = reinterpret_cast<const float*>(smem + buf + SM::fac);
-        const float *cE = reinterpret_cast<const float*>(smem + buf + SM::cols), *cV = cE + DV, *cS = cV + DV,
+        const float* fac = reinterpret_cast<const float*>(smem + buf + SM::fac) - kFacB * kC;
+        const float *cE = reinterpret_cast<const float*>(smem + buf + SM::cols), *cV = cE + 4 * DV, *cS = cV + 4 * DV,
                     *cD = cS + 2 * DV;
         const float *fB = fac + kFacB * kC, *fK = fac + kFacK * kC, *fQ = fac + kFacQ * kC, *gh = fac + kFacGh * kC,
                     *gl = fac + kFacGl * kC;
         ok = ok && wait_warp(full + (s & 1), (s >> 1) & 1);
-        float mE = 0.f, mV = 0.f, mS = 0.f, mD = 0.f;
+        float mS = 0.f, mD = 0.f;
         if (ok) {
             // dO to scaled fp16 rows in place, a row by the lanes of one warp
             constexpr int LPR = DV / 8, RPP = kDqkThreads / LPR;
+            const int n = step_of(s).n;
 #pragma unroll
             for (int b = 0; b < kC; b += RPP) {
                 const int r = b + tid / LPR, part = tid % LPR;
@@ -2025,11 +2073,16 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                 eg[tid] = exp2f(gh[tid] + gl[tid]);
                 ege[tid] = exp2f((gh[kC - 1] - gh[tid]) + (gl[kC - 1] - gl[tid]));
                 cd[tid] = exp2f((gh[tid | 15] - gh[tid]) + (gl[tid | 15] - gl[tid]));
+                ip[tid] = 1.0f / fac[kFacPk * kC + tid];
+                kp[tid] = fK[tid] / fac[kFacPk * kC + tid];
             }
-            mE = warp_max(cE, DV), mV = warp_max(cV, DV), mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
-            // 1 / m of a power of two is exact
-            one_scale(smem + oE, KS * 4, 4, 4, DV, cE, 1.0f / mE);
-            one_scale(smem + odV, KS * 4, 4, 4, DV, cV, 1.0f / mV);
+            mS = warp_max(cS, 2 * DV), mD = warp_max(cD, 2 * DV);
+            // 1 / m of a power of two is exact; the blocks of a warp are all of token tile warp % 4
+            const float xE = warp_max(cE + (warp & 3) * DV, DV), xV = warp_max(cV + (warp & 3) * DV, DV);
+            if (warp < 4 && lane == 0)
+                mE[warp] = xE, mV[warp] = xV;
+            one_scale(smem + oE, KS * 4, 4, 1, DV, cE, 1.0f / xE);
+            one_scale(smem + odV, KS * 4, 4, 1, DV, cV, 1.0f / xV);
         }
         ok = ok && wait_warp(full + 2, s & 1);
         if (ok) {
@@ -2149,8 +2202,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         if (!role_k) {
             state(odO, SM::S, eg[ia] * (sdo[ia] * mS), eg[ib] * (sdo[ib] * mS));
         } else {
-            state(odV, SM::S, -eg[ia] * (mV * mS), -eg[ib] * (mV * mS));
-            state(oE, SM::dS, ege[ia] * fB[ia] * (mE * mD), ege[ib] * fB[ib] * (mE * mD));
+            state(odV, SM::S, -eg[ia] * ip[ia] * (mV[rt] * mS), -eg[ib] * ip[ib] * (mV[rt] * mS));
+            state(oE, SM::dS, ege[ia] * fB[ia] * (mE[rt] * mD), ege[ib] * fB[ib] * (mE[rt] * mD));
         }
         sm100::fence_proxy_async_smem();
         __syncthreads();
@@ -2164,10 +2217,10 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         if (!role_k) {
             float x[4][4];
             dots(x, odO, oE, 0, rt);
-            const float fa = mE * sdo[ia], fb = mE * sdo[ib];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int tile = h + 2 * u;
+                const float fa = mE[tile] * sdo[ia], fb = mE[tile] * sdo[ib];
                 if (tile < rt) {  // a row's decay from the tile's end, a column's to it
                     const float da = fa * since(ia, tile), db = fb * since(ib, tile);
 #pragma unroll
@@ -2191,45 +2244,45 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             float x[4][4], y[4][4];
             {
                 float z[4][4];
-                const float fm = mE * mV;
                 dots(z, oE, odV, rt, 3);
                 dots(y, odV, oE, 0, rt);
                 dots(x, oE, odO, rt, 3);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int tile = h + 2 * u;
+                    // dV's rows are the warp's (y) or tile's (z), E's the other's
                     if (tile > rt) {  // i > j: the columns' decay from the rows' tile's end
-                        const float da = fB[ia] * cd[ia], db = fB[ib] * cd[ib];
+                        const float da = mE[rt] * fB[ia] * cd[ia], db = mE[rt] * fB[ib] * cd[ib], mv = -mV[tile];
 #pragma unroll
                         for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
                             const int i = 16 * tile + 8 * (nt & 1) + 2 * tq;
                             const float2 dec = make_float2(since(i, rt), since(i + 1, rt));
-                            const float2 fy = mul2(mul2(dec, pair2(fK, i)), both(-fm));
-                            const float2 fx = mul2(mul2(mul2(dec, pair2(fQ, i)), pair2(sdo, i)), both(mE * scale));
+                            const float2 fy = mul2(mul2(dec, pair2(kp, i)), both(mv));
                             set_rows(y[nt], mul2(mul2(row_a(z[nt]), both(da)), fy), mul2(mul2(row_b(z[nt]), both(db)), fy));
+                            const float2 fx = mul2(mul2(mul2(dec, pair2(fQ, i)), pair2(sdo, i)), both(scale));
                             set_rows(x[nt], mul2(mul2(row_a(x[nt]), both(da)), fx), mul2(mul2(row_b(x[nt]), both(db)), fx));
                         }
-                    } else if (tile < rt) {  // i < j: M alone
-                        const float da = -fm * since(ia, tile), db = -fm * since(ib, tile);
+                    } else if (tile < rt) {  // i < j: M alone, x is zero
+                        const float fm = -mE[tile] * mV[rt];
+                        const float da = fm * ip[ia] * since(ia, tile), db = fm * ip[ib] * since(ib, tile);
 #pragma unroll
                         for (int nt = 2 * u; nt < 2 * u + 2; ++nt) {
                             const int i = 16 * tile + 8 * (nt & 1) + 2 * tq;
                             const float2 f = mul2(mul2(pair2(fB, i), pair2(fK, i)), pair2(cd, i));
                             set_rows(y[nt], mul2(mul2(row_a(y[nt]), both(da)), f), mul2(mul2(row_b(y[nt]), both(db)), f));
-                            set_rows(x[nt], both(0.f), both(0.f));
                         }
                     } else {
+                        const float fm = mE[rt] * mV[rt], fx = mE[rt] * scale;
 #pragma unroll
                         for (int nt = 2 * u; nt < 2 * u + 2; ++nt)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int j = e >> 1 ? ib : ia, i = 16 * tile + 8 * (nt & 1) + 2 * tq + (e & 1);
                                 const float d = gap(i, j), dec = ex2(i >= j ? d : -d);
-                                y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * fK[i])
-                                           : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i])
+                                y[nt][e] = i > j   ? -z[nt][e] * fm * dec * (fB[j] * kp[i])
+                                           : i < j ? -y[nt][e] * fm * dec * (fB[i] * fK[i] * ip[j])
                                                    : 0.f;
-                                x[nt][e] =
-                                    i >= j ? x[nt][e] * (mE * sdo[i]) * dec * (fB[j] * (fQ[i] * scale)) : 0.f;
+                                x[nt][e] = i >= j ? x[nt][e] * (fx * sdo[i]) * dec * (fB[j] * fQ[i]) : 0.f;
                             }
                     }
                 }
@@ -2237,6 +2290,11 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
             rows_product(y, SM::K, 0, 3);
             rows_product(x, SM::Q, rt, 3);
         }
+        int again = s;  // the step's place is worked out anew, for registers
+        asm volatile("" : "+r"(again));
+        const Step me = step_of(again);
+        const int64_t t0 = me.t0, bh = me.bh;
+        const int n = me.n;
         // the gates' gradients from the dots over 16 columns each
         if (warp == 0) {
             float z[2], after = 0.f;
@@ -2434,11 +2492,11 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
     l.S = take(BH * (n + 1) * 2 * state);
     l.sS = take(BH * (n + 1) * 2 * a.dv * 4);
     l.E = take(BH * n * 2 * toks);
-    l.sE = take(BH * n * a.dv * 4);
+    l.sE = take(BH * n * 4 * a.dv * 4);
     l.dS = take(BH * n * state);
     l.sD = take(BH * n * 2 * a.dv * 4);
     l.dV = take(BH * n * toks);
-    l.sV = take(BH * n * a.dv * 4);
+    l.sV = take(BH * n * 4 * a.dv * 4);
     l.oo = take(BH * sl * (size_t)a.N * 4);
     l.vv = take(BH * sl * (size_t)a.N * 4);
     l.bb = take(BH * sl * (size_t)a.N * 4);

@@ -112,7 +112,7 @@ def beyond(p):
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("N", [17, 64, 100, 130])
-@pytest.mark.parametrize("writing", [2.2])
+@pytest.mark.parametrize("writing", [2.2, 2.5])
 def test_a_repeated_key_that_grows(N, writing, dtype):
     """One key everywhere: the state's row is multiplied by 1 - beta |k|^2 = -1.2 or -1.5 at each token,
     1e5 or 1e11 over a chunk."""
