@@ -386,13 +386,17 @@ __global__ void __launch_bounds__(kDecThreads)
 //   dQ = (dO U^T o D) K + diag(e^G) dO S0^T
 //   dK = (dO U^T o D)^T Q + M K + M^T K - diag(e^G) dV S0^T + diag(e^{G_C - G}) U dS1^T
 //        with M_ij = -D_ij dV_i.U_j (j < i)
-//   dlog_alpha_t = <S1, dS1> + sum_{i >= t in the chunk} (q_i.dQ_i - v_i.dV_i)
+//   dlog_alpha_t = sum_{i >= t > j} W_ij + sum_{i >= t} h_i + sum_{j < t} l_j + e^{G_C} <S0, dS1>
+//        with W_ij = D_ij (dO_i.U_j q_i.k_j - dV_i.U_j k_i.k_j), l_j = e^{G_C - G_j} k_j.(dS1 U_j)
+//        and h_i = e^{G_i} (q_i.(S0 dO_i) - k_i.(S0 dV_i))
 //
-// (the last line: every place where G_i enters is a factor of o_i's or of
-// e_i's right-hand side, and those products are q_i.dQ_i and v_i.dV_i).
+// (the last line: log_alpha_t enters every decay that spans t, and each term here has
+// such a decay as a factor.  It can be had from the rows' dots alone, as <S1, dS1> +
+// sum_{i >= t} (q_i.dQ_i - v_i.dV_i), but there the terms that do not span t cancel only
+// up to their rounding: of a gate of -8 half of the digits are left, of -16 none).
 // S0 and E come from the recurrence above, which stored them.  Two kernels: the
 // columns of dS, Y and dV never mix, so k_delta_grad_rev runs the chunks in reverse
-// for 32 columns per CTA and keeps dS1, dV and the dots over its columns (over
+// for 32 columns per CTA and keeps dS1, dV, Y.E and <S0, dS1> over its columns (over
 // segments like the recurrence: dS0 is affine in dS1, its matrix the transposed M);
 // k_delta_grad_dqk then takes every chunk on its own.  fp32 in shared memory, bound
 // by its reads: B2 H4 N201 d = 64 2 x 22 us and 24 us.
@@ -400,8 +404,7 @@ struct GradKept {
     float* dS;  // [BH][nblk][D][DV] gradient of the state after the chunk
     float* dV;  // [BH][N][DV]
     float* bb;  // [BH][DV / 32][N] Y.E over 32 columns
-    float* vv;  // [BH][DV / 32][N] v.dV
-    float* cd;  // [BH][DV / 32][nblk] <S1, dS1>
+    float* cd;  // [BH][DV / 32][nblk] <S0, dS1>
 };
 
 constexpr int kRevThreads = 256;
@@ -455,7 +458,7 @@ __device__ __forceinline__ void load_gates(double* G, float* eg, float* ege, con
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kRevThreads)
-    k_delta_grad_rev(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+    k_delta_grad_rev(const T* __restrict__ q, const T* __restrict__ k,
                      const float* __restrict__ beta, const float* __restrict__ log_alpha,
                      const T* __restrict__ dout, const float* __restrict__ dS_out,
                      const float* __restrict__ chk, const float* __restrict__ err, T* __restrict__ dv,
@@ -493,14 +496,14 @@ __global__ void __launch_bounds__(kRevThreads)
     for (int64_t b = (hi - 1) / C; b >= lo / C; --b) {
         const int64_t t0 = b * C;
         const int n = (int)min((int64_t)C, N - t0);
-        // dS1 out, <S1, dS1>
+        // dS1 out, <S0, dS1>
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < R && !ends; ++i) {
             const int64_t row = warp * R + i;
             kept.dS[((bh * nblk + b) * D + row) * DV + c0 + lane] = ds[i];
             if (log_alpha)
-                dot = fmaf(chk[((bh * (nblk + 1) + b + 1) * D + row) * DV + c0 + lane], ds[i], dot);
+                dot = fmaf(chk[((bh * (nblk + 1) + b) * D + row) * DV + c0 + lane], ds[i], dot);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(kRevThreads)
         // dV, the dots over the columns
 #pragma unroll
         for (int t = warp; t < C; t += 8) {
-            float y = sy[t * 32 + lane], db = 0.f, x = 0.f;
+            float y = sy[t * 32 + lane], db = 0.f;
             const float g = sb[t] * y;
             sy[t * 32 + lane] = g;
             if (t < n && !ends) {
@@ -604,17 +607,12 @@ __global__ void __launch_bounds__(kRevThreads)
                 dv[at] = from_f32<T>(g);
                 kept.dV[at] = g;
                 db = y * err[at];
-                x = g * to_f32<T>(v[at]);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
+            for (int o = 16; o > 0; o >>= 1)
                 db += __shfl_xor_sync(0xffffffffu, db, o);
-                x += __shfl_xor_sync(0xffffffffu, x, o);
-            }
-            if (lane == 0 && t < n && !ends) {
+            if (lane == 0 && t < n && !ends)
                 kept.bb[(bh * nsl + blockIdx.y) * N + t0 + t] = db;
-                kept.vv[(bh * nsl + blockIdx.y) * N + t0 + t] = x;
-            }
         }
         __syncthreads();
         // dS <- dS0
@@ -671,7 +669,7 @@ __global__ void __launch_bounds__(kGradThreads)
                      const float* __restrict__ log_alpha, const T* __restrict__ dout,
                      const float* __restrict__ chk, const float* __restrict__ err, GradKept kept,
                      float* __restrict__ dq, float* __restrict__ dk, float* __restrict__ dbeta,
-                     float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale, int zero_start)
+                     float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale)
 {
     using SM = GradSmem<D, DV>;
     constexpr int C = SM::C, LS = SM::LS, LK = SM::LK, LV = SM::LV, LC = SM::LC, CX = D / 16;
@@ -686,7 +684,8 @@ __global__ void __launch_bounds__(kGradThreads)
     float* Pt = P + C * LC;    // its transpose
     float* M = Pt + C * LC;    // [j][i] M_ij (i > j), M_ji (i < j): the matrix on K for dK
     __shared__ double G[C];
-    __shared__ float eg[C], ege[C], sb[C], dG[C];
+    // span: sum of W_ij over i >= t > j for four rows i; dH: h; dL: l
+    __shared__ float eg[C], ege[C], sb[C], span[kGradThreads / 32][C], dH[C], dL[C];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ty = tid >> 4, tx = tid & 15;
     const int64_t nblk = (N + C - 1) / C;
@@ -712,7 +711,7 @@ __global__ void __launch_bounds__(kGradThreads)
     __syncthreads();
     // dO_i.U_j and dV_i.U_j: 4 rows (warp) x a column (lane) per thread
     {
-        float p[4] = {}, m[4] = {};
+        float p[4] = {}, m[4] = {}, qk[4] = {}, kk[4] = {}, w = 0.f;
         for (int x = 0; x < DV; x += 4) {
             const float4 u = *reinterpret_cast<const float4*>(su + lane * LV + x);
 #pragma unroll
@@ -721,6 +720,16 @@ __global__ void __launch_bounds__(kGradThreads)
                 const float4 g = *reinterpret_cast<const float4*>(sg + (4 * warp + r) * LV + x);
                 p[r] = fmaf(o.x, u.x, fmaf(o.y, u.y, fmaf(o.z, u.z, fmaf(o.w, u.w, p[r]))));
                 m[r] = fmaf(g.x, u.x, fmaf(g.y, u.y, fmaf(g.z, u.z, fmaf(g.w, u.w, m[r]))));
+            }
+        }
+        for (int x = 0; dlog_alpha && x < D; x += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(sk + lane * LK + x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 a = *reinterpret_cast<const float4*>(sq + (4 * warp + r) * LK + x);
+                const float4 b = *reinterpret_cast<const float4*>(sk + (4 * warp + r) * LK + x);
+                qk[r] = fmaf(a.x, y.x, fmaf(a.y, y.y, fmaf(a.z, y.z, fmaf(a.w, y.w, qk[r]))));
+                kk[r] = fmaf(b.x, y.x, fmaf(b.y, y.y, fmaf(b.z, y.z, fmaf(b.w, y.w, kk[r]))));
             }
         }
 #pragma unroll
@@ -734,7 +743,18 @@ __global__ void __launch_bounds__(kGradThreads)
                 M[i * LC + j] = M[j * LC + i] = -m[r] * dec;
             else if (j == i)
                 M[i * LC + i] = 0.f;
+            // sum over j < t = lane, of the rows i >= t
+            float z = j < i ? dec * fmaf(p[r], qk[r], -m[r] * kk[r]) : 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, z, o);
+                if (lane >= o)
+                    z += y;
+            }
+            z = __shfl_up_sync(0xffffffffu, z, 1);
+            w += lane > 0 && lane <= i ? z : 0.f;
         }
+        span[warp][lane] = w;
     }
     __syncthreads();
     // x[row][column] += a[row][0 .. C) b[0 .. C)[column], rows 2 ty, 2 ty + 1
@@ -780,56 +800,77 @@ __global__ void __launch_bounds__(kGradThreads)
                 dst[(bh * N + t0 + i1) * D + tx + 16 * i] = x[1][i];
         }
     };
-    {  // dQ, q.dQ
-        float x[2][CX] = {}, d0 = 0.f, d1 = 0.f;
-        tokens(x, P, sk);
-        states(x, sdo, eg[i0], eg[i1]);
+    // row i0's and i1's dots of x with a, by the threads of lane 0
+    auto row_dots = [&](const float (&x)[2][CX], const float* a, float& d0, float& d1) {
+        d0 = d1 = 0.f;
 #pragma unroll
         for (int i = 0; i < CX; ++i) {
-            d0 = fmaf(x[0][i], sq[i0 * LK + tx + 16 * i], d0);
-            d1 = fmaf(x[1][i], sq[i1 * LK + tx + 16 * i], d1);
+            d0 = fmaf(x[0][i], a[i0 * LK + tx + 16 * i], d0);
+            d1 = fmaf(x[1][i], a[i1 * LK + tx + 16 * i], d1);
         }
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) {
             d0 += __shfl_xor_sync(0xffffffffu, d0, o);
             d1 += __shfl_xor_sync(0xffffffffu, d1, o);
         }
-        if (tx == 0)
-            dG[i0] = d0, dG[i1] = d1;
+    };
+    float h0, h1, d0, d1;
+    {  // dQ
+        float x[2][CX] = {};
+        states(x, sdo, eg[i0], eg[i1]);
+        row_dots(x, sq, h0, h1);
+        tokens(x, P, sk);
         put(dq, x);
     }
     float x[2][CX] = {};
+    states(x, sg, -eg[i0], -eg[i1]);
+    row_dots(x, sk, d0, d1);
+    if (tx == 0)
+        dH[i0] = h0 + d0, dH[i1] = h1 + d1;
     tokens(x, Pt, sq);
     tokens(x, M, sk);
-    states(x, sg, -eg[i0], -eg[i1]);
     __syncthreads();  // S0 is read
     for (int i = tid; i < D * DV; i += kGradThreads)
         S[i / DV * LS + i % DV] = kept.dS[(bh * nblk + b) * (int64_t)(D * DV) + i];
+    __syncthreads();
+    {
+        float y[2][CX] = {};
+        states(y, su, ege[i0], ege[i1]);
+        row_dots(y, sk, d0, d1);
+        if (tx == 0)
+            dL[i0] = d0, dL[i1] = d1;
+#pragma unroll
+        for (int i = 0; i < CX; ++i)
+            x[0][i] += y[0][i], x[1][i] += y[1][i];
+    }
+    put(dk, x);
+    __syncthreads();
     if (warp == 0) {  // the gates' gradients
         const int nsl = DV / 32;
-        float y = lane < n ? dG[lane] : 0.f, db = 0.f, after = 0.f;
+        float y = dH[lane], z = dL[lane], db = 0.f, w = 0.f, after = 0.f;
         for (int s = 0; s < nsl; ++s) {
-            if (lane < n) {
+            if (lane < n)
                 db += kept.bb[(bh * nsl + s) * N + t0 + lane];
-                y -= kept.vv[(bh * nsl + s) * N + t0 + lane];
-            }
             after += kept.cd[(bh * nsl + s) * nblk + b];
         }
 #pragma unroll
+        for (int i = 0; i < kGradThreads / 32; ++i)
+            w += span[i][lane];
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float z = __shfl_down_sync(0xffffffffu, y, o);
+            const float a = __shfl_down_sync(0xffffffffu, y, o), c = __shfl_up_sync(0xffffffffu, z, o);
             if (lane + o < 32)
-                y += z;
+                y += a;
+            if (lane >= o)
+                z += c;
         }
+        z = __shfl_up_sync(0xffffffffu, z, 1);
         if (lane < n) {
             dbeta[bh * N + t0 + lane] = db;
-            if (dlog_alpha)  // a first gate on a zero state has no gradient, the sums leave their rounding
-                dlog_alpha[bh * N + t0 + lane] = zero_start && t0 + lane == 0 ? 0.f : y + after;
+            if (dlog_alpha)
+                dlog_alpha[bh * N + t0 + lane] = w + y + (lane > 0 ? z : 0.f) + eg[C - 1] * after;
         }
     }
-    __syncthreads();
-    states(x, su, ege[i0], ege[i1]);
-    put(dk, x);
 }
 
 // Gradients of the key heads' rows from those of the value heads that read
@@ -987,7 +1028,7 @@ cudaError_t run_decode(const DeltaArgs& a)
 }
 
 struct GradLayout {
-    size_t chk, err, dq, dk, dS, dV, bb, vv, cd, seg, total;
+    size_t chk, err, dq, dk, dS, dV, bb, cd, seg, total;
 };
 GradLayout grad_layout(const DeltaArgs& a)
 {
@@ -1006,7 +1047,6 @@ GradLayout grad_layout(const DeltaArgs& a)
     l.dS = take(BH * nb * a.d * a.dv);
     l.dV = take(BH * N * a.dv);
     l.bb = take(BH * sl * N);
-    l.vv = take(BH * sl * N);
     l.cd = take(BH * sl * nb);
     l.seg = at;
     l.total = at + rec_layout(a).total;
@@ -1019,7 +1059,7 @@ cudaError_t run_grad(const DeltaArgs& a)
     const GradLayout l = grad_layout(a);
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    const GradKept kept = {f32(l.dS), f32(l.dV), f32(l.bb), f32(l.vv), f32(l.cd)};
+    const GradKept kept = {f32(l.dS), f32(l.dV), f32(l.bb), f32(l.cd)};
     DeltaArgs f = a;
     f.out = nullptr, f.S_out = nullptr;
     cudaError_t e = run_rec<D, T>(f, f32(l.chk), f32(l.err), ws + l.seg);
@@ -1040,7 +1080,7 @@ cudaError_t run_grad(const DeltaArgs& a)
     const int n = rec_segments(a, &seg.len);
     auto reverse = [&](const Segments& x) {
         k_delta_grad_rev<D, T><<<dim3((unsigned)(BH * x.count), DV / 32), kRevThreads, rev, a.stream>>>(
-            q, k, static_cast<const T*>(a.v), a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
+            q, k, a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
             static_cast<T*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale, x);
         count_launches(1);
         return cudaGetLastError();
@@ -1059,7 +1099,7 @@ cudaError_t run_grad(const DeltaArgs& a)
         return e;
     k_delta_grad_dqk<D, DV, T><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
         q, k, a.beta, a.log_alpha, dout, f32(l.chk), f32(l.err), kept, f32(l.dq), f32(l.dk), a.dbeta,
-        a.dlog_alpha, a.N, H, Hk, l2, a.scale, !a.S0);
+        a.dlog_alpha, a.N, H, Hk, l2, a.scale);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess)
