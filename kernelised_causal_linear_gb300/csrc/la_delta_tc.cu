@@ -28,7 +28,7 @@
 //
 // The gradient: k_delta_prep, the chain again keeping the states before the chunks
 // and E (k_delta_chain<GRAD>), k_delta_rev for the chunks in reverse, k_delta_dqk for
-// dQ and dK of every chunk on its own.
+// dQ and dK of every chunk on its own, k_delta_gates for dbeta and dlog_alpha.
 //
 // Why warp-level MMAs and not tcgen05: the chain is a string of small dependent
 // products (64 tokens x 16 columns x d), whose operands are the fp32 results of the
@@ -625,8 +625,9 @@ constexpr int kXch = 2048;  // bytes of one warp's exchange buffer: 16 floats pe
 
 template <int D, bool GRAD, int SP>
 struct ChainSmem {
-    static constexpr int stages = SP == 1 && !GRAD ? 3 : 2;  // what fits at d = 128
-    static constexpr int stage = 2 * row_image<D>() + blob_bytes<GRAD>();
+    static constexpr int stages = SP == 1 ? 3 : 2;  // what fits at d = 128
+    // [K][Q][F hi][F lo][P, for outputs][factors]
+    static constexpr int fac = 2 * row_image<D>() + (GRAD ? 2 : 3) * kTile, stage = fac + kFactors * kC * 4;
     static constexpr int v = stages * stage;
     // per slice: V twice, O (GRAD: dO), and for each of two warps four exchange buffers
     static constexpr int x = 3 * kC * 32, per_slice = x + (SP > 1 ? SP * 4 * kXch : 0);
@@ -640,18 +641,22 @@ struct ChainSmem {
 // 1 / p as beta goes with the square of that).  An 8 x 8 block is 128 bytes with its rows in
 // order, so k_delta_dqk reads it with ldmatrix whichever way round it needs it.
 struct Kept {
-    unsigned char* S;   // [BH][nchunk + 1][2 parts][D DV] fp16
-    float* sS;          // [BH][nchunk + 1][2][DV]
+    unsigned char* S;   // [BH][nchunk][2 parts][D DV] fp16
+    float* sS;          // [BH][nchunk][2][DV]
     unsigned char* E;   // [BH][nchunk][2 parts][64 DV] fp16
     float* sE;          // [BH][nchunk][4][DV]
     unsigned char* dS;  // [BH][nchunk][D DV] fp16: gradient of the state after the chunk
     float* sD;          // [BH][nchunk][2][DV]
     unsigned char* dV;  // [BH][nchunk][64 DV] fp16
     float* sV;          // [BH][nchunk][4][DV]
-    float* oo;          // [BH][DV / 16][N] dO.O over 16 columns
-    float* vv;          // [BH][DV / 16][N] v.dV
-    float* bb;          // [BH][DV / 16][N] Y.E
-    float* cd;          // [BH][DV / 16][2][nchunk] <S1, dS1> over half of the rows
+    float* bb;          // [BH][DV / 16][N] Y.E over 16 columns
+    // with gates only
+    unsigned char* dVl;  // [BH][nchunk][64 DV] the other part of dV
+    float4* KS;          // [BH][nchunk][DV / 16][8][32] S0^T K16, C tiles of 8 tokens
+    float* hq;           // [BH][DV / 16][N] e^{G_i} q_i.(S0 dO_i) over 16 columns
+    float* hk;           // [BH][DV / 16][N] -e^{G_i} k_i.(S0 dV_i)
+    float* ll;           // [BH][DV / 16][N] e^{G_C - G_j} k_j.(dS1 U_j)
+    float* cd;           // [BH][DV / 16][2][nchunk] <S0, dS1> over half of the rows
 };
 
 // One fragment's registers of plane `plane` (part_bytes each part, block = 16 x 16)
@@ -861,7 +866,7 @@ struct Segments {
 };
 
 // READS: outputs are wanted (a branch on the pointer instead cuts every stretch of
-// products in two)
+// products in two); in a gradient, S0^T K and the dots of S0^T Q with dO for the gates'
 template <int D, bool GRAD, int SP, bool READS>
 __global__ void __launch_bounds__(256, 1)
     k_delta_chain(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
@@ -899,15 +904,16 @@ __global__ void __launch_bounds__(256, 1)
         const uint32_t dst = base + (i % SM::stages) * SM::stage;
         uint64_t* bar = ring.full + i % SM::stages;
         const unsigned char *r = row_src + c * (2 * row_image<D>()), *f = blob_src + c * seg.blob;
-        if (READS) {
+        if (READS && !GRAD) {
             sm100::mbar_arrive_expect_tx(bar, SM::stage);
             delta::bulk_load(dst, r, 2 * row_image<D>(), bar);
-            delta::bulk_load(dst + 2 * row_image<D>(), f, blob_bytes<GRAD>(), bar);
-        } else {  // neither Q nor P
-            sm100::mbar_arrive_expect_tx(bar, row_image<D>() + 2 * kTile + kFactors * kC * 4);
-            delta::bulk_load(dst, r, row_image<D>(), bar);
+            delta::bulk_load(dst + 2 * row_image<D>(), f, blob_bytes<false>(), bar);
+        } else {  // no P, and Q where it is wanted
+            constexpr int img = (READS ? 2 : 1) * row_image<D>();
+            sm100::mbar_arrive_expect_tx(bar, img + 2 * kTile + kFactors * kC * 4);
+            delta::bulk_load(dst, r, img, bar);
             delta::bulk_load(dst + 2 * row_image<D>(), f, 2 * kTile, bar);
-            delta::bulk_load(dst + 2 * row_image<D>() + fac_at<GRAD>(), f + seg.fac, kFactors * kC * 4, bar);
+            delta::bulk_load(dst + SM::fac, f + seg.fac, kFactors * kC * 4, bar);
         }
     };
     // this warp's token tiles of the slice's columns
@@ -953,7 +959,7 @@ __global__ void __launch_bounds__(256, 1)
     };
     auto keep_state_scale = [&](int64_t c, Pow2 p0, Pow2 p1) {
         if (tq == 0) {
-            float* ss = kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0;
+            float* ss = kept.sS + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
             ss[g] = p0.from, ss[g + 8] = p1.from;
             if (SP == 1)
                 ss[DV + g] = p0.from, ss[DV + g + 8] = p1.from;
@@ -965,9 +971,8 @@ __global__ void __launch_bounds__(256, 1)
         const int c = lo + step;
         const uint32_t st = base + (step % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
-        const float* fac = reinterpret_cast<const float*>(smem + (step % SM::stages) * SM::stage +
-                                                          2 * row_image<D>() + fac_at<GRAD>());
-        if (GRAD) {  // dO, wanted at the end of the chunk
+        const float* fac = reinterpret_cast<const float*>(smem + (step % SM::stages) * SM::stage + SM::fac);
+        if (GRAD && READS) {  // dO, wanted after E
             load_cols(so, dout, c);
             cp_commit();
         }
@@ -985,9 +990,13 @@ __global__ void __launch_bounds__(256, 1)
         for (int kk = 0; kk < KK; ++kk) {
             uint32_t hi[4], lo[4];
             split_state(kk, p0, p1, hi, lo);
-            if (GRAD)
-                keep_parts(kept.S, bh * (nchunk + 1) + c, D * DV * 2,
-                           (col0 / 16) * (D / 16) + d0 / 16 + kk, lane, hi, lo);
+            if (GRAD) {
+                const int block = (col0 / 16) * (D / 16) + d0 / 16 + kk;
+                keep_part(kept.S, 2 * (bh * nchunk + c), D * DV * 2, block, lane, hi);
+                // the second part is read by k_delta_rev alone, fragment by fragment
+                reinterpret_cast<uint4*>(kept.S + (2 * (bh * nchunk + c) + 1) * (int64_t)(D * DV * 2))[block * 32 + lane] =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
                 uint32_t bk[2][4], bq[2][4];
@@ -1003,7 +1012,7 @@ __global__ void __launch_bounds__(256, 1)
                 if (READS)
                     mma_tiles<2>(o + 2 * j, hi, bq);
                 mma_tiles<2>(r + 2 * j, lo, bk);
-                if (GRAD)  // o enters an fp32 gradient
+                if (GRAD && READS)  // o enters an fp32 gradient
                     mma_tiles<2>(o + 2 * j, lo, bq);
             }
         }
@@ -1027,7 +1036,13 @@ __global__ void __launch_bounds__(256, 1)
             if (READS)
                 sh.template get<true>(1, pair(o, 0), pair(o, 1));
         }
-        cp_wait<GRAD ? 2 : 1>();  // V
+        if (GRAD && READS) {
+#pragma unroll
+            for (int nt = 0; nt < 2 * OWN; ++nt)
+                kept.KS[(((bh * nchunk + c) * (DV / 16) + col0 / 16) * 8 + 2 * sh.tile(nt >> 1) + (nt & 1)) * 32 + lane] =
+                    make_float4(r[nt][0], r[nt][1], r[nt][2], r[nt][3]);
+        }
+        cp_wait<GRAD && READS ? 2 : 1>();  // V
         __syncwarp();
         // R of the own tiles, z = beta p c R
         float z[8][4];
@@ -1097,9 +1112,7 @@ __global__ void __launch_bounds__(256, 1)
             sh.sync();
             sh.template get<false>(3, pair(r, 2), pair(r, 3));
         }
-        // r is E; its largest is wanted for O
-        max8(r);
-        if (GRAD) {
+        if (GRAD) {  // r is E
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 const Pow2 q0 = tile_scale(r, i, 0), q1 = tile_scale(r, i, 2);
@@ -1112,88 +1125,70 @@ __global__ void __launch_bounds__(256, 1)
                 }
             }
         }
-        // U = beta E, and the largest of the state update's factor times it
-        float w0 = 0.f, w1 = 0.f;
-        auto to_u = [&]() {
+        if (GRAD && READS) {  // dO.(e^G scale S0^T q)
+            cp_wait<1>();
+            __syncwarp();
+            float dots[OWN / 2][8];
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
-                const float2 w = fac2(fac, kFacW, sh.tile(nt >> 1), nt & 1, tq);
-                scale_cols(r[nt], be);
-                const float2 a = mul2(w, row_a(r[nt])), b = mul2(w, row_b(r[nt]));
-                w0 = max_abs(max_abs(w0, a.x), a.y);
-                w1 = max_abs(max_abs(w1, b.x), b.y);
-                if (!GRAD)
-                    set_rows(r[nt], a, b);  // W U, all that is wanted from here on
+            for (int i = 0; i < OWN; ++i) {
+                uint32_t w[4];
+                ldsm4t(w, addr_ct<32>(so, lane, 16 * sh.tile(i), 0));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int nt = 2 * i + u;
+                    dots[nt >> 2][2 * (nt & 3)] = o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]);
+                    dots[nt >> 2][2 * (nt & 3) + 1] = o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]);
+                }
             }
-        };
-        if (GRAD) {
-            to_u();
-            max8(r);
+#pragma unroll
+            for (int part = 0; part < OWN / 2; ++part)
+                sh.store_sums(kept.hq + (bh * (DV / 16) + col0 / 16) * N, dots[part], part, (int64_t)c * kC, N);
         }
         // O = inter + (P beta) E: with beta in P, a token that writes nothing does not
-        // set the scale of its row.  For the output alone one fp16 part of each is
-        // enough (2^-12 of a term, under the output's own rounding); a gradient
-        // takes both, and P without beta and U for E, since it needs P itself
-        if (READS) {
+        // set the scale of its row.  One fp16 part of each is enough (2^-12 of a term,
+        // under the output's own rounding)
+        if (READS && !GRAD) {
+            max8(r);
             const Pow2 q0 = pow2_for(e0), q1 = pow2_for(e1);
             clear(x);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 uint32_t hi[4], lo[4], b[4];
                 split8(r, kk, q0, q1, hi, lo);
-                if (GRAD) {
-                    three_products<OWN>(
-                        x, hi, lo, [&](int i) { return sh.tile(kk) <= sh.tile(i); },
-                        [&](uint32_t(&b)[4], int i, int part) {
-                            ldsm4(b, addr_b<128>(sP + part * kTile, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
-                        });
-                } else {
 #pragma unroll
-                    for (int i = 0; i < OWN; ++i) {
-                        if (sh.tile(kk) <= sh.tile(i)) {
-                            ldsm4(b, addr_b<128>(sP, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
-                            mma(x[2 * i], hi, b[0], b[1]);
-                            mma(x[2 * i + 1], hi, b[2], b[3]);
-                        }
+                for (int i = 0; i < OWN; ++i) {
+                    if (sh.tile(kk) <= sh.tile(i)) {
+                        ldsm4(b, addr_b<128>(sP, lane, 16 * sh.tile(i), 16 * sh.tile(kk)));
+                        mma(x[2 * i], hi, b[0], b[1]);
+                        mma(x[2 * i + 1], hi, b[2], b[3]);
                     }
                 }
             }
-            if (GRAD) {
-                cp_wait<1>();  // dO
-                __syncwarp();
-            }
-            float dots[OWN / 2][8];
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 uint32_t w[4];
-                if (GRAD)
-                    ldsm4t(w, addr_ct<32>(so, lane, 16 * sh.tile(i), 0));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int nt = 2 * i + u;
                     const float2 fp = fac2(fac, kFacP, sh.tile(i), u, tq);
                     set_rows(o[nt], fma2(mul2(fp, both(q0.from)), row_a(x[nt]), row_a(o[nt])),
                              fma2(mul2(fp, both(q1.from)), row_b(x[nt]), row_b(o[nt])));
-                    if (GRAD) {
-                        dots[nt >> 2][2 * (nt & 3)] = o[nt][0] * lo_f(w[2 * u]) + o[nt][2] * lo_f(w[2 * u + 1]);
-                        dots[nt >> 2][2 * (nt & 3) + 1] = o[nt][1] * hi_f(w[2 * u]) + o[nt][3] * hi_f(w[2 * u + 1]);
-                    } else {
-                        w[2 * u] = sm100::pack_bf16x2(o[nt][0], o[nt][1]);
-                        w[2 * u + 1] = sm100::pack_bf16x2(o[nt][2], o[nt][3]);
-                    }
+                    w[2 * u] = sm100::pack_bf16x2(o[nt][0], o[nt][1]);
+                    w[2 * u + 1] = sm100::pack_bf16x2(o[nt][2], o[nt][3]);
                 }
-                if (!GRAD)
-                    stsm4t(addr_ct<32>(so, lane, 16 * sh.tile(i), 0), w);
-            }
-            if (GRAD) {
-#pragma unroll
-                for (int part = 0; part < OWN / 2; ++part)
-                    sh.store_sums(kept.oo + (bh * (DV / 16) + col0 / 16) * N, dots[part], part, (int64_t)c * kC, N);
+                stsm4t(addr_ct<32>(so, lane, 16 * sh.tile(i), 0), w);
             }
         }
-        if (!GRAD)
-            to_u();
+        // W U, U = beta E: the state update's operand, and its largest
+        float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const float2 w = fac2(fac, kFacW, sh.tile(nt >> 1), nt & 1, tq);
+            scale_cols(r[nt], fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq));
+            scale_cols(r[nt], w);
+            w0 = max_abs(max_abs(w0, r[nt][0]), r[nt][1]);
+            w1 = max_abs(max_abs(w1, r[nt][2]), r[nt][3]);
+        }
         // S1 = e^{G_C} S0 + (W U)^T K16 on accumulators scaled with the operand: both
         // under one power of two, so neither overflows nor loses bits the other does
         // not drown
@@ -1210,8 +1205,6 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int nt = 2 * kk + u;
-                if (GRAD)
-                    scale_cols(r[nt], fac2(fac, kFacW, sh.tile(kk), u, tq));
                 h2_split(row_a(r[nt]), u0.to, hi[2 * u], lo[2 * u]);
                 h2_split(row_b(r[nt]), u1.to, hi[2 * u + 1], lo[2 * u + 1]);
             }
@@ -1242,19 +1235,6 @@ __global__ void __launch_bounds__(256, 1)
     if (!ring.ok && lane == 0) {  // a copy did not arrive in time: the results are void
         ring.drain();
         set_status(status, LA_ERR_TIMEOUT);
-    }
-    if (GRAD && lo + len == nchunk) {  // the final state, for <S1, dS1> of the last chunk
-        float m0, m1;
-        row_max(m0, m1);
-        const Pow2 p0 = pow2_for(m0), p1 = pow2_for(m1);
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            uint32_t hi[4], lo[4];
-            split_state(kk, p0, p1, hi, lo);
-            keep_parts(kept.S, bh * (nchunk + 1) + nchunk, D * DV * 2, (col0 / 16) * (D / 16) + d0 / 16 + kk, lane,
-                       hi, lo);
-        }
-        keep_state_scale(nchunk, p0, p1);
     }
     float* end = nullptr;
     int ld = DV;
@@ -1413,8 +1393,8 @@ __global__ void __launch_bounds__(256)
 //   Y  = dU + F^T z,  dV = beta Y          ((I + diag(beta) A)^{-T} = I + F^T beta)
 //   dS0 = e^{G_C} dS1 + (diag(e^G) Q)^T dO - (diag(e^G) K)^T dV
 //
-// and the dot products that need both directions' fp32 values: v.dV, Y.E, and
-// <S0, dS0> (which is <S1, dS1> of the chunk before).
+// and the dot products that need both directions' fp32 values: Y.E, and for the gates
+// k.(S0 dV), k.(dS1 U) and <S0, dS1>.
 //
 // Over segments as in k_delta_chain: dS0 is affine in dS1, and its matrix over a
 // segment is the transpose of the M that the states' run gave.  ENDS: a run from
@@ -1427,8 +1407,8 @@ struct RevSmem {
     static constexpr int stages = 2;
     static constexpr int stage = 2 * row_image<D>() + blob_bytes<true>();
     static constexpr int slice0 = stages * stage;
-    // per slice: dO twice, V (then dV), E hi and lo, three exchange buffers for each
-    // of two warps
+    // per slice: dO twice, dV on its way out, E hi and lo, three exchange buffers for
+    // each of two warps
     static constexpr int dO = 0, v = 2 * kC * 32, e = v + kC * 32, x = e + 2 * kC * 32,
                          per_slice = x + (SP > 1 ? SP * 3 * kXch : 0);
     static int bytes(int W) { return slice0 + W * per_slice + 128; }
@@ -1437,7 +1417,7 @@ struct RevSmem {
 template <int D, int SP, bool GATED, bool ENDS>
 __global__ void __launch_bounds__(256, 1)
     k_delta_rev(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
-                const __nv_bfloat16* __restrict__ v, const __nv_bfloat16* __restrict__ dout,
+                const __nv_bfloat16* __restrict__ dout,
                 const float* __restrict__ dS_out, __nv_bfloat16* __restrict__ dv,
                 float* __restrict__ dS0, int64_t N, int nchunk, int H, int Hk, int DV, Kept kept,
                 Segments seg, int* status)
@@ -1494,29 +1474,30 @@ __global__ void __launch_bounds__(256, 1)
                      true);
     };
     float ds[NT][4];  // dS^T[col0 + g, + 8][d0 + 8 nt + 2 tq, + 1]
-    // <S of chunk c, dS> over the warp's part -> kept.cd of the chunk before.  S is
-    // read where it lies (128 bytes per load; asked into L2 at the chunk's start):
-    // staging it took the shared memory of half of the slices
+    // <S0, dS> of chunk c over the warp's part -> kept.cd.  S0 is read where it lies
+    // (128 bytes per load; asked into L2 a chunk ahead): staging it took the shared memory
+    // of half of the slices
     auto state_at = [&](int64_t c, int part) {
-        return kept.S + (2 * (bh * (nchunk + 1) + c) + part) * (int64_t)(D * DV * 2) +
-               (slice * (D / 16) + d0 / 16) * 512;
+        return kept.S + (2 * (bh * nchunk + c) + part) * (int64_t)(D * DV * 2) + (slice * (D / 16) + d0 / 16) * 512;
     };
     auto ask_state = [&](int64_t c) {
 #pragma unroll
         for (int i = lane; i < 2 * KK * 4; i += 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(state_at(c, i / (KK * 4)) + i % (KK * 4) * 128));
     };
-    auto dot_state = [&](int64_t c, float sc0, float sc1) {
+    auto dot_state = [&](int64_t c, float sc0, float sc1, bool keep) {
         const uint32_t* part0 = reinterpret_cast<const uint32_t*>(state_at(c, 0)) + lane;
-        const uint32_t* part1 = reinterpret_cast<const uint32_t*>(state_at(c, 1)) + lane;
+        const uint4* part1 = reinterpret_cast<const uint4*>(state_at(c, 1)) + lane;
         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
+            const uint4 z = __ldg(part1 + kk * 32);
+            const uint32_t y[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // register i: row g + 8 (i & 1), tile 2 kk + (i >> 1)
-                const uint32_t x = __ldg(part0 + (kk * 4 + i) * 32), y = __ldg(part1 + (kk * 4 + i) * 32);
+                const uint32_t x = __ldg(part0 + (kk * 4 + i) * 32);
                 const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&x));
-                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&y));
+                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
                 const float* d = ds[2 * kk + (i >> 1)] + 2 * (i & 1);
                 float& a = i & 1 ? a1 : a0;
                 a = fmaf(h.x + l.x, d[0], fmaf(h.y + l.y, d[1], a));
@@ -1526,15 +1507,44 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0 && c > lo) {  // the segment before sees to its own end
-            float* cd = kept.cd + (bh * (DV / 16) + slice) * 2 * nchunk + c - 1;
+        if (lane == 0 && keep) {
+            float* cd = kept.cd + (bh * (DV / 16) + slice) * 2 * nchunk + c;
             cd[sh.half * nchunk] = x;
             if (SP == 1)
                 cd[nchunk] = 0.f;
         }
     };
-    auto state_scale = [&](int64_t c, int row) {
-        return __ldg(kept.sS + ((bh * (nchunk + 1) + c) * 2 + sh.half) * DV + col0 + row);
+    // E and S0^T K16 of the own token tiles, a chunk ahead
+    auto ask_tokens = [&](int64_t c) {
+#pragma unroll
+        for (int i = lane; i < OWN * 16; i += 32) {
+            const int tile = sh.tile(i / 16), line = i % 16;  // 4 + 4 lines of E's parts, 8 of KS
+            const unsigned char* e = kept.E + (2 * (bh * nchunk + c) + (line >> 2 & 1)) * (int64_t)(kC * DV * 2) +
+                                     (slice * 4 + tile) * 512 + (line & 3) * 128;
+            const unsigned char* ks = reinterpret_cast<const unsigned char*>(
+                kept.KS + (((bh * nchunk + c) * (DV / 16) + slice) * 8 + 2 * tile) * 32) + (line & 7) * 128;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(line < 8 ? e : ks));
+        }
+    };
+    // the scales of the kept state and of E; E's a chunk ahead where a warp is alone on its
+    // sub-partition
+    float sc[2] = {}, se[OWN][2] = {};
+    auto read_S_scales = [&](int64_t c) {
+        const float* at = kept.sS + ((bh * nchunk + c) * 2 + sh.half) * DV + col0;
+        sc[0] = __ldg(at + g), sc[1] = __ldg(at + g + 8);
+    };
+    auto read_E_scales = [&](int64_t c, float (&x)[OWN][2]) {
+        if (ENDS)
+            return;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const float* at = kept.sE + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
+            x[i][0] = __ldg(at + g), x[i][1] = __ldg(at + g + 8);
+        }
+    };
+    // S0^T K16 of the own C tile nt, as k_delta_chain left it
+    auto read_KS = [&](int64_t c, int nt) {
+        return __ldg(kept.KS + (((bh * nchunk + c) * (DV / 16) + slice) * 8 + 2 * sh.tile(nt >> 1) + (nt & 1)) * 32 + lane);
     };
 
     if (tid == 0)
@@ -1548,8 +1558,12 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             ds[nt][e] = end ? end[(d0 + 8 * nt + 2 * tq + (e & 1)) * DV + col0 + g + (e >> 1) * 8] : 0.f;
-    if (GATED)
-        dot_state(lo + len, state_scale(lo + len, g), state_scale(lo + len, g + 8));
+    if (SP > 1)
+        read_E_scales(lo + len - 1, se);
+    if (GATED) {
+        read_S_scales(lo + len - 1);
+        dot_state(lo + len - 1, sc[0], sc[1], true);
+    }
     cp_wait<0>();
     sh.sync();
     ring.wait(0);
@@ -1560,28 +1574,25 @@ __global__ void __launch_bounds__(256, 1)
         const float* fac = reinterpret_cast<const float*>(smem + (it % SM::stages) * SM::stage +
                                                           2 * row_image<D>() + fac_at<true>());
         const uint32_t tdo = sdo + (c & 1) * kC * 32;
-        // this chunk's V, E and S, wanted from the middle on; the next dO, each warp its
+        // this chunk's E and S, wanted from the middle on; the next dO, each warp its
         // token tiles, which both await before they meet at the chunk's end
-        if (!ENDS) {
-            load_cols(sv, v, c);
+        if (!ENDS)
             load_E(c);
-        }
         cp_commit();
         load_cols(sdo + ((c - 1) & 1) * kC * 32, dout, c - 1);
         cp_commit();
-        float sc0 = 0.f, sc1 = 0.f;
+        float se_next[OWN][2] = {};
+        if (SP == 1)
+            read_E_scales(c, se);
+        const int before = max(c - 1, lo);  // the last chunk asks for its own once more
         if (GATED) {
-            ask_state(c);
-            sc0 = state_scale(c, g), sc1 = state_scale(c, g + 8);
+            ask_state(before);
+            read_S_scales(before);
+            if (SP > 1)
+                ask_tokens(before);
         }
-        float se[OWN][2];
-        if (!ENDS) {
-#pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                const float* at = kept.sE + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
-                se[i][0] = at[g], se[i][1] = at[g + 8];
-            }
-        }
+        if (SP > 1)
+            read_E_scales(before, se_next);
         auto pair = [](float (&x)[8][4], int i) -> float(&)[2][4] {
             return *reinterpret_cast<float(*)[2][4]>(x + 2 * i);
         };
@@ -1661,11 +1672,42 @@ __global__ void __launch_bounds__(256, 1)
             sh.sync();
             sh.template get<true>(0, pair(u, 0), pair(u, 1));
         }
+        // E of the own C tile nt
+        auto read_E = [&](int nt, float (&y)[4]) {
+            const uint32_t* at = reinterpret_cast<const uint32_t*>(smem + mine + SM::e) +
+                                 (sh.tile(nt >> 1) * 4 + 2 * (nt & 1)) * 32 + lane;
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(at));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(at + 32));
+            const float2 l = __half22float2(*reinterpret_cast<const __half2*>(at + kC * 8));
+            const float2 m = __half22float2(*reinterpret_cast<const __half2*>(at + kC * 8 + 32));
+            const float s0 = se[nt >> 1][0], s1 = se[nt >> 1][1];
+            y[0] = s0 * (a.x + l.x), y[1] = s0 * (a.y + l.y), y[2] = s1 * (b.x + m.x), y[3] = s1 * (b.y + m.y);
+        };
+        // dU.  Its part from the state is dotted with U for the gates: two warps per slice
+        // have the registers to keep it until E is read for the other dots (534 against 553
+        // us), one does it at once (324 against 332 us)
+        constexpr bool L_NOW = GATED && !ENDS && SP == 1, L_LATE = GATED && !ENDS && SP > 1;
+        if (L_NOW) {
+            cp_wait<1>();  // E
+            __syncwarp();
+        }
+        float lsum[OWN / 2][8], us[L_LATE ? 2 * OWN : 1][4];
+        auto dot_U = [&](int nt, const float (&x)[4], const float (&y)[4]) {
+            const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
+            lsum[nt >> 2][2 * (nt & 3)] = be.x * (x[0] * y[0] + x[2] * y[2]);
+            lsum[nt >> 2][2 * (nt & 3) + 1] = be.y * (x[1] * y[1] + x[3] * y[3]);
+        };
 #pragma unroll
-        for (int i = 0; i < 2 * OWN; ++i) {  // dU
-            const float2 w = fac2(fac, kFacW, sh.tile(i >> 1), i & 1, tq);
-            set_rows(u[i], fma2(w, row_a(u[i]), mul2(row_a(x[i]), both(q0.from))),
-                     fma2(w, row_b(u[i]), mul2(row_b(x[i]), both(q1.from))));
+        for (int i = 0; i < 2 * OWN; ++i) {
+            scale_cols(u[i], fac2(fac, kFacW, sh.tile(i >> 1), i & 1, tq));
+            if (L_NOW) {
+                float y[4];
+                read_E(i, y);
+                dot_U(i, u[i], y);
+            }
+            if (L_LATE)
+                set_rows(us[i], row_a(u[i]), row_b(u[i]));
+            set_rows(u[i], fma2(row_a(x[i]), both(q0.from), row_a(u[i])), fma2(row_b(x[i]), both(q1.from), row_b(u[i])));
         }
         if (SP > 1) {
             sh.put(1, pair(u, 0), pair(u, 1));
@@ -1706,40 +1748,39 @@ __global__ void __launch_bounds__(256, 1)
                 scale_cols(u[nt], fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq));
             }
         } else {
-            cp_wait<1>();  // V, E
-            __syncwarp();
+            if (!L_NOW) {
+                cp_wait<1>();  // E
+                __syncwarp();
+            }
             // Y, the dots, dV on the own tiles
-            float bsum[OWN / 2][8], vsum[OWN / 2][8];
+            float bsum[OWN / 2][8], hsum[OWN / 2][8];
 #pragma unroll
-            for (int i = 0; i < OWN; ++i) {
-                uint32_t w[4];
-                ldsm4t(w, addr_ct<32>(sv, lane, 16 * sh.tile(i), 0));
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nt = 2 * i + h;
-                    const float2 be = fac2(fac, kFacB, sh.tile(i), h, tq);
-                    set_rows(u[nt], fma2(back(nt, y0), row_a(x[nt]), row_a(u[nt])),
-                             fma2(back(nt, y1), row_b(x[nt]), row_b(u[nt])));
-                    const uint32_t* eh =
-                        reinterpret_cast<const uint32_t*>(smem + mine + SM::e) + (sh.tile(i) * 4 + 2 * h) * 32 + lane;
-                    const uint32_t* el = eh + kC * 8;
-                    const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(eh));
-                    const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(eh + 32));
-                    const float2 l0 = __half22float2(*reinterpret_cast<const __half2*>(el));
-                    const float2 l1 = __half22float2(*reinterpret_cast<const __half2*>(el + 32));
-                    const int part = nt >> 2, k = 2 * (nt & 3);
-                    bsum[part][k] = u[nt][0] * (se[i][0] * (a0.x + l0.x)) + u[nt][2] * (se[i][1] * (a1.x + l1.x));
-                    bsum[part][k + 1] = u[nt][1] * (se[i][0] * (a0.y + l0.y)) + u[nt][3] * (se[i][1] * (a1.y + l1.y));
-                    u[nt][0] *= be.x, u[nt][1] *= be.y, u[nt][2] *= be.x, u[nt][3] *= be.y;
-                    vsum[part][k] = u[nt][0] * lo_f(w[2 * h]) + u[nt][2] * lo_f(w[2 * h + 1]);
-                    vsum[part][k + 1] = u[nt][1] * hi_f(w[2 * h]) + u[nt][3] * hi_f(w[2 * h + 1]);
+            for (int nt = 0; nt < 2 * OWN; ++nt) {
+                const float2 be = fac2(fac, kFacB, sh.tile(nt >> 1), nt & 1, tq);
+                set_rows(u[nt], fma2(back(nt, y0), row_a(x[nt]), row_a(u[nt])),
+                         fma2(back(nt, y1), row_b(x[nt]), row_b(u[nt])));
+                const int part = nt >> 2, k = 2 * (nt & 3);
+                float y[4];
+                read_E(nt, y);
+                if (L_LATE)
+                    dot_U(nt, us[nt], y);
+                bsum[part][k] = u[nt][0] * y[0] + u[nt][2] * y[2];
+                bsum[part][k + 1] = u[nt][1] * y[1] + u[nt][3] * y[3];
+                scale_cols(u[nt], be);
+                if (GATED) {
+                    const float2 fa = fac2(fac, kFacA, sh.tile(nt >> 1), nt & 1, tq);
+                    const float4 a = read_KS(c, nt);
+                    hsum[part][k] = -fa.x * (u[nt][0] * a.x + u[nt][2] * a.z);
+                    hsum[part][k + 1] = -fa.y * (u[nt][1] * a.y + u[nt][3] * a.w);
                 }
             }
 #pragma unroll
             for (int part = 0; part < OWN / 2; ++part) {
                 sh.store_sums(kept.bb + (bh * (DV / 16) + slice) * N, bsum[part], part, (int64_t)c * kC, N);
-                if (GATED)
-                    sh.store_sums(kept.vv + (bh * (DV / 16) + slice) * N, vsum[part], part, (int64_t)c * kC, N);
+                if (GATED) {
+                    sh.store_sums(kept.hk + (bh * (DV / 16) + slice) * N, hsum[part], part, (int64_t)c * kC, N);
+                    sh.store_sums(kept.ll + (bh * (DV / 16) + slice) * N, lsum[part], part, (int64_t)c * kC, N);
+                }
             }
         }
         if (SP > 1)
@@ -1748,11 +1789,10 @@ __global__ void __launch_bounds__(256, 1)
         if (SP > 1)
             sh.template get<false>(2, pair(u, 2), pair(u, 3));
         if (!ENDS) {
-            // dV leaves as bf16 (V's tile is read) and is kept, times p, as scaled fp16
-            __syncwarp();
+            // dV leaves as bf16 and is kept, times p, as scaled fp16 (both parts for the gates)
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
-                uint32_t w[4], a[4];
+                uint32_t w[4], a[4], l[4];
                 float y[8][4];  // the first two C tiles: p dV
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -1765,11 +1805,13 @@ __global__ void __launch_bounds__(256, 1)
                     const int nt = 2 * i + h;
                     w[2 * h] = sm100::pack_bf16x2(u[nt][0], u[nt][1]);
                     w[2 * h + 1] = sm100::pack_bf16x2(u[nt][2], u[nt][3]);
-                    a[2 * h] = h2(y[h][0] * s0.to, y[h][1] * s0.to);
-                    a[2 * h + 1] = h2(y[h][2] * s1.to, y[h][3] * s1.to);
+                    h2_split(row_a(y[h]), s0.to, a[2 * h], l[2 * h]);
+                    h2_split(row_b(y[h]), s1.to, a[2 * h + 1], l[2 * h + 1]);
                 }
                 stsm4t(addr_ct<32>(sv, lane, 16 * sh.tile(i), 0), w);
                 keep_part(kept.dV, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, a);
+                if (GATED)
+                    keep_part(kept.dVl, bh * nchunk + c, kC * DV * 2, slice * 4 + sh.tile(i), lane, l);
                 if (tq == 0) {
                     float* sw = kept.sV + ((bh * nchunk + c) * 4 + sh.tile(i)) * DV + col0;
                     sw[g] = s0.from, sw[g + 8] = s1.from;
@@ -1840,8 +1882,13 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             scale_rows(ds[nt], r0.from, r1.from);
-        if (GATED)
-            dot_state(c, sc0, sc1);
+        if (GATED)  // no branch at the last chunk: the loads can go up among the products
+            dot_state(before, sc[0], sc[1], it + 1 < len);
+        if (SP > 1) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                se[o][0] = se_next[o][0], se[o][1] = se_next[o][1];
+        }
         cp_wait<0>();
         sh.sync();
         if (ring.last(it) && it + SM::stages < len)
@@ -1943,8 +1990,8 @@ template <int D, int DV>
 __global__ void __launch_bounds__(kDqkThreads, 1)
     k_delta_dqk(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
                 const __nv_bfloat16* __restrict__ dout, Kept kept, __nv_bfloat16* __restrict__ dq,
-                __nv_bfloat16* __restrict__ dk, float* __restrict__ dbeta, float* __restrict__ dlog_alpha,
-                int64_t N, int nchunk, int items, int H, int Hk, int l2, float scale, int zero_start, int* status)
+                __nv_bfloat16* __restrict__ dk, int64_t N, int nchunk, int items, int H, int Hk, int l2, float scale,
+                int* status)
 {
     extern __shared__ __align__(1024) unsigned char smem[];
     using SM = DqkSmem<D, DV>;
@@ -2001,14 +2048,13 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
                          SM::facs, bar);
         delta::bulk_load(to + SM::cols, kept.sE + x.at * 4 * DV, 4 * DV * 4, bar);
         delta::bulk_load(to + SM::cols + 4 * DV * 4, kept.sV + x.at * 4 * DV, 4 * DV * 4, bar);
-        delta::bulk_load(to + SM::cols + 8 * DV * 4, kept.sS + (x.bh * (nchunk + 1) + x.c) * 2 * DV, 2 * DV * 4, bar);
+        delta::bulk_load(to + SM::cols + 8 * DV * 4, kept.sS + x.at * 2 * DV, 2 * DV * 4, bar);
         delta::bulk_load(to + SM::cols + 10 * DV * 4, kept.sD + x.at * 2 * DV, 2 * DV * 4, bar);
     };
     auto load_states = [&](int s) {
         const Step x = step_of(s);
         sm100::mbar_arrive_expect_tx(full + 2, 2 * D * DV * 2);
-        delta::bulk_load(base + SM::S, kept.S + 2 * (x.bh * (nchunk + 1) + x.c) * (int64_t)(D * DV * 2), D * DV * 2,
-                         full + 2);
+        delta::bulk_load(base + SM::S, kept.S + 2 * x.at * (int64_t)(D * DV * 2), D * DV * 2, full + 2);
         delta::bulk_load(base + SM::dS, kept.dS + x.at * (D * DV * 2), D * DV * 2, full + 2);
     };
     auto load_rows = [&](int s) {
@@ -2293,44 +2339,8 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
         int again = s;  // the step's place is worked out anew, for registers
         asm volatile("" : "+r"(again));
         const Step me = step_of(again);
-        const int64_t t0 = me.t0, bh = me.bh;
+        const int64_t t0 = me.t0;
         const int n = me.n;
-        // the gates' gradients from the dots over 16 columns each
-        if (warp == 0) {
-            float z[2], after = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = lane + 32 * h;
-                float b = 0.f, y = 0.f;
-                if (t < n) {
-                    for (int s = 0; s < KS; ++s) {
-                        const int64_t row = (bh * KS + s) * N + t0 + t;
-                        b += kept.bb[row];
-                        if (dlog_alpha)
-                            y += kept.oo[row] - kept.vv[row];
-                    }
-                    dbeta[bh * N + t0 + t] = b;
-                }
-                z[h] = y;
-            }
-            if (dlog_alpha) {
-                for (int s = 0; s < 2 * KS; ++s)
-                    after += kept.cd[(bh * 2 * KS + s) * nchunk + me.c];
-#pragma unroll
-                for (int h = 1; h >= 0; --h) {
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float y = __shfl_down_sync(0xffffffffu, z[h], o);
-                        if (lane + o < 32)
-                            z[h] += y;
-                    }
-                    const int t = lane + 32 * h;
-                    if (t < n)  // a first gate on a zero state has no gradient, the sums leave their rounding
-                        dlog_alpha[bh * N + t0 + t] = zero_start && t0 + t == 0 ? 0.f : z[h] + after;
-                    after += __shfl_sync(0xffffffffu, z[h], 0);
-                }
-            }
-        }
         if (p == per - 1) {
             // through scale and norm: unit = f image, dx = r (x - unit (unit.x))
             const int image = role_k ? SM::K : SM::Q;
@@ -2417,6 +2427,352 @@ __global__ void __launch_bounds__(kDqkThreads, 1)
     }
 }
 
+// ------------------------------------------------------------ k_delta_gates --
+// dbeta and dlog_alpha of one chunk and value head.  log_alpha_t enters every decay
+// that spans t, so its gradient is the sum of all terms with such a decay:
+//
+//   dlog_alpha_t = sum_{i >= t > j} W_ij + sum_{i >= t} h_i + sum_{j < t} l_j + e^{G_C} <S0, dS1>
+//   W_ij = D_ij (dO_i.U_j scale q_i.k_j - dV_i.U_j k_i.k_j)
+//
+// with h, l and <S0, dS1> from the chains.  (By the rows' dots alone it is <S1, dS1> +
+// sum_{i >= t} (q_i.dQ_i - v_i.dV_i), but there the terms that do not span t cancel only
+// up to their rounding, which is all that is left of a strong gate's gradient.)
+// A warp takes one or two 16 x 16 tiles of one of W's two parts: the Gram products from
+// the row images, the dots over the value columns 32 at a time, from two fp16 parts (dO is
+// exact), their column scales going to the fragments.  Then running sums along the rows,
+// every entry added where it counts and nowhere taken off again.
+// Measured: 137 us for the 4096 chunks of B4 H8 N8192 d=128, whose 480 MB alone take 94 us
+// (5.1 TB/s); two blocks per SM, whose products (26 us), Gram products and sums are only
+// partly under the other's loads.
+constexpr int kGateThreads = 384;
+constexpr int kGateCols = 32;
+
+template <int D, int DV>
+struct GateSmem {
+    static constexpr int part = kC * kGateCols * 2, step = 4 * part, steps = DV / kGateCols;
+    // the last two of four steps go where the row images were, once those are used
+    static constexpr int late = steps == 4 && 2 * step <= 2 * row_image<D>() ? 2 : 0;
+    static constexpr int K = 0, Q = row_image<D>(), buf = 2 * row_image<D>(), dO = buf + (steps - late) * step,
+                         fac = dO + kC * DV * 2, facs = (kFacC - kFacB) * kC * 4,
+                         cols = fac + facs,                            // [E, dV][4 tiles][DV] fp16 column scales
+                         sums = cols + 8 * DV * 2,                     // [12 warps][32]
+                         vec = sums + 12 * 32 * 4, bar = vec + 5 * kC * 4, bytes = bar + 128;
+    static constexpr int at(int s) { return s < steps - late ? buf + s * step : (s - (steps - late)) * step; }
+};
+
+template <int D, int DV>
+__global__ void __launch_bounds__(kGateThreads, 2)
+    k_delta_gates(const unsigned char* __restrict__ rows, const unsigned char* __restrict__ blobs,
+                  const __nv_bfloat16* __restrict__ dout, Kept kept, float* __restrict__ dbeta,
+                  float* __restrict__ dlog_alpha, int64_t N, int nchunk, int H, int Hk, float scale, int* status)
+{
+    extern __shared__ __align__(1024) unsigned char smem[];
+    using SM = GateSmem<D, DV>;
+    constexpr int RB = 2 * D, VB = 2 * DV, KS = DV / 16, STEPS = SM::steps;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+    const bool of_k = warp >= 6;  // the part of k_i.k_j
+    // tile of rows, the first tile of columns, the second there or not:
+    // (3, 0 1) (3, 2 3) (2, 0 1) (1, 0 1) (2, 2) (0, 0)
+    const int who = of_k ? warp - 6 : warp, I = 0x021233 >> 4 * who & 3, J = 0x020020 >> 4 * who & 3;
+    const bool two = who < 4;
+    const uint32_t base = smem_addr(smem);
+    const int64_t at = blockIdx.x, bh = at / nchunk;
+    const int c = (int)(at % nchunk);
+    const int64_t kh = bh / H * Hk + (bh % H) / (H / Hk), t0 = (int64_t)c * kC;
+    const int n = (int)min((int64_t)kC, N - t0);
+    float* sdo = reinterpret_cast<float*>(smem + SM::vec);  // dO's row scales
+    float *sh = sdo + kC, *sl = sh + 2 * kC;                // h in two parts, l
+    float* rest = sl + kC;                                  // [2][32] row sums of the tiles (3, 0 1) and (2, 0 1)
+    float* sums = reinterpret_cast<float*>(smem + SM::sums);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::bar);  // row images and factors, the steps
+    float* top = reinterpret_cast<float*>(full + 5);               // [E, dV][4] largest column scale
+    const float* fac = reinterpret_cast<const float*>(smem + SM::fac) - kFacB * kC;
+    const float *fB = fac + kFacB * kC, *fK = fac + kFacK * kC, *fQ = fac + kFacQ * kC, *fP = fac + kFacPk * kC,
+                *gh = fac + kFacGh * kC, *gl = fac + kFacGl * kC;
+
+    auto load_step = [&](int s) {
+        uint64_t* bar = full + 1 + s;
+        const uint32_t to = base + SM::at(s);
+        sm100::mbar_arrive_expect_tx(bar, SM::step);
+        delta::bulk_load(to, kept.E + 2 * at * (kC * DV * 2) + s * SM::part, SM::part, bar);
+        delta::bulk_load(to + SM::part, kept.E + (2 * at + 1) * (kC * DV * 2) + s * SM::part, SM::part, bar);
+        delta::bulk_load(to + 2 * SM::part, kept.dV + at * (kC * DV * 2) + s * SM::part, SM::part, bar);
+        delta::bulk_load(to + 3 * SM::part, kept.dVl + at * (kC * DV * 2) + s * SM::part, SM::part, bar);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < 1 + STEPS; ++i)
+            sm100::mbar_init(full + i, 1);
+        sm100::fence_mbar_init();
+        sm100::mbar_arrive_expect_tx(full, 2 * row_image<D>() + SM::facs);
+        delta::bulk_load(base + SM::K, rows + (kh * nchunk + c) * (int64_t)(2 * row_image<D>()), 2 * row_image<D>(), full);
+        delta::bulk_load(base + SM::fac, blobs + at * blob_bytes<true>() + fac_at<true>() + kFacB * kC * 4, SM::facs, full);
+        for (int s = 0; s < STEPS - SM::late; ++s)
+            load_step(s);
+    }
+    // Meanwhile, every load first: dO, the column scales (E's by warps 0 to 3, dV's by the
+    // others) and the chains' dots over 16 columns each
+    constexpr int LPR = DV / 8, RPP = 256 / LPR;  // lanes per row of dO, rows of 256 threads
+    uint4 w[kC / RPP];
+#pragma unroll
+    for (int b = 0; b < kC / RPP; ++b) {
+        const int r = b * RPP + tid / LPR;
+        w[b] = make_uint4(0, 0, 0, 0);
+        if (r < n && tid < 256)
+            w[b] = *reinterpret_cast<const uint4*>(dout + (bh * N + t0 + r) * DV + tid % LPR * 8);
+    }
+    float scales[DV / 32], dots[KS];
+#pragma unroll
+    for (int i = 0; i < DV / 32; ++i)
+        scales[i] = (warp < 4 ? kept.sE : kept.sV)[(at * 4 + (warp & 3)) * DV + lane + 32 * i];  // again by warps 8 ..
+    const float* sums_of = tid < kC ? kept.hq : tid < 2 * kC ? kept.hk : tid < 3 * kC ? kept.ll : kept.bb;
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+        dots[i] = tid < 256 && tid % kC < n ? sums_of[(bh * KS + i) * N + t0 + tid % kC] : 0.f;
+    float cd = tid < 2 * KS ? kept.cd[(bh * 2 * KS + tid) * nchunk + c] : 0.f;
+    if (warp < 8) {
+#pragma unroll
+        for (int b = 0; b < kC / RPP; ++b) {  // dO to fp16 rows, a row by the lanes of one warp
+            const int r = b * RPP + tid / LPR;
+            const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mx = max_abs(max_abs(mx, lo_f(u[i])), hi_f(u[i]));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const Pow2 q = pow2_for(mx);
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[i] = h2(lo_f(u[i]) * q.to, hi_f(u[i]) * q.to);
+            *reinterpret_cast<uint4*>(smem + SM::dO + tile_off<VB>(r, tid % LPR)) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (tid % LPR == 0)
+                sdo[r] = q.from;
+        }
+        {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < DV / 32; ++i)
+                m = fmaxf(m, scales[i]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            __half* dst = reinterpret_cast<__half*>(smem + SM::cols) + warp * DV;
+#pragma unroll
+            for (int i = 0; i < DV / 32; ++i)
+                dst[lane + 32 * i] = __float2half_rn(scales[i] * (1.0f / m));  // powers of two
+            if (lane == 0)
+                top[warp] = m;
+        }
+        {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                x += dots[i];
+            if (tid < 3 * kC)
+                sh[tid] = x;  // h's parts, l
+            else if (tid % kC < n)
+                dbeta[bh * N + t0 + tid % kC] = x;
+        }
+    }
+    if (warp == 0) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            cd += __shfl_xor_sync(0xffffffffu, cd, o);
+    }
+    __syncthreads();
+    bool ok = wait_warp(full, 0);
+    // this warp's rows times its columns' tokens: Gram products, then dots over value columns
+    float gm[4][4], x[4][4];
+    clear(gm);
+    clear(x);
+    if (ok) {
+#pragma unroll 4
+        for (int kk = 0; kk < D; kk += 16) {
+            uint32_t a[4], b[4];
+            ldsm4(a, addr_a<RB>(base + (of_k ? SM::K : SM::Q), lane, 16 * I, kk));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (j == 0 || two) {
+                    ldsm4(b, addr_b<RB>(base + SM::K, lane, 16 * (J + j), kk));
+                    mma(gm[2 * j], a, b[0], b[1]);
+                    mma(gm[2 * j + 1], a, b[2], b[3]);
+                }
+            }
+        }
+    }
+    if (SM::late) {
+        sm100::fence_proxy_async_smem();
+        ok = __syncthreads_and(ok);  // the row images are read
+        if (tid == 0 && ok)
+            for (int s = STEPS - SM::late; s < STEPS; ++s)
+                load_step(s);
+    }
+    auto times = [](uint32_t (&x)[4], uint32_t f0, uint32_t f1) {  // registers 0, 2 and 1, 3
+        const uint32_t f[2] = {f0, f1};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[i]), *reinterpret_cast<const __half2*>(&f[i & 1]));
+            x[i] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    };
+    // column scales of tile `row` (E: 0 .. 3, dV: 4 ..), columns c0 + 2 tq and the next
+    auto col = [&](int row, int c0) {
+        return *reinterpret_cast<const uint32_t*>(smem + SM::cols + (row * DV + c0 + 2 * tq) * 2);
+    };
+#pragma unroll 1
+    for (int s = 0; s < STEPS; ++s) {
+        ok = ok && wait_warp(full + 1 + s, 0);
+        const uint32_t buf = base + SM::at(s);
+        if (ok) {
+#pragma unroll
+            for (int ks = 0; ks < kGateCols / 16; ++ks) {
+                const int c0 = s * kGateCols + 16 * ks;
+                uint32_t ah[4], al[4];
+                if (of_k) {
+                    uint32_t y[4], z[4];
+                    ldsm4t(y, buf + 2 * SM::part + (ks * 4 + I) * 512 + lane * 16);
+                    ldsm4t(z, buf + 3 * SM::part + (ks * 4 + I) * 512 + lane * 16);
+                    times(y, col(4 + I, c0), col(4 + I, c0 + 8));
+                    times(z, col(4 + I, c0), col(4 + I, c0 + 8));
+                    ah[0] = y[0], ah[1] = y[2], ah[2] = y[1], ah[3] = y[3];
+                    al[0] = z[0], al[1] = z[2], al[2] = z[1], al[3] = z[3];
+                } else {
+                    ldsm4(ah, addr_a<VB>(base + SM::dO, lane, 16 * I, c0));
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (j == 0 || two) {
+                        uint32_t bh_[4], bl[4];
+                        ldsm4t(bh_, buf + (ks * 4 + J + j) * 512 + lane * 16);
+                        ldsm4t(bl, buf + SM::part + (ks * 4 + J + j) * 512 + lane * 16);
+                        const uint32_t f0 = col(J + j, c0), f1 = col(J + j, c0 + 8);
+                        times(bh_, f0, f1);
+                        times(bl, f0, f1);
+                        mma(x[2 * j], ah, bh_[0], bh_[1]);
+                        mma(x[2 * j + 1], ah, bh_[2], bh_[3]);
+                        mma(x[2 * j], ah, bl[0], bl[1]);
+                        mma(x[2 * j + 1], ah, bl[2], bl[3]);
+                        if (of_k) {
+                            mma(x[2 * j], al, bh_[0], bh_[1]);
+                            mma(x[2 * j + 1], al, bh_[2], bh_[3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!__syncthreads_and(ok)) {
+        // a copy did not arrive in time: the results are void.  What is in flight gets as
+        // long again before its shared memory goes
+        if (tid == 0) {
+            for (int i = 0; i < 1 + STEPS; ++i)
+                wait_for(full + i, 0);
+            set_status(status, LA_ERR_TIMEOUT);
+        }
+        __syncthreads();
+        return;
+    }
+    // W, its running sums along the rows up to column t, and those added up over rows i >= t
+    const int ia = 16 * I + g, ib = ia + 8;
+    const float ra = of_k ? -fK[ia] : fQ[ia] * scale, rb = of_k ? -fK[ib] : fQ[ib] * scale;
+    const float va = of_k ? top[4 + I] / fP[ia] : sdo[ia], vb = of_k ? top[4 + I] / fP[ib] : sdo[ib];
+    float y[8] = {}, suma = 0.f, sumb = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        if (nt < 2 || two) {
+            const int j = 16 * J + 8 * nt + 2 * tq;
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = e >> 1 ? ib : ia, jj = j + (e & 1);
+                const float d = ex2((gh[i] - gh[jj]) + (gl[i] - gl[jj]));
+                const float a = gm[nt][e] * ((e >> 1 ? rb : ra) * fK[jj]);
+                const float b = x[nt][e] * ((e >> 1 ? vb : va) * (fB[jj] * top[J + (nt >> 1)]));
+                w[e] = jj < i ? a * b * d : 0.f;
+            }
+            float pa = w[0] + w[1], pb = w[2] + w[3];  // inclusive over the quad
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const float qa = __shfl_up_sync(0xffffffffu, pa, o, 4), qb = __shfl_up_sync(0xffffffffu, pb, o, 4);
+                if (tq >= o)
+                    pa += qa, pb += qb;
+            }
+            float ea = __shfl_up_sync(0xffffffffu, pa, 1, 4), eb = __shfl_up_sync(0xffffffffu, pb, 1, 4);
+            ea = suma + (tq ? ea : 0.f), eb = sumb + (tq ? eb : 0.f);  // of the columns before j
+            y[2 * nt] = (ia >= j ? ea : 0.f) + (ib >= j ? eb : 0.f);
+            y[2 * nt + 1] = (ia > j ? ea + w[0] : 0.f) + (ib > j ? eb + w[2] : 0.f);
+            suma += __shfl_sync(0xffffffffu, pa, 3, 4), sumb += __shfl_sync(0xffffffffu, pb, 3, 4);
+        }
+    }
+    // lane 4 g + tq: C tile g >> 1, column 2 tq + (g & 1)
+    sums[warp * 32 + 8 * (g >> 1) + 2 * tq + (g & 1)] = delta::sum8(y, lane);
+    if (tq == 0 && (who == 0 || who == 2)) {  // for the columns behind tiles 0 and 1
+        float* to = rest + (of_k ? 32 : 0) + 16 * (I - 2) + g;
+        to[0] = suma, to[8] = sumb;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        float h[2], l[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            h[u] = sh[lane + 32 * u] + sh[kC + lane + 32 * u], l[u] = sl[lane + 32 * u];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float a = __shfl_down_sync(0xffffffffu, h[u], o), b = __shfl_up_sync(0xffffffffu, l[u], o);
+                if (lane + o < 32)
+                    h[u] += a;
+                if (lane >= o)
+                    l[u] += b;
+            }
+        }
+        float r = rest[lane] + rest[32 + lane];  // of rows 32 + lane
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float a = __shfl_down_sync(0xffffffffu, r, o);
+            if (lane + o < 32)
+                r += a;
+        }
+        h[0] += __shfl_sync(0xffffffffu, h[1], 0);
+        const float half = __shfl_sync(0xffffffffu, l[0], 31);
+        cd *= exp2f(gh[kC - 1] + gl[kC - 1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int t = lane + 32 * u;
+            float z = 0.f, before = __shfl_up_sync(0xffffffffu, l[u], 1);
+            before = (lane ? before : 0.f) + (u ? half : 0.f);
+#pragma unroll
+            for (int p = 0; p < 12; p += 6) {  // the tiles with this column: of both warps' halves, of the first
+                if (u == 0)
+                    z += sums[(p + 0) * 32 + lane] + sums[(p + 2) * 32 + lane] + sums[(p + 3) * 32 + lane];
+                else
+                    z += sums[(p + 1) * 32 + lane];
+                if (lane < 16)
+                    z += sums[(p + (u ? 4 : 5)) * 32 + lane];
+            }
+            if (u)
+                z += r;
+            if (t < n)
+                dlog_alpha[bh * N + t0 + t] = z + h[u] + before + cd;
+        }
+    }
+}
+
+// dbeta alone, without gates
+__global__ void __launch_bounds__(256)
+    k_delta_dbeta(const float* __restrict__ bb, float* __restrict__ dbeta, int64_t N, int64_t count, int slices)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= count)
+        return;
+    const float* at = bb + i / N * slices * N + i % N;
+    float x = 0.f;
+    for (int s = 0; s < slices; ++s)
+        x += at[s * N];
+    dbeta[i] = x;
+}
+
 // ------------------------------------------------------------------- hosts --
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 int chunks_of(int64_t N) { return (int)((N + kC - 1) / kC); }
@@ -2474,7 +2830,7 @@ TcLayout tc_layout(const DeltaArgs& a)
 }
 
 struct GradTcLayout {
-    size_t rows, blobs, S, sS, E, sE, dS, sD, dV, sV, oo, vv, bb, cd, seg, total;
+    size_t rows, blobs, S, sS, E, sE, dS, sD, dV, sV, bb, dVl, KS, hq, hk, ll, cd, seg, total;
 };
 GradTcLayout grad_tc_layout(const DeltaArgs& a)
 {
@@ -2489,17 +2845,20 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
     };
     l.rows = take((size_t)(a.B * a.Hk) * n * 2 * kC * a.d * 2);
     l.blobs = take(BH * n * blob_bytes<true>());
-    l.S = take(BH * (n + 1) * 2 * state);
-    l.sS = take(BH * (n + 1) * 2 * a.dv * 4);
+    l.S = take(BH * n * 2 * state);
+    l.sS = take(BH * n * 2 * a.dv * 4);
     l.E = take(BH * n * 2 * toks);
     l.sE = take(BH * n * 4 * a.dv * 4);
     l.dS = take(BH * n * state);
     l.sD = take(BH * n * 2 * a.dv * 4);
     l.dV = take(BH * n * toks);
     l.sV = take(BH * n * 4 * a.dv * 4);
-    l.oo = take(BH * sl * (size_t)a.N * 4);
-    l.vv = take(BH * sl * (size_t)a.N * 4);
     l.bb = take(BH * sl * (size_t)a.N * 4);
+    l.dVl = take(BH * n * toks);  // from here: with gates only, but the size is asked for without
+    l.KS = take(BH * n * 2 * toks);
+    l.hq = take(BH * sl * (size_t)a.N * 4);
+    l.hk = take(BH * sl * (size_t)a.N * 4);
+    l.ll = take(BH * sl * (size_t)a.N * 4);
     l.cd = take(BH * sl * 2 * n * 4);
     l.seg = take(seg_layout(a).total);
     l.total = at;
@@ -2590,7 +2949,7 @@ cudaError_t launch_rev(const DeltaArgs& a, int W, const unsigned char* rows, con
         return e;
     k_delta_rev<D, SP, GATED, ENDS>
         <<<(unsigned)(runs * (a.dv / (16 * W))), 32 * SP * W, smem, a.stream>>>(
-            rows, blobs, static_cast<const __nv_bfloat16*>(a.v), static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
+            rows, blobs, static_cast<const __nv_bfloat16*>(a.dout), a.dS_out,
             static_cast<__nv_bfloat16*>(a.dv_), a.dS0, a.N, chunks_of(a.N), (int)a.H, (int)a.Hk, a.dv, kept, seg,
             a.status);
     count_launches(1);
@@ -2706,7 +3065,8 @@ cudaError_t run_backward(const DeltaArgs& a)
     unsigned char* ws = static_cast<unsigned char*>(a.ws);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     const Kept kept = {ws + l.S, f32(l.sS), ws + l.E, f32(l.sE), ws + l.dS, f32(l.sD),
-                       ws + l.dV, f32(l.sV), f32(l.oo), f32(l.vv), f32(l.bb), f32(l.cd)};
+                       ws + l.dV, f32(l.sV), f32(l.bb), ws + l.dVl, reinterpret_cast<float4*>(ws + l.KS),
+                       f32(l.hq), f32(l.hk), f32(l.ll), f32(l.cd)};
     const int n = chunks_of(a.N), H = (int)a.H, Hk = (int)a.Hk, l2 = a.fm == LA_FM_L2;
     const int64_t BH = a.B * a.H;
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(a.dout);
@@ -2722,7 +3082,8 @@ cudaError_t run_backward(const DeltaArgs& a)
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const unsigned char *rows = ws + l.rows, *blobs = ws + l.blobs;
-    e = run_chain<D, true, true>(a, rows, blobs, kept, ws + l.seg);
+    e = a.log_alpha ? run_chain<D, true, true>(a, rows, blobs, kept, ws + l.seg)
+                    : run_chain<D, true, false>(a, rows, blobs, kept, ws + l.seg);
     if (e == cudaSuccess)
         e = run_rev<D>(a, rows, blobs, kept, ws + l.seg);
     if (e != cudaSuccess)
@@ -2731,8 +3092,19 @@ cudaError_t run_backward(const DeltaArgs& a)
     const int sms = device_sm_count() > 0 ? device_sm_count() : 1;
     k_delta_dqk<D, DV><<<(unsigned)(items < sms ? items : sms), kDqkThreads, DqkSmem<D, DV>::bytes, a.stream>>>(
         ws + l.rows, ws + l.blobs, dout, kept, static_cast<__nv_bfloat16*>(a.dq),
-        static_cast<__nv_bfloat16*>(a.dk), a.dbeta, a.dlog_alpha, a.N, n, (int)items, H, Hk, l2, a.scale,
-        !a.S0, a.status);
+        static_cast<__nv_bfloat16*>(a.dk), a.N, n, (int)items, H, Hk, l2, a.scale, a.status);
+    count_launches(1);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    if (a.log_alpha) {
+        if ((e = allow_smem(k_delta_gates<D, DV>, GateSmem<D, DV>::bytes)) != cudaSuccess)
+            return e;
+        k_delta_gates<D, DV><<<(unsigned)(BH * n), kGateThreads, GateSmem<D, DV>::bytes, a.stream>>>(
+            rows, blobs, dout, kept, a.dbeta, a.dlog_alpha, a.N, n, H, Hk, a.scale, a.status);
+    } else {
+        const int64_t count = BH * a.N;
+        k_delta_dbeta<<<(unsigned)((count + 255) / 256), 256, 0, a.stream>>>(kept.bb, a.dbeta, a.N, count, DV / 16);
+    }
     count_launches(1);
     return cudaGetLastError();
 }

@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 la = pytest.importorskip("kernelised_causal_linear_gb300")
 
 BF, F32 = torch.bfloat16, torch.float32
-DTYPES = [F32]
+DTYPES = [F32, BF]
 INPUTS = ("q", "k", "v", "beta", "log_alpha")
 
 
