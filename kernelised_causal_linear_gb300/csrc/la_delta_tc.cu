@@ -684,7 +684,8 @@ struct Ring {
     uint64_t *full, *read;
     unsigned* done;
     unsigned warps;
-    bool ok;  // false once a wait has run out: nothing is waited for any more
+    bool ok;  // false once a wait has run out: the warp leaves its loop, and no stage it has
+              // not read is filled again (a barrier with a copy still pending is not armed)
     __device__ __forceinline__ Ring(void* at, unsigned w)
         : full(static_cast<uint64_t*>(at)), read(full + STAGES), done(reinterpret_cast<unsigned*>(read + STAGES)),
           warps(w), ok(true)
@@ -701,9 +702,10 @@ struct Ring {
     }
     __device__ __forceinline__ void wait(int i)
     {
-        if (ok)
-            ok = __all_sync(0xffffffffu, wait_for(full + i % STAGES, (i / STAGES) & 1));
+        ok = __all_sync(0xffffffffu, wait_for(full + i % STAGES, (i / STAGES) & 1));
     }
+    // warps that meet in every chunk find out at its end, together
+    __device__ __forceinline__ bool go_on() const { return STEP || ok; }
     // after a wait has run out: what is in flight gets as long again
     __device__ __forceinline__ void drain()
     {
@@ -711,11 +713,12 @@ struct Ring {
             for (int parity = 0; parity < 2; ++parity)
                 wait_for(full + i, parity);
     }
-    // this warp is done with chunk i; true in one thread once all are
+    // this warp is done with chunk i; true in one thread once all are.  (A warp that has
+    // left does not arrive, so the others' count never fills and they run out in turn.)
     __device__ __forceinline__ bool last(int i)
     {
         if (STEP) {
-            __syncthreads();
+            ok = __syncthreads_and(ok);
             return threadIdx.x == 0;
         }
         __syncwarp();
@@ -967,7 +970,7 @@ __global__ void __launch_bounds__(256, 1)
     };
 
     ring.wait(0);
-    for (int step = 0; step < len; ++step) {
+    for (int step = 0; step < len && ring.go_on(); ++step) {
         const int c = lo + step;
         const uint32_t st = base + (step % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
@@ -1224,7 +1227,10 @@ __global__ void __launch_bounds__(256, 1)
                         *reinterpret_cast<const uint4*>(smem + (so - base) + tile_off<32>(t, p));
             }
         }
-        if (ring.last(step) && step + SM::stages < len)
+        const bool refill = ring.last(step);
+        if (!ring.ok)
+            break;
+        if (refill && step + SM::stages < len)
             load_stage(step + SM::stages);
         // here and not at the chunk's start: what is issued there (copies, addresses)
         // then shares a stretch without branches with the first products
@@ -1567,7 +1573,7 @@ __global__ void __launch_bounds__(256, 1)
     cp_wait<0>();
     sh.sync();
     ring.wait(0);
-    for (int it = 0; it < len; ++it) {
+    for (int it = 0; it < len && ring.go_on(); ++it) {
         const int c = lo + len - 1 - it;
         const uint32_t st = base + (it % SM::stages) * SM::stage;
         const uint32_t sK = st, sQ = st + row_image<D>(), sF = st + 2 * row_image<D>(), sP = sF + 2 * kTile;
@@ -1891,7 +1897,10 @@ __global__ void __launch_bounds__(256, 1)
         }
         cp_wait<0>();
         sh.sync();
-        if (ring.last(it) && it + SM::stages < len)
+        const bool refill = ring.last(it);
+        if (!ring.ok)
+            break;
+        if (refill && it + SM::stages < len)
             load_stage(it + SM::stages);
         if (it + 1 < len)
             ring.wait(it + 1);
