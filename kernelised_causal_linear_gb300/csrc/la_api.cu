@@ -474,7 +474,7 @@ la_status la_forward_delta(const void* q, const void* k, const void* v, const fl
     if (!workspace_ok(workspace, workspace_bytes, delta_forward_workspace(a)))
         return LA_ERR_WORKSPACE;
     a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha, a.out = out;
-    a.S0 = S0, a.S_out = S_out, a.ws = workspace, a.ws_bytes = workspace_bytes;
+    a.S0 = S0, a.S_out = S_out, a.ws = workspace;
     a.status = status_ptr();
     return from_cuda(delta_forward(a));
 }
@@ -528,7 +528,7 @@ la_status la_backward_delta(const void* dout, const float* dS_out, const void* q
     a.q = q, a.k = k, a.v = v, a.beta = beta, a.log_alpha = log_alpha;
     a.S0 = S0, a.dout = dout, a.dS_out = dS_out, a.dq = dq, a.dk = dk, a.dv_ = dv_out;
     a.dbeta = dbeta, a.dlog_alpha = dlog_alpha, a.dS0 = dS0;
-    a.ws = workspace, a.ws_bytes = workspace_bytes;
+    a.ws = workspace;
     a.status = status_ptr();
     return from_cuda(delta_backward(a));
 }

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kRecThreads)
 // element) and everything else is small, so the step is bound by HBM.  A CTA
 // owns D rows x CS columns; a thread keeps its rows of one 16-byte column
 // group in registers between the two products and the update.  256 x 32 heads of
-// 128 x 128: 157 us, 6.9 TB/s of the 1.09 GB it has to move, as fast as a copy.
+// 128 x 128: 162 us, 6.7 TB/s of the 1.09 GB it has to move, as fast as a copy.
 constexpr int kDecThreads = 256;
 
 template <int D, int CS, typename T>
@@ -410,8 +410,8 @@ struct GradKept {
 constexpr int kRevThreads = 256;
 
 // K and Q rows of a chunk (normalised, Q scaled; zero past n) by warps of a block
-template <int D, typename T>
-__device__ __forceinline__ void load_rows(float* sk, float* sq, int LK, const T* k, const T* q, int64_t row0, int n, int l2,
+template <int D>
+__device__ __forceinline__ void load_rows(float* sk, float* sq, int LK, const float* k, const float* q, int64_t row0, int n, int l2,
                                           float scale)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -420,8 +420,8 @@ __device__ __forceinline__ void load_rows(float* sk, float* sq, int LK, const T*
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
             const int64_t at = (row0 + t) * D + lane + 32 * i;
-            kk[i] = t < n ? to_f32<T>(k[at]) : 0.f;
-            qq[i] = t < n ? to_f32<T>(q[at]) : 0.f;
+            kk[i] = t < n ? k[at] : 0.f;
+            qq[i] = t < n ? q[at] : 0.f;
             k2 = fmaf(kk[i], kk[i], k2);
             q2 = fmaf(qq[i], qq[i], q2);
         }
@@ -456,12 +456,12 @@ __device__ __forceinline__ void load_gates(double* G, float* eg, float* ege, con
     ege[lane] = expf((float)(__shfl_sync(0xffffffffu, g, 31) - g));
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kRevThreads)
-    k_delta_grad_rev(const T* __restrict__ q, const T* __restrict__ k,
+    k_delta_grad_rev(const float* __restrict__ q, const float* __restrict__ k,
                      const float* __restrict__ beta, const float* __restrict__ log_alpha,
-                     const T* __restrict__ dout, const float* __restrict__ dS_out,
-                     const float* __restrict__ chk, const float* __restrict__ err, T* __restrict__ dv,
+                     const float* __restrict__ dout, const float* __restrict__ dS_out,
+                     const float* __restrict__ chk, const float* __restrict__ err, float* __restrict__ dv,
                      float* __restrict__ dS0, GradKept kept, int64_t N, int H, int Hk, int DV, int l2,
                      float scale, Segments seg)
 {
@@ -511,10 +511,10 @@ __global__ void __launch_bounds__(kRevThreads)
         if (lane == 0)
             red[warp] = dot;
         // rows past the end stay zero and leave nothing behind (beta = 0, G constant)
-        load_rows<D, T>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
+        load_rows<D>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
 #pragma unroll
         for (int t = warp; t < C; t += 8)
-            sdo[t * 32 + lane] = t < n ? to_f32<T>(dout[(bh * N + t0 + t) * DV + c0 + lane]) : 0.f;
+            sdo[t * 32 + lane] = t < n ? dout[(bh * N + t0 + t) * DV + c0 + lane] : 0.f;
         if (warp == 0) {
             load_gates(G, eg, ege, log_alpha ? log_alpha + bh * N + t0 : nullptr, n);
             sb[lane] = lane < n ? beta[bh * N + t0 + lane] : 0.f;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kRevThreads)
             sy[t * 32 + lane] = g;
             if (t < n && !ends) {
                 const int64_t at = (bh * N + t0 + t) * DV + c0 + lane;
-                dv[at] = from_f32<T>(g);
+                dv[at] = g;
                 kept.dV[at] = g;
                 db = y * err[at];
             }
@@ -663,10 +663,10 @@ struct GradSmem {
 
 // 16 x 16 threads per 32 x D result: thread (ty, tx) owns rows 2 ty, 2 ty + 1 and
 // columns tx, tx + 16, .. (stride: rows of S at 4 banks' distance from each other)
-template <int D, int DV, typename T>
+template <int D, int DV>
 __global__ void __launch_bounds__(kGradThreads)
-    k_delta_grad_dqk(const T* __restrict__ q, const T* __restrict__ k, const float* __restrict__ beta,
-                     const float* __restrict__ log_alpha, const T* __restrict__ dout,
+    k_delta_grad_dqk(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ beta,
+                     const float* __restrict__ log_alpha, const float* __restrict__ dout,
                      const float* __restrict__ chk, const float* __restrict__ err, GradKept kept,
                      float* __restrict__ dq, float* __restrict__ dk, float* __restrict__ dbeta,
                      float* __restrict__ dlog_alpha, int64_t N, int H, int Hk, int l2, float scale)
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kGradThreads)
     const int64_t t0 = b * C;
     const int n = (int)min((int64_t)C, N - t0);
 
-    load_rows<D, T>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
+    load_rows<D>(sk, sq, LK, k, q, kh * N + t0, n, l2, scale);
     if (warp == 0)
         load_gates(G, eg, ege, log_alpha ? log_alpha + bh * N + t0 : nullptr, n);
     if (tid < C)
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kGradThreads)
     for (int i = tid; i < C * DV; i += kGradThreads) {
         const int t = i / DV, c = i % DV;
         const int64_t at = (bh * N + t0 + t) * DV + c;
-        sdo[t * LV + c] = t < n ? to_f32<T>(dout[at]) : 0.f;
+        sdo[t * LV + c] = t < n ? dout[at] : 0.f;
         su[t * LV + c] = t < n ? beta[bh * N + t0 + t] * err[at] : 0.f;
         sg[t * LV + c] = t < n ? kept.dV[at] : 0.f;
     }
@@ -877,9 +877,9 @@ __global__ void __launch_bounds__(kGradThreads)
 // them: summed in head order, through the scale and the L2 norm
 // (x = u / l, l^2 = |u|^2 + eps: du = (dx - x (x.dx)) / l), rounded once.  A
 // warp per row.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(256)
-    k_delta_finish(const float* __restrict__ g, const T* __restrict__ u, T* __restrict__ du,
+    k_delta_finish(const float* __restrict__ g, const float* __restrict__ u, float* __restrict__ du,
                    int64_t rows, int64_t N, int H, int Hk, int l2, float scale)
 {
     const int lane = threadIdx.x & 31;
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(256)
         for (int p = 0; p < per; ++p)
             x[i] += g[((h0 + p) * N + t) * D + lane + 32 * i];
         x[i] *= scale;
-        y[i] = to_f32<T>(u[row * D + lane + 32 * i]);
+        y[i] = u[row * D + lane + 32 * i];
         n2 = fmaf(y[i], y[i], n2);
     }
     if (l2) {
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-        du[row * D + lane + 32 * i] = from_f32<T>(x[i]);
+        du[row * D + lane + 32 * i] = x[i];
 }
 
 // ----------------------------------------------------------------- hosts ----
@@ -1053,7 +1053,8 @@ GradLayout grad_layout(const DeltaArgs& a)
     return l;
 }
 
-template <int D, int DV, typename T>
+// fp32 alone: every bf16 gradient is on the tensor cores
+template <int D, int DV>
 cudaError_t run_grad(const DeltaArgs& a)
 {
     const GradLayout l = grad_layout(a);
@@ -1062,26 +1063,26 @@ cudaError_t run_grad(const DeltaArgs& a)
     const GradKept kept = {f32(l.dS), f32(l.dV), f32(l.bb), f32(l.cd)};
     DeltaArgs f = a;
     f.out = nullptr, f.S_out = nullptr;
-    cudaError_t e = run_rec<D, T>(f, f32(l.chk), f32(l.err), ws + l.seg);
+    cudaError_t e = run_rec<D, float>(f, f32(l.chk), f32(l.err), ws + l.seg);
     if (e != cudaSuccess)
         return e;
     const size_t rev = rev_smem<D>(), dqk = GradSmem<D, DV>::bytes;
-    e = cudaFuncSetAttribute(k_delta_grad_rev<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev);
+    e = cudaFuncSetAttribute(k_delta_grad_rev<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_delta_grad_dqk<D, DV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dqk);
+        e = cudaFuncSetAttribute(k_delta_grad_dqk<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dqk);
     if (e != cudaSuccess)
         return e;
-    const T* q = static_cast<const T*>(a.q);
-    const T* k = static_cast<const T*>(a.k);
-    const T* dout = static_cast<const T*>(a.dout);
+    const float* q = static_cast<const float*>(a.q);
+    const float* k = static_cast<const float*>(a.k);
+    const float* dout = static_cast<const float*>(a.dout);
     const int l2 = a.fm == LA_FM_L2, H = (int)a.H, Hk = (int)a.Hk;
     const int64_t BH = a.B * a.H;
     Segments seg = {1, 0, 0, nullptr, 0, nullptr, nullptr};
     const int n = rec_segments(a, &seg.len);
     auto reverse = [&](const Segments& x) {
-        k_delta_grad_rev<D, T><<<dim3((unsigned)(BH * x.count), DV / 32), kRevThreads, rev, a.stream>>>(
+        k_delta_grad_rev<D><<<dim3((unsigned)(BH * x.count), DV / 32), kRevThreads, rev, a.stream>>>(
             q, k, a.beta, a.log_alpha, dout, a.dS_out, f32(l.chk), f32(l.err),
-            static_cast<T*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale, x);
+            static_cast<float*>(a.dv_), a.dS0, kept, a.N, H, Hk, DV, l2, a.scale, x);
         count_launches(1);
         return cudaGetLastError();
     };
@@ -1097,7 +1098,7 @@ cudaError_t run_grad(const DeltaArgs& a)
     }
     if ((e = reverse(seg)) != cudaSuccess)
         return e;
-    k_delta_grad_dqk<D, DV, T><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
+    k_delta_grad_dqk<D, DV><<<(unsigned)(BH * rec_blocks(a.N)), kGradThreads, dqk, a.stream>>>(
         q, k, a.beta, a.log_alpha, dout, f32(l.chk), f32(l.err), kept, f32(l.dq), f32(l.dk), a.dbeta,
         a.dlog_alpha, a.N, H, Hk, l2, a.scale);
     count_launches(1);
@@ -1106,9 +1107,9 @@ cudaError_t run_grad(const DeltaArgs& a)
         return e;
     const int64_t rows = a.B * a.Hk * a.N;
     const unsigned grid = (unsigned)((rows + 7) / 8);
-    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(f32(l.dq), q, static_cast<T*>(a.dq), rows, a.N, H, Hk, l2,
+    k_delta_finish<D><<<grid, 256, 0, a.stream>>>(f32(l.dq), q, static_cast<float*>(a.dq), rows, a.N, H, Hk, l2,
                                                      a.scale);
-    k_delta_finish<D, T><<<grid, 256, 0, a.stream>>>(f32(l.dk), k, static_cast<T*>(a.dk), rows, a.N, H, Hk, l2,
+    k_delta_finish<D><<<grid, 256, 0, a.stream>>>(f32(l.dk), k, static_cast<float*>(a.dk), rows, a.N, H, Hk, l2,
                                                      1.0f);
     count_launches(2);
     return cudaGetLastError();
@@ -1118,9 +1119,9 @@ template <int D>
 cudaError_t grad_dims(const DeltaArgs& a)
 {
     switch (a.dv) {
-    case 32: return run_grad<D, 32, float>(a);
-    case 64: return run_grad<D, 64, float>(a);
-    default: return run_grad<D, 128, float>(a);
+    case 32: return run_grad<D, 32>(a);
+    case 64: return run_grad<D, 64>(a);
+    default: return run_grad<D, 128>(a);
     }
 }
 

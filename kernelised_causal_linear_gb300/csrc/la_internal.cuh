@@ -162,7 +162,6 @@ struct DeltaArgs {
     int d, dv, fm, dtype;
     float scale;
     void* ws;
-    size_t ws_bytes;
     int* status;             // device status word
     cudaStream_t stream;
     // gradients (la_backward_delta)
