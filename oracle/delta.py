@@ -17,6 +17,12 @@ import numpy as np
 EPS_L2 = 1e-6
 
 
+def _bf16(x):
+    """The nearest numbers of eight bits."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256), e - 8)
+
+
 def _rows(x, H, l2):
     """Per value head, and the lengths divided by."""
     x = np.repeat(np.asarray(x, np.float64), H // x.shape[1], axis=1)
@@ -34,6 +40,8 @@ def _decays(log_alpha, beta):
 
 
 def _token(S, k, v, b, a, plant=None):
+    if plant == "bf16_state":
+        S = _bf16(S)
     Sd = S * a[..., None, None]
     seen = S if plant == "undecayed_error" else Sd
     e = v - np.einsum("bhij,bhi->bhj", seen, k)
@@ -54,7 +62,7 @@ def forward(q, k, v, beta, log_alpha=None, *, scale, l2=True, S0=None, plant=Non
     for t in range(v.shape[2]):
         before = S
         _, e, S = _token(S, k[:, :, t], v[:, :, t], beta[:, :, t], a[:, :, t], plant)
-        read = before if plant == "read_before_write" else S
+        read = before if plant == "read_before_write" else _bf16(S) if plant == "bf16_read" else S
         out[:, :, t] = np.einsum("bhij,bhi->bhj", read, q[:, :, t])
         if magnitude:
             u = np.abs(beta[:, :, t, None] * e)
@@ -75,7 +83,8 @@ def backward(dout, q, k, v, beta, log_alpha=None, *, scale, l2=True, S0=None, dS
     S = _start(S0, v, d)
     kept = []
     for t in range(N):
-        Sd, e, S = _token(S, k[:, :, t], v[:, :, t], beta[:, :, t], a[:, :, t])
+        Sd, e, S = _token(S, k[:, :, t], v[:, :, t], beta[:, :, t], a[:, :, t],
+                          plant if plant == "bf16_state" else None)
         kept.append((Sd, e, S))
     dS = np.zeros((B, H, d, v.shape[-1])) if dS_out is None else np.array(dS_out, np.float64)
     dq, dk, dv, db, dg = (np.zeros_like(x) for x in (q, k, v, beta, beta))
@@ -83,12 +92,12 @@ def backward(dout, q, k, v, beta, log_alpha=None, *, scale, l2=True, S0=None, dS
         Sd, e, St = kept[t]
         b = beta[:, :, t, None]
         do, kt = dout[:, :, t], k[:, :, t]
-        dq[:, :, t] = scale * np.einsum("bhij,bhj->bhi", St, do)
+        dq[:, :, t] = scale * np.einsum("bhij,bhj->bhi", _bf16(St) if plant == "bf16_read" else St, do)
         dS = dS + scale * np.einsum("bhi,bhj->bhij", q[:, :, t], do)
         du = np.einsum("bhij,bhi->bhj", dS, kt)
         dv[:, :, t] = b * du
         db[:, :, t] = (du * e).sum(-1)
-        dk[:, :, t] = np.einsum("bhij,bhj->bhi", dS, b * e)
+        dk[:, :, t] = np.einsum("bhij,bhj->bhi", dS, _bf16(b * e) if plant == "bf16_written" else b * e)
         if plant != "key_only_written":
             dk[:, :, t] -= np.einsum("bhij,bhj->bhi", Sd, b * du)
         dS = dS - np.einsum("bhi,bhj->bhij", kt, b * du)
