@@ -290,8 +290,8 @@ LA_API la_status la_favor_features(const void* x, const float* w, void* out, int
  *               token, each may be NULL (zero start; not wanted), and they may
  *               be the same buffer.  out and q may be NULL together for a
  *               state-only call, which needs S_out.
- * Inputs are finite: a NaN or infinity may reach the outputs of the 63 tokens
- * before its own, and every later one.  Workspace:
+ * Inputs are finite, those of padding too: a NaN or infinity may reach the
+ * outputs of the 63 tokens before its own, and every later one.  Workspace:
  * la_delta_workspace_size() bytes, 256-byte aligned (it may be 0, then the
  * workspace may be NULL).  N = 0 copies S0 (or zero) to S_out.
  */

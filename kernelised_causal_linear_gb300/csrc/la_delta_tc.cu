@@ -114,11 +114,11 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // Decays of
 // off-diagonal blocks are a row's factor to the column block's end times a column's
 // from there, both at most 1, so only diagonal blocks take an exponential per element.
-// Measured: 98 us for the 4096 chunks of B4 H8 N8192 d=128, 345 us for 16384 (two
-// value heads per key head).  By counters on 16 x 32 heads of 512 tokens 40% of the
-// issue slots are used, DRAM moves 3.2 TB/s and the tensor cores are 18% busy: short
-// stretches between barriers, with four blocks per SM.  (On the CUDA cores the
-// off-diagonal blocks alone were a quarter of it.)
+// Measured: 101 us for the 4096 chunks of B4 H8 N8192 d=128 (107 us for a gradient),
+// 347 us for 16384 (two value heads per key head).  By counters on 16 x 32 heads of 512
+// tokens 43% of the issue slots are used, DRAM moves 2 TB/s and the tensor cores are
+// 19% busy: short stretches between barriers, with four blocks per SM.  (On the CUDA
+// cores the off-diagonal blocks alone were a quarter of it.)
 constexpr int kPrepThreads = 128;
 
 template <int D, bool GRAD>
@@ -608,11 +608,11 @@ __global__ void __launch_bounds__(kPrepThreads)
 // memory three times a chunk.  A warp's products follow one another, each waiting
 // for the last: with a slice per warp a chunk was 7100 cycles at d = 128 of which
 // the tensor core works 3100, so two warps shorten it where there are SMs to spare.
-// Measured: 277 us for the 128 chunks of B4 H8 N8192 d=128 (SP = 2: 4300 cycles per
-// chunk, tensor cores 36% busy on an SM, bound by the latency of its dependent
-// products and conversions), 629 us for B16 H32 N2011 (SP = 1: three rounds of 152
-// CTAs, 509 us, the rest with SP = 2, 120 us; by counters at N = 512, all in one launch,
-// the busiest SM's tensor cores work 57% of the time).
+// Measured: 283 us for the 128 chunks of B4 H8 N8192 d=128 (SP = 2: 4300 cycles per
+// chunk, tensor cores 38% busy on an SM, bound by the latency of its dependent
+// products and conversions), 639 us for B16 H32 N2011 (SP = 1: three rounds of 152
+// CTAs, 518 us, the rest with SP = 2, 121 us; by counters at N = 512 the tensor cores
+// work 58% of the first part's time).  The chain of a gradient 340 us.
 //
 // With two warps on a sub-partition (SP = 1, eight warps) no barrier spans the CTA
 // inside the loop: the warp that is last to finish with a stage asks for the chunk
@@ -676,9 +676,10 @@ __device__ __forceinline__ void keep_parts(unsigned char* p, int64_t plane, int6
 }
 
 // The ring of stages: barriers for filled and for read, and how many warps have read
-// (STEP: a barrier of the CTA in their place).  A warp's reads are ordered before the refill by its arrival and the refiller's
-// (satisfied) wait on the same barrier; the count only tells who is last.  A fence
-// instead would also wait for the chunk's stores to global memory.
+// (STEP: a barrier of the CTA in their place).  A warp's reads are ordered before the
+// refill by its arrival and the refiller's (satisfied) wait on the same barrier; the
+// count only tells who is last.  A fence instead would also wait for the chunk's stores
+// to global memory.
 template <int STAGES, bool STEP>
 struct Ring {
     uint64_t *full, *read;
@@ -1406,8 +1407,8 @@ __global__ void __launch_bounds__(256)
 // segment is the transpose of the M that the states' run gave.  ENDS: a run from
 // dS = 0 that leaves each segment's constant part in seg.B and nothing else.
 //
-// Measured: 485 us at B4 H8 N8192 d=128 (7600 cycles per chunk; 1.7 times the
-// forward chain's instructions), 306 to 332 us at B8 H32 N1037; bound like the chain.
+// Measured: 540 us at B4 H8 N8192 d=128 (8100 cycles per chunk; 1.9 times the
+// forward chain's instructions), 330 us at B8 H32 N1037; bound like the chain.
 template <int D, int SP>
 struct RevSmem {
     static constexpr int stages = 2;
@@ -1928,13 +1929,13 @@ __global__ void __launch_bounds__(256, 1)
 //   dK_j = sum_{i>=j} D_ij (dO_i.U_j) q_i - sum_{i>j} D_ij (dV_i.U_j) k_i
 //          - sum_{i<j} D_ji (dV_j.U_i) k_i - e^{G_j} S0 dV_j + e^{G_C-G_j} dS1 U_j
 //
-// then through scale and norm to the inputs.  Two warps own 16 tokens of dQ or
-// of dK, each half of the d columns and of the token tiles.  The kept planes arrive with a scale per value column,
-// the contracted index here; they are brought under one scale each (E and dV: one for
-// 16 tokens) in shared memory (a power of two: exact but for columns under 2^-24 of the
-// largest), so that fragments go from ldmatrix into the MMA as they are and every factor is
-// one of a row, applied to fp32 accumulators.  The 64 x 64 matrices pass through a
-// tile of the two warps' own as fp16 rows, each half under a power of two.  One fp16 part
+// then through scale and norm to the inputs.  Two warps own 16 tokens of dQ or of
+// dK, each half of the d columns and of the token tiles.  The kept planes arrive with a
+// scale per value column, the contracted index here; they are brought under one scale
+// each (E and dV: one for 16 tokens) in shared memory (a power of two: exact but for
+// columns under 2^-24 of the largest), so that fragments go from ldmatrix into the MMA
+// as they are and every factor is one of a row, applied to fp32 accumulators.  The
+// 64 x 64 matrices pass through a tile of the two warps' own as fp16 rows, each half under a power of two.  One fp16 part
 // throughout: 2^-12 of a term, a sixteenth of the bf16 rounding of the results.  (A result
 // that cancels to less than a sixteenth of its terms shows it: one token, one key head
 // and value heads whose gradients happen to oppose.)
@@ -2788,14 +2789,14 @@ int chunks_of(int64_t N) { return (int)((N + kC - 1) / kC); }
 
 // Segments of a sequence.  Two runs over a segment and a walk over their ends take
 // the place of one run over the whole, worth it from three segments on (forward and
-// gradient, B1 H12 N4096 d = 128: 156 and 500 us whole, 142 and 389 us in three; B1 H16
-// in two: 160 and 523 against 165 and 510 us); no more than give each warp of the
+// gradient, B1 H12 N4096 d = 128: 165 and 573 us whole, 153 and 450 us in three; B1 H16
+// in two: 169 and 602 against 176 and 578 us); no more than give each warp of the
 // second run a sub-partition of its own at 152 SMs, and no more than 32: the walk is
 // serial, 0.7 us a step at d = 64, 1.9 us at 128.  So a segment is at least four chunks
-// at d = 128 and two below (B1 H4: N1000 d = 128 44 and 123 us in segments of eight
-// chunks, 39 and 90 us of four, 44 and 89 us of two; N700 d = 64 29 and 76 us whole, 27
-// and 60 us of two or three; under eight chunks whole: N400 22 and 57 us, 26 and 58 us
-// in three).  By sizes alone, so that workspaces can be sized without the GPU.
+// at d = 128 and two below (calls; B1 H4: N1000 d = 128 59 and 155 us in segments of
+// eight chunks, 48 and 121 us of four, 54 and 120 us of two; N700 d = 64 34 and 98 us
+// whole, 37 and 88 us of two or three; under eight chunks whole: N400 27 and 77 us, 36
+// and 85 us in three).  By sizes alone, so that workspaces can be sized without the GPU.
 int segments_of(const DeltaArgs& a)
 {
     const int64_t slices = a.B * a.H * (a.dv / 16), most = chunks_of(a.N) / (a.d > 64 ? 4 : 2);
@@ -2880,8 +2881,8 @@ GradTcLayout grad_tc_layout(const DeltaArgs& a)
 // d = 128: 32 heads of 8192 tokens 468 us with one warp per slice, 304 us with two;
 // 512 heads of 2011 tokens 736 us with one, 886 us with two.  Two also where a head has
 // two slices, which would be two warps on an SM (dv = 32, forward and gradient, one and
-// two: 256 heads of 1024 tokens d = 128 204 and 702, 175 and 588 us; 512 of d = 64 303
-// and 1016, 283 and 942 us; not at d = 32, 240 and 742, 199 and 854 us).
+// two: 256 heads of 1024 tokens d = 128 213 and 813, 184 and 699 us; 512 of d = 64 317
+// and 1227, 295 and 1090 us; not at d = 32, 272 and 923, 229 and 979 us).
 struct Cut {
     int SP, W;
 };
@@ -2900,10 +2901,10 @@ Cut cut_of(int64_t runs, int columns, int d)  // sequences or segments, value co
 
 // The runs of the last round of CTAs, where they are few enough for two CTAs each:
 // two warps per slice then end sooner than one would.  Forward and gradient, in one
-// launch and in two (us): B5 H32 N1024 d = 128 241 and 812, 219 and 752; B16 H32 N2011
-// 1052 and 3834, 1004 and 3713; B14 H16 N1024 64 x 128 190 and 705, 185 and 676.  Not
+// launch and in two (us): B5 H32 N1024 d = 128 248 and 922, 229 and 865; B16 H32 N2011
+// 1070 and 4325, 1027 and 4265; B14 H16 N1024 64 x 128 201 and 839, 195 and 809.  Not
 // for smaller states: B20 H16 N1024 64 x 64 214 and 754, 215 and 766; B10 H16 32 x 32
-// 103 and 271, 101 and 348.
+// 103 and 271, 101 and 348 (these four before the gates had a kernel of their own).
 int64_t tail_of(const Cut& cut, int64_t runs, int columns, int d)
 {
     const int sms = device_sm_count();

@@ -10,7 +10,7 @@
 // transposition costs no pass of its own.  A row is dv / 8 lanes of eight
 // elements (16 bytes of bf16): its sums are shuffles, and each tensor is read
 // or written once.  Bound by HBM: 67 M fp32 elements with a bf16 gate 84 us (6.4
-// TB/s), 33.5 M bf16 elements 36 us (5.5 TB/s) and their gradient 62 us (5.4 TB/s).
+// TB/s), 33.5 M bf16 elements 37 us (5.4 TB/s) and their gradient 63 us (5.4 TB/s).
 #include "la_internal.cuh"
 
 namespace la {
