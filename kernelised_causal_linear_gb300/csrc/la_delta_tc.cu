@@ -111,9 +111,9 @@ constexpr int row_image()  // bytes of K16 or Q16 per chunk
 // chunk, with 2^10 to spare over the largest |A|; what grows past that, in a recurrence
 // that is not stable, takes a power of two of its own per block, and at the end one per
 // 16 rows and one per 16 columns (growth over i - j tokens is a product of the two).
-// Decays of
-// off-diagonal blocks are a row's factor to the column block's end times a column's
-// from there, both at most 1, so only diagonal blocks take an exponential per element.
+// Decays of off-diagonal blocks are a row's factor to the column block's end times a
+// column's from there, both at most 1, so only diagonal blocks take an exponential per
+// element.
 // Measured: 101 us for the 4096 chunks of B4 H8 N8192 d=128 (107 us for a gradient),
 // 347 us for 16384 (two value heads per key head).  By counters on 16 x 32 heads of 512
 // tokens 43% of the issue slots are used, DRAM moves 2 TB/s and the tensor cores are
