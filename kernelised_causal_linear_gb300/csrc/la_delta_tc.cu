@@ -47,9 +47,9 @@ using namespace delta;
 // gradients][factors], tiles of 64 x 64 fp16 in the layout the chains read them
 // from shared memory.  k^_i = fk_i K16_i and scale q^_i = fq_i Q16_i are the mapped
 // rows, fk and fq holding the image's power of two, the L2 norm and the scale.  p_i is
-// the power of two under |k^_i| (1 with LA_FM_L2): F's image is F_ij / (p_i p_j r_i c_j)
-// with powers of two r and c of 16 tokens each (r one for the chunk and c = 1 in a stable
-// recurrence).
+// the power of two under |k^_i| (1 with LA_FM_L2): a gradient's P is P_ij / p_j (else P_ij
+// beta_j), F's image F_ij / (p_i p_j r_i c_j) with powers of two r and c of 16 tokens each
+// (r one for the chunk and c = 1 in a stable recurrence).
 enum Factor {
     kFacA,    // e^{G_i} fk_i
     kFacF,    // p_i r_i
@@ -128,7 +128,7 @@ struct PrepSmem {
     static constexpr int vec = diag + 4 * 2 * 16 * 20 * 4;
     // arrays beside the factors.  With four blocks on an SM a gradient stays under 196 KB
     // of shared memory, which leaves L1 twice of what more would (108 against 116 us)
-    static constexpr int own = GRAD ? 6 : 9;
+    static constexpr int own = GRAD ? 4 : 9;
     static constexpr int bytes = vec + (own + n_factors<GRAD>()) * kC * 4 + 64;
 };
 
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kPrepThreads)
     float *fk = vec, *fq = vec + kC;  // fk: in units of p
     float* ck = vec + 2 * kC;         // fk_j times the decay from j to its block's end
     float* bp = vec + 3 * kC;         // beta p^2
-    float *pk = vec + 4 * kC, *pck = vec + 5 * kC;  // fk and ck of P's columns: times p beta (gradients: p)
+    // fk and ck of P's columns: times p beta; a gradient's P stays in units of p as F does
+    float *pk = GRAD ? fk : vec + 4 * kC, *pck = GRAD ? ck : vec + 5 * kC;
     float* fac = vec + SM::own * kC;  // [factors][kC]
     float *gh = GRAD ? fac + kFacGh * kC : vec + 6 * kC, *gl = GRAD ? fac + kFacGl * kC : vec + 7 * kC;
     float *pw = GRAD ? fac + kFacPk * kC : vec + 8 * kC, *sb = fac + kFacB * kC;
@@ -288,9 +289,10 @@ __global__ void __launch_bounds__(kPrepThreads)
         pw[tid] = p;
         fk[tid] = f * __uint_as_float((uint32_t)(127 - x) << 23);
         bp[tid] = sb[tid] * p * p;
-        const float to = exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l)), fp = GRAD ? f : f * sb[tid];
+        const float to = exp2f((gh[tid | 15] - h) + (gl[tid | 15] - l));
         ck[tid] = fk[tid] * to;
-        pk[tid] = fp, pck[tid] = fp * to;
+        if (!GRAD)
+            pk[tid] = f * sb[tid], pck[tid] = f * sb[tid] * to;
         fac[kFacA * kC + tid] = e * f;
         fac[kFacZ * kC + tid] = sb[tid] * p;
         fac[kFacO * kC + tid] = e * fq[tid];
@@ -1714,6 +1716,7 @@ __global__ void __launch_bounds__(256, 1)
             }
             if (L_LATE)
                 set_rows(us[i], row_a(u[i]), row_b(u[i]));
+            scale_cols(x[i], fac2(fac, kFacPk, sh.tile(i >> 1), i & 1, tq));
             set_rows(u[i], fma2(row_a(x[i]), both(q0.from), row_a(u[i])), fma2(row_b(x[i]), both(q1.from), row_b(u[i])));
         }
         if (SP > 1) {

@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+from delta_bounds import excess, within
 from gpu_util import to_np
 from oracle import delta
 
@@ -128,3 +129,19 @@ def test_one_token_writes_far_too_strongly(at, dtype):
     p = problem(100, torch.ones(1, 2, 100), 1.0, 6 + at, dtype)
     p["beta"][:, :, at] *= 1e4
     beyond(p)
+
+
+@pytest.mark.parametrize("N,d,dv", [(64, 128, 128), (129, 32, 32), (200, 64, 64)])
+def test_keys_of_six_orders_of_magnitude(N, d, dv):
+    """Lengths spread over 1 .. 1e-6: dv is fp32 until its rounding (delta_bounds), dbeta and S stay fp32."""
+    g = torch.Generator().manual_seed(N)
+    p = problem(N, torch.exp(-14 * torch.rand(1, 2, N, generator=g)), 1.9, N + 2, BF, d, dv, gated=False)
+    h = lambda n: None if p[n] is None else to_np(p[n])  # noqa: E731
+    args = [p[n] for n in INPUTS]
+    got = la.la_backward_delta(p["dout"], *args, feature_map="none")
+    ref = delta.backward(h("dout"), *map(h, INPUTS), scale=d ** -0.5, l2=False)
+    print(f"dv {excess(to_np(got[2]), ref[2]):.2f} parts, dbeta {errors(got[3], ref[3])[0]:.2e}")
+    assert within("dv", to_np(got[2]), ref[2])
+    assert errors(got[3], ref[3])[0] <= 1e-5
+    S = la.la_forward_delta(*args, feature_map="none", return_state=True)[1]
+    assert errors(S, delta.forward(*map(h, INPUTS), scale=d ** -0.5, l2=False)[1])[0] <= 1e-5
