@@ -1409,8 +1409,8 @@ __global__ void __launch_bounds__(256)
 // segment is the transpose of the M that the states' run gave.  ENDS: a run from
 // dS = 0 that leaves each segment's constant part in seg.B and nothing else.
 //
-// Measured: 540 us at B4 H8 N8192 d=128 (8100 cycles per chunk; 1.9 times the
-// forward chain's instructions), 330 us at B8 H32 N1037; bound like the chain.
+// Measured: 535 us at B4 H8 N8192 d=128 (8100 cycles per chunk; 1.9 times the
+// forward chain's instructions), 340 us at B8 H32 N1037; bound like the chain.
 template <int D, int SP>
 struct RevSmem {
     static constexpr int stages = 2;
