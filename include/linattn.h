@@ -365,6 +365,122 @@ LA_API la_status la_norm_gate_backward(const void* dy, const void* x, const void
                                        la_stream_t stream);
 
 /*
+ * The calls from here to la_backward_ssm work on token-major rows of C channels.
+ * Inputs marked "strided" have neighbouring channels next to one another and any
+ * strides >= 0 (in elements) from token to token and from batch row to batch row,
+ * e.g. a slice of a projection, and need only their type's alignment (16-byte
+ * rows are the fast path).  Everything else is contiguous and 16-byte aligned.
+ * No output may overlap an input or another output, but for S_out in the place
+ * of S0 where that is said.
+ *   lengths : int32 [B] on the device, or NULL for N everywhere.  Row b ends after
+ *             lengths[b] tokens (clamped to 0 .. N): the final state is the one
+ *             there, tokens behind are not read, and outputs and gradients
+ *             behind are zero.
+ *
+ * Short causal convolution, one filter of W taps (2, 3 or 4) per channel:
+ *     y_t = act(bias + sum_j weight[c,j] x_{t-W+1+j})
+ *   x         : [B,N,C] strided (x_batch, x_token), in dtype
+ *   weight    : fp32 [C,W], the last tap is the token's own.  bias: fp32 [C] or NULL.
+ *   y         : [B,H,N,C/H] in dtype: head-major for the attention calls, or
+ *               token-major with H = 1.  H divides C.
+ *   S0, S_out : [B,W-1,C] in dtype, the last W - 1 inputs before the first token,
+ *               oldest first, and after the last; each may be NULL (zeros; not
+ *               wanted), and they may be the same buffer.
+ *   activation: la_activation, of the sum itself (LA_ACT_NONE: the sum).
+ * N = 0 copies S0 (or zeros) to S_out.
+ */
+LA_API la_status la_forward_conv(const void* x, int64_t x_batch, int64_t x_token,
+                                 const float* weight, const float* bias, void* y, const void* S0,
+                                 void* S_out, const int32_t* lengths, int64_t B, int64_t N,
+                                 int64_t C, int64_t H, int W, int activation, int dtype,
+                                 la_stream_t stream);
+
+/*
+ * One token of the convolution: y [B,C] from the window S [B,W-1,C] (dtype,
+ * moved on by one token in place) and x, B rows of C channels x_batch apart.
+ */
+LA_API la_status la_decode_step_conv(void* S, const void* x, int64_t x_batch, const float* weight,
+                                     const float* bias, void* y, int64_t B, int64_t C, int W,
+                                     int activation, int dtype, la_stream_t stream);
+
+/*
+ * Gradients of la_forward_conv from dy (as y) and dS_out [B,W-1,C] (dtype, NULL
+ * for zero): dx [B,N,C] contiguous in dtype, dweight fp32 [C,W], dbias fp32 [C]
+ * (NULL exactly when bias is), dS0 [B,W-1,C] in dtype or NULL.  dweight and dbias
+ * are summed in fp32 in a fixed order.  Workspace: 256-byte aligned,
+ * la_conv_backward_workspace_size() bytes.  With N = 0, dweight and dbias are zero
+ * and dS0 receives dS_out (or zero).
+ */
+LA_API size_t la_conv_backward_workspace_size(int64_t B, int64_t N, int64_t C, int W, int dtype);
+LA_API la_status la_backward_conv(const void* dy, const void* dS_out, const void* x,
+                                  int64_t x_batch, int64_t x_token, const float* weight,
+                                  const float* bias, const void* S0, const int32_t* lengths,
+                                  void* dx, float* dweight, float* dbias, void* dS0, int64_t B,
+                                  int64_t N, int64_t C, int64_t H, int W, int activation,
+                                  int dtype, void* workspace, size_t workspace_bytes,
+                                  la_stream_t stream);
+
+/*
+ * Selective state-space scan ["Linear Attention and SSM", Mamba]: C channels with n
+ * states each (n in {8, 16, 32, 64}), decays and inputs of every token its own,
+ *     dt_t = softplus(delta_t + delta_bias)      (softplus = 0: delta_t + delta_bias)
+ *     S_t = exp(dt_t A) S_{t-1} + dt_t x_t Bm_t,  S [C,n]
+ *     out_t = (sum_s Cm_t S_t + D x_t) z_t sigmoid(z_t)
+ *   x, delta, z : [B,N,C] strided, in dtype; z may be NULL (no gate)
+ *   Bm, Cm      : [B,N,G,n] strided over tokens and rows, in dtype; the C / G channels
+ *                 of a group share them.  G divides C.
+ *   A           : fp32 [C,n] <= 0.  D, delta_bias: fp32 [C] or NULL.
+ *   out         : [B,N,C] in dtype
+ *   S0, S_out   : fp32 [B,C,n] state before the first token and after the last, each
+ *                 may be NULL (zero start; not wanted), and they may be the same buffer
+ *   strides     : HOST pointer to the pairs (batch, token) of x, delta, Bm, Cm and z,
+ *                 10 numbers, read during the call, or NULL for contiguous inputs
+ * Inputs are finite.  dt may be zero (the token leaves the state as it was) and, where
+ * A dt stays <= 0, negative.  Workspace: la_ssm_workspace_size() bytes, 256-byte aligned (it may be
+ * 0, then the workspace may be NULL).  N = 0 copies S0 (or zero) to S_out.
+ */
+LA_API size_t la_ssm_workspace_size(int64_t B, int64_t N, int64_t C, int64_t G, int n, int dtype);
+LA_API la_status la_forward_ssm(const void* x, const void* delta, const float* A, const void* Bm,
+                                const void* Cm, const float* D, const void* z,
+                                const float* delta_bias, void* out, const float* S0, float* S_out,
+                                const int32_t* lengths, const int64_t* strides, int64_t B,
+                                int64_t N, int64_t C, int64_t G, int n, int softplus, int dtype,
+                                void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
+ * One token of the scan for B rows: S [B,C,n] (fp32) is updated in place; x, delta, z
+ * [B,C], Bm, Cm [B,G,n], out [B,C].  strides: HOST pointer to the 5 strides from row to
+ * row of x, delta, Bm, Cm and z, or NULL for contiguous inputs.
+ */
+LA_API la_status la_decode_step_ssm(float* S, const void* x, const void* delta, const float* A,
+                                    const void* Bm, const void* Cm, const float* D, const void* z,
+                                    const float* delta_bias, void* out, const int64_t* strides,
+                                    int64_t B, int64_t C, int64_t G, int n, int softplus,
+                                    int dtype, la_stream_t stream);
+
+/*
+ * Gradients of la_forward_ssm from dout [B,N,C] (strided, dtype) and dS_out [B,C,n]
+ * (fp32, NULL for zero); the inputs are the forward's, and nothing else is kept from it.
+ * Written, contiguous: dx, ddelta, dz [B,N,C] and dBm, dCm [B,N,G,n] in dtype (the
+ * channels of a group summed in fp32), dA [C,n], dD, ddelta_bias [C] and dS0 [B,C,n] in
+ * fp32.  dD, dz and ddelta_bias are NULL exactly when D, z and delta_bias are; dS0 may
+ * be NULL.  All sums are in a fixed order.  strides: HOST pointer to 12 numbers, the
+ * pairs of la_forward_ssm and that of dout, or NULL.  Workspace: 256-byte aligned,
+ * la_ssm_backward_workspace_size() bytes.  With N = 0 the parameters' gradients are zero
+ * and dS0 receives dS_out (or zero).
+ */
+LA_API size_t la_ssm_backward_workspace_size(int64_t B, int64_t N, int64_t C, int64_t G, int n,
+                                             int dtype);
+LA_API la_status la_backward_ssm(const void* dout, const float* dS_out, const void* x,
+                                 const void* delta, const float* A, const void* Bm, const void* Cm,
+                                 const float* D, const void* z, const float* delta_bias,
+                                 const float* S0, const int32_t* lengths, void* dx, void* ddelta,
+                                 float* dA, void* dBm, void* dCm, float* dD, void* dz,
+                                 float* ddelta_bias, float* dS0, const int64_t* strides, int64_t B,
+                                 int64_t N, int64_t C, int64_t G, int n, int softplus, int dtype,
+                                 void* workspace, size_t workspace_bytes, la_stream_t stream);
+
+/*
  * la_forward without a workspace argument, for callers that cannot allocate
  * device memory (the pages have no counterpart: this is a deployment
  * convenience).  Typical such callers are a plugin running inside a host

@@ -18,6 +18,9 @@ _EXPORTS = {
     "la_forward_delta", "la_decode_step_delta", "la_backward_delta", "la_delta_workspace_size",
     "la_delta_backward_workspace_size", "la_norm_gate", "la_norm_gate_backward",
     "la_norm_gate_backward_workspace_size",
+    "la_forward_conv", "la_decode_step_conv", "la_backward_conv", "la_conv_backward_workspace_size",
+    "la_forward_ssm", "la_decode_step_ssm", "la_backward_ssm", "la_ssm_workspace_size",
+    "la_ssm_backward_workspace_size",
 }
 
 

@@ -86,6 +86,25 @@ _lib.la_norm_gate_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i]
 _lib.la_norm_gate_backward.restype = _i
 _lib.la_norm_gate_backward.argtypes = [_vp] * 7 + [_i64] * 3 + [_i, _i, _i, _f, _i, _i, _vp, _sz,
                                                                _vp]
+_lib.la_forward_conv.restype = _i
+_lib.la_forward_conv.argtypes = [_vp, _i64, _i64] + [_vp] * 6 + [_i64] * 4 + [_i, _i, _i, _vp]
+_lib.la_decode_step_conv.restype = _i
+_lib.la_decode_step_conv.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _vp]
+_lib.la_conv_backward_workspace_size.restype = _sz
+_lib.la_conv_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i, _i]
+_lib.la_backward_conv.restype = _i
+_lib.la_backward_conv.argtypes = [_vp, _vp, _vp, _i64, _i64] + [_vp] * 8 + [_i64] * 4 + [_i, _i, _i, _vp, _sz, _vp]
+_strides = ctypes.POINTER(ctypes.c_int64)
+_lib.la_ssm_workspace_size.restype = _sz
+_lib.la_ssm_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i, _i]
+_lib.la_forward_ssm.restype = _i
+_lib.la_forward_ssm.argtypes = [_vp] * 12 + [_strides] + [_i64] * 4 + [_i, _i, _i, _vp, _sz, _vp]
+_lib.la_decode_step_ssm.restype = _i
+_lib.la_decode_step_ssm.argtypes = [_vp] * 10 + [_strides] + [_i64] * 3 + [_i, _i, _i, _vp]
+_lib.la_ssm_backward_workspace_size.restype = _sz
+_lib.la_ssm_backward_workspace_size.argtypes = [_i64, _i64, _i64, _i64, _i, _i]
+_lib.la_backward_ssm.restype = _i
+_lib.la_backward_ssm.argtypes = [_vp] * 21 + [_strides] + [_i64] * 4 + [_i, _i, _i, _vp, _sz, _vp]
 _lib.la_forward_noalloc.restype = _i
 _lib.la_forward_noalloc.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i, _i, _i, _i, _fp,
                                     _i, _vp]
@@ -596,6 +615,247 @@ def la_norm_gate_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor 
                                       B, H, N, dv, _act(activation), heads, float(eps), _dtype(x),
                                       _dtype(dy), *ws, call.handle)
     _check(code, "la_norm_gate_backward")
+    return grads
+
+
+def _rows(t: torch.Tensor | None, name: str, shape, dtype, index: int):
+    """Pointer and row strides of an input whose last dimensions (channels, or groups
+    and states) are neighbours and whose first ones, (batch,) or (batch, token), have
+    any strides."""
+    if t is None:
+        return (None,) + (0,) * (2 if shape[1] is not None else 1)
+    lead = 1 if shape[1] is None else 2
+    shape = tuple(n for n in shape if n is not None)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
+    strides, width = t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and strides[i] != width:
+            raise ValueError(f"{name}'s channels must be next to one another")
+        width *= shape[i]
+    # the stride of a dimension of one says nothing
+    return (t.data_ptr(),) + tuple(0 if shape[i] == 1 else strides[i] for i in range(lead))
+
+
+def _lengths(t, B, index):
+    return _arg(t, "lengths", (B,), torch.int32, index)
+
+
+def la_conv_backward_workspace_size(B, N, C, W, dtype=torch.bfloat16) -> int:
+    return int(_lib.la_conv_backward_workspace_size(B, N, C, W, DTYPES[dtype]))
+
+
+def _filter(weight, bias, C, dev):
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C,W]")
+    W = weight.shape[1]
+    return _arg(weight, "weight", (C, W), torch.float32, dev), _arg(bias, "bias", (C,), torch.float32, dev), W
+
+
+def la_forward_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                    y: torch.Tensor | None = None, *, activation="silu", heads: int | None = None,
+                    S0: torch.Tensor | None = None, S_out: torch.Tensor | None = None,
+                    return_state: bool = False, lengths: torch.Tensor | None = None, stream=None):
+    """Short causal convolution of x [B,N,C] (bf16 or fp32, any batch and token
+    strides) with weight [C,W] and bias [C] (fp32) -> (y, S_out).
+
+    y is token-major [B,N,C], or head-major [B,heads,N,C/heads] for the attention
+    calls.  S0 [B,W-1,C] holds the inputs before the first token (None: zeros); the
+    last W-1 inputs are written when S_out is given (it may be S0) or return_state is
+    set.  lengths (int32 [B]): row b ends after lengths[b] tokens, y is zero behind."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B,N,C]")
+    dev = _current(x, "x")
+    B, N, C = x.shape
+    if heads is not None and (heads < 1 or C % heads):
+        raise ValueError(f"heads must divide the {C} channels")
+    call = _Call(stream, dev)
+    shape = (B, N, C) if heads is None else (B, heads, N, C // heads)
+    if y is None:
+        y = call.empty(shape, x.dtype)
+    w, b, W = _filter(weight, bias, C, dev)
+    window = (B, W - 1, C)
+    if S_out is None and return_state:
+        S_out = call.empty(window, x.dtype)
+    xs = _rows(x, "x", (B, N, C), x.dtype, dev)
+    yp = _arg(y, "y", shape, x.dtype, dev)
+    _apart("y", yp, xs[0])
+    code = _lib.la_forward_conv(*xs, w, b, yp, _arg(S0, "S0", window, x.dtype, dev),
+                                _arg(S_out, "S_out", window, x.dtype, dev), _lengths(lengths, B, dev),
+                                B, N, C, heads or 1, W, _act(activation), _dtype(x), call.handle)
+    _check(code, "la_forward_conv")
+    return y, S_out
+
+
+def la_decode_step_conv(S: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                        bias: torch.Tensor | None = None, y: torch.Tensor | None = None, *,
+                        activation="silu", stream=None) -> torch.Tensor:
+    """One token per sequence: x [B,C] (any row stride); the window S [B,W-1,C] moves on
+    in place -> y [B,C]."""
+    if x.dim() != 2:
+        raise ValueError("x must be [B,C]")
+    dev = _current(x, "x")
+    B, C = x.shape
+    call = _Call(stream, dev)
+    if y is None:
+        y = call.empty((B, C), x.dtype)
+    w, b, W = _filter(weight, bias, C, dev)
+    xs = _rows(x, "x", (B, None, C), x.dtype, dev)
+    yp = _arg(y, "y", (B, C), x.dtype, dev)
+    _apart("y", yp, xs[0])
+    code = _lib.la_decode_step_conv(_arg(S, "S", (B, W - 1, C), x.dtype, dev), *xs, w, b, yp, B, C, W,
+                                    _act(activation), _dtype(x), call.handle)
+    _check(code, "la_decode_step_conv")
+    return y
+
+
+def la_backward_conv(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                     bias: torch.Tensor | None = None, *, activation="silu",
+                     S0: torch.Tensor | None = None, dS_out: torch.Tensor | None = None,
+                     lengths: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Gradients of la_forward_conv -> (dx, dweight, dbias, dS0), with None for dbias
+    without bias and for dS0 without S0.  dy is [B,N,C], or [B,heads,N,C/heads] for a
+    head-major y; dS_out (None: zero) is the gradient of the final window."""
+    if x.dim() != 3 or dy.dim() not in (3, 4):
+        raise ValueError("x must be [B,N,C], dy [B,N,C] or [B,heads,N,C/heads]")
+    dev = _current(x, "x")
+    B, N, C = x.shape
+    heads = dy.shape[1] if dy.dim() == 4 else 1
+    if heads < 1 or C % heads:
+        raise ValueError(f"heads must divide the {C} channels")
+    call = _Call(stream, dev)
+    w, b, W = _filter(weight, bias, C, dev)
+    window, f32 = (B, W - 1, C), torch.float32
+    shape = (B, heads, N, C // heads) if dy.dim() == 4 else (B, N, C)
+    ins = (_arg(dy, "dy", shape, x.dtype, dev), _arg(dS_out, "dS_out", window, x.dtype, dev),
+           *_rows(x, "x", (B, N, C), x.dtype, dev), w, b, _arg(S0, "S0", window, x.dtype, dev),
+           _lengths(lengths, B, dev))
+    grads = (call.empty((B, N, C), x.dtype), call.empty((C, W), f32),
+             call.empty((C,), f32) if bias is not None else None,
+             call.empty(window, x.dtype) if S0 is not None else None)
+    ws = call.scratch(workspace, la_conv_backward_workspace_size(B, N, C, W, x.dtype))
+    code = _lib.la_backward_conv(*ins, *(None if g is None else g.data_ptr() for g in grads), B, N, C,
+                                 heads, W, _act(activation), _dtype(x), *ws, call.handle)
+    _check(code, "la_backward_conv")
+    return grads
+
+
+def la_ssm_workspace_size(B, N, C, G, n, dtype=torch.bfloat16) -> int:
+    return int(_lib.la_ssm_workspace_size(B, N, C, G, n, DTYPES[dtype]))
+
+
+def la_ssm_backward_workspace_size(B, N, C, G, n, dtype=torch.bfloat16) -> int:
+    return int(_lib.la_ssm_backward_workspace_size(B, N, C, G, n, DTYPES[dtype]))
+
+
+def _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, step):
+    """Sizes (B, N, C, G, n), pointers in the calls' order from x to delta_bias, strides."""
+    if x.dim() != (2 if step else 3) or Bm.dim() != x.dim() + 1:
+        raise ValueError("x must be [B,C] and Bm [B,G,n]" if step else "x must be [B,N,C] and Bm [B,N,G,n]")
+    B, N, C = (x.shape[0], None, x.shape[1]) if step else x.shape
+    G, n = Bm.shape[-2:]
+    f32, wide, shared = torch.float32, (B, N, C), (B, N, G, n)
+    rows = [_rows(x, "x", wide, x.dtype, dev), _rows(delta, "delta", wide, x.dtype, dev),
+            _rows(Bm, "Bm", shared, x.dtype, dev), _rows(Cm, "Cm", shared, x.dtype, dev),
+            _rows(z, "z", wide, x.dtype, dev)]
+    ptrs = (rows[0][0], rows[1][0], _arg(A, "A", (C, n), f32, dev), rows[2][0], rows[3][0],
+            _arg(D, "D", (C,), f32, dev), rows[4][0], _arg(delta_bias, "delta_bias", (C,), f32, dev))
+    return (B, N, C, G, n), ptrs, [s for r in rows for s in r[1:]]
+
+
+def _host_strides(strides):
+    return (ctypes.c_int64 * len(strides))(*strides)
+
+
+def la_forward_ssm(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor,
+                   Cm: torch.Tensor, out: torch.Tensor | None = None, *,
+                   D: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                   delta_bias: torch.Tensor | None = None, softplus: bool = True,
+                   S0: torch.Tensor | None = None, S_out: torch.Tensor | None = None,
+                   return_state: bool = False, lengths: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Selective state-space scan over whole sequences -> (out, S_out).
+
+    x, delta, z [B,N,C] and Bm, Cm [B,N,G,n] (bf16 or fp32, any batch and token strides),
+    A [C,n], D and delta_bias [C] fp32; out [B,N,C] in x's type:
+    S_t = exp(dt A) S_{t-1} + dt x Bm, out = (Cm S_t + D x) silu(z) with
+    dt = softplus(delta + delta_bias).  S0 [B,C,n] is the state before the first token
+    (None: zero); the final state is written when S_out is given (it may be S0) or
+    return_state is set.  lengths (int32 [B]): row b ends after lengths[b] tokens, out is
+    zero behind."""
+    dev = _current(x, "x")
+    (B, N, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, False)
+    call = _Call(stream, dev)
+    if out is None:
+        out = call.empty((B, N, C), x.dtype)
+    state = (B, C, n)
+    if S_out is None and return_state:
+        S_out = call.empty(state, torch.float32)
+    op = _arg(out, "out", (B, N, C), x.dtype, dev)
+    _apart("out", op, ptrs[0], ptrs[1], ptrs[6])
+    ws = call.scratch(workspace, la_ssm_workspace_size(B, N, C, G, n, x.dtype))
+    code = _lib.la_forward_ssm(*ptrs, op, _arg(S0, "S0", state, torch.float32, dev),
+                               _arg(S_out, "S_out", state, torch.float32, dev), _lengths(lengths, B, dev),
+                               _host_strides(strides), B, N, C, G, n, int(bool(softplus)), _dtype(x), *ws,
+                               call.handle)
+    _check(code, "la_forward_ssm")
+    return out, S_out
+
+
+def la_decode_step_ssm(S: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor,
+                       Bm: torch.Tensor, Cm: torch.Tensor, out: torch.Tensor | None = None, *,
+                       D: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                       delta_bias: torch.Tensor | None = None, softplus: bool = True,
+                       stream=None) -> torch.Tensor:
+    """One token per sequence: x, delta, z [B,C], Bm, Cm [B,G,n] (any row stride); the state
+    S [B,C,n] (fp32) is updated in place -> out [B,C] in x's type."""
+    dev = _current(x, "x")
+    (B, _, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, True)
+    call = _Call(stream, dev)
+    if out is None:
+        out = call.empty((B, C), x.dtype)
+    op = _arg(out, "out", (B, C), x.dtype, dev)
+    _apart("out", op, ptrs[0], ptrs[1], ptrs[6])
+    code = _lib.la_decode_step_ssm(_arg(S, "S", (B, C, n), torch.float32, dev), *ptrs, op,
+                                   _host_strides(strides), B, C, G, n, int(bool(softplus)), _dtype(x),
+                                   call.handle)
+    _check(code, "la_decode_step_ssm")
+    return out
+
+
+def la_backward_ssm(dout: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor,
+                    Bm: torch.Tensor, Cm: torch.Tensor, *, D: torch.Tensor | None = None,
+                    z: torch.Tensor | None = None, delta_bias: torch.Tensor | None = None,
+                    softplus: bool = True, S0: torch.Tensor | None = None,
+                    dS_out: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of la_forward_ssm -> (dx, ddelta, dA, dBm, dCm, dD, dz, ddelta_bias, dS0),
+    with None for what was not given.  dout [B,N,C] (any batch and token strides) and dS_out
+    [B,C,n] (None: zero) are the gradients of out and of the final state."""
+    dev = _current(x, "x")
+    (B, N, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, False)
+    call = _Call(stream, dev)
+    dop, *ds = _rows(dout, "dout", (B, N, C), x.dtype, dev)
+    f32, state = torch.float32, (B, C, n)
+    ins = (dop, _arg(dS_out, "dS_out", state, f32, dev), *ptrs, _arg(S0, "S0", state, f32, dev),
+           _lengths(lengths, B, dev))
+
+    def like(t, shape, dtype):
+        return call.empty(shape, dtype) if t is not None else None
+
+    grads = (call.empty((B, N, C), x.dtype), call.empty((B, N, C), x.dtype), call.empty((C, n), f32),
+             call.empty((B, N, G, n), x.dtype), call.empty((B, N, G, n), x.dtype), like(D, (C,), f32),
+             like(z, (B, N, C), x.dtype), like(delta_bias, (C,), f32), like(S0, state, f32))
+    ws = call.scratch(workspace, la_ssm_backward_workspace_size(B, N, C, G, n, x.dtype))
+    code = _lib.la_backward_ssm(*ins, *(None if g is None else g.data_ptr() for g in grads),
+                                _host_strides(strides + ds), B, N, C, G, n, int(bool(softplus)), _dtype(x),
+                                *ws, call.handle)
+    _check(code, "la_backward_ssm")
     return grads
 
 

@@ -607,6 +607,267 @@ la_status la_norm_gate_backward(const void* dy, const void* x, const void* gate,
     return from_cuda(norm_gate_backward(a));
 }
 
+// dst <- src, or zero for a NULL src
+static la_status copy_bytes(void* dst, const void* src, size_t bytes, cudaStream_t st)
+{
+    if (!dst || dst == src)
+        return LA_OK;
+    return from_cuda(src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, st)
+                         : cudaMemsetAsync(dst, 0, bytes, st));
+}
+
+static la_status clear(float* dst, int64_t count, cudaStream_t st)
+{
+    return dst ? from_cuda(cudaMemsetAsync(dst, 0, sizeof(float) * (size_t)count, st)) : LA_OK;
+}
+
+static int type_size(int dtype) { return dtype == LA_BF16 ? 2 : 4; }
+
+// A strided input: aligned to its type.
+static bool rows_ok(const void* p, int dtype, bool need = true)
+{
+    return p ? reinterpret_cast<uintptr_t>(p) % (unsigned)type_size(dtype) == 0 : !need;
+}
+
+static bool lengths_ok(const int32_t* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+constexpr int64_t kMaxChannels = 1 << 24;
+
+static la_status check_conv(const ConvArgs& a)
+{
+    if (a.B < 1 || a.N < 0 || a.C < 1 || a.H < 1 || a.C % a.H || a.W < 1 || a.xb < 0 || a.xt < 0)
+        return LA_ERR_INVALID_ARG;
+    if ((a.act != LA_ACT_SILU && a.act != LA_ACT_SIGMOID && a.act != LA_ACT_NONE) ||
+        (a.dtype != LA_BF16 && a.dtype != LA_FP32))
+        return LA_ERR_INVALID_ARG;
+    // blocks of 128 threads, each with four tokens at least
+    if (a.W < 2 || a.W > 4 || a.C > kMaxChannels || a.N > INT32_MAX ||
+        (double)a.B * ((double)a.N / 4 + 1) * ((double)a.C / 128 + 1) > INT32_MAX)
+        return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+static ConvArgs conv_sizes(int64_t B, int64_t N, int64_t C, int64_t H, int W, int act, int dtype,
+                           int64_t xb, int64_t xt, la_stream_t stream)
+{
+    ConvArgs a{};
+    a.B = B, a.N = N, a.C = C, a.H = H, a.W = W, a.act = act, a.dtype = dtype;
+    a.xb = xb, a.xt = xt;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return a;
+}
+
+static size_t window_bytes(const ConvArgs& a)
+{
+    return (size_t)(a.B * (a.W - 1) * a.C) * type_size(a.dtype);
+}
+
+la_status la_forward_conv(const void* x, int64_t x_batch, int64_t x_token, const float* weight,
+                          const float* bias, void* y, const void* S0, void* S_out,
+                          const int32_t* lengths, int64_t B, int64_t N, int64_t C, int64_t H, int W,
+                          int activation, int dtype, la_stream_t stream)
+{
+    ConvArgs a = conv_sizes(B, N, C, H, W, activation, dtype, x_batch, x_token, stream);
+    const la_status st = check_conv(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S0, false) || !ptr_ok(S_out, false) || !lengths_ok(lengths))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0)
+        return copy_bytes(S_out, S0, window_bytes(a), a.stream);
+    if (!rows_ok(x, dtype) || !ptr_ok(weight) || !ptr_ok(bias, false) || !ptr_ok(y))
+        return LA_ERR_INVALID_ARG;
+    a.x = x, a.weight = weight, a.bias = bias, a.y = y, a.S0 = S0, a.S_out = S_out;
+    a.lengths = lengths;
+    return from_cuda(conv_forward(a));
+}
+
+la_status la_decode_step_conv(void* S, const void* x, int64_t x_batch, const float* weight,
+                              const float* bias, void* y, int64_t B, int64_t C, int W,
+                              int activation, int dtype, la_stream_t stream)
+{
+    ConvArgs a = conv_sizes(B, 1, C, 1, W, activation, dtype, x_batch, 0, stream);
+    const la_status st = check_conv(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S) || !rows_ok(x, dtype) || !ptr_ok(weight) || !ptr_ok(bias, false) || !ptr_ok(y))
+        return LA_ERR_INVALID_ARG;
+    a.S_out = S, a.x = x, a.weight = weight, a.bias = bias, a.y = y;
+    return from_cuda(conv_step(a));
+}
+
+size_t la_conv_backward_workspace_size(int64_t B, int64_t N, int64_t C, int W, int dtype)
+{
+    const ConvArgs a = conv_sizes(B, N, C, 1, W, LA_ACT_SILU, dtype, 0, 0, nullptr);
+    return check_conv(a) != LA_OK || N == 0 ? 0 : conv_backward_workspace(a);
+}
+
+la_status la_backward_conv(const void* dy, const void* dS_out, const void* x, int64_t x_batch,
+                           int64_t x_token, const float* weight, const float* bias, const void* S0,
+                           const int32_t* lengths, void* dx, float* dweight, float* dbias,
+                           void* dS0, int64_t B, int64_t N, int64_t C, int64_t H, int W,
+                           int activation, int dtype, void* workspace, size_t workspace_bytes,
+                           la_stream_t stream)
+{
+    ConvArgs a = conv_sizes(B, N, C, H, W, activation, dtype, x_batch, x_token, stream);
+    la_status st = check_conv(a);
+    if (st != LA_OK)
+        return st;
+    if (!ptr_ok(S0, false) || !ptr_ok(dS_out, false) || !ptr_ok(dS0, false) || !lengths_ok(lengths) ||
+        !ptr_ok(dweight) || !ptr_ok(dbias, false) || !bias != !dbias)
+        return LA_ERR_INVALID_ARG;
+    if (N == 0) {
+        if ((st = copy_bytes(dS0, dS_out, window_bytes(a), a.stream)) != LA_OK ||
+            (st = clear(dweight, C * W, a.stream)) != LA_OK)
+            return st;
+        return clear(dbias, C, a.stream);
+    }
+    if (!ptr_ok(dy) || !rows_ok(x, dtype) || !ptr_ok(weight) || !ptr_ok(bias, false) || !ptr_ok(dx))
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, conv_backward_workspace(a)))
+        return LA_ERR_WORKSPACE;
+    a.dy = dy, a.dS_out = dS_out, a.x = x, a.weight = weight, a.bias = bias, a.S0 = S0;
+    a.lengths = lengths, a.dx = dx, a.dweight = dweight, a.dbias = dbias, a.dS0 = dS0;
+    a.ws = workspace;
+    return from_cuda(conv_backward(a));
+}
+
+static la_status check_ssm(const SsmArgs& a)
+{
+    if (a.B < 1 || a.N < 0 || a.C < 1 || a.G < 1 || a.C % a.G || a.n < 1 ||
+        (a.softplus != 0 && a.softplus != 1) || (a.dtype != LA_BF16 && a.dtype != LA_FP32))
+        return LA_ERR_INVALID_ARG;
+    if ((a.n != 8 && a.n != 16 && a.n != 32 && a.n != 64) || a.C > kMaxChannels || a.N > INT32_MAX)
+        return LA_ERR_UNSUPPORTED;
+    // blocks: segments of at least 8 tokens times tiles of at least 32 channels of a
+    // group; threads of the sums and of a step
+    const double tiles = (double)a.G * ((double)(a.C / a.G) / 32 + 1);
+    if ((double)a.B * ((double)a.N / 8 + 1) * tiles > INT32_MAX ||
+        (double)a.B * a.C * a.n / 1024 + 1 > INT32_MAX || (double)a.B * a.N * a.G * a.n / 128 + 1 > INT32_MAX)
+        return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// `s`: the caller's strides, or NULL.  A step has one stride for each input.
+static bool ssm_strides(SsmArgs* a, const int64_t* s, bool step, bool grad)
+{
+    const int64_t row = a->C, shared = a->G * a->n, rows = step ? 1 : a->N;
+    int64_t *const batch[6] = {&a->x_batch, &a->delta_batch, &a->B_batch, &a->C_batch, &a->z_batch, &a->dout_batch};
+    int64_t *const token[6] = {&a->x_token, &a->delta_token, &a->B_token, &a->C_token, &a->z_token, &a->dout_token};
+    for (int i = 0; i < (grad ? 6 : 5); ++i) {
+        const int64_t width = i == 2 || i == 3 ? shared : row;
+        *batch[i] = s ? s[step ? i : 2 * i] : width * rows;
+        *token[i] = step ? 0 : s ? s[2 * i + 1] : width;
+        if (*batch[i] < 0 || *token[i] < 0)
+            return false;
+    }
+    return true;
+}
+
+static SsmArgs ssm_sizes(int64_t B, int64_t N, int64_t C, int64_t G, int n, int softplus, int dtype,
+                         la_stream_t stream)
+{
+    SsmArgs a{};
+    a.B = B, a.N = N, a.C = C, a.G = G, a.n = n, a.softplus = softplus, a.dtype = dtype;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return a;
+}
+
+static bool ssm_inputs_ok(const SsmArgs& a)
+{
+    return rows_ok(a.x, a.dtype) && rows_ok(a.delta, a.dtype) && ptr_ok(a.A) && rows_ok(a.Bm, a.dtype) &&
+           rows_ok(a.Cm, a.dtype) && ptr_ok(a.D, false) && rows_ok(a.z, a.dtype, false) && ptr_ok(a.bias, false);
+}
+
+size_t la_ssm_workspace_size(int64_t B, int64_t N, int64_t C, int64_t G, int n, int dtype)
+{
+    const SsmArgs a = ssm_sizes(B, N, C, G, n, 1, dtype, nullptr);
+    return check_ssm(a) != LA_OK || N == 0 ? 0 : ssm_forward_workspace(a);
+}
+
+la_status la_forward_ssm(const void* x, const void* delta, const float* A, const void* Bm,
+                         const void* Cm, const float* D, const void* z, const float* delta_bias,
+                         void* out, const float* S0, float* S_out, const int32_t* lengths,
+                         const int64_t* strides, int64_t B, int64_t N, int64_t C, int64_t G, int n,
+                         int softplus, int dtype, void* workspace, size_t workspace_bytes,
+                         la_stream_t stream)
+{
+    SsmArgs a = ssm_sizes(B, N, C, G, n, softplus, dtype, stream);
+    const la_status st = check_ssm(a);
+    if (st != LA_OK)
+        return st;
+    if (!ssm_strides(&a, strides, false, false) || !ptr_ok(S0, false) || !ptr_ok(S_out, false) ||
+        !lengths_ok(lengths))
+        return LA_ERR_INVALID_ARG;
+    if (N == 0)
+        return copy_bytes(S_out, S0, sizeof(float) * (size_t)(B * C) * n, a.stream);
+    a.x = x, a.delta = delta, a.A = A, a.Bm = Bm, a.Cm = Cm, a.D = D, a.z = z, a.bias = delta_bias;
+    if (!ssm_inputs_ok(a) || !ptr_ok(out))
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, ssm_forward_workspace(a)))
+        return LA_ERR_WORKSPACE;
+    a.out = out, a.S0 = S0, a.S_out = S_out, a.lengths = lengths, a.ws = workspace;
+    return from_cuda(ssm_forward(a));
+}
+
+la_status la_decode_step_ssm(float* S, const void* x, const void* delta, const float* A,
+                             const void* Bm, const void* Cm, const float* D, const void* z,
+                             const float* delta_bias, void* out, const int64_t* strides, int64_t B,
+                             int64_t C, int64_t G, int n, int softplus, int dtype,
+                             la_stream_t stream)
+{
+    SsmArgs a = ssm_sizes(B, 1, C, G, n, softplus, dtype, stream);
+    const la_status st = check_ssm(a);
+    if (st != LA_OK)
+        return st;
+    a.x = x, a.delta = delta, a.A = A, a.Bm = Bm, a.Cm = Cm, a.D = D, a.z = z, a.bias = delta_bias;
+    if (!ssm_strides(&a, strides, true, false) || !ptr_ok(S) || !ssm_inputs_ok(a) || !ptr_ok(out))
+        return LA_ERR_INVALID_ARG;
+    a.S_out = S, a.out = out;
+    return from_cuda(ssm_step(a));
+}
+
+size_t la_ssm_backward_workspace_size(int64_t B, int64_t N, int64_t C, int64_t G, int n, int dtype)
+{
+    const SsmArgs a = ssm_sizes(B, N, C, G, n, 1, dtype, nullptr);
+    return check_ssm(a) != LA_OK || N == 0 ? 0 : ssm_backward_workspace(a);
+}
+
+la_status la_backward_ssm(const void* dout, const float* dS_out, const void* x, const void* delta,
+                          const float* A, const void* Bm, const void* Cm, const float* D,
+                          const void* z, const float* delta_bias, const float* S0,
+                          const int32_t* lengths, void* dx, void* ddelta, float* dA, void* dBm,
+                          void* dCm, float* dD, void* dz, float* ddelta_bias, float* dS0,
+                          const int64_t* strides, int64_t B, int64_t N, int64_t C, int64_t G, int n,
+                          int softplus, int dtype, void* workspace, size_t workspace_bytes,
+                          la_stream_t stream)
+{
+    SsmArgs a = ssm_sizes(B, N, C, G, n, softplus, dtype, stream);
+    la_status st = check_ssm(a);
+    if (st != LA_OK)
+        return st;
+    if (!ssm_strides(&a, strides, false, true) || !ptr_ok(S0, false) || !ptr_ok(dS_out, false) ||
+        !ptr_ok(dS0, false) || !lengths_ok(lengths) || !ptr_ok(dA) || !ptr_ok(dD, false) ||
+        !ptr_ok(ddelta_bias, false) || !D != !dD || !delta_bias != !ddelta_bias)
+        return LA_ERR_INVALID_ARG;
+    if (N == 0) {
+        if ((st = copy_bytes(dS0, dS_out, sizeof(float) * (size_t)(B * C) * n, a.stream)) != LA_OK ||
+            (st = clear(dA, C * n, a.stream)) != LA_OK || (st = clear(dD, C, a.stream)) != LA_OK)
+            return st;
+        return clear(ddelta_bias, C, a.stream);
+    }
+    a.x = x, a.delta = delta, a.A = A, a.Bm = Bm, a.Cm = Cm, a.D = D, a.z = z, a.bias = delta_bias;
+    if (!ssm_inputs_ok(a) || !rows_ok(dout, dtype) || !ptr_ok(dx) || !ptr_ok(ddelta) || !ptr_ok(dBm) ||
+        !ptr_ok(dCm) || !ptr_ok(dz, false) || !z != !dz)
+        return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, ssm_backward_workspace(a)))
+        return LA_ERR_WORKSPACE;
+    a.dout = dout, a.dS_out = dS_out, a.S0 = S0, a.lengths = lengths;
+    a.dx = dx, a.ddelta = ddelta, a.dA = dA, a.dB = dBm, a.dC = dCm, a.dD = dD, a.dz = dz;
+    a.dbias = ddelta_bias, a.dS0 = dS0, a.ws = workspace;
+    return from_cuda(ssm_backward(a));
+}
+
 la_status la_state_prefix(const float* S_parts, const float* z_parts, int nparts,
                           const int64_t* part_len, int upto, float* S_out, float* z_out,
                           int64_t B, int64_t H, int d, int dv, const float* gamma,

@@ -206,6 +206,58 @@ size_t norm_gate_backward_workspace(const NormGateArgs& a);
 cudaError_t norm_gate(const NormGateArgs& a);
 cudaError_t norm_gate_backward(const NormGateArgs& a);
 
+// short causal convolution (la_forward_conv, la_decode_step_conv, la_backward_conv)
+struct ConvArgs {
+    const void* x;           // [B,N,C], strides xb and xt in elements; step: [B,C], stride xb
+    const float* weight;     // [C,W]
+    const float* bias;       // [C], or NULL
+    void* y;                 // [B,H,N,C/H]; step: [B,C]
+    const void* S0;          // [B,W-1,C] in dtype, or NULL for zeros
+    void* S_out;             // [B,W-1,C], or NULL; step: the window, updated in place
+    const int* lengths;      // [B], or NULL
+    int64_t B, N, C, H, xb, xt;
+    int W, act, dtype;
+    void* ws;
+    cudaStream_t stream;
+    // gradients (la_backward_conv)
+    const void* dy;          // as y
+    const void* dS_out;      // [B,W-1,C] in dtype, or NULL
+    void* dx;                // [B,N,C]
+    float* dweight;          // [C,W]
+    float* dbias;            // [C], or NULL
+    void* dS0;               // [B,W-1,C] in dtype, or NULL
+};
+size_t conv_backward_workspace(const ConvArgs& a);
+cudaError_t conv_forward(const ConvArgs& a);
+cudaError_t conv_step(const ConvArgs& a);
+cudaError_t conv_backward(const ConvArgs& a);
+
+// selective state-space scan (la_forward_ssm, la_decode_step_ssm, la_backward_ssm)
+struct SsmArgs {
+    const void *x, *delta, *Bm, *Cm, *z;  // [B,N,C], [B,N,C], [B,N,G,n] twice, [B,N,C] or NULL
+    int64_t x_batch, x_token, delta_batch, delta_token, B_batch, B_token, C_batch, C_token, z_batch, z_token;
+    const float *A, *D, *bias;            // [C,n], [C] or NULL, [C] or NULL
+    void* out;                            // [B,N,C]; step: [B,C]
+    const float* S0;                      // [B,C,n], or NULL for a zero start
+    float* S_out;                         // [B,C,n], or NULL; step: the state, updated in place
+    const int* lengths;                   // [B], or NULL
+    int64_t B, N, C, G;
+    int n, softplus, dtype;
+    void* ws;
+    cudaStream_t stream;
+    // gradients (la_backward_ssm)
+    const void* dout;                     // [B,N,C]
+    int64_t dout_batch, dout_token;
+    const float* dS_out;                  // [B,C,n], or NULL
+    void *dx, *ddelta, *dB, *dC, *dz;     // contiguous, in the inputs' shapes and type
+    float *dA, *dD, *dbias, *dS0;
+};
+size_t ssm_forward_workspace(const SsmArgs& a);
+size_t ssm_backward_workspace(const SsmArgs& a);
+cudaError_t ssm_forward(const SsmArgs& a);
+cudaError_t ssm_step(const SsmArgs& a);
+cudaError_t ssm_backward(const SsmArgs& a);
+
 struct DecodeArgs {
     float* S;
     float* z;

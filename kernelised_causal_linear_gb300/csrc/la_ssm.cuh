@@ -1,0 +1,237 @@
+// la_ssm.cuh -- what the forward and the gradient of the selective scan share: how
+// channels and states lie over threads, tiles of tokens in shared memory, steps.
+//
+//   dt_t = softplus(delta_t + delta_bias),  a_t = exp(dt_t A[c,s]),
+//   S_t = a_t S_{t-1} + dt_t x_t B_t,       y_t = sum_s C_t S_t + D x_t
+//
+// A thread owns four neighbouring channels times four states; n / 4 lanes share a
+// channel quad.  A token then costs it four 16-byte reads of shared memory for 16
+// elements, and the sum over states is three shuffles for four channels.  (One
+// channel with all 16 states per thread reads shared memory twice as often; two
+// channels times eight states as often, for more shuffles.)
+#pragma once
+
+#include "la_rows.cuh"
+
+namespace la {
+namespace ssm {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+
+template <int NS>
+struct Lay {
+    static constexpr int LPC = NS / 4;               // lanes that share a channel quad
+    static constexpr int QPW = 32 / LPC;             // quads of a warp
+    static constexpr int CT = kWarps * QPW * 4;      // channels of a block
+    static constexpr int TT = NS == 8 ? 8 : NS == 16 ? 16 : 32;  // tokens of a tile
+    static constexpr int OWN = LPC == 2 ? 2 : 1;     // channels whose sums end in a lane
+};
+
+// Where a block works: channels c0 .. c0 + valid - 1 of group g, row b, segment.
+struct Place {
+    int64_t b;
+    int seg, g, c0, valid, tile;
+};
+
+struct Grid {
+    int64_t B, N;
+    int C, G, per_group;  // channel tiles of a group
+    int segs, seg_len;    // seg_len a multiple of the tile
+};
+
+template <int NS>
+__device__ __forceinline__ Place place_of(const Grid& q, int64_t block)
+{
+    const int tiles = q.G * q.per_group;
+    const int64_t rest = block / tiles;
+    Place p;
+    p.tile = (int)(block - rest * tiles);
+    p.b = rest / q.segs, p.seg = (int)(rest - p.b * q.segs);
+    p.g = p.tile / q.per_group;
+    const int in = (p.tile - p.g * q.per_group) * Lay<NS>::CT, cg = q.C / q.G;
+    p.c0 = p.g * cg + in, p.valid = min(Lay<NS>::CT, cg - in);
+    return p;
+}
+
+// Strided rows of one input.
+struct Rows {
+    const void* p;
+    int64_t batch, token;
+};
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 2^x in hardware, 2.4 * 2^-24 at most off relative to the result; results under the
+// smallest normal number are zero.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The decay 2^(dt A2), A2 = A log2(e).  The hardware exponential is low by 0.1 (arguments
+// above -2^-9) to 0.46 * 2^-24 in the mean, which a state that remembers a thousand tokens
+// adds up a thousand times; a quarter of 2^-24 more in the argument, in the same
+// instruction as the product, brings that to within 0.09 above -2^-9 and 0.29 elsewhere
+// above -1/4.  2^kLift itself is exactly 1: dt = 0 leaves a state as it was.
+constexpr float kLift = 0.25f / 16777216.0f;
+__device__ __forceinline__ float decay(float dt, float A2) { return ex2(fmaf(dt, A2, kLift)); }
+__device__ __forceinline__ float2 decay(float2 dt, float2 A2)
+{
+    const float2 t = fma2(dt, A2, both(kLift));
+    return make_float2(ex2(t.x), ex2(t.y));
+}
+
+// log(1 + e^u) = max(u, 0) + log1p(e), e = exp(-|u|) in (0, 1].  log1p(e) = 2 atanh(w),
+// w = e / (2 + e) <= 1/3, by its power series to w^15 (the next term is 1e-9 of it):
+// a small step keeps all its digits, which log(1 + e) would not.
+__device__ __forceinline__ float softplus(float u)
+{
+    const float e = ex2(-fabsf(u) * kLog2e);
+    const float w = __fdividef(e, 2.0f + e), q = w * w;
+    float s = 1.0f / 15.0f;
+    s = fmaf(s, q, 1.0f / 13.0f);
+    s = fmaf(s, q, 1.0f / 11.0f);
+    s = fmaf(s, q, 1.0f / 9.0f);
+    s = fmaf(s, q, 1.0f / 7.0f);
+    s = fmaf(s, q, 1.0f / 5.0f);
+    s = fmaf(s, q, 1.0f / 3.0f);
+    s = fmaf(s, q, 1.0f);
+    return fmaxf(u, 0.0f) + 2.0f * w * s;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+                 "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// A tile of `WIDE` columns from token t0 into shared memory [TT][WIDE], `live` tokens
+// and `cols` columns of it from memory, the rest zero (bytes behind either are not
+// read).  ASYNC: 16-byte copies in flight, every row on a 16-byte boundary; else
+// element by element.
+template <typename T, int TT, int WIDE, bool ASYNC>
+__device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, int live, int cols)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    if constexpr (ASYNC) {
+        constexpr int PER = WIDE / V;
+#pragma unroll
+        for (int k = 0; k < (TT * PER + kThreads - 1) / kThreads; ++k) {
+            const int i = k * kThreads + threadIdx.x, t = i / PER, c = i % PER * V;
+            if (TT * PER % kThreads && i >= TT * PER)
+                break;
+            const bool on = t < live && c < cols;
+            cp_async16(dst + t * WIDE + c, on ? src + t * token + c : src,
+                       on ? min(V, cols - c) * (int)sizeof(T) : 0);
+        }
+    } else {
+        for (int i = threadIdx.x; i < TT * WIDE; i += kThreads) {
+            const int t = i / WIDE, c = i % WIDE;
+            dst[i] = t < live && c < cols ? src[t * token + c] : from_f32<T>(0.0f);
+        }
+    }
+}
+
+// Sums over the lanes of a quad, of channel pairs (y[0], y[1]): a lane ends with the
+// sum of its channel lane & 3 (LPC = 2: of the pair y[lane & 1]).
+template <int LPC>
+__device__ __forceinline__ void sum_states(const float2 (&y)[2], int lane, float (&own)[LPC == 2 ? 2 : 1])
+{
+    constexpr unsigned full = 0xffffffffu;
+    if constexpr (LPC == 2) {
+        const bool up = lane & 1;
+        const float2 keep = up ? y[1] : y[0], give = up ? y[0] : y[1];
+        own[0] = keep.x + __shfl_xor_sync(full, give.x, 1);
+        own[1] = keep.y + __shfl_xor_sync(full, give.y, 1);
+    } else {
+        const bool up = lane & 2, odd = lane & 1;
+        float2 keep = up ? y[1] : y[0];
+        const float2 give = up ? y[0] : y[1];
+        keep.x += __shfl_xor_sync(full, give.x, 2);
+        keep.y += __shfl_xor_sync(full, give.y, 2);
+        float r = (odd ? keep.y : keep.x) + __shfl_xor_sync(full, odd ? keep.x : keep.y, 1);
+#pragma unroll
+        for (int o = 4; o < LPC; o *= 2)
+            r += __shfl_xor_sync(full, r, o);
+        own[0] = r;
+    }
+}
+
+// Four states of four channels between memory [C][n] and pairs [channel pair][state];
+// channels behind the last are zero and are not written.
+template <int NS>
+__device__ __forceinline__ void load_quad(const float* __restrict__ p, int valid, float2 (&h)[2][4])
+{
+    float f[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = i < valid ? *reinterpret_cast<const float4*>(p + i * NS) : make_float4(0.f, 0.f, 0.f, 0.f);
+        f[i][0] = v.x, f[i][1] = v.y, f[i][2] = v.z, f[i][3] = v.w;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        h[0][s] = make_float2(f[0][s], f[1][s]), h[1][s] = make_float2(f[2][s], f[3][s]);
+}
+
+template <int NS>
+__device__ __forceinline__ void store_quad(float* __restrict__ p, int valid, const float2 (&h)[2][4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2* q = h[i / 2];
+        if (i < valid)
+            *reinterpret_cast<float4*>(p + i * NS) = i & 1 ? make_float4(q[0].y, q[1].y, q[2].y, q[3].y)
+                                                           : make_float4(q[0].x, q[1].x, q[2].x, q[3].x);
+    }
+}
+
+// h and a of one token: a = exp(dt A), h = a h + u B with u = dt x.
+__device__ __forceinline__ void step(const float4& dt, const float4& u, const float4& B, const float2 (&A2)[2][4],
+                                     float2 (&h)[2][4])
+{
+    const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
+    const float b[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            h[p][s] = fma2(decay(d[p], A2[p][s]), h[p][s], mul2(v[p], both(b[s])));
+}
+
+// Segments between their ends and their starts: S_{i+1} = exp(A sum dt_i) S_i + E_i.
+cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const float* sums);
+
+}  // namespace ssm
+}  // namespace la
