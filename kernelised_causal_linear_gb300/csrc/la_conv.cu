@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     u = fmaf(w[j][i], win[j][i], u);
-                o.f[i] = t + k < live ? activate(u, s.act).x : 0.0f;
+                o.f[i] = t + k < live ? activated(u, s.act) : 0.0f;
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
                     win[j][i] = win[j + 1][i];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads)
     Vec<V> o;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        o.f[i] = activate(u[i], act).x;
+        o.f[i] = activated(u[i], act);
     store(y + b * C + c, o);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)

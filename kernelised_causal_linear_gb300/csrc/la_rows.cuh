@@ -93,6 +93,16 @@ __device__ __forceinline__ float2 activate(float u, int act)
     return act == LA_ACT_SIGMOID ? s : make_float2(u * s.x, fmaf(u, s.y, s.x));
 }
 
+// act(u) alone.  The exponential of a large -u is infinite and its quotient zero: under
+// u = -87 the result is 0 in place of less than 1e-36.
+__device__ __forceinline__ float activated(float u, int act)
+{
+    if (act == LA_ACT_NONE)
+        return u;
+    const float s = __fdividef(1.0f, 1.0f + __expf(-u));
+    return act == LA_ACT_SIGMOID ? s : u * s;
+}
+
 // Tokens of row b: lengths clamped to 0 .. N, or N.
 __device__ __forceinline__ int64_t row_length(const int* lengths, int64_t b, int64_t N)
 {

@@ -2,7 +2,17 @@
 // token for every sequence.
 //
 // The recurrence is exact, token after token in fp32, with no products of decays
-// kept.  Few long sequences are cut into segments: k_ssm<END> runs each from a zero
+// kept.  A thread owns two neighbouring channels with up to 16 states each, in pairs of
+// states: B and C, the same for every lane, are eight 16-byte reads of shared memory for
+// 32 elements, and the sum over the states stays in the thread (n = 32 and 64: two and
+// four lanes per channel pair).  What bounds it is arithmetic: an element costs one
+// hardware exponential (32 a clock and SM) and four fp32 operations in two-wide
+// instructions (128 a clock and SM), which overlap: 512 elements take about 155 clocks of a sub-partition, 80 of them of the
+// exponentials' unit, those of the steps and the gate among them (B4 N8192 C2048 n = 16 bf16:
+// 288 us, and 206 us for the run for the ends).  (Four channels times four states per
+// thread, with steps in shared memory and shuffles, took 198 clocks.)
+//
+// Few long sequences are cut into segments: k_ssm<END> runs each from a zero
 // state for its end, k_ssm_join walks the ends (the decay of a segment is exp(A sum
 // dt)), and k_ssm runs every segment again from its true start.
 #include "la_ssm.cuh"
@@ -13,14 +23,22 @@ namespace {
 
 using namespace rows;
 
+template <typename T, int NS>
+struct Cut {
+    static constexpr int NT = 64;                   // threads
+    static constexpr int SPT = NS < 16 ? NS : 16;   // states of a thread
+    static constexpr int LPC = NS / SPT;            // lanes that share a channel pair
+    static constexpr int CT = NT / LPC * 2;         // channels of a block
+    static constexpr int TT = sizeof(T) == 2 ? 16 : 8;  // tokens of a tile: 4 KB of 128 channels
+};
+
 template <typename T, int NS, bool END>
 struct Tiles {
-    using L = Lay<NS>;
-    // raw tiles, two of each: the next one is on its way while this one is used
+    using L = Cut<T, NS>;
+    // as they lie in memory, two of each: the next tile is on its way while this one is used
     T x[2][L::TT][L::CT], delta[2][L::TT][L::CT], z[END ? 1 : 2][END ? 1 : L::TT][END ? 8 : L::CT];
     T B[2][L::TT][NS], C[2][L::TT][NS];
-    // in use, fp32
-    float dt[L::TT][L::CT], u[L::TT][L::CT], Bf[L::TT][NS], Cf[END ? 1 : L::TT][NS];
+    float Bf[L::TT][NS], Cf[END ? 1 : L::TT][NS];
 };
 
 struct Ins {
@@ -30,50 +48,87 @@ struct Ins {
     int softplus;
 };
 
-// END: the state after each segment from a zero start (ends) and the sum of its steps
-// (sums).  Else the outputs, from S0 or (segments) from `ends`, which then holds starts.
+__device__ __forceinline__ float2 two(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 two(const __nv_bfloat16* p)
+{
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void put_two(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void put_two(__nv_bfloat16* p, float2 v)
+{
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+
+// States s0 .. of two channels, [channel][state pair]; channels behind the last are zero
+// and not written.
+template <int NS, int SPT>
+__device__ __forceinline__ void load_pair(const float* p, int have, float2 (&h)[2][SPT / 2])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int s = 0; s < SPT / 2; s += 2) {
+            const float4 v = c < have ? *reinterpret_cast<const float4*>(p + c * NS + 2 * s)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            h[c][s] = make_float2(v.x, v.y), h[c][s + 1] = make_float2(v.z, v.w);
+        }
+}
+
+template <int NS, int SPT>
+__device__ __forceinline__ void store_pair(float* p, int have, const float2 (&h)[2][SPT / 2])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int s = 0; s < SPT / 2; s += 2)
+            if (c < have)
+                *reinterpret_cast<float4*>(p + c * NS + 2 * s) =
+                    make_float4(h[c][s].x, h[c][s].y, h[c][s + 1].x, h[c][s + 1].y);
+}
+
+// END: the state after each segment but the last from a zero start (ends) and the sum of
+// its steps (sums).  Else the outputs, from S0 or (segments) from `ends`, which then holds
+// starts.
 template <typename T, int NS, bool END, bool ASYNC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Cut<T, NS>::NT)
     k_ssm(Ins in, T* __restrict__ out, const float* S0, float* S_out, float* __restrict__ ends,
           float* __restrict__ sums, Grid q)
 {
-    using L = Lay<NS>;
-    constexpr int TT = L::TT, CT = L::CT, V = 16 / (int)sizeof(T);
+    using L = Cut<T, NS>;
+    constexpr int NT = L::NT, TT = L::TT, CT = L::CT, SPT = L::SPT, LPC = L::LPC;
     extern __shared__ __align__(16) unsigned char smem[];
     auto& sm = *reinterpret_cast<Tiles<T, NS, END>*>(smem);
-    const Place at = place_of<NS>(q, blockIdx.x);
+    const Place at = place_of(q, blockIdx.x, CT);
+    if (END && at.seg == q.segs - 1)
+        return;
     const int64_t len = row_length(in.lengths, at.b, q.N);
     const int64_t first = (int64_t)at.seg * q.seg_len, end = min(q.N, first + q.seg_len);
     const int live = (int)max((int64_t)0, min(end, len) - first);  // tokens of this segment that the row has
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c4 = (warp * L::QPW + lane / L::LPC) * 4, s4 = lane % L::LPC * 4;  // quad and states
-    const int have = max(0, min(4, at.valid - c4));
+    const int part = threadIdx.x % LPC, s0 = part * SPT, c2 = threadIdx.x / LPC * 2;
+    const int have = max(0, min(2, at.valid - c2));
     const int64_t C = q.C;
 
-    float2 A2[2][4], h[2][4], sum[2] = {}, low[2] = {};
-    load_quad<NS>(in.A + (at.c0 + c4) * (int64_t)NS + s4, have, A2);
+    float2 A2[2][SPT / 2], h[2][SPT / 2], sum = {}, low = {};
+    load_pair<NS, SPT>(in.A + (at.c0 + c2) * (int64_t)NS + s0, have, A2);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-            A2[p][s] = mul2(A2[p][s], both(kLog2e)), h[p][s] = make_float2(0.f, 0.f);
-    const int64_t state = (at.b * C + at.c0 + c4) * NS + s4;
-    const int64_t kept = ((at.b * q.segs + at.seg) * C + at.c0 + c4) * NS + s4;
+        for (int s = 0; s < SPT / 2; ++s)
+            A2[c][s] = mul2(A2[c][s], both(kLog2e)), h[c][s] = make_float2(0.f, 0.f);
+    const int64_t state = (at.b * C + at.c0 + c2) * NS + s0;
+    const int64_t kept = ((at.b * q.segs + at.seg) * C + at.c0 + c2) * NS + s0;
     if (!END) {
         if (q.segs > 1)
-            load_quad<NS>(ends + kept, have, h);
+            load_pair<NS, SPT>(ends + kept, have, h);
         else if (S0)
-            load_quad<NS>(S0 + state, have, h);
+            load_pair<NS, SPT>(S0 + state, have, h);
     }
-    // the channels whose sums end in this lane
-    const int co = L::LPC == 2 ? c4 + (lane & 1) * 2 : c4 + (lane & 3);
-    float Dv[L::OWN];
-    bool mine[L::OWN];
-#pragma unroll
-    for (int i = 0; i < L::OWN; ++i) {
-        mine[i] = !END && co + i < at.valid && s4 < 16;
-        Dv[i] = mine[i] && in.D ? in.D[at.c0 + co + i] : 0.0f;
-    }
+    auto channels = [&](const float* p) {
+        return p ? make_float2(have > 0 ? p[at.c0 + c2] : 0.f, have > 1 ? p[at.c0 + c2 + 1] : 0.f)
+                 : make_float2(0.f, 0.f);
+    };
+    const float2 bias = channels(in.bias), D = channels(in.D);
 
     const T* xs = static_cast<const T*>(in.x.p) + at.b * in.x.batch + at.c0;
     const T* ds = static_cast<const T*>(in.delta.p) + at.b * in.delta.batch + at.c0;
@@ -84,13 +139,13 @@ __global__ void __launch_bounds__(kThreads)
         const int k = tile & 1;
         const int64_t t0 = first + (int64_t)tile * TT;
         const int n = min(TT, live - tile * TT);
-        copy_tile<T, TT, CT, ASYNC>(sm.x[k][0], xs + t0 * in.x.token, in.x.token, n, at.valid);
-        copy_tile<T, TT, CT, ASYNC>(sm.delta[k][0], ds + t0 * in.delta.token, in.delta.token, n, at.valid);
-        copy_tile<T, TT, NS, ASYNC>(sm.B[k][0], Bs + t0 * in.B.token, in.B.token, n, NS);
+        copy_tile<T, TT, CT, ASYNC, NT>(sm.x[k][0], xs + t0 * in.x.token, in.x.token, n, at.valid);
+        copy_tile<T, TT, CT, ASYNC, NT>(sm.delta[k][0], ds + t0 * in.delta.token, in.delta.token, n, at.valid);
+        copy_tile<T, TT, NS, ASYNC, NT>(sm.B[k][0], Bs + t0 * in.B.token, in.B.token, n, NS);
         if constexpr (!END) {
-            copy_tile<T, TT, NS, ASYNC>(sm.C[k][0], Cs + t0 * in.C.token, in.C.token, n, NS);
+            copy_tile<T, TT, NS, ASYNC, NT>(sm.C[k][0], Cs + t0 * in.C.token, in.C.token, n, NS);
             if (zs)
-                copy_tile<T, TT, CT, ASYNC>(sm.z[k][0], zs + t0 * in.z.token, in.z.token, n, at.valid);
+                copy_tile<T, TT, CT, ASYNC, NT>(sm.z[k][0], zs + t0 * in.z.token, in.z.token, n, at.valid);
         }
         cp_commit();
     };
@@ -98,130 +153,147 @@ __global__ void __launch_bounds__(kThreads)
     const int tiles = (live + TT - 1) / TT;
     if (tiles > 0)
         load(0);
+    T* po = out + (at.b * q.N + first) * C + at.c0 + c2;
     for (int tile = 0; tile < tiles; ++tile) {
         const int k = tile & 1, n = min(TT, live - tile * TT);
         cp_wait<0>();
         __syncthreads();  // this tile is there, and the last one is no longer read
         if (tile + 1 < tiles)
             load(tile + 1);
-        // dt and u = dt x in fp32; tokens behind the last have dt = 0
-#pragma unroll
-        for (int i = threadIdx.x; i < TT * CT / V; i += kThreads) {
-            const int t = i / (CT / V), c = i % (CT / V) * V;
-            Raw<T, V> rd, rx;
-            rd.w = *reinterpret_cast<const decltype(rd.w)*>(&sm.delta[k][t][c]);
-            rx.w = *reinterpret_cast<const decltype(rx.w)*>(&sm.x[k][t][c]);
-            const Vec<V> d = wide(rd), x = wide(rx);
-            float dt[V], u[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float raw = d.f[j] + (in.bias && c + j < at.valid ? __ldg(in.bias + at.c0 + c + j) : 0.0f);
-                dt[j] = t < n ? (in.softplus ? softplus(raw) : raw) : 0.0f;
-                u[j] = dt[j] * x.f[j];
-            }
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                *reinterpret_cast<float4*>(&sm.dt[t][c + j]) = make_float4(dt[j], dt[j + 1], dt[j + 2], dt[j + 3]);
-                *reinterpret_cast<float4*>(&sm.u[t][c + j]) = make_float4(u[j], u[j + 1], u[j + 2], u[j + 3]);
-            }
-        }
-        for (int i = threadIdx.x; i < TT * NS; i += kThreads) {
+        for (int i = threadIdx.x; i < TT * NS; i += NT) {
             sm.Bf[0][i] = to_f32(sm.B[k][0][i]);
             if constexpr (!END)
                 sm.Cf[0][i] = to_f32(sm.C[k][0][i]);
         }
         __syncthreads();
-        T* po = out + (at.b * q.N + first + (int64_t)tile * TT) * C + at.c0 + co;
-        float2 part[2] = {};
-#pragma unroll 4
-        for (int t = 0; t < TT; ++t) {
-            const float4 dt = *reinterpret_cast<const float4*>(&sm.dt[t][c4]);
-            const float4 u = *reinterpret_cast<const float4*>(&sm.u[t][c4]);
-            const float4 B = *reinterpret_cast<const float4*>(&sm.Bf[t][s4]);
-            step(dt, u, B, A2, h);
-            if constexpr (END) {
-                part[0] = add2(part[0], make_float2(dt.x, dt.y));
-                part[1] = add2(part[1], make_float2(dt.z, dt.w));
-            } else {
-                const float4 Cr = *reinterpret_cast<const float4*>(&sm.Cf[t][s4]);
-                float2 y[2];
-                float own[L::OWN];
+        float2 added = {};
+#pragma unroll 2
+        for (int t = 0; t < n; ++t, po += C) {
+            const float2 x = two(&sm.x[k][t][c2]);
+            float2 dt = add2(two(&sm.delta[k][t][c2]), bias);
+            if (in.softplus)
+                dt = softplus(dt);
+            const float2 u = mul2(dt, x);
+            const float4* B4 = reinterpret_cast<const float4*>(&sm.Bf[t][s0]);
+            const float4* C4 = reinterpret_cast<const float4*>(&sm.Cf[END ? 0 : t][s0]);
+            float2 y[2];
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    y[p] = fma2(h[p][3], both(Cr.w), fma2(h[p][2], both(Cr.z), fma2(h[p][1], both(Cr.y),
-                                mul2(h[p][0], both(Cr.x)))));
-                sum_states<L::LPC>(y, lane, own);
+            for (int s = 0; s < SPT / 2; s += 2) {
+                const float4 b = B4[s / 2];
+                float4 c;
+                if constexpr (!END)
+                    c = C4[s / 2];
 #pragma unroll
-                for (int i = 0; i < L::OWN; ++i) {
-                    float o = fmaf(Dv[i], to_f32(sm.x[k][t][co + i]), own[i]);
-                    if (zs)
-                        o *= activate(to_f32(sm.z[k][t][co + i]), LA_ACT_SILU).x;
-                    if (mine[i] && t < n)
-                        po[t * C + i] = from_f32<T>(o);
+                for (int i = 0; i < 2; ++i) {
+                    const float2 bi = i ? make_float2(b.z, b.w) : make_float2(b.x, b.y);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        float2& hs = h[p][s + i];
+                        hs = fma2(decay(both(p ? dt.y : dt.x), A2[p][s + i]), hs, mul2(both(p ? u.y : u.x), bi));
+                        if constexpr (!END) {
+                            const float2 ci = i ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+                            y[p] = s + i ? fma2(hs, ci, y[p]) : mul2(hs, ci);
+                        }
+                    }
                 }
+            }
+            if constexpr (END) {
+                added = add2(added, dt);
+            } else if constexpr (LPC == 1) {
+                float2 o = fma2(D, x, make_float2(y[0].x + y[0].y, y[1].x + y[1].y));
+                if (zs) {
+                    const float2 z = two(&sm.z[k][t][c2]);
+                    o = mul2(o, make_float2(activated(z.x, LA_ACT_SILU), activated(z.y, LA_ACT_SILU)));
+                }
+                if (ASYNC && have == 2) {  // rows of an even number of channels
+                    put_two(po, o);
+                } else {
+                    if (have > 0)
+                        po[0] = from_f32<T>(o.x);
+                    if (have > 1)
+                        po[1] = from_f32<T>(o.y);
+                }
+            } else {
+                // halves are traded: an even lane ends with channel 0, an odd one with channel 1
+                const bool odd = part & 1;
+                const float y0 = y[0].x + y[0].y, y1 = y[1].x + y[1].y;
+                float o = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+                if constexpr (LPC == 4)
+                    o += __shfl_xor_sync(0xffffffffu, o, 2);
+                o = fmaf(odd ? D.y : D.x, odd ? x.y : x.x, o);
+                if (zs)
+                    o *= activated(to_f32(sm.z[k][t][c2 + odd]), LA_ACT_SILU);
+                if (part < 2 && have > odd)
+                    po[odd] = from_f32<T>(o);
             }
         }
         if constexpr (END) {
             // the tiles' sums with what their addition loses kept beside
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float2 s = add2(sum[p], part[p]);
-                low[p].x += (sum[p].x - s.x) + part[p].x;
-                low[p].y += (sum[p].y - s.y) + part[p].y;
-                sum[p] = s;
-            }
+            const float2 s = add2(sum, added);
+            low.x += (sum.x - s.x) + added.x;
+            low.y += (sum.y - s.y) + added.y;
+            sum = s;
         }
     }
     if constexpr (END) {
-        store_quad<NS>(ends + kept, have, h);
-        if (s4 == 0) {
-            const float f[4] = {sum[0].x + low[0].x, sum[0].y + low[0].y, sum[1].x + low[1].x, sum[1].y + low[1].y};
-            for (int i = 0; i < have; ++i)
-                sums[(at.b * q.segs + at.seg) * C + at.c0 + c4 + i] = f[i];
+        store_pair<NS, SPT>(ends + kept, have, h);
+        if (part == 0) {
+            float* p = sums + (at.b * q.segs + at.seg) * C + at.c0 + c2;
+            if (have > 0)
+                p[0] = sum.x + low.x;
+            if (have > 1)
+                p[1] = sum.y + low.y;
         }
     } else {
         // outputs behind the row's last token
-        for (int64_t i = threadIdx.x + (int64_t)live * at.valid; i < (end - first) * at.valid; i += kThreads) {
+        for (int64_t i = threadIdx.x + (int64_t)live * at.valid; i < (end - first) * at.valid; i += NT) {
             const int64_t t = i / at.valid;
             out[(at.b * q.N + first + t) * C + at.c0 + (i - t * at.valid)] = from_f32<T>(0.0f);
         }
         if (S_out && at.seg == q.segs - 1)
-            store_quad<NS>(S_out + state, have, h);
+            store_pair<NS, SPT>(S_out + state, have, h);
     }
 }
 
-// ends -> starts in place, one thread per four states; rows in flight ahead of the chain.
-__global__ void __launch_bounds__(256)
+// ends -> starts in place, one thread per state: a chain of one product and sum per
+// segment, with the loads of sixteen segments ahead of it (eight ahead with four states per
+// thread: 41 us in place of 18 for 76 segments of B4 C2048 n = 16).
+__global__ void __launch_bounds__(128)
     k_ssm_join(const float* __restrict__ A, const float* S0, float* __restrict__ ends, const float* __restrict__ sums,
                int segs, int64_t C, int NS, int64_t items)
 {
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t item = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (item >= items)
         return;
-    const int64_t row = C * NS / 4, b = item / row, e = item - b * row;  // e: four states of [C][n]
-    const int64_t c = e * 4 / NS;
-    const float4 a = reinterpret_cast<const float4*>(A)[e];
-    float4 S = S0 ? reinterpret_cast<const float4*>(S0)[item] : make_float4(0.f, 0.f, 0.f, 0.f);
-    float4* p = reinterpret_cast<float4*>(ends) + b * segs * row + e;
-    const float* d = sums + b * segs * C + c;
-    constexpr int kAhead = 8;
-    for (int i = 0; i < segs; i += kAhead) {
-        float4 E[kAhead];
-        float sd[kAhead];
+    const int64_t row = C * NS, b = item / row, e = item - b * row;
+    const float a = A[e] * kLog2e;
+    float S = S0 ? S0[item] : 0.0f;
+    float* p = ends + b * segs * row + e;
+    const float* d = sums + b * segs * C + e / NS;
+    constexpr int kAhead = 16;
+    float E[2][kAhead], P[2][kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (i + k < segs)
-                E[k] = p[(i + k) * row], sd[k] = d[(i + k) * C] * kLog2e;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (i + k < segs) {
-                p[(i + k) * row] = S;
-                S.x = fmaf(ex2(a.x * sd[k]), S.x, E[k].x);
-                S.y = fmaf(ex2(a.y * sd[k]), S.y, E[k].y);
-                S.z = fmaf(ex2(a.z * sd[k]), S.z, E[k].z);
-                S.w = fmaf(ex2(a.w * sd[k]), S.w, E[k].w);
-            }
+    for (int k = 0; k < kAhead; ++k) {  // the last segment's end is not needed
+        E[0][k] = k < segs - 1 ? p[k * row] : 0.0f;
+        P[0][k] = k < segs - 1 ? d[k * C] : 0.0f;
     }
+    for (int i0 = 0; i0 < segs; i0 += 2 * kAhead)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = i0 + half * kAhead;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool on = i + kAhead + k < segs - 1;
+                E[half ^ 1][k] = on ? p[(i + kAhead + k) * row] : 0.0f;
+                P[half ^ 1][k] = on ? d[(i + kAhead + k) * C] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i + k < segs)
+                    p[(i + k) * row] = S;
+                S = fmaf(ex2(a * P[half][k]), S, E[half][k]);
+            }
+        }
 }
 
 // One token: n / 4 lanes per channel, four states each; bound by the state's bytes.
@@ -246,7 +318,7 @@ __global__ void __launch_bounds__(256)
     const float x = to_f32(static_cast<const T*>(in.x.p)[b * in.x.batch + c]);
     float dt = to_f32(static_cast<const T*>(in.delta.p)[b * in.delta.batch + c]) + (in.bias ? __ldg(in.bias + c) : 0.0f);
     if (in.softplus)
-        dt = softplus(dt);
+        dt = softplus(both(dt)).x;
     const T* Bp = static_cast<const T*>(in.B.p) + b * in.B.batch + g * NS + s4;
     const T* Cp = static_cast<const T*>(in.C.p) + b * in.C.batch + g * NS + s4;
     const float u = dt * x, d2 = dt * kLog2e;
@@ -268,24 +340,28 @@ __global__ void __launch_bounds__(256)
         if (in.D)
             y = fmaf(__ldg(in.D + c), x, y);
         if (in.z.p)
-            y *= activate(to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]), LA_ACT_SILU).x;
+            y *= activated(to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]), LA_ACT_SILU);
         out[b * C + c] = from_f32<T>(y);
     }
 }
 
-template <int NS>
+// Segments.  The run for the ends costs 0.7 of the one that counts, so rows stay whole
+// where they alone are three blocks an SM (N8192 C2048 n = 16 bf16: 320 blocks whole 3.14 ms,
+// cut 2.31; 432 blocks 3.14 both; 576 blocks 3.15 and 4.11).  Else about four rounds of
+// blocks, which fill up better than one (64 blocks: 24 segments 543 us, 76 segments 511 us),
+// a tile each at least (fp32 B2 N333 C197: 21 segments 28 us, 42 segments 20 us).
+template <typename T, int NS>
 Grid grid_of(const SsmArgs& a)
 {
-    using L = Lay<NS>;
+    using L = Cut<T, NS>;
     Grid q;
     q.B = a.B, q.N = a.N, q.C = (int)a.C, q.G = (int)a.G;
     q.per_group = (int)((a.C / a.G + L::CT - 1) / L::CT);
     const int64_t blocks = a.B * q.G * q.per_group, tiles = (a.N + L::TT - 1) / L::TT;
     int64_t segs = 1;
-    if (blocks < 152 * 2) {
-        segs = (152 * 4 + blocks - 1) / blocks;
-        const int64_t most = (tiles + 3) / 4;  // four tiles at least
-        segs = segs < most ? segs : most;
+    if (blocks < 450) {
+        segs = 152 * 8 * 4 / blocks;
+        segs = segs < tiles ? segs : tiles;
     }
     const int64_t per = (tiles + segs - 1) / segs;
     q.seg_len = (int)(per * L::TT), q.segs = (int)((tiles + per - 1) / per);
@@ -295,7 +371,8 @@ Grid grid_of(const SsmArgs& a)
 template <typename T, int NS>
 cudaError_t run_ssm(const SsmArgs& a)
 {
-    const Grid q = grid_of<NS>(a);
+    using L = Cut<T, NS>;
+    const Grid q = grid_of<T, NS>(a);
     Ins in{{a.x, a.x_batch, a.x_token}, {a.delta, a.delta_batch, a.delta_token}, {a.Bm, a.B_batch, a.B_token},
            {a.Cm, a.C_batch, a.C_token}, {a.z, a.z_batch, a.z_token}, a.A, a.D, a.bias, a.lengths, a.softplus};
     const int es = (int)sizeof(T);
@@ -309,7 +386,7 @@ cudaError_t run_ssm(const SsmArgs& a)
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess)
             return e;
-        kernel<<<blocks, kThreads, bytes, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
+        kernel<<<blocks, L::NT, bytes, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
         count_launches(1);
         return cudaGetLastError();
     };
@@ -346,13 +423,14 @@ cudaError_t states(const SsmArgs& a, bool step)
     }
 }
 
+template <typename T>
 Grid grid_any(const SsmArgs& a)
 {
     switch (a.n) {
-    case 8: return grid_of<8>(a);
-    case 16: return grid_of<16>(a);
-    case 32: return grid_of<32>(a);
-    default: return grid_of<64>(a);
+    case 8: return grid_of<T, 8>(a);
+    case 16: return grid_of<T, 16>(a);
+    case 32: return grid_of<T, 32>(a);
+    default: return grid_of<T, 64>(a);
     }
 }
 
@@ -360,8 +438,8 @@ Grid grid_any(const SsmArgs& a)
 
 cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const float* sums)
 {
-    const int64_t items = a.B * a.C * a.n / 4;
-    k_ssm_join<<<(unsigned)((items + 255) / 256), 256, 0, a.stream>>>(a.A, a.S0, ends, sums, q.segs, a.C, a.n, items);
+    const int64_t items = a.B * a.C * a.n;
+    k_ssm_join<<<(unsigned)((items + 127) / 128), 128, 0, a.stream>>>(a.A, a.S0, ends, sums, q.segs, a.C, a.n, items);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -370,7 +448,7 @@ cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const flo
 
 size_t ssm_forward_workspace(const SsmArgs& a)
 {
-    const ssm::Grid q = ssm::grid_any(a);
+    const ssm::Grid q = a.dtype == LA_BF16 ? ssm::grid_any<__nv_bfloat16>(a) : ssm::grid_any<float>(a);
     return q.segs == 1 ? 0 : sizeof(float) * (size_t)(a.B * q.segs) * a.C * (a.n + 1);
 }
 

@@ -1,14 +1,8 @@
-// la_ssm.cuh -- what the forward and the gradient of the selective scan share: how
-// channels and states lie over threads, tiles of tokens in shared memory, steps.
+// la_ssm.cuh -- what the forward and the gradient of the selective scan share: tiles of
+// tokens in shared memory, steps and decays, where a block works.
 //
 //   dt_t = softplus(delta_t + delta_bias),  a_t = exp(dt_t A[c,s]),
 //   S_t = a_t S_{t-1} + dt_t x_t B_t,       y_t = sum_s C_t S_t + D x_t
-//
-// A thread owns four neighbouring channels times four states; n / 4 lanes share a
-// channel quad.  A token then costs it four 16-byte reads of shared memory for 16
-// elements, and the sum over states is three shuffles for four channels.  (One
-// channel with all 16 states per thread reads shared memory twice as often; two
-// channels times eight states as often, for more shuffles.)
 #pragma once
 
 #include "la_rows.cuh"
@@ -24,7 +18,6 @@ struct Lay {
     static constexpr int LPC = NS / 4;               // lanes that share a channel quad
     static constexpr int QPW = 32 / LPC;             // quads of a warp
     static constexpr int CT = kWarps * QPW * 4;      // channels of a block
-    static constexpr int TT = NS == 8 ? 8 : NS == 16 ? 16 : 32;  // tokens of a tile
     static constexpr int OWN = LPC == 2 ? 2 : 1;     // channels whose sums end in a lane
 };
 
@@ -40,8 +33,7 @@ struct Grid {
     int segs, seg_len;    // seg_len a multiple of the tile
 };
 
-template <int NS>
-__device__ __forceinline__ Place place_of(const Grid& q, int64_t block)
+__device__ __forceinline__ Place place_of(const Grid& q, int64_t block, int width)
 {
     const int tiles = q.G * q.per_group;
     const int64_t rest = block / tiles;
@@ -49,8 +41,8 @@ __device__ __forceinline__ Place place_of(const Grid& q, int64_t block)
     p.tile = (int)(block - rest * tiles);
     p.b = rest / q.segs, p.seg = (int)(rest - p.b * q.segs);
     p.g = p.tile / q.per_group;
-    const int in = (p.tile - p.g * q.per_group) * Lay<NS>::CT, cg = q.C / q.G;
-    p.c0 = p.g * cg + in, p.valid = min(Lay<NS>::CT, cg - in);
+    const int in = (p.tile - p.g * q.per_group) * width, cg = q.C / q.G;
+    p.c0 = p.g * cg + in, p.valid = min(width, cg - in);
     return p;
 }
 
@@ -107,21 +99,41 @@ __device__ __forceinline__ float2 decay(float2 dt, float2 A2)
 }
 
 // log(1 + e^u) = max(u, 0) + log1p(e), e = exp(-|u|) in (0, 1].  log1p(e) = 2 atanh(w),
-// w = e / (2 + e) <= 1/3, by its power series to w^15 (the next term is 1e-9 of it):
-// a small step keeps all its digits, which log(1 + e) would not.
-__device__ __forceinline__ float softplus(float u)
+// w = e / (2 + e) <= 1/3, atanh(w) / w = 1 + q p(q) with q = w^2 and p the cubic through
+// (atanh(w) / w - 1) / q at the Chebyshev points of [0, 1/9]: 1.6e-8 of the result.  A small
+// step keeps all its digits, which log(1 + e) would not.
+__device__ __forceinline__ float2 softplus(float2 u)
 {
-    const float e = ex2(-fabsf(u) * kLog2e);
-    const float w = __fdividef(e, 2.0f + e), q = w * w;
-    float s = 1.0f / 15.0f;
-    s = fmaf(s, q, 1.0f / 13.0f);
-    s = fmaf(s, q, 1.0f / 11.0f);
-    s = fmaf(s, q, 1.0f / 9.0f);
-    s = fmaf(s, q, 1.0f / 7.0f);
-    s = fmaf(s, q, 1.0f / 5.0f);
-    s = fmaf(s, q, 1.0f / 3.0f);
-    s = fmaf(s, q, 1.0f);
-    return fmaxf(u, 0.0f) + 2.0f * w * s;
+    const float2 e = make_float2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
+    const float2 w = make_float2(__fdividef(e.x, 2.0f + e.x), __fdividef(e.y, 2.0f + e.y)), q = mul2(w, w);
+    float2 s = fma2(q, both(0.134257495f), both(0.141183093f));
+    s = fma2(s, q, both(0.200037807f));
+    s = fma2(s, q, both(0.333333194f));
+    s = fma2(s, q, both(1.0f));
+    return fma2(add2(w, w), s, make_float2(fmaxf(u.x, 0.0f), fmaxf(u.y, 0.0f)));
+}
+
+// Steps and inputs of V channels of one token from what lies in memory: dt and u = dt x,
+// zero behind the row's last token.
+template <int V>
+__device__ __forceinline__ void steps(const rows::Vec<V>& raw, const rows::Vec<V>& x, const float (&bias)[V],
+                                      int plus, bool on, float* dt, float* u)
+{
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+        float2 d[2], v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = j + 2 * k;
+            float2 r = add2(make_float2(raw.f[i], raw.f[i + 1]), make_float2(bias[i], bias[i + 1]));
+            if (plus)
+                r = softplus(r);
+            d[k] = on ? r : make_float2(0.f, 0.f);
+            v[k] = mul2(d[k], make_float2(x.f[i], x.f[i + 1]));
+        }
+        *reinterpret_cast<float4*>(dt + j) = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
+        *reinterpret_cast<float4*>(u + j) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes)
@@ -141,25 +153,34 @@ __device__ __forceinline__ void cp_wait()
 // and `cols` columns of it from memory, the rest zero (bytes behind either are not
 // read).  ASYNC: 16-byte copies in flight, every row on a 16-byte boundary; else
 // element by element.
-template <typename T, int TT, int WIDE, bool ASYNC>
+template <typename T, int TT, int WIDE, bool ASYNC, int NT = kThreads>
 __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, int live, int cols)
 {
     constexpr int V = 16 / (int)sizeof(T);
     if constexpr (ASYNC) {
         constexpr int PER = WIDE / V;
 #pragma unroll
-        for (int k = 0; k < (TT * PER + kThreads - 1) / kThreads; ++k) {
-            const int i = k * kThreads + threadIdx.x, t = i / PER, c = i % PER * V;
-            if (TT * PER % kThreads && i >= TT * PER)
+        for (int k = 0; k < (TT * PER + NT - 1) / NT; ++k) {
+            const int i = k * NT + threadIdx.x, t = i / PER, c = i % PER * V;
+            if (TT * PER % NT && i >= TT * PER)
                 break;
             const bool on = t < live && c < cols;
             cp_async16(dst + t * WIDE + c, on ? src + t * token + c : src,
                        on ? min(V, cols - c) * (int)sizeof(T) : 0);
         }
     } else {
-        for (int i = threadIdx.x; i < TT * WIDE; i += kThreads) {
-            const int t = i / WIDE, c = i % WIDE;
-            dst[i] = t < live && c < cols ? src[t * token + c] : from_f32<T>(0.0f);
+        constexpr int kAhead = 8;  // loads in flight together
+        for (int i0 = threadIdx.x; i0 < TT * WIDE; i0 += kAhead * NT) {
+            T v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * NT, t = i / WIDE, c = i % WIDE;
+                v[k] = t < live && c < cols ? __ldg(src + t * token + c) : from_f32<T>(0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * NT < TT * WIDE)
+                    dst[i0 + k * NT] = v[k];
         }
     }
 }
@@ -217,17 +238,27 @@ __device__ __forceinline__ void store_quad(float* __restrict__ p, int valid, con
     }
 }
 
-// h and a of one token: a = exp(dt A), h = a h + u B with u = dt x.
-__device__ __forceinline__ void step(const float4& dt, const float4& u, const float4& B, const float2 (&A2)[2][4],
+// B or C of a thread's four states, each twice (one register pair per product): as they
+// lie in shared memory, which costs a read more and saves eight moves a token.
+struct Four {
+    float2 s[4];
+};
+__device__ __forceinline__ Four twice(const float2* p)
+{
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    return {{{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}}};
+}
+
+// One token: h = exp(dt A) h + u B with u = dt x.
+__device__ __forceinline__ void step(const float4& dt, const float4& u, const Four& B, const float2 (&A2)[2][4],
                                      float2 (&h)[2][4])
 {
     const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
-    const float b[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-            h[p][s] = fma2(decay(d[p], A2[p][s]), h[p][s], mul2(v[p], both(b[s])));
+            h[p][s] = fma2(decay(d[p], A2[p][s]), h[p][s], mul2(v[p], B.s[s]));
 }
 
 // Segments between their ends and their starts: S_{i+1} = exp(A sum dt_i) S_i + E_i.

@@ -49,7 +49,7 @@ template <int NS>
 struct Wide {
     using L = Lay<NS>;
     float dt[Seg<NS>::SUB][L::CT], u[Seg<NS>::SUB][L::CT], dy[Seg<NS>::SUB][L::CT];
-    float B[Seg<NS>::SUB][NS], C[Seg<NS>::SUB][NS];
+    float2 B[Seg<NS>::SUB][NS], C[Seg<NS>::SUB][NS];  // every number twice
 };
 
 template <typename T, int NS>
@@ -97,8 +97,13 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
 {
     using L = Lay<NS>;
     constexpr int SUB = Seg<NS>::SUB, CT = L::CT, V = 16 / (int)sizeof(T);
-    for (int i = threadIdx.x; i < SUB * CT / V; i += kThreads) {
-        const int t = i / (CT / V), c = i % (CT / V) * V;
+    const int c = threadIdx.x % (CT / V) * V;
+    float bias[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        bias[j] = in.bias && c + j < at.valid ? __ldg(in.bias + at.c0 + c + j) : 0.0f;
+#pragma unroll
+    for (int t = threadIdx.x / (CT / V); t < SUB; t += kThreads / (CT / V)) {
         auto vec = [&](const T* p) {
             Raw<T, V> r;
             r.w = *reinterpret_cast<const decltype(r.w)*>(p);
@@ -109,17 +114,8 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
             for (int j = 0; j < V; j += 4)
                 *reinterpret_cast<float4*>(p + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
         };
-        const Vec<V> d = vec(&raw.delta[t0 + t][c]), x = vec(&raw.x[t0 + t][c]);
-        const bool on = t0 + t < live;
-        float dt[V], u[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float r = d.f[j] + (in.bias && c + j < at.valid ? __ldg(in.bias + at.c0 + c + j) : 0.0f);
-            dt[j] = on ? (in.softplus ? softplus(r) : r) : 0.0f;
-            u[j] = dt[j] * x.f[j];
-        }
-        put(&w.dt[t][c], dt);
-        put(&w.u[t][c], u);
+        steps<V>(vec(&raw.delta[t0 + t][c]), vec(&raw.x[t0 + t][c]), bias, in.softplus, t0 + t < live, &w.dt[t][c],
+                 &w.u[t][c]);
         if constexpr (GRAD) {
             const Vec<V> o = vec(&raw.dout[t0 + t][c]);
             float dy[V];
@@ -127,7 +123,7 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
                 const Vec<V> z = vec(&raw.z[t0 + t][c]);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    dy[j] = o.f[j] * activate(z.f[j], LA_ACT_SILU).x;
+                    dy[j] = o.f[j] * activated(z.f[j], LA_ACT_SILU);
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -137,9 +133,9 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
         }
     }
     for (int i = threadIdx.x; i < SUB * NS; i += kThreads) {
-        w.B[0][i] = to_f32(raw.B[t0][i]);
+        w.B[0][i] = both(to_f32(raw.B[t0][i]));
         if constexpr (GRAD)
-            w.C[0][i] = to_f32(raw.C[t0][i]);
+            w.C[0][i] = both(to_f32(raw.C[t0][i]));
     }
 }
 
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(kThreads)
     using L = Lay<NS>;
     extern __shared__ __align__(16) unsigned char smem[];
     auto& sm = *reinterpret_cast<EndsSmem<T, NS>*>(smem);
-    const Place at = place_of<NS>(q, blockIdx.x);
+    const Place at = place_of(q, blockIdx.x, L::CT);
     const int64_t len = row_length(in.lengths, at.b, q.N), first = (int64_t)at.seg * q.seg_len;
     const int live = (int)max((int64_t)0, min((int64_t)q.seg_len, len - first));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,19 +184,17 @@ __global__ void __launch_bounds__(kThreads)
             const float4 dt = *reinterpret_cast<const float4*>(&sm.w.dt[t][c4]);
             const float4 u = *reinterpret_cast<const float4*>(&sm.w.u[t][c4]);
             const float4 dy = *reinterpret_cast<const float4*>(&sm.w.dy[t][c4]);
-            const float4 B = *reinterpret_cast<const float4*>(&sm.w.B[t][s4]);
-            const float4 Cr = *reinterpret_cast<const float4*>(&sm.w.C[t][s4]);
+            const Four B = twice(&sm.w.B[t][s4]), Cr = twice(&sm.w.C[t][s4]);
             const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
             const float2 y[2] = {{dy.x, dy.y}, {dy.z, dy.w}};
-            const float b[4] = {B.x, B.y, B.z, B.w}, c[4] = {Cr.x, Cr.y, Cr.z, Cr.w};
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const float2 a = decay(d[p], A2[p][s]);
-                    h[p][s] = fma2(a, h[p][s], mul2(v[p], both(b[s])));
+                    h[p][s] = fma2(a, h[p][s], mul2(v[p], B.s[s]));
                     P[p][s] = mul2(P[p][s], a);
-                    G[p][s] = fma2(P[p][s], mul2(y[p], both(c[s])), G[p][s]);
+                    G[p][s] = fma2(P[p][s], mul2(y[p], Cr.s[s]), G[p][s]);
                 }
         }
     }
@@ -286,7 +280,7 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int SUB = Seg<NS>::SUB, BLK = Seg<NS>::BLK;
     extern __shared__ __align__(16) unsigned char smem[];
     auto& sm = *reinterpret_cast<GradSmem<T, NS>*>(smem);
-    const Place at = place_of<NS>(q, blockIdx.x);
+    const Place at = place_of(q, blockIdx.x, L::CT);
     const int64_t len = row_length(in.lengths, at.b, q.N), first = (int64_t)at.seg * q.seg_len;
     const int here = (int)min((int64_t)q.seg_len, q.N - first);  // tokens of the segment
     const int live = (int)max((int64_t)0, min((int64_t)here, len - first));
@@ -342,7 +336,7 @@ __global__ void __launch_bounds__(kThreads)
                                     h[i / 2][i % 2 * 2 + 1].y);
             }
             step(*reinterpret_cast<const float4*>(&sm.w.dt[t][c4]), *reinterpret_cast<const float4*>(&sm.w.u[t][c4]),
-                 *reinterpret_cast<const float4*>(&sm.w.B[t][s4]), A2, h);
+                 twice(&sm.w.B[t][s4]), A2, h);
         }
     }
     // and back
@@ -367,15 +361,14 @@ __global__ void __launch_bounds__(kThreads)
                 const int t = blk * BLK + j;
                 const float4 dt = *reinterpret_cast<const float4*>(&sm.w.dt[t][c4]);
                 const float4 u = *reinterpret_cast<const float4*>(&sm.w.u[t][c4]);
-                const float4 B = *reinterpret_cast<const float4*>(&sm.w.B[t][s4]);
+                const Four B = twice(&sm.w.B[t][s4]);
                 const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
-                const float b[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         a[j][p][s] = decay(d[p], A2[p][s]);
-                        hs[j][p][s] = fma2(a[j][p][s], j ? hs[j ? j - 1 : 0][p][s] : base[p][s], mul2(v[p], both(b[s])));
+                        hs[j][p][s] = fma2(a[j][p][s], j ? hs[j ? j - 1 : 0][p][s] : base[p][s], mul2(v[p], B.s[s]));
                     }
             }
 #pragma unroll
@@ -384,22 +377,20 @@ __global__ void __launch_bounds__(kThreads)
                 const float4 dt = *reinterpret_cast<const float4*>(&sm.w.dt[t][c4]);
                 const float4 u = *reinterpret_cast<const float4*>(&sm.w.u[t][c4]);
                 const float4 dy = *reinterpret_cast<const float4*>(&sm.w.dy[t][c4]);
-                const float4 B = *reinterpret_cast<const float4*>(&sm.w.B[t][s4]);
-                const float4 Cr = *reinterpret_cast<const float4*>(&sm.w.C[t][s4]);
+                const Four B = twice(&sm.w.B[t][s4]), Cr = twice(&sm.w.C[t][s4]);
                 const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
                 const float2 e[2] = {{dy.x, dy.y}, {dy.z, dy.w}};
-                const float b[4] = {B.x, B.y, B.z, B.w}, c[4] = {Cr.x, Cr.y, Cr.z, Cr.w};
                 float2 y[2], w[2], ddt[2], dB[4], dC[4];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     y[p] = w[p] = ddt[p] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const float2 g = fma2(e[p], both(c[s]), ag[p][s]);
-                        w[p] = fma2(g, both(b[s]), w[p]);
+                        const float2 g = fma2(e[p], Cr.s[s], ag[p][s]);
+                        w[p] = fma2(g, B.s[s], w[p]);
                         dB[s] = p ? fma2(g, v[p], dB[s]) : mul2(g, v[p]);
                         dC[s] = p ? fma2(e[p], hs[j][p][s], dC[s]) : mul2(e[p], hs[j][p][s]);
-                        y[p] = fma2(hs[j][p][s], both(c[s]), y[p]);
+                        y[p] = fma2(hs[j][p][s], Cr.s[s], y[p]);
                         ag[p][s] = mul2(a[j][p][s], g);
                         const float2 qt = mul2(ag[p][s], j ? hs[j ? j - 1 : 0][p][s] : base[p][s]);
                         ddt[p] = fma2(qt, A2[p][s], ddt[p]);
