@@ -8,9 +8,10 @@
 //
 // x is token-major with any token and batch strides (a slice of a projection), y
 // head-major [B,H,N,C/H] (H = 1: token-major), so the transposition in front of
-// the attention calls costs no pass of its own.  A thread owns a vector of
-// channels and walks a run of tokens with the last W - 1 inputs in registers: each
-// tensor crosses HBM once, plus W - 1 rows per run that come from L2.
+// the attention calls costs no pass of its own.  A thread owns four neighbouring
+// channels, as two pairs in two-wide instructions, and walks a run of tokens with the
+// last W - 1 inputs in registers: each tensor crosses HBM once, plus W - 1 rows per run
+// that come from L2.
 #include "la_rows.cuh"
 
 namespace la {
@@ -19,39 +20,72 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // tokens whose loads are in flight together
 
 struct ConvShape {
     int64_t N, xb, xt;  // x strides in elements
     int C, H;
     int64_t runs;
-    int run;  // tokens per run, a multiple of kAhead
-    int act;
+    int run;  // tokens per run
 };
 
-// filters of V channels from weight [C][W]
+// V channels in pairs (V = 1: half a pair)
+template <int V>
+struct Pairs {
+    static constexpr int P = (V + 1) / 2;
+    float2 p[P];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pairs<V> pairs(const Raw<T, V>& r)
+{
+    const Vec<V> v = wide(r);
+    Pairs<V> q;
+    if constexpr (V == 1) {
+        q.p[0] = make_float2(v.f[0], 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            q.p[i] = make_float2(v.f[2 * i], v.f[2 * i + 1]);
+    }
+    return q;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* p, const Pairs<V>& q)
+{
+    Vec<V> v;
+    if constexpr (V == 1) {
+        v.f[0] = q.p[0].x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            v.f[2 * i] = q.p[i].x, v.f[2 * i + 1] = q.p[i].y;
+    }
+    store(p, v);
+}
+
+// filters of V channels from weight [C][W], and their biases
 template <int V, int W>
 __device__ __forceinline__ void load_filter(const float* __restrict__ weight, const float* __restrict__ bias, int c,
-                                            float (&w)[W][V], float (&b)[V])
+                                            Pairs<V> (&w)[W], Pairs<V>& b)
 {
+    float flat[2 * Pairs<V>::P * W] = {};  // neighbouring filters are neighbours in memory
     if constexpr (V > 1) {
-        float flat[V * W];  // neighbouring filters are neighbours in memory
 #pragma unroll
         for (int k = 0; k < V * W / 4; ++k) {
             const float4 q = __ldg(reinterpret_cast<const float4*>(weight + (int64_t)c * W) + k);
             flat[4 * k] = q.x, flat[4 * k + 1] = q.y, flat[4 * k + 2] = q.z, flat[4 * k + 3] = q.w;
         }
-#pragma unroll
-        for (int k = 0; k < V * W; ++k)
-            w[k % W][k / W] = flat[k];
     } else {
 #pragma unroll
         for (int j = 0; j < W; ++j)
-            w[j][0] = __ldg(weight + (int64_t)c * W + j);
+            flat[j] = __ldg(weight + (int64_t)c * W + j);
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        b[i] = bias ? __ldg(bias + c + i) : 0.0f;
+    for (int i = 0; i < Pairs<V>::P; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            w[j].p[i] = make_float2(flat[2 * i * W + j], flat[(2 * i + 1) * W + j]);
+        b.p[i] = make_float2(bias ? __ldg(bias + c + 2 * i) : 0.0f, bias && V > 1 ? __ldg(bias + c + 2 * i + 1) : 0.0f);
+    }
 }
 
 // Input at position p of row b, before the first token from the window, as it lies
@@ -74,11 +108,19 @@ __device__ __forceinline__ int64_t y_at(int64_t b, int64_t t, int c, const ConvS
     return ((b * s.H + h) * s.N + t) * dh + (c - h * dh);
 }
 
-template <typename T, int V, int W>
+// Tokens whose loads are in flight together.
+template <typename T>
+constexpr int ahead()
+{
+    return sizeof(T) == 2 ? 8 : 4;
+}
+
+template <typename T, int V, int W, int ACT>
 __global__ void __launch_bounds__(kThreads)
     k_conv(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
            T* __restrict__ y, const T* S0, T* S_out, const int* __restrict__ lengths, ConvShape s, int64_t items)
 {
+    constexpr int P = Pairs<V>::P, kAhead = ahead<T>();
     const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (item >= items)
         return;
@@ -86,18 +128,12 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t br = item / vecs, b = br / s.runs, r = br - b * s.runs;
     const int c = (int)(item - br * vecs) * V;
     const int64_t len = row_length(lengths, b, s.N);
-    float w[W][V], bs[V];
+    Pairs<V> w[W], bs, win[W];  // win: the last W - 1 inputs, then the new one
     load_filter<V, W>(weight, bias, c, w, bs);
-    int64_t t = r * s.run;
-    const int64_t end = min(s.N, t + s.run), live = min(end, len);
-    float win[W][V];  // the last W - 1 inputs, then the new one
+    const int64_t first = r * s.run, end = min(s.N, first + s.run), live = min(end, len);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const Vec<V> v = wide(input<T, V, W>(x, S0, b, t - (W - 1) + j, c, s));
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            win[j][i] = v.f[i];
-    }
+    for (int j = 0; j < W - 1; ++j)
+        win[j] = pairs(input<T, V, W>(x, S0, b, first - (W - 1) + j, c, s));
     if (r == 0 && S_out) {
         // the window after the last token; S_out may be S0, whose rows of these channels
         // this thread alone reads
@@ -109,47 +145,48 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < W - 1; ++j)
             *reinterpret_cast<Raw<T, V>*>(S_out + (b * (W - 1) + j) * s.C + c) = last[j];
     }
-    const T* xp = x + b * s.xb + t * s.xt + c;
-    T* yp = y + y_at(b, t, c, s);
     const int dh = s.C / s.H;
-    for (; t < live; t += kAhead, xp += kAhead * s.xt, yp += kAhead * dh) {
+    const T* xp = x + b * s.xb + first * s.xt + c;
+    T* yp = y + y_at(b, first, c, s);
+    auto token = [&](const Raw<T, V>& in) {
+        Pairs<V> o;
+        win[W - 1] = pairs(in);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float2 u = bs.p[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                u = fma2(w[j].p[i], win[j].p[i], u);
+            o.p[i] = value<ACT>(u);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            win[j] = win[j + 1];
+        store_pairs(yp, o);
+        yp += dh;
+    };
+    int left = (int)max((int64_t)0, live - first);
+    for (; left >= kAhead; left -= kAhead, xp += kAhead * s.xt) {
         Raw<T, V> in[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            in[k] = t + k < live ? fetch<T, V>(xp + k * s.xt) : none<T, V>();
+            in[k] = fetch<T, V>(xp + k * s.xt);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const Vec<V> v = wide(in[k]);
-            Vec<V> o;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                win[W - 1][i] = v.f[i];
-                float u = bs[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    u = fmaf(w[j][i], win[j][i], u);
-                o.f[i] = t + k < live ? activated(u, s.act) : 0.0f;
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    win[j][i] = win[j + 1][i];
-            }
-            if (t + k < end)
-                store(yp + k * dh, o);
-        }
+        for (int k = 0; k < kAhead; ++k)
+            token(in[k]);
     }
-    Vec<V> zero;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        zero.f[i] = 0.0f;
-    for (; t < end; ++t, yp += dh)
-        store(yp, zero);
+    for (; left > 0; --left, xp += s.xt)
+        token(fetch<T, V>(xp));
+    Pairs<V> zero = {};
+    for (int64_t t = max(first, live); t < end; ++t, yp += dh)
+        store_pairs(yp, zero);
 }
 
 // One token: y from the window and x, the window moved on in place.
-template <typename T, int V, int W>
+template <typename T, int V, int W, int ACT>
 __global__ void __launch_bounds__(kThreads)
     k_conv_step(T* __restrict__ S, const T* __restrict__ x, const float* __restrict__ weight,
-                const float* __restrict__ bias, T* __restrict__ y, int64_t xb, int C, int act, int64_t items)
+                const float* __restrict__ bias, T* __restrict__ y, int64_t xb, int C, int64_t items)
 {
     const int64_t item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (item >= items)
@@ -163,152 +200,151 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < W - 1; ++j)
         in[j] = *reinterpret_cast<const Raw<T, V>*>(win + (int64_t)j * C);
     in[W - 1] = fetch<T, V>(x + b * xb + c);
-    float w[W][V], u[V];
+    Pairs<V> w[W], u;
     load_filter<V, W>(weight, bias, c, w, u);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        const Vec<V> v = wide(in[j]);
+        const Pairs<V> v = pairs(in[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            u[i] = fmaf(w[j][i], v.f[i], u[i]);
+        for (int i = 0; i < Pairs<V>::P; ++i)
+            u.p[i] = fma2(w[j].p[i], v.p[i], u.p[i]);
     }
-    Vec<V> o;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        o.f[i] = activated(u[i], act);
-    store(y + b * C + c, o);
+    for (int i = 0; i < Pairs<V>::P; ++i)
+        u.p[i] = value<ACT>(u.p[i]);
+    store_pairs(y + b * C + c, u);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
         *reinterpret_cast<Raw<T, V>*>(win + (int64_t)j * C) = in[j + 1];
 }
 
-// Gradients.  A thread walks its runs forwards and holds the last W - 1 slopes du:
+// Gradients.  A thread walks its run forwards and holds the last W - 1 slopes du:
 // dx lags W - 1 tokens behind, so a run reads that many tokens of the next one.
 // dw and dbias stay in registers over all of a thread's runs; block row p leaves
 // part [p][W+1][C], summed in a fixed order by k_conv_dw (no atomics).
-template <typename T, int V, int W>
+template <typename T, int V, int W, int ACT>
 __global__ void __launch_bounds__(kThreads)
     k_conv_grad(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const T* __restrict__ S0, const T* __restrict__ dS_out,
                 const int* __restrict__ lengths, T* __restrict__ dx, T* __restrict__ dS0, float* __restrict__ part,
                 ConvShape s, int64_t jobs)
 {
+    constexpr int P = Pairs<V>::P, kAhead = 4;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
     if (c >= s.C)
         return;
-    float w[W][V], bs[V], dw[W][V], db[V];
+    Pairs<V> w[W], bs, dw[W] = {}, db = {};
     load_filter<V, W>(weight, bias, c, w, bs);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            dw[j][i] = 0.0f;
-    }
     const int dh = s.C / s.H;
     for (int64_t job = blockIdx.y; job < jobs; job += gridDim.y) {
         const int64_t b = job / s.runs, r = job - b * s.runs;
         const int64_t len = row_length(lengths, b, s.N);
         const int64_t first = r * s.run, end = min(s.N, first + s.run);
-        float win[W][V], du[W][V];  // inputs t-W+1 .. t; slopes of the same tokens
+        Pairs<V> win[W], du[W] = {};  // inputs t-W+1 .. t; slopes of the same tokens
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int64_t p = first - (W - 1) + j;  // not behind the row's last: nothing is known of that
-            const Vec<V> v = wide(p < len ? input<T, V, W>(x, S0, b, p, c, s) : none<T, V>());
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                win[j][i] = v.f[i], du[j + 1][i] = 0.0f;
+            win[j] = pairs(p < len ? input<T, V, W>(x, S0, b, p, c, s) : none<T, V>());
         }
-        const T* xp = x + b * s.xb + c;
-        const T* dp = dy + y_at(b, 0, c, s);
-        T* out = dx + b * s.N * s.C + c;
-        // token t gives du_t and, W - 1 behind, dx; the row's first run also walks back
-        // into the window (positions before 0)
-        for (int64_t t = first; t < end + W - 1; t += kAhead) {
+        // From token t, its inputs x and dy and whether dw takes it: du_t, and dx of the token
+        // W - 1 before.
+        auto token = [&](const Raw<T, V>& xin, const Raw<T, V>& din, bool own) {
+            win[W - 1] = pairs(xin);
+            const Pairs<V> d = pairs(din);
+            Pairs<V> o;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float2 u = bs.p[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    u = fma2(w[j].p[i], win[j].p[i], u);
+                const float2 g = mul2(d.p[i], slope<ACT>(u)), t = own ? g : both(0.0f);
+                db.p[i] = add2(db.p[i], t);
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    dw[j].p[i] = fma2(t, win[j].p[i], dw[j].p[i]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+                    du[j].p[i] = du[j + 1].p[i], win[j].p[i] = win[j + 1].p[i];
+                du[W - 1].p[i] = g;
+                o.p[i] = mul2(w[W - 1].p[i], du[0].p[i]);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+                    o.p[i] = fma2(w[j].p[i], du[W - 1 - j].p[i], o.p[i]);
+            }
+            return o;
+        };
+        const T* xp = x + b * s.xb + first * s.xt + c;
+        const T* dp = dy + y_at(b, first, c, s);
+        T* out = dx + (b * s.N + first) * s.C + c;
+        // the edges: a run's first W - 1 tokens, of which the row's first run passes what lies
+        // before them to the window, and its end, where tokens may be missing, dx may end and
+        // the final window (positions len - W + 1 .. len - 1) adds its gradient
+        auto edge = [&](int64_t t) {
+            const bool on = t < len && t < s.N;
+            Pairs<V> o = token(on ? fetch<T, V>(xp) : none<T, V>(), on ? fetch<T, V>(dp) : none<T, V>(), t < end);
+            xp += s.xt, dp += dh;
+            const int64_t at = t - (W - 1), row = at - (len - (W - 1));
+            if (at < first && (r > 0 || !dS0))
+                return;
+            if (dS_out && row >= 0 && row < W - 1) {
+                const Pairs<V> g = pairs(fetch<T, V>(dS_out + (b * (W - 1) + row) * s.C + c));
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    o.p[i] = add2(o.p[i], g.p[i]);
+            }
+            if (at >= first) {
+                store_pairs(out, o);
+                out += s.C;
+            } else {
+                store_pairs(dS0 + (b * (W - 1) + at + W - 1) * s.C + c, o);
+            }
+        };
+        int64_t t = first;
+        for (; t < first + W - 1; ++t)
+            edge(t);
+        // whole groups of tokens of this run, none of them near the row's end
+        for (; t + kAhead <= min(end, len); t += kAhead) {
             Raw<T, V> xin[kAhead], din[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const bool on = t + k < len && t + k < end + W - 1;
-                xin[k] = on ? fetch<T, V>(xp + (t + k) * s.xt) : none<T, V>();
-                din[k] = on ? fetch<T, V>(dp + (t + k) * dh) : none<T, V>();
+                xin[k] = fetch<T, V>(xp), din[k] = fetch<T, V>(dp);
+                xp += s.xt, dp += dh;
             }
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const Vec<V> v = wide(xin[k]), d = wide(din[k]);
-                Vec<V> o;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    win[W - 1][i] = v.f[i];
-                    float u = bs[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        u = fmaf(w[j][i], win[j][i], u);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-                        du[j][i] = du[j + 1][i];
-                    const float g = t + k < len ? d.f[i] * activate(u, s.act).y : 0.0f;
-                    du[W - 1][i] = g;
-                    if (t + k < end) {
-                        db[i] += g;
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            dw[j][i] = fmaf(g, win[j][i], dw[j][i]);
-                    }
-                    o.f[i] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-                        o.f[i] = fmaf(w[j][i], du[W - 1 - j][i], o.f[i]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-                        win[j][i] = win[j + 1][i];
-                }
-                const int64_t at = t + k - (W - 1);
-                if (at >= end || (at < first && (r > 0 || !dS0)))
-                    continue;
-                // the final window holds positions len - W + 1 .. len - 1
-                const int64_t row = at - (len - (W - 1));
-                if (dS_out && row >= 0 && row < W - 1) {
-                    const Vec<V> g = wide(fetch<T, V>(dS_out + (b * (W - 1) + row) * s.C + c));
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        o.f[i] += g.f[i];
-                }
-                if (at >= first)
-                    store(out + at * s.C, o);
-                else if (at >= -(W - 1))
-                    store(dS0 + (b * (W - 1) + at + W - 1) * s.C + c, o);
-            }
+            for (int k = 0; k < kAhead; ++k, out += s.C)
+                store_pairs(out, token(xin[k], din[k], true));
         }
+        for (; t < end + W - 1; ++t)
+            edge(t);
     }
     float* p = part + (int64_t)blockIdx.y * (W + 1) * s.C + c;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        p[(int64_t)W * s.C + i] = db[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            p[(int64_t)j * s.C + i] = dw[j][i];
+    for (int j = 0; j <= W; ++j) {
+        const Pairs<V>& q = j < W ? dw[j < W ? j : 0] : db;
+        store_pairs(p + (int64_t)j * s.C, q);
     }
 }
 
-// dw [C][W] and dbias [C] from the parts: 32 channels x 8 partial sums per block.
-__global__ void __launch_bounds__(256)
+// dw [C][W] and dbias [C] from the parts: 32 channels x 32 partial sums per block.
+__global__ void __launch_bounds__(1024)
     k_conv_dw(const float* __restrict__ part, float* __restrict__ dw, float* __restrict__ dbias, int parts, int W,
               int C)
 {
-    __shared__ float sums[8][33];
+    __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, j = blockIdx.y;
     float x = 0.f;
     if (c < C) {
 #pragma unroll 4
-        for (int p = grp; p < parts; p += 8)
+        for (int p = grp; p < parts; p += 32)
             x += part[((int64_t)p * (W + 1) + j) * C + c];
     }
     sums[grp][lane] = x;
     __syncthreads();
     if (grp == 0 && c < C) {
         x = 0.f;
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 32; ++i)
             x += sums[i][lane];
         if (j < W)
             dw[(int64_t)c * W + j] = x;
@@ -317,101 +353,109 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Tokens per run: long enough that the W - 1 rows read twice are few, short enough
-// that the GPU is full.
+// Tokens per run of the forward: long enough that the W - 1 rows read twice are few, short
+// enough that the GPU is full.
 int run_length(const ConvArgs& a, int vec)
 {
     const int64_t vecs = a.C / vec * a.B;
     int run = 64;
-    while (run > kAhead && vecs * ((a.N + run - 1) / run) < 152 * 1024)
+    while (run > 4 && vecs * ((a.N + run - 1) / run) < 152 * 1024)
         run /= 2;
     return run;
 }
 
+// Block rows of the gradient, four blocks an SM in all, and their runs: one for each where
+// there are no more sequences than block rows, eight tokens at least.
+int64_t grad_rows(const ConvArgs& a, int vec)
+{
+    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads, rows = 152 * 4 / cols;
+    return rows > 1 ? rows : 1;
+}
+int grad_run(const ConvArgs& a, int64_t rows)
+{
+    const int64_t runs = rows > a.B ? rows / a.B : 1, run = (a.N + runs - 1) / runs;
+    return (int)(run > 8 ? run : 8);
+}
+
 bool vectors(const ConvArgs& a, int es, bool step)
 {
-    const int v = 16 / es;
-    return a.C % v == 0 && (a.C / a.H) % v == 0 && rows16(a.x, a.xb, step ? 0 : a.xt, es);
+    return a.C / a.H % 4 == 0 && rows_on(a.x, a.xb, step ? 0 : a.xt, es, 4 * es);
 }
 
-// Block rows of the gradient, for any vector width: the parts are sized by them.
-int64_t grad_rows(const ConvArgs& a, int vec, int64_t jobs)
-{
-    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads;
-    const int64_t want = (152 * 4 + cols - 1) / cols;
-    return want < jobs ? want : jobs;
-}
-
-ConvShape shape_of(const ConvArgs& a, int run)
-{
-    ConvShape s;
-    s.N = a.N, s.xb = a.xb, s.xt = a.xt, s.C = (int)a.C, s.H = (int)a.H, s.run = run;
-    s.runs = (a.N + run - 1) / run, s.act = a.act;
-    return s;
-}
-
-template <typename T, int V, int W>
+template <typename T, int V, int W, int ACT>
 cudaError_t run_conv(const ConvArgs& a, int mode)
 {
     const T *x = static_cast<const T*>(a.x), *S0 = static_cast<const T*>(a.S0);
     if (mode == 1) {
         const int64_t items = a.B * (a.C / V);
-        k_conv_step<T, V, W><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, a.stream>>>(
-            static_cast<T*>(a.S_out), x, a.weight, a.bias, static_cast<T*>(a.y), a.xb, (int)a.C, a.act, items);
+        k_conv_step<T, V, W, ACT><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, a.stream>>>(
+            static_cast<T*>(a.S_out), x, a.weight, a.bias, static_cast<T*>(a.y), a.xb, (int)a.C, items);
         count_launches(1);
         return cudaGetLastError();
     }
-    const ConvShape s = shape_of(a, run_length(a, V));
+    ConvShape s;
+    const int64_t rows = grad_rows(a, V);
+    s.N = a.N, s.xb = a.xb, s.xt = a.xt, s.C = (int)a.C, s.H = (int)a.H;
+    s.run = mode == 0 ? run_length(a, V) : grad_run(a, rows);
+    s.runs = (a.N + s.run - 1) / s.run;
     const int64_t jobs = a.B * s.runs;
     if (mode == 0) {
         const int64_t items = jobs * (a.C / V);
-        k_conv<T, V, W><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, a.stream>>>(
+        k_conv<T, V, W, ACT><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, a.stream>>>(
             x, a.weight, a.bias, static_cast<T*>(a.y), S0, static_cast<T*>(a.S_out), a.lengths, s, items);
         count_launches(1);
         return cudaGetLastError();
     }
-    const int rows = (int)grad_rows(a, V, jobs);
-    const dim3 grid((unsigned)((a.C / V + kThreads - 1) / kThreads), (unsigned)rows);
+    const int parts = (int)(rows < jobs ? rows : jobs);
+    const dim3 grid((unsigned)((a.C / V + kThreads - 1) / kThreads), (unsigned)parts);
     float* part = static_cast<float*>(a.ws);
-    k_conv_grad<T, V, W><<<grid, kThreads, 0, a.stream>>>(
+    k_conv_grad<T, V, W, ACT><<<grid, kThreads, 0, a.stream>>>(
         static_cast<const T*>(a.dy), x, a.weight, a.bias, S0, static_cast<const T*>(a.dS_out), a.lengths,
         static_cast<T*>(a.dx), static_cast<T*>(a.dS0), part, s, jobs);
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    k_conv_dw<<<dim3((unsigned)((a.C + 31) / 32), W + 1), 256, 0, a.stream>>>(part, a.dweight, a.dbias, rows, W,
-                                                                              (int)a.C);
+    k_conv_dw<<<dim3((unsigned)((a.C + 31) / 32), W + 1), 1024, 0, a.stream>>>(part, a.dweight, a.dbias, parts, W,
+                                                                               (int)a.C);
     count_launches(1);
     return cudaGetLastError();
+}
+
+template <typename T, int V, int W>
+cudaError_t conv_act(const ConvArgs& a, int mode)
+{
+    switch (a.act) {
+    case LA_ACT_SILU: return run_conv<T, V, W, LA_ACT_SILU>(a, mode);
+    case LA_ACT_SIGMOID: return run_conv<T, V, W, LA_ACT_SIGMOID>(a, mode);
+    default: return run_conv<T, V, W, LA_ACT_NONE>(a, mode);
+    }
 }
 
 template <typename T, int V>
 cudaError_t conv_taps(const ConvArgs& a, int mode)
 {
     switch (a.W) {
-    case 2: return run_conv<T, V, 2>(a, mode);
-    case 3: return run_conv<T, V, 3>(a, mode);
-    default: return run_conv<T, V, 4>(a, mode);
+    case 2: return conv_act<T, V, 2>(a, mode);
+    case 3: return conv_act<T, V, 3>(a, mode);
+    default: return conv_act<T, V, 4>(a, mode);
     }
 }
 
 cudaError_t conv_types(const ConvArgs& a, int mode)
 {
     if (a.dtype == LA_BF16)
-        return vectors(a, 2, mode == 1) ? conv_taps<__nv_bfloat16, 8>(a, mode) : conv_taps<__nv_bfloat16, 1>(a, mode);
+        return vectors(a, 2, mode == 1) ? conv_taps<__nv_bfloat16, 4>(a, mode) : conv_taps<__nv_bfloat16, 1>(a, mode);
     return vectors(a, 4, mode == 1) ? conv_taps<float, 4>(a, mode) : conv_taps<float, 1>(a, mode);
 }
 
 }  // namespace
 
-// Block rows are most with the widest vectors (fewest column blocks).
+// Block rows are most with vectors (fewest column blocks).
 size_t conv_backward_workspace(const ConvArgs& a)
 {
-    const int vec = a.dtype == LA_BF16 ? 8 : 4;
-    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads;
-    const int64_t most = 152 * 4 / (cols > 0 ? cols : 1) + 1, jobs = a.B * ((a.N + kAhead - 1) / kAhead);
-    return sizeof(float) * (size_t)(most < jobs ? most : jobs) * (a.W + 1) * a.C;
+    const int64_t rows = grad_rows(a, 4);
+    return sizeof(float) * (size_t)rows * (a.W + 1) * a.C;
 }
 
 cudaError_t conv_forward(const ConvArgs& a) { return conv_types(a, 0); }

@@ -7,14 +7,13 @@
 namespace la {
 namespace rows {
 
-// V neighbouring channels: 16 bytes where every row starts on a 16-byte boundary,
-// else one element.
+// V neighbouring channels as they lie in memory.
 template <typename T, int V> struct Raw;
 template <> struct Raw<float, 4> {
     float4 w;
 };
-template <> struct Raw<__nv_bfloat16, 8> {
-    uint4 w;
+template <> struct Raw<__nv_bfloat16, 4> {
+    uint2 w;
 };
 template <> struct Raw<float, 1> {
     float w;
@@ -47,16 +46,10 @@ struct Vec {
 __device__ __forceinline__ Vec<4> wide(const Raw<float, 4>& x) { return {{x.w.x, x.w.y, x.w.z, x.w.w}}; }
 __device__ __forceinline__ Vec<1> wide(const Raw<float, 1>& x) { return {{x.w}}; }
 __device__ __forceinline__ Vec<1> wide(const Raw<__nv_bfloat16, 1>& x) { return {{__bfloat162float(x.w)}}; }
-__device__ __forceinline__ Vec<8> wide(const Raw<__nv_bfloat16, 8>& x)
+__device__ __forceinline__ Vec<4> wide(const Raw<__nv_bfloat16, 4>& x)
 {
-    Vec<8> r;
-    const uint32_t u[4] = {x.w.x, x.w.y, x.w.z, x.w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.f[2 * i] = __uint_as_float(u[i] << 16);
-        r.f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-    return r;
+    return {{__uint_as_float(x.w.x << 16), __uint_as_float(x.w.x & 0xffff0000u), __uint_as_float(x.w.y << 16),
+             __uint_as_float(x.w.y & 0xffff0000u)}};
 }
 
 __device__ __forceinline__ void store(float* p, const Vec<4>& r)
@@ -65,42 +58,88 @@ __device__ __forceinline__ void store(float* p, const Vec<4>& r)
 }
 __device__ __forceinline__ void store(float* p, const Vec<1>& r) { *p = r.f[0]; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, const Vec<1>& r) { *p = __float2bfloat16_rn(r.f[0]); }
-__device__ __forceinline__ void store(__nv_bfloat16* p, const Vec<8>& r)
+__device__ __forceinline__ void store(__nv_bfloat16* p, const Vec<4>& r)
 {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(r.f[2 * i], r.f[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(r.f[0], r.f[1]), b = __floats2bfloat162_rn(r.f[2], r.f[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// sigmoid(g) and its slope from e = exp(-|g|), so that neither 1 - s nor the
-// exponential of a large number is formed.
-__device__ __forceinline__ float2 sigmoid_slope(float g)
+// Pairs of fp32 in one instruction, and the same for one.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
-    return make_float2(g >= 0.0f ? r : e * r, e * r * r);
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x and 1/x in hardware, a few 2^-24 off; what is under the smallest normal number is zero.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// act(u) and act'(u)
-__device__ __forceinline__ float2 activate(float u, int act)
+// sigmoid(u) = 1 / (1 + e), e = exp(-u), and 1 - sigmoid(u) = e sigmoid(u), which keeps its
+// digits where the difference would not.  u is held above -87, where e is still finite: what
+// lies under it has results under 1e-35.
+struct Sigmoid {
+    float2 u, s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float2 u)
 {
-    if (act == LA_ACT_NONE)
-        return make_float2(u, 1.0f);
-    const float2 s = sigmoid_slope(u);
-    return act == LA_ACT_SIGMOID ? s : make_float2(u * s.x, fmaf(u, s.y, s.x));
+    u = make_float2(fmaxf(u.x, -87.0f), fmaxf(u.y, -87.0f));
+    const float2 t = mul2(u, both(-kLog2e)), e = make_float2(ex2(t.x), ex2(t.y)), q = add2(e, both(1.0f));
+    const float2 s = make_float2(rcp(q.x), rcp(q.y));
+    return {u, s, mul2(e, s)};
 }
 
-// act(u) alone.  The exponential of a large -u is infinite and its quotient zero: under
-// u = -87 the result is 0 in place of less than 1e-36.
-__device__ __forceinline__ float activated(float u, int act)
+// act(u), and act'(u)
+template <int ACT>
+__device__ __forceinline__ float2 value(float2 u)
 {
-    if (act == LA_ACT_NONE)
+    if (ACT == LA_ACT_NONE)
         return u;
-    const float s = __fdividef(1.0f, 1.0f + __expf(-u));
-    return act == LA_ACT_SIGMOID ? s : u * s;
+    const Sigmoid g = sigmoid(u);
+    return ACT == LA_ACT_SIGMOID ? g.s : mul2(g.u, g.s);
+}
+template <int ACT>
+__device__ __forceinline__ float2 slope(float2 u)
+{
+    if (ACT == LA_ACT_NONE)
+        return both(1.0f);
+    const Sigmoid g = sigmoid(u);
+    return mul2(g.s, ACT == LA_ACT_SIGMOID ? g.rest : fma2(g.u, g.rest, both(1.0f)));
 }
 
 // Tokens of row b: lengths clamped to 0 .. N, or N.
@@ -112,10 +151,11 @@ __device__ __forceinline__ int64_t row_length(const int* lengths, int64_t b, int
     return n < 0 ? 0 : n < N ? n : N;
 }
 
-// Whether pointer and strides (in elements) put every row on a 16-byte boundary.
-inline bool rows16(const void* p, int64_t batch, int64_t token, int es)
+// Whether pointer and strides (in elements of es bytes) put every row on a boundary of
+// `bytes` (a power of two).
+inline bool rows_on(const void* p, int64_t batch, int64_t token, int es, unsigned bytes)
 {
-    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(batch * es) | (uintptr_t)(token * es)) & 15u) == 0;
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(batch * es) | (uintptr_t)(token * es)) & (bytes - 1)) == 0;
 }
 
 }  // namespace rows

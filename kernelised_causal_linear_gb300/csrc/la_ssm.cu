@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(Cut<T, NS>::NT)
                 float2 o = fma2(D, x, make_float2(y[0].x + y[0].y, y[1].x + y[1].y));
                 if (zs) {
                     const float2 z = two(&sm.z[k][t][c2]);
-                    o = mul2(o, make_float2(activated(z.x, LA_ACT_SILU), activated(z.y, LA_ACT_SILU)));
+                    o = mul2(o, value<LA_ACT_SILU>(z));
                 }
                 if (ASYNC && have == 2) {  // rows of an even number of channels
                     put_two(po, o);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Cut<T, NS>::NT)
                     o += __shfl_xor_sync(0xffffffffu, o, 2);
                 o = fmaf(odd ? D.y : D.x, odd ? x.y : x.x, o);
                 if (zs)
-                    o *= activated(to_f32(sm.z[k][t][c2 + odd]), LA_ACT_SILU);
+                    o *= value<LA_ACT_SILU>(both(to_f32(sm.z[k][t][c2 + odd]))).x;
                 if (part < 2 && have > odd)
                     po[odd] = from_f32<T>(o);
             }
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256)
         if (in.D)
             y = fmaf(__ldg(in.D + c), x, y);
         if (in.z.p)
-            y *= activated(to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]), LA_ACT_SILU);
+            y *= value<LA_ACT_SILU>(both(to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]))).x;
         out[b * C + c] = from_f32<T>(y);
     }
 }
@@ -376,9 +376,9 @@ cudaError_t run_ssm(const SsmArgs& a)
     Ins in{{a.x, a.x_batch, a.x_token}, {a.delta, a.delta_batch, a.delta_token}, {a.Bm, a.B_batch, a.B_token},
            {a.Cm, a.C_batch, a.C_token}, {a.z, a.z_batch, a.z_token}, a.A, a.D, a.bias, a.lengths, a.softplus};
     const int es = (int)sizeof(T);
-    const bool async = rows16(a.x, a.x_batch, a.x_token, es) && rows16(a.delta, a.delta_batch, a.delta_token, es) &&
-                       rows16(a.Bm, a.B_batch, a.B_token, es) && rows16(a.Cm, a.C_batch, a.C_token, es) &&
-                       (!a.z || rows16(a.z, a.z_batch, a.z_token, es)) && a.C / a.G * es % 16 == 0;
+    const bool async = rows_on(a.x, a.x_batch, a.x_token, es, 16) && rows_on(a.delta, a.delta_batch, a.delta_token, es, 16) &&
+                       rows_on(a.Bm, a.B_batch, a.B_token, es, 16) && rows_on(a.Cm, a.C_batch, a.C_token, es, 16) &&
+                       (!a.z || rows_on(a.z, a.z_batch, a.z_token, es, 16)) && a.C / a.G * es % 16 == 0;
     const unsigned blocks = (unsigned)(a.B * q.segs * q.G * q.per_group);
     float* ends = static_cast<float*>(a.ws);
     float* sums = ends + a.B * q.segs * a.C * NS;

@@ -52,38 +52,12 @@ struct Rows {
     int64_t batch, token;
 };
 
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
-// 2^x in hardware, 2.4 * 2^-24 at most off relative to the result; results under the
-// smallest normal number are zero.
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
+using rows::add2;
+using rows::both;
+using rows::ex2;
+using rows::fma2;
+using rows::kLog2e;
+using rows::mul2;
 
 // The decay 2^(dt A2), A2 = A log2(e).  The hardware exponential is low by 0.1 (arguments
 // above -2^-9) to 0.46 * 2^-24 in the mean, which a state that remembers a thousand tokens
@@ -105,7 +79,7 @@ __device__ __forceinline__ float2 decay(float2 dt, float2 A2)
 __device__ __forceinline__ float2 softplus(float2 u)
 {
     const float2 e = make_float2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
-    const float2 w = make_float2(__fdividef(e.x, 2.0f + e.x), __fdividef(e.y, 2.0f + e.y)), q = mul2(w, w);
+    const float2 f = add2(e, both(2.0f)), w = mul2(e, make_float2(rows::rcp(f.x), rows::rcp(f.y))), q = mul2(w, w);
     float2 s = fma2(q, both(0.134257495f), both(0.141183093f));
     s = fma2(s, q, both(0.200037807f));
     s = fma2(s, q, both(0.333333194f));

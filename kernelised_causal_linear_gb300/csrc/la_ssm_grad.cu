@@ -96,7 +96,7 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
                                       int live)
 {
     using L = Lay<NS>;
-    constexpr int SUB = Seg<NS>::SUB, CT = L::CT, V = 16 / (int)sizeof(T);
+    constexpr int SUB = Seg<NS>::SUB, CT = L::CT, V = 4;
     const int c = threadIdx.x % (CT / V) * V;
     float bias[V];
 #pragma unroll
@@ -122,8 +122,10 @@ __device__ __forceinline__ void widen(const RawSeg<T, NS>& raw, Wide<NS>& w, con
             if (in.z.p) {
                 const Vec<V> z = vec(&raw.z[t0 + t][c]);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    dy[j] = o.f[j] * activated(z.f[j], LA_ACT_SILU);
+                for (int j = 0; j < V; j += 2) {
+                    const float2 g = value<LA_ACT_SILU>(make_float2(z.f[j], z.f[j + 1]));
+                    dy[j] = o.f[j] * g.x, dy[j + 1] = o.f[j + 1] * g.y;
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j)
@@ -423,15 +425,17 @@ __global__ void __launch_bounds__(kThreads)
                     float vx = 0.f, vd = 0.f, vz = 0.f;
                     if (ts < live) {
                         const float x = to_f32(sm.raw.x[ts][co + i]), dyo = sm.w.dy[t][co + i];
-                        const float slope =
-                            in.softplus ? sigmoid_slope(to_f32(sm.raw.delta[ts][co + i]) + bias[i]).x : 1.0f;
+                        // the slopes of the step and of the gate, side by side
+                        const float zr = dz ? to_f32(sm.raw.z[ts][co + i]) : 0.f;
+                        const Sigmoid sg = sigmoid(make_float2(to_f32(sm.raw.delta[ts][co + i]) + bias[i], zr));
+                        const float slope = in.softplus ? sg.s.x : 1.0f;
                         vx = fmaf(sm.w.dt[t][co + i], wo[i], Dv[i] * dyo);
                         vd = fmaf(x, wo[i], to[i] * 0.6931471805599453f) * slope;
                         dD[i] = fmaf(dyo, x, dD[i]);
                         dbias[i] += vd;
                         if (dz)
-                            vz = to_f32(sm.raw.dout[ts][co + i]) * fmaf(Dv[i], x, yo[i]) *
-                                 activate(to_f32(sm.raw.z[ts][co + i]), LA_ACT_SILU).y;
+                            vz = to_f32(sm.raw.dout[ts][co + i]) * fmaf(Dv[i], x, yo[i]) * sg.s.y *
+                                 fmaf(sg.u.y, sg.rest.y, 1.0f);
                     }
                     dx[o] = from_f32<T>(vx);
                     ddelta[o] = from_f32<T>(vd);
@@ -603,7 +607,7 @@ cudaError_t grad_rows(const SsmArgs& a)
                      {a.dout, a.dout_batch, a.dout_token}, a.A, a.D, a.bias, a.lengths, a.softplus};
     bool async = a.C / a.G * (int)sizeof(T) % 16 == 0;
     for (const Rows& r : {in.x, in.delta, in.B, in.C, in.z, in.dout})
-        async = async && (!r.p || rows16(r.p, r.batch, r.token, (int)sizeof(T)));
+        async = async && (!r.p || rows_on(r.p, r.batch, r.token, (int)sizeof(T), 16));
     const Grid q = grid_of<NS>(a);
     return async ? run_grad<T, NS, true>(a, in, q) : run_grad<T, NS, false>(a, in, q);
 }
