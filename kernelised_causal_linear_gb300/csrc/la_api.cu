@@ -743,7 +743,7 @@ static la_status check_ssm(const SsmArgs& a)
     // group; threads of the sums and of a step
     const double tiles = (double)a.G * ((double)(a.C / a.G) / 32 + 1);
     if ((double)a.B * ((double)a.N / 8 + 1) * tiles > INT32_MAX ||
-        (double)a.B * a.C * a.n / 128 + 1 > INT32_MAX || (double)a.B * a.N * a.G * a.n / 128 + 1 > INT32_MAX)
+        (double)a.B * ((double)a.C * a.n / 128 + 1) > INT32_MAX || (double)a.B * a.N * a.G * a.n / 128 + 1 > INT32_MAX)
         return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }

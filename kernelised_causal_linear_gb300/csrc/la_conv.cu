@@ -108,10 +108,13 @@ __device__ __forceinline__ int64_t y_at(int64_t b, int64_t t, int c, const ConvS
     return ((b * s.H + h) * s.N + t) * dh + (c - h * dh);
 }
 
-// Tokens whose loads are in flight together.
+// Tokens whose loads are issued together, one group ahead of the one in use (bf16 B4 N8192
+// C4096: eight with none ahead 114 us, eight and one group ahead with streaming loads 100 us,
+// sixteen 101 us; the same bytes in fp32 87 us).
 template <typename T>
 constexpr int ahead()
 {
+    
     return sizeof(T) == 2 ? 8 : 4;
 }
 
@@ -166,14 +169,28 @@ __global__ void __launch_bounds__(kThreads)
         yp += dh;
     };
     int left = (int)max((int64_t)0, live - first);
-    for (; left >= kAhead; left -= kAhead, xp += kAhead * s.xt) {
-        Raw<T, V> in[kAhead];
+    // the next group is on its way while this one is used
+    Raw<T, V> in[2][kAhead];
+    auto group = [&](Raw<T, V> (&g)[kAhead]) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            in[k] = fetch<T, V>(xp + k * s.xt);
+            g[k] = fetch<T, V>(xp + k * s.xt);
+        xp += kAhead * s.xt;
+    };
+    if (left >= kAhead)
+        group(in[0]);
+    while (left >= kAhead) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            token(in[k]);
+        for (int half = 0; half < 2; ++half) {
+            if (left < kAhead)
+                break;
+            left -= kAhead;
+            if (left >= kAhead)
+                group(in[half ^ 1]);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                token(in[half][k]);
+        }
     }
     for (; left > 0; --left, xp += s.xt)
         token(fetch<T, V>(xp));
@@ -222,14 +239,20 @@ __global__ void __launch_bounds__(kThreads)
 // dx lags W - 1 tokens behind, so a run reads that many tokens of the next one.
 // dw and dbias stay in registers over all of a thread's runs; block row p leaves
 // part [p][W+1][C], summed in a fixed order by k_conv_dw (no atomics).
+// Bound by HBM's latency: four blocks an SM, which 128 registers allow, with two groups of
+// tokens in flight (bf16 B4 N8192 C2048: three blocks 131 us, four 80 us, five with spills 101
+// us; groups of two, four and six tokens 95, 80 and 89 us; the same bytes in fp32 with two 74 us).
+constexpr int kGradPerSm = 4;
+
 template <typename T, int V, int W, int ACT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kGradPerSm)
     k_conv_grad(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ weight,
                 const float* __restrict__ bias, const T* __restrict__ S0, const T* __restrict__ dS_out,
                 const int* __restrict__ lengths, T* __restrict__ dx, T* __restrict__ dS0, float* __restrict__ part,
                 ConvShape s, int64_t jobs)
 {
-    constexpr int P = Pairs<V>::P, kAhead = 4;
+    
+    constexpr int P = Pairs<V>::P, kAhead = sizeof(T) == 2 ? 4 : 2;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
     if (c >= s.C)
         return;
@@ -304,16 +327,29 @@ __global__ void __launch_bounds__(kThreads)
         for (; t < first + W - 1; ++t)
             edge(t);
         // whole groups of tokens of this run, none of them near the row's end
-        for (; t + kAhead <= min(end, len); t += kAhead) {
-            Raw<T, V> xin[kAhead], din[kAhead];
+        Raw<T, V> xin[2][kAhead], din[2][kAhead];
+        auto group = [&](Raw<T, V> (&a)[kAhead], Raw<T, V> (&b)[kAhead]) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                xin[k] = fetch<T, V>(xp), din[k] = fetch<T, V>(dp);
+                a[k] = fetch<T, V>(xp), b[k] = fetch<T, V>(dp);
                 xp += s.xt, dp += dh;
             }
+        };
+        int left = (int)(max(t, min(end, len)) - t);
+        if (left >= kAhead)
+            group(xin[0], din[0]);
+        while (left >= kAhead) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k, out += s.C)
-                store_pairs(out, token(xin[k], din[k], true));
+            for (int half = 0; half < 2; ++half) {
+                if (left < kAhead)
+                    break;
+                left -= kAhead, t += kAhead;
+                if (left >= kAhead)
+                    group(xin[half ^ 1], din[half ^ 1]);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k, out += s.C)
+                    store_pairs(out, token(xin[half][k], din[half][k], true));
+            }
         }
         for (; t < end + W - 1; ++t)
             edge(t);
@@ -358,7 +394,7 @@ __global__ void __launch_bounds__(1024)
 int run_length(const ConvArgs& a, int vec)
 {
     const int64_t vecs = a.C / vec * a.B;
-    int run = 64;
+    int run = 128;
     while (run > 4 && vecs * ((a.N + run - 1) / run) < 152 * 1024)
         run /= 2;
     return run;
@@ -368,7 +404,7 @@ int run_length(const ConvArgs& a, int vec)
 // there are no more sequences than block rows, eight tokens at least.
 int64_t grad_rows(const ConvArgs& a, int vec)
 {
-    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads, rows = 152 * 4 / cols;
+    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads, rows = kGradPerSm * 152 / cols;
     return rows > 1 ? rows : 1;
 }
 int grad_run(const ConvArgs& a, int64_t rows)

@@ -26,7 +26,7 @@ template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> fetch(const T* p)
 {
     Raw<T, V> r;
-    r.w = __ldg(reinterpret_cast<const decltype(r.w)*>(p));
+    r.w = __ldcs(reinterpret_cast<const decltype(r.w)*>(p));
     return r;
 }
 
@@ -130,8 +130,10 @@ __device__ __forceinline__ float2 value(float2 u)
 {
     if (ACT == LA_ACT_NONE)
         return u;
-    const Sigmoid g = sigmoid(u);
-    return ACT == LA_ACT_SIGMOID ? g.s : mul2(g.u, g.s);
+    // exp(-u) may be infinite here: its quotient is zero
+    const float2 t = mul2(u, both(-kLog2e)), q = add2(make_float2(ex2(t.x), ex2(t.y)), both(1.0f));
+    const float2 s = make_float2(rcp(q.x), rcp(q.y));
+    return ACT == LA_ACT_SIGMOID ? s : mul2(u, s);
 }
 template <int ACT>
 __device__ __forceinline__ float2 slope(float2 u)

@@ -296,52 +296,99 @@ __global__ void __launch_bounds__(128)
         }
 }
 
-// One token: n / 4 lanes per channel, four states each; bound by the state's bytes.
+// One token: n / 4 lanes per channel, four states each, for ROWS rows of the batch with A,
+// bias and D loaded once; bound by the state's bytes.
 struct StepIns {
     Rows x, delta, B, C, z;  // .batch: from row to row
     const float *A, *D, *bias;
-    int softplus;
+    int softplus, four;      // four: B and C rows allow loads of four
 };
 
-template <typename T, int NS>
-__global__ void __launch_bounds__(256)
-    k_ssm_step(float* __restrict__ S, StepIns in, T* __restrict__ out, int64_t C, int64_t per_group, int64_t quads)
+template <typename T>
+__device__ __forceinline__ Raw<T, 4> four_of(const T* p, bool four)
+{
+    Raw<T, 4> r;
+    if (four) {
+        r.w = __ldg(reinterpret_cast<const decltype(r.w)*>(p));
+    } else {
+        T v[4] = {p[0], p[1], p[2], p[3]};
+        memcpy(&r, v, sizeof r);
+    }
+    return r;
+}
+
+// What is in flight stays as narrow as it is in memory, for registers that leave room for more
+// blocks on an SM (B256 C4096 n = 16: bf16 four 33.4 us, six 32.2, seven 27.7, eight 30.6; fp32
+// 36, 33, 37 and 40).
+template <typename T, int NS, int ROWS>
+__global__ void __launch_bounds__(128, ROWS == 1 ? 1 : sizeof(T) == 2 ? 7 : 6)
+    k_ssm_step(float* __restrict__ S, StepIns in, T* __restrict__ out, int64_t B, int C, int per_group,
+               unsigned across)
 {
     constexpr int LPC = NS / 4;
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const bool on = item < quads;  // whole groups of lanes: the sums below need every one
-    const int64_t ch = (on ? item : 0) / LPC, b = ch / C, c = ch - b * C, g = c / per_group;
-    const int s4 = (int)(item % LPC) * 4;
-    float4* sp = reinterpret_cast<float4*>(S + ch * NS + s4);
-    float4 h = *sp;
-    const float4 a = __ldg(reinterpret_cast<const float4*>(in.A + c * NS + s4));
-    const float x = to_f32(static_cast<const T*>(in.x.p)[b * in.x.batch + c]);
-    float dt = to_f32(static_cast<const T*>(in.delta.p)[b * in.delta.batch + c]) + (in.bias ? __ldg(in.bias + c) : 0.0f);
-    if (in.softplus)
-        dt = softplus(both(dt)).x;
-    const T* Bp = static_cast<const T*>(in.B.p) + b * in.B.batch + g * NS + s4;
-    const T* Cp = static_cast<const T*>(in.C.p) + b * in.C.batch + g * NS + s4;
-    const float u = dt * x, d2 = dt * kLog2e;
-    h.x = fmaf(decay(d2, a.x), h.x, u * to_f32(Bp[0]));
-    h.y = fmaf(decay(d2, a.y), h.y, u * to_f32(Bp[1]));
-    h.z = fmaf(decay(d2, a.z), h.z, u * to_f32(Bp[2]));
-    h.w = fmaf(decay(d2, a.w), h.w, u * to_f32(Bp[3]));
-    float y = h.x * to_f32(Cp[0]);
-    y = fmaf(h.y, to_f32(Cp[1]), y);
-    y = fmaf(h.z, to_f32(Cp[2]), y);
-    y = fmaf(h.w, to_f32(Cp[3]), y);
+    const unsigned down = blockIdx.x / across;  // `across` blocks hold the channels of ROWS rows
+    const int item = (int)(blockIdx.x - down * across) * 128 + threadIdx.x;
+    const bool on = item / LPC < C;  // whole groups of lanes: the sums below need every one
+    const int c = on ? item / LPC : 0, g = c / per_group, s4 = item % LPC * 4;
+    const int64_t b0 = (int64_t)down * ROWS;
+    const int live = (int)min((int64_t)ROWS, B - b0);  // rows behind the last read it again, and write nothing
+    float4* Sp = reinterpret_cast<float4*>(S + (b0 * C + c) * NS + s4);
+    const int64_t step = (int64_t)C * (NS / 4);
+    const T* xp = static_cast<const T*>(in.x.p) + b0 * in.x.batch + c;
+    const T* dp = static_cast<const T*>(in.delta.p) + b0 * in.delta.batch + c;
+    const T* zp = in.z.p ? static_cast<const T*>(in.z.p) + b0 * in.z.batch + c : nullptr;
+    const T* Bp = static_cast<const T*>(in.B.p) + b0 * in.B.batch + g * NS + s4;
+    const T* Cp = static_cast<const T*>(in.C.p) + b0 * in.C.batch + g * NS + s4;
+    float4 h[ROWS];
+    Raw<T, 4> Br[ROWS], Cr[ROWS];
+    T xr[ROWS], dr[ROWS], zr[ROWS];
 #pragma unroll
-    for (int o = LPC / 2; o > 0; o >>= 1)
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (!on)
-        return;
-    *sp = h;
-    if (s4 == 0) {
-        if (in.D)
-            y = fmaf(__ldg(in.D + c), x, y);
-        if (in.z.p)
-            y *= value<LA_ACT_SILU>(both(to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]))).x;
-        out[b * C + c] = from_f32<T>(y);
+    for (int r = 0; r < ROWS; ++r) {
+        const int k = min(r, live - 1);
+        h[r] = __ldcs(Sp + k * step);
+        dr[r] = dp[k * in.delta.batch];
+        Br[r] = four_of(Bp + k * in.B.batch, in.four);
+        xr[r] = xp[k * in.x.batch];
+        Cr[r] = four_of(Cp + k * in.C.batch, in.four);
+        zr[r] = zp ? zp[k * in.z.batch] : from_f32<T>(0.0f);
+    }
+    const float4 A = __ldg(reinterpret_cast<const float4*>(in.A + (int64_t)c * NS + s4));
+    const float2 A2[2] = {mul2(make_float2(A.x, A.y), both(kLog2e)), mul2(make_float2(A.z, A.w), both(kLog2e))};
+    const float bias = in.bias ? __ldg(in.bias + c) : 0.0f, D = in.D ? __ldg(in.D + c) : 0.0f;
+    float dt[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+        dt[r] = to_f32(dr[r]) + bias;
+    if (in.softplus) {
+#pragma unroll
+        for (int r = 0; r < ROWS; r += 2) {
+            const float2 d = softplus(make_float2(dt[r], r + 1 < ROWS ? dt[r + 1 < ROWS ? r + 1 : r] : 0.f));
+            dt[r] = d.x;
+            if (r + 1 < ROWS)
+                dt[r + 1 < ROWS ? r + 1 : r] = d.y;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const float x = to_f32(xr[r]);
+        const Vec<4> Bv = wide(Br[r]), Cv = wide(Cr[r]);
+        const float2 d = both(dt[r]), u = both(dt[r] * x);
+        const float2 lo = fma2(decay(d, A2[0]), make_float2(h[r].x, h[r].y), mul2(u, make_float2(Bv.f[0], Bv.f[1])));
+        const float2 hi = fma2(decay(d, A2[1]), make_float2(h[r].z, h[r].w), mul2(u, make_float2(Bv.f[2], Bv.f[3])));
+        const float2 p = fma2(hi, make_float2(Cv.f[2], Cv.f[3]), mul2(lo, make_float2(Cv.f[0], Cv.f[1])));
+        float y = p.x + p.y;
+#pragma unroll
+        for (int o = LPC / 2; o > 0; o >>= 1)
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (!on || r >= live)
+            continue;
+        __stcs(Sp + r * step, make_float4(lo.x, lo.y, hi.x, hi.y));
+        if (s4 == 0) {
+            y = fmaf(D, x, y);
+            if (zp)
+                y *= value<LA_ACT_SILU>(both(to_f32(zr[r]))).x;
+            out[(b0 + r) * C + c] = from_f32<T>(y);
+        }
     }
 }
 
@@ -400,16 +447,26 @@ cudaError_t run_ssm(const SsmArgs& a)
     return async ? launch(k_ssm<T, NS, false, true>, bytes) : launch(k_ssm<T, NS, false, false>, bytes);
 }
 
+template <typename T, int NS, int ROWS>
+cudaError_t launch_step(const SsmArgs& a, const StepIns& in)
+{
+    const int64_t across = (a.C * (NS / 4) + 127) / 128;
+    k_ssm_step<T, NS, ROWS><<<(unsigned)(across * ((a.B + ROWS - 1) / ROWS)), 128, 0, a.stream>>>(
+        a.S_out, in, static_cast<T*>(a.out), a.B, (int)a.C, (int)(a.C / a.G), (unsigned)across);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+// Four rows a thread where that leaves a block for every SM (n = 16 bf16 C4096: B16 one row a
+// thread 5.1 us, four 4.0; B256 38 and 28 us), else one: latency counts.
 template <typename T, int NS>
 cudaError_t run_step(const SsmArgs& a)
 {
-    StepIns in{{a.x, a.x_batch, 0}, {a.delta, a.delta_batch, 0}, {a.Bm, a.B_batch, 0}, {a.Cm, a.C_batch, 0},
-               {a.z, a.z_batch, 0}, a.A, a.D, a.bias, a.softplus};
-    const int64_t quads = a.B * a.C * (NS / 4);
-    k_ssm_step<T, NS><<<(unsigned)((quads + 255) / 256), 256, 0, a.stream>>>(a.S_out, in, static_cast<T*>(a.out), a.C,
-                                                                            a.C / a.G, quads);
-    count_launches(1);
-    return cudaGetLastError();
+    const int es = (int)sizeof(T);
+    const StepIns in{{a.x, a.x_batch, 0}, {a.delta, a.delta_batch, 0}, {a.Bm, a.B_batch, 0}, {a.Cm, a.C_batch, 0},
+                     {a.z, a.z_batch, 0}, a.A, a.D, a.bias, a.softplus,
+                     rows_on(a.Bm, a.B_batch, 0, es, 4 * es) && rows_on(a.Cm, a.C_batch, 0, es, 4 * es)};
+    return a.B * a.C * (NS / 4) >= 152 * 128 * 4 ? launch_step<T, NS, 4>(a, in) : launch_step<T, NS, 1>(a, in);
 }
 
 template <typename T>
