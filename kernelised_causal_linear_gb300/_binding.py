@@ -618,27 +618,27 @@ def la_norm_gate_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor 
     return grads
 
 
-def _rows(t: torch.Tensor | None, name: str, shape, dtype, index: int):
-    """Pointer and row strides of an input whose last dimensions (channels, or groups
-    and states) are neighbours and whose first ones, (batch,) or (batch, token), have
-    any strides."""
+def _rows(t: torch.Tensor | None, name: str, shape, lead: int, dtype, index: int):
+    """Pointer and row strides of an input whose dimensions from `lead` on (channels, or
+    groups and states) are neighbours and whose first ones, (batch,) or (batch, token),
+    have any strides."""
     if t is None:
-        return (None,) + (0,) * (2 if shape[1] is not None else 1)
-    lead = 1 if shape[1] is None else 2
-    shape = tuple(n for n in shape if n is not None)
+        return (None, 0) if lead == 1 else (None, 0, 0)
     if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
-    strides, width = t.stride(), 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and strides[i] != width:
-            raise ValueError(f"{name}'s channels must be next to one another")
-        width *= shape[i]
+    strides = t.stride()
+    if (strides[-1] != 1 and shape[-1] != 1) or (
+            len(shape) - lead == 2 and shape[-2] != 1 and strides[-2] != shape[-1]):
+        raise ValueError(f"{name}'s channels must be next to one another")
     # the stride of a dimension of one says nothing
-    return (t.data_ptr(),) + tuple(0 if shape[i] == 1 else strides[i] for i in range(lead))
+    batch = strides[0] if shape[0] != 1 else 0
+    if lead == 1:
+        return t.data_ptr(), batch
+    return t.data_ptr(), batch, strides[1] if shape[1] != 1 else 0
 
 
 def _lengths(t, B, index):
@@ -681,7 +681,7 @@ def la_forward_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | 
     window = (B, W - 1, C)
     if S_out is None and return_state:
         S_out = call.empty(window, x.dtype)
-    xs = _rows(x, "x", (B, N, C), x.dtype, dev)
+    xs = _rows(x, "x", x.shape, 2, x.dtype, dev)
     yp = _arg(y, "y", shape, x.dtype, dev)
     _apart("y", yp, xs[0])
     code = _lib.la_forward_conv(*xs, w, b, yp, _arg(S0, "S0", window, x.dtype, dev),
@@ -704,7 +704,7 @@ def la_decode_step_conv(S: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     if y is None:
         y = call.empty((B, C), x.dtype)
     w, b, W = _filter(weight, bias, C, dev)
-    xs = _rows(x, "x", (B, None, C), x.dtype, dev)
+    xs = _rows(x, "x", x.shape, 1, x.dtype, dev)
     yp = _arg(y, "y", (B, C), x.dtype, dev)
     _apart("y", yp, xs[0])
     code = _lib.la_decode_step_conv(_arg(S, "S", (B, W - 1, C), x.dtype, dev), *xs, w, b, yp, B, C, W,
@@ -733,7 +733,7 @@ def la_backward_conv(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     window, f32 = (B, W - 1, C), torch.float32
     shape = (B, heads, N, C // heads) if dy.dim() == 4 else (B, N, C)
     ins = (_arg(dy, "dy", shape, x.dtype, dev), _arg(dS_out, "dS_out", window, x.dtype, dev),
-           *_rows(x, "x", (B, N, C), x.dtype, dev), w, b, _arg(S0, "S0", window, x.dtype, dev),
+           *_rows(x, "x", x.shape, 2, x.dtype, dev), w, b, _arg(S0, "S0", window, x.dtype, dev),
            _lengths(lengths, B, dev))
     grads = (call.empty((B, N, C), x.dtype), call.empty((C, W), f32),
              call.empty((C,), f32) if bias is not None else None,
@@ -753,23 +753,28 @@ def la_ssm_backward_workspace_size(B, N, C, G, n, dtype=torch.bfloat16) -> int:
     return int(_lib.la_ssm_backward_workspace_size(B, N, C, G, n, DTYPES[dtype]))
 
 
-def _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, step):
-    """Sizes (B, N, C, G, n), pointers in the calls' order from x to delta_bias, strides."""
-    if x.dim() != (2 if step else 3) or Bm.dim() != x.dim() + 1:
-        raise ValueError("x must be [B,C] and Bm [B,G,n]" if step else "x must be [B,N,C] and Bm [B,N,G,n]")
-    B, N, C = (x.shape[0], None, x.shape[1]) if step else x.shape
-    G, n = Bm.shape[-2:]
-    f32, wide, shared = torch.float32, (B, N, C), (B, N, G, n)
-    rows = [_rows(x, "x", wide, x.dtype, dev), _rows(delta, "delta", wide, x.dtype, dev),
-            _rows(Bm, "Bm", shared, x.dtype, dev), _rows(Cm, "Cm", shared, x.dtype, dev),
-            _rows(z, "z", wide, x.dtype, dev)]
+def _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, lead):
+    """Groups and states, pointers in the calls' order from x to delta_bias, strides on the host."""
+    wide, shared, dtype, f32 = x.shape, Bm.shape, x.dtype, torch.float32
+    if len(wide) != lead + 1 or len(shared) != lead + 2 or shared[:lead] != wide[:lead]:
+        raise ValueError("x must be [B,C] and Bm [B,G,n]" if lead == 1 else "x must be [B,N,C] and Bm [B,N,G,n]")
+    C, G, n = wide[-1], shared[-2], shared[-1]
+    rows = (_rows(x, "x", wide, lead, dtype, dev), _rows(delta, "delta", wide, lead, dtype, dev),
+            _rows(Bm, "Bm", shared, lead, dtype, dev), _rows(Cm, "Cm", shared, lead, dtype, dev),
+            _rows(z, "z", wide, lead, dtype, dev))
     ptrs = (rows[0][0], rows[1][0], _arg(A, "A", (C, n), f32, dev), rows[2][0], rows[3][0],
             _arg(D, "D", (C,), f32, dev), rows[4][0], _arg(delta_bias, "delta_bias", (C,), f32, dev))
-    return (B, N, C, G, n), ptrs, [s for r in rows for s in r[1:]]
+    strides = []
+    for r in rows:
+        strides += r[1:]
+    return G, n, ptrs, strides
+
+
+_STRIDES = {k: ctypes.c_int64 * k for k in (5, 10, 12)}
 
 
 def _host_strides(strides):
-    return (ctypes.c_int64 * len(strides))(*strides)
+    return _STRIDES[len(strides)](*strides)
 
 
 def la_forward_ssm(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor,
@@ -789,7 +794,8 @@ def la_forward_ssm(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm: to
     return_state is set.  lengths (int32 [B]): row b ends after lengths[b] tokens, out is
     zero behind."""
     dev = _current(x, "x")
-    (B, N, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, False)
+    G, n, ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, 2)
+    B, N, C = x.shape
     call = _Call(stream, dev)
     if out is None:
         out = call.empty((B, N, C), x.dtype)
@@ -815,7 +821,8 @@ def la_decode_step_ssm(S: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A:
     """One token per sequence: x, delta, z [B,C], Bm, Cm [B,G,n] (any row stride); the state
     S [B,C,n] (fp32) is updated in place -> out [B,C] in x's type."""
     dev = _current(x, "x")
-    (B, _, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, True)
+    G, n, ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, 1)
+    B, C = x.shape
     call = _Call(stream, dev)
     if out is None:
         out = call.empty((B, C), x.dtype)
@@ -838,9 +845,10 @@ def la_backward_ssm(dout: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A:
     with None for what was not given.  dout [B,N,C] (any batch and token strides) and dS_out
     [B,C,n] (None: zero) are the gradients of out and of the final state."""
     dev = _current(x, "x")
-    (B, N, C, G, n), ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, False)
+    G, n, ptrs, strides = _ssm_inputs(x, delta, A, Bm, Cm, D, z, delta_bias, dev, 2)
+    B, N, C = x.shape
     call = _Call(stream, dev)
-    dop, *ds = _rows(dout, "dout", (B, N, C), x.dtype, dev)
+    dop, *ds = _rows(dout, "dout", x.shape, 2, x.dtype, dev)
     f32, state = torch.float32, (B, C, n)
     ins = (dop, _arg(dS_out, "dS_out", state, f32, dev), *ptrs, _arg(S0, "S0", state, f32, dev),
            _lengths(lengths, B, dev))

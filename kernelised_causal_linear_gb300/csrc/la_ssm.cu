@@ -429,10 +429,8 @@ cudaError_t run_ssm(const SsmArgs& a)
     const unsigned blocks = (unsigned)(a.B * q.segs * q.G * q.per_group);
     float* ends = static_cast<float*>(a.ws);
     float* sums = ends + a.B * q.segs * a.C * NS;
+    static_assert(sizeof(Tiles<T, NS, false>) <= 48 * 1024, "shared memory of a launch without attributes");
     auto launch = [&](auto kernel, size_t bytes) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != cudaSuccess)
-            return e;
         kernel<<<blocks, L::NT, bytes, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
         count_launches(1);
         return cudaGetLastError();
