@@ -739,9 +739,9 @@ static la_status check_ssm(const SsmArgs& a)
         return LA_ERR_INVALID_ARG;
     if ((a.n != 8 && a.n != 16 && a.n != 32 && a.n != 64) || a.C > kMaxChannels || a.N > INT32_MAX)
         return LA_ERR_UNSUPPORTED;
-    // blocks: segments of at least 8 tokens times tiles of at least 32 channels of a
+    // blocks: segments of at least 8 tokens times tiles of at least 16 channels of a
     // group; threads of the sums and of a step
-    const double tiles = (double)a.G * ((double)(a.C / a.G) / 32 + 1);
+    const double tiles = (double)a.G * ((double)(a.C / a.G) / 16 + 1);
     if ((double)a.B * ((double)a.N / 8 + 1) * tiles > INT32_MAX ||
         (double)a.B * ((double)a.C * a.n / 128 + 1) > INT32_MAX || (double)a.B * a.N * a.G * a.n / 128 + 1 > INT32_MAX)
         return LA_ERR_UNSUPPORTED;

@@ -10,17 +10,6 @@
 namespace la {
 namespace ssm {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-
-template <int NS>
-struct Lay {
-    static constexpr int LPC = NS / 4;               // lanes that share a channel quad
-    static constexpr int QPW = 32 / LPC;             // quads of a warp
-    static constexpr int CT = kWarps * QPW * 4;      // channels of a block
-    static constexpr int OWN = LPC == 2 ? 2 : 1;     // channels whose sums end in a lane
-};
-
 // Where a block works: channels c0 .. c0 + valid - 1 of group g, row b, segment.
 struct Place {
     int64_t b;
@@ -127,7 +116,7 @@ __device__ __forceinline__ void cp_wait()
 // and `cols` columns of it from memory, the rest zero (bytes behind either are not
 // read).  ASYNC: 16-byte copies in flight, every row on a 16-byte boundary; else
 // element by element.
-template <typename T, int TT, int WIDE, bool ASYNC, int NT = kThreads>
+template <typename T, int TT, int WIDE, bool ASYNC, int NT>
 __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, int live, int cols)
 {
     constexpr int V = 16 / (int)sizeof(T);
@@ -157,82 +146,6 @@ __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, i
                     dst[i0 + k * NT] = v[k];
         }
     }
-}
-
-// Sums over the lanes of a quad, of channel pairs (y[0], y[1]): a lane ends with the
-// sum of its channel lane & 3 (LPC = 2: of the pair y[lane & 1]).
-template <int LPC>
-__device__ __forceinline__ void sum_states(const float2 (&y)[2], int lane, float (&own)[LPC == 2 ? 2 : 1])
-{
-    constexpr unsigned full = 0xffffffffu;
-    if constexpr (LPC == 2) {
-        const bool up = lane & 1;
-        const float2 keep = up ? y[1] : y[0], give = up ? y[0] : y[1];
-        own[0] = keep.x + __shfl_xor_sync(full, give.x, 1);
-        own[1] = keep.y + __shfl_xor_sync(full, give.y, 1);
-    } else {
-        const bool up = lane & 2, odd = lane & 1;
-        float2 keep = up ? y[1] : y[0];
-        const float2 give = up ? y[0] : y[1];
-        keep.x += __shfl_xor_sync(full, give.x, 2);
-        keep.y += __shfl_xor_sync(full, give.y, 2);
-        float r = (odd ? keep.y : keep.x) + __shfl_xor_sync(full, odd ? keep.x : keep.y, 1);
-#pragma unroll
-        for (int o = 4; o < LPC; o *= 2)
-            r += __shfl_xor_sync(full, r, o);
-        own[0] = r;
-    }
-}
-
-// Four states of four channels between memory [C][n] and pairs [channel pair][state];
-// channels behind the last are zero and are not written.
-template <int NS>
-__device__ __forceinline__ void load_quad(const float* __restrict__ p, int valid, float2 (&h)[2][4])
-{
-    float f[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = i < valid ? *reinterpret_cast<const float4*>(p + i * NS) : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[i][0] = v.x, f[i][1] = v.y, f[i][2] = v.z, f[i][3] = v.w;
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-        h[0][s] = make_float2(f[0][s], f[1][s]), h[1][s] = make_float2(f[2][s], f[3][s]);
-}
-
-template <int NS>
-__device__ __forceinline__ void store_quad(float* __restrict__ p, int valid, const float2 (&h)[2][4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2* q = h[i / 2];
-        if (i < valid)
-            *reinterpret_cast<float4*>(p + i * NS) = i & 1 ? make_float4(q[0].y, q[1].y, q[2].y, q[3].y)
-                                                           : make_float4(q[0].x, q[1].x, q[2].x, q[3].x);
-    }
-}
-
-// B or C of a thread's four states, each twice (one register pair per product): as they
-// lie in shared memory, which costs a read more and saves eight moves a token.
-struct Four {
-    float2 s[4];
-};
-__device__ __forceinline__ Four twice(const float2* p)
-{
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    return {{{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}}};
-}
-
-// One token: h = exp(dt A) h + u B with u = dt x.
-__device__ __forceinline__ void step(const float4& dt, const float4& u, const Four& B, const float2 (&A2)[2][4],
-                                     float2 (&h)[2][4])
-{
-    const float2 d[2] = {{dt.x, dt.y}, {dt.z, dt.w}}, v[2] = {{u.x, u.y}, {u.z, u.w}};
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            h[p][s] = fma2(decay(d[p], A2[p][s]), h[p][s], mul2(v[p], B.s[s]));
 }
 
 // Segments between their ends and their starts: S_{i+1} = exp(A sum dt_i) S_i + E_i.
