@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 }
 
 // In place, one thread per state: ends -> starts of the segments, fronts -> gradients at
-// their ends; loads of sixteen segments ahead of the chain.
+// their ends; loads of eight segments ahead of the chain (B16 N512 C2048 n = 16:
+// sixteen 58 us, eight 32; B1 N8192: 37 and 39).
 __global__ void __launch_bounds__(128)
     k_ssm_join_grad(const float* __restrict__ A, const float* __restrict__ S0, const float* __restrict__ dS_out,
                     float* __restrict__ ends, const float* __restrict__ sums, float* __restrict__ fronts,
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(128)
     float S = init ? init[item] : 0.0f;
     float* p = (back ? fronts : ends) + b * segs * row + e;
     const float* d = sums + b * segs * C + e / NS;
-    constexpr int kAhead = 16;
+    constexpr int kAhead = 8;
     float E[2][kAhead], P[2][kAhead];
     auto at = [&](int i) { return (int64_t)(back ? segs - 1 - i : i); };
 #pragma unroll
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The sums over blocks, in a fixed order.  Blocks 0 .. row_blocks - 1: dB, dC [rows][G][n] from
-// the channel tiles' parts [tile][rows][G][2][n].  Then columns x 32 partial sums a block:
+// the channel tiles' parts [tile][rows][G][2][n].  Then columns x 8 partial sums a block:
 // those of dA (128), dD and dbias (32) over the segments.
 struct Sums {
     const float* rows;
@@ -684,35 +685,48 @@ __device__ __forceinline__ float4 plus(float4 a, float4 b)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) k_ssm_sums(Sums q, T* __restrict__ dB, T* __restrict__ dC)
+__global__ void __launch_bounds__(256) k_ssm_sums(Sums q, T* __restrict__ dB, T* __restrict__ dC)
 {
     if (blockIdx.x < q.row_blocks) {
-        const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
         if (i >= q.values)
             return;
         float s = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < q.tiles; ++k)
-            s += __ldg(q.rows + k * q.values + i);
+        for (int k0 = 0; k0 < q.tiles; k0 += 8) {
+            float v[8];  // in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = k0 + k < q.tiles ? __ldg(q.rows + (k0 + k) * q.values + i) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s += v[k];
+        }
         const int64_t pair = i / q.NS;
         (pair & 1 ? dC : dB)[pair / 2 * q.NS + i % q.NS] = from_f32<T>(s);
         return;
     }
-    __shared__ float4 sums[32][33];
+    __shared__ float4 sums[8][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     unsigned block = blockIdx.x - q.row_blocks;
     if (block < q.dA_blocks) {
         const int64_t c = (int64_t)block * 32 + lane, cols = q.cols[0] / 4;  // four columns a lane
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < cols) {
-#pragma unroll 8
-            for (int64_t r = grp; r < q.segs; r += 32)
-                x = plus(x, __ldg(reinterpret_cast<const float4*>(q.part[0]) + r * cols + c));
+            const float4* p = reinterpret_cast<const float4*>(q.part[0]) + c;
+            for (int64_t r = grp; r < q.segs; r += 64) {
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = r + 8 * k < q.segs ? __ldg(p + (r + 8 * k) * cols) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x = plus(x, v[k]);
+            }
         }
         sums[grp][lane] = x;
         __syncthreads();
         if (grp == 0 && c < cols) {
-            for (int i = 1; i < 32; ++i)
+            for (int i = 1; i < 8; ++i)
                 x = plus(x, sums[i][lane]);
             reinterpret_cast<float4*>(q.out[0])[c] = x;
         }
@@ -725,13 +739,13 @@ __global__ void __launch_bounds__(1024) k_ssm_sums(Sums q, T* __restrict__ dB, T
     float x = 0.f;
     if (c < cols) {
 #pragma unroll 8
-        for (int64_t r = grp; r < q.segs; r += 32)
+        for (int64_t r = grp; r < q.segs; r += 8)
             x += __ldg(q.part[which] + r * cols + c);
     }
     sums[grp][lane].x = x;
     __syncthreads();
     if (grp == 0 && c < cols && q.out[which]) {
-        for (int i = 1; i < 32; ++i)
+        for (int i = 1; i < 8; ++i)
             x += sums[i][lane].x;
         q.out[which][c] = x;
     }
@@ -800,9 +814,9 @@ cudaError_t run_grad(const SsmArgs& a, const GradIns& in, const Grid& q)
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     const int64_t values = a.B * a.N * a.G * 2 * NS;
-    const int64_t row_blocks = (values + 1023) / 1024, dA_blocks = (a.C * NS + 127) / 128;
+    const int64_t row_blocks = (values + 255) / 256, dA_blocks = (a.C * NS + 127) / 128;
     const int64_t col_blocks = dA_blocks + 2 * ((a.C + 31) / 32);
-    k_ssm_sums<T><<<(unsigned)(row_blocks + col_blocks), 1024, 0, a.stream>>>(
+    k_ssm_sums<T><<<(unsigned)(row_blocks + col_blocks), 256, 0, a.stream>>>(
         Sums{rows, values, q.per_group, NS, (unsigned)row_blocks, (unsigned)dA_blocks, {dA, sums, dbias},
              {a.dA, a.dD, a.dbias}, {a.C * NS, a.C}, a.B * q.segs},
         static_cast<T*>(a.dB), static_cast<T*>(a.dC));
