@@ -396,10 +396,10 @@ __global__ void __launch_bounds__(128, ROWS == 1 ? 1 : sizeof(T) == 2 ? 7 : 6)
 }
 
 // Segments.  The run for the ends costs 0.7 of the one that counts, so rows stay whole
-// where they alone are three blocks an SM (N8192 C2048 n = 16 bf16: 320 blocks whole 3.14 ms,
-// cut 2.31; 432 blocks 3.14 both; 576 blocks 3.15 and 4.11).  Else about four rounds of
-// blocks, which fill up better than one (64 blocks: 24 segments 543 us, 76 segments 511 us),
-// a tile each at least (fp32 B2 N333 C197: 21 segments 28 us, 42 segments 20 us).
+// where they alone are nearly three blocks an SM (N2048 C2048 n = 16 bf16: 320 blocks whole
+// 727 us, cut 608; 448 blocks 728 and 823).  Else about four rounds of blocks, which fill up
+// better than one (N8192, 64 blocks: 24 segments 543 us, 76 segments 511 us), a tile each at
+// least (fp32 B2 N333 C197: 21 segments 28 us, 42 segments 20 us).
 template <typename T, int NS>
 Grid grid_of(const SsmArgs& a)
 {
@@ -409,7 +409,7 @@ Grid grid_of(const SsmArgs& a)
     q.per_group = (int)((a.C / a.G + L::CT - 1) / L::CT);
     const int64_t blocks = a.B * q.G * q.per_group, tiles = (a.N + L::TT - 1) / L::TT;
     int64_t segs = 1;
-    if (blocks < 450) {
+    if (blocks < 390) {
         segs = 152 * 8 * 4 / blocks;
         segs = segs < tiles ? segs : tiles;
     }
