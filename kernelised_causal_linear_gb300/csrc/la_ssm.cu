@@ -6,11 +6,12 @@
 // states: B and C, the same for every lane, are eight 16-byte reads of shared memory for
 // 32 elements, and the sum over the states stays in the thread (n = 32 and 64: two and
 // four lanes per channel pair).  What bounds it is arithmetic: an element costs one
-// hardware exponential (32 a clock and SM) and four fp32 operations in two-wide
-// instructions (128 a clock and SM), which overlap: 512 elements take about 155 clocks of a sub-partition, 80 of them of the
-// exponentials' unit, those of the steps and the gate among them (B4 N8192 C2048 n = 16 bf16:
-// 288 us, and 206 us for the run for the ends).  (Four channels times four states per
-// thread, with steps in shared memory and shuffles, took 198 clocks.)
+// hardware exponential (32 a clock and SM) and four fp32 operations in two-wide instructions,
+// which reach some 90 a clock and SM, not 128, where all three operands differ.  Both overlap in
+// part: 512 elements take about 150 clocks of a sub-partition, 80 of them of the exponentials'
+// unit, those of the steps and the gate among them (B4 N8192 C2048 n = 16 bf16: 275 us, and 190
+// us for the run for the ends).  (Four channels times four states per thread, with steps in
+// shared memory and shuffles, took 198 clocks.)
 //
 // Few long sequences are cut into segments: k_ssm<END> runs each from a zero
 // state for its end, k_ssm_join walks the ends (the decay of a segment is exp(A sum
@@ -320,78 +321,85 @@ __device__ __forceinline__ Raw<T, 4> four_of(const T* p, bool four)
     return r;
 }
 
-// What is in flight stays as narrow as it is in memory, for registers that leave room for more
-// blocks on an SM (B256 C4096 n = 16: bf16 four 33.4 us, six 32.2, seven 27.7, eight 30.6; fp32
-// 36, 33, 37 and 40).
+// The lanes of a channel share its rows: each reads x, delta and z of one row and finishes that
+// row (ROWS <= LPC), and the steps travel by shuffles.
 template <typename T, int NS, int ROWS>
-__global__ void __launch_bounds__(128, ROWS == 1 ? 1 : sizeof(T) == 2 ? 7 : 6)
+__global__ void __launch_bounds__(128)
     k_ssm_step(float* __restrict__ S, StepIns in, T* __restrict__ out, int64_t B, int C, int per_group,
                unsigned across)
 {
     constexpr int LPC = NS / 4;
+    constexpr unsigned full = 0xffffffffu;
+    static_assert(ROWS <= LPC && (ROWS & (ROWS - 1)) == 0, "a row for a lane");
     const unsigned down = blockIdx.x / across;  // `across` blocks hold the channels of ROWS rows
     const int item = (int)(blockIdx.x - down * across) * 128 + threadIdx.x;
     const bool on = item / LPC < C;  // whole groups of lanes: the sums below need every one
-    const int c = on ? item / LPC : 0, g = c / per_group, s4 = item % LPC * 4;
+    const int c = on ? item / LPC : 0, g = c / per_group, part = item % LPC, s4 = part * 4, mine = part & (ROWS - 1);
     const int64_t b0 = (int64_t)down * ROWS;
-    const int live = (int)min((int64_t)ROWS, B - b0);  // rows behind the last read it again, and write nothing
+    const int live = on ? (int)min((int64_t)ROWS, B - b0) : 0;
     float4* Sp = reinterpret_cast<float4*>(S + (b0 * C + c) * NS + s4);
-    const int64_t step = (int64_t)C * (NS / 4);
-    const T* xp = static_cast<const T*>(in.x.p) + b0 * in.x.batch + c;
-    const T* dp = static_cast<const T*>(in.delta.p) + b0 * in.delta.batch + c;
-    const T* zp = in.z.p ? static_cast<const T*>(in.z.p) + b0 * in.z.batch + c : nullptr;
     const T* Bp = static_cast<const T*>(in.B.p) + b0 * in.B.batch + g * NS + s4;
     const T* Cp = static_cast<const T*>(in.C.p) + b0 * in.C.batch + g * NS + s4;
     float4 h[ROWS];
     Raw<T, 4> Br[ROWS], Cr[ROWS];
-    T xr[ROWS], dr[ROWS], zr[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const int k = min(r, live - 1);
-        h[r] = __ldcs(Sp + k * step);
-        dr[r] = dp[k * in.delta.batch];
-        Br[r] = four_of(Bp + k * in.B.batch, in.four);
-        xr[r] = xp[k * in.x.batch];
-        Cr[r] = four_of(Cp + k * in.C.batch, in.four);
-        zr[r] = zp ? zp[k * in.z.batch] : from_f32<T>(0.0f);
+        if (r < live) {
+            h[r] = __ldcs(Sp + (int64_t)r * C * (NS / 4));
+            Br[r] = four_of(Bp, in.four);
+            Cr[r] = four_of(Cp, in.four);
+        } else {
+            h[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            Br[r] = Cr[r] = none<T, 4>();
+        }
+        Bp += in.B.batch, Cp += in.C.batch;
+    }
+    float x = 0.f, dt = 0.f, z = 0.f;
+    if (mine < live) {
+        const int64_t b = b0 + mine;
+        x = to_f32(static_cast<const T*>(in.x.p)[b * in.x.batch + c]);
+        dt = to_f32(static_cast<const T*>(in.delta.p)[b * in.delta.batch + c]);
+        if (in.z.p)
+            z = to_f32(static_cast<const T*>(in.z.p)[b * in.z.batch + c]);
     }
     const float4 A = __ldg(reinterpret_cast<const float4*>(in.A + (int64_t)c * NS + s4));
     const float2 A2[2] = {mul2(make_float2(A.x, A.y), both(kLog2e)), mul2(make_float2(A.z, A.w), both(kLog2e))};
-    const float bias = in.bias ? __ldg(in.bias + c) : 0.0f, D = in.D ? __ldg(in.D + c) : 0.0f;
-    float dt[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-        dt[r] = to_f32(dr[r]) + bias;
-    if (in.softplus) {
-#pragma unroll
-        for (int r = 0; r < ROWS; r += 2) {
-            const float2 d = softplus(make_float2(dt[r], r + 1 < ROWS ? dt[r + 1 < ROWS ? r + 1 : r] : 0.f));
-            dt[r] = d.x;
-            if (r + 1 < ROWS)
-                dt[r + 1 < ROWS ? r + 1 : r] = d.y;
-        }
-    }
+    if (in.bias)
+        dt += __ldg(in.bias + c);
+    if (in.softplus)
+        dt = softplus(both(dt)).x;
+    const float u = dt * x;
+    float y[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        const float x = to_f32(xr[r]);
+        const float2 d = both(ROWS > 1 ? __shfl_sync(full, dt, r, LPC) : dt);
+        const float2 v = both(ROWS > 1 ? __shfl_sync(full, u, r, LPC) : u);
         const Vec<4> Bv = wide(Br[r]), Cv = wide(Cr[r]);
-        const float2 d = both(dt[r]), u = both(dt[r] * x);
-        const float2 lo = fma2(decay(d, A2[0]), make_float2(h[r].x, h[r].y), mul2(u, make_float2(Bv.f[0], Bv.f[1])));
-        const float2 hi = fma2(decay(d, A2[1]), make_float2(h[r].z, h[r].w), mul2(u, make_float2(Bv.f[2], Bv.f[3])));
+        const float2 lo = fma2(decay(d, A2[0]), make_float2(h[r].x, h[r].y), mul2(v, make_float2(Bv.f[0], Bv.f[1])));
+        const float2 hi = fma2(decay(d, A2[1]), make_float2(h[r].z, h[r].w), mul2(v, make_float2(Bv.f[2], Bv.f[3])));
         const float2 p = fma2(hi, make_float2(Cv.f[2], Cv.f[3]), mul2(lo, make_float2(Cv.f[0], Cv.f[1])));
-        float y = p.x + p.y;
+        y[r] = p.x + p.y;
+        if (r < live)
+            __stcs(Sp + (int64_t)r * C * (NS / 4), make_float4(lo.x, lo.y, hi.x, hi.y));
+    }
+    // rows are traded, so that a lane ends with the sum of its own
 #pragma unroll
-        for (int o = LPC / 2; o > 0; o >>= 1)
-            y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (!on || r >= live)
-            continue;
-        __stcs(Sp + r * step, make_float4(lo.x, lo.y, hi.x, hi.y));
-        if (s4 == 0) {
-            y = fmaf(D, x, y);
-            if (zp)
-                y *= value<LA_ACT_SILU>(both(to_f32(zr[r]))).x;
-            out[(b0 + r) * C + c] = from_f32<T>(y);
-        }
+    for (int o = ROWS / 2; o > 0; o /= 2) {
+        const bool up = part & o;
+#pragma unroll
+        for (int r = 0; r < o; ++r)
+            y[r] = (up ? y[r + o] : y[r]) + __shfl_xor_sync(full, up ? y[r] : y[r + o], o);
+    }
+#pragma unroll
+    for (int o = ROWS; o < LPC; o *= 2)
+        y[0] += __shfl_xor_sync(full, y[0], o);
+    if (part < ROWS && mine < live) {
+        float o = y[0];
+        if (in.D)
+            o = fmaf(__ldg(in.D + c), x, o);
+        if (in.z.p)
+            o *= value<LA_ACT_SILU>(both(z)).x;
+        out[(b0 + mine) * C + c] = from_f32<T>(o);
     }
 }
 
@@ -459,8 +467,9 @@ cudaError_t launch_step(const SsmArgs& a, const StepIns& in)
     return cudaGetLastError();
 }
 
-// Four rows a thread where that leaves a block for every SM (n = 16 bf16 C4096: B16 one row a
-// thread 5.1 us, four 4.0; B256 38 and 28 us), else one: latency counts.
+// Four rows a thread (n = 8: two) where that leaves a block for every SM (n = 16 bf16 C4096: B16
+// one row a thread 5.1 us, four 4.3; B256 38 and 22 us, 6.4 TB/s; with every lane reading all
+// four rows' x, delta and z 28 us, of instructions), else one: latency counts.
 template <typename T, int NS>
 cudaError_t run_step(const SsmArgs& a)
 {
@@ -468,7 +477,7 @@ cudaError_t run_step(const SsmArgs& a)
     const StepIns in{{a.x, a.x_batch, 0}, {a.delta, a.delta_batch, 0}, {a.Bm, a.B_batch, 0}, {a.Cm, a.C_batch, 0},
                      {a.z, a.z_batch, 0}, a.A, a.D, a.bias, a.softplus,
                      rows_on(a.Bm, a.B_batch, 0, es, 4 * es) && rows_on(a.Cm, a.C_batch, 0, es, 4 * es)};
-    return a.B * a.C * (NS / 4) >= 152 * 128 * 4 ? launch_step<T, NS, 4>(a, in) : launch_step<T, NS, 1>(a, in);
+    return a.B * a.C * (NS / 4) >= 152 * 128 * 4 ? launch_step<T, NS, NS == 8 ? 2 : 4>(a, in) : launch_step<T, NS, 1>(a, in);
 }
 
 template <typename T>
