@@ -109,8 +109,8 @@ __device__ __forceinline__ int64_t y_at(int64_t b, int64_t t, int c, const ConvS
 }
 
 // Tokens whose loads are issued together, one group ahead of the one in use (bf16 B4 N8192
-// C4096: eight with none ahead 114 us, eight and one group ahead with streaming loads 100 us,
-// sixteen 101 us; the same bytes in fp32 87 us).
+// C4096: eight with none ahead 114 us; one group ahead four 92, eight 87, sixteen 87 us; the same
+// bytes in fp32 79 us).
 template <typename T>
 constexpr int ahead()
 {
@@ -118,8 +118,9 @@ constexpr int ahead()
     return sizeof(T) == 2 ? 8 : 4;
 }
 
+// Five blocks an SM, 96 registers: 87 us; as many registers as it likes 116, six blocks 97.
 template <typename T, int V, int W, int ACT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     k_conv(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
            T* __restrict__ y, const T* S0, T* S_out, const int* __restrict__ lengths, ConvShape s, int64_t items)
 {
@@ -135,8 +136,10 @@ __global__ void __launch_bounds__(kThreads)
     load_filter<V, W>(weight, bias, c, w, bs);
     const int64_t first = r * s.run, end = min(s.N, first + s.run), live = min(end, len);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        win[j] = pairs(input<T, V, W>(x, S0, b, first - (W - 1) + j, c, s));
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t p = first - (W - 1) + j;  // not behind the row's last
+        win[j] = pairs(p < len ? input<T, V, W>(x, S0, b, p, c, s) : none<T, V>());
+    }
     if (r == 0 && S_out) {
         // the window after the last token; S_out may be S0, whose rows of these channels
         // this thread alone reads
