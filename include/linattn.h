@@ -371,7 +371,8 @@ LA_API la_status la_norm_gate_backward(const void* dy, const void* x, const void
  * e.g. a slice of a projection, and need only their type's alignment (16-byte
  * rows are the fast path).  Everything else is contiguous and 16-byte aligned.
  * No output may overlap an input or another output, but for S_out in the place
- * of S0 where that is said.
+ * of S0 where that is said.  A workspace must not be used by another call that runs
+ * concurrently.
  *   lengths : int32 [B] on the device, or NULL for N everywhere.  Row b ends after
  *             lengths[b] tokens (clamped to 0 .. N): the final state is the one
  *             there, tokens behind are not read, and outputs and gradients

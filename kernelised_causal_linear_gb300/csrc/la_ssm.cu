@@ -16,6 +16,8 @@
 // Few long sequences are cut into segments: k_ssm<END> runs each from a zero
 // state for its end, k_ssm_join walks the ends (the decay of a segment is exp(A sum
 // dt)), and k_ssm runs every segment again from its true start.
+#include <type_traits>
+
 #include "la_ssm.cuh"
 
 namespace la {
@@ -94,7 +96,7 @@ __device__ __forceinline__ void store_pair(float* p, int have, const float2 (&h)
 // END: the state after each segment but the last from a zero start (ends) and the sum of
 // its steps (sums).  Else the outputs, from S0 or (segments) from `ends`, which then holds
 // starts.
-template <typename T, int NS, bool END, bool ASYNC>
+template <typename T, int NS, bool END, int BYTES>
 __global__ void __launch_bounds__(Cut<T, NS>::NT, 8)
     k_ssm(Ins in, T* __restrict__ out, const float* S0, float* S_out, float* __restrict__ ends,
           float* __restrict__ sums, Grid q)
@@ -143,13 +145,13 @@ __global__ void __launch_bounds__(Cut<T, NS>::NT, 8)
         const int k = tile & 1;
         const int64_t t0 = first + (int64_t)tile * TT;
         const int n = min(TT, live - tile * TT);
-        copy_tile<T, TT, CT, ASYNC, NT>(sm.x[k][0], xs + t0 * in.x.token, in.x.token, n, at.valid);
-        copy_tile<T, TT, CT, ASYNC, NT>(sm.delta[k][0], ds + t0 * in.delta.token, in.delta.token, n, at.valid);
-        copy_tile<T, TT, NS, ASYNC, NT>(sm.B[k][0], Bs + t0 * in.B.token, in.B.token, n, NS);
+        copy_tile<T, TT, CT, BYTES, NT>(sm.x[k][0], xs + t0 * in.x.token, in.x.token, n, at.valid);
+        copy_tile<T, TT, CT, BYTES, NT>(sm.delta[k][0], ds + t0 * in.delta.token, in.delta.token, n, at.valid);
+        copy_tile<T, TT, NS, BYTES, NT>(sm.B[k][0], Bs + t0 * in.B.token, in.B.token, n, NS);
         if constexpr (!END) {
-            copy_tile<T, TT, NS, ASYNC, NT>(sm.C[k][0], Cs + t0 * in.C.token, in.C.token, n, NS);
+            copy_tile<T, TT, NS, BYTES, NT>(sm.C[k][0], Cs + t0 * in.C.token, in.C.token, n, NS);
             if (zs)
-                copy_tile<T, TT, CT, ASYNC, NT>(sm.z[k][0], zs + t0 * in.z.token, in.z.token, n, at.valid);
+                copy_tile<T, TT, CT, BYTES, NT>(sm.z[k][0], zs + t0 * in.z.token, in.z.token, n, at.valid);
         }
         cp_commit();
     };
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(Cut<T, NS>::NT, 8)
                     const float2 z = two(&sm.z[k][t][c2]);
                     o = mul2(o, value<LA_ACT_SILU>(z));
                 }
-                if (ASYNC && have == 2) {  // rows of an even number of channels
+                if (BYTES >= 2 * (int)sizeof(T) && have == 2) {  // rows of an even number of channels
                     put_two(po, o);
                 } else {
                     if (have > 0)
@@ -434,27 +436,38 @@ cudaError_t run_ssm(const SsmArgs& a)
     Ins in{{a.x, a.x_batch, a.x_token}, {a.delta, a.delta_batch, a.delta_token}, {a.Bm, a.B_batch, a.B_token},
            {a.Cm, a.C_batch, a.C_token}, {a.z, a.z_batch, a.z_token}, a.A, a.D, a.bias, a.lengths, a.softplus};
     const int es = (int)sizeof(T);
-    const bool async = rows_on(a.x, a.x_batch, a.x_token, es, 16) && rows_on(a.delta, a.delta_batch, a.delta_token, es, 16) &&
-                       rows_on(a.Bm, a.B_batch, a.B_token, es, 16) && rows_on(a.Cm, a.C_batch, a.C_token, es, 16) &&
-                       (!a.z || rows_on(a.z, a.z_batch, a.z_token, es, 16)) && a.C / a.G * es % 16 == 0;
+    auto on = [&](unsigned bytes) {
+        return rows_on(a.x, a.x_batch, a.x_token, es, bytes) && rows_on(a.delta, a.delta_batch, a.delta_token, es, bytes) &&
+               rows_on(a.Bm, a.B_batch, a.B_token, es, bytes) && rows_on(a.Cm, a.C_batch, a.C_token, es, bytes) &&
+               (!a.z || rows_on(a.z, a.z_batch, a.z_token, es, bytes)) && a.C / a.G * es % bytes == 0;
+    };
+    const int bytes = on(16) ? 16 : on(4) ? 4 : 0;
     const unsigned blocks = (unsigned)(a.B * q.segs * q.G * q.per_group);
     float* ends = static_cast<float*>(a.ws);
     float* sums = ends + a.B * q.segs * a.C * NS;
     
     static_assert(sizeof(Tiles<T, NS, false>) <= 48 * 1024, "shared memory of a launch without attributes");
-    auto launch = [&](auto kernel, size_t bytes) {
-        kernel<<<blocks, L::NT, bytes, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
+    auto launch = [&](auto kernel, size_t shared) {
+        kernel<<<blocks, L::NT, shared, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
         count_launches(1);
         return cudaGetLastError();
     };
+    auto run = [&](auto end) {
+        constexpr bool END = decltype(end)::value;
+        constexpr size_t shared = sizeof(Tiles<T, NS, END>);
+        if (bytes == 16)
+            return launch(k_ssm<T, NS, END, 16>, shared);
+        if constexpr (sizeof(T) == 2)
+            if (bytes == 0)
+                return launch(k_ssm<T, NS, END, 0>, shared);
+        return launch(k_ssm<T, NS, END, 4>, shared);
+    };
     if (q.segs > 1) {
-        const size_t bytes = sizeof(Tiles<T, NS, true>);
-        cudaError_t e = async ? launch(k_ssm<T, NS, true, true>, bytes) : launch(k_ssm<T, NS, true, false>, bytes);
+        cudaError_t e = run(std::true_type{});
         if (e != cudaSuccess || (e = join_forward(a, q, ends, sums)) != cudaSuccess)
             return e;
     }
-    const size_t bytes = sizeof(Tiles<T, NS, false>);
-    return async ? launch(k_ssm<T, NS, false, true>, bytes) : launch(k_ssm<T, NS, false, false>, bytes);
+    return run(std::false_type{});
 }
 
 template <typename T, int NS, int ROWS>

@@ -99,11 +99,15 @@ __device__ __forceinline__ void steps(const rows::Vec<V>& raw, const rows::Vec<V
     }
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes)
+// BYTES (4 or 16) from memory, of which the first `have` are read and the rest zero.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, int have)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
-                 "l"(src), "r"(bytes)
-                 : "memory");
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(have) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(src), "r"(have) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -112,27 +116,26 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// A tile of `WIDE` columns from token t0 into shared memory [TT][WIDE], `live` tokens
-// and `cols` columns of it from memory, the rest zero (bytes behind either are not
-// read).  ASYNC: 16-byte copies in flight, every row on a 16-byte boundary; else
-// element by element.
-template <typename T, int TT, int WIDE, bool ASYNC, int NT>
+// A tile of `WIDE` columns into shared memory [TT][WIDE], `live` tokens and `cols` columns of it
+// from memory, the rest zero (bytes behind either are not read).  BYTES: what every row starts
+// and ends on a multiple of, 16 or 4, for copies of that size in flight; 0 for neither, element
+// by element (forward of B4 N8192 C2048 n = 16 bf16: 498 us on 16 bytes, 580 off by two elements,
+// 811 off by one; fp32 B2: 288 us, and 382 off by one).
+template <typename T, int TT, int WIDE, int BYTES, int NT>
 __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, int live, int cols)
 {
-    constexpr int V = 16 / (int)sizeof(T);
-    if constexpr (ASYNC) {
-        constexpr int PER = WIDE / V;
+    if constexpr (BYTES > 0) {
+        constexpr int V = BYTES / (int)sizeof(T), PER = WIDE / V;
 #pragma unroll
         for (int k = 0; k < (TT * PER + NT - 1) / NT; ++k) {
             const int i = k * NT + threadIdx.x, t = i / PER, c = i % PER * V;
             if (TT * PER % NT && i >= TT * PER)
                 break;
             const bool on = t < live && c < cols;
-            cp_async16(dst + t * WIDE + c, on ? src + t * token + c : src,
-                       on ? min(V, cols - c) * (int)sizeof(T) : 0);
+            cp_async<BYTES>(dst + t * WIDE + c, on ? src + t * token + c : src, on ? BYTES : 0);
         }
     } else {
-        constexpr int kAhead = 8;  // loads in flight together
+        constexpr int kAhead = 16;  // loads in flight together
         for (int i0 = threadIdx.x; i0 < TT * WIDE; i0 += kAhead * NT) {
             T v[kAhead];
 #pragma unroll
