@@ -422,7 +422,7 @@ LA_API la_status la_backward_conv(const void* dy, const void* dS_out, const void
                                   la_stream_t stream);
 
 /*
- * Selective state-space scan ["Linear Attention and SSM", Mamba]: C channels with n
+ * Selective state-space scan ["Linear Attention and SSM"]: C channels with n
  * states each (n in {8, 16, 32, 64}), decays and inputs of every token its own,
  *     dt_t = softplus(delta_t + delta_bias)      (softplus = 0: delta_t + delta_bias)
  *     S_t = exp(dt_t A) S_{t-1} + dt_t x_t Bm_t,  S [C,n]

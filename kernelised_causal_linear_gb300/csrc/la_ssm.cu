@@ -428,6 +428,14 @@ Grid grid_of(const SsmArgs& a)
     return q;
 }
 
+cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const float* sums)
+{
+    const int64_t items = a.B * a.C * a.n;
+    k_ssm_join<<<(unsigned)((items + 127) / 128), 128, 0, a.stream>>>(a.A, a.S0, ends, sums, q.segs, a.C, a.n, items);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 template <typename T, int NS>
 cudaError_t run_ssm(const SsmArgs& a)
 {
@@ -516,14 +524,6 @@ Grid grid_any(const SsmArgs& a)
 }
 
 }  // namespace
-
-cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const float* sums)
-{
-    const int64_t items = a.B * a.C * a.n;
-    k_ssm_join<<<(unsigned)((items + 127) / 128), 128, 0, a.stream>>>(a.A, a.S0, ends, sums, q.segs, a.C, a.n, items);
-    count_launches(1);
-    return cudaGetLastError();
-}
 
 }  // namespace ssm
 

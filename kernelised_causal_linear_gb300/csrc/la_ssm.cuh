@@ -54,7 +54,6 @@ using rows::mul2;
 // instruction as the product, brings that to within 0.09 above -2^-9 and 0.29 elsewhere
 // above -1/4.  2^kLift itself is exactly 1: dt = 0 leaves a state as it was.
 constexpr float kLift = 0.25f / 16777216.0f;
-__device__ __forceinline__ float decay(float dt, float A2) { return ex2(fmaf(dt, A2, kLift)); }
 __device__ __forceinline__ float2 decay(float2 dt, float2 A2)
 {
     const float2 t = fma2(dt, A2, both(kLift));
@@ -150,9 +149,6 @@ __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, i
         }
     }
 }
-
-// Segments between their ends and their starts: S_{i+1} = exp(A sum dt_i) S_i + E_i.
-cudaError_t join_forward(const SsmArgs& a, const Grid& q, float* ends, const float* sums);
 
 }  // namespace ssm
 }  // namespace la

@@ -184,18 +184,10 @@ __device__ __forceinline__ void raw_two(const T* p, int have, T (&v)[2])
     }
 }
 
-// Two channels of one token, as four_at.
-template <typename T, bool VEC>
-__device__ __forceinline__ float2 two_at(const T* p, int have)
+// Two channels of a parameter.
+__device__ __forceinline__ float2 two_of(const float* p, int have)
 {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const uint32_t w = have > 0 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    } else if constexpr (VEC) {
-        return have > 0 ? __ldg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
-    } else {
-        return make_float2(have > 0 ? to_f32(__ldg(p)) : 0.f, have > 1 ? to_f32(__ldg(p + 1)) : 0.f);
-    }
+    return make_float2(have > 0 ? __ldg(p) : 0.f, have > 1 ? __ldg(p + 1) : 0.f);
 }
 template <bool VEC>
 __device__ __forceinline__ void put_two(float* p, float2 v, int have)
@@ -478,8 +470,8 @@ __global__ void __launch_bounds__(kThreads)
             A2[p][s] = mul2(A2[p][s], both(kLog2e));
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) {
-        D[p] = in.D ? two_at<float, false>(in.D + at.c0 + cf + 2 * p, fin - 2 * p) : both(0.f);
-        bias[p] = in.bias ? two_at<float, false>(in.bias + at.c0 + cf + 2 * p, fin - 2 * p) : both(0.f);
+        D[p] = in.D ? two_of(in.D + at.c0 + cf + 2 * p, fin - 2 * p) : both(0.f);
+        bias[p] = in.bias ? two_of(in.bias + at.c0 + cf + 2 * p, fin - 2 * p) : both(0.f);
     }
     const int64_t row0 = at.b * q.N + first, wide_rows = (int64_t)q.G * 2 * NS;
     float* parts = out.rows + ((int64_t)(at.tile - at.g * q.per_group) * q.B * q.N + row0) * wide_rows + at.g * 2 * NS;

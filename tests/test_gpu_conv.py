@@ -28,7 +28,8 @@ def util():
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("W", [2, 3, 4])
-@pytest.mark.parametrize("B,N,C", [(1, 1, 1), (2, 2, 8), (1, 3, 33), (3, 5, 40), (2, 67, 24), (1, 130, 257)])
+@pytest.mark.parametrize("B,N,C", [(1, 1, 1), (2, 2, 8), (1, 3, 33), (3, 5, 40), (2, 67, 24), (1, 130, 257),
+                                   (700, 5, 8)])
 def test_sizes(B, N, C, W, dtype):
     u = util()
     u.check_conv(u.conv_problem(B, N, C, W, dtype, N + C))

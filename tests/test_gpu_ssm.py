@@ -119,9 +119,9 @@ def test_lengths(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("slices,n", [(8, 16), (3, 16), (8, 8), (5, 32), (16, 64)])
+@pytest.mark.parametrize("slices,n", [(8, 16), (3, 16), (2, 16), (8, 8), (6, 8), (5, 32), (4, 32), (16, 64), (2, 64)])
 def test_strides(slices, n, dtype):
-    """Slices of wider rows on and off 16-byte boundaries, in pieces of a longer sequence."""
+    """Slices of wider rows on boundaries of 16, 8, 4 and 2 bytes, in pieces of a longer sequence."""
     u = util()
     p = u.ssm_problem(2, 41, 32, n, 1, dtype, 7, slices=slices)
     assert not p["x"].is_contiguous() and not p["Cm"].is_contiguous()
@@ -187,7 +187,46 @@ def test_step(B, C, n, G, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("B,N,C,n", [(1, 1500, 200, 16), (2, 1111, 24, 8), (1, 700, 520, 64), (40, 40, 512, 16)])
+@pytest.mark.parametrize("B,C,n,G,slices", [(203, 128, 16, 1, 0), (401, 129, 8, 3, 0), (37, 160, 64, 2, 0), (82, 130, 32, 1, 3),
+                                            (206, 98, 16, 2, 4)])
+def test_step_of_many_rows(B, C, n, G, slices, dtype):
+    """Several rows a thread, batches that do not divide by them, B and C on and off the boundaries
+    of their loads."""
+    u = util()
+    p = u.ssm_problem(B, 1, C, n, G, dtype, 15, slices=slices)
+    S = p["S0"].clone()
+    out = la.la_decode_step_ssm(S, p["x"][:, 0], p["delta"][:, 0], p["A"], p["Bm"][:, 0], p["Cm"][:, 0], D=p["D"],
+                                z=p["z"][:, 0], delta_bias=p["delta_bias"])
+    ref, r_S = u.ssm_oracle(p)
+    u.near(out, ref[:, 0], "out")
+    u.near(S, r_S, "S")
+
+
+def test_captured_steps():
+    """A captured step moves window and state on at every replay, as eager calls do."""
+    u = util()
+    p, c = u.ssm_problem(3, 1, 64, 16, 1, BF, 16), u.conv_problem(3, 1, 64, 4, BF, 16)
+    step = [p[k][:, 0] for k in ("delta", "A", "Bm", "Cm")]
+    step[1] = p["A"]
+
+    def one(win, S):
+        x = la.la_decode_step_conv(win, c["x"][:, 0], c["weight"], c["bias"])
+        return la.la_decode_step_ssm(S, x, *step, D=p["D"], z=p["z"][:, 0], delta_bias=p["delta_bias"])
+
+    win, S = c["S0"].clone(), p["S0"].clone()
+    want = [one(win, S).clone() for _ in range(3)]
+    win2, S2 = c["S0"].clone(), p["S0"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = one(win2, S2)
+    for k in range(3):
+        graph.replay()
+        assert torch.equal(out, want[k]), k
+    assert torch.equal(win, win2) and torch.equal(S, S2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,N,C,n", [(400, 20, 16, 16), (1, 1500, 200, 16), (2, 1111, 24, 8), (1, 700, 520, 64), (40, 40, 512, 16)])
 def test_segments(B, N, C, n, dtype):
     """Few long rows (segments and their join) and many short ones, twice the same bits; scratch
     of any content, none of it written behind its end.  N = 1500: the mean error of a decay
