@@ -114,7 +114,6 @@ __device__ __forceinline__ int64_t y_at(int64_t b, int64_t t, int c, const ConvS
 template <typename T>
 constexpr int ahead()
 {
-    
     return sizeof(T) == 2 ? 8 : 4;
 }
 
@@ -254,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
                 const int* __restrict__ lengths, T* __restrict__ dx, T* __restrict__ dS0, float* __restrict__ part,
                 ConvShape s, int64_t jobs)
 {
-    
     constexpr int P = Pairs<V>::P, kAhead = sizeof(T) == 2 ? 4 : 2;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * V;
     if (c >= s.C)

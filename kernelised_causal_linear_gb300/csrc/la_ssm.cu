@@ -28,7 +28,6 @@ using namespace rows;
 
 template <typename T, int NS>
 struct Cut {
-    
     static constexpr int NT = 64;                   // threads
     static constexpr int SPT = NS < 16 ? NS : 16;   // states of a thread
     static constexpr int LPC = NS / SPT;            // lanes that share a channel pair
@@ -453,7 +452,6 @@ cudaError_t run_ssm(const SsmArgs& a)
     const unsigned blocks = (unsigned)(a.B * q.segs * q.G * q.per_group);
     float* ends = static_cast<float*>(a.ws);
     float* sums = ends + a.B * q.segs * a.C * NS;
-    
     static_assert(sizeof(Tiles<T, NS, false>) <= 48 * 1024, "shared memory of a launch without attributes");
     auto launch = [&](auto kernel, size_t shared) {
         kernel<<<blocks, L::NT, shared, a.stream>>>(in, static_cast<T*>(a.out), a.S0, a.S_out, ends, sums, q);
