@@ -68,7 +68,13 @@ __device__ __forceinline__ void load_filter(const float* __restrict__ weight, co
                                             Pairs<V> (&w)[W], Pairs<V>& b)
 {
     float flat[2 * Pairs<V>::P * W] = {};  // neighbouring filters are neighbours in memory
-    if constexpr (V > 1) {
+    if constexpr (V == 2) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float2 q = __ldg(reinterpret_cast<const float2*>(weight + (int64_t)c * W) + k);
+            flat[2 * k] = q.x, flat[2 * k + 1] = q.y;
+        }
+    } else if constexpr (V == 4) {
 #pragma unroll
         for (int k = 0; k < V * W / 4; ++k) {
             const float4 q = __ldg(reinterpret_cast<const float4*>(weight + (int64_t)c * W) + k);
@@ -414,11 +420,14 @@ int grad_run(const ConvArgs& a, int64_t rows)
     return (int)(run > 8 ? run : 8);
 }
 
-// Four channels in a load where rows and heads allow it, else one (bf16, off by one element: forward
-// of B4 N8192 C4096 99 and 150 us, gradient of C2048 92 and 230 us).
-bool vectors(const ConvArgs& a, int es, bool step)
+// Channels of a load, as many as rows and heads allow (bf16, forward of B4 N8192 C4096: four 99 us,
+// two 134, one 150; gradient of C2048 92, 131 and 231 us).
+int width(const ConvArgs& a, int es, bool step)
 {
-    return a.C / a.H % 4 == 0 && rows_on(a.x, a.xb, step ? 0 : a.xt, es, 4 * es);
+    for (int v = 4; v > 1; v /= 2)
+        if (a.C / a.H % v == 0 && rows_on(a.x, a.xb, step ? 0 : a.xt, es, v * es))
+            return v;
+    return 1;
 }
 
 template <typename T, int V, int W, int ACT>
@@ -481,11 +490,19 @@ cudaError_t conv_taps(const ConvArgs& a, int mode)
     }
 }
 
+template <typename T>
+cudaError_t conv_widths(const ConvArgs& a, int mode)
+{
+    switch (width(a, (int)sizeof(T), mode == 1)) {
+    case 4: return conv_taps<T, 4>(a, mode);
+    case 2: return conv_taps<T, 2>(a, mode);
+    default: return conv_taps<T, 1>(a, mode);
+    }
+}
+
 cudaError_t conv_types(const ConvArgs& a, int mode)
 {
-    if (a.dtype == LA_BF16)
-        return vectors(a, 2, mode == 1) ? conv_taps<__nv_bfloat16, 4>(a, mode) : conv_taps<__nv_bfloat16, 1>(a, mode);
-    return vectors(a, 4, mode == 1) ? conv_taps<float, 4>(a, mode) : conv_taps<float, 1>(a, mode);
+    return a.dtype == LA_BF16 ? conv_widths<__nv_bfloat16>(a, mode) : conv_widths<float>(a, mode);
 }
 
 }  // namespace

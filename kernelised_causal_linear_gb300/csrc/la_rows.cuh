@@ -15,6 +15,12 @@ template <> struct Raw<float, 4> {
 template <> struct Raw<__nv_bfloat16, 4> {
     uint2 w;
 };
+template <> struct Raw<float, 2> {
+    float2 w;
+};
+template <> struct Raw<__nv_bfloat16, 2> {
+    uint32_t w;
+};
 template <> struct Raw<float, 1> {
     float w;
 };
@@ -52,9 +58,23 @@ __device__ __forceinline__ Vec<4> wide(const Raw<__nv_bfloat16, 4>& x)
              __uint_as_float(x.w.y & 0xffff0000u)}};
 }
 
+__device__ __forceinline__ Vec<2> wide(const Raw<float, 2>& x) { return {{x.w.x, x.w.y}}; }
+__device__ __forceinline__ Vec<2> wide(const Raw<__nv_bfloat16, 2>& x)
+{
+    return {{__uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u)}};
+}
+
 __device__ __forceinline__ void store(float* p, const Vec<4>& r)
 {
     *reinterpret_cast<float4*>(p) = make_float4(r.f[0], r.f[1], r.f[2], r.f[3]);
+}
+__device__ __forceinline__ void store(float* p, const Vec<2>& r)
+{
+    *reinterpret_cast<float2*>(p) = make_float2(r.f[0], r.f[1]);
+}
+__device__ __forceinline__ void store(__nv_bfloat16* p, const Vec<2>& r)
+{
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(r.f[0], r.f[1]);
 }
 __device__ __forceinline__ void store(float* p, const Vec<1>& r) { *p = r.f[0]; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, const Vec<1>& r) { *p = __float2bfloat16_rn(r.f[0]); }

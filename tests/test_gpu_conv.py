@@ -29,7 +29,7 @@ def util():
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("W", [2, 3, 4])
 @pytest.mark.parametrize("B,N,C", [(1, 1, 1), (2, 2, 8), (1, 3, 33), (3, 5, 40), (2, 67, 24), (1, 130, 257),
-                                   (700, 5, 8)])
+                                   (700, 5, 8), (2, 70, 66), (1, 9, 2)])
 def test_sizes(B, N, C, W, dtype):
     u = util()
     u.check_conv(u.conv_problem(B, N, C, W, dtype, N + C))
@@ -44,7 +44,7 @@ def test_options(activation, bias, state):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("heads,C", [(1, 16), (3, 96), (4, 20), (7, 7), (2, 128)])
+@pytest.mark.parametrize("heads,C", [(1, 16), (3, 96), (4, 20), (7, 7), (2, 128), (5, 30), (3, 6)])
 def test_head_major(heads, C, dtype):
     u = util()
     u.check_conv(u.conv_problem(2, 70, C, 4, dtype, C, heads=heads))
@@ -71,7 +71,7 @@ def test_lengths(W, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
-@pytest.mark.parametrize("slices", [8, 3])
+@pytest.mark.parametrize("slices", [8, 3, 2, 4])
 def test_strides(slices, dtype):
     """Slices of wider rows, on and off 16-byte boundaries; tokens out of a longer tensor;
     tokens in another order; one row for all (stride 0)."""
