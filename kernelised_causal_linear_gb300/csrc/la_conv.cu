@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
             const int64_t p = first - (W - 1) + j;  // not behind the row's last: nothing is known of that
             win[j] = pairs(p < len ? input<T, V, W>(x, S0, b, p, c, s) : none<T, V>());
         }
-        // From token t, its inputs x and dy and whether dw takes it: du_t, and dx of the token
-        // W - 1 before.
-        auto token = [&](const Raw<T, V>& xin, const Raw<T, V>& din, bool own) {
+        // From token t, its inputs x and dy, whether the row has it (behind its end the slope of
+        // an infinite u would make 0 dy a NaN) and whether dw takes it: du_t, and dx of the
+        // token W - 1 before.
+        auto token = [&](const Raw<T, V>& xin, const Raw<T, V>& din, bool on, bool own) {
             win[W - 1] = pairs(xin);
             const Pairs<V> d = pairs(din);
             Pairs<V> o;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     u = fma2(w[j].p[i], win[j].p[i], u);
-                const float2 g = mul2(d.p[i], slope<ACT>(u)), t = own ? g : both(0.0f);
+                const float2 g = on ? mul2(d.p[i], slope<ACT>(u)) : both(0.0f), t = own ? g : both(0.0f);
                 db.p[i] = add2(db.p[i], t);
 #pragma unroll
                 for (int j = 0; j < W; ++j)
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
         // the final window (positions len - W + 1 .. len - 1) adds its gradient
         auto edge = [&](int64_t t) {
             const bool on = t < len && t < s.N;
-            Pairs<V> o = token(on ? fetch<T, V>(xp) : none<T, V>(), on ? fetch<T, V>(dp) : none<T, V>(), t < end);
+            Pairs<V> o = token(on ? fetch<T, V>(xp) : none<T, V>(), on ? fetch<T, V>(dp) : none<T, V>(), on, t < end);
             xp += s.xt, dp += dh;
             const int64_t at = t - (W - 1), row = at - (len - (W - 1));
             if (at < first && (r > 0 || !dS0))
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
                     group(xin[half ^ 1], din[half ^ 1]);
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k, out += s.C)
-                    store_pairs(out, token(xin[half][k], din[half][k], true));
+                    store_pairs(out, token(xin[half][k], din[half][k], true, true));
             }
         }
         for (; t < end + W - 1; ++t)

@@ -70,6 +70,23 @@ def test_lengths(W, dtype):
     assert all(torch.isfinite(g).all() for g in grads)
 
 
+@pytest.mark.parametrize("activation", ["silu", "sigmoid"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_infinite_last_token(W, activation):
+    """What a row's last token is does not reach behind it, nor other rows and channels."""
+    u = util()
+    lengths = [1, 2, 3, 5, 8, 33, 64, 70]
+    p = u.conv_problem(8, 70, 24, W, F32, 13, lengths=lengths)
+    for b, n in enumerate(lengths):
+        p["x"][b, n - 1, 0] = float("inf")
+    y, _ = la.la_forward_conv(p["x"], p["weight"], p["bias"], activation=activation, S0=p["S0"], lengths=p["lengths"])
+    dx, dw, db, dS0 = la.la_backward_conv(p["dy"], p["x"], p["weight"], p["bias"], activation=activation, S0=p["S0"],
+                                          dS_out=p["dS_out"], lengths=p["lengths"])
+    for b, n in enumerate(lengths):
+        assert not y[b, n:].any() and not dx[b, n:].any()
+    assert all(torch.isfinite(g).all() for g in (y[..., 1:], dx[..., 1:], dw[1:], db[1:], dS0[..., 1:]))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("slices", [8, 3, 2, 4])
 def test_strides(slices, dtype):
