@@ -611,7 +611,9 @@ __global__ void __launch_bounds__(kThreads)
                     if (in.z.p) {
                         const float2 z = make_float2(to_f32(zr[p][0]), to_f32(zr[p][1]));
                         const float2 o = make_float2(to_f32(orr[p][0]), to_f32(orr[p][1]));
-                        const float2 vz = mul2(mul2(o, fma2(D[p], x, y[0][p])), slope<LA_ACT_SILU>(z));
+                        float2 vz = mul2(mul2(o, fma2(D[p], x, y[0][p])), slope<LA_ACT_SILU>(z));
+                        if (!on)  // zero times an infinite state
+                            vz = both(0.f);
                         put_two<VEC>(static_cast<T*>(out.dz) + dst + 2 * p, vz, some);
                     }
                 }
@@ -626,11 +628,11 @@ __global__ void __launch_bounds__(kThreads)
                 for (int i = threadIdx.x; i < SUB * 2 * NS; i += kThreads) {
                     const int t = i / (2 * NS), m = i - t * 2 * NS;
                     if (blk * BLK + t < min(here, blocks * BLK)) {
-                        float sum = sm.sums[0][t][m];
+                        float sum = sm.sums[0][t][m];  // behind the row's last token perhaps zero times infinity
 #pragma unroll
                         for (int k = 1; k < kWarps; ++k)
                             sum += sm.sums[k][t][m];
-                        parts[(blk * BLK + t) * wide_rows + m] = sum;
+                        parts[(blk * BLK + t) * wide_rows + m] = blk * BLK + t < live ? sum : 0.0f;
                     }
                 }
                 __syncthreads();

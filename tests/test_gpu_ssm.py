@@ -118,6 +118,24 @@ def test_lengths(n, dtype):
     assert all(torch.equal(a, b) for a, b in zip((*run(), *back()), want))
 
 
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+def test_infinite_last_token(n):
+    """A state that the row's last token made infinite does not reach behind it."""
+    u = util()
+    lengths = [1, 2, 3, 5, 30, 33, 67, 70]
+    p = u.ssm_problem(8, 70, 20, n, 1, F32, 16, lengths=lengths)
+    for b, m in enumerate(lengths):
+        p["x"][b, m - 1] = float("inf")
+    pos, kw = u.ssm_args(p)
+    out, _ = la.la_forward_ssm(*pos, **kw, S0=p["S0"], lengths=p["lengths"])
+    g = dict(zip(u.LEAVES, la.la_backward_ssm(p["dout"], *pos, **kw, S0=p["S0"], dS_out=p["dS_out"],
+                                              lengths=p["lengths"])))
+    for b, m in enumerate(lengths):
+        assert not out[b, m:].any()
+        for name in ("x", "delta", "z", "Bm", "Cm"):
+            assert not g[name][b, m:].any(), (name, m)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("slices,n", [(8, 16), (3, 16), (2, 16), (8, 8), (6, 8), (5, 32), (4, 32), (16, 64), (2, 64)])
 def test_strides(slices, n, dtype):
