@@ -412,7 +412,7 @@ int run_length(const ConvArgs& a, int vec)
 // there are no more sequences than block rows, eight tokens at least.
 int64_t grad_rows(const ConvArgs& a, int vec)
 {
-    const int64_t cols = (a.C / vec + kThreads - 1) / kThreads, rows = kGradPerSm * 152 / cols;
+    const int64_t wide = vec * kThreads, cols = (a.C + wide - 1) / wide, rows = kGradPerSm * 152 / cols;
     return rows > 1 ? rows : 1;
 }
 int grad_run(const ConvArgs& a, int64_t rows)
@@ -508,7 +508,8 @@ cudaError_t conv_types(const ConvArgs& a, int mode)
 
 }  // namespace
 
-// Block rows are most with vectors (fewest column blocks).
+// A part for every block row of the launch.  Block rows are most with four channels a thread
+// (fewest column blocks), whatever width the launch then takes.
 size_t conv_backward_workspace(const ConvArgs& a)
 {
     const int64_t rows = grad_rows(a, 4);

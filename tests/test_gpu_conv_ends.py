@@ -1,0 +1,56 @@
+"""The short causal convolution where its sizes and rows end, on the GPU against fp64."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import to_np
+from oracle import ssm
+
+pytestmark = pytest.mark.gpu
+
+la = pytest.importorskip("kernelised_causal_linear_gb300")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a CUDA device")
+    yield
+    assert la.la_get_device_status() == 0
+
+
+def util():
+    import ssm_util
+
+    return ssm_util
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("W", [2, 4])
+@pytest.mark.parametrize("C", [1, 2, 3, 5])
+def test_few_channels(C, W, dtype):
+    """Hundreds of block rows for a channel or two: parts in a workspace of exactly the stated size,
+    with nothing written behind it.  A sum's longest chain is 25 tokens, 19 parts and 32 joins, each
+    term a few 2^-24 off (20 taken): 96 roundings of at most the sum of the terms' sizes, which is at most
+    1.1 |dy| |x| (1.1: the largest slope of silu)."""
+    u = util()
+    p = u.conv_problem(3, 5003, C, W, dtype, 20 + C, lengths=[5003, 4001, 17])
+    need = la.la_conv_backward_workspace_size(3, 5003, C, W, dtype)
+    ws = torch.randint(0, 256, (need + 65536,), dtype=torch.uint8, device="cuda")
+    tail = ws[need:].clone()
+    run = lambda **k: la.la_backward_conv(p["dy"], p["x"], p["weight"], p["bias"], S0=p["S0"],  # noqa: E731
+                                          dS_out=p["dS_out"], lengths=p["lengths"], **k)
+    got = run(workspace=ws[:need])
+    assert torch.equal(ws[need:], tail)
+    assert all(torch.equal(a, b) for a, b in zip(got, run()))
+    h = {k: to_np(p[k]) for k in ("x", "weight", "bias", "S0", "lengths", "dS_out", "dy")}
+    _, _, dx, dw, db, dS0 = ssm.conv(h.pop("x"), h.pop("weight"), h.pop("bias"), **h)
+    u.near(got[0], dx, "dx")
+    u.near(got[3], dS0, "dS0")
+    size = lambda *ts: np.sqrt(sum((t.astype(np.float64) ** 2).sum((0, 1)) for t in ts))  # noqa: E731
+    terms = 96 * 2.0 ** -24 * 1.1 * size(h["dy"])
+    inputs = np.maximum(size(to_np(p["x"]), h["S0"]), np.sqrt(3 * 5003))
+    for name, g, want in (("dw", got[1], dw.T), ("db", got[2], db)):
+        g = to_np(g).T
+        assert np.all(np.abs(g - want) <= terms * inputs), (name, np.abs(g - want).max())
