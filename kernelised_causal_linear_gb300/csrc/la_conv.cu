@@ -277,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
             win[j] = pairs(p < len ? input<T, V, W>(x, S0, b, p, c, s) : none<T, V>());
         }
         // From token t, its inputs x and dy, whether the row has it (behind its end the slope of
-        // an infinite u would make 0 dy a NaN) and whether dw takes it: du_t, and dx of the
-        // token W - 1 before.
+        // an infinite u would make 0 dy a NaN) and whether it is one of this run's, which alone
+        // dw and dbias take (zero times an infinite input of the window would be a NaN): du_t, and
+        // dx of the token W - 1 before.
         auto token = [&](const Raw<T, V>& xin, const Raw<T, V>& din, bool on, bool own) {
             win[W - 1] = pairs(xin);
             const Pairs<V> d = pairs(din);
@@ -289,11 +290,13 @@ __global__ void __launch_bounds__(kThreads, kGradPerSm)
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     u = fma2(w[j].p[i], win[j].p[i], u);
-                const float2 g = on ? mul2(d.p[i], slope<ACT>(u)) : both(0.0f), t = own ? g : both(0.0f);
-                db.p[i] = add2(db.p[i], t);
+                const float2 g = on ? mul2(d.p[i], slope<ACT>(u)) : both(0.0f);
+                if (on && own) {
+                    db.p[i] = add2(db.p[i], g);
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    dw[j].p[i] = fma2(t, win[j].p[i], dw[j].p[i]);
+                    for (int j = 0; j < W; ++j)
+                        dw[j].p[i] = fma2(g, win[j].p[i], dw[j].p[i]);
+                }
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
                     du[j].p[i] = du[j + 1].p[i], win[j].p[i] = win[j + 1].p[i];

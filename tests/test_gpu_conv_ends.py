@@ -54,3 +54,24 @@ def test_few_channels(C, W, dtype):
     for name, g, want in (("dw", got[1], dw.T), ("db", got[2], db)):
         g = to_np(g).T
         assert np.all(np.abs(g - want) <= terms * inputs), (name, np.abs(g - want).max())
+
+
+@pytest.mark.parametrize("activation", ["none", "sigmoid"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_infinite_last_token_and_the_filters(dtype, W, activation):
+    """Where a row's last token is infinite, only the last tap meets it: the others' gradients, the
+    bias's and dx stay what they are, for rows that end inside a run and just behind one."""
+    u = util()
+    lengths = [1, 2, 3, 5, 8, 9, 33, 64, 69, 70]
+    p = u.conv_problem(10, 70, 24, W, dtype, 14, lengths=lengths)
+    for b, n in enumerate(lengths):
+        p["x"][b, n - 1, 0] = float("inf")
+    dx, dw, db, dS0 = la.la_backward_conv(p["dy"], p["x"], p["weight"], p["bias"], activation=activation, S0=p["S0"],
+                                          dS_out=p["dS_out"], lengths=p["lengths"])
+    h = {k: to_np(p[k]) for k in ("x", "weight", "bias", "S0", "lengths", "dS_out", "dy")}
+    with np.errstate(invalid="ignore"):
+        _, _, rdx, rdw, rdb, rdS0 = ssm.conv(h.pop("x"), h.pop("weight"), h.pop("bias"), activation=activation, **h)
+    for got, want, name in ((dx, rdx, "dx"), (dw[:, :-1], rdw[:, :-1], "dw"), (dw[1:], rdw[1:], "dw"), (db, rdb, "db"),
+                            (dS0, rdS0, "dS0")):
+        u.near(got, want, name)
