@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kThreads)
                         ag[p][s] = mul2(decay(d[p], A2[p][s]), g);
                         const float2 qt = mul2(ag[p][s], j ? hs[j ? j - 1 : 0][p][s] : base[p][s]);
                         ddt[j][p] = s ? fma2(qt, A2[p][s], ddt[j][p]) : mul2(qt, A2[p][s]);
-                        dA[p][s] = fma2(qt, d[p], dA[p][s]);
+                        if (t < live)  // behind the row's last token perhaps infinity times zero
+                            dA[p][s] = fma2(qt, d[p], dA[p][s]);
                     }
                 float r[2 * SPT];
 #pragma unroll
