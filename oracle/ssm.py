@@ -109,22 +109,25 @@ def scan(x, delta, A, Bm, Cm, *, D=None, z=None, delta_bias=None, softplus_on=Tr
     for t in reversed(range(N)):
         on = (t < ends)[:, None]
         held, new = kept[t]
-        do = np.where(on, _f(dout)[:, t], 0.0)
-        y = (new * wide(Cm[:, t])).sum(-1) + d_skip * x[:, t]
-        g["z"][:, t] = do * y * gate_slope[:, t]
-        dy = do * gate[:, t]
+        # behind a row's end every input is zero, and the states of its last token are not read
+        live = lambda v: np.where(on if v.ndim == 2 else on[..., None], v, 0.0)  # noqa: E731
+        held, new, do, xt, dtt = map(live, (held, new, _f(dout)[:, t], x[:, t], dt[:, t]))
+        Bt, Ct = live(wide(Bm[:, t])), live(wide(Cm[:, t]))
+        y = (new * Ct).sum(-1) + d_skip * xt
+        g["z"][:, t] = do * y * live(gate_slope[:, t])
+        dy = do * live(gate[:, t])
         g["Cm"][:, t] = group(dy[..., None] * new)
-        dS = dS + dy[..., None] * wide(Cm[:, t])
-        here = np.where(on[..., None], dS, 0.0)
+        dS = dS + dy[..., None] * Ct
+        here = live(dS)
         q = here * (new if plant == "decay_of_the_new_state" else held)
-        w = (here * wide(Bm[:, t])).sum(-1)
-        g["Bm"][:, t] = group(here * (dt[:, t] * x[:, t])[..., None])
-        g["A"] += (q * dt[:, t, :, None]).sum(0)
-        g["x"][:, t] = w * dt[:, t] + d_skip * dy
-        g["D"] += (dy * x[:, t]).sum(0)
-        g["delta"][:, t] = (q * A).sum(-1) + w * x[:, t]
+        w = (here * Bt).sum(-1)
+        g["Bm"][:, t] = group(here * (dtt * xt)[..., None])
+        g["A"] += (q * dtt[..., None]).sum(0)
+        g["x"][:, t] = w * dtt + d_skip * dy
+        g["D"] += (dy * xt).sum(0)
+        g["delta"][:, t] = (q * A).sum(-1) + w * xt
         if plant != "softplus_not_differentiated":
-            g["delta"][:, t] *= slope[:, t]
+            g["delta"][:, t] *= live(slope[:, t])
         g["delta_bias"] += g["delta"][:, t].sum(0)
         dS = np.where(on[..., None], dS * np.exp(dt[:, t, :, None] * A), dS)
     return dict(g, S0=dS, out=out, S=S)
