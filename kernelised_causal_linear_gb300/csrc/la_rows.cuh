@@ -130,15 +130,23 @@ __device__ __forceinline__ float rcp(float x)
     return y;
 }
 
+// The larger one, and a NaN where either is one (fmaxf takes the other).
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // sigmoid(u) = 1 / (1 + e), e = exp(-u), and 1 - sigmoid(u) = e sigmoid(u), which keeps its
 // digits where the difference would not.  u is held above -87, where e is still finite: what
-// lies under it has results under 1e-35.
+// lies under it has results under 1e-35.  A NaN stays one.
 struct Sigmoid {
     float2 u, s, rest;
 };
 __device__ __forceinline__ Sigmoid sigmoid(float2 u)
 {
-    u = make_float2(fmaxf(u.x, -87.0f), fmaxf(u.y, -87.0f));
+    u = make_float2(max_nan(u.x, -87.0f), max_nan(u.y, -87.0f));
     const float2 t = mul2(u, both(-kLog2e)), e = make_float2(ex2(t.x), ex2(t.y)), q = add2(e, both(1.0f));
     const float2 s = make_float2(rcp(q.x), rcp(q.y));
     return {u, s, mul2(e, s)};

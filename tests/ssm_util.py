@@ -129,3 +129,12 @@ def check_conv(p, activation="silu", tol=1e-5):
             assert p["bias" if name == "dbias" else "S0"] is None
         else:
             near(got, ref, name, tol)
+
+
+def same_nan(results, tol=1e-5):
+    """(name, got, reference) each: NaN in the same places, and near elsewhere."""
+    for name, got, ref in results:
+        bad = np.isnan(ref)
+        assert np.array_equal(np.isnan(to_np(got)), bad), (name, np.argwhere(np.isnan(to_np(got)) != bad)[:8])
+        ok = torch.from_numpy(~bad).to(got.device)
+        near(got[ok], np.asarray(ref)[~bad], name, tol)

@@ -75,3 +75,21 @@ def test_infinite_last_token_and_the_filters(dtype, W, activation):
     for got, want, name in ((dx, rdx, "dx"), (dw[:, :-1], rdw[:, :-1], "dw"), (dw[1:], rdw[1:], "dw"), (db, rdb, "db"),
                             (dS0, rdS0, "dS0")):
         u.near(got, want, name)
+
+
+@pytest.mark.parametrize("activation", ["silu", "sigmoid", "none"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_nan_of_a_token_is_seen(dtype, activation):
+    """A NaN that a row has comes out wherever the definition takes it, and nowhere else."""
+    u = util()
+    p = u.conv_problem(3, 40, 10, 4, dtype, 15, lengths=[40, 17, 30])
+    p["x"][0, 20, 3] = p["x"][1, 16, 4] = p["x"][2, 30, 5] = float("nan")  # the last one behind its row
+    y, _ = la.la_forward_conv(p["x"], p["weight"], p["bias"], activation=activation, S0=p["S0"], lengths=p["lengths"])
+    got = (y, *la.la_backward_conv(p["dy"], p["x"], p["weight"], p["bias"], activation=activation, S0=p["S0"],
+                                   dS_out=p["dS_out"], lengths=p["lengths"]))
+    h = {k: to_np(p[k]) for k in ("x", "weight", "bias", "S0", "lengths", "dS_out", "dy")}
+    ref = ssm.conv(h.pop("x"), h.pop("weight"), h.pop("bias"), activation=activation, **h)
+    u.same_nan(zip(("y", "dx", "dw", "db", "dS0"), got, (ref[0], *ref[2:])))
+    win = p["S0"].clone()
+    y1 = la.la_decode_step_conv(win, p["x"][:, 20], p["weight"], p["bias"], activation=activation)
+    assert torch.isnan(y1).nonzero().tolist() == [[0, 3]]

@@ -41,3 +41,19 @@ def test_overflow_of_a_last_state_and_dA(ragged, n, dtype):
         assert torch.isinf(S).all()
         g = la.la_backward_ssm(p["dout"], *pos, **kw, S0=p["S0"], dS_out=p["dS_out"], lengths=p["lengths"])
         u.near(g[2], u.ssm_oracle(p, grad=True)["A"], "dA")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("name", ["z", "x", "delta", "dout", "Bm", "Cm"])
+def test_nan_of_a_token_is_seen(name, n, dtype):
+    """A NaN that a row has comes out wherever the definition takes it, and nowhere else."""
+    u = util()
+    p = u.ssm_problem(3, 75, 11, n, 1, dtype, 18, lengths=[75, 40, 61])
+    p[name].view(3, 75, -1)[0, 37, 3] = p[name].view(3, 75, -1)[1, 39, 4] = float("nan")
+    ref = u.ssm_oracle(p, grad=True)
+    p[name].view(3, 75, -1)[2, 61, 5] = float("nan")  # behind its row: not read
+    pos, kw = u.ssm_args(p)
+    out, S = la.la_forward_ssm(*pos, **kw, S0=p["S0"], return_state=True, lengths=p["lengths"])
+    g = la.la_backward_ssm(p["dout"], *pos, **kw, S0=p["S0"], dS_out=p["dS_out"], lengths=p["lengths"])
+    u.same_nan([("out", out, ref["out"]), ("S", S, ref["S"])] + [(k, t, ref[k]) for k, t in zip(u.LEAVES, g)])
