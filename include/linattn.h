@@ -467,8 +467,10 @@ LA_API la_status la_decode_step_ssm(float* S, const void* x, const void* delta, 
  * fp32.  dD, dz and ddelta_bias are NULL exactly when D, z and delta_bias are; dS0 may
  * be NULL.  All sums are in a fixed order.  strides: HOST pointer to 12 numbers, the
  * pairs of la_forward_ssm and that of dout, or NULL.  Workspace: 256-byte aligned,
- * la_ssm_backward_workspace_size() bytes.  With N = 0 the parameters' gradients are zero
- * and dS0 receives dS_out (or zero).
+ * la_ssm_backward_workspace_size() bytes: three states for every 32 tokens and a part of
+ * dBm and dCm for every 128 channels of a group (n = 32: 64, n = 64: 32), whatever the type,
+ * e.g. 487 MB for B = 4, N = 8192, C = 2048, G = 1, n = 16 and 2.7 GB for n = 64.  With N = 0
+ * the parameters' gradients are zero and dS0 receives dS_out (or zero).
  */
 LA_API size_t la_ssm_backward_workspace_size(int64_t B, int64_t N, int64_t C, int64_t G, int n,
                                              int dtype);

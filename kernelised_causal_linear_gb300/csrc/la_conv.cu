@@ -114,16 +114,19 @@ __device__ __forceinline__ int64_t y_at(int64_t b, int64_t t, int c, const ConvS
     return ((b * s.H + h) * s.N + t) * dh + (c - h * dh);
 }
 
-// Tokens whose loads are issued together, one group ahead of the one in use (bf16 B4 N8192
-// C4096: eight with none ahead 114 us; one group ahead four 92, eight 87, sixteen 87 us; the same
-// bytes in fp32 79 us).
+// Tokens whose loads are issued together, one group ahead of the one in use (B4 N8192 C4096 bf16:
+// four 109 us, eight 96, sixteen 111; the same bytes in fp32: four 95 us, sixteen 130).  Times in this
+// file are of a call among others, device and no host; after a flush of L2, when no earlier call's
+// lines wait to be written, the same kernel takes 87 us (fp32 82).
 template <typename T>
 constexpr int ahead()
 {
     return sizeof(T) == 2 ? 8 : 4;
 }
 
-// Five blocks an SM, 96 registers: 87 us; as many registers as it likes 116, six blocks 97.
+// Five blocks an SM, 96 registers: 96 us; as many registers as it likes 103, four blocks 111, six
+// 106.  In three forms four or eight bytes a thread spill (fp32 with sigmoid W = 4 and silu W = 2, bf16
+// with silu W = 3).
 template <typename T, int V, int W, int ACT>
 __global__ void __launch_bounds__(kThreads, 5)
     k_conv(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
@@ -248,8 +251,10 @@ __global__ void __launch_bounds__(kThreads)
 // dw and dbias stay in registers over all of a thread's runs; block row p leaves
 // part [p][W+1][C], summed in a fixed order by k_conv_dw (no atomics).
 // Bound by HBM's latency: four blocks an SM, which 128 registers allow, with two groups of
-// tokens in flight (bf16 B4 N8192 C2048: three blocks 131 us, four 80 us, five with spills 101
-// us; groups of two, four and six tokens 95, 80 and 89 us; the same bytes in fp32 with two 74 us).
+// tokens in flight (B4 N8192 C2048 bf16, sums included: three blocks 106 us, four 86, five with spills
+// 120; groups of two, four and six tokens 102, 86 and 95 us; the same bytes in fp32: 81, 92 and 98).
+// After a flush of L2 77 us and 4.4 for the sums.  One channel a load in bf16 spills 32 bytes, a
+// few forms 4 to 12.
 constexpr int kGradPerSm = 4;
 
 template <typename T, int V, int W, int ACT>
@@ -400,8 +405,11 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// Tokens per run of the forward: long enough that the W - 1 rows read twice are few, short
-// enough that the GPU is full.
+// Tokens per run of the forward: long enough that the W - 1 rows read twice are few (B4 N8192 C4096
+// bf16: runs of 32 tokens 105 us, 64 97, 128 and 256 96), short enough that the GPU is full (B64 N256
+// C4096: runs until there are 152 * 1024 threads 53 us, a quarter or half as many 58, twice 57).
+// The other side: a call as small as B1 N1024 C2048 has runs of four tokens, which load one after the
+// other, and takes 10 us where runs of eight would take 6.
 int run_length(const ConvArgs& a, int vec)
 {
     const int64_t vecs = a.C / vec * a.B;
@@ -424,8 +432,8 @@ int grad_run(const ConvArgs& a, int64_t rows)
     return (int)(run > 8 ? run : 8);
 }
 
-// Channels of a load, as many as rows and heads allow (bf16, forward of B4 N8192 C4096: four 99 us,
-// two 134, one 150; gradient of C2048 92, 131 and 231 us).
+// Channels of a load, as many as rows and heads allow (bf16, forward of B4 N8192 C4096: four 96 us,
+// two 129, one 148; gradient of C2048 86, 125 and 227 us; fp32 95, 93 and 95, gradient 81, 96 and 162).
 int width(const ConvArgs& a, int es, bool step)
 {
     for (int v = 4; v > 1; v /= 2)

@@ -9,7 +9,7 @@
 // hardware exponential (32 a clock and SM) and four fp32 operations in two-wide instructions,
 // which reach some 90 a clock and SM, not 128, where all three operands differ.  Both overlap in
 // part: 512 elements take about 150 clocks of a sub-partition, 80 of them of the exponentials'
-// unit, those of the steps and the gate among them (B4 N8192 C2048 n = 16 bf16: 275 us, and 190
+// unit, those of the steps and the gate among them (B4 N8192 C2048 n = 16 bf16: 277 us, and 188
 // us for the run for the ends).  (Four channels times four states per thread, with steps in
 // shared memory and shuffles, took 198 clocks.)
 //
@@ -90,7 +90,9 @@ __device__ __forceinline__ void store_pair(float* p, int have, const float2 (&h)
                     make_float4(h[c][s].x, h[c][s].y, h[c][s + 1].x, h[c][s + 1].y);
 }
 
-// Eight blocks an SM (128 registers): seven 490 us, eight 482, ten 556 (B4 N8192 C2048 n = 16).
+// Registers for eight blocks an SM (128 each): bounds of seven and eight blocks 485 and 484 us, of nine
+// and ten 580 (B4 N8192 C2048 n = 16 bf16; fp32 B2 281, 276, 336; n = 8 326, 324, 316; n = 64 B1 508,
+// 501, 572).  Shared memory admits eight too, but for the outputs with n = 16 in bf16: 28 KB, seven.
 //
 // END: the state after each segment but the last from a zero start (ends) and the sum of
 // its steps (sums).  Else the outputs, from S0 or (segments) from `ends`, which then holds
@@ -261,8 +263,8 @@ __global__ void __launch_bounds__(Cut<T, NS>::NT, 8)
 }
 
 // ends -> starts in place, one thread per state: a chain of one product and sum per
-// segment, with the loads of sixteen segments ahead of it (eight ahead with four states per
-// thread: 41 us in place of 18 for 76 segments of B4 C2048 n = 16).
+// segment, with the loads of sixteen segments ahead of it (18 us for 76 segments of B4 C2048 n = 16;
+// eight ahead with four states per thread took 41).
 __global__ void __launch_bounds__(128)
     k_ssm_join(const float* __restrict__ A, const float* S0, float* __restrict__ ends, const float* __restrict__ sums,
                int segs, int64_t C, int NS, int64_t items)
@@ -404,11 +406,17 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// Segments.  The run for the ends costs 0.7 of the one that counts, so rows stay whole
-// where they alone are nearly three blocks an SM (N2048 C2048 n = 16 bf16: 320 blocks whole
-// 727 us, cut 608; 448 blocks 728 and 823).  Else about four rounds of blocks, which fill up
-// better than one (N8192, 64 blocks: 24 segments 543 us, 76 segments 511 us), a tile each at
-// least (fp32 B2 N333 C197: 21 segments 28 us, 42 segments 20 us).
+// Segments.  The run for the ends costs 0.7 of the one that counts, so rows stay whole where they
+// alone are more than two and a half blocks an SM.  Whole and cut at N2048, us:
+//               320 blocks    384 blocks    448 blocks
+//   n = 8       562    411    562    477    562    544   bf16
+//   n = 16      762    611    763    724    763    826   bf16     fp32 at 448: 815 and 846
+//   n = 32      717    604    719    708    719    796   bf16     fp32        766     835
+//   n = 64      802    631    803    746    803    848   bf16     fp32        838     882
+// (n = 8 would be cut up to some 470 blocks: 3%.)  Else about four rounds of eight blocks an SM, a tile
+// each at least (fp32 B2 N333 C197: whole 92 us, a tile each 18.5; B1 N64 bf16 23 and 18.5).  One,
+// two, four and eight rounds, 64 blocks of N8192: n = 16 bf16 509, 497, 484, 485 us; n = 32 961, 894, 914,
+// 900; n = 8 312, 322, 324, 320; 32 blocks in fp32 260, 269, 277, 287; 16 blocks 150, 145, 152, 186.
 template <typename T, int NS>
 Grid grid_of(const SsmArgs& a)
 {
@@ -486,9 +494,10 @@ cudaError_t launch_step(const SsmArgs& a, const StepIns& in)
     return cudaGetLastError();
 }
 
-// Four rows a thread (n = 8: two) where that leaves a block for every SM (n = 16 bf16 C4096: B16
-// one row a thread 5.1 us, four 4.3; B256 38 and 22 us, 6.4 TB/s; with every lane reading all
-// four rows' x, delta and z 28 us, of instructions), else one: latency counts.
+// Four rows a thread (n = 8: two) where that leaves a block for every SM, else one: latency counts.
+// C4096 bf16, one row a thread and several: B256 n = 16 35 and 21 us, n = 8 19 and 14; B64 n = 64 35 and
+// 21, n = 16 in fp32 12 and 10; B16 and B5 the same.  Right after a flush of L2 23 us, 6.3 TB/s.  (With
+// every lane reading all four rows' x, delta and z it took 28 us, of instructions.)
 template <typename T, int NS>
 cudaError_t run_step(const SsmArgs& a)
 {

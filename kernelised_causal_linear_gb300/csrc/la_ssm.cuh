@@ -118,8 +118,8 @@ __device__ __forceinline__ void cp_wait()
 // A tile of `WIDE` columns into shared memory [TT][WIDE], `live` tokens and `cols` columns of it
 // from memory, the rest zero (bytes behind either are not read).  BYTES: what every row starts
 // and ends on a multiple of, 16 or 4, for copies of that size in flight; 0 for neither, element
-// by element (forward of B4 N8192 C2048 n = 16 bf16: 498 us on 16 bytes, 580 off by two elements,
-// 811 off by one; fp32 B2: 288 us, and 382 off by one).
+// by element (forward of B4 N8192 C2048 n = 16 bf16: 486 us on 16 bytes, 568 off by two elements,
+// 796 off by one; fp32 B2: 277 us, and 371 off by one).
 template <typename T, int TT, int WIDE, int BYTES, int NT>
 __device__ __forceinline__ void copy_tile(T* dst, const T* src, int64_t token, int live, int cols)
 {

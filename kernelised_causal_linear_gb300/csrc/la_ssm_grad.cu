@@ -22,7 +22,7 @@
 //
 // Bound by arithmetic: k_ssm_grad has 15 fp32 operations and three exponentials an element and
 // 400 instructions for 512 elements, at half of the issue slots with the two warps a
-// sub-partition that 255 registers leave (B4 N2048 C2048 n = 16 bf16: 333 us, of 475 with the ends
+// sub-partition that 255 registers leave (B4 N2048 C2048 n = 16 bf16: 332 us, of 474 with the ends
 // 99, the join 29 and the sums 15).  Two states per thread and twice the warps take a third
 // more instructions for the same time (392 us); twelve warps with 168 registers spill (435 us);
 // keeping the decays saves 2% and costs 64 registers; halves of 16 tokens, walked one and a half
@@ -279,7 +279,9 @@ __device__ __forceinline__ void pair_up(const float4& v, float2 (&p)[2])
 // Per segment: end of the state from zero, sum of the steps, and sum over its tokens of (the
 // decays up to t) C_t dy_t, the gradient in front of it.
 template <typename T, int NS, bool VEC>
-// (bf16: three blocks an SM 111 us, four 99 us; fp32 at four spills: 13 and 18 us, B3 N701 C600.)
+// (Blocks an SM, the whole gradient: bf16 B4 N2048 C2048 three 486 us, four 474; fp32 at four spills,
+// B2 273 and 286, B3 N701 C600 47 and 51.  bf16 at four spills 112 bytes with n = 16 off rows of four
+// elements, 4 to 8 in four other forms.)
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
     k_ssm_ends(GradIns in, float* __restrict__ ends, float* __restrict__ sums, float* __restrict__ fronts, Grid q)
 {
@@ -335,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
 }
 
 // In place, one thread per state: ends -> starts of the segments, fronts -> gradients at
-// their ends; loads of eight segments ahead of the chain (B16 N512 C2048 n = 16:
-// sixteen 58 us, eight 32; B1 N8192: 37 and 39).
+// their ends; loads of eight segments ahead of the chain (the whole gradient, C2048 n = 16, four, eight
+// and sixteen ahead: B16 N512 473, 477 and 503 us, B4 N2048 473, 474 and 481, B1 N8192 486, 484 and 481).
 __global__ void __launch_bounds__(128)
     k_ssm_join_grad(const float* __restrict__ A, const float* __restrict__ S0, const float* __restrict__ dS_out,
                     float* __restrict__ ends, const float* __restrict__ sums, float* __restrict__ fronts,
@@ -833,8 +835,8 @@ cudaError_t grad_rows(const SsmArgs& a)
     const GradIns in{{a.x, a.x_batch, a.x_token}, {a.delta, a.delta_batch, a.delta_token},
                      {a.Bm, a.B_batch, a.B_token}, {a.Cm, a.C_batch, a.C_token}, {a.z, a.z_batch, a.z_token},
                      {a.dout, a.dout_batch, a.dout_token}, a.A, a.D, a.bias, a.lengths, a.softplus};
-    // four channels in a load where rows and groups allow it (B4 N2048 C2048 n = 16 bf16: 493 us, off by
-    // one element 611)
+    // four channels in a load where rows and groups allow it (B4 N2048 C2048 n = 16 bf16, rows a little
+    // wider than their channels: 488 us, off by one element 597)
     bool vec = a.C / a.G % 4 == 0;
     for (const Rows& r : {in.x, in.delta, in.z, in.dout})
         vec = vec && (!r.p || rows_on(r.p, r.batch, r.token, (int)sizeof(T), 4 * sizeof(T)));
